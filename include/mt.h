@@ -41,7 +41,7 @@
 extern "C" {
 #endif
 
-#define MT_ABI_VERSION 2
+#define MT_ABI_VERSION 3
 
 /* Status codes. */
 enum {
@@ -289,6 +289,134 @@ size_t mt_backward_pooled_workspace_bytes(const mt_table* t, int64_t n, int64_t 
 int mt_backward_adam_pooled(mt_table* t, const mt_lookup_result* res, int64_t n, const int64_t* bag_offsets,
                             int64_t num_bags, int mode, const float* dpooled, const mt_adam* hp, float* gsum_out,
                             void* ws, size_t ws_bytes, mt_stream stream);
+
+/* ---- the dense block over ragged groups of rows ------------------------------ */
+
+/* What stands between a lookup and its gradient in a recommendation model's
+ * dense part: matrix products whose weights differ by feature or expert,
+ * norms with a gate and a residual scale, and activations kept in 8 bits for
+ * the backward.  Conventions of this section:
+ *  - A row tensor is n rows of d columns of `dtype` (MT_F32 or MT_BF16), row i
+ *    at data + i * ld elements, ld >= d: a slice of columns of a wider tensor
+ *    is a row tensor.  Any element-aligned pointer and stride is taken; rows
+ *    that all start on 16 bytes, with widths that are multiples of 8, take
+ *    faster kernels.
+ *  - Group g holds the rows [offsets[g], offsets[g+1]); offsets is device
+ *    int64 [groups + 1], non-decreasing within [0, n].  Rows in no group give
+ *    zero outputs and zero gradients; groups may be empty.  Offsets that
+ *    break this latch MT_EINVAL into *status and count as clamped to [0, n]
+ *    and raised to their running maximum, so every access stays in bounds.
+ *  - status: device int32 or NULL; the first error found on the device is
+ *    written there when it holds 0 (it is never cleared by a call).
+ *  - Outputs must not overlap inputs or one another (two column slices of one
+ *    buffer do not overlap).
+ *  - Sums, statistics and accumulators are fp32 or wider; results are rounded
+ *    once to `dtype`.  No atomics: the same call gives the same bits. */
+#define MT_MAX_GROUPS 1024
+#define MT_MAX_BLOCK_DIM 8192
+#define MT_PACK_BLOCK 32
+
+/* A row tensor as plain rows (data, ld), in 8 bits (codes, exps; data NULL),
+ * or absent (all NULL).  Where a call writes a checkpoint beside the rows, both
+ * are given. */
+typedef struct {
+  void* data;
+  int64_t ld;
+  int8_t* codes;  /* [n, d], contiguous */
+  uint8_t* exps;  /* [n, ceil(d / 32)], contiguous */
+} mt_rows;
+
+/* Activation checkpoints in 8 bits.  Each run of 32 columns of a row (the last
+ * run may be shorter) shares one exponent e, the least with
+ * max|x| <= 127 * 2^e, held in [-120, 121]; a column is kept as
+ * codes = rint(x * 2^-e) in [-127, 127] (ties to even) and stands for
+ * codes * 2^e.  exps holds e + 127.  A run with an infinity or a NaN is kept
+ * as exps = 255 and stands for NaN.  Every value a checkpoint stands for is
+ * exact in bf16 and in fp32. */
+int mt_pack8(const void* x, int64_t ldx, int64_t n, int32_t d, int dtype, int8_t* codes, uint8_t* exps,
+             mt_stream stream);
+/* The values a checkpoint stands for, as rows of `dtype`. */
+int mt_unpack8(const int8_t* codes, const uint8_t* exps, int64_t n, int32_t d, int dtype, void* out, int64_t ldo,
+               mt_stream stream);
+
+/* Matrix products grouped by row segment: y_i = W_g x_i for the rows i of group g.
+ *  x       row tensor [n, in_dim].
+ *  w       device [groups, out_dim, in_dim] of dtype, contiguous.
+ *  y       row tensor [n, out_dim], written. */
+int mt_group_linear_forward(const void* x, int64_t ldx, const void* w, const int64_t* offsets, int32_t groups,
+                            int64_t n, int32_t in_dim, int32_t out_dim, int dtype, void* y, int64_t ldy,
+                            int32_t* status, mt_stream stream);
+
+/* Workspace bytes of mt_group_linear_backward (partial products of long groups). */
+size_t mt_group_linear_workspace_bytes(int64_t n, int32_t in_dim, int32_t out_dim);
+
+/* Its backward: dx_i = W_g^T dy_i and dW_g = sum over the group's rows of dy_i x_i^T.
+ *  dy   row tensor [n, out_dim].
+ *  x    the forward's input, plain or in 8 bits (the product then reads the
+ *       values the checkpoint stands for, with no further rounding); only dw
+ *       needs it.
+ *  dx   row tensor [n, in_dim], written, or NULL.
+ *  dw   device fp32 [groups, out_dim, in_dim], written (zeros for an empty
+ *       group), or NULL.
+ *  ws   workspace of mt_group_linear_workspace_bytes; only dw needs it. */
+int mt_group_linear_backward(const void* dy, int64_t lddy, const mt_rows* x, const void* w, const int64_t* offsets,
+                             int32_t groups, int64_t n, int32_t in_dim, int32_t out_dim, int dtype, void* dx,
+                             int64_t lddx, float* dw, int32_t* status, void* ws, size_t ws_bytes, mt_stream stream);
+
+#define MT_NORM_RMS 0   /* v / sqrt(mean(v^2) + eps) */
+#define MT_NORM_LAYER 1 /* (v - mean(v)) / sqrt(var(v) + eps) */
+#define MT_GATE_NONE 0    /* no gate: a = 1 */
+#define MT_GATE_LINEAR 1  /* a = u */
+#define MT_GATE_SIGMOID 2 /* a = 1 / (1 + exp(-u)) */
+#define MT_GATE_SILU 3    /* a = u / (1 + exp(-u)) */
+
+/* The norm after a block, its gate and its residual scale, the residual sum,
+ * and the next block's norm:
+ *   z = x + scale * (post_weight * norm(y) + post_bias) * act(u)
+ *   h = pre_weight * norm(z) + pre_bias
+ * Parameters are device fp32 [groups, dim] (row g for the rows of group g);
+ * post_bias, scale (1 when NULL) and pre_bias may be NULL.  post_weight NULL: there
+ * is no y, and z is x.  pre_weight NULL: there is no h. */
+typedef struct {
+  int64_t n;
+  int32_t dim;
+  int32_t groups;
+  int32_t dtype;
+  int32_t kind;  /* MT_NORM_RMS or MT_NORM_LAYER, both norms */
+  int32_t gate;  /* MT_GATE_*; MT_GATE_NONE exactly when there is no u */
+  float eps;     /* > 0 */
+  const int64_t* offsets; /* NULL: one group of all rows (groups = 1) */
+  int32_t* status;
+  const float* post_weight;
+  const float* post_bias;
+  const float* scale;
+  const float* pre_weight;
+  const float* pre_bias;
+} mt_gated_norm;
+
+/* Forward.  x: plain.  y, gate: plain, or NULL (absent); with codes and exps
+ * set too, their checkpoints are written.  z: written (and its checkpoint where
+ * codes and exps are set); without y it has no plain rows of its own (z is x)
+ * and only its checkpoint can be asked for.  h: written, and its checkpoint
+ * where asked.  A checkpoint holds the values as they are stored in `dtype`:
+ * the same bytes mt_pack8 makes of the plain rows (zeros for rows in no group). */
+int mt_gated_norm_forward(const mt_gated_norm* cfg, const mt_rows* x, const mt_rows* y, const mt_rows* gate,
+                          const mt_rows* z, const mt_rows* h, mt_stream stream);
+
+/* Workspace bytes of mt_gated_norm_backward (partial sums of the parameter gradients). */
+size_t mt_gated_norm_workspace_bytes(int64_t n, int32_t dim, int32_t groups);
+
+/* Backward from dz (plain or NULL: zero) and dh (plain; needed with
+ * pre_weight).  y, gate and z: the forward's y, gate and z, each plain or in 8
+ * bits (the gradient is then the formula's at the values the checkpoint
+ * stands for); z is needed with pre_weight only.  The statistics are
+ * recomputed from y and z: nothing else is kept from the forward.
+ * Written: dx, dy (with y), dgate (with gate); fp32 [groups, dim] gradients of
+ * exactly the parameters that cfg has (the others NULL). */
+int mt_gated_norm_backward(const mt_gated_norm* cfg, const mt_rows* dz, const mt_rows* dh, const mt_rows* y,
+                           const mt_rows* gate, const mt_rows* z, const mt_rows* dx, const mt_rows* dy,
+                           const mt_rows* dgate, float* dpost_weight, float* dpost_bias, float* dscale,
+                           float* dpre_weight, float* dpre_bias, void* ws, size_t ws_bytes, mt_stream stream);
 
 /* ---- automatic table merging ------------------------------------------------ */
 

@@ -22,10 +22,11 @@ import numpy as np
 
 __all__ = ["Table", "ShardGroup", "MergedTables", "plan_merge", "LookupResult", "load_library", "MTError", "MT_F32", "MT_BF16", "POOL_SUM", "POOL_MEAN",
            "KEY_EMPTY", "KEY_TOMBSTONE",
+           "Packed8", "pack8", "unpack8", "GroupedLinear", "GatedNorm", "NormParams", "NormForward", "NormGrads",
            "ABI_FUNCTIONS", "profile_enable", "profile_report", "kernel_launches"]
 
 MT_OK, MT_EINVAL, MT_ENOSPACE, MT_EFULL, MT_EKEY, MT_ECUDA, MT_ETOOBIG = 0, -1, -2, -3, -4, -5, -6
-ABI_VERSION = 2
+ABI_VERSION = 3
 LOOKUP_STATIC_MAX_IDS = 65536
 MT_F32, MT_BF16 = 0, 1
 POOL_SUM, POOL_MEAN = 0, 1
@@ -69,6 +70,7 @@ class _Stats(ctypes.Structure):
 
 
 _P, _I64, _SZ, _I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+_C32 = ctypes.c_int32
 # name -> (restype, argtypes); every entry point of include/mt.h
 ABI_FUNCTIONS = {
     "mt_abi_version": (_I32, []),
@@ -100,6 +102,15 @@ ABI_FUNCTIONS = {
     "mt_lookup_grouped": (_I32, [_P, _I32, _P, _P, _I64, _P, _I32, _I32, _P, _P, _P, _P, _SZ, _P]),
     "mt_backward_grouped_workspace_bytes": (_SZ, [_P, _I32, _P]),
     "mt_backward_adam_grouped": (_I32, [_P, _I32, _P, _P, _P, _I32, _P, _P, _P, _SZ, _P]),
+    "mt_pack8": (_I32, [_P, _I64, _I64, _C32, _I32, _P, _P, _P]),
+    "mt_unpack8": (_I32, [_P, _P, _I64, _C32, _I32, _P, _I64, _P]),
+    "mt_group_linear_forward": (_I32, [_P, _I64, _P, _P, _C32, _I64, _C32, _C32, _I32, _P, _I64, _P, _P]),
+    "mt_group_linear_workspace_bytes": (_SZ, [_I64, _C32, _C32]),
+    "mt_group_linear_backward": (_I32, [_P, _I64, _P, _P, _P, _C32, _I64, _C32, _C32, _I32, _P, _I64, _P, _P, _P, _SZ,
+                                        _P]),
+    "mt_gated_norm_forward": (_I32, [_P, _P, _P, _P, _P, _P, _P]),
+    "mt_gated_norm_workspace_bytes": (_SZ, [_I64, _C32, _C32]),
+    "mt_gated_norm_backward": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "mt_erase_workspace_bytes": (_SZ, [_I64]),
     "mt_erase": (_I32, [_P, _P, _I64, _P, _P, _SZ, _P]),
     "mt_compact_workspace_bytes": (_SZ, [_P]),
@@ -736,3 +747,6 @@ class MergedTables:
                                                  ctypes.byref(hp), gs, ws.data_ptr(), ws.numel(), _stream(stream)),
                "mt_backward_adam_grouped")
         return gsums
+
+
+from .block import GatedNorm, GroupedLinear, NormForward, NormGrads, NormParams, Packed8, pack8, unpack8  # noqa: E402

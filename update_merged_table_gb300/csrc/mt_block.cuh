@@ -1,0 +1,334 @@
+// Shared device code of the dense block's operators (mt_linear*.cu, mt_norm.cu,
+// mt_pack.cu): ragged groups of rows, loads and stores of eight columns, and the
+// 8-bit form of a block of 32 columns.
+#pragma once
+
+#include "mt_kernels.cuh"
+
+namespace mt {
+
+// Row tensors as the kernels see them (mt_rows with its data typed away).
+using Rows = mt_rows;
+
+// ---- ragged groups -------------------------------------------------------------
+//
+// Group g holds the rows [off[g], off[g+1]).  The offsets are device data, so
+// they are made safe where they are read: clamped to [0, n] and replaced by
+// their running maximum.  Offsets that needed either latch MT_EINVAL; whatever
+// they were, the groups are then disjoint, in order and inside [0, n], so no
+// access leaves a buffer and no row belongs to two groups.
+
+__device__ __forceinline__ long long warp_max_scan(long long v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long w = __shfl_up_sync(kFull, v, o);
+    if (lane >= o) v = w > v ? w : v;
+  }
+  return v;
+}
+
+__device__ __forceinline__ int warp_sum_scan(int v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int w = __shfl_up_sync(kFull, v, o);
+    if (lane >= o) v += w;
+  }
+  return v;
+}
+
+// Fills s_off[0 .. G] (shared) with the safe offsets; every thread of the block calls it.
+// offsets = NULL: one group of all rows.
+__device__ __forceinline__ void load_offsets(const long long* offsets, int G, long long n, long long* s_off,
+                                             int32_t* status) {
+  if (offsets == nullptr) {
+    if (threadIdx.x == 0) {
+      s_off[0] = 0;
+      s_off[1] = n;
+    }
+    __syncthreads();
+    return;
+  }
+  for (int i = threadIdx.x; i <= G; i += blockDim.x) s_off[i] = __ldg(&offsets[i]);
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    long long carry = 0;
+    bool bad = false;
+    for (int i0 = 0; i0 <= G; i0 += 32) {
+      const int i = i0 + lane;
+      const long long raw = i <= G ? s_off[i] : 0;
+      long long v = raw < 0 ? 0 : (raw > n ? n : raw);
+      v = warp_max_scan(v, lane);
+      v = v < carry ? carry : v;
+      if (i <= G) {
+        bad |= v != raw;
+        s_off[i] = v;
+      }
+      carry = __shfl_sync(kFull, v, 31);
+    }
+    if (bad && status != nullptr && blockIdx.x == 0 && blockIdx.y == 0) atomicCAS(status, 0, MT_EINVAL);
+  }
+  __syncthreads();
+}
+
+// s_cum[0 .. G] (shared): tiles of R rows in the groups before each one; after load_offsets, by every thread.
+__device__ __forceinline__ void count_tiles(const long long* s_off, int G, int R, int* s_cum) {
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int carry = 0;
+    for (int i0 = 0; i0 < G; i0 += 32) {
+      const int i = i0 + lane;
+      const int t = i < G ? (int)((s_off[i + 1] - s_off[i] + R - 1) / R) : 0;
+      const int inc = warp_sum_scan(t, lane);
+      if (i < G) s_cum[i] = carry + inc - t;
+      carry += __shfl_sync(kFull, inc, 31);
+    }
+    if (lane == 0) s_cum[G] = carry;
+  }
+  __syncthreads();
+}
+
+// The last i in [0, G) with s_cum[i] <= t (so the group of tile t when t < s_cum[G]; empty groups are passed over).
+__device__ __forceinline__ int tile_group(const int* s_cum, int G, int t) {
+  int lo = 0, hi = G;  // s_cum[lo] <= t < s_cum[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (s_cum[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// The group of a row, -1 when the row is in none.
+__device__ __forceinline__ int row_group(const long long* s_off, int G, long long row) {
+  if (row < s_off[0] || row >= s_off[G]) return -1;
+  int lo = 0, hi = G;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (s_off[mid] <= row) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// ---- 8-bit blocks ----------------------------------------------------------------
+//
+// 32 columns share the exponent e: the least with max|x| <= 127 * 2^e, held in
+// [-120, 121] so that every value and both powers of two stay normal fp32
+// numbers.  A column is q * 2^e with q = rint(x * 2^-e) in [-127, 127]: seven
+// bits and a sign times a power of two, exact in bf16, so a product that reads
+// it rounds nothing.  A block that holds an infinity or a NaN is stored with
+// exponent byte 255 and stands for NaN.
+
+constexpr int kPackBlock = MT_PACK_BLOCK;
+constexpr uint32_t kPackNan = 255;
+
+// Exponent byte (e + 127) of a block from the largest |x| as fp32 bits.
+__device__ __forceinline__ uint32_t pack_exp_byte(uint32_t top) {
+  if (top >= 0x7F800000u) return kPackNan;
+  int e = (int)(top >> 23) - 127 - 6 + ((top & 0x7FFFFFu) > 0x7E0000u ? 1 : 0);  // 127 = 1.984375 * 2^6
+  e = e < -120 ? -120 : (e > 121 ? 121 : e);
+  return (uint32_t)(e + 127);
+}
+__device__ __forceinline__ float pack_inv(uint32_t byte) {  // 2^-e; 0 for a block that is not finite
+  return byte == kPackNan ? 0.0f : __uint_as_float((254u - byte) << 23);
+}
+__device__ __forceinline__ float pack_scale(uint32_t byte) {  // 2^e, or NaN
+  return byte == kPackNan ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte << 23);
+}
+__device__ __forceinline__ int pack_code(float x, float inv) {
+  if (inv == 0.0f) return 0;
+  const int q = __float2int_rn(x * inv);
+  return q < -127 ? -127 : (q > 127 ? 127 : q);
+}
+
+// ---- eight columns of a row --------------------------------------------------------
+
+template <typename T>
+__device__ __forceinline__ float to_f(T x);
+template <>
+__device__ __forceinline__ float to_f<float>(float x) {
+  return x;
+}
+template <>
+__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 x) {
+  return __bfloat162float(x);
+}
+template <typename T>
+__device__ __forceinline__ T from_f(float x);
+template <>
+__device__ __forceinline__ float from_f<float>(float x) {
+  return x;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  uint32_t w;
+  memcpy(&w, &v, 4);
+  return w;
+}
+
+// Eight columns as they were loaded: bf16 in a, fp32 in a and b, 8-bit codes in a.x and a.y with the exponent
+// byte in a.z.  Kept raw so that a row's loads are all issued before the first is used.
+template <typename T>
+struct Raw8 {
+  uint4 a;
+};
+template <>
+struct Raw8<float> {
+  uint4 a, b;
+};
+
+// Columns [8 vec, 8 vec + 8) of `row`, or zeros where they lie past d.  AL: every row starts on 16 bytes (codes: 8)
+// and d is a multiple of 8.
+template <typename T, bool AL>
+__device__ __forceinline__ Raw8<T> load8(const Rows& r, long long row, int vec, int d) {
+  Raw8<T> v;
+  v.a = make_uint4(0u, 0u, 0u, 0u);
+  if constexpr (sizeof(T) == 4) v.b = v.a;
+  const int c0 = vec * 8;
+  if (c0 >= d) return v;
+  if (r.data != nullptr) {
+    const T* p = static_cast<const T*>(r.data) + row * r.ld + c0;
+    if constexpr (AL) {
+      v.a = __ldg(reinterpret_cast<const uint4*>(p));
+      if constexpr (sizeof(T) == 4) v.b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    } else {
+      const int k = min(8, d - c0);
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = j < k ? to_f<T>(p[j]) : 0.0f;
+      if constexpr (sizeof(T) == 4) {
+        v.a = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+        v.b = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+      } else {
+        v.a = make_uint4(bf16x2_of(f[0], f[1]), bf16x2_of(f[2], f[3]), bf16x2_of(f[4], f[5]), bf16x2_of(f[6], f[7]));
+      }
+    }
+  } else {
+    const int nb = (d + kPackBlock - 1) / kPackBlock;
+    const int8_t* p = r.codes + row * d + c0;
+    if constexpr (AL) {
+      const uint2 c = __ldg(reinterpret_cast<const uint2*>(p));
+      v.a.x = c.x;
+      v.a.y = c.y;
+    } else {
+      const int k = min(8, d - c0);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t q = j < k ? (uint32_t)(uint8_t)p[j] : 0u;
+        if (j < 4) v.a.x |= q << (8 * j);
+        else v.a.y |= q << (8 * (j - 4));
+      }
+    }
+    v.a.z = __ldg(r.exps + row * nb + c0 / kPackBlock);
+  }
+  return v;
+}
+
+// Byte j of w, as the signed number it holds.
+__device__ __forceinline__ float code_f(uint32_t w, int j) { return (float)(int8_t)(w >> (8 * j)); }
+
+template <typename T>
+__device__ __forceinline__ void widen8(const Raw8<T>& v, bool packed, float f[8]) {
+  if (packed) {
+    const float s = pack_scale(v.a.z);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[j] = code_f(v.a.x, j) * s;
+      f[4 + j] = code_f(v.a.y, j) * s;
+    }
+  } else if constexpr (sizeof(T) == 4) {
+    const uint32_t w[8] = {v.a.x, v.a.y, v.a.z, v.a.w, v.b.x, v.b.y, v.b.z, v.b.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(w[j]);
+  } else {
+    const uint32_t w[4] = {v.a.x, v.a.y, v.a.z, v.a.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[2 * j] = __uint_as_float(w[j] << 16);
+      f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+  }
+}
+
+// Writes eight columns (those below d) rounded to T; f comes back as the values that were stored.
+template <typename T, bool AL>
+__device__ __forceinline__ void store8(void* data, long long ld, long long row, int vec, int d, float f[8]) {
+  const int c0 = vec * 8;
+  if (c0 >= d) return;
+  T* p = static_cast<T*>(data) + row * ld + c0;
+  if constexpr (AL && sizeof(T) == 4) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  } else if constexpr (AL) {
+    Raw8<T> v;
+    v.a = make_uint4(bf16x2_of(f[0], f[1]), bf16x2_of(f[2], f[3]), bf16x2_of(f[4], f[5]), bf16x2_of(f[6], f[7]));
+    *reinterpret_cast<uint4*>(p) = v.a;
+    widen8<T>(v, false, f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const T t = from_f<T>(f[j]);
+      if (c0 + j < d) p[j] = t;
+      f[j] = to_f<T>(t);
+    }
+  }
+}
+
+// The 8-bit form of eight columns f (values past d are zero): four neighbouring lanes hold a block's 32 columns and
+// call this together.
+template <bool AL>
+__device__ __forceinline__ void store_packed8(const Rows& r, long long row, int vec, int d, const float f[8], bool live) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+  top = max(top, __shfl_xor_sync(kFull, top, 1));
+  top = max(top, __shfl_xor_sync(kFull, top, 2));
+  const int c0 = vec * 8;
+  if (!live || c0 >= d) return;
+  const uint32_t byte = pack_exp_byte(top);
+  const float inv = pack_inv(byte);
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j >> 2] |= (uint32_t)(uint8_t)(int8_t)pack_code(f[j], inv) << (8 * (j & 3));
+  int8_t* p = r.codes + row * d + c0;
+  if constexpr (AL) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c0 + j < d) p[j] = (int8_t)(w[j >> 2] >> (8 * (j & 3)));
+  }
+  if ((vec & 3) == 0) r.exps[row * ((d + kPackBlock - 1) / kPackBlock) + vec / 4] = (uint8_t)byte;
+}
+
+// ---- host-side checks ------------------------------------------------------------------
+
+inline bool is_aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+inline size_t elem_bytes(int dtype) { return dtype == MT_F32 ? 4 : 2; }
+
+// A plain row tensor: pointer, element alignment, row stride of at least d.
+inline bool rows_ok(const void* data, int64_t ld, int64_t d, int dtype) {
+  return data != nullptr && is_aligned(data, elem_bytes(dtype)) && ld >= d;
+}
+
+// Whether eight-column vectors of a row tensor may be reached with 16-byte (codes: 8-byte) accesses.
+inline bool rows_wide(const Rows& r, int64_t d, int dtype) {
+  if (d % 8 != 0) return false;
+  if (r.data != nullptr && (!is_aligned(r.data, 16) || (r.ld * elem_bytes(dtype)) % 16 != 0)) return false;
+  return r.codes == nullptr || is_aligned(r.codes, 8);
+}
+
+// Whether [a, a + na) and [b, b + nb) meet.
+inline bool ranges_meet(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a != nullptr && b != nullptr && x < y + nb && y < x + na;
+}
+
+}  // namespace mt

@@ -1,0 +1,331 @@
+// Matrix products grouped by ragged row segments (features, or experts):
+//
+//   forward   y_i  = W_g x_i             W [groups, out, in]
+//   backward  dx_i = W_g^T dy_i          dW_g = sum over the group's rows of dy_i x_i^T
+//
+// This file holds the entry points and the kernels that take every type, width,
+// stride and alignment on the fp32 pipes:
+//  k_linear_rows     forward and dx: a 64 x 64 tile of one group's rows per
+//                    block, both operands staged in shared memory as fp32.
+//  k_linear_weights  dW: a 64 x 64 tile of one group's dW over one chunk of its
+//                    rows; x may come in 8 bits (its values are read as they
+//                    stand, exact in fp32).
+//  k_linear_sums     dW of the groups whose rows were split over several chunks,
+//                    from the chunks' partial products in chunk order (no
+//                    atomics: the sum has one order), and zeros for empty groups.
+#include <algorithm>
+
+#include "mt_linear.cuh"
+
+namespace mt {
+namespace {
+
+constexpr int kT = 64;    // tile edge
+constexpr int kI = 16;    // contraction step
+constexpr int kThreadsL = 256;
+
+// ---- forward and dx ----------------------------------------------------------------
+//
+// C[row, j] = sum over i < I of A[row, i] * W_g(i, j), with W_g(i, j) = w[g * wg + i * wi + j * wj].
+template <typename T>
+__global__ void __launch_bounds__(kThreadsL) k_linear_rows(const LinearRows p) {
+  extern __shared__ long long s_off[];
+  __shared__ float s_a[kI][kT + 4], s_b[kI][kT + 4];
+  int* s_cum = reinterpret_cast<int*>(s_off + p.groups + 1);
+  load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
+  count_tiles(s_off, p.groups, kT, s_cum);
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const T* A = static_cast<const T*>(p.a);
+  T* C = static_cast<T*>(p.c);
+
+  zero_outside<T>(s_off, p.groups, p.n, C, p.ldc, p.J);
+
+  const long long total = (long long)s_cum[p.groups] * p.jtiles;
+  for (long long t = blockIdx.x; t < total; t += gridDim.x) {
+    const int rt = (int)(t / p.jtiles), j0 = (int)(t - (long long)rt * p.jtiles) * kT;
+    const int g = tile_group(s_cum, p.groups, rt);
+    const long long r0 = s_off[g] + (long long)(rt - s_cum[g]) * kT;
+    const int rows = (int)min((long long)kT, s_off[g + 1] - r0);
+    const T* W = static_cast<const T*>(p.w) + (size_t)g * p.wg;
+    float acc[4][4] = {};
+    for (int i0 = 0; i0 < p.I; i0 += kI) {
+#pragma unroll
+      for (int q = tid; q < kT * kI; q += kThreadsL) {
+        const int i = q % kI, r = q / kI;
+        s_a[i][r] = r < rows && i0 + i < p.I ? to_f<T>(A[(r0 + r) * p.lda + i0 + i]) : 0.0f;
+      }
+#pragma unroll
+      for (int q = tid; q < kT * kI; q += kThreadsL) {
+        const int i = p.wi == 1 ? q % kI : q / kT, j = p.wi == 1 ? q / kI : q % kT;
+        s_b[i][j] = i0 + i < p.I && j0 + j < p.J ? to_f<T>(W[(size_t)(i0 + i) * p.wi + (size_t)(j0 + j) * p.wj]) : 0.0f;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kI; ++i) {
+        float a[4], b[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          a[q] = s_a[i][ty * 4 + q];
+          b[q] = s_b[i][tx * 4 + q];
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[u][v] = fmaf(a[u], b[v], acc[u][v]);
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = ty * 4 + u;
+      if (r >= rows) continue;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int j = j0 + tx * 4 + v;
+        if (j < p.J) C[(r0 + r) * p.ldc + j] = from_f<T>(acc[u][v]);
+      }
+    }
+  }
+}
+
+// ---- dW ---------------------------------------------------------------------------
+
+template <typename T>
+__global__ void __launch_bounds__(kThreadsL) k_linear_weights(const LinearWeights p) {
+  extern __shared__ long long s_off[];
+  __shared__ float s_a[kI][kT + 4], s_b[kI][kT + 4];
+  int* s_cum = reinterpret_cast<int*>(s_off + p.groups + 1);
+  int* s_slot = s_cum + p.groups + 1;
+  load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
+  count_tiles(s_off, p.groups, p.chunk, s_cum);
+  count_slots(s_cum, p.groups, s_slot);
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const T* DY = static_cast<const T*>(p.dy);
+  const T* X = static_cast<const T*>(p.x.data);
+  const int nb = (p.K + kPackBlock - 1) / kPackBlock;
+  const int mt = (p.M + kT - 1) / kT, kt = (p.K + kT - 1) / kT;
+  const long long total = (long long)s_cum[p.groups] * mt * kt;
+  for (long long t = blockIdx.x; t < total; t += gridDim.x) {
+    const int c = (int)(t / (mt * kt)), q0 = (int)(t - (long long)c * (mt * kt));
+    const int m0 = q0 / kt * kT, k0 = (q0 - q0 / kt * kt) * kT;
+    const int g = tile_group(s_cum, p.groups, c);
+    const long long first = s_off[g] + (long long)(c - s_cum[g]) * p.chunk;
+    const long long last = min(first + p.chunk, s_off[g + 1]);
+    float acc[4][4] = {};
+    for (long long r0 = first; r0 < last; r0 += kI) {
+#pragma unroll
+      for (int q = tid; q < kT * kI; q += kThreadsL) {
+        const int r = q / kT, m = q % kT;
+        s_a[r][m] = r0 + r < last && m0 + m < p.M ? to_f<T>(DY[(r0 + r) * p.lddy + m0 + m]) : 0.0f;
+      }
+#pragma unroll
+      for (int q = tid; q < kT * kI; q += kThreadsL) {
+        const int r = q / kT, k = q % kT;
+        float v = 0.0f;
+        if (r0 + r < last && k0 + k < p.K) {
+          if (X != nullptr) v = to_f<T>(X[(r0 + r) * p.x.ld + k0 + k]);
+          else
+            v = (float)p.x.codes[(r0 + r) * p.K + k0 + k] *
+                pack_scale(p.x.exps[(r0 + r) * nb + (k0 + k) / kPackBlock]);
+        }
+        s_b[r][k] = v;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kI; ++i) {
+        float a[4], b[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          a[q] = s_a[i][ty * 4 + q];
+          b[q] = s_b[i][tx * 4 + q];
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[u][v] = fmaf(a[u], b[v], acc[u][v]);
+      }
+      __syncthreads();
+    }
+    float* out = weights_out(p, s_cum, s_slot, g, c);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int m = m0 + ty * 4 + u, k = k0 + tx * 4 + v;
+        if (m < p.M && k < p.K) out[(size_t)m * p.K + k] = acc[u][v];
+      }
+  }
+}
+
+__global__ void __launch_bounds__(256) k_linear_sums(const LinearWeights p) {
+  extern __shared__ long long s_off[];
+  int* s_cum = reinterpret_cast<int*>(s_off + p.groups + 1);
+  int* s_slot = s_cum + p.groups + 1;
+  load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
+  count_tiles(s_off, p.groups, p.chunk, s_cum);
+  count_slots(s_cum, p.groups, s_slot);
+  const size_t size = (size_t)p.M * p.K;
+  for (int g = blockIdx.y; g < p.groups; g += gridDim.y) {
+    const int c = s_cum[g + 1] - s_cum[g];
+    if (c == 1) continue;  // written by its only chunk
+    const float* part = p.part + (size_t)s_slot[g] * size;
+    for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < size; i += (size_t)gridDim.x * blockDim.x) {
+      float s = 0.0f;
+      for (int k = 0; k < c; ++k) s += __ldg(part + (size_t)k * size + i);
+      p.dw[(size_t)g * size + i] = s;
+    }
+  }
+}
+
+size_t rows_smem(int groups) { return (size_t)(groups + 1) * (8 + 4); }
+
+// The shapes, offsets and types that both directions share.
+int linear_check(const int64_t* offsets, int32_t groups, int64_t n, int32_t k, int32_t m, int dtype,
+                 const int32_t* status) {
+  if (dtype != MT_F32 && dtype != MT_BF16) return MT_EINVAL;
+  if (n < 0 || n > 0x7FFFFFFF || groups < 1 || groups > MT_MAX_GROUPS) return MT_EINVAL;
+  if (k < 1 || k > MT_MAX_BLOCK_DIM || m < 1 || m > MT_MAX_BLOCK_DIM) return MT_EINVAL;
+  if (offsets == nullptr || !is_aligned(offsets, 8) || !is_aligned(status, 4)) return MT_EINVAL;
+  return MT_OK;
+}
+
+cudaError_t launch_linear_rows(LinearRows p, int dtype, cudaStream_t s) {
+  p.jtiles = (p.J + kT - 1) / kT;
+  const long long tiles = ((p.n + kT - 1) / kT + p.groups) * p.jtiles;
+  const int grid = (int)std::min<long long>(tiles, (long long)sm_count() * 8);
+  MT_LAUNCH("k_linear_rows", s);
+  if (dtype == MT_F32) k_linear_rows<float><<<grid, kThreadsL, rows_smem(p.groups), s>>>(p);
+  else k_linear_rows<__nv_bfloat16><<<grid, kThreadsL, rows_smem(p.groups), s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_linear_weights(const LinearWeights& p, int dtype, cudaStream_t s) {
+  if (p.n > 0) {
+    const long long tiles = (long long)((p.M + kT - 1) / kT) * ((p.K + kT - 1) / kT) * (p.n / p.chunk + p.groups);
+    const int grid = (int)std::min<long long>(tiles, (long long)sm_count() * 8);
+    MT_LAUNCH("k_linear_weights", s);
+    if (dtype == MT_F32) k_linear_weights<float><<<grid, kThreadsL, weights_smem(p.groups), s>>>(p);
+    else k_linear_weights<__nv_bfloat16><<<grid, kThreadsL, weights_smem(p.groups), s>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_linear_sums(const LinearWeights& p, cudaStream_t s) {
+  MT_LAUNCH("k_linear_sums", s);
+  const long long size = (long long)p.M * p.K;
+  const dim3 grid((unsigned)std::min<long long>((size + 255) / 256, 1024), p.groups);
+  k_linear_sums<<<grid, 256, weights_smem(p.groups), s>>>(p);
+  return cudaGetLastError();
+}
+
+// Rows per chunk of dW: enough chunks that the tiles fill the SMs twice, at most kMaxChunk rows (longer sums are
+// split, which also keeps their fp32 rounding short), at least kMinChunk.
+int chunk_of(int64_t n, int32_t k, int32_t m) {
+  const long long tiles = (long long)((m + 127) / 128) * ((k + 127) / 128);
+  const long long want = n * tiles / (2LL * sm_count());
+  const long long c = std::min<long long>(kMaxChunk, std::max<long long>(kMinChunk, want));
+  return (int)((c + 63) / 64 * 64);
+}
+
+}  // namespace
+}  // namespace mt
+
+extern "C" {
+
+int mt_group_linear_forward(const void* x, int64_t ldx, const void* w, const int64_t* offsets, int32_t groups,
+                            int64_t n, int32_t in_dim, int32_t out_dim, int dtype, void* y, int64_t ldy,
+                            int32_t* status, mt_stream stream) {
+  using namespace mt;
+  const int rc = linear_check(offsets, groups, n, in_dim, out_dim, dtype, status);
+  if (rc != MT_OK) return rc;
+  if (w == nullptr || !is_aligned(w, elem_bytes(dtype))) return MT_EINVAL;
+  if (n == 0) return MT_OK;
+  if (!rows_ok(x, ldx, in_dim, dtype) || !rows_ok(y, ldy, out_dim, dtype)) return MT_EINVAL;
+  LinearRows p{};
+  p.n = n;
+  p.groups = groups;
+  p.offsets = reinterpret_cast<const long long*>(offsets);
+  p.status = status;
+  p.a = x;
+  p.lda = ldx;
+  p.w = w;
+  p.wg = (size_t)in_dim * out_dim;
+  p.wi = 1;
+  p.wj = in_dim;
+  p.c = y;
+  p.ldc = ldy;
+  p.I = in_dim;
+  p.J = out_dim;
+  return launch_linear_rows(p, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MT_OK : MT_ECUDA;
+}
+
+size_t mt_group_linear_workspace_bytes(int64_t n, int32_t in_dim, int32_t out_dim) {
+  using namespace mt;
+  if (n < 0 || n > 0x7FFFFFFF || in_dim < 1 || in_dim > MT_MAX_BLOCK_DIM || out_dim < 1 || out_dim > MT_MAX_BLOCK_DIM)
+    return 0;
+  // a group of more than one chunk has fewer than 2 len / chunk of them
+  const size_t slots = (size_t)(2 * n / chunk_of(n, in_dim, out_dim));
+  return align_up(slots * in_dim * out_dim * 4 + 256, 256);
+}
+
+int mt_group_linear_backward(const void* dy, int64_t lddy, const mt_rows* x, const void* w, const int64_t* offsets,
+                             int32_t groups, int64_t n, int32_t in_dim, int32_t out_dim, int dtype, void* dx,
+                             int64_t lddx, float* dw, int32_t* status, void* ws, size_t ws_bytes, mt_stream stream) {
+  using namespace mt;
+  const int rc = linear_check(offsets, groups, n, in_dim, out_dim, dtype, status);
+  if (rc != MT_OK) return rc;
+  if (dx == nullptr && dw == nullptr) return MT_EINVAL;
+  if (n > 0 && !rows_ok(dy, lddy, out_dim, dtype)) return MT_EINVAL;
+  if (dx != nullptr) {
+    if (w == nullptr || !is_aligned(w, elem_bytes(dtype))) return MT_EINVAL;
+    if (n > 0 && !rows_ok(dx, lddx, in_dim, dtype)) return MT_EINVAL;
+  }
+  if (dw != nullptr) {
+    if (!is_aligned(dw, 4) || x == nullptr) return MT_EINVAL;
+    const bool packed = x->data == nullptr;
+    if (n > 0 && (packed ? x->codes == nullptr || x->exps == nullptr : !rows_ok(x->data, x->ld, in_dim, dtype)))
+      return MT_EINVAL;
+    if (ws == nullptr || !is_aligned(ws, 256) || ws_bytes < mt_group_linear_workspace_bytes(n, in_dim, out_dim))
+      return MT_ENOSPACE;
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (dx != nullptr && n > 0) {
+    LinearRows p{};
+    p.n = n;
+    p.groups = groups;
+    p.offsets = reinterpret_cast<const long long*>(offsets);
+    p.status = status;
+    p.a = dy;
+    p.lda = lddy;
+    p.w = w;
+    p.wg = (size_t)in_dim * out_dim;
+    p.wi = in_dim;
+    p.wj = 1;
+    p.c = dx;
+    p.ldc = lddx;
+    p.I = out_dim;
+    p.J = in_dim;
+    e = launch_linear_rows(p, dtype, s);
+  }
+  if (dw != nullptr && e == cudaSuccess) {
+    LinearWeights p{};
+    p.n = n;
+    p.groups = groups;
+    p.offsets = reinterpret_cast<const long long*>(offsets);
+    p.status = status;
+    p.dy = dy;
+    p.lddy = lddy;
+    p.x = *x;
+    p.K = in_dim;
+    p.M = out_dim;
+    p.chunk = chunk_of(n, in_dim, out_dim);
+    p.part = static_cast<float*>(ws);
+    p.dw = dw;
+    e = launch_linear_weights(p, dtype, s);
+    if (e == cudaSuccess) e = launch_linear_sums(p, s);
+  }
+  return e == cudaSuccess ? MT_OK : MT_ECUDA;
+}
+
+}  // extern "C"
