@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(kThreadsL) k_linear_rows(const LinearRows p) {
   const T* A = static_cast<const T*>(p.a);
   T* C = static_cast<T*>(p.c);
 
-  zero_outside<T>(s_off, p.groups, p.n, C, p.ldc, p.J);
+  zero_outside<T>(s_off, p.groups, p.n, C, p.ldc, p.J, kThreadsL, tid);
 
   const long long total = (long long)s_cum[p.groups] * p.jtiles;
   for (long long t = blockIdx.x; t < total; t += gridDim.x) {
@@ -190,6 +190,7 @@ int linear_check(const int64_t* offsets, int32_t groups, int64_t n, int32_t k, i
 }
 
 cudaError_t launch_linear_rows(LinearRows p, int dtype, cudaStream_t s) {
+  if (dtype == MT_BF16 && linear_rows_fits_tc(p)) return launch_linear_rows_tc(p, s);
   p.jtiles = (p.J + kT - 1) / kT;
   const long long tiles = ((p.n + kT - 1) / kT + p.groups) * p.jtiles;
   const int grid = (int)std::min<long long>(tiles, (long long)sm_count() * 8);
@@ -200,6 +201,7 @@ cudaError_t launch_linear_rows(LinearRows p, int dtype, cudaStream_t s) {
 }
 
 cudaError_t launch_linear_weights(const LinearWeights& p, int dtype, cudaStream_t s) {
+  if (p.n > 0 && dtype == MT_BF16 && linear_weights_fits_tc(p)) return launch_linear_weights_tc(p, s);
   if (p.n > 0) {
     const long long tiles = (long long)((p.M + kT - 1) / kT) * ((p.K + kT - 1) / kT) * (p.n / p.chunk + p.groups);
     const int grid = (int)std::min<long long>(tiles, (long long)sm_count() * 8);

@@ -66,16 +66,22 @@ __device__ __forceinline__ float* weights_out(const LinearWeights& p, const int*
   return p.part + (size_t)(s_slot[g] + c - s_cum[g]) * size;
 }
 
-// Zeros for the rows in no group; the whole grid calls it.
+// Zeros for the rows in no group, by the threads [0, threads) of every block.
 template <typename T>
-__device__ __forceinline__ void zero_outside(const long long* s_off, int G, long long n, T* c, long long ldc, int J) {
+__device__ __forceinline__ void zero_outside(const long long* s_off, int G, long long n, T* c, long long ldc, int J,
+                                             int threads, int thread) {
   const long long before = s_off[0], outside = before + (n - s_off[G]);
-  for (long long q = (long long)blockIdx.x * blockDim.x + threadIdx.x; q < outside * J;
-       q += (long long)gridDim.x * blockDim.x) {
+  for (long long q = (long long)blockIdx.x * threads + thread; q < outside * J; q += (long long)gridDim.x * threads) {
     const long long o = q / J;
     const long long row = o < before ? o : o - before + s_off[G];
     c[row * ldc + (q - o * J)] = from_f<T>(0.0f);
   }
 }
+
+// The tensor-core forms (mt_linear_tc.cu): bf16, widths and strides in multiples of 8, rows on 16 bytes.
+bool linear_rows_fits_tc(const LinearRows& p);
+cudaError_t launch_linear_rows_tc(const LinearRows& p, cudaStream_t s);
+bool linear_weights_fits_tc(const LinearWeights& p);
+cudaError_t launch_linear_weights_tc(const LinearWeights& p, cudaStream_t s);
 
 }  // namespace mt
