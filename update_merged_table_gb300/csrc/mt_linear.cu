@@ -229,6 +229,15 @@ int chunk_of(int64_t n, int32_t k, int32_t m) {
   return (int)((c + 63) / 64 * 64);
 }
 
+// Partial products: a group of more than one chunk has fewer than 2 len / chunk of them.
+size_t partial_bytes(int64_t n, int32_t k, int32_t m) {
+  return align_up((size_t)(2 * n / chunk_of(n, k, m)) * k * m * 4 + 256, 256);
+}
+
+// 8-bit x whose rows do not lie a multiple of 16 bytes apart cannot be copied as it is: it is widened to bf16 rows in
+// the workspace first (one more pass over x, 3 bytes per value).
+bool widened_first(int32_t k) { return k % 16 == 8; }
+
 }  // namespace
 }  // namespace mt
 
@@ -265,9 +274,7 @@ size_t mt_group_linear_workspace_bytes(int64_t n, int32_t in_dim, int32_t out_di
   using namespace mt;
   if (n < 0 || n > 0x7FFFFFFF || in_dim < 1 || in_dim > MT_MAX_BLOCK_DIM || out_dim < 1 || out_dim > MT_MAX_BLOCK_DIM)
     return 0;
-  // a group of more than one chunk has fewer than 2 len / chunk of them
-  const size_t slots = (size_t)(2 * n / chunk_of(n, in_dim, out_dim));
-  return align_up(slots * in_dim * out_dim * 4 + 256, 256);
+  return partial_bytes(n, in_dim, out_dim) + (widened_first(in_dim) ? align_up((size_t)n * in_dim * 2, 256) : 0);
 }
 
 int mt_group_linear_backward(const void* dy, int64_t lddy, const mt_rows* x, const void* w, const int64_t* offsets,
@@ -324,6 +331,15 @@ int mt_group_linear_backward(const void* dy, int64_t lddy, const mt_rows* x, con
     p.chunk = chunk_of(n, in_dim, out_dim);
     p.part = static_cast<float*>(ws);
     p.dw = dw;
+    if (dtype == MT_BF16 && x->data == nullptr && widened_first(in_dim) && n > 0) {
+      LinearWeights q = p;
+      q.x = Rows{static_cast<char*>(ws) + partial_bytes(n, in_dim, out_dim), in_dim, nullptr, nullptr};
+      if (linear_weights_fits_tc(q)) {
+        const int rc8 = mt_unpack8(x->codes, x->exps, n, in_dim, dtype, q.x.data, in_dim, stream);
+        if (rc8 != MT_OK) return rc8;
+        p = q;
+      }
+    }
     e = launch_linear_weights(p, dtype, s);
     if (e == cudaSuccess) e = launch_linear_sums(p, s);
   }

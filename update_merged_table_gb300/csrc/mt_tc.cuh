@@ -125,6 +125,18 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
                : "memory");
 }
 
+// 32 bits of two signed bytes each: the pair at bytes 2 * h and 2 * h + 1 of w as two bf16 times `scale` (two equal bf16
+// powers of two, or NaN).  A byte q = u - 128 s (u its low seven bits, s its sign): 128 + u and -128 - 128 s are bf16
+// numbers with u and s among their bits, their sum q is exact, and so is its product with a power of two.
+__device__ __forceinline__ uint32_t codes_bf16x2(uint32_t w, int h, uint32_t scale) {
+  const uint32_t x = __byte_perm(w, 0u, h ? 0x4342 : 0x4140);
+  const uint32_t a = (x & 0x007F007Fu) | 0x43004300u, b = (x & 0x00800080u) | 0xC300C300u;
+  uint32_t q;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(q) : "r"(a), "r"(b));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(q) : "r"(q), "r"(scale));
+  return q;
+}
+
 // ---- tensor maps (host) -------------------------------------------------------------------
 
 // A map of bf16 elements [d1][d0] (rank 2) or [d2][d1][d0] (rank 3), element strides ld1 and ld2, copied in boxes of
@@ -132,6 +144,8 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
 // the map has.  False when the driver refuses it.
 bool encode_bf16(CUtensorMap* map, int rank, const void* base, uint64_t d0, uint64_t d1, uint64_t ld1, uint64_t d2,
                  uint64_t ld2, uint32_t box0, uint32_t box1);
+// A map of bytes [d1][d0], rows ld1 bytes apart, in boxes of box0 x box1 that land as they lie (no swizzle).
+bool encode_u8(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t ld1, uint32_t box0, uint32_t box1);
 
 }  // namespace tc
 }  // namespace mt
