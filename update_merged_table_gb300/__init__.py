@@ -749,4 +749,14 @@ class MergedTables:
         return gsums
 
 
-from .block import GatedNorm, GroupedLinear, NormForward, NormGrads, NormParams, Packed8, pack8, unpack8  # noqa: E402
+_BLOCK = frozenset(("Packed8", "pack8", "unpack8", "GroupedLinear", "GatedNorm", "NormParams", "NormForward", "NormGrads"))
+
+
+def __getattr__(name: str):
+    # the dense block's operators import torch, which importing this package alone does not
+    if name in _BLOCK:
+        from . import block
+        value = getattr(block, name)
+        globals()[name] = value
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

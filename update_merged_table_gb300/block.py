@@ -15,8 +15,11 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import threading
 
-from . import MT_BF16, MT_EINVAL, MT_F32, MTError, _check, _torch, load_library
+import torch
+
+from . import MT_BF16, MT_EINVAL, MT_F32, MTError, _check, load_library
 
 __all__ = ["Packed8", "pack8", "unpack8", "GroupedLinear", "GatedNorm", "NormParams", "NormForward", "NormGrads"]
 
@@ -41,57 +44,78 @@ class _GatedNorm(ctypes.Structure):
                 ("pre_weight", ctypes.c_void_p), ("pre_bias", ctypes.c_void_p)]
 
 
-def _torch_dtype(dtype: str):
-    torch = _torch()
-    return torch.float32 if dtype == "f32" else torch.bfloat16
+_TORCH = {"f32": torch.float32, "bf16": torch.bfloat16}
+_CODES = {torch.float32: MT_F32, torch.bfloat16: MT_BF16}
+_current_device = torch.cuda.current_device
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _dtype_code(t):
-    torch = _torch()
-    if t == torch.bfloat16:
-        return MT_BF16
-    if t == torch.float32:
-        return MT_F32
-    raise TypeError("rows must be float32 or bfloat16")
+    code = _CODES.get(t)
+    if code is None:
+        raise TypeError("rows must be float32 or bfloat16")
+    return code
 
 
-def _rows_2d(t, what: str, width: int | None = None, n: int | None = None, dtype=None, device=None):
-    """Check a row tensor: a CUDA tensor [n, width] whose columns are contiguous; returns its row stride."""
-    if not _torch().is_tensor(t):
-        raise TypeError(f"{what} must be a CUDA tensor")
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{what} must be a 2-D CUDA tensor")
-    if dtype is not None and t.dtype != dtype:
+def _rows_2d(t, what: str, width: int, n: int, dtype, device) -> int:
+    """The row stride of a row tensor: a CUDA tensor [n, width] of this dtype whose columns are contiguous and whose
+    rows do not overlap."""
+    try:
+        shape, (ld, step) = t.shape, t.stride()
+    except (AttributeError, ValueError):
+        raise (ValueError if torch.is_tensor(t) else TypeError)(f"{what} must be a 2-D CUDA tensor") from None
+    if shape[0] == n and shape[1] == width and step == 1 and ld >= width and t.dtype is dtype and t.device == device:
+        return ld
+    if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}")
-    if (width is not None and t.shape[1] != width) or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{what} must be [{'n' if n is None else n}, {'d' if width is None else width}], "
-                         f"not {tuple(t.shape)}")
-    if device is not None and t.device != device:
+    if t.device != device:
         raise ValueError(f"{what} is on {t.device}, not on {device}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    if tuple(shape) != (n, width):
+        raise ValueError(f"{what} must be [{n}, {width}], not {list(shape)}")
+    if width > 1 and step != 1:
         raise ValueError(f"the columns of {what} must be contiguous")
-    if t.shape[0] <= 1:
-        return max(t.shape[1], t.stride(0))
-    if t.stride(0) < t.shape[1]:
+    if n <= 1:
+        return max(width, ld)
+    if ld < width:
         raise ValueError(f"the rows of {what} overlap")
-    return t.stride(0)
+    return ld
+
+
+def _count(t, what: str) -> int:
+    """Rows of a tensor that may be a row tensor (the rest is checked by _rows_2d)."""
+    if not torch.is_tensor(t):
+        raise TypeError(f"{what} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be a 2-D CUDA tensor")
+    return t.shape[0]
+
+
+def _cuda(t, what: str):
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    return t.device
 
 
 class _On:
     """The stream a call runs on: its device made current, and torch allocating on it."""
 
+    __slots__ = ("ctx", "index")
+
     def __init__(self, device, stream):
-        torch = _torch()
-        self.ctx = None
+        self.index = device.index
         if stream is not None:
+            if stream.device.index != self.index:
+                raise ValueError(f"the stream is on {stream.device}, not on {device}")
             self.ctx = torch.cuda.stream(stream)
-        elif torch.cuda.current_device() != device.index:
+        elif _current_device() != self.index:
             self.ctx = torch.cuda.device(device)
+        else:
+            self.ctx = None
 
     def __enter__(self):
         if self.ctx is not None:
             self.ctx.__enter__()
-        return _torch().cuda.current_stream().cuda_stream
+        return _raw_stream(self.index)
 
     def __exit__(self, *a):
         if self.ctx is not None:
@@ -108,7 +132,6 @@ class Packed8:
     __slots__ = ("codes", "exps")
 
     def __init__(self, codes, exps):
-        torch = _torch()
         if codes.dim() != 2 or codes.dtype != torch.int8 or not codes.is_cuda or not codes.is_contiguous():
             raise ValueError("codes must be a contiguous int8 CUDA tensor [n, d]")
         if exps.dtype != torch.uint8 or not exps.is_contiguous() or exps.device != codes.device \
@@ -130,9 +153,10 @@ class Packed8:
 
 
 def _new_packed(n: int, d: int, device) -> Packed8:
-    torch = _torch()
-    return Packed8(torch.empty((n, d), dtype=torch.int8, device=device),
-                   torch.empty((n, -(-d // PACK_BLOCK)), dtype=torch.uint8, device=device))
+    p = Packed8.__new__(Packed8)
+    p.codes = torch.empty((n, d), dtype=torch.int8, device=device)
+    p.exps = torch.empty((n, -(-d // PACK_BLOCK)), dtype=torch.uint8, device=device)
+    return p
 
 
 def _width_ok(d: int, what: str):
@@ -142,14 +166,15 @@ def _width_ok(d: int, what: str):
 
 def pack8(x, out: Packed8 | None = None, stream=None) -> Packed8:
     """The 8-bit form of the rows x [n, d] (float32 or bfloat16; rows may be strided)."""
-    ld = _rows_2d(x, "x")
-    n, d = x.shape
+    n = _count(x, "x")
+    d, device = x.shape[1], _cuda(x, "x")
     _width_ok(d, "x")
     dt = _dtype_code(x.dtype)
-    with _On(x.device, stream) as s:
+    ld = _rows_2d(x, "x", d, n, x.dtype, device)
+    with _On(device, stream) as s:
         if out is None:
-            out = _new_packed(n, d, x.device)
-        elif out.shape != x.shape or out.device != x.device:
+            out = _new_packed(n, d, device)
+        elif out.shape != x.shape or out.device != device:
             raise ValueError("out has another shape or device")
         _check(load_library().mt_pack8(x.data_ptr(), ld, n, d, dt, out.codes.data_ptr(), out.exps.data_ptr(), s),
                "mt_pack8")
@@ -158,36 +183,57 @@ def pack8(x, out: Packed8 | None = None, stream=None) -> Packed8:
 
 def unpack8(p: Packed8, dtype=None, out=None, stream=None):
     """The values p stands for, as rows of `dtype` (bfloat16 by default, which holds them exactly)."""
-    torch = _torch()
-    n, d = p.shape
+    n, d = p.codes.shape
     _width_ok(d, "p")
-    if out is not None and dtype is not None and out.dtype != dtype:
-        raise TypeError("out has another dtype")
-    with _On(p.device, stream) as s:
+    device = p.codes.device
+    if out is not None:
+        if dtype is not None and out.dtype != dtype:
+            raise TypeError("out has another dtype")
+        dtype = out.dtype
+    elif dtype is None:
+        dtype = torch.bfloat16
+    dt = _dtype_code(dtype)
+    with _On(device, stream) as s:
+        ld = d
         if out is None:
-            out = torch.empty((n, d), dtype=dtype or torch.bfloat16, device=p.device)
-        ld = _rows_2d(out, "out", d, n, device=p.device)
-        _check(load_library().mt_unpack8(p.codes.data_ptr(), p.exps.data_ptr(), n, d, _dtype_code(out.dtype),
-                                         out.data_ptr(), ld, s), "mt_unpack8")
+            out = torch.empty((n, d), dtype=dtype, device=device)
+        else:
+            ld = _rows_2d(out, "out", d, n, dtype, device)
+        _check(load_library().mt_unpack8(p.codes.data_ptr(), p.exps.data_ptr(), n, d, dt, out.data_ptr(), ld, s),
+               "mt_unpack8")
     return out
+
+
+# Status words of the handles: one zeroed buffer per device, a word (16 bytes apart) to each handle, so that making a
+# handle neither allocates nor waits.
+_STATUS_WORDS = 1024
+_status_pool = {}
+_status_lock = threading.Lock()
+
+
+def _status_word(device):
+    with _status_lock:
+        buf, used = _status_pool.get(device, (None, _STATUS_WORDS))
+        if used == _STATUS_WORDS:
+            buf, used = torch.zeros(4 * _STATUS_WORDS, dtype=torch.int32, device=device), 0
+            torch.cuda.current_stream(device).synchronize()  # a handle's first call may come on any stream
+        _status_pool[device] = (buf, used + 1)
+    return buf[4 * used: 4 * used + 1]
 
 
 class _Handle:
     """What the block operators keep: their device, a status word and a workspace per stream."""
 
     def __init__(self, device):
-        torch = _torch()
         self.lib = load_library()
-        self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        self.device = torch.device(device) if device is not None else torch.device("cuda", _current_device())
         if self.device.index is None:
-            self.device = torch.device("cuda", torch.cuda.current_device())
-        self._status = torch.zeros(1, dtype=torch.int32, device=self.device)
-        torch.cuda.current_stream(self.device).synchronize()  # the first call may come on another stream
+            self.device = torch.device("cuda", _current_device())
+        self._status = _status_word(self.device)
         self._status_ptr = self._status.data_ptr()
         self._ws = {}
 
     def _workspace(self, stream: int, nbytes: int):
-        torch = _torch()
         buf = self._ws.get(stream)
         if buf is None or buf.numel() < nbytes:
             if torch.cuda.is_current_stream_capturing():
@@ -199,16 +245,13 @@ class _Handle:
         return buf
 
     def _offsets(self, offsets, groups: int):
-        torch = _torch()
-        if not torch.is_tensor(offsets) or offsets.dtype != torch.int64 or not offsets.is_cuda \
-                or offsets.dim() != 1 or offsets.numel() != groups + 1 or not offsets.is_contiguous() \
-                or offsets.device != self.device:
+        if not torch.is_tensor(offsets) or offsets.dtype is not torch.int64 or offsets.device != self.device \
+                or offsets.shape != (groups + 1,) or not offsets.is_contiguous():
             raise TypeError(f"offsets must be a contiguous int64 CUDA tensor [{groups + 1}] on {self.device}")
         return offsets.data_ptr()
 
     def error(self, clear: bool = False) -> int:
         """First error a call found on the device (MT_EINVAL: bad offsets), 0 if none; waits for the device."""
-        torch = _torch()
         torch.cuda.synchronize(self.device)
         e = int(self._status.item())
         if clear:
@@ -230,12 +273,13 @@ class GroupedLinear(_Handle):
         super().__init__(device)
         self.num_groups, self.in_dim, self.out_dim = num_groups, in_dim, out_dim
         self.dtype = dtype
-        self.torch_dtype = _torch_dtype(dtype)
+        self.torch_dtype = _TORCH[dtype]
         self._dt = _DTYPES[dtype]
+        self._w_shape = (num_groups, out_dim, in_dim)
 
     def _weight(self, w):
-        if tuple(w.shape) != (self.num_groups, self.out_dim, self.in_dim) or w.dtype != self.torch_dtype \
-                or not w.is_contiguous() or w.device != self.device:
+        if w.shape != self._w_shape or w.dtype is not self.torch_dtype or w.device != self.device \
+                or not w.is_contiguous():
             raise ValueError(f"weight must be a contiguous {self.torch_dtype} CUDA tensor "
                              f"[{self.num_groups}, {self.out_dim}, {self.in_dim}]")
         return w.data_ptr()
@@ -243,9 +287,8 @@ class GroupedLinear(_Handle):
     def forward(self, x, weight, offsets, out=None, stream=None):
         """y [n, out_dim] of x [n, in_dim], weight [num_groups, out_dim, in_dim] and offsets int64 CUDA
         [num_groups + 1]; rows in no group give zeros."""
-        torch = _torch()
-        ldx = _rows_2d(x, "x", self.in_dim, None, self.torch_dtype, self.device)
-        n = x.shape[0]
+        n = _count(x, "x")
+        ldx = _rows_2d(x, "x", self.in_dim, n, self.torch_dtype, self.device)
         w, off = self._weight(weight), self._offsets(offsets, self.num_groups)
         with _On(self.device, stream) as s:
             if out is None:
@@ -262,9 +305,8 @@ class GroupedLinear(_Handle):
                  stream=None):
         """(dx [n, in_dim], dw fp32 [num_groups, out_dim, in_dim]) of dy [n, out_dim]; x: the forward's input, plain
         or ``Packed8`` (None without want_dw)."""
-        torch = _torch()
-        lddy = _rows_2d(dy, "dy", self.out_dim, None, self.torch_dtype, self.device)
-        n = dy.shape[0]
+        n = _count(dy, "dy")
+        lddy = _rows_2d(dy, "dy", self.out_dim, n, self.torch_dtype, self.device)
         if not want_dx and not want_dw:
             raise ValueError("nothing to compute")
         w = self._weight(weight) if want_dx else None
@@ -291,7 +333,7 @@ class GroupedLinear(_Handle):
                     return dx, None
             ws_ptr, ws_len = None, 0
             if want_dw:
-                shape = (self.num_groups, self.out_dim, self.in_dim)
+                shape = self._w_shape
                 dw = out_dw
                 if dw is None:
                     dw = torch.empty(shape, dtype=torch.float32, device=self.device)
@@ -359,12 +401,12 @@ class GatedNorm(_Handle):
             raise MTError(MT_EINVAL, "GatedNorm")
         super().__init__(device)
         self.dim, self.num_groups, self.kind, self.gate, self.eps, self.dtype = dim, num_groups, kind, gate, eps, dtype
-        self.torch_dtype = _torch_dtype(dtype)
+        self.torch_dtype = _TORCH[dtype]
+        self._p_shapes = ((num_groups, dim), (dim,)) if num_groups == 1 else ((num_groups, dim),)
+        self._codes = (_DTYPES[dtype], _KINDS[kind], _GATES[gate])
 
     def _config(self, n: int, params: NormParams, offsets) -> _GatedNorm:
-        torch = _torch()
-        c = _GatedNorm(n, self.dim, self.num_groups, _DTYPES[self.dtype], _KINDS[self.kind], _GATES[self.gate],
-                       self.eps, None, self._status_ptr)
+        c = _GatedNorm(n, self.dim, self.num_groups, *self._codes, self.eps, None, self._status_ptr)
         if offsets is not None:
             c.offsets = self._offsets(offsets, self.num_groups)
         elif self.num_groups != 1:
@@ -373,13 +415,13 @@ class GatedNorm(_Handle):
             t = getattr(params, name)
             if t is None:
                 continue
-            if t.dtype != torch.float32 or not t.is_contiguous() or t.device != self.device \
-                    or tuple(t.shape) not in ((self.num_groups, self.dim), (self.dim,) if self.num_groups == 1 else ()):
+            if t.dtype is not torch.float32 or t.device != self.device or t.shape not in self._p_shapes \
+                    or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous float32 CUDA tensor [{self.num_groups}, {self.dim}]")
             setattr(c, name, t.data_ptr())
         return c
 
-    def _plain(self, t, what: str, n: int | None):
+    def _plain(self, t, what: str, n: int):
         if t is None:
             return _Rows()
         ld = _rows_2d(t, what, self.dim, n, self.torch_dtype, self.device)
@@ -409,11 +451,10 @@ class GatedNorm(_Handle):
                 stream=None) -> NormForward:
         """One pass over the rows x, y, u [n, dim].  Without y, z is x itself.  pack: the letters of the checkpoints to
         write, any of "yuzh" (``packed`` holds them by letter)."""
-        torch = _torch()
         params = params if params is not None else NormParams()
         self._parts(y, u, params)
-        rx = self._plain(x, "x", None)
-        n = x.shape[0]
+        n = _count(x, "x")
+        rx = self._plain(x, "x", n)
         ry, ru = self._plain(y, "y", n), self._plain(u, "u", n)
         c = self._config(n, params, offsets)
         if y is None:
@@ -425,14 +466,14 @@ class GatedNorm(_Handle):
             if y is not None:
                 z = out_z if out_z is not None else torch.empty((n, self.dim), dtype=self.torch_dtype,
                                                                 device=self.device)
-                rz = self._plain(z, "out_z", n)
+                rz = self._plain(z, "out_z", n) if out_z is not None else _Rows(z.data_ptr(), self.dim)
             elif out_z is not None:
                 raise ValueError("without y there is no z to write")
             h = None
             if has_h:
                 h = out_h if out_h is not None else torch.empty((n, self.dim), dtype=self.torch_dtype,
                                                                 device=self.device)
-                rh = self._plain(h, "out_h", n)
+                rh = self._plain(h, "out_h", n) if out_h is not None else _Rows(h.data_ptr(), self.dim)
             elif out_h is not None:
                 raise ValueError("without pre_weight there is no h to write")
             packed = {}
@@ -454,7 +495,6 @@ class GatedNorm(_Handle):
         """Gradients from dz [n, dim] (None: zero) and dh (None without pre_weight).  y, u, z: the forward's, each
         plain or ``Packed8``; z is needed with pre_weight only.  out_dy and out_du may be column slices of one
         tensor (the gradient of a product that made y and u side by side)."""
-        torch = _torch()
         params = params if params is not None else NormParams()
         self._parts(y, u, params)
         has_h = params.pre_weight is not None
@@ -465,7 +505,7 @@ class GatedNorm(_Handle):
         lead = dh if has_h else dz
         if lead is None:
             raise ValueError("dz is needed without pre_weight")
-        n = lead.shape[0]
+        n = _count(lead, "dh" if has_h else "dz")
         rdz, rdh = self._plain(dz, "dz", n), self._plain(dh, "dh", n)
         ry, ru, rz = self._saved(y, "y", n), self._saved(u, "u", n), self._saved(z if has_h else None, "z", n)
         c = self._config(n, params, offsets)
@@ -473,8 +513,10 @@ class GatedNorm(_Handle):
             c.gate = 0
         with _On(self.device, stream) as s:
             def rows(out, what):
-                t = out if out is not None else torch.empty((n, self.dim), dtype=self.torch_dtype, device=self.device)
-                return t, self._plain(t, what, n)
+                if out is not None:
+                    return out, self._plain(out, what, n)
+                t = torch.empty((n, self.dim), dtype=self.torch_dtype, device=self.device)
+                return t, _Rows(t.data_ptr(), self.dim)
 
             dx, rdx = rows(out_dx, "out_dx")
             dy, rdy = rows(out_dy, "out_dy") if y is not None else (None, _Rows())

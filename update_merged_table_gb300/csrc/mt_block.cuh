@@ -136,11 +136,23 @@ __device__ __forceinline__ float pack_inv(uint32_t byte) {  // 2^-e; 0 for a blo
 __device__ __forceinline__ float pack_scale(uint32_t byte) {  // 2^e, or NaN
   return byte == kPackNan ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte << 23);
 }
-__device__ __forceinline__ int pack_code(float x, float inv) {
-  if (inv == 0.0f) return 0;
-  const int q = __float2int_rn(x * inv);
-  return q < -127 ? -127 : (q > 127 ? 127 : q);
+// The codes of four columns as bytes, v[j] = x[j] * 2^-e with |v[j]| <= 127.  Adding 1.5 * 2^23 rounds a product to
+// the nearest integer (ties to even) in the last bits of the sum, whose low byte is then the code; the product itself
+// is exact, so a fused multiply-add rounds once.
+__device__ __forceinline__ uint32_t pack_codes4(float x0, float x1, float x2, float x3, float inv) {
+  constexpr float kMagic = 12582912.0f;
+  const uint32_t a = __float_as_uint(fmaf(x0, inv, kMagic)), b = __float_as_uint(fmaf(x1, inv, kMagic));
+  const uint32_t c = __float_as_uint(fmaf(x2, inv, kMagic)), d = __float_as_uint(fmaf(x3, inv, kMagic));
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
+// The same where the codes have to be clamped to [-127, 127] (the exponent is at its upper end), or the block is not
+// finite (codes 0).
+__device__ __forceinline__ uint32_t pack_codes4_edge(float x0, float x1, float x2, float x3, float inv) {
+  if (inv == 0.0f) return 0u;
+  auto cut = [&](float x) { return fminf(fmaxf(x * inv, -127.0f), 127.0f); };
+  return pack_codes4(cut(x0), cut(x1), cut(x2), cut(x3), 1.0f);
+}
+constexpr uint32_t kPackEdge = 248;  // exponent bytes from here on take the edge form
 
 // ---- eight columns of a row --------------------------------------------------------
 
@@ -230,18 +242,20 @@ __device__ __forceinline__ Raw8<T> load8(const Rows& r, long long row, int vec, 
   return v;
 }
 
-// Byte j of w, as the signed number it holds.
-__device__ __forceinline__ float code_f(uint32_t w, int j) { return (float)(int8_t)(w >> (8 * j)); }
+// The signed bytes of w times s: with the sign bit flipped a byte is q + 128, which stands in the last bits of
+// 2^23 + 128 + q; taking 2^23 + 128 off leaves q exactly.
+__device__ __forceinline__ void codes_f(uint32_t w, float s, float* f) {
+  const uint32_t x = w ^ 0x80808080u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] = (__uint_as_float(__byte_perm(x, 0x4B000000u, 0x7540 + j)) - 8388736.0f) * s;
+}
 
 template <typename T>
 __device__ __forceinline__ void widen8(const Raw8<T>& v, bool packed, float f[8]) {
   if (packed) {
     const float s = pack_scale(v.a.z);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[j] = code_f(v.a.x, j) * s;
-      f[4 + j] = code_f(v.a.y, j) * s;
-    }
+    codes_f(v.a.x, s, f);
+    codes_f(v.a.y, s, f + 4);
   } else if constexpr (sizeof(T) == 4) {
     const uint32_t w[8] = {v.a.x, v.a.y, v.a.z, v.a.w, v.b.x, v.b.y, v.b.z, v.b.w};
 #pragma unroll
@@ -293,9 +307,14 @@ __device__ __forceinline__ void store_packed8(const Rows& r, long long row, int 
   if (!live || c0 >= d) return;
   const uint32_t byte = pack_exp_byte(top);
   const float inv = pack_inv(byte);
-  uint32_t w[2] = {0u, 0u};
-#pragma unroll
-  for (int j = 0; j < 8; ++j) w[j >> 2] |= (uint32_t)(uint8_t)(int8_t)pack_code(f[j], inv) << (8 * (j & 3));
+  uint32_t w[2];
+  if (byte < kPackEdge) {
+    w[0] = pack_codes4(f[0], f[1], f[2], f[3], inv);
+    w[1] = pack_codes4(f[4], f[5], f[6], f[7], inv);
+  } else {
+    w[0] = pack_codes4_edge(f[0], f[1], f[2], f[3], inv);
+    w[1] = pack_codes4_edge(f[4], f[5], f[6], f[7], inv);
+  }
   int8_t* p = r.codes + row * d + c0;
   if constexpr (AL) {
     *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);

@@ -12,11 +12,14 @@
 // checkpoints in 8 bits need nothing stored beside them.
 //
 // Kernels:
-//  k_norm_fwd    teams stride over the rows.
-//  k_norm_bwd    a block per chunk of rows of one group: the parameter
-//                gradients of the chunk stay in registers and leave as one
-//                partial sum per chunk (no atomics, so the sums have one order).
-//  k_norm_sums   the chunks' partial sums of each group, in fp64.
+//  k_norm_fwd    each block takes an even run of the rows in the groups; teams
+//                stride over it.
+//  k_norm_bwd    the same split; the parameter gradients of a run stay in
+//                registers and leave as one partial sum per block and group (no
+//                atomics, so the sums have one order).  With S1 = sum D a yh and
+//                S2 = sum D a, dwp = s S1, dbp = s S2 and ds = wp S1 + bp S2: two
+//                sums for three gradients, and one when there is no bp.
+//  k_norm_sums   the blocks' partial sums of each group, in fp64.
 #include <algorithm>
 
 #include "mt_block.cuh"
@@ -24,9 +27,8 @@
 namespace mt {
 namespace {
 
-constexpr int kNV = 2;         // vectors of eight columns per lane
-constexpr int kNormThreads = 256;
-constexpr int kSums = 5;       // partial sums: dwp, dbp, ds, dwq, dbq
+constexpr int kNV = 2;   // vectors of eight columns per lane
+constexpr int kSums = 4; // partial sums: S1 = sum D a yh, S2 = sum D a, T1 = sum dh zh, T2 = sum dh
 
 struct NormParams {
   long long n;
@@ -37,12 +39,17 @@ struct NormParams {
   const float *wp, *bp, *sc, *wq, *bq;
   Rows x, y, u, z, h;            // forward
   Rows dz, dh, dx, dy, du;       // backward (with y, u, z)
-  float* part;                   // [chunks][kSums][d]
+  float* part;                   // [blocks + groups - 1][kSums][d]: block b's sums over group g at b + g
   float *dwp, *dbp, *dsc, *dwq, *dbq;
   int log_team;                  // log2 lanes per row
-  int chunk_rows, chunks;        // chunks: upper bound (the launch's grid)
+  int blocks;                    // blocks of k_norm_bwd
   int wide;                      // parameters reached with 16-byte loads
 };
+
+// The rows of block b of B: an even run of the rows [off0, off0 + m) that lie in groups.
+__device__ __forceinline__ long long run_start(long long off0, long long m, int b, int B) { return off0 + m * b / B; }
+// The block whose run holds the row off0 + r (0 <= r < m).
+__device__ __forceinline__ int run_of(long long r, long long m, int B) { return (int)(((r + 1) * B - 1) / m); }
 
 // Sums a and b over a team: shuffles inside a warp, shared memory across a team's warps.  A team of more than one
 // warp owns the named barrier 1 + team; `slot` alternates so that one barrier per call is enough.
@@ -95,127 +102,186 @@ __device__ __forceinline__ float gate_value(int gate, float u, float& da) {
   }
   float p;
   if constexpr (sizeof(T) == 4) p = 1.0f / (1.0f + expf(-u));
-  else p = __frcp_rn(1.0f + __expf(-u));
+  else p = __fdividef(1.0f, 1.0f + __expf(-fmaxf(u, -80.0f)));  // the fast division is 0 past 2^126: exp(80) < 2^116
   if (gate == MT_GATE_SIGMOID) {
     da = p * (1.0f - p);
     return p;
   }
-  da = p * (1.0f + u * (1.0f - p));
-  // silu(-inf) = -inf * 0 is NaN by the formula; u * p keeps that
-  return u * p;
+  const float a = u * p;
+  da = p + a * (1.0f - p);
+  return a;
 }
 
-// Mean (layer norm; 0 for rms) and inverse deviation of the row held in v; columns past d are zero and stay out.
-__device__ __forceinline__ void row_stats(const float (&v)[kNV][8], const NormParams& p, int team, int lt, float2* s_red,
-                                          int& slot, float& mean, float& r) {
+// Mean (layer norm; 0 for rms) and inverse deviation of the rows held in v and w at once (one of them may be absent:
+// zeros).  Columns past d hold zeros and stay out of the deviation.
+struct Stats {
+  float mean, r;
+};
+__device__ __forceinline__ void row_stats2(const float (&v)[kNV][8], const float (&w)[kNV][8], const NormParams& p,
+                                           int team, int lt, float2* s_red, int& slot, Stats& sv, Stats& sw) {
   float a = 0.0f, b = 0.0f;
-  mean = 0.0f;
   const float inv_d = 1.0f / (float)p.d;
+  sv.mean = sw.mean = 0.0f;
   if (p.kind == MT_NORM_LAYER) {
 #pragma unroll
     for (int k = 0; k < kNV; ++k)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) a += v[k][j];
+      for (int j = 0; j < 8; ++j) {
+        a += v[k][j];
+        b += w[k][j];
+      }
     team_sum2(a, b, team, s_red, slot);
-    mean = a * inv_d;
-    a = 0.0f;
-  }
+    sv.mean = a * inv_d;
+    sw.mean = b * inv_d;
+    a = b = 0.0f;
 #pragma unroll
-  for (int k = 0; k < kNV; ++k) {
-    const int left = p.d - (k * team + lt) * 8;
+    for (int k = 0; k < kNV; ++k) {
+      const int left = p.d - (k * team + lt) * 8;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float c = j < left ? v[k][j] - mean : 0.0f;
-      a += c * c;
+      for (int j = 0; j < 8; ++j) {
+        const float c = j < left ? v[k][j] - sv.mean : 0.0f, e = j < left ? w[k][j] - sw.mean : 0.0f;
+        a += c * c;
+        b += e * e;
+      }
     }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kNV; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        a += v[k][j] * v[k][j];
+        b += w[k][j] * w[k][j];
+      }
   }
-  b = 0.0f;
   team_sum2(a, b, team, s_red, slot);
-  r = rsqrtf(a * inv_d + p.eps);
+  sv.r = rsqrtf(a * inv_d + p.eps);
+  sw.r = rsqrtf(b * inv_d + p.eps);
+}
+__device__ __forceinline__ Stats row_stats(const float (&v)[kNV][8], const NormParams& p, int team, int lt, float2* s_red,
+                                           int& slot) {
+  Stats a, b;
+  const float none[kNV][8] = {};
+  row_stats2(v, none, p, team, lt, s_red, slot, a, b);
+  return a;
 }
 
+// Blocks of 128 threads that share an SM's registers (wider rows: one block of 512).
+constexpr int kFwdBlocks = 6, kBwdBlocks = 3;
+
 template <typename T, bool AL, int THREADS>
-__global__ void __launch_bounds__(THREADS) k_norm_fwd(const NormParams p) {
+__global__ void __launch_bounds__(THREADS, THREADS == 128 ? (sizeof(T) == 4 ? 4 : kFwdBlocks) : 1)
+k_norm_fwd(const NormParams p) {
   extern __shared__ long long s_off[];
   __shared__ float2 s_red[32];
   load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
   const int team = 1 << p.log_team;
   const int lt = threadIdx.x & (team - 1);
   const int sub = threadIdx.x >> p.log_team;
-  const int teams = blockDim.x >> p.log_team;  // teams per block
+  const int teams = THREADS >> p.log_team;  // teams per block
   const bool has_y = p.y.data != nullptr, has_u = p.u.data != nullptr, has_h = p.wq != nullptr;
-  const bool put_z = p.z.data != nullptr || p.z.codes != nullptr;
+  const long long off0 = s_off[0], m = s_off[p.groups] - off0;
   int slot = 0;
-  // every team of a block runs the same number of rounds, so the shuffles and barriers meet
-  for (long long base = (long long)blockIdx.x * teams; base < p.n; base += (long long)gridDim.x * teams) {
-    const long long row = base + sub;
-    const int g = row < p.n ? row_group(s_off, p.groups, row) : -1;
-    const bool in = row < p.n, live = g >= 0;
-    Raw8<T> rx[kNV], ry[kNV], ru[kNV];
-#pragma unroll
-    for (int k = 0; k < kNV; ++k) {
-      const int vec = k * team + lt, dd = live ? p.d : 0;
-      const long long rr = live ? row : 0;
-      rx[k] = load8<T, AL>(p.x, rr, vec, dd);
-      if (has_y) ry[k] = load8<T, AL>(p.y, rr, vec, dd);
-      if (has_u) ru[k] = load8<T, AL>(p.u, rr, vec, dd);
-    }
-    float z[kNV][8], mean, r;
-#pragma unroll
-    for (int k = 0; k < kNV; ++k) widen8<T>(rx[k], false, z[k]);
-    if (has_y) {
-      float y[kNV][8];
-#pragma unroll
-      for (int k = 0; k < kNV; ++k) {
-        widen8<T>(ry[k], false, y[k]);
-        if (p.y.codes != nullptr) store_packed8<AL>(p.y, row, k * team + lt, p.d, y[k], in);
-      }
-      row_stats(y, p, team, lt, s_red, slot, mean, r);
-#pragma unroll
-      for (int k = 0; k < kNV; ++k) {
-        const int vec = k * team + lt;
-        float w[8], b[8], s[8], u[8];
-        param8(p.wp, live ? g : 0, vec, p.d, p.wide, 1.0f, w);
-        param8(p.bp, live ? g : 0, vec, p.d, p.wide, 0.0f, b);
-        param8(p.sc, live ? g : 0, vec, p.d, p.wide, 1.0f, s);
-        if (has_u) {
-          widen8<T>(ru[k], false, u);
-          if (p.u.codes != nullptr) store_packed8<AL>(p.u, row, vec, p.d, u, in);
-        }
-        const int left = p.d - vec * 8;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float t = (w[j] * ((y[k][j] - mean) * r) + b[j]) * s[j], da;
-          if (has_u) t *= gate_value<T>(p.gate, u[j], da);
-          if (live && j < left) z[k][j] += t;
-        }
-      }
-    }
-    if (has_h) row_stats(z, p, team, lt, s_red, slot, mean, r);
+
+  // rows in no group: zeros, and their checkpoints zeros
+  for (long long q0 = (long long)blockIdx.x * teams; q0 < p.n - m; q0 += (long long)gridDim.x * teams) {
+    const long long q = q0 + sub, row = q < off0 ? q : q + m;
+    const bool in = q < p.n - m;
 #pragma unroll
     for (int k = 0; k < kNV; ++k) {
       const int vec = k * team + lt;
-      if (has_h) {
-        float w[8], b[8], h[8];
-        param8(p.wq, live ? g : 0, vec, p.d, p.wide, 1.0f, w);
-        param8(p.bq, live ? g : 0, vec, p.d, p.wide, 0.0f, b);
-        const int left = p.d - vec * 8;
+      float zero[8] = {};
+      if (in && p.z.data != nullptr) store8<T, AL>(p.z.data, p.z.ld, row, vec, p.d, zero);
+      if (in && has_h) store8<T, AL>(p.h.data, p.h.ld, row, vec, p.d, zero);
+      if (p.y.codes != nullptr) store_packed8<AL>(p.y, row, vec, p.d, zero, in);
+      if (p.u.codes != nullptr) store_packed8<AL>(p.u, row, vec, p.d, zero, in);
+      if (p.z.codes != nullptr) store_packed8<AL>(p.z, row, vec, p.d, zero, in);
+      if (p.h.codes != nullptr) store_packed8<AL>(p.h, row, vec, p.d, zero, in);
+    }
+  }
+
+  const long long end = run_start(off0, m, blockIdx.x + 1, gridDim.x);
+  long long first = run_start(off0, m, blockIdx.x, gridDim.x);
+  for (int g = first < end ? row_group(s_off, p.groups, first) : 0; first < end; ++g) {
+    const long long last = min(end, s_off[g + 1]);
+    // every team of the block runs the same number of rounds, so the shuffles and barriers meet
+    for (long long base = first; base < last; base += teams) {
+      const bool live = base + sub < last;
+      const long long row = live ? base + sub : base;
+      const int dd = live ? p.d : 0;
+      Raw8<T> rx[kNV], ry[kNV], ru[kNV];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = live && j < left ? w[j] * ((z[k][j] - mean) * r) + b[j] : 0.0f;
-        if (in) store8<T, AL>(p.h.data, p.h.ld, row, vec, p.d, h);
-        if (p.h.codes != nullptr) store_packed8<AL>(p.h, row, vec, p.d, h, in);
+      for (int k = 0; k < kNV; ++k) {
+        const int vec = k * team + lt;
+        if (has_y) ry[k] = load8<T, AL>(p.y, row, vec, dd);
+        rx[k] = load8<T, AL>(p.x, row, vec, dd);
+        if (has_u) ru[k] = load8<T, AL>(p.u, row, vec, dd);
       }
-      if (put_z) {
-        if (p.z.data != nullptr && in) store8<T, AL>(p.z.data, p.z.ld, row, vec, p.d, z[k]);
-        if (p.z.codes != nullptr) store_packed8<AL>(p.z, row, vec, p.d, z[k], in);
+      float z[kNV][8];
+      if (has_y) {
+        float y[kNV][8];
+#pragma unroll
+        for (int k = 0; k < kNV; ++k) widen8<T>(ry[k], false, y[k]);
+        const Stats st = row_stats(y, p, team, lt, s_red, slot);
+#pragma unroll
+        for (int k = 0; k < kNV; ++k) {
+          const int vec = k * team + lt;
+          if (p.y.codes != nullptr) store_packed8<AL>(p.y, row, vec, p.d, y[k], live);
+          float w[8], b[8], s[8], u[8];
+          param8(p.wp, g, vec, p.d, p.wide, 1.0f, w);
+          param8(p.bp, g, vec, p.d, p.wide, 0.0f, b);
+          param8(p.sc, g, vec, p.d, p.wide, 1.0f, s);
+          if (has_u) {
+            widen8<T>(ru[k], false, u);
+            if (p.u.codes != nullptr) store_packed8<AL>(p.u, row, vec, p.d, u, live);
+          }
+          widen8<T>(rx[k], false, z[k]);
+          const int left = p.d - vec * 8;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float t = (w[j] * ((y[k][j] - st.mean) * st.r) + b[j]) * s[j], da;
+            if (has_u) t *= gate_value<T>(p.gate, u[j], da);
+            if (AL || j < left) z[k][j] += t;
+          }
+          if (AL && left <= 0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) z[k][j] = 0.0f;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < kNV; ++k) widen8<T>(rx[k], false, z[k]);
+      }
+      if (has_h) {
+        const Stats st = row_stats(z, p, team, lt, s_red, slot);
+#pragma unroll
+        for (int k = 0; k < kNV; ++k) {
+          const int vec = k * team + lt, left = p.d - vec * 8;
+          float w[8], b[8], h[8];
+          param8(p.wq, g, vec, p.d, p.wide, 1.0f, w);
+          param8(p.bq, g, vec, p.d, p.wide, 0.0f, b);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            h[j] = w[j] * ((z[k][j] - st.mean) * st.r) + b[j];
+            if (AL ? left <= 0 : j >= left) h[j] = 0.0f;
+          }
+          if (live) store8<T, AL>(p.h.data, p.h.ld, row, vec, p.d, h);
+          if (p.h.codes != nullptr) store_packed8<AL>(p.h, row, vec, p.d, h, live);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kNV; ++k) {
+        const int vec = k * team + lt;
+        if (p.z.data != nullptr && live) store8<T, AL>(p.z.data, p.z.ld, row, vec, p.d, z[k]);
+        if (p.z.codes != nullptr) store_packed8<AL>(p.z, row, vec, p.d, z[k], live);
       }
     }
+    first = last;
   }
 }
 
 // dv = r * (dvh - [mean dvh] - vh * mean(dvh * vh)), the gradient through a norm, in place of dvh.
 __device__ __forceinline__ void norm_grad(float (&dvh)[kNV][8], const float (&vh)[kNV][8], float r, const NormParams& p,
-                                          int team, int lt, float2* s_red, int& slot) {
+                                          int team, float2* s_red, int& slot) {
   float a = 0.0f, b = 0.0f;
 #pragma unroll
   for (int k = 0; k < kNV; ++k)
@@ -226,35 +292,35 @@ __device__ __forceinline__ void norm_grad(float (&dvh)[kNV][8], const float (&vh
     }
   team_sum2(a, b, team, s_red, slot);
   const float inv_d = 1.0f / (float)p.d;
-  const float ma = a * inv_d, mb = p.kind == MT_NORM_LAYER ? b * inv_d : 0.0f;
+  const float ma = r * a * inv_d, mb = p.kind == MT_NORM_LAYER ? r * b * inv_d : 0.0f;
 #pragma unroll
   for (int k = 0; k < kNV; ++k)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dvh[k][j] = r * (dvh[k][j] - mb - vh[k][j] * ma);
+    for (int j = 0; j < 8; ++j) dvh[k][j] = r * dvh[k][j] - mb - vh[k][j] * ma;
 }
 
-template <typename T, bool AL, int THREADS>
-__global__ void __launch_bounds__(THREADS) k_norm_bwd(const NormParams p) {
-  extern __shared__ long long s_off[];  // [groups + 1], then int [groups + 1] chunks before each group
+// BIAS: the norms have biases (their sums S2 and T2 are kept too).
+template <typename T, bool AL, int THREADS, bool BIAS>
+__global__ void __launch_bounds__(THREADS, THREADS == 128 ? (sizeof(T) == 4 ? 2 : kBwdBlocks) : 1)
+k_norm_bwd(const NormParams p) {
+  constexpr int kAcc = BIAS ? 4 : 2;       // S1, T1, S2, T2
+  extern __shared__ long long s_off[];     // [groups + 1], then the sums of the block's teams: teams * d floats
   __shared__ float2 s_red[32];
-  __shared__ float s_sum[8192];         // one parameter's sums of the block's teams: teams * d <= 8192
-  int* s_cum = reinterpret_cast<int*>(s_off + p.groups + 1);
+  float* s_sum = reinterpret_cast<float*>(s_off + p.groups + 1);
   load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
-  count_tiles(s_off, p.groups, p.chunk_rows, s_cum);
   const int team = 1 << p.log_team;
   const int lt = threadIdx.x & (team - 1);
   const int sub = threadIdx.x >> p.log_team;
-  const int teams = blockDim.x >> p.log_team;
+  const int teams = THREADS >> p.log_team;
   const bool has_y = p.y.data != nullptr || p.y.codes != nullptr, has_u = p.u.data != nullptr || p.u.codes != nullptr;
   const bool has_h = p.wq != nullptr, has_dz = p.dz.data != nullptr;
   const bool y8 = p.y.data == nullptr, u8 = p.u.data == nullptr, z8 = p.z.data == nullptr;
-  const int total = s_cum[p.groups];
+  const long long off0 = s_off[0], m = s_off[p.groups] - off0;
   int slot = 0;
 
   // rows in no group: their gradients are zero
-  const long long outside = s_off[0] + (p.n - s_off[p.groups]);
-  for (long long q = (long long)blockIdx.x * teams + sub; q < outside; q += (long long)gridDim.x * teams) {
-    const long long row = q < s_off[0] ? q : q - s_off[0] + s_off[p.groups];
+  for (long long q = (long long)blockIdx.x * teams + sub; q < p.n - m; q += (long long)gridDim.x * teams) {
+    const long long row = q < off0 ? q : q + m;
     float zero[8] = {};
 #pragma unroll
     for (int k = 0; k < kNV; ++k) {
@@ -265,59 +331,59 @@ __global__ void __launch_bounds__(THREADS) k_norm_bwd(const NormParams p) {
     }
   }
 
-  for (int c = blockIdx.x; c < total; c += gridDim.x) {
-    const int g = tile_group(s_cum, p.groups, c);
-    const long long first = s_off[g] + (long long)(c - s_cum[g]) * p.chunk_rows;
-    const long long last = min(first + p.chunk_rows, s_off[g + 1]);
-    float acc[kSums][kNV][8];
+  const long long end = run_start(off0, m, blockIdx.x + 1, gridDim.x);
+  long long first = run_start(off0, m, blockIdx.x, gridDim.x);
+  for (int g = first < end ? row_group(s_off, p.groups, first) : 0; first < end; ++g) {
+    const long long last = min(end, s_off[g + 1]);
+    if (last <= first) continue;  // an empty group
+    float acc[kAcc][kNV][8];
 #pragma unroll
-    for (int q = 0; q < kSums; ++q)
+    for (int q = 0; q < kAcc; ++q)
 #pragma unroll
       for (int k = 0; k < kNV; ++k)
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[q][k][j] = 0.0f;
     for (long long base = first; base < last; base += teams) {
-      const long long row = base + sub;
-      const bool live = row < last;
-      const int dd = live ? p.d : 0;
-      const long long rr = live ? row : first;
+      const bool live = base + sub < last;
+      const long long row = live ? base + sub : base;
+      const int dd = live ? p.d : 0;  // a team without a row computes on zeros
       Raw8<T> ry[kNV], ru[kNV], rz[kNV], rdz[kNV], rdh[kNV];
 #pragma unroll
       for (int k = 0; k < kNV; ++k) {
         const int vec = k * team + lt;
-        if (has_h) {
-          rz[k] = load8<T, AL>(p.z, rr, vec, dd);
-          rdh[k] = load8<T, AL>(p.dh, rr, vec, dd);
-        }
-        if (has_dz) rdz[k] = load8<T, AL>(p.dz, rr, vec, dd);
-        if (has_y) ry[k] = load8<T, AL>(p.y, rr, vec, dd);
-        if (has_u) ru[k] = load8<T, AL>(p.u, rr, vec, dd);
+        if (has_h) rz[k] = load8<T, AL>(p.z, row, vec, dd);
+        if (has_y) ry[k] = load8<T, AL>(p.y, row, vec, dd);
+        if (has_h) rdh[k] = load8<T, AL>(p.dh, row, vec, dd);
+        if (has_dz) rdz[k] = load8<T, AL>(p.dz, row, vec, dd);
+        if (has_u) ru[k] = load8<T, AL>(p.u, row, vec, dd);
       }
-      float D[kNV][8], mean, r;
-#pragma unroll
-      for (int k = 0; k < kNV; ++k)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) D[k][j] = 0.0f;
-      if (has_h) {  // through the next block's norm
-        float zh[kNV][8];
-#pragma unroll
-        for (int k = 0; k < kNV; ++k) widen8<T>(rz[k], z8, zh[k]);
-        row_stats(zh, p, team, lt, s_red, slot, mean, r);
+      Stats sy, sz;
+      float yh[kNV][8] = {}, D[kNV][8] = {};
+      {
+        float zh[kNV][8] = {};
 #pragma unroll
         for (int k = 0; k < kNV; ++k) {
-          const int vec = k * team + lt, left = p.d - vec * 8;
-          float dh[8], w[8];
-          widen8<T>(rdh[k], false, dh);
-          param8(p.wq, g, vec, p.d, p.wide, 1.0f, w);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            zh[k][j] = live && j < left ? (zh[k][j] - mean) * r : 0.0f;
-            acc[3][k][j] += dh[j] * zh[k][j];
-            acc[4][k][j] += dh[j];
-            D[k][j] = j < left ? dh[j] * w[j] : 0.0f;
-          }
+          if (has_h) widen8<T>(rz[k], z8, zh[k]);
+          if (has_y) widen8<T>(ry[k], y8, yh[k]);
         }
-        norm_grad(D, zh, r, p, team, lt, s_red, slot);
+        row_stats2(yh, zh, p, team, lt, s_red, slot, sy, sz);
+        if (has_h) {  // through the next block's norm
+#pragma unroll
+          for (int k = 0; k < kNV; ++k) {
+            const int vec = k * team + lt, left = p.d - vec * 8;
+            float dh[8], w[8];
+            widen8<T>(rdh[k], false, dh);
+            param8(p.wq, g, vec, p.d, p.wide, 1.0f, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              zh[k][j] = (AL ? left > 0 : j < left) ? (zh[k][j] - sz.mean) * sz.r : 0.0f;
+              acc[1][k][j] += dh[j] * zh[k][j];
+              if constexpr (BIAS) acc[3][k][j] += dh[j];
+              D[k][j] = dh[j] * w[j];  // dh is zero past d
+            }
+          }
+          norm_grad(D, zh, sz.r, p, team, s_red, slot);
+        }
       }
       if (has_dz) {
 #pragma unroll
@@ -329,10 +395,7 @@ __global__ void __launch_bounds__(THREADS) k_norm_bwd(const NormParams p) {
         }
       }
       if (has_y) {
-        float yh[kNV][8], dyh[kNV][8];
-#pragma unroll
-        for (int k = 0; k < kNV; ++k) widen8<T>(ry[k], y8, yh[k]);
-        row_stats(yh, p, team, lt, s_red, slot, mean, r);
+        float dyh[kNV][8];
 #pragma unroll
         for (int k = 0; k < kNV; ++k) {
           const int vec = k * team + lt, left = p.d - vec * 8;
@@ -343,22 +406,19 @@ __global__ void __launch_bounds__(THREADS) k_norm_bwd(const NormParams p) {
           if (has_u) widen8<T>(ru[k], u8, u);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const bool on = live && j < left;
-            yh[k][j] = on ? (yh[k][j] - mean) * r : 0.0f;
+            const bool on = AL ? left > 0 : j < left;
+            yh[k][j] = on ? (yh[k][j] - sy.mean) * sy.r : 0.0f;
             float a = 1.0f, da = 0.0f;
             if (has_u) a = gate_value<T>(p.gate, u[j], da);
-            const float t = w[j] * yh[k][j] + b[j];
-            const float dst = D[k][j] * s[j];
-            const float dt = on ? dst * a : 0.0f;
-            du[j] = dst * t * da;
-            acc[0][k][j] += dt * yh[k][j];
-            acc[1][k][j] += dt;
-            acc[2][k][j] += on ? D[k][j] * t * a : 0.0f;
-            dyh[k][j] = on ? dt * w[j] : 0.0f;
+            const float Da = on && live ? D[k][j] * a : 0.0f, Ds = D[k][j] * s[j];
+            acc[0][k][j] += Da * yh[k][j];
+            if constexpr (BIAS) acc[2][k][j] += Da;
+            dyh[k][j] = Da * s[j] * w[j];
+            du[j] = Ds * (w[j] * yh[k][j] + b[j]) * da;
           }
           if (has_u && live) store8<T, AL>(p.du.data, p.du.ld, row, vec, p.d, du);
         }
-        norm_grad(dyh, yh, r, p, team, lt, s_red, slot);
+        norm_grad(dyh, yh, sy.r, p, team, s_red, slot);
         if (live) {
 #pragma unroll
           for (int k = 0; k < kNV; ++k) store8<T, AL>(p.dy.data, p.dy.ld, row, k * team + lt, p.d, dyh[k]);
@@ -369,10 +429,10 @@ __global__ void __launch_bounds__(THREADS) k_norm_bwd(const NormParams p) {
         for (int k = 0; k < kNV; ++k) store8<T, AL>(p.dx.data, p.dx.ld, row, k * team + lt, p.d, D[k]);
       }
     }
-    // the chunk's sums: the teams' registers meet in shared memory, one parameter at a time, in the teams' order
+    // the run's sums: the teams' registers meet in shared memory, one sum at a time, in the teams' order
 #pragma unroll
-    for (int q = 0; q < kSums; ++q) {
-      if (q < 3 ? !has_y : !has_h) continue;
+    for (int q = 0; q < kAcc; ++q) {
+      if (q % 2 == 0 ? !has_y : !has_h) continue;
       __syncthreads();
 #pragma unroll
       for (int k = 0; k < kNV; ++k)
@@ -382,42 +442,59 @@ __global__ void __launch_bounds__(THREADS) k_norm_bwd(const NormParams p) {
           if (col < p.d) s_sum[sub * p.d + col] = acc[q][k][j];
         }
       __syncthreads();
-      float* out = p.part + ((size_t)c * kSums + q) * p.d;
-      for (int col = threadIdx.x; col < p.d; col += blockDim.x) {
+      float* out = p.part + ((size_t)(blockIdx.x + g) * kSums + (q == 0 ? 0 : q == 1 ? 2 : q == 2 ? 1 : 3)) * p.d;
+      for (int col = threadIdx.x; col < p.d; col += THREADS) {
         float s = 0.0f;
-        for (int m = 0; m < teams; ++m) s += s_sum[m * p.d + col];
+        for (int t = 0; t < teams; ++t) s += s_sum[t * p.d + col];
         out[col] = s;
       }
     }
+    first = last;
   }
 }
 
-// The sums of each group over its chunks: 32 columns by 8 slices of chunks per block, in fp64, joined in the slices'
-// order.
+// The parameter gradients of each group from its runs' partial sums: 32 columns by 8 slices of runs per block, in
+// fp64, the slices joined in their order.
 __global__ void __launch_bounds__(256) k_norm_sums(const NormParams p) {
   extern __shared__ long long s_off[];
-  __shared__ double s_part[8][33];
-  int* s_cum = reinterpret_cast<int*>(s_off + p.groups + 1);
+  __shared__ double s_part[2][8][33];
   load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
-  count_tiles(s_off, p.groups, p.chunk_rows, s_cum);
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-  const int col = blockIdx.x * 32 + lane, q = blockIdx.y;
-  float* const outs[kSums] = {p.dwp, p.dbp, p.dsc, p.dwq, p.dbq};
-  float* out = nullptr;
-#pragma unroll
-  for (int i = 0; i < kSums; ++i)
-    if (i == q) out = outs[i];
-  if (out == nullptr) return;  // uniform over the block
+  const int col = blockIdx.x * 32 + lane;
+  const bool post = blockIdx.y == 0;  // the block's two sums: S1, S2 or T1, T2
+  if (post ? p.dwp == nullptr : p.dwq == nullptr) return;
+  const bool second = post ? p.bp != nullptr : p.bq != nullptr;
+  const long long off0 = s_off[0], m = s_off[p.groups] - off0;
   for (int g = blockIdx.z; g < p.groups; g += gridDim.z) {
-    double s = 0.0;
-    if (col < p.d) {
-      for (int c = s_cum[g] + slice; c < s_cum[g + 1]; c += 8) s += (double)__ldg(&p.part[((size_t)c * kSums + q) * p.d + col]);
+    double a = 0.0, b = 0.0;
+    if (col < p.d && s_off[g] < s_off[g + 1]) {
+      const int b0 = run_of(s_off[g] - off0, m, p.blocks), b1 = run_of(s_off[g + 1] - 1 - off0, m, p.blocks);
+      const float* base = p.part + (size_t)(post ? 0 : 2) * p.d + col;
+#pragma unroll 4
+      for (int k = b0 + slice; k <= b1; k += 8) {
+        const float* at = base + (size_t)(k + g) * kSums * p.d;
+        a += (double)__ldg(at);
+        if (second) b += (double)__ldg(at + p.d);
+      }
     }
-    s_part[slice][lane] = s;
+    s_part[0][slice][lane] = a;
+    s_part[1][slice][lane] = b;
     __syncthreads();
     if (slice == 0 && col < p.d) {
-      for (int k = 1; k < 8; ++k) s += s_part[k][lane];
-      out[(size_t)g * p.d + col] = (float)s;
+      for (int k = 1; k < 8; ++k) {
+        a += s_part[0][k][lane];
+        b += s_part[1][k][lane];
+      }
+      const size_t at = (size_t)g * p.d + col;
+      if (post) {
+        const double s = p.sc != nullptr ? (double)p.sc[at] : 1.0;
+        p.dwp[at] = (float)(s * a);
+        if (p.dbp != nullptr) p.dbp[at] = (float)(s * b);
+        if (p.dsc != nullptr) p.dsc[at] = (float)((double)p.wp[at] * a + (p.bp != nullptr ? (double)p.bp[at] * b : 0.0));
+      } else {
+        p.dwq[at] = (float)a;
+        if (p.dbq != nullptr) p.dbq[at] = (float)b;
+      }
     }
     __syncthreads();
   }
@@ -430,18 +507,14 @@ int log_team_of(int d) {  // 16 columns per lane; at least the four lanes of an 
   while ((16 << l) < d) ++l;
   return l;
 }
-int threads_of(int log_team) { return log_team > 8 ? 1 << log_team : kNormThreads; }
+int threads_of(int log_team) { return log_team > 7 ? 512 : 128; }
 
-// Rows per chunk: two chunks per SM when the rows are many (each leaves kSums sums of d columns), at least four
-// rows per team.
-int chunk_rows_of(long long n, int d) {
-  const int teams = threads_of(log_team_of(d)) >> log_team_of(d);
-  const long long want = (n + 2LL * sm_count() - 1) / (2LL * sm_count());
-  const long long least = 4LL * teams;
-  return (int)std::max<long long>(least, (want + teams - 1) / teams * teams);
+// Blocks of a backward over n rows: what the SMs hold at once, and at least two rows per team.
+int bwd_blocks(long long n, int d) {
+  const int lt = log_team_of(d), threads = threads_of(lt), teams = threads >> lt;
+  const long long most = (long long)sm_count() * (threads == 128 ? kBwdBlocks : 1);
+  return (int)std::max<long long>(1, std::min<long long>(most, (n + 2 * teams - 1) / (2 * teams)));
 }
-
-size_t norm_smem(int groups) { return (size_t)(groups + 1) * (8 + 4); }
 
 int norm_params(const mt_gated_norm* c, NormParams& p) {
   if (c == nullptr) return MT_EINVAL;
@@ -476,32 +549,19 @@ int norm_params(const mt_gated_norm* c, NormParams& p) {
 }
 
 template <typename T, bool AL>
-void norm_launch_fwd_as(const NormParams& p, int grid, int threads, size_t smem, cudaStream_t s) {
-  if (threads > kNormThreads) k_norm_fwd<T, AL, 2 * kNormThreads><<<grid, threads, smem, s>>>(p);
-  else k_norm_fwd<T, AL, kNormThreads><<<grid, threads, smem, s>>>(p);
+void norm_fwd_as(const NormParams& p, int grid, int threads, size_t smem, cudaStream_t s) {
+  if (threads > 128) k_norm_fwd<T, AL, 512><<<grid, threads, smem, s>>>(p);
+  else k_norm_fwd<T, AL, 128><<<grid, threads, smem, s>>>(p);
 }
-void norm_launch_fwd(const NormParams& p, int dtype, bool wide, int grid, int threads, size_t smem, cudaStream_t s) {
-  if (dtype == MT_F32) {
-    if (wide) norm_launch_fwd_as<float, true>(p, grid, threads, smem, s);
-    else norm_launch_fwd_as<float, false>(p, grid, threads, smem, s);
-  } else {
-    if (wide) norm_launch_fwd_as<__nv_bfloat16, true>(p, grid, threads, smem, s);
-    else norm_launch_fwd_as<__nv_bfloat16, false>(p, grid, threads, smem, s);
-  }
-}
-
 template <typename T, bool AL>
-void norm_launch_bwd_as(const NormParams& p, int grid, int threads, size_t smem, cudaStream_t s) {
-  if (threads > kNormThreads) k_norm_bwd<T, AL, 2 * kNormThreads><<<grid, threads, smem, s>>>(p);
-  else k_norm_bwd<T, AL, kNormThreads><<<grid, threads, smem, s>>>(p);
-}
-void norm_launch_bwd(const NormParams& p, int dtype, bool wide, int grid, int threads, size_t smem, cudaStream_t s) {
-  if (dtype == MT_F32) {
-    if (wide) norm_launch_bwd_as<float, true>(p, grid, threads, smem, s);
-    else norm_launch_bwd_as<float, false>(p, grid, threads, smem, s);
+void norm_bwd_as(const NormParams& p, int threads, size_t smem, cudaStream_t s) {
+  const bool bias = p.bp != nullptr || p.bq != nullptr;
+  if (threads > 128) {
+    if (bias) k_norm_bwd<T, AL, 512, true><<<p.blocks, threads, smem, s>>>(p);
+    else k_norm_bwd<T, AL, 512, false><<<p.blocks, threads, smem, s>>>(p);
   } else {
-    if (wide) norm_launch_bwd_as<__nv_bfloat16, true>(p, grid, threads, smem, s);
-    else norm_launch_bwd_as<__nv_bfloat16, false>(p, grid, threads, smem, s);
+    if (bias) k_norm_bwd<T, AL, 128, true><<<p.blocks, threads, smem, s>>>(p);
+    else k_norm_bwd<T, AL, 128, false><<<p.blocks, threads, smem, s>>>(p);
   }
 }
 
@@ -541,11 +601,17 @@ int mt_gated_norm_forward(const mt_gated_norm* cfg, const mt_rows* x, const mt_r
   for (const Rows* r : {&p.x, &p.y, &p.u, &p.z, &p.h}) wide = wide && rows_wide(*r, p.d, cfg->dtype);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int threads = threads_of(p.log_team), teams = threads >> p.log_team;
-  const int grid = grid_for((p.n + teams - 1) / teams * threads, threads, 2048 / threads);
-  const size_t smem = norm_smem(p.groups);
+  const int grid = grid_for((p.n + teams - 1) / teams * threads, threads, threads == 128 ? kFwdBlocks : 1);
+  const size_t smem = (size_t)(p.groups + 1) * 8;
   {
     MT_LAUNCH("k_norm_fwd", s);
-    norm_launch_fwd(p, cfg->dtype, wide, grid, threads, smem, s);
+    if (cfg->dtype == MT_F32) {
+      if (wide) norm_fwd_as<float, true>(p, grid, threads, smem, s);
+      else norm_fwd_as<float, false>(p, grid, threads, smem, s);
+    } else {
+      if (wide) norm_fwd_as<__nv_bfloat16, true>(p, grid, threads, smem, s);
+      else norm_fwd_as<__nv_bfloat16, false>(p, grid, threads, smem, s);
+    }
   }
   return cudaGetLastError() == cudaSuccess ? MT_OK : MT_ECUDA;
 }
@@ -553,8 +619,7 @@ int mt_gated_norm_forward(const mt_gated_norm* cfg, const mt_rows* x, const mt_r
 size_t mt_gated_norm_workspace_bytes(int64_t n, int32_t dim, int32_t groups) {
   using namespace mt;
   if (n < 0 || n > 0x7FFFFFFF || dim < 1 || dim > MT_MAX_BLOCK_DIM || groups < 1 || groups > MT_MAX_GROUPS) return 0;
-  const long long chunks = n / chunk_rows_of(n, dim) + groups;
-  return align_up((size_t)chunks * kSums * dim * 4, 256);
+  return align_up(((size_t)bwd_blocks(n, dim) + groups) * kSums * dim * 4, 256);
 }
 
 int mt_gated_norm_backward(const mt_gated_norm* cfg, const mt_rows* dz, const mt_rows* dh, const mt_rows* y,
@@ -610,22 +675,27 @@ int mt_gated_norm_backward(const mt_gated_norm* cfg, const mt_rows* dz, const mt
   if (ws == nullptr || !is_aligned(ws, 256) || ws_bytes < mt_gated_norm_workspace_bytes(p.n, p.d, p.groups))
     return MT_ENOSPACE;
   p.part = static_cast<float*>(ws);
-  p.chunk_rows = chunk_rows_of(p.n, p.d);
-  p.chunks = (int)(p.n / p.chunk_rows) + p.groups;
+  p.blocks = bwd_blocks(p.n, p.d);
   bool wide = true;
   for (const Rows* r : {&p.dz, &p.dh, &p.y, &p.u, &p.z, &p.dx, &p.dy, &p.du})
     wide = wide && rows_wide(*r, p.d, cfg->dtype);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int threads = threads_of(p.log_team);
-  const size_t smem = norm_smem(p.groups);
+  const size_t smem = (size_t)(p.groups + 1) * 8;
   if (p.n > 0) {
     MT_LAUNCH("k_norm_bwd", s);
-    const int grid = p.chunks;
-    norm_launch_bwd(p, cfg->dtype, wide, grid, threads, smem, s);
+    const size_t sums = (size_t)(threads >> p.log_team) * p.d * 4;
+    if (cfg->dtype == MT_F32) {
+      if (wide) norm_bwd_as<float, true>(p, threads, smem + sums, s);
+      else norm_bwd_as<float, false>(p, threads, smem + sums, s);
+    } else {
+      if (wide) norm_bwd_as<__nv_bfloat16, true>(p, threads, smem + sums, s);
+      else norm_bwd_as<__nv_bfloat16, false>(p, threads, smem + sums, s);
+    }
   }
   {
     MT_LAUNCH("k_norm_sums", s);
-    const dim3 grid((p.d + 31) / 32, kSums, p.groups);
+    const dim3 grid((p.d + 31) / 32, 2, p.groups);
     k_norm_sums<<<grid, 256, smem, s>>>(p);
   }
   return cudaGetLastError() == cudaSuccess ? MT_OK : MT_ECUDA;
