@@ -52,7 +52,9 @@ __device__ __forceinline__ long long run_start(long long off0, long long m, int 
 __device__ __forceinline__ int run_of(long long r, long long m, int B) { return (int)(((r + 1) * B - 1) / m); }
 
 // Sums a and b over a team: shuffles inside a warp, shared memory across a team's warps.  A team of more than one
-// warp owns the named barrier 1 + team; `slot` alternates so that one barrier per call is enough.
+// warp owns a named barrier (a block has at most two such teams; the barriers' numbers are constants, as a number from
+// a register would reserve all sixteen and leave an SM four blocks); `slot` alternates so that one barrier per call is
+// enough.
 __device__ __forceinline__ void team_sum2(float& a, float& b, int team_lanes, float2* s_red, int& slot) {
   const int in_warp = team_lanes < 32 ? team_lanes : 32;
   for (int o = in_warp >> 1; o > 0; o >>= 1) {
@@ -63,7 +65,8 @@ __device__ __forceinline__ void team_sum2(float& a, float& b, int team_lanes, fl
   const int warp = threadIdx.x >> 5, warps = team_lanes >> 5, first = warp / warps * warps;
   float2* buf = s_red + slot * 16;
   if ((threadIdx.x & 31) == 0) buf[warp] = make_float2(a, b);
-  asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / warps), "r"(team_lanes) : "memory");
+  if (first == 0) asm volatile("bar.sync 1, %0;" ::"r"(team_lanes) : "memory");
+  else asm volatile("bar.sync 2, %0;" ::"r"(team_lanes) : "memory");
   a = b = 0.0f;
   for (int k = 0; k < warps; ++k) {
     const float2 v = buf[first + k];
@@ -92,24 +95,38 @@ __device__ __forceinline__ void param8(const float* p, int g, int vec, int d, in
   }
 }
 
-// The gate's factor a = act(u) and its derivative.  fp32 rows take the accurate exponential and division; for bf16
-// rows the fast ones (a few units of 2^-22) are far below the rounding of the result.
+// The gate's factors a = act(u) of eight columns and their derivatives.  fp32 rows take the accurate exponential and
+// division; for bf16 rows the fast ones (a few units of 2^-22) are far below the rounding of the result.  The choice is
+// made once for the eight, so that their chains overlap.
 template <typename T>
-__device__ __forceinline__ float gate_value(int gate, float u, float& da) {
+__device__ __forceinline__ void gate8(int gate, const float (&u)[8], float (&a)[8], float (&da)[8]) {
   if (gate == MT_GATE_LINEAR) {
-    da = 1.0f;
-    return u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      a[j] = u[j];
+      da[j] = 1.0f;
+    }
+    return;
   }
-  float p;
-  if constexpr (sizeof(T) == 4) p = 1.0f / (1.0f + expf(-u));
-  else p = __fdividef(1.0f, 1.0f + __expf(-fmaxf(u, -80.0f)));  // the fast division is 0 past 2^126: exp(80) < 2^116
+  float p[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if constexpr (sizeof(T) == 4) p[j] = 1.0f / (1.0f + expf(-u[j]));
+    else p[j] = __fdividef(1.0f, 1.0f + __expf(-fmaxf(u[j], -80.0f)));  // the fast division is 0 past 2^126: exp(80) < 2^116
+  }
   if (gate == MT_GATE_SIGMOID) {
-    da = p * (1.0f - p);
-    return p;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      a[j] = p[j];
+      da[j] = p[j] * (1.0f - p[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      a[j] = u[j] * p[j];
+      da[j] = p[j] + a[j] * (1.0f - p[j]);
+    }
   }
-  const float a = u * p;
-  da = p + a * (1.0f - p);
-  return a;
 }
 
 // Mean (layer norm; 0 for rms) and inverse deviation of the rows held in v and w at once (one of them may be absent:
@@ -226,22 +243,33 @@ k_norm_fwd(const NormParams p) {
         for (int k = 0; k < kNV; ++k) {
           const int vec = k * team + lt;
           if (p.y.codes != nullptr) store_packed8<AL>(p.y, row, vec, p.d, y[k], live);
-          float w[8], b[8], s[8], u[8];
+          float w[8], f[8];
           param8(p.wp, g, vec, p.d, p.wide, 1.0f, w);
-          param8(p.bp, g, vec, p.d, p.wide, 0.0f, b);
-          param8(p.sc, g, vec, p.d, p.wide, 1.0f, s);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[k][j] = w[j] * ((y[k][j] - st.mean) * st.r);
+          if (p.bp != nullptr) {
+            param8(p.bp, g, vec, p.d, p.wide, 0.0f, f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[k][j] += f[j];
+          }
+          if (p.sc != nullptr) {
+            param8(p.sc, g, vec, p.d, p.wide, 1.0f, f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[k][j] *= f[j];
+          }
           if (has_u) {
+            float u[8], da[8];
             widen8<T>(ru[k], false, u);
             if (p.u.codes != nullptr) store_packed8<AL>(p.u, row, vec, p.d, u, live);
+            gate8<T>(p.gate, u, f, da);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[k][j] *= f[j];
           }
           widen8<T>(rx[k], false, z[k]);
           const int left = p.d - vec * 8;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float t = (w[j] * ((y[k][j] - st.mean) * st.r) + b[j]) * s[j], da;
-            if (has_u) t *= gate_value<T>(p.gate, u[j], da);
-            if (AL || j < left) z[k][j] += t;
-          }
+          for (int j = 0; j < 8; ++j)
+            if (AL || j < left) z[k][j] += y[k][j];
           if (AL && left <= 0) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) z[k][j] = 0.0f;
@@ -256,14 +284,18 @@ k_norm_fwd(const NormParams p) {
 #pragma unroll
         for (int k = 0; k < kNV; ++k) {
           const int vec = k * team + lt, left = p.d - vec * 8;
-          float w[8], b[8], h[8];
+          float w[8], h[8];
           param8(p.wq, g, vec, p.d, p.wide, 1.0f, w);
-          param8(p.bq, g, vec, p.d, p.wide, 0.0f, b);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            h[j] = w[j] * ((z[k][j] - st.mean) * st.r) + b[j];
-            if (AL ? left <= 0 : j >= left) h[j] = 0.0f;
+          for (int j = 0; j < 8; ++j) h[j] = w[j] * ((z[k][j] - st.mean) * st.r);
+          if (p.bq != nullptr) {
+            param8(p.bq, g, vec, p.d, p.wide, 0.0f, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[j] += w[j];
           }
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (AL ? left <= 0 : j >= left) h[j] = 0.0f;
           if (live) store8<T, AL>(p.h.data, p.h.ld, row, vec, p.d, h);
           if (p.h.codes != nullptr) store_packed8<AL>(p.h, row, vec, p.d, h, live);
         }
@@ -399,24 +431,42 @@ k_norm_bwd(const NormParams p) {
 #pragma unroll
         for (int k = 0; k < kNV; ++k) {
           const int vec = k * team + lt, left = p.d - vec * 8;
-          float w[8], b[8], s[8], u[8], du[8];
+          float w[8], s[8], Da[8];
           param8(p.wp, g, vec, p.d, p.wide, 1.0f, w);
-          param8(p.bp, g, vec, p.d, p.wide, 0.0f, b);
           param8(p.sc, g, vec, p.d, p.wide, 1.0f, s);
-          if (has_u) widen8<T>(ru[k], u8, u);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const bool on = AL ? left > 0 : j < left;
+            const bool on = live && (AL ? left > 0 : j < left);
             yh[k][j] = on ? (yh[k][j] - sy.mean) * sy.r : 0.0f;
-            float a = 1.0f, da = 0.0f;
-            if (has_u) a = gate_value<T>(p.gate, u[j], da);
-            const float Da = on && live ? D[k][j] * a : 0.0f, Ds = D[k][j] * s[j];
-            acc[0][k][j] += Da * yh[k][j];
-            if constexpr (BIAS) acc[2][k][j] += Da;
-            dyh[k][j] = Da * s[j] * w[j];
-            du[j] = Ds * (w[j] * yh[k][j] + b[j]) * da;
+            Da[j] = on ? D[k][j] : 0.0f;
           }
-          if (has_u && live) store8<T, AL>(p.du.data, p.du.ld, row, vec, p.d, du);
+          if (has_u) {
+            float u[8], a[8], da[8];
+            widen8<T>(ru[k], u8, u);
+            gate8<T>(p.gate, u, a, da);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              u[j] = w[j] * yh[k][j];
+              da[j] *= Da[j] * s[j];
+              Da[j] *= a[j];
+            }
+            if constexpr (BIAS) {
+              if (p.bp != nullptr) {
+                param8(p.bp, g, vec, p.d, p.wide, 0.0f, a);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) u[j] += a[j];
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) da[j] *= u[j];
+            if (live) store8<T, AL>(p.du.data, p.du.ld, row, vec, p.d, da);
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            acc[0][k][j] += Da[j] * yh[k][j];
+            if constexpr (BIAS) acc[2][k][j] += Da[j];
+            dyh[k][j] = Da[j] * s[j] * w[j];
+          }
         }
         norm_grad(dyh, yh, sy.r, p, team, s_red, slot);
         if (live) {
