@@ -182,14 +182,80 @@ __device__ __forceinline__ Stats row_stats(const float (&v)[kNV][8], const NormP
   return a;
 }
 
+// ---- rows on their way -------------------------------------------------------------
+//
+// The next rows of a team are copied to shared memory while it works on the
+// present ones.  A lane copies exactly what it will read, so waiting for its
+// own copies is all the synchronisation there is, and the rows in flight cost no
+// registers.  Rows that cannot be reached with 16-byte accesses, and the
+// widest rows in fp32 (whose stages would not fit), are loaded when they are used.
+
+template <typename T, bool AL, int THREADS>
+constexpr bool kStaged = AL && (THREADS == 128 || sizeof(T) == 2);
+constexpr uint32_t kNoExp = 0xFFFFFFFFu;  // plain rows have no exponent byte
+template <typename T>
+constexpr int kVecBytes = 8 * (int)sizeof(T);
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// NROWS row tensors, two stages; the lane's vector k of tensor i in stage s.
+template <typename T, int THREADS, int NROWS>
+struct Stages {
+  static constexpr int kBytes = 2 * NROWS * kNV * THREADS * kVecBytes<T>;
+  uint32_t base;
+  __device__ __forceinline__ uint32_t at(int s, int i, int k) const {
+    return base + (uint32_t)((((s * NROWS + i) * kNV + k) * THREADS + threadIdx.x) * kVecBytes<T>);
+  }
+};
+
+// Starts the copy of eight columns (zeros where they lie past d or the row is not there); e: a packed block's exponent
+// byte, which comes by an ordinary load.
+template <typename T>
+__device__ __forceinline__ void fetch8(uint32_t dst, const Rows& r, long long row, int vec, int d, bool packed, uint32_t& e) {
+  const int c0 = vec * 8;
+  const bool on = c0 < d;
+  if (packed) {
+    const int nb = (d + kPackBlock - 1) / kPackBlock;
+    copy8(dst, r.codes + (on ? row * d + c0 : 0), on);
+    e = on ? (uint32_t)__ldg(r.exps + row * nb + c0 / kPackBlock) : 127u;
+  } else {
+    const T* p = static_cast<const T*>(r.data) + (on ? row * r.ld + c0 : 0);
+    copy16(dst, p, on);
+    if constexpr (sizeof(T) == 4) copy16(dst + 16, p + 4, on);
+  }
+}
+template <typename T>
+__device__ __forceinline__ Raw8<T> staged8(uint32_t at, uint32_t e) {
+  Raw8<T> v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.a.x), "=r"(v.a.y), "=r"(v.a.z), "=r"(v.a.w) : "r"(at));
+  if constexpr (sizeof(T) == 4)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.b.x), "=r"(v.b.y), "=r"(v.b.z), "=r"(v.b.w) : "r"(at + 16));
+  if (e != kNoExp) v.a.z = e;
+  return v;
+}
+
 // Blocks of 128 threads that share an SM's registers (wider rows: one block of 512).
 constexpr int kFwdBlocks = 6, kBwdBlocks = 3;
 
 template <typename T, bool AL, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == 128 ? (sizeof(T) == 4 ? 4 : kFwdBlocks) : 1)
 k_norm_fwd(const NormParams p) {
-  extern __shared__ long long s_off[];
+  constexpr bool STAGED = kStaged<T, AL, THREADS>;
+  using St = Stages<T, THREADS, 3>;
+  extern __shared__ __align__(16) uint8_t s_raw[];  // the stages, then the offsets
   __shared__ float2 s_red[32];
+  const St st{(uint32_t)__cvta_generic_to_shared(s_raw)};
+  long long* s_off = reinterpret_cast<long long*>(s_raw + (STAGED ? St::kBytes : 0));
   load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
   const int team = 1 << p.log_team;
   const int lt = threadIdx.x & (team - 1);
@@ -220,25 +286,54 @@ k_norm_fwd(const NormParams p) {
   long long first = run_start(off0, m, blockIdx.x, gridDim.x);
   for (int g = first < end ? row_group(s_off, p.groups, first) : 0; first < end; ++g) {
     const long long last = min(end, s_off[g + 1]);
+    auto fetch = [&](long long base, int s) {
+      const bool live = base + sub < last;
+      const long long row = live ? base + sub : base;
+      const int dd = live ? p.d : 0;
+      uint32_t none;
+#pragma unroll
+      for (int k = 0; k < kNV; ++k) {
+        const int vec = k * team + lt;
+        if (has_y) fetch8<T>(st.at(s, 0, k), p.y, row, vec, dd, false, none);
+        if (has_u) fetch8<T>(st.at(s, 1, k), p.u, row, vec, dd, false, none);
+        fetch8<T>(st.at(s, 2, k), p.x, row, vec, dd, false, none);
+      }
+    };
+    int cur = 0;
+    if constexpr (STAGED) {
+      if (first < last) fetch(first, 0);
+      copies_close();
+    }
     // every team of the block runs the same number of rounds, so the shuffles and barriers meet
-    for (long long base = first; base < last; base += teams) {
+    for (long long base = first; base < last; base += teams, cur ^= 1) {
       const bool live = base + sub < last;
       const long long row = live ? base + sub : base;
       const int dd = live ? p.d : 0;
       Raw8<T> rx[kNV], ry[kNV], ru[kNV];
+      if constexpr (STAGED) {
+        if (base + teams < last) fetch(base + teams, cur ^ 1);
+        copies_close();
+        copies_wait<1>();
+      }
 #pragma unroll
       for (int k = 0; k < kNV; ++k) {
         const int vec = k * team + lt;
-        if (has_y) ry[k] = load8<T, AL>(p.y, row, vec, dd);
-        rx[k] = load8<T, AL>(p.x, row, vec, dd);
-        if (has_u) ru[k] = load8<T, AL>(p.u, row, vec, dd);
+        if constexpr (STAGED) {
+          if (has_y) ry[k] = staged8<T>(st.at(cur, 0, k), kNoExp);
+          if (has_u) ru[k] = staged8<T>(st.at(cur, 1, k), kNoExp);
+          rx[k] = staged8<T>(st.at(cur, 2, k), kNoExp);
+        } else {
+          if (has_y) ry[k] = load8<T, AL>(p.y, row, vec, dd);
+          rx[k] = load8<T, AL>(p.x, row, vec, dd);
+          if (has_u) ru[k] = load8<T, AL>(p.u, row, vec, dd);
+        }
       }
       float z[kNV][8];
       if (has_y) {
         float y[kNV][8];
 #pragma unroll
         for (int k = 0; k < kNV; ++k) widen8<T>(ry[k], false, y[k]);
-        const Stats st = row_stats(y, p, team, lt, s_red, slot);
+        const Stats sy = row_stats(y, p, team, lt, s_red, slot);
 #pragma unroll
         for (int k = 0; k < kNV; ++k) {
           const int vec = k * team + lt;
@@ -246,7 +341,7 @@ k_norm_fwd(const NormParams p) {
           float w[8], f[8];
           param8(p.wp, g, vec, p.d, p.wide, 1.0f, w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) y[k][j] = w[j] * ((y[k][j] - st.mean) * st.r);
+          for (int j = 0; j < 8; ++j) y[k][j] = w[j] * ((y[k][j] - sy.mean) * sy.r);
           if (p.bp != nullptr) {
             param8(p.bp, g, vec, p.d, p.wide, 0.0f, f);
 #pragma unroll
@@ -280,14 +375,14 @@ k_norm_fwd(const NormParams p) {
         for (int k = 0; k < kNV; ++k) widen8<T>(rx[k], false, z[k]);
       }
       if (has_h) {
-        const Stats st = row_stats(z, p, team, lt, s_red, slot);
+        const Stats sz = row_stats(z, p, team, lt, s_red, slot);
 #pragma unroll
         for (int k = 0; k < kNV; ++k) {
           const int vec = k * team + lt, left = p.d - vec * 8;
           float w[8], h[8];
           param8(p.wq, g, vec, p.d, p.wide, 1.0f, w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) h[j] = w[j] * ((z[k][j] - st.mean) * st.r);
+          for (int j = 0; j < 8; ++j) h[j] = w[j] * ((z[k][j] - sz.mean) * sz.r);
           if (p.bq != nullptr) {
             param8(p.bq, g, vec, p.d, p.wide, 0.0f, w);
 #pragma unroll
@@ -336,9 +431,14 @@ template <typename T, bool AL, int THREADS, bool BIAS>
 __global__ void __launch_bounds__(THREADS, THREADS == 128 ? (sizeof(T) == 4 ? 2 : kBwdBlocks) : 1)
 k_norm_bwd(const NormParams p) {
   constexpr int kAcc = BIAS ? 4 : 2;       // S1, T1, S2, T2
-  extern __shared__ long long s_off[];     // [groups + 1], then the sums of the block's teams: teams * d floats
+  constexpr bool STAGED = kStaged<T, AL, THREADS>;
+  using St = Stages<T, THREADS, 5>;
+  extern __shared__ __align__(16) uint8_t s_raw[];  // the stages (later the sums of the block's teams), the offsets
   __shared__ float2 s_red[32];
-  float* s_sum = reinterpret_cast<float*>(s_off + p.groups + 1);
+  const St st{(uint32_t)__cvta_generic_to_shared(s_raw)};
+  float* s_sum = reinterpret_cast<float*>(s_raw);   // teams * d <= 16 * THREADS floats
+  static_assert(St::kBytes >= 16 * THREADS * 4, "the sums fit the stages");
+  long long* s_off = reinterpret_cast<long long*>(s_raw + (STAGED ? St::kBytes : 16 * THREADS * 4));
   load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
   const int team = 1 << p.log_team;
   const int lt = threadIdx.x & (team - 1);
@@ -375,19 +475,58 @@ k_norm_bwd(const NormParams p) {
       for (int k = 0; k < kNV; ++k)
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[q][k][j] = 0.0f;
-    for (long long base = first; base < last; base += teams) {
+    uint32_t next_e[3][kNV];  // exponent bytes of the rows on their way: z, y, u
+    auto fetch = [&](long long base, int s) {
       const bool live = base + sub < last;
       const long long row = live ? base + sub : base;
       const int dd = live ? p.d : 0;  // a team without a row computes on zeros
-      Raw8<T> ry[kNV], ru[kNV], rz[kNV], rdz[kNV], rdh[kNV];
 #pragma unroll
       for (int k = 0; k < kNV; ++k) {
         const int vec = k * team + lt;
-        if (has_h) rz[k] = load8<T, AL>(p.z, row, vec, dd);
-        if (has_y) ry[k] = load8<T, AL>(p.y, row, vec, dd);
-        if (has_h) rdh[k] = load8<T, AL>(p.dh, row, vec, dd);
-        if (has_dz) rdz[k] = load8<T, AL>(p.dz, row, vec, dd);
-        if (has_u) ru[k] = load8<T, AL>(p.u, row, vec, dd);
+        uint32_t none;
+        if (has_h) fetch8<T>(st.at(s, 0, k), p.z, row, vec, dd, z8, next_e[0][k]);
+        if (has_y) fetch8<T>(st.at(s, 1, k), p.y, row, vec, dd, y8, next_e[1][k]);
+        if (has_h) fetch8<T>(st.at(s, 2, k), p.dh, row, vec, dd, false, none);
+        if (has_dz) fetch8<T>(st.at(s, 3, k), p.dz, row, vec, dd, false, none);
+        if (has_u) fetch8<T>(st.at(s, 4, k), p.u, row, vec, dd, u8, next_e[2][k]);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+#pragma unroll
+      for (int k = 0; k < kNV; ++k) next_e[i][k] = kNoExp;
+    int cur = 0;
+    if constexpr (STAGED) {
+      fetch(first, 0);
+      copies_close();
+    }
+    for (long long base = first; base < last; base += teams, cur ^= 1) {
+      const bool live = base + sub < last;
+      const long long row = live ? base + sub : base;
+      const int dd = live ? p.d : 0;
+      uint32_t e[3][kNV];
+      if constexpr (STAGED) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+#pragma unroll
+          for (int k = 0; k < kNV; ++k) e[i][k] = next_e[i][k];
+        if (base + teams < last) fetch(base + teams, cur ^ 1);
+        copies_close();
+        copies_wait<1>();
+      }
+      // a row's vector, from its stage or from where it lies
+      auto get = [&](int i, const Rows& r, int k, uint32_t ex) {
+        if constexpr (STAGED) return staged8<T>(st.at(cur, i, k), ex);
+        else return load8<T, AL>(r, row, k * team + lt, dd);
+      };
+      Raw8<T> ry[kNV], ru[kNV], rz[kNV], rdz[kNV], rdh[kNV];
+#pragma unroll
+      for (int k = 0; k < kNV; ++k) {
+        if (has_h) rz[k] = get(0, p.z, k, e[0][k]);
+        if (has_y) ry[k] = get(1, p.y, k, e[1][k]);
+        if (has_h) rdh[k] = get(2, p.dh, k, kNoExp);
+        if (has_dz) rdz[k] = get(3, p.dz, k, kNoExp);
+        if (has_u) ru[k] = get(4, p.u, k, e[2][k]);
       }
       Stats sy, sz;
       float yh[kNV][8] = {}, D[kNV][8] = {};
@@ -479,6 +618,7 @@ k_norm_bwd(const NormParams p) {
         for (int k = 0; k < kNV; ++k) store8<T, AL>(p.dx.data, p.dx.ld, row, k * team + lt, p.d, D[k]);
       }
     }
+    if constexpr (STAGED) copies_wait<0>();
     // the run's sums: the teams' registers meet in shared memory, one sum at a time, in the teams' order
 #pragma unroll
     for (int q = 0; q < kAcc; ++q) {
@@ -499,6 +639,7 @@ k_norm_bwd(const NormParams p) {
         out[col] = s;
       }
     }
+    __syncthreads();  // the next group's rows may come
     first = last;
   }
 }
@@ -598,21 +739,39 @@ int norm_params(const mt_gated_norm* c, NormParams& p) {
   return MT_OK;
 }
 
-template <typename T, bool AL>
-void norm_fwd_as(const NormParams& p, int grid, int threads, size_t smem, cudaStream_t s) {
-  if (threads > 128) k_norm_fwd<T, AL, 512><<<grid, threads, smem, s>>>(p);
-  else k_norm_fwd<T, AL, 128><<<grid, threads, smem, s>>>(p);
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes) {
+  return cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <typename T, bool AL, int THREADS>
+cudaError_t norm_fwd_as(const NormParams& p, cudaStream_t s) {
+  const int teams = THREADS >> p.log_team;
+  const int grid = grid_for((p.n + teams - 1) / teams * THREADS, THREADS, THREADS == 128 ? kFwdBlocks : 1);
+  const size_t smem = (kStaged<T, AL, THREADS> ? Stages<T, THREADS, 3>::kBytes : 0) + (size_t)(p.groups + 1) * 8;
+  const cudaError_t e = allow_smem(k_norm_fwd<T, AL, THREADS>, smem);
+  if (e != cudaSuccess) return e;
+  k_norm_fwd<T, AL, THREADS><<<grid, THREADS, smem, s>>>(p);
+  return cudaGetLastError();
+}
+template <typename T, bool AL, int THREADS, bool BIAS>
+cudaError_t norm_bwd_as(const NormParams& p, cudaStream_t s) {
+  const size_t smem =
+      (kStaged<T, AL, THREADS> ? Stages<T, THREADS, 5>::kBytes : 16 * THREADS * 4) + (size_t)(p.groups + 1) * 8;
+  const cudaError_t e = allow_smem(k_norm_bwd<T, AL, THREADS, BIAS>, smem);
+  if (e != cudaSuccess) return e;
+  k_norm_bwd<T, AL, THREADS, BIAS><<<p.blocks, THREADS, smem, s>>>(p);
+  return cudaGetLastError();
 }
 template <typename T, bool AL>
-void norm_bwd_as(const NormParams& p, int threads, size_t smem, cudaStream_t s) {
+cudaError_t norm_fwd(const NormParams& p, cudaStream_t s) {
+  return p.log_team > 7 ? norm_fwd_as<T, AL, 512>(p, s) : norm_fwd_as<T, AL, 128>(p, s);
+}
+template <typename T, bool AL>
+cudaError_t norm_bwd(const NormParams& p, cudaStream_t s) {
   const bool bias = p.bp != nullptr || p.bq != nullptr;
-  if (threads > 128) {
-    if (bias) k_norm_bwd<T, AL, 512, true><<<p.blocks, threads, smem, s>>>(p);
-    else k_norm_bwd<T, AL, 512, false><<<p.blocks, threads, smem, s>>>(p);
-  } else {
-    if (bias) k_norm_bwd<T, AL, 128, true><<<p.blocks, threads, smem, s>>>(p);
-    else k_norm_bwd<T, AL, 128, false><<<p.blocks, threads, smem, s>>>(p);
-  }
+  if (p.log_team > 7) return bias ? norm_bwd_as<T, AL, 512, true>(p, s) : norm_bwd_as<T, AL, 512, false>(p, s);
+  return bias ? norm_bwd_as<T, AL, 128, true>(p, s) : norm_bwd_as<T, AL, 128, false>(p, s);
 }
 
 bool packed_rows(const Rows& r) { return r.codes != nullptr && r.exps != nullptr; }
@@ -650,20 +809,13 @@ int mt_gated_norm_forward(const mt_gated_norm* cfg, const mt_rows* x, const mt_r
   bool wide = true;
   for (const Rows* r : {&p.x, &p.y, &p.u, &p.z, &p.h}) wide = wide && rows_wide(*r, p.d, cfg->dtype);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int threads = threads_of(p.log_team), teams = threads >> p.log_team;
-  const int grid = grid_for((p.n + teams - 1) / teams * threads, threads, threads == 128 ? kFwdBlocks : 1);
-  const size_t smem = (size_t)(p.groups + 1) * 8;
+  cudaError_t e;
   {
     MT_LAUNCH("k_norm_fwd", s);
-    if (cfg->dtype == MT_F32) {
-      if (wide) norm_fwd_as<float, true>(p, grid, threads, smem, s);
-      else norm_fwd_as<float, false>(p, grid, threads, smem, s);
-    } else {
-      if (wide) norm_fwd_as<__nv_bfloat16, true>(p, grid, threads, smem, s);
-      else norm_fwd_as<__nv_bfloat16, false>(p, grid, threads, smem, s);
-    }
+    if (cfg->dtype == MT_F32) e = wide ? norm_fwd<float, true>(p, s) : norm_fwd<float, false>(p, s);
+    else e = wide ? norm_fwd<__nv_bfloat16, true>(p, s) : norm_fwd<__nv_bfloat16, false>(p, s);
   }
-  return cudaGetLastError() == cudaSuccess ? MT_OK : MT_ECUDA;
+  return e == cudaSuccess ? MT_OK : MT_ECUDA;
 }
 
 size_t mt_gated_norm_workspace_bytes(int64_t n, int32_t dim, int32_t groups) {
@@ -730,23 +882,17 @@ int mt_gated_norm_backward(const mt_gated_norm* cfg, const mt_rows* dz, const mt
   for (const Rows* r : {&p.dz, &p.dh, &p.y, &p.u, &p.z, &p.dx, &p.dy, &p.du})
     wide = wide && rows_wide(*r, p.d, cfg->dtype);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int threads = threads_of(p.log_team);
-  const size_t smem = (size_t)(p.groups + 1) * 8;
   if (p.n > 0) {
     MT_LAUNCH("k_norm_bwd", s);
-    const size_t sums = (size_t)(threads >> p.log_team) * p.d * 4;
-    if (cfg->dtype == MT_F32) {
-      if (wide) norm_bwd_as<float, true>(p, threads, smem + sums, s);
-      else norm_bwd_as<float, false>(p, threads, smem + sums, s);
-    } else {
-      if (wide) norm_bwd_as<__nv_bfloat16, true>(p, threads, smem + sums, s);
-      else norm_bwd_as<__nv_bfloat16, false>(p, threads, smem + sums, s);
-    }
+    cudaError_t e;
+    if (cfg->dtype == MT_F32) e = wide ? norm_bwd<float, true>(p, s) : norm_bwd<float, false>(p, s);
+    else e = wide ? norm_bwd<__nv_bfloat16, true>(p, s) : norm_bwd<__nv_bfloat16, false>(p, s);
+    if (e != cudaSuccess) return MT_ECUDA;
   }
   {
     MT_LAUNCH("k_norm_sums", s);
     const dim3 grid((p.d + 31) / 32, 2, p.groups);
-    k_norm_sums<<<grid, 256, smem, s>>>(p);
+    k_norm_sums<<<grid, 256, (size_t)(p.groups + 1) * 8, s>>>(p);
   }
   return cudaGetLastError() == cudaSuccess ? MT_OK : MT_ECUDA;
 }
