@@ -297,8 +297,8 @@ int mt_backward_adam_pooled(mt_table* t, const mt_lookup_result* res, int64_t n,
  * norms with a gate and a residual scale, and activations kept in 8 bits for
  * the backward.  Conventions of this section:
  *  - A row tensor is n rows of d columns of `dtype` (MT_F32 or MT_BF16), row i
- *    at data + i * ld elements, ld >= d: a slice of columns of a wider tensor
- *    is a row tensor.  Any element-aligned pointer and stride is taken; rows
+ *    at data + i * ld elements, d <= ld < 2^31: a slice of columns of a wider
+ *    tensor is a row tensor; n < 2^31.  Any element-aligned pointer and stride is taken; rows
  *    that all start on 16 bytes, with widths that are multiples of 8, take
  *    faster kernels.
  *  - Group g holds the rows [offsets[g], offsets[g+1]); offsets is device

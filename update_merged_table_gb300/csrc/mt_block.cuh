@@ -195,6 +195,9 @@ struct Raw8<float> {
   uint4 a, b;
 };
 
+// Element offset of a row: rows and strides fit 32 bits (checked on the host), so one wide multiplication.
+__device__ __forceinline__ size_t row_offset(long long row, int64_t ld) { return (size_t)(uint32_t)row * (uint32_t)ld; }
+
 // Columns [8 vec, 8 vec + 8) of `row`, or zeros where they lie past d.  AL: every row starts on 16 bytes (codes: 8)
 // and d is a multiple of 8.
 template <typename T, bool AL>
@@ -205,7 +208,7 @@ __device__ __forceinline__ Raw8<T> load8(const Rows& r, long long row, int vec, 
   const int c0 = vec * 8;
   if (c0 >= d) return v;
   if (r.data != nullptr) {
-    const T* p = static_cast<const T*>(r.data) + row * r.ld + c0;
+    const T* p = static_cast<const T*>(r.data) + row_offset(row, r.ld) + c0;
     if constexpr (AL) {
       v.a = __ldg(reinterpret_cast<const uint4*>(p));
       if constexpr (sizeof(T) == 4) v.b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
@@ -223,7 +226,7 @@ __device__ __forceinline__ Raw8<T> load8(const Rows& r, long long row, int vec, 
     }
   } else {
     const int nb = (d + kPackBlock - 1) / kPackBlock;
-    const int8_t* p = r.codes + row * d + c0;
+    const int8_t* p = r.codes + row_offset(row, d) + c0;
     if constexpr (AL) {
       const uint2 c = __ldg(reinterpret_cast<const uint2*>(p));
       v.a.x = c.x;
@@ -237,7 +240,7 @@ __device__ __forceinline__ Raw8<T> load8(const Rows& r, long long row, int vec, 
         else v.a.y |= q << (8 * (j - 4));
       }
     }
-    v.a.z = __ldg(r.exps + row * nb + c0 / kPackBlock);
+    v.a.z = __ldg(r.exps + row_offset(row, nb) + c0 / kPackBlock);
   }
   return v;
 }
@@ -270,39 +273,98 @@ __device__ __forceinline__ void widen8(const Raw8<T>& v, bool packed, float f[8]
   }
 }
 
-// Writes eight columns (those below d) rounded to T; f comes back as the values that were stored.
-template <typename T, bool AL>
-__device__ __forceinline__ void store8(void* data, long long ld, long long row, int vec, int d, float f[8]) {
-  const int c0 = vec * 8;
-  if (c0 >= d) return;
-  T* p = static_cast<T*>(data) + row * ld + c0;
-  if constexpr (AL && sizeof(T) == 4) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-  } else if constexpr (AL) {
-    Raw8<T> v;
-    v.a = make_uint4(bf16x2_of(f[0], f[1]), bf16x2_of(f[2], f[3]), bf16x2_of(f[4], f[5]), bf16x2_of(f[6], f[7]));
-    *reinterpret_cast<uint4*>(p) = v.a;
-    widen8<T>(v, false, f);
-  } else {
+// ---- eight columns as four pairs ----------------------------------------------------
+//
+// The norms are bound by the instructions they issue as soon as their loads
+// keep up, so their arithmetic works on pairs of columns (one instruction for
+// two fp32 operations, each rounded as the single one is).
+
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 both(float x) { return pk(x, x); }
+
+template <typename T>
+__device__ __forceinline__ void widen8(const Raw8<T>& v, bool packed, f32x2 (&f)[4]) {
+  if (packed) {
+    const float s = pack_scale(v.a.z);
+    float g[8];
+    codes_f(v.a.x, s, g);
+    codes_f(v.a.y, s, g + 4);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const T t = from_f<T>(f[j]);
-      if (c0 + j < d) p[j] = t;
-      f[j] = to_f<T>(t);
-    }
+    for (int j = 0; j < 4; ++j) f[j] = pk(g[2 * j], g[2 * j + 1]);
+  } else if constexpr (sizeof(T) == 4) {
+    const uint32_t w[8] = {v.a.x, v.a.y, v.a.z, v.a.w, v.b.x, v.b.y, v.b.z, v.b.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = pk(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+  } else {
+    const uint32_t w[4] = {v.a.x, v.a.y, v.a.z, v.a.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = bf16x2_to_f32x2(w[j]);
   }
 }
 
-// The 8-bit form of eight columns f (values past d are zero): four neighbouring lanes hold a block's 32 columns and
-// call this together.
-template <bool AL>
-__device__ __forceinline__ void store_packed8(const Rows& r, long long row, int vec, int d, const float f[8], bool live) {
-  uint32_t top = 0;
+// Rounds eight columns to T.
+template <typename T>
+__device__ __forceinline__ Raw8<T> narrow8(const f32x2 (&f)[4]) {
+  Raw8<T> v;
+  float2 g[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(f[j]) & 0x7FFFFFFFu);
-  top = max(top, __shfl_xor_sync(kFull, top, 1));
-  top = max(top, __shfl_xor_sync(kFull, top, 2));
+  for (int j = 0; j < 4; ++j) g[j] = upk(f[j]);
+  if constexpr (sizeof(T) == 4) {
+    v.a = make_uint4(__float_as_uint(g[0].x), __float_as_uint(g[0].y), __float_as_uint(g[1].x), __float_as_uint(g[1].y));
+    v.b = make_uint4(__float_as_uint(g[2].x), __float_as_uint(g[2].y), __float_as_uint(g[3].x), __float_as_uint(g[3].y));
+  } else {
+    v.a = make_uint4(bf16x2_of(g[0].x, g[0].y), bf16x2_of(g[1].x, g[1].y), bf16x2_of(g[2].x, g[2].y),
+                     bf16x2_of(g[3].x, g[3].y));
+  }
+  return v;
+}
+
+// Stores the columns of a vector that lie below d.
+template <typename T, bool AL>
+__device__ __forceinline__ void put8(const Rows& r, long long row, int vec, int d, const Raw8<T>& v) {
+  const int c0 = vec * 8;
+  if (c0 >= d) return;
+  T* p = static_cast<T*>(r.data) + row_offset(row, r.ld) + c0;
+  if constexpr (AL) {
+    *reinterpret_cast<uint4*>(p) = v.a;
+    if constexpr (sizeof(T) == 4) reinterpret_cast<uint4*>(p)[1] = v.b;
+  } else {
+    float f[8];
+    widen8<T>(v, false, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c0 + j < d) p[j] = from_f<T>(f[j]);
+  }
+}
+
+// The 8-bit form of a vector as it was stored or loaded (zeros past d): four neighbouring lanes hold a block's 32
+// columns and call this together.
+template <typename T, bool AL>
+__device__ __forceinline__ void put_packed8(const Rows& r, long long row, int vec, int d, const Raw8<T>& v, bool live) {
+  float f[8];
+  widen8<T>(v, false, f);
+  uint32_t top = 0;  // the largest magnitude as fp32 bits
+  if constexpr (sizeof(T) == 2) {  // magnitudes of bf16 order as their 15 bits do, two to a word
+    constexpr uint32_t k = 0x7FFF7FFFu;
+    top = __vmaxu2(__vmaxu2(v.a.x & k, v.a.y & k), __vmaxu2(v.a.z & k, v.a.w & k));
+    top = __vmaxu2(top, __shfl_xor_sync(kFull, top, 1));
+    top = __vmaxu2(top, __shfl_xor_sync(kFull, top, 2));
+    top = max(top << 16, top & 0xFFFF0000u);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+    top = max(top, __shfl_xor_sync(kFull, top, 1));
+    top = max(top, __shfl_xor_sync(kFull, top, 2));
+  }
   const int c0 = vec * 8;
   if (!live || c0 >= d) return;
   const uint32_t byte = pack_exp_byte(top);
@@ -315,7 +377,7 @@ __device__ __forceinline__ void store_packed8(const Rows& r, long long row, int 
     w[0] = pack_codes4_edge(f[0], f[1], f[2], f[3], inv);
     w[1] = pack_codes4_edge(f[4], f[5], f[6], f[7], inv);
   }
-  int8_t* p = r.codes + row * d + c0;
+  int8_t* p = r.codes + row_offset(row, d) + c0;
   if constexpr (AL) {
     *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
   } else {
@@ -323,7 +385,7 @@ __device__ __forceinline__ void store_packed8(const Rows& r, long long row, int 
     for (int j = 0; j < 8; ++j)
       if (c0 + j < d) p[j] = (int8_t)(w[j >> 2] >> (8 * (j & 3)));
   }
-  if ((vec & 3) == 0) r.exps[row * ((d + kPackBlock - 1) / kPackBlock) + vec / 4] = (uint8_t)byte;
+  if ((vec & 3) == 0) r.exps[row_offset(row, (d + kPackBlock - 1) / kPackBlock) + vec / 4] = (uint8_t)byte;
 }
 
 // ---- host-side checks ------------------------------------------------------------------
@@ -332,9 +394,9 @@ inline bool is_aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0
 
 inline size_t elem_bytes(int dtype) { return dtype == MT_F32 ? 4 : 2; }
 
-// A plain row tensor: pointer, element alignment, row stride of at least d.
+// A plain row tensor: pointer, element alignment, row stride of at least d and below 2^31.
 inline bool rows_ok(const void* data, int64_t ld, int64_t d, int dtype) {
-  return data != nullptr && is_aligned(data, elem_bytes(dtype)) && ld >= d;
+  return data != nullptr && is_aligned(data, elem_bytes(dtype)) && ld >= d && ld <= 0x7FFFFFFF;
 }
 
 // Whether eight-column vectors of a row tensor may be reached with 16-byte (codes: 8-byte) accesses.

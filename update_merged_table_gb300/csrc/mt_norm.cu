@@ -76,109 +76,155 @@ __device__ __forceinline__ void team_sum2(float& a, float& b, int team_lanes, fl
   slot ^= 1;
 }
 
-// Eight parameters of a group's row, `none` for an absent parameter and zero past d.
-__device__ __forceinline__ void param8(const float* p, int g, int vec, int d, int wide, float none, float f[8]) {
+// How the rows lie: any strides and widths; 16-byte vectors; 16-byte vectors that fill their team exactly (no lane
+// holds columns past d, so nothing is masked).
+constexpr int kAny = 0, kVectors = 1, kWhole = 2;
+
+// Zeros where a vector's columns lie past d.
+template <int MODE>
+__device__ __forceinline__ void mask8(f32x2 (&v)[4], int left) {
+  if constexpr (MODE == kVectors) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = left > 0 ? v[j] : 0ull;
+  } else if constexpr (MODE == kAny) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = upk(v[j]);
+      v[j] = pk(2 * j < left ? f.x : 0.0f, 2 * j + 1 < left ? f.y : 0.0f);
+    }
+  }
+}
+
+// Eight parameters of a group's row, `none` for an absent parameter and for a vector past d; zeros past d inside one.
+__device__ __forceinline__ void param8(const float* p, int g, int vec, int d, int wide, float none, f32x2 (&f)[4]) {
   const int c0 = vec * 8;
   if (p == nullptr || c0 >= d) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = none;
+    for (int j = 0; j < 4; ++j) f[j] = both(none);
     return;
   }
-  p += (size_t)g * d + c0;
+  p += (uint32_t)(g * d + c0);  // groups * d <= 2^23
   if (wide) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2*>(p)), b = __ldg(reinterpret_cast<const ulonglong2*>(p) + 1);
+    f[0] = a.x;
+    f[1] = a.y;
+    f[2] = b.x;
+    f[3] = b.y;
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = c0 + j < d ? __ldg(p + j) : 0.0f;
+    for (int j = 0; j < 4; ++j)
+      f[j] = pk(c0 + 2 * j < d ? __ldg(p + 2 * j) : 0.0f, c0 + 2 * j + 1 < d ? __ldg(p + 2 * j + 1) : 0.0f);
   }
 }
 
-// The gate's factors a = act(u) of eight columns and their derivatives.  fp32 rows take the accurate exponential and
-// division; for bf16 rows the fast ones (a few units of 2^-22) are far below the rounding of the result.  The choice is
-// made once for the eight, so that their chains overlap.
+// 1 / (1 + exp(-u)).  fp32 rows take the accurate exponential and division; for bf16 rows the hardware's own (2^-22 off)
+// are far below the rounding of the result.
 template <typename T>
-__device__ __forceinline__ void gate8(int gate, const float (&u)[8], float (&a)[8], float (&da)[8]) {
+__device__ __forceinline__ float sigmoid(float u) {
+  if constexpr (sizeof(T) == 4) return 1.0f / (1.0f + expf(-u));
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(u * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return r;
+}
+
+// The gate's factors a = act(u) of eight columns and their derivatives (where DA).  The choice of the gate is made once
+// for the eight, so that their chains overlap.
+template <typename T, bool DA>
+__device__ __forceinline__ void gate8(int gate, const f32x2 (&u)[4], f32x2 (&a)[4], f32x2 (&da)[4]) {
+  const f32x2 one = both(1.0f);
   if (gate == MT_GATE_LINEAR) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 4; ++j) {
       a[j] = u[j];
-      da[j] = 1.0f;
+      if constexpr (DA) da[j] = one;
     }
     return;
   }
-  float p[8];
+  f32x2 p[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if constexpr (sizeof(T) == 4) p[j] = 1.0f / (1.0f + expf(-u[j]));
-    else p[j] = __fdividef(1.0f, 1.0f + __expf(-fmaxf(u[j], -80.0f)));  // the fast division is 0 past 2^126: exp(80) < 2^116
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = upk(u[j]);
+    p[j] = pk(sigmoid<T>(f.x), sigmoid<T>(f.y));
   }
-  if (gate == MT_GATE_SIGMOID) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      a[j] = p[j];
-      da[j] = p[j] * (1.0f - p[j]);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      a[j] = u[j] * p[j];
-      da[j] = p[j] + a[j] * (1.0f - p[j]);
-    }
+  for (int j = 0; j < 4; ++j) {
+    const f32x2 q = sub2(one, p[j]);
+    a[j] = gate == MT_GATE_SIGMOID ? p[j] : mul2(u[j], p[j]);
+    if constexpr (DA) da[j] = gate == MT_GATE_SIGMOID ? mul2(p[j], q) : fma2(a[j], q, p[j]);
   }
 }
 
-// Mean (layer norm; 0 for rms) and inverse deviation of the rows held in v and w at once (one of them may be absent:
-// zeros).  Columns past d hold zeros and stay out of the deviation.
+__device__ __forceinline__ float pair_sum(f32x2 a) {
+  const float2 f = upk(a);
+  return f.x + f.y;
+}
+
+// A row v normalised is v * r + c: r its inverse deviation, c = -mean * r (0 for rms).  Both rows v and w at once (one
+// of them may be absent: zeros).  Columns past d hold zeros and stay out of the deviation.
 struct Stats {
-  float mean, r;
+  float r, c;
 };
-__device__ __forceinline__ void row_stats2(const float (&v)[kNV][8], const float (&w)[kNV][8], const NormParams& p,
+template <int MODE>
+__device__ __forceinline__ void row_stats2(const f32x2 (&v)[kNV][4], const f32x2 (&w)[kNV][4], const NormParams& p,
                                            int team, int lt, float2* s_red, int& slot, Stats& sv, Stats& sw) {
-  float a = 0.0f, b = 0.0f;
+  f32x2 a = 0ull, b = 0ull;
   const float inv_d = 1.0f / (float)p.d;
-  sv.mean = sw.mean = 0.0f;
+  float x, y, mv = 0.0f, mw = 0.0f;
   if (p.kind == MT_NORM_LAYER) {
 #pragma unroll
     for (int k = 0; k < kNV; ++k)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        a += v[k][j];
-        b += w[k][j];
+      for (int j = 0; j < 4; ++j) {
+        a = add2(a, v[k][j]);
+        b = add2(b, w[k][j]);
       }
-    team_sum2(a, b, team, s_red, slot);
-    sv.mean = a * inv_d;
-    sw.mean = b * inv_d;
-    a = b = 0.0f;
+    x = pair_sum(a);
+    y = pair_sum(b);
+    team_sum2(x, y, team, s_red, slot);
+    mv = x * inv_d;
+    mw = y * inv_d;
+    a = b = 0ull;
+    const f32x2 nv = both(-mv), nw = both(-mw);
 #pragma unroll
     for (int k = 0; k < kNV; ++k) {
-      const int left = p.d - (k * team + lt) * 8;
+      f32x2 cv[4], cw[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float c = j < left ? v[k][j] - sv.mean : 0.0f, e = j < left ? w[k][j] - sw.mean : 0.0f;
-        a += c * c;
-        b += e * e;
+      for (int j = 0; j < 4; ++j) {
+        cv[j] = add2(v[k][j], nv);
+        cw[j] = add2(w[k][j], nw);
+      }
+      mask8<MODE>(cv, p.d - (k * team + lt) * 8);
+      mask8<MODE>(cw, p.d - (k * team + lt) * 8);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        a = fma2(cv[j], cv[j], a);
+        b = fma2(cw[j], cw[j], b);
       }
     }
   } else {
 #pragma unroll
     for (int k = 0; k < kNV; ++k)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        a += v[k][j] * v[k][j];
-        b += w[k][j] * w[k][j];
+      for (int j = 0; j < 4; ++j) {
+        a = fma2(v[k][j], v[k][j], a);
+        b = fma2(w[k][j], w[k][j], b);
       }
   }
-  team_sum2(a, b, team, s_red, slot);
-  sv.r = rsqrtf(a * inv_d + p.eps);
-  sw.r = rsqrtf(b * inv_d + p.eps);
+  x = pair_sum(a);
+  y = pair_sum(b);
+  team_sum2(x, y, team, s_red, slot);
+  sv.r = rsqrtf(x * inv_d + p.eps);
+  sw.r = rsqrtf(y * inv_d + p.eps);
+  sv.c = -mv * sv.r;
+  sw.c = -mw * sw.r;
 }
-__device__ __forceinline__ Stats row_stats(const float (&v)[kNV][8], const NormParams& p, int team, int lt, float2* s_red,
+template <int MODE>
+__device__ __forceinline__ Stats row_stats(const f32x2 (&v)[kNV][4], const NormParams& p, int team, int lt, float2* s_red,
                                            int& slot) {
   Stats a, b;
-  const float none[kNV][8] = {};
-  row_stats2(v, none, p, team, lt, s_red, slot, a, b);
+  const f32x2 none[kNV][4] = {};
+  row_stats2<MODE>(v, none, p, team, lt, s_red, slot, a, b);
   return a;
 }
 
@@ -190,8 +236,8 @@ __device__ __forceinline__ Stats row_stats(const float (&v)[kNV][8], const NormP
 // registers.  Rows that cannot be reached with 16-byte accesses, and the
 // widest rows in fp32 (whose stages would not fit), are loaded when they are used.
 
-template <typename T, bool AL, int THREADS>
-constexpr bool kStaged = AL && (THREADS == 128 || sizeof(T) == 2);
+template <typename T, int MODE, int THREADS>
+constexpr bool kStaged = MODE != kAny && (THREADS == 128 || sizeof(T) == 2);
 constexpr uint32_t kNoExp = 0xFFFFFFFFu;  // plain rows have no exponent byte
 template <typename T>
 constexpr int kVecBytes = 8 * (int)sizeof(T);
@@ -226,10 +272,10 @@ __device__ __forceinline__ void fetch8(uint32_t dst, const Rows& r, long long ro
   const bool on = c0 < d;
   if (packed) {
     const int nb = (d + kPackBlock - 1) / kPackBlock;
-    copy8(dst, r.codes + (on ? row * d + c0 : 0), on);
-    e = on ? (uint32_t)__ldg(r.exps + row * nb + c0 / kPackBlock) : 127u;
+    copy8(dst, r.codes + (on ? row_offset(row, d) + c0 : 0), on);
+    e = on ? (uint32_t)__ldg(r.exps + row_offset(row, nb) + c0 / kPackBlock) : 127u;
   } else {
-    const T* p = static_cast<const T*>(r.data) + (on ? row * r.ld + c0 : 0);
+    const T* p = static_cast<const T*>(r.data) + (on ? row_offset(row, r.ld) + c0 : 0);
     copy16(dst, p, on);
     if constexpr (sizeof(T) == 4) copy16(dst + 16, p + 4, on);
   }
@@ -247,10 +293,10 @@ __device__ __forceinline__ Raw8<T> staged8(uint32_t at, uint32_t e) {
 // Blocks of 128 threads that share an SM's registers (wider rows: one block of 512).
 constexpr int kFwdBlocks = 6, kBwdBlocks = 3;
 
-template <typename T, bool AL, int THREADS>
+template <typename T, int MODE, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == 128 ? (sizeof(T) == 4 ? 4 : kFwdBlocks) : 1)
 k_norm_fwd(const NormParams p) {
-  constexpr bool STAGED = kStaged<T, AL, THREADS>;
+  constexpr bool AL = MODE != kAny, STAGED = kStaged<T, MODE, THREADS>;
   using St = Stages<T, THREADS, 3>;
   extern __shared__ __align__(16) uint8_t s_raw[];  // the stages, then the offsets
   __shared__ float2 s_red[32];
@@ -269,27 +315,27 @@ k_norm_fwd(const NormParams p) {
   for (long long q0 = (long long)blockIdx.x * teams; q0 < p.n - m; q0 += (long long)gridDim.x * teams) {
     const long long q = q0 + sub, row = q < off0 ? q : q + m;
     const bool in = q < p.n - m;
+    const Raw8<T> zero{};
 #pragma unroll
     for (int k = 0; k < kNV; ++k) {
       const int vec = k * team + lt;
-      float zero[8] = {};
-      if (in && p.z.data != nullptr) store8<T, AL>(p.z.data, p.z.ld, row, vec, p.d, zero);
-      if (in && has_h) store8<T, AL>(p.h.data, p.h.ld, row, vec, p.d, zero);
-      if (p.y.codes != nullptr) store_packed8<AL>(p.y, row, vec, p.d, zero, in);
-      if (p.u.codes != nullptr) store_packed8<AL>(p.u, row, vec, p.d, zero, in);
-      if (p.z.codes != nullptr) store_packed8<AL>(p.z, row, vec, p.d, zero, in);
-      if (p.h.codes != nullptr) store_packed8<AL>(p.h, row, vec, p.d, zero, in);
+      if (in && p.z.data != nullptr) put8<T, AL>(p.z, row, vec, p.d, zero);
+      if (in && has_h) put8<T, AL>(p.h, row, vec, p.d, zero);
+      if (p.y.codes != nullptr) put_packed8<T, AL>(p.y, row, vec, p.d, zero, in);
+      if (p.u.codes != nullptr) put_packed8<T, AL>(p.u, row, vec, p.d, zero, in);
+      if (p.z.codes != nullptr) put_packed8<T, AL>(p.z, row, vec, p.d, zero, in);
+      if (p.h.codes != nullptr) put_packed8<T, AL>(p.h, row, vec, p.d, zero, in);
     }
   }
 
   const long long end = run_start(off0, m, blockIdx.x + 1, gridDim.x);
   long long first = run_start(off0, m, blockIdx.x, gridDim.x);
   for (int g = first < end ? row_group(s_off, p.groups, first) : 0; first < end; ++g) {
-    const long long last = min(end, s_off[g + 1]);
-    auto fetch = [&](long long base, int s) {
+    const int last = (int)min(end, s_off[g + 1]);
+    // a row's vectors start on their way, or are loaded where they are used
+    auto fetch = [&](int base, int s) {
       const bool live = base + sub < last;
-      const long long row = live ? base + sub : base;
-      const int dd = live ? p.d : 0;
+      const int row = live ? base + sub : base, dd = live ? p.d : 0;
       uint32_t none;
 #pragma unroll
       for (int k = 0; k < kNV; ++k) {
@@ -301,105 +347,97 @@ k_norm_fwd(const NormParams p) {
     };
     int cur = 0;
     if constexpr (STAGED) {
-      if (first < last) fetch(first, 0);
+      if (first < last) fetch((int)first, 0);
       copies_close();
     }
     // every team of the block runs the same number of rounds, so the shuffles and barriers meet
-    for (long long base = first; base < last; base += teams, cur ^= 1) {
+    for (int base = (int)first; base < last; base += teams, cur ^= 1) {
       const bool live = base + sub < last;
-      const long long row = live ? base + sub : base;
-      const int dd = live ? p.d : 0;
-      Raw8<T> rx[kNV], ry[kNV], ru[kNV];
+      const int row = live ? base + sub : base, dd = live ? p.d : 0;  // a team without a row computes on zeros
       if constexpr (STAGED) {
         if (base + teams < last) fetch(base + teams, cur ^ 1);
         copies_close();
         copies_wait<1>();
       }
-#pragma unroll
-      for (int k = 0; k < kNV; ++k) {
-        const int vec = k * team + lt;
-        if constexpr (STAGED) {
-          if (has_y) ry[k] = staged8<T>(st.at(cur, 0, k), kNoExp);
-          if (has_u) ru[k] = staged8<T>(st.at(cur, 1, k), kNoExp);
-          rx[k] = staged8<T>(st.at(cur, 2, k), kNoExp);
-        } else {
-          if (has_y) ry[k] = load8<T, AL>(p.y, row, vec, dd);
-          rx[k] = load8<T, AL>(p.x, row, vec, dd);
-          if (has_u) ru[k] = load8<T, AL>(p.u, row, vec, dd);
-        }
-      }
-      float z[kNV][8];
+      auto get = [&](int i, const Rows& r, int k) {
+        if constexpr (STAGED) return staged8<T>(st.at(cur, i, k), kNoExp);
+        else return load8<T, AL>(r, row, k * team + lt, dd);
+      };
+      f32x2 z[kNV][4];
       if (has_y) {
-        float y[kNV][8];
+        f32x2 y[kNV][4];
 #pragma unroll
-        for (int k = 0; k < kNV; ++k) widen8<T>(ry[k], false, y[k]);
-        const Stats sy = row_stats(y, p, team, lt, s_red, slot);
+        for (int k = 0; k < kNV; ++k) {
+          const Raw8<T> raw = get(0, p.y, k);
+          widen8<T>(raw, false, y[k]);
+          if (p.y.codes != nullptr) put_packed8<T, AL>(p.y, row, k * team + lt, p.d, raw, live);
+        }
+        const Stats sy = row_stats<MODE>(y, p, team, lt, s_red, slot);
+        const f32x2 r2 = both(sy.r), c2 = both(sy.c);
 #pragma unroll
         for (int k = 0; k < kNV; ++k) {
           const int vec = k * team + lt;
-          if (p.y.codes != nullptr) store_packed8<AL>(p.y, row, vec, p.d, y[k], live);
-          float w[8], f[8];
-          param8(p.wp, g, vec, p.d, p.wide, 1.0f, w);
+          f32x2 f[4];
+          param8(p.wp, g, vec, p.d, p.wide, 1.0f, f);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) y[k][j] = w[j] * ((y[k][j] - sy.mean) * sy.r);
+          for (int j = 0; j < 4; ++j) y[k][j] = mul2(f[j], fma2(y[k][j], r2, c2));
+          if (MODE != kWhole) mask8<MODE>(y[k], p.d - vec * 8);
           if (p.bp != nullptr) {
             param8(p.bp, g, vec, p.d, p.wide, 0.0f, f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[k][j] += f[j];
+            for (int j = 0; j < 4; ++j) y[k][j] = add2(y[k][j], f[j]);
           }
           if (p.sc != nullptr) {
             param8(p.sc, g, vec, p.d, p.wide, 1.0f, f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[k][j] *= f[j];
+            for (int j = 0; j < 4; ++j) y[k][j] = mul2(y[k][j], f[j]);
           }
+          widen8<T>(get(2, p.x, k), false, z[k]);
           if (has_u) {
-            float u[8], da[8];
-            widen8<T>(ru[k], false, u);
-            if (p.u.codes != nullptr) store_packed8<AL>(p.u, row, vec, p.d, u, live);
-            gate8<T>(p.gate, u, f, da);
+            f32x2 u[4], da[4];
+            const Raw8<T> raw = get(1, p.u, k);
+            widen8<T>(raw, false, u);
+            if (p.u.codes != nullptr) put_packed8<T, AL>(p.u, row, vec, p.d, raw, live);
+            gate8<T, false>(p.gate, u, f, da);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[k][j] *= f[j];
-          }
-          widen8<T>(rx[k], false, z[k]);
-          const int left = p.d - vec * 8;
+            for (int j = 0; j < 4; ++j) z[k][j] = fma2(y[k][j], f[j], z[k][j]);
+          } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (AL || j < left) z[k][j] += y[k][j];
-          if (AL && left <= 0) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) z[k][j] = 0.0f;
+            for (int j = 0; j < 4; ++j) z[k][j] = add2(z[k][j], y[k][j]);
           }
         }
       } else {
 #pragma unroll
-        for (int k = 0; k < kNV; ++k) widen8<T>(rx[k], false, z[k]);
+        for (int k = 0; k < kNV; ++k) widen8<T>(get(2, p.x, k), false, z[k]);
       }
-      if (has_h) {
-        const Stats sz = row_stats(z, p, team, lt, s_red, slot);
+      if (p.z.data != nullptr || p.z.codes != nullptr) {
 #pragma unroll
         for (int k = 0; k < kNV; ++k) {
-          const int vec = k * team + lt, left = p.d - vec * 8;
-          float w[8], h[8];
-          param8(p.wq, g, vec, p.d, p.wide, 1.0f, w);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) h[j] = w[j] * ((z[k][j] - sz.mean) * sz.r);
-          if (p.bq != nullptr) {
-            param8(p.bq, g, vec, p.d, p.wide, 0.0f, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) h[j] += w[j];
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (AL ? left <= 0 : j >= left) h[j] = 0.0f;
-          if (live) store8<T, AL>(p.h.data, p.h.ld, row, vec, p.d, h);
-          if (p.h.codes != nullptr) store_packed8<AL>(p.h, row, vec, p.d, h, live);
+          const Raw8<T> raw = narrow8<T>(z[k]);
+          if (p.z.data != nullptr && live) put8<T, AL>(p.z, row, k * team + lt, p.d, raw);
+          if (p.z.codes != nullptr) put_packed8<T, AL>(p.z, row, k * team + lt, p.d, raw, live);
         }
       }
+      if (has_h) {
+        const Stats sz = row_stats<MODE>(z, p, team, lt, s_red, slot);
+        const f32x2 r2 = both(sz.r), c2 = both(sz.c);
 #pragma unroll
-      for (int k = 0; k < kNV; ++k) {
-        const int vec = k * team + lt;
-        if (p.z.data != nullptr && live) store8<T, AL>(p.z.data, p.z.ld, row, vec, p.d, z[k]);
-        if (p.z.codes != nullptr) store_packed8<AL>(p.z, row, vec, p.d, z[k], live);
+        for (int k = 0; k < kNV; ++k) {
+          const int vec = k * team + lt;
+          f32x2 f[4];
+          param8(p.wq, g, vec, p.d, p.wide, 1.0f, f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) z[k][j] = mul2(f[j], fma2(z[k][j], r2, c2));
+          if (MODE != kWhole) mask8<MODE>(z[k], p.d - vec * 8);
+          if (p.bq != nullptr) {
+            param8(p.bq, g, vec, p.d, p.wide, 0.0f, f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) z[k][j] = add2(z[k][j], f[j]);
+          }
+          const Raw8<T> raw = narrow8<T>(z[k]);
+          if (live) put8<T, AL>(p.h, row, vec, p.d, raw);
+          if (p.h.codes != nullptr) put_packed8<T, AL>(p.h, row, vec, p.d, raw, live);
+        }
       }
     }
     first = last;
@@ -407,31 +445,39 @@ k_norm_fwd(const NormParams p) {
 }
 
 // dv = r * (dvh - [mean dvh] - vh * mean(dvh * vh)), the gradient through a norm, in place of dvh.
-__device__ __forceinline__ void norm_grad(float (&dvh)[kNV][8], const float (&vh)[kNV][8], float r, const NormParams& p,
-                                          int team, float2* s_red, int& slot) {
-  float a = 0.0f, b = 0.0f;
+template <int MODE>
+__device__ __forceinline__ void norm_grad(f32x2 (&dvh)[kNV][4], const f32x2 (&vh)[kNV][4], float r, const NormParams& p,
+                                          int team, int lt, float2* s_red, int& slot) {
+  const bool layer = p.kind == MT_NORM_LAYER;
+  f32x2 a = 0ull, b = 0ull;
 #pragma unroll
   for (int k = 0; k < kNV; ++k)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      a += dvh[k][j] * vh[k][j];
-      b += dvh[k][j];
-    }
-  team_sum2(a, b, team, s_red, slot);
+    for (int j = 0; j < 4; ++j) a = fma2(dvh[k][j], vh[k][j], a);
+  if (layer) {
+#pragma unroll
+    for (int k = 0; k < kNV; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b = add2(b, dvh[k][j]);
+  }
+  float x = pair_sum(a), y = pair_sum(b);
+  team_sum2(x, y, team, s_red, slot);
   const float inv_d = 1.0f / (float)p.d;
-  const float ma = r * a * inv_d, mb = p.kind == MT_NORM_LAYER ? r * b * inv_d : 0.0f;
+  const f32x2 r2 = both(r), ma = both(-r * x * inv_d), mb = both(-r * y * inv_d);
 #pragma unroll
-  for (int k = 0; k < kNV; ++k)
+  for (int k = 0; k < kNV; ++k) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dvh[k][j] = r * dvh[k][j] - mb - vh[k][j] * ma;
+    for (int j = 0; j < 4; ++j) dvh[k][j] = fma2(vh[k][j], ma, fma2(dvh[k][j], r2, mb));
+    if (MODE != kWhole && layer) mask8<MODE>(dvh[k], p.d - (k * team + lt) * 8);
+  }
 }
 
 // BIAS: the norms have biases (their sums S2 and T2 are kept too).
-template <typename T, bool AL, int THREADS, bool BIAS>
+template <typename T, int MODE, int THREADS, bool BIAS>
 __global__ void __launch_bounds__(THREADS, THREADS == 128 ? (sizeof(T) == 4 ? 2 : kBwdBlocks) : 1)
 k_norm_bwd(const NormParams p) {
+  constexpr bool AL = MODE != kAny, STAGED = kStaged<T, MODE, THREADS>;
   constexpr int kAcc = BIAS ? 4 : 2;       // S1, T1, S2, T2
-  constexpr bool STAGED = kStaged<T, AL, THREADS>;
   using St = Stages<T, THREADS, 5>;
   extern __shared__ __align__(16) uint8_t s_raw[];  // the stages (later the sums of the block's teams), the offsets
   __shared__ float2 s_red[32];
@@ -453,33 +499,30 @@ k_norm_bwd(const NormParams p) {
   // rows in no group: their gradients are zero
   for (long long q = (long long)blockIdx.x * teams + sub; q < p.n - m; q += (long long)gridDim.x * teams) {
     const long long row = q < off0 ? q : q + m;
-    float zero[8] = {};
+    const Raw8<T> zero{};
 #pragma unroll
     for (int k = 0; k < kNV; ++k) {
       const int vec = k * team + lt;
-      store8<T, AL>(p.dx.data, p.dx.ld, row, vec, p.d, zero);
-      if (has_y) store8<T, AL>(p.dy.data, p.dy.ld, row, vec, p.d, zero);
-      if (has_u) store8<T, AL>(p.du.data, p.du.ld, row, vec, p.d, zero);
+      put8<T, AL>(p.dx, row, vec, p.d, zero);
+      if (has_y) put8<T, AL>(p.dy, row, vec, p.d, zero);
+      if (has_u) put8<T, AL>(p.du, row, vec, p.d, zero);
     }
   }
 
   const long long end = run_start(off0, m, blockIdx.x + 1, gridDim.x);
   long long first = run_start(off0, m, blockIdx.x, gridDim.x);
   for (int g = first < end ? row_group(s_off, p.groups, first) : 0; first < end; ++g) {
-    const long long last = min(end, s_off[g + 1]);
+    const int last = (int)min(end, s_off[g + 1]);
     if (last <= first) continue;  // an empty group
-    float acc[kAcc][kNV][8];
-#pragma unroll
-    for (int q = 0; q < kAcc; ++q)
-#pragma unroll
-      for (int k = 0; k < kNV; ++k)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[q][k][j] = 0.0f;
+    f32x2 acc[kAcc][kNV][4] = {};
     uint32_t next_e[3][kNV];  // exponent bytes of the rows on their way: z, y, u
-    auto fetch = [&](long long base, int s) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+#pragma unroll
+      for (int k = 0; k < kNV; ++k) next_e[i][k] = kNoExp;
+    auto fetch = [&](int base, int s) {
       const bool live = base + sub < last;
-      const long long row = live ? base + sub : base;
-      const int dd = live ? p.d : 0;  // a team without a row computes on zeros
+      const int row = live ? base + sub : base, dd = live ? p.d : 0;
 #pragma unroll
       for (int k = 0; k < kNV; ++k) {
         const int vec = k * team + lt;
@@ -491,19 +534,14 @@ k_norm_bwd(const NormParams p) {
         if (has_u) fetch8<T>(st.at(s, 4, k), p.u, row, vec, dd, u8, next_e[2][k]);
       }
     };
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-#pragma unroll
-      for (int k = 0; k < kNV; ++k) next_e[i][k] = kNoExp;
     int cur = 0;
     if constexpr (STAGED) {
-      fetch(first, 0);
+      fetch((int)first, 0);
       copies_close();
     }
-    for (long long base = first; base < last; base += teams, cur ^= 1) {
+    for (int base = (int)first; base < last; base += teams, cur ^= 1) {
       const bool live = base + sub < last;
-      const long long row = live ? base + sub : base;
-      const int dd = live ? p.d : 0;
+      const int row = live ? base + sub : base, dd = live ? p.d : 0;  // a team without a row computes on zeros
       uint32_t e[3][kNV];
       if constexpr (STAGED) {
 #pragma unroll
@@ -519,103 +557,95 @@ k_norm_bwd(const NormParams p) {
         if constexpr (STAGED) return staged8<T>(st.at(cur, i, k), ex);
         else return load8<T, AL>(r, row, k * team + lt, dd);
       };
-      Raw8<T> ry[kNV], ru[kNV], rz[kNV], rdz[kNV], rdh[kNV];
-#pragma unroll
-      for (int k = 0; k < kNV; ++k) {
-        if (has_h) rz[k] = get(0, p.z, k, e[0][k]);
-        if (has_y) ry[k] = get(1, p.y, k, e[1][k]);
-        if (has_h) rdh[k] = get(2, p.dh, k, kNoExp);
-        if (has_dz) rdz[k] = get(3, p.dz, k, kNoExp);
-        if (has_u) ru[k] = get(4, p.u, k, e[2][k]);
-      }
       Stats sy, sz;
-      float yh[kNV][8] = {}, D[kNV][8] = {};
+      f32x2 yh[kNV][4] = {}, D[kNV][4] = {};
       {
-        float zh[kNV][8] = {};
+        f32x2 zh[kNV][4] = {};
 #pragma unroll
         for (int k = 0; k < kNV; ++k) {
-          if (has_h) widen8<T>(rz[k], z8, zh[k]);
-          if (has_y) widen8<T>(ry[k], y8, yh[k]);
+          if (has_h) widen8<T>(get(0, p.z, k, e[0][k]), z8, zh[k]);
+          if (has_y) widen8<T>(get(1, p.y, k, e[1][k]), y8, yh[k]);
         }
-        row_stats2(yh, zh, p, team, lt, s_red, slot, sy, sz);
+        row_stats2<MODE>(yh, zh, p, team, lt, s_red, slot, sy, sz);
         if (has_h) {  // through the next block's norm
+          const f32x2 r2 = both(sz.r), c2 = both(sz.c);
 #pragma unroll
           for (int k = 0; k < kNV; ++k) {
-            const int vec = k * team + lt, left = p.d - vec * 8;
-            float dh[8], w[8];
-            widen8<T>(rdh[k], false, dh);
+            const int vec = k * team + lt;
+            f32x2 dh[4], w[4];
+            widen8<T>(get(2, p.dh, k, kNoExp), false, dh);
             param8(p.wq, g, vec, p.d, p.wide, 1.0f, w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              zh[k][j] = (AL ? left > 0 : j < left) ? (zh[k][j] - sz.mean) * sz.r : 0.0f;
-              acc[1][k][j] += dh[j] * zh[k][j];
-              if constexpr (BIAS) acc[3][k][j] += dh[j];
-              D[k][j] = dh[j] * w[j];  // dh is zero past d
+            for (int j = 0; j < 4; ++j) zh[k][j] = fma2(zh[k][j], r2, c2);
+            mask8<MODE>(zh[k], p.d - vec * 8);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              acc[1][k][j] = fma2(dh[j], zh[k][j], acc[1][k][j]);
+              if constexpr (BIAS) acc[3][k][j] = add2(acc[3][k][j], dh[j]);
+              D[k][j] = mul2(dh[j], w[j]);  // dh is zero past d
             }
           }
-          norm_grad(D, zh, sz.r, p, team, s_red, slot);
+          norm_grad<MODE>(D, zh, sz.r, p, team, lt, s_red, slot);
         }
       }
       if (has_dz) {
 #pragma unroll
         for (int k = 0; k < kNV; ++k) {
-          float dz[8];
-          widen8<T>(rdz[k], false, dz);
+          f32x2 dz[4];
+          widen8<T>(get(3, p.dz, k, kNoExp), false, dz);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) D[k][j] += dz[j];
+          for (int j = 0; j < 4; ++j) D[k][j] = add2(D[k][j], dz[j]);
         }
       }
+      if (live) {
+#pragma unroll
+        for (int k = 0; k < kNV; ++k) put8<T, AL>(p.dx, row, k * team + lt, p.d, narrow8<T>(D[k]));
+      }
       if (has_y) {
-        float dyh[kNV][8];
+        const f32x2 r2 = both(sy.r), c2 = both(sy.c);
 #pragma unroll
         for (int k = 0; k < kNV; ++k) {
-          const int vec = k * team + lt, left = p.d - vec * 8;
-          float w[8], s[8], Da[8];
+          const int vec = k * team + lt;
+          f32x2 w[4], s[4];
           param8(p.wp, g, vec, p.d, p.wide, 1.0f, w);
           param8(p.sc, g, vec, p.d, p.wide, 1.0f, s);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const bool on = live && (AL ? left > 0 : j < left);
-            yh[k][j] = on ? (yh[k][j] - sy.mean) * sy.r : 0.0f;
-            Da[j] = on ? D[k][j] : 0.0f;
-          }
+          for (int j = 0; j < 4; ++j) yh[k][j] = fma2(yh[k][j], r2, c2);
+          mask8<MODE>(yh[k], p.d - vec * 8);
           if (has_u) {
-            float u[8], a[8], da[8];
-            widen8<T>(ru[k], u8, u);
-            gate8<T>(p.gate, u, a, da);
+            f32x2 u[4], a[4], da[4];
+            widen8<T>(get(4, p.u, k, e[2][k]), u8, u);
+            gate8<T, true>(p.gate, u, a, da);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              u[j] = w[j] * yh[k][j];
-              da[j] *= Da[j] * s[j];
-              Da[j] *= a[j];
+            for (int j = 0; j < 4; ++j) {
+              u[j] = mul2(w[j], yh[k][j]);
+              da[j] = mul2(da[j], mul2(D[k][j], s[j]));
+              D[k][j] = mul2(D[k][j], a[j]);
             }
             if constexpr (BIAS) {
               if (p.bp != nullptr) {
                 param8(p.bp, g, vec, p.d, p.wide, 0.0f, a);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) u[j] += a[j];
+                for (int j = 0; j < 4; ++j) u[j] = add2(u[j], a[j]);
               }
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) da[j] *= u[j];
-            if (live) store8<T, AL>(p.du.data, p.du.ld, row, vec, p.d, da);
+            for (int j = 0; j < 4; ++j) da[j] = mul2(da[j], u[j]);
+            if (live) put8<T, AL>(p.du, row, vec, p.d, narrow8<T>(da));
           }
+          // D now holds D a
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            acc[0][k][j] += Da[j] * yh[k][j];
-            if constexpr (BIAS) acc[2][k][j] += Da[j];
-            dyh[k][j] = Da[j] * s[j] * w[j];
+          for (int j = 0; j < 4; ++j) {
+            acc[0][k][j] = fma2(D[k][j], yh[k][j], acc[0][k][j]);
+            if constexpr (BIAS) acc[2][k][j] = add2(acc[2][k][j], D[k][j]);
+            D[k][j] = mul2(mul2(D[k][j], s[j]), w[j]);
           }
         }
-        norm_grad(dyh, yh, sy.r, p, team, s_red, slot);
+        norm_grad<MODE>(D, yh, sy.r, p, team, lt, s_red, slot);
         if (live) {
 #pragma unroll
-          for (int k = 0; k < kNV; ++k) store8<T, AL>(p.dy.data, p.dy.ld, row, k * team + lt, p.d, dyh[k]);
+          for (int k = 0; k < kNV; ++k) put8<T, AL>(p.dy, row, k * team + lt, p.d, narrow8<T>(D[k]));
         }
-      }
-      if (live) {
-#pragma unroll
-        for (int k = 0; k < kNV; ++k) store8<T, AL>(p.dx.data, p.dx.ld, row, k * team + lt, p.d, D[k]);
       }
     }
     if constexpr (STAGED) copies_wait<0>();
@@ -627,9 +657,11 @@ k_norm_bwd(const NormParams p) {
 #pragma unroll
       for (int k = 0; k < kNV; ++k)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int col = (k * team + lt) * 8 + j;
-          if (col < p.d) s_sum[sub * p.d + col] = acc[q][k][j];
+        for (int j = 0; j < 4; ++j) {
+          const int col = (k * team + lt) * 8 + 2 * j;
+          const float2 f = upk(acc[q][k][j]);
+          if (col < p.d) s_sum[sub * p.d + col] = f.x;
+          if (col + 1 < p.d) s_sum[sub * p.d + col + 1] = f.y;
         }
       __syncthreads();
       float* out = p.part + ((size_t)(blockIdx.x + g) * kSums + (q == 0 ? 0 : q == 1 ? 2 : q == 2 ? 1 : 3)) * p.d;
@@ -644,11 +676,12 @@ k_norm_bwd(const NormParams p) {
   }
 }
 
-// The parameter gradients of each group from its runs' partial sums: 32 columns by 8 slices of runs per block, in
+// The parameter gradients of each group from its runs' partial sums: 32 columns by 32 slices of runs per block, in
 // fp64, the slices joined in their order.
-__global__ void __launch_bounds__(256) k_norm_sums(const NormParams p) {
+constexpr int kSlices = 32;
+__global__ void __launch_bounds__(32 * kSlices) k_norm_sums(const NormParams p) {
   extern __shared__ long long s_off[];
-  __shared__ double s_part[2][8][33];
+  __shared__ double s_part[2][kSlices][33];
   load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;
@@ -662,7 +695,7 @@ __global__ void __launch_bounds__(256) k_norm_sums(const NormParams p) {
       const int b0 = run_of(s_off[g] - off0, m, p.blocks), b1 = run_of(s_off[g + 1] - 1 - off0, m, p.blocks);
       const float* base = p.part + (size_t)(post ? 0 : 2) * p.d + col;
 #pragma unroll 4
-      for (int k = b0 + slice; k <= b1; k += 8) {
+      for (int k = b0 + slice; k <= b1; k += kSlices) {
         const float* at = base + (size_t)(k + g) * kSums * p.d;
         a += (double)__ldg(at);
         if (second) b += (double)__ldg(at + p.d);
@@ -672,7 +705,7 @@ __global__ void __launch_bounds__(256) k_norm_sums(const NormParams p) {
     s_part[1][slice][lane] = b;
     __syncthreads();
     if (slice == 0 && col < p.d) {
-      for (int k = 1; k < 8; ++k) {
+      for (int k = 1; k < kSlices; ++k) {
         a += s_part[0][k][lane];
         b += s_part[1][k][lane];
       }
@@ -744,35 +777,37 @@ cudaError_t allow_smem(K kernel, size_t bytes) {
   return cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-template <typename T, bool AL, int THREADS>
+template <typename T, int MODE, int THREADS>
 cudaError_t norm_fwd_as(const NormParams& p, cudaStream_t s) {
   const int teams = THREADS >> p.log_team;
   const int grid = grid_for((p.n + teams - 1) / teams * THREADS, THREADS, THREADS == 128 ? kFwdBlocks : 1);
-  const size_t smem = (kStaged<T, AL, THREADS> ? Stages<T, THREADS, 3>::kBytes : 0) + (size_t)(p.groups + 1) * 8;
-  const cudaError_t e = allow_smem(k_norm_fwd<T, AL, THREADS>, smem);
+  const size_t smem = (kStaged<T, MODE, THREADS> ? Stages<T, THREADS, 3>::kBytes : 0) + (size_t)(p.groups + 1) * 8;
+  const cudaError_t e = allow_smem(k_norm_fwd<T, MODE, THREADS>, smem);
   if (e != cudaSuccess) return e;
-  k_norm_fwd<T, AL, THREADS><<<grid, THREADS, smem, s>>>(p);
+  k_norm_fwd<T, MODE, THREADS><<<grid, THREADS, smem, s>>>(p);
   return cudaGetLastError();
 }
-template <typename T, bool AL, int THREADS, bool BIAS>
+template <typename T, int MODE, int THREADS, bool BIAS>
 cudaError_t norm_bwd_as(const NormParams& p, cudaStream_t s) {
   const size_t smem =
-      (kStaged<T, AL, THREADS> ? Stages<T, THREADS, 5>::kBytes : 16 * THREADS * 4) + (size_t)(p.groups + 1) * 8;
-  const cudaError_t e = allow_smem(k_norm_bwd<T, AL, THREADS, BIAS>, smem);
+      (kStaged<T, MODE, THREADS> ? Stages<T, THREADS, 5>::kBytes : 16 * THREADS * 4) + (size_t)(p.groups + 1) * 8;
+  const cudaError_t e = allow_smem(k_norm_bwd<T, MODE, THREADS, BIAS>, smem);
   if (e != cudaSuccess) return e;
-  k_norm_bwd<T, AL, THREADS, BIAS><<<p.blocks, THREADS, smem, s>>>(p);
+  k_norm_bwd<T, MODE, THREADS, BIAS><<<p.blocks, THREADS, smem, s>>>(p);
   return cudaGetLastError();
 }
-template <typename T, bool AL>
+template <typename T, int MODE>
 cudaError_t norm_fwd(const NormParams& p, cudaStream_t s) {
-  return p.log_team > 7 ? norm_fwd_as<T, AL, 512>(p, s) : norm_fwd_as<T, AL, 128>(p, s);
+  return p.log_team > 7 ? norm_fwd_as<T, MODE, 512>(p, s) : norm_fwd_as<T, MODE, 128>(p, s);
 }
-template <typename T, bool AL>
+template <typename T, int MODE>
 cudaError_t norm_bwd(const NormParams& p, cudaStream_t s) {
   const bool bias = p.bp != nullptr || p.bq != nullptr;
-  if (p.log_team > 7) return bias ? norm_bwd_as<T, AL, 512, true>(p, s) : norm_bwd_as<T, AL, 512, false>(p, s);
-  return bias ? norm_bwd_as<T, AL, 128, true>(p, s) : norm_bwd_as<T, AL, 128, false>(p, s);
+  if (p.log_team > 7) return bias ? norm_bwd_as<T, MODE, 512, true>(p, s) : norm_bwd_as<T, MODE, 512, false>(p, s);
+  return bias ? norm_bwd_as<T, MODE, 128, true>(p, s) : norm_bwd_as<T, MODE, 128, false>(p, s);
 }
+
+int mode_of(const NormParams& p, bool wide) { return !wide ? kAny : (16 << p.log_team) == p.d ? kWhole : kVectors; }
 
 bool packed_rows(const Rows& r) { return r.codes != nullptr && r.exps != nullptr; }
 bool half_packed(const Rows& r) { return (r.codes == nullptr) != (r.exps == nullptr); }
@@ -812,8 +847,13 @@ int mt_gated_norm_forward(const mt_gated_norm* cfg, const mt_rows* x, const mt_r
   cudaError_t e;
   {
     MT_LAUNCH("k_norm_fwd", s);
-    if (cfg->dtype == MT_F32) e = wide ? norm_fwd<float, true>(p, s) : norm_fwd<float, false>(p, s);
-    else e = wide ? norm_fwd<__nv_bfloat16, true>(p, s) : norm_fwd<__nv_bfloat16, false>(p, s);
+    const int mode = mode_of(p, wide);
+    if (cfg->dtype == MT_F32)
+      e = mode == kWhole ? norm_fwd<float, kWhole>(p, s) : mode == kVectors ? norm_fwd<float, kVectors>(p, s) : norm_fwd<float, kAny>(p, s);
+    else
+      e = mode == kWhole     ? norm_fwd<__nv_bfloat16, kWhole>(p, s)
+          : mode == kVectors ? norm_fwd<__nv_bfloat16, kVectors>(p, s)
+                             : norm_fwd<__nv_bfloat16, kAny>(p, s);
   }
   return e == cudaSuccess ? MT_OK : MT_ECUDA;
 }
@@ -885,14 +925,19 @@ int mt_gated_norm_backward(const mt_gated_norm* cfg, const mt_rows* dz, const mt
   if (p.n > 0) {
     MT_LAUNCH("k_norm_bwd", s);
     cudaError_t e;
-    if (cfg->dtype == MT_F32) e = wide ? norm_bwd<float, true>(p, s) : norm_bwd<float, false>(p, s);
-    else e = wide ? norm_bwd<__nv_bfloat16, true>(p, s) : norm_bwd<__nv_bfloat16, false>(p, s);
+    const int mode = mode_of(p, wide);
+    if (cfg->dtype == MT_F32)
+      e = mode == kWhole ? norm_bwd<float, kWhole>(p, s) : mode == kVectors ? norm_bwd<float, kVectors>(p, s) : norm_bwd<float, kAny>(p, s);
+    else
+      e = mode == kWhole     ? norm_bwd<__nv_bfloat16, kWhole>(p, s)
+          : mode == kVectors ? norm_bwd<__nv_bfloat16, kVectors>(p, s)
+                             : norm_bwd<__nv_bfloat16, kAny>(p, s);
     if (e != cudaSuccess) return MT_ECUDA;
   }
   {
     MT_LAUNCH("k_norm_sums", s);
     const dim3 grid((p.d + 31) / 32, 2, p.groups);
-    k_norm_sums<<<grid, 256, (size_t)(p.groups + 1) * 8, s>>>(p);
+    k_norm_sums<<<grid, 32 * kSlices, (size_t)(p.groups + 1) * 8, s>>>(p);
   }
   return cudaGetLastError() == cudaSuccess ? MT_OK : MT_ECUDA;
 }

@@ -27,9 +27,9 @@ __global__ void __launch_bounds__(256) k_pack8(const PackParams p) {
     const bool live = it < total;
     const long long row = live ? it / p.vecs : 0;
     const int vec = live ? (int)(it - row * p.vecs) : 0;
-    float f[8] = {};
-    if (live) widen8<T>(load8<T, AL>(p.r, row, vec, p.d), false, f);
-    store_packed8<AL>(p.q, row, vec, p.d, f, live);
+    Raw8<T> v{};
+    if (live) v = load8<T, AL>(p.r, row, vec, p.d);
+    put_packed8<T, AL>(p.q, row, vec, p.d, v, live);
   }
 }
 
@@ -40,9 +40,9 @@ __global__ void __launch_bounds__(256) k_unpack8(const PackParams p) {
        it += (long long)gridDim.x * blockDim.x) {
     const long long row = it / p.vecs;
     const int vec = (int)(it - row * p.vecs);
-    float f[8];
+    f32x2 f[4];
     widen8<T>(load8<T, AL>(p.q, row, vec, p.d), true, f);
-    store8<T, AL>(p.r.data, p.r.ld, row, vec, p.d, f);
+    put8<T, AL>(p.r, row, vec, p.d, narrow8<T>(f));
   }
 }
 
