@@ -19,7 +19,7 @@
 //                atomics, so the sums have one order).  With S1 = sum D a yh and
 //                S2 = sum D a, dwp = s S1, dbp = s S2 and ds = wp S1 + bp S2: two
 //                sums for three gradients, and one when there is no bp.
-//  k_norm_sums   the blocks' partial sums of each group, in fp64.
+//  k_norm_sums   the blocks' partial sums of each group.
 #include <algorithm>
 
 #include "mt_block.cuh"
@@ -51,15 +51,16 @@ __device__ __forceinline__ long long run_start(long long off0, long long m, int 
 // The block whose run holds the row off0 + r (0 <= r < m).
 __device__ __forceinline__ int run_of(long long r, long long m, int B) { return (int)(((r + 1) * B - 1) / m); }
 
-// Sums a and b over a team: shuffles inside a warp, shared memory across a team's warps.  A team of more than one
+// Sums a (and b, where TWO) over a team: shuffles inside a warp, shared memory across a team's warps.  A team of more than one
 // warp owns a named barrier (a block has at most two such teams; the barriers' numbers are constants, as a number from
 // a register would reserve all sixteen and leave an SM four blocks); `slot` alternates so that one barrier per call is
 // enough.
-__device__ __forceinline__ void team_sum2(float& a, float& b, int team_lanes, float2* s_red, int& slot) {
+template <bool TWO>
+__device__ __forceinline__ void team_sum(float& a, float& b, int team_lanes, float2* s_red, int& slot) {
   const int in_warp = team_lanes < 32 ? team_lanes : 32;
   for (int o = in_warp >> 1; o > 0; o >>= 1) {
     a += __shfl_xor_sync(kFull, a, o);
-    b += __shfl_xor_sync(kFull, b, o);
+    if (TWO) b += __shfl_xor_sync(kFull, b, o);
   }
   if (team_lanes <= 32) return;
   const int warp = threadIdx.x >> 5, warps = team_lanes >> 5, first = warp / warps * warps;
@@ -71,7 +72,7 @@ __device__ __forceinline__ void team_sum2(float& a, float& b, int team_lanes, fl
   for (int k = 0; k < warps; ++k) {
     const float2 v = buf[first + k];
     a += v.x;
-    b += v.y;
+    if (TWO) b += v.y;
   }
   slot ^= 1;
 }
@@ -79,6 +80,10 @@ __device__ __forceinline__ void team_sum2(float& a, float& b, int team_lanes, fl
 // How the rows lie: any strides and widths; 16-byte vectors; 16-byte vectors that fill their team exactly (no lane
 // holds columns past d, so nothing is masked).
 constexpr int kAny = 0, kVectors = 1, kWhole = 2;
+
+// Which parts there are: asked at run time; all of them (y, a gate, a scale, the next norm, dz; every parameter on 16
+// bytes), saved rows plain; the same with saved rows in 8 bits.  The last two leave out the checks.
+constexpr int kParts = 0, kAllPlain = 1, kAllPacked = 2;
 
 // Zeros where a vector's columns lie past d.
 template <int MODE>
@@ -96,15 +101,17 @@ __device__ __forceinline__ void mask8(f32x2 (&v)[4], int left) {
 }
 
 // Eight parameters of a group's row, `none` for an absent parameter and for a vector past d; zeros past d inside one.
+// SURE: it is there, on 16 bytes, and the vector lies below d.
+template <bool SURE>
 __device__ __forceinline__ void param8(const float* p, int g, int vec, int d, int wide, float none, f32x2 (&f)[4]) {
   const int c0 = vec * 8;
-  if (p == nullptr || c0 >= d) {
+  if (!SURE && (p == nullptr || c0 >= d)) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) f[j] = both(none);
     return;
   }
   p += (uint32_t)(g * d + c0);  // groups * d <= 2^23
-  if (wide) {
+  if (SURE || wide) {
     const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2*>(p)), b = __ldg(reinterpret_cast<const ulonglong2*>(p) + 1);
     f[0] = a.x;
     f[1] = a.y;
@@ -160,46 +167,47 @@ __device__ __forceinline__ float pair_sum(f32x2 a) {
   return f.x + f.y;
 }
 
-// A row v normalised is v * r + c: r its inverse deviation, c = -mean * r (0 for rms).  Both rows v and w at once (one
-// of them may be absent: zeros).  Columns past d hold zeros and stay out of the deviation.
+// A row v normalised is v * r + c: r its inverse deviation, c = -mean * r (0 for rms).  TWO rows v and w at once, or v
+// alone.  Columns past d hold zeros and stay out of the deviation.
 struct Stats {
   float r, c;
 };
-template <int MODE>
-__device__ __forceinline__ void row_stats2(const f32x2 (&v)[kNV][4], const f32x2 (&w)[kNV][4], const NormParams& p,
-                                           int team, int lt, float2* s_red, int& slot, Stats& sv, Stats& sw) {
+template <int MODE, bool TWO>
+__device__ __forceinline__ void row_stats(const f32x2 (&v)[kNV][4], const f32x2 (&w)[kNV][4], const NormParams& p, int team,
+                                          int lt, float2* s_red, int& slot, Stats& sv, Stats& sw) {
   f32x2 a = 0ull, b = 0ull;
   const float inv_d = 1.0f / (float)p.d;
-  float x, y, mv = 0.0f, mw = 0.0f;
+  float x, y = 0.0f, mv = 0.0f, mw = 0.0f;
   if (p.kind == MT_NORM_LAYER) {
 #pragma unroll
     for (int k = 0; k < kNV; ++k)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         a = add2(a, v[k][j]);
-        b = add2(b, w[k][j]);
+        if (TWO) b = add2(b, w[k][j]);
       }
     x = pair_sum(a);
-    y = pair_sum(b);
-    team_sum2(x, y, team, s_red, slot);
+    if (TWO) y = pair_sum(b);
+    team_sum<TWO>(x, y, team, s_red, slot);
     mv = x * inv_d;
     mw = y * inv_d;
     a = b = 0ull;
     const f32x2 nv = both(-mv), nw = both(-mw);
 #pragma unroll
     for (int k = 0; k < kNV; ++k) {
-      f32x2 cv[4], cw[4];
+      const int left = p.d - (k * team + lt) * 8;
+      f32x2 c[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        cv[j] = add2(v[k][j], nv);
-        cw[j] = add2(w[k][j], nw);
-      }
-      mask8<MODE>(cv, p.d - (k * team + lt) * 8);
-      mask8<MODE>(cw, p.d - (k * team + lt) * 8);
+      for (int j = 0; j < 4; ++j) c[j] = add2(v[k][j], nv);
+      mask8<MODE>(c, left);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        a = fma2(cv[j], cv[j], a);
-        b = fma2(cw[j], cw[j], b);
+      for (int j = 0; j < 4; ++j) a = fma2(c[j], c[j], a);
+      if (TWO) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[j] = add2(w[k][j], nw);
+        mask8<MODE>(c, left);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b = fma2(c[j], c[j], b);
       }
     }
   } else {
@@ -208,24 +216,18 @@ __device__ __forceinline__ void row_stats2(const f32x2 (&v)[kNV][4], const f32x2
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         a = fma2(v[k][j], v[k][j], a);
-        b = fma2(w[k][j], w[k][j], b);
+        if (TWO) b = fma2(w[k][j], w[k][j], b);
       }
   }
   x = pair_sum(a);
-  y = pair_sum(b);
-  team_sum2(x, y, team, s_red, slot);
+  if (TWO) y = pair_sum(b);
+  team_sum<TWO>(x, y, team, s_red, slot);
   sv.r = rsqrtf(x * inv_d + p.eps);
-  sw.r = rsqrtf(y * inv_d + p.eps);
   sv.c = -mv * sv.r;
-  sw.c = -mw * sw.r;
-}
-template <int MODE>
-__device__ __forceinline__ Stats row_stats(const f32x2 (&v)[kNV][4], const NormParams& p, int team, int lt, float2* s_red,
-                                           int& slot) {
-  Stats a, b;
-  const f32x2 none[kNV][4] = {};
-  row_stats2<MODE>(v, none, p, team, lt, s_red, slot, a, b);
-  return a;
+  if (TWO) {
+    sw.r = rsqrtf(y * inv_d + p.eps);
+    sw.c = -mw * sw.r;
+  }
 }
 
 // ---- rows on their way -------------------------------------------------------------
@@ -266,16 +268,17 @@ struct Stages {
 
 // Starts the copy of eight columns (zeros where they lie past d or the row is not there); e: a packed block's exponent
 // byte, which comes by an ordinary load.
-template <typename T>
-__device__ __forceinline__ void fetch8(uint32_t dst, const Rows& r, long long row, int vec, int d, bool packed, uint32_t& e) {
+template <typename T, bool SURE>
+__device__ __forceinline__ void fetch8(uint32_t dst, const Rows& r, int row, int vec, int d, bool live, bool packed,
+                                       uint32_t& e) {
   const int c0 = vec * 8;
-  const bool on = c0 < d;
+  const bool on = live && (SURE || c0 < d);
   if (packed) {
     const int nb = (d + kPackBlock - 1) / kPackBlock;
-    copy8(dst, r.codes + (on ? row_offset(row, d) + c0 : 0), on);
+    copy8(dst, r.codes + row_offset(row, d) + (SURE || on ? c0 : 0), on);
     e = on ? (uint32_t)__ldg(r.exps + row_offset(row, nb) + c0 / kPackBlock) : 127u;
   } else {
-    const T* p = static_cast<const T*>(r.data) + (on ? row_offset(row, r.ld) + c0 : 0);
+    const T* p = static_cast<const T*>(r.data) + row_offset(row, r.ld) + (SURE || on ? c0 : 0);
     copy16(dst, p, on);
     if constexpr (sizeof(T) == 4) copy16(dst + 16, p + 4, on);
   }
@@ -290,11 +293,12 @@ __device__ __forceinline__ Raw8<T> staged8(uint32_t at, uint32_t e) {
   return v;
 }
 
-// Blocks of 128 threads that share an SM's registers (wider rows: one block of 512).
-constexpr int kFwdBlocks = 6, kBwdBlocks = 3;
+// Blocks of 128 threads that share an SM's registers and stages (wider rows: one block of 512).
+constexpr int fwd_blocks_per_sm(int elem) { return elem == 4 ? 4 : 6; }
+constexpr int bwd_blocks_per_sm(int elem, bool bias) { return elem == 4 ? 2 : bias ? 3 : 4; }
 
-template <typename T, int MODE, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == 128 ? (sizeof(T) == 4 ? 4 : kFwdBlocks) : 1)
+template <typename T, int MODE, int THREADS, int FORM>
+__global__ void __launch_bounds__(THREADS, THREADS == 128 ? fwd_blocks_per_sm(sizeof(T)) : 1)
 k_norm_fwd(const NormParams p) {
   constexpr bool AL = MODE != kAny, STAGED = kStaged<T, MODE, THREADS>;
   using St = Stages<T, THREADS, 3>;
@@ -307,7 +311,8 @@ k_norm_fwd(const NormParams p) {
   const int lt = threadIdx.x & (team - 1);
   const int sub = threadIdx.x >> p.log_team;
   const int teams = THREADS >> p.log_team;  // teams per block
-  const bool has_y = p.y.data != nullptr, has_u = p.u.data != nullptr, has_h = p.wq != nullptr;
+  constexpr bool ALL = FORM != kParts, SURE = ALL && MODE == kWhole;
+  const bool has_y = ALL || p.y.data != nullptr, has_u = ALL || p.u.data != nullptr, has_h = ALL || p.wq != nullptr;
   const long long off0 = s_off[0], m = s_off[p.groups] - off0;
   int slot = 0;
 
@@ -335,14 +340,14 @@ k_norm_fwd(const NormParams p) {
     // a row's vectors start on their way, or are loaded where they are used
     auto fetch = [&](int base, int s) {
       const bool live = base + sub < last;
-      const int row = live ? base + sub : base, dd = live ? p.d : 0;
+      const int row = live ? base + sub : base;
       uint32_t none;
 #pragma unroll
       for (int k = 0; k < kNV; ++k) {
         const int vec = k * team + lt;
-        if (has_y) fetch8<T>(st.at(s, 0, k), p.y, row, vec, dd, false, none);
-        if (has_u) fetch8<T>(st.at(s, 1, k), p.u, row, vec, dd, false, none);
-        fetch8<T>(st.at(s, 2, k), p.x, row, vec, dd, false, none);
+        if (has_y) fetch8<T, SURE>(st.at(s, 0, k), p.y, row, vec, p.d, live, false, none);
+        if (has_u) fetch8<T, SURE>(st.at(s, 1, k), p.u, row, vec, p.d, live, false, none);
+        fetch8<T, SURE>(st.at(s, 2, k), p.x, row, vec, p.d, live, false, none);
       }
     };
     int cur = 0;
@@ -372,23 +377,24 @@ k_norm_fwd(const NormParams p) {
           widen8<T>(raw, false, y[k]);
           if (p.y.codes != nullptr) put_packed8<T, AL>(p.y, row, k * team + lt, p.d, raw, live);
         }
-        const Stats sy = row_stats<MODE>(y, p, team, lt, s_red, slot);
+        Stats sy;
+        row_stats<MODE, false>(y, y, p, team, lt, s_red, slot, sy, sy);
         const f32x2 r2 = both(sy.r), c2 = both(sy.c);
 #pragma unroll
         for (int k = 0; k < kNV; ++k) {
           const int vec = k * team + lt;
           f32x2 f[4];
-          param8(p.wp, g, vec, p.d, p.wide, 1.0f, f);
+          param8<SURE>(p.wp, g, vec, p.d, p.wide, 1.0f, f);
 #pragma unroll
           for (int j = 0; j < 4; ++j) y[k][j] = mul2(f[j], fma2(y[k][j], r2, c2));
           if (MODE != kWhole) mask8<MODE>(y[k], p.d - vec * 8);
           if (p.bp != nullptr) {
-            param8(p.bp, g, vec, p.d, p.wide, 0.0f, f);
+            param8<false>(p.bp, g, vec, p.d, p.wide, 0.0f, f);
 #pragma unroll
             for (int j = 0; j < 4; ++j) y[k][j] = add2(y[k][j], f[j]);
           }
-          if (p.sc != nullptr) {
-            param8(p.sc, g, vec, p.d, p.wide, 1.0f, f);
+          if (ALL || p.sc != nullptr) {
+            param8<SURE>(p.sc, g, vec, p.d, p.wide, 1.0f, f);
 #pragma unroll
             for (int j = 0; j < 4; ++j) y[k][j] = mul2(y[k][j], f[j]);
           }
@@ -410,27 +416,28 @@ k_norm_fwd(const NormParams p) {
 #pragma unroll
         for (int k = 0; k < kNV; ++k) widen8<T>(get(2, p.x, k), false, z[k]);
       }
-      if (p.z.data != nullptr || p.z.codes != nullptr) {
+      if (ALL || p.z.data != nullptr || p.z.codes != nullptr) {
 #pragma unroll
         for (int k = 0; k < kNV; ++k) {
           const Raw8<T> raw = narrow8<T>(z[k]);
-          if (p.z.data != nullptr && live) put8<T, AL>(p.z, row, k * team + lt, p.d, raw);
+          if ((ALL || p.z.data != nullptr) && live) put8<T, AL>(p.z, row, k * team + lt, p.d, raw);
           if (p.z.codes != nullptr) put_packed8<T, AL>(p.z, row, k * team + lt, p.d, raw, live);
         }
       }
       if (has_h) {
-        const Stats sz = row_stats<MODE>(z, p, team, lt, s_red, slot);
+        Stats sz;
+        row_stats<MODE, false>(z, z, p, team, lt, s_red, slot, sz, sz);
         const f32x2 r2 = both(sz.r), c2 = both(sz.c);
 #pragma unroll
         for (int k = 0; k < kNV; ++k) {
           const int vec = k * team + lt;
           f32x2 f[4];
-          param8(p.wq, g, vec, p.d, p.wide, 1.0f, f);
+          param8<SURE>(p.wq, g, vec, p.d, p.wide, 1.0f, f);
 #pragma unroll
           for (int j = 0; j < 4; ++j) z[k][j] = mul2(f[j], fma2(z[k][j], r2, c2));
           if (MODE != kWhole) mask8<MODE>(z[k], p.d - vec * 8);
           if (p.bq != nullptr) {
-            param8(p.bq, g, vec, p.d, p.wide, 0.0f, f);
+            param8<false>(p.bq, g, vec, p.d, p.wide, 0.0f, f);
 #pragma unroll
             for (int j = 0; j < 4; ++j) z[k][j] = add2(z[k][j], f[j]);
           }
@@ -461,7 +468,8 @@ __device__ __forceinline__ void norm_grad(f32x2 (&dvh)[kNV][4], const f32x2 (&vh
       for (int j = 0; j < 4; ++j) b = add2(b, dvh[k][j]);
   }
   float x = pair_sum(a), y = pair_sum(b);
-  team_sum2(x, y, team, s_red, slot);
+  if (layer) team_sum<true>(x, y, team, s_red, slot);
+  else team_sum<false>(x, y, team, s_red, slot);
   const float inv_d = 1.0f / (float)p.d;
   const f32x2 r2 = both(r), ma = both(-r * x * inv_d), mb = both(-r * y * inv_d);
 #pragma unroll
@@ -473,8 +481,8 @@ __device__ __forceinline__ void norm_grad(f32x2 (&dvh)[kNV][4], const f32x2 (&vh
 }
 
 // BIAS: the norms have biases (their sums S2 and T2 are kept too).
-template <typename T, int MODE, int THREADS, bool BIAS>
-__global__ void __launch_bounds__(THREADS, THREADS == 128 ? (sizeof(T) == 4 ? 2 : kBwdBlocks) : 1)
+template <typename T, int MODE, int THREADS, bool BIAS, int FORM>
+__global__ void __launch_bounds__(THREADS, THREADS == 128 ? bwd_blocks_per_sm(sizeof(T), BIAS) : 1)
 k_norm_bwd(const NormParams p) {
   constexpr bool AL = MODE != kAny, STAGED = kStaged<T, MODE, THREADS>;
   constexpr int kAcc = BIAS ? 4 : 2;       // S1, T1, S2, T2
@@ -490,9 +498,11 @@ k_norm_bwd(const NormParams p) {
   const int lt = threadIdx.x & (team - 1);
   const int sub = threadIdx.x >> p.log_team;
   const int teams = THREADS >> p.log_team;
-  const bool has_y = p.y.data != nullptr || p.y.codes != nullptr, has_u = p.u.data != nullptr || p.u.codes != nullptr;
-  const bool has_h = p.wq != nullptr, has_dz = p.dz.data != nullptr;
-  const bool y8 = p.y.data == nullptr, u8 = p.u.data == nullptr, z8 = p.z.data == nullptr;
+  constexpr bool ALL = FORM != kParts, SURE = ALL && MODE == kWhole, P8 = FORM == kAllPacked;
+  const bool has_y = ALL || p.y.data != nullptr || p.y.codes != nullptr;
+  const bool has_u = ALL || p.u.data != nullptr || p.u.codes != nullptr;
+  const bool has_h = ALL || p.wq != nullptr, has_dz = ALL || p.dz.data != nullptr;
+  const bool y8 = ALL ? P8 : p.y.data == nullptr, u8 = ALL ? P8 : p.u.data == nullptr, z8 = ALL ? P8 : p.z.data == nullptr;
   const long long off0 = s_off[0], m = s_off[p.groups] - off0;
   int slot = 0;
 
@@ -522,16 +532,16 @@ k_norm_bwd(const NormParams p) {
       for (int k = 0; k < kNV; ++k) next_e[i][k] = kNoExp;
     auto fetch = [&](int base, int s) {
       const bool live = base + sub < last;
-      const int row = live ? base + sub : base, dd = live ? p.d : 0;
+      const int row = live ? base + sub : base;
 #pragma unroll
       for (int k = 0; k < kNV; ++k) {
         const int vec = k * team + lt;
         uint32_t none;
-        if (has_h) fetch8<T>(st.at(s, 0, k), p.z, row, vec, dd, z8, next_e[0][k]);
-        if (has_y) fetch8<T>(st.at(s, 1, k), p.y, row, vec, dd, y8, next_e[1][k]);
-        if (has_h) fetch8<T>(st.at(s, 2, k), p.dh, row, vec, dd, false, none);
-        if (has_dz) fetch8<T>(st.at(s, 3, k), p.dz, row, vec, dd, false, none);
-        if (has_u) fetch8<T>(st.at(s, 4, k), p.u, row, vec, dd, u8, next_e[2][k]);
+        if (has_h) fetch8<T, SURE>(st.at(s, 0, k), p.z, row, vec, p.d, live, z8, next_e[0][k]);
+        if (has_y) fetch8<T, SURE>(st.at(s, 1, k), p.y, row, vec, p.d, live, y8, next_e[1][k]);
+        if (has_h) fetch8<T, SURE>(st.at(s, 2, k), p.dh, row, vec, p.d, live, false, none);
+        if (has_dz) fetch8<T, SURE>(st.at(s, 3, k), p.dz, row, vec, p.d, live, false, none);
+        if (has_u) fetch8<T, SURE>(st.at(s, 4, k), p.u, row, vec, p.d, live, u8, next_e[2][k]);
       }
     };
     int cur = 0;
@@ -566,7 +576,7 @@ k_norm_bwd(const NormParams p) {
           if (has_h) widen8<T>(get(0, p.z, k, e[0][k]), z8, zh[k]);
           if (has_y) widen8<T>(get(1, p.y, k, e[1][k]), y8, yh[k]);
         }
-        row_stats2<MODE>(yh, zh, p, team, lt, s_red, slot, sy, sz);
+        row_stats<MODE, true>(yh, zh, p, team, lt, s_red, slot, sy, sz);
         if (has_h) {  // through the next block's norm
           const f32x2 r2 = both(sz.r), c2 = both(sz.c);
 #pragma unroll
@@ -574,7 +584,7 @@ k_norm_bwd(const NormParams p) {
             const int vec = k * team + lt;
             f32x2 dh[4], w[4];
             widen8<T>(get(2, p.dh, k, kNoExp), false, dh);
-            param8(p.wq, g, vec, p.d, p.wide, 1.0f, w);
+            param8<SURE>(p.wq, g, vec, p.d, p.wide, 1.0f, w);
 #pragma unroll
             for (int j = 0; j < 4; ++j) zh[k][j] = fma2(zh[k][j], r2, c2);
             mask8<MODE>(zh[k], p.d - vec * 8);
@@ -607,8 +617,8 @@ k_norm_bwd(const NormParams p) {
         for (int k = 0; k < kNV; ++k) {
           const int vec = k * team + lt;
           f32x2 w[4], s[4];
-          param8(p.wp, g, vec, p.d, p.wide, 1.0f, w);
-          param8(p.sc, g, vec, p.d, p.wide, 1.0f, s);
+          param8<SURE>(p.wp, g, vec, p.d, p.wide, 1.0f, w);
+          param8<SURE>(p.sc, g, vec, p.d, p.wide, 1.0f, s);
 #pragma unroll
           for (int j = 0; j < 4; ++j) yh[k][j] = fma2(yh[k][j], r2, c2);
           mask8<MODE>(yh[k], p.d - vec * 8);
@@ -624,7 +634,7 @@ k_norm_bwd(const NormParams p) {
             }
             if constexpr (BIAS) {
               if (p.bp != nullptr) {
-                param8(p.bp, g, vec, p.d, p.wide, 0.0f, a);
+                param8<false>(p.bp, g, vec, p.d, p.wide, 0.0f, a);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) u[j] = add2(u[j], a[j]);
               }
@@ -676,12 +686,12 @@ k_norm_bwd(const NormParams p) {
   }
 }
 
-// The parameter gradients of each group from its runs' partial sums: 32 columns by 32 slices of runs per block, in
-// fp64, the slices joined in their order.
-constexpr int kSlices = 32;
+// The parameter gradients of each group from its runs' partial sums (a few hundred, each already a sum of many rows):
+// 32 columns by 16 slices of runs per block, the slices joined in their order.
+constexpr int kSlices = 16;
 __global__ void __launch_bounds__(32 * kSlices) k_norm_sums(const NormParams p) {
   extern __shared__ long long s_off[];
-  __shared__ double s_part[2][kSlices][33];
+  __shared__ float2 s_part[kSlices][33];
   load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;
@@ -690,34 +700,34 @@ __global__ void __launch_bounds__(32 * kSlices) k_norm_sums(const NormParams p) 
   const bool second = post ? p.bp != nullptr : p.bq != nullptr;
   const long long off0 = s_off[0], m = s_off[p.groups] - off0;
   for (int g = blockIdx.z; g < p.groups; g += gridDim.z) {
-    double a = 0.0, b = 0.0;
+    float a = 0.0f, b = 0.0f;
     if (col < p.d && s_off[g] < s_off[g + 1]) {
       const int b0 = run_of(s_off[g] - off0, m, p.blocks), b1 = run_of(s_off[g + 1] - 1 - off0, m, p.blocks);
       const float* base = p.part + (size_t)(post ? 0 : 2) * p.d + col;
-#pragma unroll 4
+#pragma unroll 8
       for (int k = b0 + slice; k <= b1; k += kSlices) {
         const float* at = base + (size_t)(k + g) * kSums * p.d;
-        a += (double)__ldg(at);
-        if (second) b += (double)__ldg(at + p.d);
+        a += __ldg(at);
+        if (second) b += __ldg(at + p.d);
       }
     }
-    s_part[0][slice][lane] = a;
-    s_part[1][slice][lane] = b;
+    s_part[slice][lane] = make_float2(a, b);
     __syncthreads();
     if (slice == 0 && col < p.d) {
       for (int k = 1; k < kSlices; ++k) {
-        a += s_part[0][k][lane];
-        b += s_part[1][k][lane];
+        const float2 v = s_part[k][lane];
+        a += v.x;
+        b += v.y;
       }
       const size_t at = (size_t)g * p.d + col;
       if (post) {
-        const double s = p.sc != nullptr ? (double)p.sc[at] : 1.0;
-        p.dwp[at] = (float)(s * a);
-        if (p.dbp != nullptr) p.dbp[at] = (float)(s * b);
-        if (p.dsc != nullptr) p.dsc[at] = (float)((double)p.wp[at] * a + (p.bp != nullptr ? (double)p.bp[at] * b : 0.0));
+        const float s = p.sc != nullptr ? p.sc[at] : 1.0f;
+        p.dwp[at] = s * a;
+        if (p.dbp != nullptr) p.dbp[at] = s * b;
+        if (p.dsc != nullptr) p.dsc[at] = p.wp[at] * a + (p.bp != nullptr ? p.bp[at] * b : 0.0f);
       } else {
-        p.dwq[at] = (float)a;
-        if (p.dbq != nullptr) p.dbq[at] = (float)b;
+        p.dwq[at] = a;
+        if (p.dbq != nullptr) p.dbq[at] = b;
       }
     }
     __syncthreads();
@@ -734,9 +744,9 @@ int log_team_of(int d) {  // 16 columns per lane; at least the four lanes of an 
 int threads_of(int log_team) { return log_team > 7 ? 512 : 128; }
 
 // Blocks of a backward over n rows: what the SMs hold at once, and at least two rows per team.
-int bwd_blocks(long long n, int d) {
+int bwd_blocks(long long n, int d, int elem, bool bias) {
   const int lt = log_team_of(d), threads = threads_of(lt), teams = threads >> lt;
-  const long long most = (long long)sm_count() * (threads == 128 ? kBwdBlocks : 1);
+  const long long most = (long long)sm_count() * (threads == 128 ? bwd_blocks_per_sm(elem, bias) : 1);
   return (int)std::max<long long>(1, std::min<long long>(most, (n + 2 * teams - 1) / (2 * teams)));
 }
 
@@ -772,46 +782,61 @@ int norm_params(const mt_gated_norm* c, NormParams& p) {
   return MT_OK;
 }
 
+bool absent(const Rows& r) { return r.data == nullptr && r.codes == nullptr && r.exps == nullptr; }
+
 template <typename K>
 cudaError_t allow_smem(K kernel, size_t bytes) {
   return cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-template <typename T, int MODE, int THREADS>
+template <typename T, int MODE, int THREADS, int FORM>
 cudaError_t norm_fwd_as(const NormParams& p, cudaStream_t s) {
   const int teams = THREADS >> p.log_team;
-  const int grid = grid_for((p.n + teams - 1) / teams * THREADS, THREADS, THREADS == 128 ? kFwdBlocks : 1);
+  const int grid = grid_for((p.n + teams - 1) / teams * THREADS, THREADS, THREADS == 128 ? fwd_blocks_per_sm(sizeof(T)) : 1);
   const size_t smem = (kStaged<T, MODE, THREADS> ? Stages<T, THREADS, 3>::kBytes : 0) + (size_t)(p.groups + 1) * 8;
-  const cudaError_t e = allow_smem(k_norm_fwd<T, MODE, THREADS>, smem);
+  const cudaError_t e = allow_smem(k_norm_fwd<T, MODE, THREADS, FORM>, smem);
   if (e != cudaSuccess) return e;
-  k_norm_fwd<T, MODE, THREADS><<<grid, THREADS, smem, s>>>(p);
+  k_norm_fwd<T, MODE, THREADS, FORM><<<grid, THREADS, smem, s>>>(p);
   return cudaGetLastError();
 }
-template <typename T, int MODE, int THREADS, bool BIAS>
+template <typename T, int MODE, int THREADS, bool BIAS, int FORM>
 cudaError_t norm_bwd_as(const NormParams& p, cudaStream_t s) {
   const size_t smem =
       (kStaged<T, MODE, THREADS> ? Stages<T, THREADS, 5>::kBytes : 16 * THREADS * 4) + (size_t)(p.groups + 1) * 8;
-  const cudaError_t e = allow_smem(k_norm_bwd<T, MODE, THREADS, BIAS>, smem);
+  const cudaError_t e = allow_smem(k_norm_bwd<T, MODE, THREADS, BIAS, FORM>, smem);
   if (e != cudaSuccess) return e;
-  k_norm_bwd<T, MODE, THREADS, BIAS><<<p.blocks, THREADS, smem, s>>>(p);
+  k_norm_bwd<T, MODE, THREADS, BIAS, FORM><<<p.blocks, THREADS, smem, s>>>(p);
   return cudaGetLastError();
 }
 template <typename T, int MODE>
 cudaError_t norm_fwd(const NormParams& p, cudaStream_t s) {
-  return p.log_team > 7 ? norm_fwd_as<T, MODE, 512>(p, s) : norm_fwd_as<T, MODE, 128>(p, s);
+  if (p.log_team > 7) return norm_fwd_as<T, MODE, 512, kParts>(p, s);
+  if constexpr (MODE == kWhole) {
+    if (p.y.data != nullptr && p.u.data != nullptr && p.wq != nullptr && p.sc != nullptr && p.wide)
+      return norm_fwd_as<T, MODE, 128, kAllPlain>(p, s);
+  }
+  return norm_fwd_as<T, MODE, 128, kParts>(p, s);
+}
+template <typename T, int MODE, bool BIAS>
+cudaError_t norm_bwd(const NormParams& p, cudaStream_t s) {
+  if (p.log_team > 7) return norm_bwd_as<T, MODE, 512, BIAS, kParts>(p, s);
+  if constexpr (MODE == kWhole) {
+    if (!absent(p.y) && !absent(p.u) && p.wq != nullptr && p.sc != nullptr && p.dz.data != nullptr && p.wide) {
+      if (p.y.data != nullptr && p.u.data != nullptr && p.z.data != nullptr) return norm_bwd_as<T, MODE, 128, BIAS, kAllPlain>(p, s);
+      if (p.y.data == nullptr && p.u.data == nullptr && p.z.data == nullptr) return norm_bwd_as<T, MODE, 128, BIAS, kAllPacked>(p, s);
+    }
+  }
+  return norm_bwd_as<T, MODE, 128, BIAS, kParts>(p, s);
 }
 template <typename T, int MODE>
 cudaError_t norm_bwd(const NormParams& p, cudaStream_t s) {
-  const bool bias = p.bp != nullptr || p.bq != nullptr;
-  if (p.log_team > 7) return bias ? norm_bwd_as<T, MODE, 512, true>(p, s) : norm_bwd_as<T, MODE, 512, false>(p, s);
-  return bias ? norm_bwd_as<T, MODE, 128, true>(p, s) : norm_bwd_as<T, MODE, 128, false>(p, s);
+  return p.bp != nullptr || p.bq != nullptr ? norm_bwd<T, MODE, true>(p, s) : norm_bwd<T, MODE, false>(p, s);
 }
 
 int mode_of(const NormParams& p, bool wide) { return !wide ? kAny : (16 << p.log_team) == p.d ? kWhole : kVectors; }
 
 bool packed_rows(const Rows& r) { return r.codes != nullptr && r.exps != nullptr; }
 bool half_packed(const Rows& r) { return (r.codes == nullptr) != (r.exps == nullptr); }
-bool absent(const Rows& r) { return r.data == nullptr && r.codes == nullptr && r.exps == nullptr; }
 Rows rows_of(const mt_rows* r) { return r != nullptr ? *r : Rows{nullptr, 0, nullptr, nullptr}; }
 
 }  // namespace
@@ -861,7 +886,7 @@ int mt_gated_norm_forward(const mt_gated_norm* cfg, const mt_rows* x, const mt_r
 size_t mt_gated_norm_workspace_bytes(int64_t n, int32_t dim, int32_t groups) {
   using namespace mt;
   if (n < 0 || n > 0x7FFFFFFF || dim < 1 || dim > MT_MAX_BLOCK_DIM || groups < 1 || groups > MT_MAX_GROUPS) return 0;
-  return align_up(((size_t)bwd_blocks(n, dim) + groups) * kSums * dim * 4, 256);
+  return align_up(((size_t)bwd_blocks(n, dim, 2, false) + groups) * kSums * dim * 4, 256);
 }
 
 int mt_gated_norm_backward(const mt_gated_norm* cfg, const mt_rows* dz, const mt_rows* dh, const mt_rows* y,
@@ -917,7 +942,7 @@ int mt_gated_norm_backward(const mt_gated_norm* cfg, const mt_rows* dz, const mt
   if (ws == nullptr || !is_aligned(ws, 256) || ws_bytes < mt_gated_norm_workspace_bytes(p.n, p.d, p.groups))
     return MT_ENOSPACE;
   p.part = static_cast<float*>(ws);
-  p.blocks = bwd_blocks(p.n, p.d);
+  p.blocks = bwd_blocks(p.n, p.d, (int)elem_bytes(cfg->dtype), p.bp != nullptr || p.bq != nullptr);
   bool wide = true;
   for (const Rows* r : {&p.dz, &p.dh, &p.y, &p.u, &p.z, &p.dx, &p.dy, &p.du})
     wide = wide && rows_wide(*r, p.d, cfg->dtype);
