@@ -13,36 +13,66 @@ namespace {
 struct PackParams {
   Rows r;          // plain rows (data, ld)
   Rows q;          // codes, exps
-  long long n;
-  int d, vecs;     // vecs: vectors of eight columns per row, rounded up to whole blocks of four
+  long long n, total;  // total: vectors of all rows
+  int d, vecs;     // vecs: vectors of eight columns per row (packing: rounded up to whole blocks of four)
 };
 
-template <typename T, bool AL>
+constexpr int kUnroll = 4;  // vectors a lane has in flight
+
+// Vectors of a launch: lane `lane` of a warp takes the vectors it0 + 32 u + lane, u < kUnroll, so a warp covers 1024
+// neighbouring columns.  Where the rows follow one another without gaps and are whole blocks (FLAT), finding a vector
+// takes no division: everything is cut into rows of 2^20 vectors.
+struct Item {
+  long long row;
+  int vec;
+};
+template <bool FLAT>
+__device__ __forceinline__ Item item_of(const PackParams& p, long long it) {
+  if (FLAT) return Item{it >> 20, (int)(it & ((1 << 20) - 1))};
+  const long long row = p.total >> 32 ? it / p.vecs : (long long)((uint32_t)it / (uint32_t)p.vecs);
+  return Item{row, (int)(it - row * p.vecs)};
+}
+
+template <typename T, bool AL, bool FLAT>
 __global__ void __launch_bounds__(256) k_pack8(const PackParams p) {
-  const long long total = p.n * p.vecs;  // a multiple of four: a block's four lanes stay together
-  const long long step = (long long)gridDim.x * blockDim.x;
-  const long long rounds = (total + step - 1) / step;
-  long long it = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  for (long long k = 0; k < rounds; ++k, it += step) {
-    const bool live = it < total;
-    const long long row = live ? it / p.vecs : 0;
-    const int vec = live ? (int)(it - row * p.vecs) : 0;
-    Raw8<T> v{};
-    if (live) v = load8<T, AL>(p.r, row, vec, p.d);
-    put_packed8<T, AL>(p.q, row, vec, p.d, v, live);
+  const long long total = p.total;  // a multiple of four: a block's four lanes stay together
+  const int lane = threadIdx.x & 31;
+  const long long warp = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5, warps = ((long long)gridDim.x * blockDim.x) >> 5;
+  for (long long it0 = warp * 32 * kUnroll; it0 < total; it0 += warps * 32 * kUnroll) {
+    Raw8<T> v[kUnroll];
+    Item x[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const long long it = it0 + u * 32 + lane;
+      x[u] = item_of<FLAT>(p, it < total ? it : 0);
+      v[u] = it < total ? load8<T, AL>(p.r, x[u].row, x[u].vec, p.d) : Raw8<T>{};
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      put_packed8<T, AL>(p.q, x[u].row, x[u].vec, p.d, v[u], it0 + u * 32 + lane < total);
   }
 }
 
-template <typename T, bool AL>
+template <typename T, bool AL, bool FLAT>
 __global__ void __launch_bounds__(256) k_unpack8(const PackParams p) {
-  const long long total = p.n * p.vecs;
-  for (long long it = (long long)blockIdx.x * blockDim.x + threadIdx.x; it < total;
-       it += (long long)gridDim.x * blockDim.x) {
-    const long long row = it / p.vecs;
-    const int vec = (int)(it - row * p.vecs);
-    f32x2 f[4];
-    widen8<T>(load8<T, AL>(p.q, row, vec, p.d), true, f);
-    put8<T, AL>(p.r, row, vec, p.d, narrow8<T>(f));
+  const long long total = p.total;
+  const int lane = threadIdx.x & 31;
+  const long long warp = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5, warps = ((long long)gridDim.x * blockDim.x) >> 5;
+  for (long long it0 = warp * 32 * kUnroll; it0 < total; it0 += warps * 32 * kUnroll) {
+    Raw8<T> v[kUnroll];
+    Item x[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const long long it = it0 + u * 32 + lane;
+      x[u] = item_of<FLAT>(p, it < total ? it : 0);
+      v[u] = it < total ? load8<T, AL>(p.q, x[u].row, x[u].vec, p.d) : Raw8<T>{};
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      f32x2 f[4];
+      widen8<T>(v[u], true, f);
+      if (it0 + u * 32 + lane < total) put8<T, AL>(p.r, x[u].row, x[u].vec, p.d, narrow8<T>(f));
+    }
   }
 }
 
@@ -54,6 +84,16 @@ int pack_check(const PackParams& p, int dtype) {
 }
 
 bool pack_wide(const PackParams& p, int dtype) { return rows_wide(p.r, p.d, dtype) && rows_wide(p.q, p.d, dtype); }
+
+// Sets the vectors of a launch and, where the rows allow it, cuts them anew (FLAT).
+bool pack_flat(PackParams& p, bool wide, int vecs) {
+  p.vecs = vecs;
+  p.total = p.n * vecs;
+  if (!wide || p.r.ld != p.d || p.d % kPackBlock != 0) return false;
+  p.d = 8 << 20;
+  p.r.ld = p.d;
+  return true;
+}
 
 }  // namespace
 }  // namespace mt
@@ -70,18 +110,19 @@ int mt_pack8(const void* x, int64_t ldx, int64_t n, int32_t d, int dtype, int8_t
   p.d = d;
   const int rc = pack_check(p, dtype);
   if (rc != MT_OK || n == 0) return rc;
-  p.vecs = (d + kPackBlock - 1) / kPackBlock * 4;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int grid = grid_for(n * p.vecs, 256, 8);
-  const bool wide = pack_wide(p, dtype);
+  const bool wide = pack_wide(p, dtype), flat = pack_flat(p, wide, (d + kPackBlock - 1) / kPackBlock * 4);
+  const int grid = grid_for((p.total + kUnroll - 1) / kUnroll, 256, 8);
   {
     MT_LAUNCH("k_pack8", s);
     if (dtype == MT_F32) {
-      if (wide) k_pack8<float, true><<<grid, 256, 0, s>>>(p);
-      else k_pack8<float, false><<<grid, 256, 0, s>>>(p);
+      if (flat) k_pack8<float, true, true><<<grid, 256, 0, s>>>(p);
+      else if (wide) k_pack8<float, true, false><<<grid, 256, 0, s>>>(p);
+      else k_pack8<float, false, false><<<grid, 256, 0, s>>>(p);
     } else {
-      if (wide) k_pack8<__nv_bfloat16, true><<<grid, 256, 0, s>>>(p);
-      else k_pack8<__nv_bfloat16, false><<<grid, 256, 0, s>>>(p);
+      if (flat) k_pack8<__nv_bfloat16, true, true><<<grid, 256, 0, s>>>(p);
+      else if (wide) k_pack8<__nv_bfloat16, true, false><<<grid, 256, 0, s>>>(p);
+      else k_pack8<__nv_bfloat16, false, false><<<grid, 256, 0, s>>>(p);
     }
   }
   return cudaGetLastError() == cudaSuccess ? MT_OK : MT_ECUDA;
@@ -97,18 +138,19 @@ int mt_unpack8(const int8_t* codes, const uint8_t* exps, int64_t n, int32_t d, i
   p.d = d;
   const int rc = pack_check(p, dtype);
   if (rc != MT_OK || n == 0) return rc;
-  p.vecs = (d + 7) / 8;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int grid = grid_for(n * p.vecs, 256, 8);
-  const bool wide = pack_wide(p, dtype);
+  const bool wide = pack_wide(p, dtype), flat = pack_flat(p, wide, (d + 7) / 8);
+  const int grid = grid_for((p.total + kUnroll - 1) / kUnroll, 256, 8);
   {
     MT_LAUNCH("k_unpack8", s);
     if (dtype == MT_F32) {
-      if (wide) k_unpack8<float, true><<<grid, 256, 0, s>>>(p);
-      else k_unpack8<float, false><<<grid, 256, 0, s>>>(p);
+      if (flat) k_unpack8<float, true, true><<<grid, 256, 0, s>>>(p);
+      else if (wide) k_unpack8<float, true, false><<<grid, 256, 0, s>>>(p);
+      else k_unpack8<float, false, false><<<grid, 256, 0, s>>>(p);
     } else {
-      if (wide) k_unpack8<__nv_bfloat16, true><<<grid, 256, 0, s>>>(p);
-      else k_unpack8<__nv_bfloat16, false><<<grid, 256, 0, s>>>(p);
+      if (flat) k_unpack8<__nv_bfloat16, true, true><<<grid, 256, 0, s>>>(p);
+      else if (wide) k_unpack8<__nv_bfloat16, true, false><<<grid, 256, 0, s>>>(p);
+      else k_unpack8<__nv_bfloat16, false, false><<<grid, 256, 0, s>>>(p);
     }
   }
   return cudaGetLastError() == cudaSuccess ? MT_OK : MT_ECUDA;
