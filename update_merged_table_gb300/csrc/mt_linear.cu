@@ -169,10 +169,28 @@ __global__ void __launch_bounds__(256) k_linear_sums(const LinearWeights p) {
     const int c = s_cum[g + 1] - s_cum[g];
     if (c == 1) continue;  // written by its only chunk
     const float* part = p.part + (size_t)s_slot[g] * size;
-    for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < size; i += (size_t)gridDim.x * blockDim.x) {
-      float s = 0.0f;
-      for (int k = 0; k < c; ++k) s += __ldg(part + (size_t)k * size + i);
-      p.dw[(size_t)g * size + i] = s;
+    float* out = p.dw + (size_t)g * size;
+    const size_t i0 = (size_t)blockIdx.x * blockDim.x + threadIdx.x, step = (size_t)gridDim.x * blockDim.x;
+    if (size % 4 == 0 && ((uintptr_t)p.dw & 15) == 0) {  // four values at once, four chunks in flight
+      for (size_t i = i0; i < size / 4; i += step) {
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int k = 0; k < c; ++k) {
+          const float4 v = __ldg(reinterpret_cast<const float4*>(part + (size_t)k * size) + i);
+          s.x += v.x;
+          s.y += v.y;
+          s.z += v.z;
+          s.w += v.w;
+        }
+        reinterpret_cast<float4*>(out)[i] = s;
+      }
+    } else {
+      for (size_t i = i0; i < size; i += step) {
+        float s = 0.0f;
+#pragma unroll 4
+        for (int k = 0; k < c; ++k) s += __ldg(part + (size_t)k * size + i);
+        out[i] = s;
+      }
     }
   }
 }
@@ -215,7 +233,7 @@ cudaError_t launch_linear_weights(const LinearWeights& p, int dtype, cudaStream_
 cudaError_t launch_linear_sums(const LinearWeights& p, cudaStream_t s) {
   MT_LAUNCH("k_linear_sums", s);
   const long long size = (long long)p.M * p.K;
-  const dim3 grid((unsigned)std::min<long long>((size + 255) / 256, 1024), p.groups);
+  const dim3 grid((unsigned)std::min<long long>((size + 1023) / 1024, 1024), p.groups);
   k_linear_sums<<<grid, 256, weights_smem(p.groups), s>>>(p);
   return cudaGetLastError();
 }

@@ -317,7 +317,6 @@ constexpr int kWarpsW = 4 + kReadWarps;  // a warpgroup for copies and products 
 // launch = 64512) are split anew, 56 for a control thread and 224 for a read-out thread (128 x 56 + 256 x 224 = 64512).
 constexpr int kRegsLaunch = 168, kRegsControl = 56, kRegsRead = 224;
 static_assert(128 * kRegsControl + 32 * kReadWarps * kRegsRead <= kWarpsW * 32 * kRegsLaunch, "the split fits the launch");
-constexpr int kLag = 2;       // stages the read-out of a finished accumulator waits behind the widening (8-bit x)
 
 template <int BN, bool X8>
 __global__ void __launch_bounds__(kWarpsW * 32, 1)
@@ -457,7 +456,7 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     bool ok = true;
     float sum[kCols];
 
-    auto read_out = [&](bool first) {
+    auto read_out = [&]() {
       ok = __all_sync(kFull, tc::mbar_wait(&bar.acc_full[acc], acc_phase));
       if (!ok) return;
       tc::fence_after();
@@ -467,7 +466,7 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         tc::tmem_load32(from + acc * BN + c0, v);
         tc::tmem_load_wait();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) sum[c0 + j] = first ? __uint_as_float(v[j]) : sum[c0 + j] + __uint_as_float(v[j]);
+        for (int j = 0; j < 32; ++j) sum[c0 + j] += __uint_as_float(v[j]);
       }
       tc::fence_before();
       __syncwarp();
@@ -479,62 +478,75 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     for (long long t = blockIdx.x; t < total && ok; t += gridDim.x) {
       const Tile x = tile_of(t);
       const int parts = (x.stages + kPromote - 1) / kPromote;
-      int read = 0;
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) sum[j] = 0.0f;
       if constexpr (X8) {
-        // the exponents of the next stages come while earlier ones are widened
+        // The exponents of the next kAhead stages are on their way while one is widened.  The stages are unrolled so
+        // that a register waits for its own load only (handing it on to another would wait at once).
         constexpr int kAhead = 4;
+        static_assert(kPromote % kAhead == 0, "a part is whole rounds");
         const bool has = x.k0 + cq * 32 < p.K;
         const uint8_t* ex = p.x.exps + (x.first + crow) * nb + x.k0 / kPackBlock + cq;
+        const int rows = (int)(x.last - x.first) - crow;  // rows of the chunk from this thread's first on
+        const uint32_t ex_step = (uint32_t)(kBK * nb);
         uint32_t e[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-          e[i] = has && x.first + crow + i * kBK < x.last ? __ldg(ex + (size_t)i * kBK * nb) : 127u;
-        for (int k = 0; k < x.stages && ok; ++k) {
-          const uint32_t byte = e[0];
+        for (int i = 0; i < kAhead; ++i) e[i] = has && i * kBK < rows ? (uint32_t)__ldg(ex + (size_t)i * ex_step) : 127u;
+        for (int part = 0; part <= parts; ++part) {
+          const int last_k = min((part + 1) * kPromote, x.stages);  // no stages are left for part = parts
+#pragma unroll 1
+          for (int k0 = part * kPromote; k0 < last_k; k0 += kAhead) {
 #pragma unroll
-          for (int i = 0; i + 1 < kAhead; ++i) e[i] = e[i + 1];
-          const long long ahead = (long long)(k + kAhead) * kBK;
-          e[kAhead - 1] = has && x.first + crow + ahead < x.last ? __ldg(ex + (size_t)ahead * nb) : 127u;
-          ok = __all_sync(kFull, tc::mbar_wait(&bar.full[s.stage], s.phase));
-          // every warp goes through the barriers below, also after a wait ran out
-          uint8_t* st = ring + s.stage * R::kStage;
-          uint4 q[2];
+            for (int i = 0; i < kAhead; ++i) {
+              const int k = k0 + i;
+              if (k >= last_k) break;
+              const uint32_t byte = e[i];
+              e[i] = has && (k + kAhead) * kBK < rows ? (uint32_t)__ldg(ex + (size_t)(k + kAhead) * ex_step) : 127u;
+              // every warp goes through the barriers below, also after a wait ran out
+              ok = __all_sync(kFull, tc::mbar_wait(&bar.full[s.stage], s.phase)) && ok;
+              uint8_t* st = ring + s.stage * R::kStage;
+              uint4 q[2];
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            q[i] = *reinterpret_cast<const uint4*>(st + crow * 128 + cq * 32 + ((i ^ (cq >> 1)) << 4));
-          asm volatile("bar.sync 1, 256;" ::: "memory");  // the codes are in registers: their place may be written
-          // 2^e as bf16, twice; bf16 holds every exponent a checkpoint has
-          const uint32_t scale = byte == kPackNan ? 0x7FC07FC0u : (byte << 7) * 0x00010001u;
+              for (int j = 0; j < 2; ++j)
+                q[j] = *reinterpret_cast<const uint4*>(st + crow * 128 + cq * 32 + ((j ^ (cq >> 1)) << 4));
+              asm volatile("bar.sync 1, 256;" ::: "memory");  // the codes are in registers: their place may be written
+              // 2^e as bf16, twice; bf16 holds every exponent a checkpoint has
+              const uint32_t scale = byte == kPackNan ? 0x7FC07FC0u : (byte << 7) * 0x00010001u;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint4 o = make_uint4(tc::codes_bf16x2(w[2 * h], 0, scale), tc::codes_bf16x2(w[2 * h], 1, scale),
-                                         tc::codes_bf16x2(w[2 * h + 1], 0, scale), tc::codes_bf16x2(w[2 * h + 1], 1, scale));
-              const int c = (cq & 1) * 4 + (i ^ (cq >> 1)) * 2 + h;  // piece of the row's 128 bytes
-              *reinterpret_cast<uint4*>(st + (cq >> 1) * 8192 + crow * 128 + ((c ^ (crow & 7)) << 4)) = o;
+                for (int h = 0; h < 2; ++h) {
+                  const uint4 o = make_uint4(tc::codes_bf16x2(w[2 * h], 0, scale), tc::codes_bf16x2(w[2 * h], 1, scale),
+                                             tc::codes_bf16x2(w[2 * h + 1], 0, scale), tc::codes_bf16x2(w[2 * h + 1], 1, scale));
+                  const int c = (cq & 1) * 4 + (j ^ (cq >> 1)) * 2 + h;  // piece of the row's 128 bytes
+                  *reinterpret_cast<uint4*>(st + (cq >> 1) * 8192 + crow * 128 + ((c ^ (crow & 7)) << 4)) = o;
+                }
+              }
+              tc::fence_async_proxy();
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive(&bar.wide[s.stage]);
+              s.next<R::kStages>();
             }
           }
-          tc::fence_async_proxy();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&bar.wide[s.stage]);
-          s.next<R::kStages>();
-          if (ok && read < parts - 1 && k >= (read + 1) * kPromote - 1 + kLag) {
-            read_out(read == 0);
-            ++read;
-          }
+          // the part before this one: its products are done or nearly so, and this part's go on meanwhile
+          if (part > 0 && ok) read_out();
         }
+      } else {
+        for (int part = 0; part < parts && ok; ++part) read_out();
       }
-      for (; read < parts && ok; ++read) read_out(read == 0);
       if (!ok) break;
       // sum[j]: dW at column k0 + 32 quad + lane and row m0 + half kCols + j: 32 lanes write 128 bytes of a row
-      float* out = weights_out(p, s_cum, s_slot, x.g, x.c);
       const int k = x.k0 + quad * 32 + lane, m0 = x.m0 + half * kCols;
+      float* out = weights_out(p, s_cum, s_slot, x.g, x.c) + (size_t)m0 * p.K + k;
+      size_t ld = p.K;
+      asm volatile("" : "+l"(ld));  // keeps the compiler from holding a register per row's offset across the tiles
       if (k < p.K) {
 #pragma unroll
-        for (int j = 0; j < kCols; ++j)
-          if (m0 + j < p.M) out[(size_t)(m0 + j) * p.K + k] = sum[j];
+        for (int j = 0; j < kCols; ++j) {
+          if (m0 + j < p.M) *out = sum[j];
+          out += ld;
+        }
       }
       __syncwarp();
     }
