@@ -84,17 +84,19 @@ constexpr int kBK = 64;          // contraction per stage: one 128-byte swizzled
 constexpr int kWarpsTC = 6;      // copies, products, four to read out
 constexpr int kStageOut = 4096;  // bytes per read-out warp: 32 rows x 128 bytes
 
-template <int BN>
+// Shared memory of a block: stages of both operands (of a pair's block: its half of the columns), and where the rows
+// kernel turns its tiles.
+template <int BN, int CG>
 struct Ring {
-  static constexpr int kStageA = kBM * kBK * 2, kStageB = BN * kBK * 2;
+  static constexpr int kStageA = kBM * kBK * 2, kStageB = BN / CG * kBK * 2;
   static constexpr int kStage = kStageA + kStageB;
-  static constexpr int kStages = 196608 / kStage;       // 4 (BN 256), 6 (128), 8 (64)
+  static constexpr int kStages = 196608 / kStage;       // 4 (BN 256), 6 (128, and 256 of a pair), 8 (64)
   static constexpr int kBytes = kStages * kStage + 4 * kStageOut;
 };
 
 struct Barriers {
   uint64_t full[8], empty[8];    // a stage's copies have landed; its products are done
-  uint64_t wide[8];              // a stage's 8-bit operand has been widened
+  uint64_t ready[8];             // a stage's operands are as the product wants them (widened, or zeroed past the end)
   uint64_t acc_full[2], acc_empty[2];  // an accumulator is finished; it has been read out
   uint64_t done;                 // every product issued is done
   uint32_t tmem;
@@ -104,36 +106,47 @@ __device__ __forceinline__ void latch_status(int32_t* status, int code) {
   if (status != nullptr) atomicCAS(status, 0, code);
 }
 
-// Set-up that both kernels share: barriers, tensor memory.  Every thread calls it; ends with the block synchronised.
-template <int BN>
-__device__ __forceinline__ uint32_t tc_begin(Barriers& b, int read_warps) {
+// Set-up that both kernels share: barriers, tensor memory.  Every thread calls it; ends with the block (the pair)
+// synchronised.
+template <int BN, int CG>
+__device__ __forceinline__ uint32_t tc_begin(Barriers& b, int ready_count, int read_warps) {
   if (threadIdx.x == 0) {
-    for (int i = 0; i < Ring<BN>::kStages; ++i) {
+    for (int i = 0; i < Ring<BN, CG>::kStages; ++i) {
       tc::mbar_init(&b.full[i], 1);
       tc::mbar_init(&b.empty[i], 1);
-      tc::mbar_init(&b.wide[i], read_warps);
+      tc::mbar_init(&b.ready[i], ready_count);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&b.acc_full[i], 1);
-      tc::mbar_init(&b.acc_empty[i], read_warps);
+      tc::mbar_init(&b.acc_empty[i], read_warps * CG);
     }
     tc::mbar_init(&b.done, 1);
     tc::mbar_init_fence();
   }
-  if (threadIdx.x >> 5 == 1) tc::tmem_alloc(&b.tmem, 2 * BN);
+  __syncwarp();
+  if (threadIdx.x >> 5 == 1) tc::tmem_alloc<CG>(&b.tmem, 2 * BN);
   tc::fence_before();
-  __syncthreads();
+  if constexpr (CG == 2) tc::cluster_sync();
+  else __syncthreads();
   tc::fence_after();
   return b.tmem;
 }
 
-template <int BN>
+template <int BN, int CG>
 __device__ __forceinline__ void tc_end(uint32_t tmem) {
   __syncwarp();
   tc::fence_before();
-  __syncthreads();
+  if constexpr (CG == 2) tc::cluster_sync();
+  else __syncthreads();
   tc::fence_after();
-  if (threadIdx.x >> 5 == 1) tc::tmem_free(tmem, 2 * BN);
+  if (threadIdx.x >> 5 == 1) tc::tmem_free<CG>(tmem, 2 * BN);
+}
+
+// Arrives at a barrier of the block that issues the products.
+template <int CG>
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  if constexpr (CG == 2) tc::mbar_arrive_at(tc::of_leader(bar));
+  else tc::mbar_arrive(bar);
 }
 
 // The ring's position: stage and the parity of its current use.
@@ -148,6 +161,21 @@ struct Slot {
     }
   }
 };
+
+// The last stages' products are done, and what a pair's first block signals of them has arrived here.
+template <int STAGES>
+__device__ __forceinline__ bool all_released(Barriers& b, Slot s, long long issued) {
+  const long long k = issued < STAGES ? issued : STAGES;
+  for (long long i = 0; i < k; ++i) {
+    if (s.stage == 0) {
+      s.stage = STAGES;
+      s.phase ^= 1;
+    }
+    --s.stage;
+    if (!tc::mbar_wait(&b.empty[s.stage], s.phase)) return false;
+  }
+  return true;
+}
 
 // After a wait ran out: the copies already issued are waited for (again with a limit) so that none lands in a block
 // that has ended.
@@ -167,10 +195,14 @@ __device__ __forceinline__ void drain(Barriers& b, Slot s, long long issued) {
 // ---- forward and dx ------------------------------------------------------------------------
 
 // B_MN: W_g(i, j) has its columns j contiguous (dx); otherwise its contraction i (forward).
-template <int BN, bool B_MN>
+// CG = 2: a pair of blocks takes 256 rows, each its 128 and half of the tile's columns of W: a block then writes and
+// reads 64 KB of shared memory per stage instead of 96, which at 128 bytes a clock is what the tensor core's 512 clocks
+// allow (one block alone is bound by its shared memory: 768 clocks).
+template <int BN, bool B_MN, int CG>
 __global__ void __launch_bounds__(kWarpsTC * 32, 1)
 k_linear_rows_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w, const LinearRows p) {
-  using R = Ring<BN>;
+  using R = Ring<BN, CG>;
+  constexpr int kRows = kBM * CG, kCols = BN / CG;  // rows of a tile; columns of W that a block copies
   extern __shared__ uint8_t s_raw[];
   __shared__ Barriers bar;
   uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)s_raw + 1023) & ~(uintptr_t)1023);
@@ -178,56 +210,72 @@ k_linear_rows_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constan
   long long* s_off = reinterpret_cast<long long*>(ring + R::kBytes);
   int* s_cum = reinterpret_cast<int*>(s_off + p.groups + 1);
   load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
-  count_tiles(s_off, p.groups, kBM, s_cum);
-  const uint32_t tmem = tc_begin<BN>(bar, 4);
+  count_tiles(s_off, p.groups, kRows, s_cum);
+  const uint32_t tmem = tc_begin<BN, CG>(bar, 1, 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x % CG;  // in the pair
   const int steps = (p.I + kBK - 1) / kBK;
   const long long total = (long long)s_cum[p.groups] * p.jtiles;
+  const long long t0 = blockIdx.x / CG, tstep = gridDim.x / CG;
 
   if (warp == 0) {
     if (lane == 0) {
       Slot s;
       long long issued = 0;
       bool ok = true;
-      for (long long t = blockIdx.x; t < total && ok; t += gridDim.x) {
-        const int rt = (int)(t / p.jtiles), j0 = (int)(t - (long long)rt * p.jtiles) * BN;
+      for (long long t = t0; t < total && ok; t += tstep) {
+        const int rt = (int)(t / p.jtiles), j0 = (int)(t - (long long)rt * p.jtiles) * BN + rank * kCols;
         const int g = tile_group(s_cum, p.groups, rt);
-        const int r0 = (int)(s_off[g] + (long long)(rt - s_cum[g]) * kBM);
+        const int r0 = (int)(s_off[g] + (long long)(rt - s_cum[g]) * kRows) + rank * kBM;
         for (int k = 0; k < steps; ++k) {
           ok = tc::mbar_wait(&bar.empty[s.stage], s.phase ^ 1);
           if (!ok) break;
           uint8_t* st = ring + s.stage * R::kStage;
-          tc::mbar_expect(&bar.full[s.stage], R::kStage);
-          tc::tma_load_2d(st, &map_a, &bar.full[s.stage], k * kBK, r0);
-          if constexpr (B_MN) {
+          if constexpr (CG == 2) {  // both blocks' copies count on the first block's barrier
+            const uint32_t full = tc::of_leader(&bar.full[s.stage]);
+            if (rank == 0) tc::mbar_expect(&bar.full[s.stage], 2 * R::kStage);
+            tc::tma_load_2d_pair(st, &map_a, full, k * kBK, r0);
+            if constexpr (B_MN) {
 #pragma unroll
-            for (int c = 0; c < BN / 64; ++c)
-              tc::tma_load_3d(st + R::kStageA + c * 8192, &map_w, &bar.full[s.stage], j0 + c * 64, k * kBK, g);
+              for (int c = 0; c < kCols / 64; ++c)
+                tc::tma_load_3d_pair(st + R::kStageA + c * 8192, &map_w, full, j0 + c * 64, k * kBK, g);
+            } else {
+              tc::tma_load_3d_pair(st + R::kStageA, &map_w, full, k * kBK, j0, g);
+            }
           } else {
-            tc::tma_load_3d(st + R::kStageA, &map_w, &bar.full[s.stage], k * kBK, j0, g);
+            tc::mbar_expect(&bar.full[s.stage], R::kStage);
+            tc::tma_load_2d(st, &map_a, &bar.full[s.stage], k * kBK, r0);
+            if constexpr (B_MN) {
+#pragma unroll
+              for (int c = 0; c < kCols / 64; ++c)
+                tc::tma_load_3d(st + R::kStageA + c * 8192, &map_w, &bar.full[s.stage], j0 + c * 64, k * kBK, g);
+            } else {
+              tc::tma_load_3d(st + R::kStageA, &map_w, &bar.full[s.stage], k * kBK, j0, g);
+            }
           }
           ++issued;
           s.next<R::kStages>();
         }
       }
+      ok = ok && all_released<R::kStages>(bar, s, issued);
       if (!ok) {
         latch_status(p.status, MT_ECUDA);
-        drain<R::kStages>(bar, s, issued);
+        if (rank == 0) drain<R::kStages>(bar, s, issued);
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t instr = tc::instr_bf16(kBM, BN, false, B_MN);
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t instr = tc::instr_bf16(kRows, BN, false, B_MN);
       Slot s;
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true;
-      for (long long t = blockIdx.x; t < total && ok; t += gridDim.x) {
-        ok = tc::mbar_wait(&bar.acc_empty[acc], acc_phase ^ 1);
+      for (long long t = t0; t < total && ok; t += tstep) {
+        ok = tc::mbar_wait<CG == 2>(&bar.acc_empty[acc], acc_phase ^ 1);
         if (!ok) break;
         tc::fence_after();
         for (int k = 0; k < steps; ++k) {
-          ok = tc::mbar_wait(&bar.full[s.stage], s.phase);
+          ok = tc::mbar_wait<CG == 2>(&bar.full[s.stage], s.phase);
           if (!ok) break;
           tc::fence_after();
           const uint32_t a = tc::smem_addr(ring + s.stage * R::kStage), b = a + R::kStageA;
@@ -235,19 +283,21 @@ k_linear_rows_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constan
           for (int i = 0; i < kBK / 16; ++i) {
             const uint64_t da = tc::smem_desc(a + i * 32, 16);
             const uint64_t db = B_MN ? tc::smem_desc(b + i * 2048, 8192) : tc::smem_desc(b + i * 32, 16);
-            tc::mma_bf16(tmem + acc * BN, da, db, instr, k > 0 || i > 0);
+            tc::mma_bf16<CG>(tmem + acc * BN, da, db, instr, k > 0 || i > 0);
           }
-          tc::mma_commit(&bar.empty[s.stage]);
+          tc::mma_commit<CG>(&bar.empty[s.stage]);
           s.next<R::kStages>();
         }
         if (!ok) break;
-        tc::mma_commit(&bar.acc_full[acc]);
+        tc::mma_commit<CG>(&bar.acc_full[acc]);
         acc ^= 1;
         acc_phase ^= acc == 0;
       }
-      tc::mma_commit(&bar.done);  // tensor memory is freed only when no product writes it, also after a wait ran out
+      tc::mma_commit<CG>(&bar.done);  // tensor memory is freed only when no product writes it, also after a wait ran out
       ok = tc::mbar_wait(&bar.done, 0) && ok;
       if (!ok) latch_status(p.status, MT_ECUDA);
+    } else if (lane == 0) {
+      if (!tc::mbar_wait(&bar.done, 0)) latch_status(p.status, MT_ECUDA);
     }
   } else {
     const int quad = warp & 3;  // the lanes of tensor memory this warp may read
@@ -257,12 +307,12 @@ k_linear_rows_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
-    for (long long t = blockIdx.x; t < total; t += gridDim.x) {
+    for (long long t = t0; t < total; t += tstep) {
       const int rt = (int)(t / p.jtiles), j0 = (int)(t - (long long)rt * p.jtiles) * BN;
       const int g = tile_group(s_cum, p.groups, rt);
-      const long long r0 = s_off[g] + (long long)(rt - s_cum[g]) * kBM + quad * 32;
+      const long long r0 = s_off[g] + (long long)(rt - s_cum[g]) * kRows + rank * kBM + quad * 32;
       const int rows = (int)min((long long)32, s_off[g + 1] - r0);  // <= 0: none of this warp's rows is in the group
-      ok = __all_sync(kFull, tc::mbar_wait(&bar.acc_full[acc], acc_phase));
+      ok = __all_sync(kFull, tc::mbar_wait<CG == 2>(&bar.acc_full[acc], acc_phase));
       if (!ok) break;
       tc::fence_after();
       const uint32_t from = tmem + acc * BN + ((uint32_t)(quad * 32) << 16);
@@ -275,7 +325,7 @@ k_linear_rows_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         if (c0 + 64 == BN) {  // read out: the accumulator may be written again
           tc::fence_before();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&bar.acc_empty[acc]);
+          if (lane == 0) arrive<CG>(&bar.acc_empty[acc]);
         }
         // 64 columns of the lane's row as eight 16-byte pieces, piece c at c ^ (lane & 7): writes and reads of eight
         // neighbouring lanes then meet all banks
@@ -305,7 +355,7 @@ k_linear_rows_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constan
     }
     if (!ok) latch_status(p.status, MT_ECUDA);
   }
-  tc_end<BN>(tmem);
+  tc_end<BN, CG>(tmem);
 }
 
 // ---- dW -----------------------------------------------------------------------------------------
@@ -318,10 +368,23 @@ constexpr int kWarpsW = 4 + kReadWarps;  // a warpgroup for copies and products 
 constexpr int kRegsLaunch = 168, kRegsControl = 56, kRegsRead = 224;
 static_assert(128 * kRegsControl + 32 * kReadWarps * kRegsRead <= kWarpsW * 32 * kRegsLaunch, "the split fits the launch");
 
-template <int BN, bool X8>
+// Rows [left, kBK) of `slabs` slabs become zero, by a warp.  Row i of a 64-column slab is the 128 bytes at i * 128,
+// whatever the swizzle does inside them.
+__device__ __forceinline__ void zero_rows(uint8_t* st, int slabs, int left, int lane) {
+  for (int slab = 0; slab < slabs; ++slab)
+    for (int i = left * 8 + lane; i < kBK * 8; i += 32)
+      *reinterpret_cast<uint4*>(st + slab * 8192 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+  tc::fence_async_proxy();
+  __syncwarp();
+}
+
+// CG = 2: a pair takes 256 columns of x, each block its 128 and half of the tile's columns of dy (the split of
+// k_linear_rows_tc, for the same reason).
+template <int BN, bool X8, int CG>
 __global__ void __launch_bounds__(kWarpsW * 32, 1)
 k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_dy, const LinearWeights p) {
-  using R = Ring<BN>;
+  using R = Ring<BN, CG>;
+  constexpr int kRowsD = kBM * CG, kColsB = BN / CG;  // columns of x in a tile; columns of dy that a block copies
   extern __shared__ uint8_t s_raw[];
   __shared__ Barriers bar;
   uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)s_raw + 1023) & ~(uintptr_t)1023);
@@ -331,12 +394,14 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
   load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
   count_tiles(s_off, p.groups, p.chunk, s_cum);
   count_slots(s_cum, p.groups, s_slot);
-  const uint32_t tmem = tc_begin<BN>(bar, kReadWarps);
+  const uint32_t tmem = tc_begin<BN, CG>(bar, X8 ? kReadWarps / 2 * CG : 1, kReadWarps);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int mt = (p.M + BN - 1) / BN, tiles = (p.K + kBM - 1) / kBM * mt;
+  const int rank = blockIdx.x % CG;
+  const int mt = (p.M + BN - 1) / BN, tiles = (p.K + kRowsD - 1) / kRowsD * mt;
   const long long total = (long long)s_cum[p.groups] * tiles;
+  const long long t0 = blockIdx.x / CG, tstep = gridDim.x / CG;
 
-  // tile t: chunk c of group g, the chunk's rows [first, last), dW's corner (m0, k0)
+  // tile t: chunk c of group g, the chunk's rows [first, last), dW's corner (m0, k0 of this block)
   struct Tile {
     int g, c, m0, k0, stages;
     long long first, last;
@@ -345,7 +410,7 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     Tile x;
     x.c = (int)(t / tiles);
     const int q = (int)(t - (long long)x.c * tiles);
-    x.k0 = q / mt * kBM;
+    x.k0 = q / mt * kRowsD + rank * kBM;
     x.m0 = (q - q / mt * mt) * BN;
     x.g = tile_group(s_cum, p.groups, x.c);
     x.first = s_off[x.g] + (long long)(x.c - s_cum[x.g]) * p.chunk;
@@ -362,7 +427,7 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         Slot s;
         long long issued = 0;
         bool ok = true;
-        for (long long t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        for (long long t = t0; t < total && ok; t += tstep) {
           const Tile x = tile_of(t);
           for (long long r = x.first; r < x.last; r += kBK) {
             ok = tc::mbar_wait(&bar.empty[s.stage], s.phase ^ 1);
@@ -372,61 +437,66 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
             if constexpr (X8) {
               tc::tma_load_2d(st, &map_x, &bar.full[s.stage], x.k0, (int)r);
             } else {
-  #pragma unroll
+#pragma unroll
               for (int c = 0; c < kBM / 64; ++c)
                 tc::tma_load_2d(st + c * 8192, &map_x, &bar.full[s.stage], x.k0 + c * 64, (int)r);
             }
-  #pragma unroll
-            for (int c = 0; c < BN / 64; ++c)
-              tc::tma_load_2d(st + R::kStageA + c * 8192, &map_dy, &bar.full[s.stage], x.m0 + c * 64, (int)r);
+#pragma unroll
+            for (int c = 0; c < kColsB / 64; ++c)
+              tc::tma_load_2d(st + R::kStageA + c * 8192, &map_dy, &bar.full[s.stage], x.m0 + rank * kColsB + c * 64, (int)r);
             ++issued;
             s.next<R::kStages>();
           }
         }
+        ok = ok && all_released<R::kStages>(bar, s, issued);
         if (!ok) {
           latch_status(p.status, MT_ECUDA);
           drain<R::kStages>(bar, s, issued);
         }
       }
     }
+    // Plain x: warp 1 of each block sees its copies land and zeroes the rows past the chunk's end, which belong to
+    // others, in both operands, so that nothing of them (an infinity or NaN too) reaches the sum; the second block of a
+    // pair then tells the first.  8-bit x: the widening warps do all that.
     if (warp == 1) {
-      constexpr uint32_t instr = tc::instr_bf16(kBM, BN, true, true);
+      constexpr uint32_t instr = tc::instr_bf16(kRowsD, BN, true, true);
       Slot s;
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true;
-      for (long long t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      for (long long t = X8 && rank != 0 ? total : t0; t < total && ok; t += tstep) {
         const Tile x = tile_of(t);
         for (int k = 0; k < x.stages; ++k) {
-          if (k % kPromote == 0) {
-            ok = __all_sync(kFull, tc::mbar_wait(&bar.acc_empty[acc], acc_phase ^ 1));
+          if (k % kPromote == 0 && rank == 0) {
+            ok = __all_sync(kFull, tc::mbar_wait<CG == 2>(&bar.acc_empty[acc], acc_phase ^ 1));
             if (!ok) break;
           }
-          ok = __all_sync(kFull, tc::mbar_wait(X8 ? &bar.wide[s.stage] : &bar.full[s.stage], s.phase));
-          if (!ok) break;
           uint8_t* st = ring + s.stage * R::kStage;
-          const long long r = x.first + (long long)k * kBK;
-          const int left = (int)min((long long)kBK, x.last - r);
-          if (left < kBK) {
-            // Rows past the chunk's end belong to others: both operands become zero there, so that nothing of them
-            // (an infinity or NaN too) reaches the sum.  Row i of a 64-column slab is the 128 bytes at i * 128,
-            // whatever the swizzle does inside them.
-            for (int slab = 0; slab < kBM / 64 + BN / 64; ++slab)
-              for (int i = left * 8 + lane; i < kBK * 8; i += 32)
-                *reinterpret_cast<uint4*>(st + slab * 8192 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-            tc::fence_async_proxy();
-            __syncwarp();
+          if constexpr (!X8) {
+            ok = __all_sync(kFull, tc::mbar_wait(&bar.full[s.stage], s.phase));
+            if (!ok) break;
+            const int left = (int)min((long long)kBK, x.last - x.first - (long long)k * kBK);
+            if (left < kBK) zero_rows(st, (kBM + kColsB) / 64, left, lane);
+            if (rank != 0) {
+              if (lane == 0) arrive<CG>(&bar.ready[s.stage]);
+              s.next<R::kStages>();
+              continue;
+            }
+          }
+          if (X8 || CG == 2) {
+            ok = __all_sync(kFull, tc::mbar_wait<CG == 2>(&bar.ready[s.stage], s.phase));
+            if (!ok) break;
           }
           tc::fence_after();
           const bool closes = k % kPromote == kPromote - 1 || k + 1 == x.stages;
           if (lane == 0) {
             const uint32_t a = tc::smem_addr(st), b = a + R::kStageA;
-  #pragma unroll
+#pragma unroll
             for (int i = 0; i < kBK / 16; ++i)
-              tc::mma_bf16(tmem + acc * BN, tc::smem_desc(a + i * 2048, 8192), tc::smem_desc(b + i * 2048, 8192), instr,
-                           k % kPromote > 0 || i > 0);
-            tc::mma_commit(&bar.empty[s.stage]);
-            if (closes) tc::mma_commit(&bar.acc_full[acc]);
+              tc::mma_bf16<CG>(tmem + acc * BN, tc::smem_desc(a + i * 2048, 8192), tc::smem_desc(b + i * 2048, 8192), instr,
+                               k % kPromote > 0 || i > 0);
+            tc::mma_commit<CG>(&bar.empty[s.stage]);
+            if (closes) tc::mma_commit<CG>(&bar.acc_full[acc]);
           }
           __syncwarp();
           if (closes) {
@@ -437,7 +507,8 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         }
       }
       if (lane == 0) {
-        tc::mma_commit(&bar.done);  // tensor memory is freed only when no product writes it, also after a wait ran out
+        // tensor memory is freed only when no product writes it, also after a wait ran out
+        if (rank == 0) tc::mma_commit<CG>(&bar.done);
         ok = tc::mbar_wait(&bar.done, 0) && ok;
         if (!ok) latch_status(p.status, MT_ECUDA);
       }
@@ -448,16 +519,15 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     constexpr int kCols = BN / 2;
     const int quad = warp & 3, half = (warp - 4) >> 2;
     const uint32_t from = tmem + half * kCols + ((uint32_t)(quad * 32) << 16);
-    const int tid = threadIdx.x - 128, crow = tid >> 2, cq = tid & 3;  // 8-bit x: this thread's row and 32 columns
     const int nb = (p.K + kPackBlock - 1) / kPackBlock;
-    Slot s;
     int acc = 0;
     uint32_t acc_phase = 0;
+    uint32_t seq = 0;  // stages before this tile
     bool ok = true;
     float sum[kCols];
 
     auto read_out = [&]() {
-      ok = __all_sync(kFull, tc::mbar_wait(&bar.acc_full[acc], acc_phase));
+      ok = __all_sync(kFull, tc::mbar_wait<CG == 2>(&bar.acc_full[acc], acc_phase));
       if (!ok) return;
       tc::fence_after();
 #pragma unroll
@@ -470,68 +540,84 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
       }
       tc::fence_before();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bar.acc_empty[acc]);
+      if (lane == 0) arrive<CG>(&bar.acc_empty[acc]);
       acc ^= 1;
       acc_phase ^= acc == 0;
     };
 
-    for (long long t = blockIdx.x; t < total && ok; t += gridDim.x) {
+    for (long long t = t0; t < total && ok; t += tstep) {
       const Tile x = tile_of(t);
       const int parts = (x.stages + kPromote - 1) / kPromote;
 #pragma unroll
       for (int j = 0; j < kCols; ++j) sum[j] = 0.0f;
       if constexpr (X8) {
-        // The exponents of the next kAhead stages are on their way while one is widened.  The stages are unrolled so
-        // that a register waits for its own load only (handing it on to another would wait at once).
-        constexpr int kAhead = 4;
-        static_assert(kPromote % kAhead == 0, "a part is whole rounds");
-        const bool has = x.k0 + cq * 32 < p.K;
-        const uint8_t* ex = p.x.exps + (x.first + crow) * nb + x.k0 / kPackBlock + cq;
+        // Two teams of four warps widen alternate stages, so that one's barriers and fences overlap the other's work: a
+        // thread takes a row and 64 columns (two blocks) of a stage.  The exponents of a thread's next four stages are on
+        // their way while it works; the stages are unrolled so that a register waits for its own load only.
+        constexpr int kOwn = kPromote / 2;
+        const int tid = threadIdx.x & 127, crow = tid >> 1, ch = tid & 1;
+        const int off = (half + seq) & 1;                 // this team's first stage of the tile
         const int rows = (int)(x.last - x.first) - crow;  // rows of the chunk from this thread's first on
+        const int kb = x.k0 / kPackBlock + ch * 2;
+        const uint8_t* ex = p.x.exps + (x.first + crow) * nb + kb;
+        const bool has0 = kb < nb, has1 = kb + 1 < nb;
         const uint32_t ex_step = (uint32_t)(kBK * nb);
-        uint32_t e[kAhead];
+        uint32_t e0[kOwn], e1[kOwn];
+        auto exponents = [&](int i, int k) {
+          const bool in = k * kBK < rows;
+          e0[i] = in && has0 ? (uint32_t)__ldg(ex + (size_t)k * ex_step) : 127u;
+          e1[i] = in && has1 ? (uint32_t)__ldg(ex + (size_t)k * ex_step + 1) : 127u;
+        };
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) e[i] = has && i * kBK < rows ? (uint32_t)__ldg(ex + (size_t)i * ex_step) : 127u;
+        for (int i = 0; i < kOwn; ++i) exponents(i, off + 2 * i);
         for (int part = 0; part <= parts; ++part) {
-          const int last_k = min((part + 1) * kPromote, x.stages);  // no stages are left for part = parts
-#pragma unroll 1
-          for (int k0 = part * kPromote; k0 < last_k; k0 += kAhead) {
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-              const int k = k0 + i;
-              if (k >= last_k) break;
-              const uint32_t byte = e[i];
-              e[i] = has && (k + kAhead) * kBK < rows ? (uint32_t)__ldg(ex + (size_t)(k + kAhead) * ex_step) : 127u;
-              // every warp goes through the barriers below, also after a wait ran out
-              ok = __all_sync(kFull, tc::mbar_wait(&bar.full[s.stage], s.phase)) && ok;
-              uint8_t* st = ring + s.stage * R::kStage;
-              uint4 q[2];
+          for (int i = 0; i < kOwn; ++i) {
+            const int k = part * kPromote + off + 2 * i;
+            if (k >= x.stages) break;  // always for part = parts
+            const uint32_t b0 = e0[i], b1 = e1[i];
+            exponents(i, k + kPromote);
+            const uint32_t stage = (seq + k) % R::kStages, phase = (seq + k) / R::kStages & 1;
+            // every warp goes through the barriers below, also after a wait ran out (it then waits no more)
+            if (ok) ok = __all_sync(kFull, tc::mbar_wait(&bar.full[stage], phase));
+            uint8_t* st = ring + stage * R::kStage;
+            uint4 q[4];
 #pragma unroll
-              for (int j = 0; j < 2; ++j)
-                q[j] = *reinterpret_cast<const uint4*>(st + crow * 128 + cq * 32 + ((j ^ (cq >> 1)) << 4));
-              asm volatile("bar.sync 1, 256;" ::: "memory");  // the codes are in registers: their place may be written
-              // 2^e as bf16, twice; bf16 holds every exponent a checkpoint has
-              const uint32_t scale = byte == kPackNan ? 0x7FC07FC0u : (byte << 7) * 0x00010001u;
+            for (int j = 0; j < 4; ++j)  // pieces in an order that spreads eight lanes over the banks
+              q[j] = *reinterpret_cast<const uint4*>(st + crow * 128 + ch * 64 + (((j + (lane >> 1)) & 3) << 4));
+            if (half == 0) asm volatile("bar.sync 1, 128;" ::: "memory");  // the codes are in registers: their place
+            else asm volatile("bar.sync 2, 128;" ::: "memory");            // may be written
+            const bool in = k * kBK < rows;  // past the chunk's end: zeros, in both operands
+            // 2^e as bf16, twice; bf16 holds every exponent a checkpoint has
+            const uint32_t s0 = b0 == kPackNan ? 0x7FC07FC0u : (b0 << 7) * 0x00010001u;
+            const uint32_t s1 = b1 == kPackNan ? 0x7FC07FC0u : (b1 << 7) * 0x00010001u;
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+            for (int j = 0; j < 4; ++j) {
+              const int piece = (j + (lane >> 1)) & 3;  // 16 codes: two 16-byte pieces of the slab's row
+              const uint32_t scale = piece < 2 ? s0 : s1;
+              const uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const uint4 o = make_uint4(tc::codes_bf16x2(w[2 * h], 0, scale), tc::codes_bf16x2(w[2 * h], 1, scale),
-                                             tc::codes_bf16x2(w[2 * h + 1], 0, scale), tc::codes_bf16x2(w[2 * h + 1], 1, scale));
-                  const int c = (cq & 1) * 4 + (j ^ (cq >> 1)) * 2 + h;  // piece of the row's 128 bytes
-                  *reinterpret_cast<uint4*>(st + (cq >> 1) * 8192 + crow * 128 + ((c ^ (crow & 7)) << 4)) = o;
-                }
+              for (int h = 0; h < 2; ++h) {
+                uint4 o = make_uint4(tc::codes_bf16x2(w[2 * h], 0, scale), tc::codes_bf16x2(w[2 * h], 1, scale),
+                                     tc::codes_bf16x2(w[2 * h + 1], 0, scale), tc::codes_bf16x2(w[2 * h + 1], 1, scale));
+                if (!in) o = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(st + ch * 8192 + crow * 128 + (((piece * 2 + h) ^ (crow & 7)) << 4)) = o;
               }
-              tc::fence_async_proxy();
-              __syncwarp();
-              if (lane == 0) tc::mbar_arrive(&bar.wide[s.stage]);
-              s.next<R::kStages>();
             }
+            if (!in) {
+              for (int slab = 0; slab < kColsB / 64; ++slab)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                  *reinterpret_cast<uint4*>(st + R::kStageA + slab * 8192 + crow * 128 + ch * 64 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            tc::fence_async_proxy();
+            __syncwarp();
+            if (lane == 0) arrive<CG>(&bar.ready[stage]);
           }
           // the part before this one: its products are done or nearly so, and this part's go on meanwhile
           if (part > 0 && ok) read_out();
         }
+        seq += x.stages;
       } else {
         for (int part = 0; part < parts && ok; ++part) read_out();
       }
@@ -552,7 +638,7 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     }
     if (!ok) latch_status(p.status, MT_ECUDA);
   }
-  tc_end<BN>(tmem);
+  tc_end<BN, CG>(tmem);
 }
 
 // ---- host --------------------------------------------------------------------------------------------
@@ -565,40 +651,57 @@ int tile_width(int J, long long row_tiles) {
   return bn;
 }
 
-template <typename Kernel>
-cudaError_t allow_smem(Kernel k, size_t bytes) {
-  return cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+// Launches a kernel of 1024-aligned dynamic shared memory, in clusters of `pair` blocks.
+template <typename Kernel, typename Params>
+cudaError_t launch_tc(Kernel kernel, int grid, int threads, size_t smem, int pair, cudaStream_t s, const CUtensorMap& a,
+                      const CUtensorMap& b, const Params& p) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = pair;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pair > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, a, b, p);
 }
 
-template <int BN, bool B_MN>
+int tc_grid(long long tiles, int pair) { return (int)std::min<long long>(tiles, sm_count() / pair) * pair; }
+
+template <int BN, bool B_MN, int CG>
 cudaError_t rows_tc(const CUtensorMap& a, const CUtensorMap& w, LinearRows p, cudaStream_t s) {
-  const size_t smem = 1024 + Ring<BN>::kBytes + (size_t)(p.groups + 1) * 12;
-  cudaError_t e = allow_smem(k_linear_rows_tc<BN, B_MN>, smem);
-  if (e != cudaSuccess) return e;
   p.jtiles = (p.J + BN - 1) / BN;
-  const long long tiles = ((p.n + kBM - 1) / kBM + p.groups) * p.jtiles;
-  const int grid = (int)std::min<long long>(tiles, sm_count());
+  const long long tiles = (p.n / (kBM * CG) + p.groups) * p.jtiles;
   MT_LAUNCH("k_linear_rows_tc", s);
-  k_linear_rows_tc<BN, B_MN><<<grid, kWarpsTC * 32, smem, s>>>(a, w, p);
-  return cudaGetLastError();
+  return launch_tc(k_linear_rows_tc<BN, B_MN, CG>, tc_grid(tiles, CG), kWarpsTC * 32,
+                   1024 + Ring<BN, CG>::kBytes + (size_t)(p.groups + 1) * 12, CG, s, a, w, p);
 }
 
-template <int BN, bool X8>
+template <int BN, bool X8, int CG>
 cudaError_t weights_tc(const CUtensorMap& x, const CUtensorMap& dy, const LinearWeights& p, cudaStream_t s) {
-  const size_t smem = 1024 + Ring<BN>::kStages * Ring<BN>::kStage + weights_smem(p.groups);
-  cudaError_t e = allow_smem(k_linear_weights_tc<BN, X8>, smem);
-  if (e != cudaSuccess) return e;
   if (BN == 256) {  // the split of the registers needs the launch to bring them
     cudaFuncAttributes a;
-    e = cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(k_linear_weights_tc<BN, X8>));
+    const cudaError_t e = cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(k_linear_weights_tc<BN, X8, CG>));
     if (e != cudaSuccess) return e;
     if (a.numRegs < kRegsLaunch) return cudaErrorInvalidValue;
   }
-  const long long tiles = (p.n / p.chunk + p.groups) * ((p.K + kBM - 1) / kBM) * ((p.M + BN - 1) / BN);
-  const int grid = (int)std::min<long long>(tiles, sm_count());
+  const long long tiles = (p.n / p.chunk + p.groups) * ((p.K + kBM * CG - 1) / (kBM * CG)) * ((p.M + BN - 1) / BN);
   MT_LAUNCH("k_linear_weights_tc", s);
-  k_linear_weights_tc<BN, X8><<<grid, kWarpsW * 32, smem, s>>>(x, dy, p);
-  return cudaGetLastError();
+  return launch_tc(k_linear_weights_tc<BN, X8, CG>, tc_grid(tiles, CG), kWarpsW * 32,
+                   1024 + Ring<BN, CG>::kStages * Ring<BN, CG>::kStage + weights_smem(p.groups), CG, s, x, dy, p);
+}
+
+template <bool X8>
+cudaError_t weights_tc(const CUtensorMap& x, const CUtensorMap& dy, const LinearWeights& p, int bn, bool pair, cudaStream_t s) {
+  if (pair) return weights_tc<256, X8, 2>(x, dy, p, s);
+  return bn == 256 ? weights_tc<256, X8, 1>(x, dy, p, s) : bn == 128 ? weights_tc<128, X8, 1>(x, dy, p, s)
+                                                                     : weights_tc<64, X8, 1>(x, dy, p, s);
 }
 
 }  // namespace
@@ -608,16 +711,21 @@ bool linear_rows_fits_tc(const LinearRows& p) {
          is_aligned(p.w, 16);
 }
 
+// Pairs where the product is bound by its arithmetic (several stages per tile) and tiles of 256 rows neither waste rows
+// (groups of 512 and more on average) nor leave SMs without work.
 cudaError_t launch_linear_rows_tc(const LinearRows& p, cudaStream_t s) {
   const bool b_mn = p.wj == 1 && p.wi != 1;
   const int bn = tile_width(p.J, (p.n + kBM - 1) / kBM + p.groups - 1);
+  const bool pair = bn == 256 && p.I > 2 * kBK && p.n / p.groups >= 512 && p.n / 256 * ((p.J + 255) / 256) >= sm_count() / 2;
   CUtensorMap a, w;
   if (!tc::encode_bf16(&a, 2, p.a, p.I, p.n, p.lda, 1, 0, kBK, kBM)) return cudaErrorInvalidValue;
   if (b_mn ? !tc::encode_bf16(&w, 3, p.w, p.J, p.I, p.J, p.groups, (uint64_t)p.I * p.J, 64, kBK)
-           : !tc::encode_bf16(&w, 3, p.w, p.I, p.J, p.I, p.groups, (uint64_t)p.I * p.J, kBK, bn))
+           : !tc::encode_bf16(&w, 3, p.w, p.I, p.J, p.I, p.groups, (uint64_t)p.I * p.J, kBK, pair ? 128 : bn))
     return cudaErrorInvalidValue;
-  if (b_mn) return bn == 256 ? rows_tc<256, true>(a, w, p, s) : bn == 128 ? rows_tc<128, true>(a, w, p, s) : rows_tc<64, true>(a, w, p, s);
-  return bn == 256 ? rows_tc<256, false>(a, w, p, s) : bn == 128 ? rows_tc<128, false>(a, w, p, s) : rows_tc<64, false>(a, w, p, s);
+  if (pair) return b_mn ? rows_tc<256, true, 2>(a, w, p, s) : rows_tc<256, false, 2>(a, w, p, s);
+  if (b_mn)
+    return bn == 256 ? rows_tc<256, true, 1>(a, w, p, s) : bn == 128 ? rows_tc<128, true, 1>(a, w, p, s) : rows_tc<64, true, 1>(a, w, p, s);
+  return bn == 256 ? rows_tc<256, false, 1>(a, w, p, s) : bn == 128 ? rows_tc<128, false, 1>(a, w, p, s) : rows_tc<64, false, 1>(a, w, p, s);
 }
 
 // 8-bit x lands by byte copies whose rows lie K bytes apart: K has to be a multiple of 16 there.
@@ -628,17 +736,17 @@ bool linear_weights_fits_tc(const LinearWeights& p) {
 }
 
 cudaError_t launch_linear_weights_tc(const LinearWeights& p, cudaStream_t s) {
-  const int bn = tile_width(p.M, (p.n / p.chunk + p.groups) * ((p.K + kBM - 1) / kBM));
+  const long long chunks = p.n / p.chunk + p.groups;
+  const int bn = tile_width(p.M, chunks * ((p.K + kBM - 1) / kBM));
+  const bool pair = bn == 256 && p.K > kBM && chunks * ((p.K + 255) / 256) * ((p.M + 255) / 256) >= sm_count() / 2;
   CUtensorMap dy, x;
   if (!tc::encode_bf16(&dy, 2, p.dy, p.M, p.n, p.lddy, 1, 0, 64, kBK)) return cudaErrorInvalidValue;
   if (p.x.data == nullptr) {
     if (!tc::encode_u8(&x, p.x.codes, p.K, p.n, p.K, kBM, kBK)) return cudaErrorInvalidValue;
-    return bn == 256 ? weights_tc<256, true>(x, dy, p, s) : bn == 128 ? weights_tc<128, true>(x, dy, p, s)
-                                                                      : weights_tc<64, true>(x, dy, p, s);
+    return weights_tc<true>(x, dy, p, bn, pair, s);
   }
   if (!tc::encode_bf16(&x, 2, p.x.data, p.K, p.n, p.x.ld, 1, 0, 64, kBK)) return cudaErrorInvalidValue;
-  return bn == 256 ? weights_tc<256, false>(x, dy, p, s) : bn == 128 ? weights_tc<128, false>(x, dy, p, s)
-                                                                     : weights_tc<64, false>(x, dy, p, s);
+  return weights_tc<false>(x, dy, p, bn, pair, s);
 }
 
 }  // namespace mt
