@@ -348,7 +348,7 @@ int mt_group_linear_forward(const void* x, int64_t ldx, const void* w, const int
                             int32_t* status, mt_stream stream);
 
 /* Workspace bytes of mt_group_linear_backward (partial products of long groups). */
-size_t mt_group_linear_workspace_bytes(int64_t n, int32_t in_dim, int32_t out_dim);
+size_t mt_group_linear_workspace_bytes(int64_t n, int32_t groups, int32_t in_dim, int32_t out_dim);
 
 /* Its backward: dx_i = W_g^T dy_i and dW_g = sum over the group's rows of dy_i x_i^T.
  *  dy   row tensor [n, out_dim].

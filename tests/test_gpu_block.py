@@ -164,6 +164,22 @@ def test_linear_long_groups(dtype, k, m, sizes):
         near(dw, wdw, (max(sizes) + 16) * F * sdw, "dw")
 
 
+@pytest.mark.parametrize("k,m", [(256, 512), (512, 1024), (264, 272)])
+def test_linear_many_short_groups(k, m):
+    """More tiles than the SMs hold at once, most of them shorter than a stage of 64 rows: the short last stages of
+    several chunks are on their way together."""
+    sizes = [5, 70, 3, 64, 1, 130, 0, 63] * 12 + [700, 2000]
+    x, w, dy, off = linear_case(4, sizes, 2, 1, "bf16", k, m)
+    lin = mt.GroupedLinear(len(sizes), k, m)
+    p = mt.pack8(x)
+    for xx, xv in ((x, wide(x)), (p, R.unpack(p.codes.cpu().numpy(), p.exps.cpu().numpy()))):
+        dx, dw = lin.backward(dy, xx, w, off)
+        wdx, sdx, wdw, sdw = R.linear_backward(wide(dy), xv, wide(w), wide(off))
+        near(dx, wdx, 2.0 ** -8 * np.abs(wdx) + (m + 16) * F * sdx, "dx")
+        near(dw, wdw, (max(sizes) + 16) * F * sdw, "dw")
+    assert lin.error() == 0
+
+
 def test_linear_strided_rows_and_outputs():
     """Column slices of wider tensors as inputs and outputs, aligned and not; what lies beside them stays."""
     gen = torch.Generator(device=DEV).manual_seed(5)

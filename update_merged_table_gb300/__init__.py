@@ -105,7 +105,7 @@ ABI_FUNCTIONS = {
     "mt_pack8": (_I32, [_P, _I64, _I64, _C32, _I32, _P, _P, _P]),
     "mt_unpack8": (_I32, [_P, _P, _I64, _C32, _I32, _P, _I64, _P]),
     "mt_group_linear_forward": (_I32, [_P, _I64, _P, _P, _C32, _I64, _C32, _C32, _I32, _P, _I64, _P, _P]),
-    "mt_group_linear_workspace_bytes": (_SZ, [_I64, _C32, _C32]),
+    "mt_group_linear_workspace_bytes": (_SZ, [_I64, _C32, _C32, _C32]),
     "mt_group_linear_backward": (_I32, [_P, _I64, _P, _P, _P, _C32, _I64, _C32, _C32, _I32, _P, _I64, _P, _P, _P, _SZ,
                                         _P]),
     "mt_gated_norm_forward": (_I32, [_P, _P, _P, _P, _P, _P, _P]),

@@ -340,7 +340,8 @@ class GroupedLinear(_Handle):
                 elif tuple(dw.shape) != shape or dw.dtype != torch.float32 or not dw.is_contiguous() \
                         or dw.device != self.device:
                     raise ValueError(f"out_dw must be a contiguous float32 CUDA tensor {list(shape)}")
-                ws = self._workspace(s, self.lib.mt_group_linear_workspace_bytes(n, self.in_dim, self.out_dim))
+                ws = self._workspace(s, self.lib.mt_group_linear_workspace_bytes(n, self.num_groups, self.in_dim,
+                                                                                 self.out_dim))
                 ws_ptr, ws_len = ws.data_ptr(), ws.numel()
             # an empty batch has no dx rows to point at: only dw is asked for
             _check(self.lib.mt_group_linear_backward(
@@ -352,7 +353,8 @@ class GroupedLinear(_Handle):
     def reserve_workspace(self, n: int, stream=None):
         """Allocate, on this stream, the workspace a backward over n rows needs (before a CUDA graph capture)."""
         with _On(self.device, stream) as s:
-            self._workspace(s, self.lib.mt_group_linear_workspace_bytes(n, self.in_dim, self.out_dim))
+            self._workspace(s, self.lib.mt_group_linear_workspace_bytes(n, self.num_groups, self.in_dim,
+                                                                                 self.out_dim))
 
 
 @dataclasses.dataclass

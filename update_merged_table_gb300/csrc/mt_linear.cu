@@ -94,10 +94,12 @@ template <typename T>
 __global__ void __launch_bounds__(kThreadsL) k_linear_weights(const LinearWeights p) {
   extern __shared__ long long s_off[];
   __shared__ float s_a[kI][kT + 4], s_b[kI][kT + 4];
+  __shared__ int s_chunk;
   int* s_cum = reinterpret_cast<int*>(s_off + p.groups + 1);
   int* s_slot = s_cum + p.groups + 1;
   load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
-  count_tiles(s_off, p.groups, p.chunk, s_cum);
+  const int chunk = choose_chunk(p, s_off, &s_chunk);
+  count_tiles(s_off, p.groups, chunk, s_cum);
   count_slots(s_cum, p.groups, s_slot);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const T* DY = static_cast<const T*>(p.dy);
@@ -109,8 +111,8 @@ __global__ void __launch_bounds__(kThreadsL) k_linear_weights(const LinearWeight
     const int c = (int)(t / (mt * kt)), q0 = (int)(t - (long long)c * (mt * kt));
     const int m0 = q0 / kt * kT, k0 = (q0 - q0 / kt * kt) * kT;
     const int g = tile_group(s_cum, p.groups, c);
-    const long long first = s_off[g] + (long long)(c - s_cum[g]) * p.chunk;
-    const long long last = min(first + p.chunk, s_off[g + 1]);
+    const long long first = s_off[g] + (long long)(c - s_cum[g]) * chunk;
+    const long long last = min(first + chunk, s_off[g + 1]);
     float acc[4][4] = {};
     for (long long r0 = first; r0 < last; r0 += kI) {
 #pragma unroll
@@ -159,19 +161,21 @@ __global__ void __launch_bounds__(kThreadsL) k_linear_weights(const LinearWeight
 
 __global__ void __launch_bounds__(256) k_linear_sums(const LinearWeights p) {
   extern __shared__ long long s_off[];
+  __shared__ int s_chunk;
   int* s_cum = reinterpret_cast<int*>(s_off + p.groups + 1);
   int* s_slot = s_cum + p.groups + 1;
   load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
-  count_tiles(s_off, p.groups, p.chunk, s_cum);
+  count_tiles(s_off, p.groups, choose_chunk(p, s_off, &s_chunk), s_cum);
   count_slots(s_cum, p.groups, s_slot);
   const size_t size = (size_t)p.M * p.K;
-  for (int g = blockIdx.y; g < p.groups; g += gridDim.y) {
+  const bool four = size % 4 == 0 && ((uintptr_t)p.dw & 15) == 0;  // four values at once
+  const size_t i0 = (size_t)blockIdx.x * blockDim.x + threadIdx.x, step = (size_t)gridDim.x * blockDim.x;
+  for (int g = 0; g < p.groups; ++g) {
     const int c = s_cum[g + 1] - s_cum[g];
     if (c == 1) continue;  // written by its only chunk
     const float* part = p.part + (size_t)s_slot[g] * size;
     float* out = p.dw + (size_t)g * size;
-    const size_t i0 = (size_t)blockIdx.x * blockDim.x + threadIdx.x, step = (size_t)gridDim.x * blockDim.x;
-    if (size % 4 == 0 && ((uintptr_t)p.dw & 15) == 0) {  // four values at once, four chunks in flight
+    if (four) {
       for (size_t i = i0; i < size / 4; i += step) {
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
@@ -221,7 +225,7 @@ cudaError_t launch_linear_rows(LinearRows p, int dtype, cudaStream_t s) {
 cudaError_t launch_linear_weights(const LinearWeights& p, int dtype, cudaStream_t s) {
   if (p.n > 0 && dtype == MT_BF16 && linear_weights_fits_tc(p)) return launch_linear_weights_tc(p, s);
   if (p.n > 0) {
-    const long long tiles = (long long)((p.M + kT - 1) / kT) * ((p.K + kT - 1) / kT) * (p.n / p.chunk + p.groups);
+    const long long tiles = (long long)((p.M + kT - 1) / kT) * ((p.K + kT - 1) / kT) * p.chunks;
     const int grid = (int)std::min<long long>(tiles, (long long)sm_count() * 8);
     MT_LAUNCH("k_linear_weights", s);
     if (dtype == MT_F32) k_linear_weights<float><<<grid, kThreadsL, weights_smem(p.groups), s>>>(p);
@@ -233,23 +237,31 @@ cudaError_t launch_linear_weights(const LinearWeights& p, int dtype, cudaStream_
 cudaError_t launch_linear_sums(const LinearWeights& p, cudaStream_t s) {
   MT_LAUNCH("k_linear_sums", s);
   const long long size = (long long)p.M * p.K;
-  const dim3 grid((unsigned)std::min<long long>((size + 1023) / 1024, 1024), p.groups);
-  k_linear_sums<<<grid, 256, weights_smem(p.groups), s>>>(p);
+  k_linear_sums<<<grid_for((size + 3) / 4, 256, 8), 256, weights_smem(p.groups), s>>>(p);
   return cudaGetLastError();
 }
 
-// Rows per chunk of dW: enough chunks that the tiles fill the SMs twice, at most kMaxChunk rows (longer sums are
-// split, which also keeps their fp32 rounding short), at least kMinChunk.
-int chunk_of(int64_t n, int32_t k, int32_t m) {
-  const long long tiles = (long long)((m + 127) / 128) * ((k + 127) / 128);
-  const long long want = n * tiles / (2LL * sm_count());
-  const long long c = std::min<long long>(kMaxChunk, std::max<long long>(kMinChunk, want));
-  return (int)((c + 63) / 64 * 64);
+// How far dW's rows are split: into what makes about kRounds tiles per SM (per pair), and beyond one chunk per group into
+// no more than that.  More rounds even the work out better, but each chunk of a split group costs a partial product of
+// dW's size, written and read.
+constexpr int kRounds = 4;
+struct Split {
+  int chunks, slots;
+};
+Split split_of(int64_t n, int32_t groups, int32_t k, int32_t m) {
+  const long long tile = k > 128 && m > 128 ? 256 * 256 : 128 * 256;  // of the tensor-core forms: a pair's, or a block's
+  const long long tiles = ((long long)k * m + tile - 1) / tile;
+  const long long units = (long long)sm_count() * (128 * 256) / tile;
+  const long long want = kRounds * units / tiles, few = n / kMinChunk;  // a split leaves chunks of kMinChunk and more
+  Split s;
+  s.chunks = (int)std::max<long long>(want, groups + want / 2);
+  s.slots = (int)std::min<long long>(std::max<long long>(want, 2), 2 * few);
+  return s;
 }
 
-// Partial products: a group of more than one chunk has fewer than 2 len / chunk of them.
-size_t partial_bytes(int64_t n, int32_t k, int32_t m) {
-  return align_up((size_t)(2 * n / chunk_of(n, k, m)) * k * m * 4 + 256, 256);
+// Partial products of the split groups.
+size_t partial_bytes(int64_t n, int32_t groups, int32_t k, int32_t m) {
+  return align_up((size_t)split_of(n, groups, k, m).slots * k * m * 4 + 256, 256);
 }
 
 // 8-bit x whose rows do not lie a multiple of 16 bytes apart cannot be copied as it is: it is widened to bf16 rows in
@@ -288,11 +300,11 @@ int mt_group_linear_forward(const void* x, int64_t ldx, const void* w, const int
   return launch_linear_rows(p, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MT_OK : MT_ECUDA;
 }
 
-size_t mt_group_linear_workspace_bytes(int64_t n, int32_t in_dim, int32_t out_dim) {
+size_t mt_group_linear_workspace_bytes(int64_t n, int32_t groups, int32_t in_dim, int32_t out_dim) {
   using namespace mt;
-  if (n < 0 || n > 0x7FFFFFFF || in_dim < 1 || in_dim > MT_MAX_BLOCK_DIM || out_dim < 1 || out_dim > MT_MAX_BLOCK_DIM)
+  if (n < 0 || n > 0x7FFFFFFF || groups < 1 || groups > MT_MAX_GROUPS || in_dim < 1 || in_dim > MT_MAX_BLOCK_DIM || out_dim < 1 || out_dim > MT_MAX_BLOCK_DIM)
     return 0;
-  return partial_bytes(n, in_dim, out_dim) + (widened_first(in_dim) ? align_up((size_t)n * in_dim * 2, 256) : 0);
+  return partial_bytes(n, groups, in_dim, out_dim) + (widened_first(in_dim) ? align_up((size_t)n * in_dim * 2, 256) : 0);
 }
 
 int mt_group_linear_backward(const void* dy, int64_t lddy, const mt_rows* x, const void* w, const int64_t* offsets,
@@ -312,7 +324,7 @@ int mt_group_linear_backward(const void* dy, int64_t lddy, const mt_rows* x, con
     const bool packed = x->data == nullptr;
     if (n > 0 && (packed ? x->codes == nullptr || x->exps == nullptr : !rows_ok(x->data, x->ld, in_dim, dtype)))
       return MT_EINVAL;
-    if (ws == nullptr || !is_aligned(ws, 256) || ws_bytes < mt_group_linear_workspace_bytes(n, in_dim, out_dim))
+    if (ws == nullptr || !is_aligned(ws, 256) || ws_bytes < mt_group_linear_workspace_bytes(n, groups, in_dim, out_dim))
       return MT_ENOSPACE;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -346,12 +358,14 @@ int mt_group_linear_backward(const void* dy, int64_t lddy, const mt_rows* x, con
     p.x = *x;
     p.K = in_dim;
     p.M = out_dim;
-    p.chunk = chunk_of(n, in_dim, out_dim);
+    const Split split = split_of(n, groups, in_dim, out_dim);
+    p.chunks = split.chunks;
+    p.slots = split.slots;
     p.part = static_cast<float*>(ws);
     p.dw = dw;
     if (dtype == MT_BF16 && x->data == nullptr && widened_first(in_dim) && n > 0) {
       LinearWeights q = p;
-      q.x = Rows{static_cast<char*>(ws) + partial_bytes(n, in_dim, out_dim), in_dim, nullptr, nullptr};
+      q.x = Rows{static_cast<char*>(ws) + partial_bytes(n, groups, in_dim, out_dim), in_dim, nullptr, nullptr};
       if (linear_weights_fits_tc(q)) {
         const int rc8 = mt_unpack8(x->codes, x->exps, n, in_dim, dtype, q.x.data, in_dim, stream);
         if (rc8 != MT_OK) return rc8;

@@ -5,8 +5,7 @@
 
 namespace mt {
 
-constexpr int kMaxChunk = 4096;  // most rows one partial product of dW sums over
-constexpr int kMinChunk = 256;
+constexpr int kMinChunk = 256;  // fewest rows that a group is split into
 
 // C[row, j] = sum over i < I of A[row, i] * w[g * wg + i * wi + j * wj], for the rows of group g; rows in no group
 // become zeros.
@@ -34,12 +33,43 @@ struct LinearWeights {
   long long lddy;
   Rows x;
   int K, M;
-  int chunk;      // rows per chunk
+  int chunks;     // most chunks the rows are split into (at least the groups)
+  int slots;      // most of them that belong to groups of several
   float* part;    // [slots][M][K]: partial products of the groups that have several chunks
   float* dw;      // [groups][M][K]
 };
 
 inline size_t weights_smem(int groups) { return (size_t)(groups + 1) * (8 + 4 + 4); }
+
+// The rows of a chunk: the least multiple of 64 (and at least kMinChunk) with which the groups' rows make no more than
+// p.chunks chunks and need no more than p.slots partial products.  The kernels give every SM (or pair) the same number
+// of chunk tiles, so the chunks' number has to fit a whole number of rounds however ragged the groups are; equal chunks
+// then make equal rounds.  Every thread calls it.
+__device__ __forceinline__ int choose_chunk(const LinearWeights& p, const long long* s_off, int* s_value) {
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x, G = p.groups;
+    int longest = 0;
+    for (int i = lane; i < G; i += 32) longest = max(longest, (int)((s_off[i + 1] - s_off[i] + 63) / 64));
+    longest = __reduce_max_sync(kFull, longest);
+    int lo = kMinChunk / 64, hi = max(lo, longest);  // in units of 64 rows; hi always fits (one chunk per group)
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      int count = 0, split = 0;
+      for (int i = lane; i < G; i += 32) {
+        const int c = ((int)((s_off[i + 1] - s_off[i] + 63) / 64) + mid - 1) / mid;
+        count += c;
+        split += c > 1 ? c : 0;
+      }
+      count = __reduce_add_sync(kFull, count);
+      split = __reduce_add_sync(kFull, split);
+      if (count <= p.chunks && split <= p.slots) hi = mid;
+      else lo = mid + 1;
+    }
+    if (lane == 0) *s_value = lo * 64;
+  }
+  __syncthreads();
+  return *s_value;
+}
 
 // s_slot[g]: partial products of the groups before g that have more than one chunk; after count_tiles, by every thread.
 __device__ __forceinline__ void count_slots(const int* s_cum, int G, int* s_slot) {

@@ -96,7 +96,10 @@ struct Ring {
 
 struct Barriers {
   uint64_t full[8], empty[8];    // a stage's copies have landed; its products are done
-  uint64_t ready[8];             // a stage's operands are as the product wants them (widened, or zeroed past the end)
+  uint64_t ready[8];             // a stage's 8-bit operand has been widened
+  // The second block of a pair, in a chunk's last, short stage: its copies have landed; their rows past the end are
+  // zeroed.  One per stage, as the others: the short stages of several small chunks can be on their way at once.
+  uint64_t tail_full[8], tail_ready[8];
   uint64_t acc_full[2], acc_empty[2];  // an accumulator is finished; it has been read out
   uint64_t done;                 // every product issued is done
   uint32_t tmem;
@@ -115,6 +118,8 @@ __device__ __forceinline__ uint32_t tc_begin(Barriers& b, int ready_count, int r
       tc::mbar_init(&b.full[i], 1);
       tc::mbar_init(&b.empty[i], 1);
       tc::mbar_init(&b.ready[i], ready_count);
+      tc::mbar_init(&b.tail_full[i], 1);
+      tc::mbar_init(&b.tail_ready[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&b.acc_full[i], 1);
@@ -271,11 +276,11 @@ k_linear_rows_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constan
       uint32_t acc_phase = 0;
       bool ok = true;
       for (long long t = t0; t < total && ok; t += tstep) {
-        ok = tc::mbar_wait<CG == 2>(&bar.acc_empty[acc], acc_phase ^ 1);
+        ok = tc::mbar_wait(&bar.acc_empty[acc], acc_phase ^ 1);
         if (!ok) break;
         tc::fence_after();
         for (int k = 0; k < steps; ++k) {
-          ok = tc::mbar_wait<CG == 2>(&bar.full[s.stage], s.phase);
+          ok = tc::mbar_wait(&bar.full[s.stage], s.phase);
           if (!ok) break;
           tc::fence_after();
           const uint32_t a = tc::smem_addr(ring + s.stage * R::kStage), b = a + R::kStageA;
@@ -312,7 +317,7 @@ k_linear_rows_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constan
       const int g = tile_group(s_cum, p.groups, rt);
       const long long r0 = s_off[g] + (long long)(rt - s_cum[g]) * kRows + rank * kBM + quad * 32;
       const int rows = (int)min((long long)32, s_off[g + 1] - r0);  // <= 0: none of this warp's rows is in the group
-      ok = __all_sync(kFull, tc::mbar_wait<CG == 2>(&bar.acc_full[acc], acc_phase));
+      ok = __all_sync(kFull, tc::mbar_wait(&bar.acc_full[acc], acc_phase));
       if (!ok) break;
       tc::fence_after();
       const uint32_t from = tmem + acc * BN + ((uint32_t)(quad * 32) << 16);
@@ -391,10 +396,12 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
   long long* s_off = reinterpret_cast<long long*>(ring + R::kStages * R::kStage);
   int* s_cum = reinterpret_cast<int*>(s_off + p.groups + 1);
   int* s_slot = s_cum + p.groups + 1;
+  __shared__ int s_chunk;
   load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
-  count_tiles(s_off, p.groups, p.chunk, s_cum);
+  const int chunk = choose_chunk(p, s_off, &s_chunk);
+  count_tiles(s_off, p.groups, chunk, s_cum);
   count_slots(s_cum, p.groups, s_slot);
-  const uint32_t tmem = tc_begin<BN, CG>(bar, X8 ? kReadWarps / 2 * CG : 1, kReadWarps);
+  const uint32_t tmem = tc_begin<BN, CG>(bar, kReadWarps / 2 * CG, kReadWarps);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = blockIdx.x % CG;
   const int mt = (p.M + BN - 1) / BN, tiles = (p.K + kRowsD - 1) / kRowsD * mt;
@@ -413,8 +420,8 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     x.k0 = q / mt * kRowsD + rank * kBM;
     x.m0 = (q - q / mt * mt) * BN;
     x.g = tile_group(s_cum, p.groups, x.c);
-    x.first = s_off[x.g] + (long long)(x.c - s_cum[x.g]) * p.chunk;
-    x.last = min(x.first + p.chunk, s_off[x.g + 1]);
+    x.first = s_off[x.g] + (long long)(x.c - s_cum[x.g]) * chunk;
+    x.last = min(x.first + chunk, s_off[x.g + 1]);
     x.stages = (int)((x.last - x.first + kBK - 1) / kBK);
     return x;
   };
@@ -433,17 +440,28 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
             ok = tc::mbar_wait(&bar.empty[s.stage], s.phase ^ 1);
             if (!ok) break;
             uint8_t* st = ring + s.stage * R::kStage;
-            tc::mbar_expect(&bar.full[s.stage], bytes);
-            if constexpr (X8) {
-              tc::tma_load_2d(st, &map_x, &bar.full[s.stage], x.k0, (int)r);
+            const int dy0 = x.m0 + rank * kColsB;
+            if (CG == 2 && !X8 && x.last - r >= kBK) {  // both blocks' copies count on the first block's barrier
+              const uint32_t full = tc::of_leader(&bar.full[s.stage]);
+              if (rank == 0) tc::mbar_expect(&bar.full[s.stage], 2 * bytes);
+#pragma unroll
+              for (int c = 0; c < kBM / 64; ++c) tc::tma_load_2d_pair(st + c * 8192, &map_x, full, x.k0 + c * 64, (int)r);
+#pragma unroll
+              for (int c = 0; c < kColsB / 64; ++c)
+                tc::tma_load_2d_pair(st + R::kStageA + c * 8192, &map_dy, full, dy0 + c * 64, (int)r);
             } else {
+              uint64_t* full = CG == 2 && !X8 && rank != 0 ? &bar.tail_full[s.stage] : &bar.full[s.stage];
+              tc::mbar_expect(full, bytes);
+              if constexpr (X8) {
+                tc::tma_load_2d(st, &map_x, full, x.k0, (int)r);
+              } else {
 #pragma unroll
-              for (int c = 0; c < kBM / 64; ++c)
-                tc::tma_load_2d(st + c * 8192, &map_x, &bar.full[s.stage], x.k0 + c * 64, (int)r);
+                for (int c = 0; c < kBM / 64; ++c) tc::tma_load_2d(st + c * 8192, &map_x, full, x.k0 + c * 64, (int)r);
+              }
+#pragma unroll
+              for (int c = 0; c < kColsB / 64; ++c)
+                tc::tma_load_2d(st + R::kStageA + c * 8192, &map_dy, full, dy0 + c * 64, (int)r);
             }
-#pragma unroll
-            for (int c = 0; c < kColsB / 64; ++c)
-              tc::tma_load_2d(st + R::kStageA + c * 8192, &map_dy, &bar.full[s.stage], x.m0 + rank * kColsB + c * 64, (int)r);
             ++issued;
             s.next<R::kStages>();
           }
@@ -451,41 +469,52 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         ok = ok && all_released<R::kStages>(bar, s, issued);
         if (!ok) {
           latch_status(p.status, MT_ECUDA);
-          drain<R::kStages>(bar, s, issued);
+          if (X8 || rank == 0) drain<R::kStages>(bar, s, issued);
         }
       }
     }
-    // Plain x: warp 1 of each block sees its copies land and zeroes the rows past the chunk's end, which belong to
-    // others, in both operands, so that nothing of them (an infinity or NaN too) reaches the sum; the second block of a
-    // pair then tells the first.  8-bit x: the widening warps do all that.
+    // Plain x: the rows past the chunk's end in its last stage belong to others; warp 1 zeroes them in both operands, so
+    // that nothing of them (an infinity or NaN too) reaches the sum.  The second block of a pair does so for its own
+    // copies, which count on a barrier of its own in that stage, and tells the first.  8-bit x: the widening warps do it.
     if (warp == 1) {
       constexpr uint32_t instr = tc::instr_bf16(kRowsD, BN, true, true);
       Slot s;
       int acc = 0;
-      uint32_t acc_phase = 0;
+      uint32_t acc_phase = 0, tail_phase = 0;  // tail_phase: a bit per stage
       bool ok = true;
-      for (long long t = X8 && rank != 0 ? total : t0; t < total && ok; t += tstep) {
+      if (rank != 0) {
+        uint32_t seq = 0;  // stages before this tile
+        for (long long t = t0; t < total && ok && !X8; t += tstep) {
+          const Tile x = tile_of(t);
+          const int left = (int)(x.last - x.first) & (kBK - 1);
+          seq += x.stages;
+          if (left == 0) continue;
+          const uint32_t stage = (seq - 1) % R::kStages;
+          ok = __all_sync(kFull, tc::mbar_wait(&bar.tail_full[stage], tail_phase >> stage & 1));
+          if (!ok) break;
+          tail_phase ^= 1u << stage;
+          zero_rows(ring + stage * R::kStage, (kBM + kColsB) / 64, left, lane);
+          if (lane == 0) arrive<CG>(&bar.tail_ready[stage]);
+        }
+      }
+      for (long long t = t0; rank == 0 && t < total && ok; t += tstep) {
         const Tile x = tile_of(t);
         for (int k = 0; k < x.stages; ++k) {
-          if (k % kPromote == 0 && rank == 0) {
-            ok = __all_sync(kFull, tc::mbar_wait<CG == 2>(&bar.acc_empty[acc], acc_phase ^ 1));
+          if (k % kPromote == 0) {
+            ok = __all_sync(kFull, tc::mbar_wait(&bar.acc_empty[acc], acc_phase ^ 1));
             if (!ok) break;
           }
           uint8_t* st = ring + s.stage * R::kStage;
-          if constexpr (!X8) {
-            ok = __all_sync(kFull, tc::mbar_wait(&bar.full[s.stage], s.phase));
-            if (!ok) break;
-            const int left = (int)min((long long)kBK, x.last - x.first - (long long)k * kBK);
-            if (left < kBK) zero_rows(st, (kBM + kColsB) / 64, left, lane);
-            if (rank != 0) {
-              if (lane == 0) arrive<CG>(&bar.ready[s.stage]);
-              s.next<R::kStages>();
-              continue;
+          ok = __all_sync(kFull, tc::mbar_wait(X8 ? &bar.ready[s.stage] : &bar.full[s.stage], s.phase));
+          if (!ok) break;
+          const int left = (int)min((long long)kBK, x.last - x.first - (long long)k * kBK);
+          if (!X8 && left < kBK) {
+            zero_rows(st, (kBM + kColsB) / 64, left, lane);
+            if constexpr (CG == 2) {
+              ok = __all_sync(kFull, tc::mbar_wait(&bar.tail_ready[s.stage], tail_phase >> s.stage & 1));
+              if (!ok) break;
+              tail_phase ^= 1u << s.stage;
             }
-          }
-          if (X8 || CG == 2) {
-            ok = __all_sync(kFull, tc::mbar_wait<CG == 2>(&bar.ready[s.stage], s.phase));
-            if (!ok) break;
           }
           tc::fence_after();
           const bool closes = k % kPromote == kPromote - 1 || k + 1 == x.stages;
@@ -527,7 +556,7 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     float sum[kCols];
 
     auto read_out = [&]() {
-      ok = __all_sync(kFull, tc::mbar_wait<CG == 2>(&bar.acc_full[acc], acc_phase));
+      ok = __all_sync(kFull, tc::mbar_wait(&bar.acc_full[acc], acc_phase));
       if (!ok) return;
       tc::fence_after();
 #pragma unroll
@@ -691,7 +720,7 @@ cudaError_t weights_tc(const CUtensorMap& x, const CUtensorMap& dy, const Linear
     if (e != cudaSuccess) return e;
     if (a.numRegs < kRegsLaunch) return cudaErrorInvalidValue;
   }
-  const long long tiles = (p.n / p.chunk + p.groups) * ((p.K + kBM * CG - 1) / (kBM * CG)) * ((p.M + BN - 1) / BN);
+  const long long tiles = (long long)p.chunks * ((p.K + kBM * CG - 1) / (kBM * CG)) * ((p.M + BN - 1) / BN);
   MT_LAUNCH("k_linear_weights_tc", s);
   return launch_tc(k_linear_weights_tc<BN, X8, CG>, tc_grid(tiles, CG), kWarpsW * 32,
                    1024 + Ring<BN, CG>::kStages * Ring<BN, CG>::kStage + weights_smem(p.groups), CG, s, x, dy, p);
@@ -736,7 +765,7 @@ bool linear_weights_fits_tc(const LinearWeights& p) {
 }
 
 cudaError_t launch_linear_weights_tc(const LinearWeights& p, cudaStream_t s) {
-  const long long chunks = p.n / p.chunk + p.groups;
+  const long long chunks = p.chunks;
   const int bn = tile_width(p.M, chunks * ((p.K + kBM - 1) / kBM));
   const bool pair = bn == 256 && p.K > kBM && chunks * ((p.K + 255) / 256) * ((p.M + 255) / 256) >= sm_count() / 2;
   CUtensorMap dy, x;

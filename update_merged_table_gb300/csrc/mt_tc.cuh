@@ -29,30 +29,18 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 
 // Waits until the barrier's phase of this parity is over; false when it is not after kWaitTries tries of up to about a
 // millisecond each (the hardware suspends the thread during a try), so no wait is endless.
-// CLUSTER: arrivals of the paired block count too.
 constexpr int kWaitTries = 2000;
-template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   const uint32_t a = smem_addr(bar);
   for (int i = 0; i < kWaitTries; ++i) {
     uint32_t done;
-    if constexpr (CLUSTER) {
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(done)
-          : "r"(a), "r"(parity), "r"(1000000u)
-          : "memory");
-    } else {
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(done)
-          : "r"(a), "r"(parity), "r"(1000000u)
-          : "memory");
-    }
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(a), "r"(parity), "r"(1000000u)
+        : "memory");
     if (done) return true;
   }
   return false;
