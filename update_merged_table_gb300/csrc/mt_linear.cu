@@ -94,11 +94,11 @@ template <typename T>
 __global__ void __launch_bounds__(kThreadsL) k_linear_weights(const LinearWeights p) {
   extern __shared__ long long s_off[];
   __shared__ float s_a[kI][kT + 4], s_b[kI][kT + 4];
-  __shared__ int s_chunk;
+  __shared__ ChunkChoice s_choice;
   int* s_cum = reinterpret_cast<int*>(s_off + p.groups + 1);
   int* s_slot = s_cum + p.groups + 1;
   load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
-  const int chunk = choose_chunk(p, s_off, &s_chunk);
+  const int chunk = choose_chunk(p, s_off, s_choice);
   count_tiles(s_off, p.groups, chunk, s_cum);
   count_slots(s_cum, p.groups, s_slot);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
@@ -159,33 +159,51 @@ __global__ void __launch_bounds__(kThreadsL) k_linear_weights(const LinearWeight
   }
 }
 
-__global__ void __launch_bounds__(256) k_linear_sums(const LinearWeights p) {
+constexpr int kSumSlices = 8;  // warps of a block
+__global__ void __launch_bounds__(32 * kSumSlices) k_linear_sums(const LinearWeights p) {
   extern __shared__ long long s_off[];
-  __shared__ int s_chunk;
+  __shared__ float4 s_sum[kSumSlices][32];
   int* s_cum = reinterpret_cast<int*>(s_off + p.groups + 1);
   int* s_slot = s_cum + p.groups + 1;
   load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
-  count_tiles(s_off, p.groups, choose_chunk(p, s_off, &s_chunk), s_cum);
+  count_tiles(s_off, p.groups, *p.chosen, s_cum);
   count_slots(s_cum, p.groups, s_slot);
   const size_t size = (size_t)p.M * p.K;
   const bool four = size % 4 == 0 && ((uintptr_t)p.dw & 15) == 0;  // four values at once
   const size_t i0 = (size_t)blockIdx.x * blockDim.x + threadIdx.x, step = (size_t)gridDim.x * blockDim.x;
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  auto add4 = [](float4& s, const float4& v) {
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+  };
   for (int g = 0; g < p.groups; ++g) {
     const int c = s_cum[g + 1] - s_cum[g];
     if (c == 1) continue;  // written by its only chunk
     const float* part = p.part + (size_t)s_slot[g] * size;
     float* out = p.dw + (size_t)g * size;
-    if (four) {
+    if (four && c >= 2 * kSumSlices) {  // many chunks: the block's warps take every kSumSlices-th, joined in their order
+      for (size_t b = blockIdx.x; b * 32 < size / 4; b += gridDim.x) {
+        const size_t i = b * 32 + lane;
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (i < size / 4) {
+#pragma unroll 4
+          for (int k = slice; k < c; k += kSumSlices) add4(s, __ldg(reinterpret_cast<const float4*>(part + (size_t)k * size) + i));
+        }
+        s_sum[slice][lane] = s;
+        __syncthreads();
+        if (slice == 0 && i < size / 4) {
+          for (int k = 1; k < kSumSlices; ++k) add4(s, s_sum[k][lane]);
+          reinterpret_cast<float4*>(out)[i] = s;
+        }
+        __syncthreads();
+      }
+    } else if (four) {
       for (size_t i = i0; i < size / 4; i += step) {
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-        for (int k = 0; k < c; ++k) {
-          const float4 v = __ldg(reinterpret_cast<const float4*>(part + (size_t)k * size) + i);
-          s.x += v.x;
-          s.y += v.y;
-          s.z += v.z;
-          s.w += v.w;
-        }
+        for (int k = 0; k < c; ++k) add4(s, __ldg(reinterpret_cast<const float4*>(part + (size_t)k * size) + i));
         reinterpret_cast<float4*>(out)[i] = s;
       }
     } else {
@@ -200,6 +218,18 @@ __global__ void __launch_bounds__(256) k_linear_sums(const LinearWeights p) {
 }
 
 size_t rows_smem(int groups) { return (size_t)(groups + 1) * (8 + 4); }
+
+// Partial products of dW there is room for: as many as give every block (pair) kRounds tiles, if the rows allow any split
+// (a split leaves chunks of kMinChunk rows and more, so a group of one more than that makes two).
+constexpr int kRounds = 4;
+int slots_of(int64_t n, int32_t groups, int32_t k, int32_t m) {
+  const Cut c = cut_of(n, groups, k, m);
+  const long long want = std::max<long long>(2, (long long)kRounds * c.units / c.tiles);
+  return (int)std::min<long long>(want, 2 * (n / kMinChunk));
+}
+size_t partial_bytes(int64_t n, int32_t groups, int32_t k, int32_t m) {
+  return align_up((size_t)slots_of(n, groups, k, m) * k * m * 4 + 256, 256);
+}
 
 // The shapes, offsets and types that both directions share.
 int linear_check(const int64_t* offsets, int32_t groups, int64_t n, int32_t k, int32_t m, int dtype,
@@ -222,11 +252,18 @@ cudaError_t launch_linear_rows(LinearRows p, int dtype, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_linear_weights(const LinearWeights& p, int dtype, cudaStream_t s) {
-  if (p.n > 0 && dtype == MT_BF16 && linear_weights_fits_tc(p)) return launch_linear_weights_tc(p, s);
+// The rest of p is filled in here: the sums go by it too.
+cudaError_t launch_linear_weights(LinearWeights& p, int dtype, cudaStream_t s) {
+  Cut cut = cut_of(p.n, p.groups, p.K, p.M);
+  const bool tc = dtype == MT_BF16 && linear_weights_fits_tc(p);
+  p.slots = slots_of(p.n, p.groups, p.K, p.M);
+  // a partial product is written and read once, at about 4 TB/s; 64 rows of a tile take 0.42 us (the fp32 pipes: 13 us)
+  p.slot_cost = (float)((double)p.K * p.M * 8 / 4e6 / (tc ? 0.42 : 13.0));
+  p.tiles = tc ? cut.tiles : ((p.M + kT - 1) / kT) * ((p.K + kT - 1) / kT);
+  p.units = tc ? cut.units : sm_count() * 8;
+  if (p.n > 0 && tc) return launch_linear_weights_tc(p, cut, s);
   if (p.n > 0) {
-    const long long tiles = (long long)((p.M + kT - 1) / kT) * ((p.K + kT - 1) / kT) * p.chunks;
-    const int grid = (int)std::min<long long>(tiles, (long long)sm_count() * 8);
+    const int grid = p.units;
     MT_LAUNCH("k_linear_weights", s);
     if (dtype == MT_F32) k_linear_weights<float><<<grid, kThreadsL, weights_smem(p.groups), s>>>(p);
     else k_linear_weights<__nv_bfloat16><<<grid, kThreadsL, weights_smem(p.groups), s>>>(p);
@@ -235,33 +272,11 @@ cudaError_t launch_linear_weights(const LinearWeights& p, int dtype, cudaStream_
 }
 
 cudaError_t launch_linear_sums(const LinearWeights& p, cudaStream_t s) {
+  if (p.n == 0) return cudaMemsetAsync(p.dw, 0, (size_t)p.groups * p.M * p.K * 4, s);
   MT_LAUNCH("k_linear_sums", s);
   const long long size = (long long)p.M * p.K;
-  k_linear_sums<<<grid_for((size + 3) / 4, 256, 8), 256, weights_smem(p.groups), s>>>(p);
+  k_linear_sums<<<grid_for((size + 3) / 4 * kSumSlices, 256, 4), 256, weights_smem(p.groups), s>>>(p);
   return cudaGetLastError();
-}
-
-// How far dW's rows are split: into what makes about kRounds tiles per SM (per pair), and beyond one chunk per group into
-// no more than that.  More rounds even the work out better, but each chunk of a split group costs a partial product of
-// dW's size, written and read.
-constexpr int kRounds = 4;
-struct Split {
-  int chunks, slots;
-};
-Split split_of(int64_t n, int32_t groups, int32_t k, int32_t m) {
-  const long long tile = k > 128 && m > 128 ? 256 * 256 : 128 * 256;  // of the tensor-core forms: a pair's, or a block's
-  const long long tiles = ((long long)k * m + tile - 1) / tile;
-  const long long units = (long long)sm_count() * (128 * 256) / tile;
-  const long long want = kRounds * units / tiles, few = n / kMinChunk;  // a split leaves chunks of kMinChunk and more
-  Split s;
-  s.chunks = (int)std::max<long long>(want, groups + want / 2);
-  s.slots = (int)std::min<long long>(std::max<long long>(want, 2), 2 * few);
-  return s;
-}
-
-// Partial products of the split groups.
-size_t partial_bytes(int64_t n, int32_t groups, int32_t k, int32_t m) {
-  return align_up((size_t)split_of(n, groups, k, m).slots * k * m * 4 + 256, 256);
 }
 
 // 8-bit x whose rows do not lie a multiple of 16 bytes apart cannot be copied as it is: it is widened to bf16 rows in
@@ -358,10 +373,8 @@ int mt_group_linear_backward(const void* dy, int64_t lddy, const mt_rows* x, con
     p.x = *x;
     p.K = in_dim;
     p.M = out_dim;
-    const Split split = split_of(n, groups, in_dim, out_dim);
-    p.chunks = split.chunks;
-    p.slots = split.slots;
-    p.part = static_cast<float*>(ws);
+    p.chosen = static_cast<int*>(ws);
+    p.part = static_cast<float*>(ws) + 64;
     p.dw = dw;
     if (dtype == MT_BF16 && x->data == nullptr && widened_first(in_dim) && n > 0) {
       LinearWeights q = p;

@@ -5,7 +5,8 @@
 
 namespace mt {
 
-constexpr int kMinChunk = 256;  // fewest rows that a group is split into
+constexpr int kMinChunk = 256;  // fewest rows of a chunk that a group is split into
+constexpr int kSplits = 32;     // ways of splitting that choose_chunk weighs
 
 // C[row, j] = sum over i < I of A[row, i] * w[g * wg + i * wi + j * wj], for the rows of group g; rows in no group
 // become zeros.
@@ -33,42 +34,86 @@ struct LinearWeights {
   long long lddy;
   Rows x;
   int K, M;
-  int chunks;     // most chunks the rows are split into (at least the groups)
-  int slots;      // most of them that belong to groups of several
+  int tiles;        // tiles of dW (of the kernel that runs)
+  int units;        // blocks (pairs) that walk over them
+  float slot_cost;  // what a partial product costs, in units of 64 rows of a tile
+  int slots;        // partial products there is room for
+  int* chosen;      // [1] workspace: the rows of a chunk, as the products chose them, for their sums
   float* part;    // [slots][M][K]: partial products of the groups that have several chunks
   float* dw;      // [groups][M][K]
 };
 
 inline size_t weights_smem(int groups) { return (size_t)(groups + 1) * (8 + 4 + 4); }
 
-// The rows of a chunk: the least multiple of 64 (and at least kMinChunk) with which the groups' rows make no more than
-// p.chunks chunks and need no more than p.slots partial products.  The kernels give every SM (or pair) the same number
-// of chunk tiles, so the chunks' number has to fit a whole number of rounds however ragged the groups are; equal chunks
-// then make equal rounds.  Every thread calls it.
-__device__ __forceinline__ int choose_chunk(const LinearWeights& p, const long long* s_off, int* s_value) {
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x, G = p.groups;
-    int longest = 0;
-    for (int i = lane; i < G; i += 32) longest = max(longest, (int)((s_off[i + 1] - s_off[i] + 63) / 64));
-    longest = __reduce_max_sync(kFull, longest);
-    int lo = kMinChunk / 64, hi = max(lo, longest);  // in units of 64 rows; hi always fits (one chunk per group)
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      int count = 0, split = 0;
-      for (int i = lane; i < G; i += 32) {
-        const int c = ((int)((s_off[i + 1] - s_off[i] + 63) / 64) + mid - 1) / mid;
-        count += c;
-        split += c > 1 ? c : 0;
-      }
-      count = __reduce_add_sync(kFull, count);
-      split = __reduce_add_sync(kFull, split);
-      if (count <= p.chunks && split <= p.slots) hi = mid;
-      else lo = mid + 1;
+// The rows of a chunk.  A group may be split into chunks whose products are summed afterwards, so that every block (pair)
+// gets about the same work however ragged the groups are; a partial product costs a write and a read of dW's size.  What
+// is weighed is the longest group in 1, 2, ... kSplits equal chunks, by the time of the last block in units of 64 rows:
+// rounds of tiles of that many rows, or what a block has on average plus one tile where the rounds differ in length,
+// and per round kRoundCost for the tile's last read-out and store (measured: 6 us against 0.42 us per 64 rows of a
+// 256 x 256 tile).  Every thread calls it, after load_offsets.
+constexpr float kRoundCost = 14.0f, kSumsCost = 12.0f;
+struct ChunkChoice {
+  int count[kSplits], split[kSplits];  // chunks; those of groups that have several
+  int longest, rows, chunk;            // in units of 64 rows, and in rows
+};
+__device__ __forceinline__ int choose_chunk(const LinearWeights& p, const long long* s_off, ChunkChoice& c) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  auto units_of = [&](int g) { return (int)((s_off[g + 1] - s_off[g] + 63) / 64); };
+  if (warp == 0) {
+    int longest = 0, rows = 0;
+    for (int g = lane; g < p.groups; g += 32) {
+      const int u = units_of(g);
+      longest = max(longest, u);
+      rows += u;
     }
-    if (lane == 0) *s_value = lo * 64;
+    longest = __reduce_max_sync(kFull, longest);
+    rows = __reduce_add_sync(kFull, rows);
+    c.count[lane] = c.split[lane] = 0;
+    if (lane == 0) {
+      c.longest = longest;
+      c.rows = rows;
+    }
   }
   __syncthreads();
-  return *s_value;
+  const int s = max(kMinChunk / 64, (c.longest + lane) / (lane + 1));  // this lane's chunk
+  const float inv = 1.0f / (float)s;
+  int count = 0, split = 0;
+  for (int g = warp; g < p.groups; g += warps) {
+    const int u = units_of(g);
+    int k = (int)((float)u * inv);  // within one of u / s
+    k += (k + 1) * s <= u;
+    k -= k * s > u;
+    k += k * s < u;  // rounded up
+    count += k;
+    split += k > 1 ? k : 0;
+  }
+  atomicAdd(&c.count[lane], count);  // integers: any order gives the same sum
+  atomicAdd(&c.split[lane], split);
+  __syncthreads();
+  if (warp == 0) {
+    const float rounds = ceilf((float)c.count[lane] * (float)p.tiles / (float)p.units);
+    const float mean = (float)c.rows * (float)p.tiles / (float)p.units;
+    const int sp = c.split[lane];
+    float cost = fmaxf(mean, fminf(rounds * (float)s, mean + (float)s)) + rounds * kRoundCost + (float)sp * p.slot_cost +
+                 (sp > 0 ? kSumsCost : 0.0f);
+    if (sp > p.slots) cost = 3.0e38f;  // lane 0 splits nothing: it always has room
+    int best = lane;
+    for (int o = 16; o > 0; o >>= 1) {  // the cheapest, of equals the one that splits least
+      const float oc = __shfl_xor_sync(kFull, cost, o);
+      const int ob = __shfl_xor_sync(kFull, best, o);
+      if (oc < cost || (oc == cost && ob < best)) {
+        cost = oc;
+        best = ob;
+      }
+    }
+    const int chosen = __shfl_sync(kFull, s, best) * 64;
+    if (lane == 0) {
+      c.chunk = chosen;
+      if (blockIdx.x == 0) *p.chosen = chosen;
+    }
+  }
+  __syncthreads();
+  return c.chunk;
 }
 
 // s_slot[g]: partial products of the groups before g that have more than one chunk; after count_tiles, by every thread.
@@ -108,10 +153,18 @@ __device__ __forceinline__ void zero_outside(const long long* s_off, int G, long
   }
 }
 
+// How a dW of this shape is cut into tiles, and over how many blocks (pairs) they are dealt.
+struct Cut {
+  int bn;        // columns of dy in a tile (rows of dW)
+  bool pair;     // tiles of 256 columns of x by pairs of blocks, else of 128
+  int tiles, units;
+};
+Cut cut_of(int64_t n, int32_t groups, int32_t k, int32_t m);
+
 // The tensor-core forms (mt_linear_tc.cu): bf16, widths and strides in multiples of 8, rows on 16 bytes.
 bool linear_rows_fits_tc(const LinearRows& p);
 cudaError_t launch_linear_rows_tc(const LinearRows& p, cudaStream_t s);
 bool linear_weights_fits_tc(const LinearWeights& p);
-cudaError_t launch_linear_weights_tc(const LinearWeights& p, cudaStream_t s);
+cudaError_t launch_linear_weights_tc(const LinearWeights& p, const Cut& cut, cudaStream_t s);
 
 }  // namespace mt

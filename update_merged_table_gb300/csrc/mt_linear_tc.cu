@@ -396,9 +396,9 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
   long long* s_off = reinterpret_cast<long long*>(ring + R::kStages * R::kStage);
   int* s_cum = reinterpret_cast<int*>(s_off + p.groups + 1);
   int* s_slot = s_cum + p.groups + 1;
-  __shared__ int s_chunk;
+  __shared__ ChunkChoice s_choice;
   load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
-  const int chunk = choose_chunk(p, s_off, &s_chunk);
+  const int chunk = choose_chunk(p, s_off, s_choice);
   count_tiles(s_off, p.groups, chunk, s_cum);
   count_slots(s_cum, p.groups, s_slot);
   const uint32_t tmem = tc_begin<BN, CG>(bar, kReadWarps / 2 * CG, kReadWarps);
@@ -720,9 +720,8 @@ cudaError_t weights_tc(const CUtensorMap& x, const CUtensorMap& dy, const Linear
     if (e != cudaSuccess) return e;
     if (a.numRegs < kRegsLaunch) return cudaErrorInvalidValue;
   }
-  const long long tiles = (long long)p.chunks * ((p.K + kBM * CG - 1) / (kBM * CG)) * ((p.M + BN - 1) / BN);
   MT_LAUNCH("k_linear_weights_tc", s);
-  return launch_tc(k_linear_weights_tc<BN, X8, CG>, tc_grid(tiles, CG), kWarpsW * 32,
+  return launch_tc(k_linear_weights_tc<BN, X8, CG>, p.units * CG, kWarpsW * 32,
                    1024 + Ring<BN, CG>::kStages * Ring<BN, CG>::kStage + weights_smem(p.groups), CG, s, x, dy, p);
 }
 
@@ -764,18 +763,27 @@ bool linear_weights_fits_tc(const LinearWeights& p) {
   return p.x.ld % 8 == 0 && is_aligned(p.x.data, 16);
 }
 
-cudaError_t launch_linear_weights_tc(const LinearWeights& p, cudaStream_t s) {
-  const long long chunks = p.chunks;
-  const int bn = tile_width(p.M, chunks * ((p.K + kBM - 1) / kBM));
-  const bool pair = bn == 256 && p.K > kBM && chunks * ((p.K + 255) / 256) * ((p.M + 255) / 256) >= sm_count() / 2;
+Cut cut_of(int64_t n, int32_t groups, int32_t k, int32_t m) {
+  // the tiles' width goes by the chunks that the rows may make
+  const long long chunks = groups + n / 4096;
+  Cut c;
+  c.bn = tile_width(m, chunks * ((k + kBM - 1) / kBM));
+  c.pair = c.bn == 256 && k > kBM && n / 512 * ((k + 255) / 256) * ((m + 255) / 256) >= sm_count() / 2;
+  const int across = c.pair ? 2 * kBM : kBM;
+  c.tiles = ((k + across - 1) / across) * ((m + c.bn - 1) / c.bn);
+  c.units = std::max(1, sm_count() / (c.pair ? 2 : 1));
+  return c;
+}
+
+cudaError_t launch_linear_weights_tc(const LinearWeights& p, const Cut& cut, cudaStream_t s) {
   CUtensorMap dy, x;
   if (!tc::encode_bf16(&dy, 2, p.dy, p.M, p.n, p.lddy, 1, 0, 64, kBK)) return cudaErrorInvalidValue;
   if (p.x.data == nullptr) {
     if (!tc::encode_u8(&x, p.x.codes, p.K, p.n, p.K, kBM, kBK)) return cudaErrorInvalidValue;
-    return weights_tc<true>(x, dy, p, bn, pair, s);
+    return weights_tc<true>(x, dy, p, cut.bn, cut.pair, s);
   }
   if (!tc::encode_bf16(&x, 2, p.x.data, p.K, p.n, p.x.ld, 1, 0, 64, kBK)) return cudaErrorInvalidValue;
-  return weights_tc<false>(x, dy, p, bn, pair, s);
+  return weights_tc<false>(x, dy, p, cut.bn, cut.pair, s);
 }
 
 }  // namespace mt
