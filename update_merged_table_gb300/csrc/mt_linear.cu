@@ -5,9 +5,9 @@
 //
 // This file holds the entry points and the kernels that take every type, width,
 // stride and alignment on the fp32 pipes:
-//  k_linear_rows     forward and dx: a 64 x 64 tile of one group's rows per
+//  k_linear_rows     forward and dx: a 128 x 64 tile of one group's rows per
 //                    block, both operands staged in shared memory as fp32.
-//  k_linear_weights  dW: a 64 x 64 tile of one group's dW over one chunk of its
+//  k_linear_weights  dW: a 128 x 64 tile of one group's dW over one chunk of its
 //                    rows; x may come in 8 bits (its values are read as they
 //                    stand, exact in fp32).
 //  k_linear_sums     dW of the groups whose rows were split over several chunks,
@@ -20,69 +20,127 @@
 namespace mt {
 namespace {
 
-constexpr int kT = 64;    // tile edge
-constexpr int kI = 16;    // contraction step
-constexpr int kThreadsL = 256;
+constexpr int kTM = 128, kTN = 64;  // a tile: rows (of C, or of dW) by columns
+constexpr int kI = 16;              // contraction per step
+constexpr int kThreadsL = 256;      // a thread holds 8 x 4 values of the tile
+
+// Both operands of a step in shared memory, contraction first.
+struct Steps {
+  float a[kI][kTM + 4], b[kI][kTN + 4];
+};
+
+// acc += a^T b over one step.  A thread's eight rows are four pairs (one instruction for two products); its four columns
+// come one by one.
+__device__ __forceinline__ void multiply(const Steps& s, int tx, int ty, f32x2 (&acc)[4][4]) {
+#pragma unroll
+  for (int i = 0; i < kI; ++i) {
+    const ulonglong2 a0 = *reinterpret_cast<const ulonglong2*>(&s.a[i][ty * 8]);
+    const ulonglong2 a1 = *reinterpret_cast<const ulonglong2*>(&s.a[i][ty * 8 + 4]);
+    const float4 b = *reinterpret_cast<const float4*>(&s.b[i][tx * 4]);
+    const f32x2 a[4] = {a0.x, a0.y, a1.x, a1.y}, c[4] = {both(b.x), both(b.y), both(b.z), both(b.w)};
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[u][v] = fma2(a[u], c[v], acc[u][v]);
+  }
+}
+
+// Four neighbouring elements of a row (zeros from `left` on); VEC: one access.
+template <typename T, bool VEC>
+__device__ __forceinline__ float4 load4(const T* p, int left) {
+  float f[4];
+  if (VEC) {
+    if (left <= 0) return make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if constexpr (sizeof(T) == 4) return __ldg(reinterpret_cast<const float4*>(p));
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                       __uint_as_float(w.y & 0xFFFF0000u));
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] = j < left ? to_f<T>(__ldg(p + j)) : 0.0f;
+  return make_float4(f[0], f[1], f[2], f[3]);
+}
 
 // ---- forward and dx ----------------------------------------------------------------
 //
-// C[row, j] = sum over i < I of A[row, i] * W_g(i, j), with W_g(i, j) = w[g * wg + i * wi + j * wj].
-template <typename T>
+// C[row, j] = sum over i < I of A[row, i] * W_g(i, j), with W_g(i, j) = w[g * wg + i * wi + j * wj]; one of wi and wj is
+// 1.  The next step's operands are on their way to registers while one is multiplied.  VEC: widths and strides are
+// multiples of four elements and everything starts on four.
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreadsL) k_linear_rows(const LinearRows p) {
   extern __shared__ long long s_off[];
-  __shared__ float s_a[kI][kT + 4], s_b[kI][kT + 4];
+  __shared__ __align__(16) Steps s;
   int* s_cum = reinterpret_cast<int*>(s_off + p.groups + 1);
   load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
-  count_tiles(s_off, p.groups, kT, s_cum);
+  count_tiles(s_off, p.groups, kTM, s_cum);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const T* A = static_cast<const T*>(p.a);
   T* C = static_cast<T*>(p.c);
+  const bool across = p.wi != 1;  // W's rows run along j (else along i)
 
   zero_outside<T>(s_off, p.groups, p.n, C, p.ldc, p.J, kThreadsL, tid);
 
   const long long total = (long long)s_cum[p.groups] * p.jtiles;
   for (long long t = blockIdx.x; t < total; t += gridDim.x) {
-    const int rt = (int)(t / p.jtiles), j0 = (int)(t - (long long)rt * p.jtiles) * kT;
+    const int rt = (int)(t / p.jtiles), j0 = (int)(t - (long long)rt * p.jtiles) * kTN;
     const int g = tile_group(s_cum, p.groups, rt);
-    const long long r0 = s_off[g] + (long long)(rt - s_cum[g]) * kT;
-    const int rows = (int)min((long long)kT, s_off[g + 1] - r0);
+    const long long r0 = s_off[g] + (long long)(rt - s_cum[g]) * kTM;
+    const int rows = (int)min((long long)kTM, s_off[g + 1] - r0);
     const T* W = static_cast<const T*>(p.w) + (size_t)g * p.wg;
-    float acc[4][4] = {};
+    // this thread's four-element pieces: two of A (rows ar and ar + 64), one of W
+    const int ar = tid >> 2, ai = (tid & 3) * 4;
+    const int wr = across ? tid >> 4 : tid >> 2, wc = across ? (tid & 15) * 4 : (tid & 3) * 4;  // W: row i or j, place in it
+    float4 ra[2], rw;
+    auto fetch = [&](int i0) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        ra[q] = load4<T, VEC>(A + row_offset(r0 + ar + q * 64, p.lda) + i0 + ai, ar + q * 64 < rows ? p.I - i0 - ai : 0);
+      if (across) rw = load4<T, VEC>(W + (size_t)(i0 + wr) * p.wi + j0 + wc, i0 + wr < p.I ? p.J - j0 - wc : 0);
+      else rw = load4<T, VEC>(W + (size_t)(j0 + wr) * p.wj + i0 + wc, j0 + wr < p.J ? p.I - i0 - wc : 0);
+    };
+    f32x2 acc[4][4] = {};
+    fetch(0);
     for (int i0 = 0; i0 < p.I; i0 += kI) {
 #pragma unroll
-      for (int q = tid; q < kT * kI; q += kThreadsL) {
-        const int i = q % kI, r = q / kI;
-        s_a[i][r] = r < rows && i0 + i < p.I ? to_f<T>(A[(r0 + r) * p.lda + i0 + i]) : 0.0f;
+      for (int q = 0; q < 2; ++q) {
+        s.a[ai][ar + q * 64] = ra[q].x;
+        s.a[ai + 1][ar + q * 64] = ra[q].y;
+        s.a[ai + 2][ar + q * 64] = ra[q].z;
+        s.a[ai + 3][ar + q * 64] = ra[q].w;
       }
-#pragma unroll
-      for (int q = tid; q < kT * kI; q += kThreadsL) {
-        const int i = p.wi == 1 ? q % kI : q / kT, j = p.wi == 1 ? q / kI : q % kT;
-        s_b[i][j] = i0 + i < p.I && j0 + j < p.J ? to_f<T>(W[(size_t)(i0 + i) * p.wi + (size_t)(j0 + j) * p.wj]) : 0.0f;
+      if (across) {
+        *reinterpret_cast<float4*>(&s.b[wr][wc]) = rw;
+      } else {
+        s.b[wc][wr] = rw.x;
+        s.b[wc + 1][wr] = rw.y;
+        s.b[wc + 2][wr] = rw.z;
+        s.b[wc + 3][wr] = rw.w;
       }
       __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kI; ++i) {
-        float a[4], b[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          a[q] = s_a[i][ty * 4 + q];
-          b[q] = s_b[i][tx * 4 + q];
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) acc[u][v] = fmaf(a[u], b[v], acc[u][v]);
-      }
+      if (i0 + kI < p.I) fetch(i0 + kI);
+      multiply(s, tx, ty, acc);
       __syncthreads();
     }
+    const int col = j0 + tx * 4;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int r = ty * 4 + u;
-      if (r >= rows) continue;
+      const float2 f[4] = {upk(acc[u][0]), upk(acc[u][1]), upk(acc[u][2]), upk(acc[u][3])};
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int j = j0 + tx * 4 + v;
-        if (j < p.J) C[(r0 + r) * p.ldc + j] = from_f<T>(acc[u][v]);
+      for (int h = 0; h < 2; ++h) {
+        const int r = ty * 8 + u * 2 + h;
+        if (r >= rows) continue;
+        T* c = C + row_offset(r0 + r, p.ldc) + col;
+        const float4 v = h ? make_float4(f[0].y, f[1].y, f[2].y, f[3].y) : make_float4(f[0].x, f[1].x, f[2].x, f[3].x);
+        if (VEC && sizeof(T) == 4) {
+          if (col < p.J) *reinterpret_cast<float4*>(c) = v;
+        } else if (VEC) {
+          if (col < p.J) *reinterpret_cast<uint2*>(c) = make_uint2(bf16x2_of(v.x, v.y), bf16x2_of(v.z, v.w));
+        } else {
+          const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (col + j < p.J) c[j] = from_f<T>(x[j]);
+        }
       }
     }
   }
@@ -90,10 +148,10 @@ __global__ void __launch_bounds__(kThreadsL) k_linear_rows(const LinearRows p) {
 
 // ---- dW ---------------------------------------------------------------------------
 
-template <typename T>
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreadsL) k_linear_weights(const LinearWeights p) {
   extern __shared__ long long s_off[];
-  __shared__ float s_a[kI][kT + 4], s_b[kI][kT + 4];
+  __shared__ __align__(16) Steps s;
   __shared__ ChunkChoice s_choice;
   int* s_cum = reinterpret_cast<int*>(s_off + p.groups + 1);
   int* s_slot = s_cum + p.groups + 1;
@@ -105,57 +163,75 @@ __global__ void __launch_bounds__(kThreadsL) k_linear_weights(const LinearWeight
   const T* DY = static_cast<const T*>(p.dy);
   const T* X = static_cast<const T*>(p.x.data);
   const int nb = (p.K + kPackBlock - 1) / kPackBlock;
-  const int mt = (p.M + kT - 1) / kT, kt = (p.K + kT - 1) / kT;
-  const long long total = (long long)s_cum[p.groups] * mt * kt;
+  const bool is_wide = ((uintptr_t)p.dw & 15) == 0;  // (partial products always are)
+  const int kt = (p.K + kTN - 1) / kTN, tiles = (p.M + kTM - 1) / kTM * kt;
+  const long long total = (long long)s_cum[p.groups] * tiles;
   for (long long t = blockIdx.x; t < total; t += gridDim.x) {
-    const int c = (int)(t / (mt * kt)), q0 = (int)(t - (long long)c * (mt * kt));
-    const int m0 = q0 / kt * kT, k0 = (q0 - q0 / kt * kt) * kT;
+    const int c = (int)(t / tiles), q0 = (int)(t - (long long)c * tiles);
+    const int m0 = q0 / kt * kTM, k0 = (q0 - q0 / kt * kt) * kTN;
     const int g = tile_group(s_cum, p.groups, c);
     const long long first = s_off[g] + (long long)(c - s_cum[g]) * chunk;
     const long long last = min(first + chunk, s_off[g + 1]);
-    float acc[4][4] = {};
+    // this thread's four-element pieces: two of dy (rows yr and yr + 8), one of x
+    const int yr = tid >> 5, yc = (tid & 31) * 4, xr = tid >> 4, xc = (tid & 15) * 4;
+    float4 ry[2], rx;
+    auto fetch = [&](long long r0) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const long long r = r0 + yr + q * 8;
+        ry[q] = load4<T, VEC>(DY + row_offset(r, p.lddy) + m0 + yc, r < last ? p.M - m0 - yc : 0);
+      }
+      const long long r = r0 + xr;
+      const int k = k0 + xc, left = r < last ? p.K - k : 0;
+      if (X != nullptr) {
+        rx = load4<T, VEC>(X + row_offset(r, p.x.ld) + k, left);
+      } else {
+        float f[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)  // four columns never straddle a block of 32
+          f[j] = j < left ? (float)p.x.codes[row_offset(r, p.K) + k + j] : 0.0f;
+        const float scale = left > 0 ? pack_scale(p.x.exps[row_offset(r, nb) + k / kPackBlock]) : 0.0f;
+        rx = make_float4(f[0] * scale, f[1] * scale, f[2] * scale, f[3] * scale);
+        if (left < 4) {  // a block that is not finite makes its columns NaN, not the columns past K
+          if (left < 1) rx.x = 0.0f;
+          if (left < 2) rx.y = 0.0f;
+          if (left < 3) rx.z = 0.0f;
+          rx.w = 0.0f;
+        }
+      }
+    };
+    f32x2 acc[4][4] = {};
+    fetch(first);
     for (long long r0 = first; r0 < last; r0 += kI) {
-#pragma unroll
-      for (int q = tid; q < kT * kI; q += kThreadsL) {
-        const int r = q / kT, m = q % kT;
-        s_a[r][m] = r0 + r < last && m0 + m < p.M ? to_f<T>(DY[(r0 + r) * p.lddy + m0 + m]) : 0.0f;
-      }
-#pragma unroll
-      for (int q = tid; q < kT * kI; q += kThreadsL) {
-        const int r = q / kT, k = q % kT;
-        float v = 0.0f;
-        if (r0 + r < last && k0 + k < p.K) {
-          if (X != nullptr) v = to_f<T>(X[(r0 + r) * p.x.ld + k0 + k]);
-          else
-            v = (float)p.x.codes[(r0 + r) * p.K + k0 + k] *
-                pack_scale(p.x.exps[(r0 + r) * nb + (k0 + k) / kPackBlock]);
-        }
-        s_b[r][k] = v;
-      }
+      *reinterpret_cast<float4*>(&s.a[yr][yc]) = ry[0];
+      *reinterpret_cast<float4*>(&s.a[yr + 8][yc]) = ry[1];
+      *reinterpret_cast<float4*>(&s.b[xr][xc]) = rx;
       __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kI; ++i) {
-        float a[4], b[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          a[q] = s_a[i][ty * 4 + q];
-          b[q] = s_b[i][tx * 4 + q];
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) acc[u][v] = fmaf(a[u], b[v], acc[u][v]);
-      }
+      if (r0 + kI < last) fetch(r0 + kI);
+      multiply(s, tx, ty, acc);
       __syncthreads();
     }
     float* out = weights_out(p, s_cum, s_slot, g, c);
+    const int k = k0 + tx * 4;
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < 4; ++u) {
+      const float2 f[4] = {upk(acc[u][0]), upk(acc[u][1]), upk(acc[u][2]), upk(acc[u][3])};
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int m = m0 + ty * 4 + u, k = k0 + tx * 4 + v;
-        if (m < p.M && k < p.K) out[(size_t)m * p.K + k] = acc[u][v];
+      for (int h = 0; h < 2; ++h) {
+        const int m = m0 + ty * 8 + u * 2 + h;
+        if (m >= p.M) continue;
+        float* o = out + (size_t)m * p.K + k;
+        const float4 v = h ? make_float4(f[0].y, f[1].y, f[2].y, f[3].y) : make_float4(f[0].x, f[1].x, f[2].x, f[3].x);
+        if (VEC && is_wide) {
+          if (k < p.K) *reinterpret_cast<float4*>(o) = v;
+        } else {
+          const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (k + j < p.K) o[j] = x[j];
+        }
       }
+    }
   }
 }
 
@@ -243,12 +319,20 @@ int linear_check(const int64_t* offsets, int32_t groups, int64_t n, int32_t k, i
 
 cudaError_t launch_linear_rows(LinearRows p, int dtype, cudaStream_t s) {
   if (dtype == MT_BF16 && linear_rows_fits_tc(p)) return launch_linear_rows_tc(p, s);
-  p.jtiles = (p.J + kT - 1) / kT;
-  const long long tiles = ((p.n + kT - 1) / kT + p.groups) * p.jtiles;
-  const int grid = (int)std::min<long long>(tiles, (long long)sm_count() * 8);
+  p.jtiles = (p.J + kTN - 1) / kTN;
+  const long long tiles = (p.n / kTM + p.groups) * p.jtiles;
+  const int grid = (int)std::min<long long>(tiles, (long long)sm_count() * 4);
+  const size_t four = 4 * elem_bytes(dtype);
+  const bool vec = p.I % 4 == 0 && p.J % 4 == 0 && p.lda % 4 == 0 && p.ldc % 4 == 0 && is_aligned(p.a, four) &&
+                   is_aligned(p.w, four) && is_aligned(p.c, four);
   MT_LAUNCH("k_linear_rows", s);
-  if (dtype == MT_F32) k_linear_rows<float><<<grid, kThreadsL, rows_smem(p.groups), s>>>(p);
-  else k_linear_rows<__nv_bfloat16><<<grid, kThreadsL, rows_smem(p.groups), s>>>(p);
+  if (dtype == MT_F32) {
+    if (vec) k_linear_rows<float, true><<<grid, kThreadsL, rows_smem(p.groups), s>>>(p);
+    else k_linear_rows<float, false><<<grid, kThreadsL, rows_smem(p.groups), s>>>(p);
+  } else {
+    if (vec) k_linear_rows<__nv_bfloat16, true><<<grid, kThreadsL, rows_smem(p.groups), s>>>(p);
+    else k_linear_rows<__nv_bfloat16, false><<<grid, kThreadsL, rows_smem(p.groups), s>>>(p);
+  }
   return cudaGetLastError();
 }
 
@@ -257,16 +341,24 @@ cudaError_t launch_linear_weights(LinearWeights& p, int dtype, cudaStream_t s) {
   Cut cut = cut_of(p.n, p.groups, p.K, p.M);
   const bool tc = dtype == MT_BF16 && linear_weights_fits_tc(p);
   p.slots = slots_of(p.n, p.groups, p.K, p.M);
-  // a partial product is written and read once, at about 4 TB/s; 64 rows of a tile take 0.42 us (the fp32 pipes: 13 us)
-  p.slot_cost = (float)((double)p.K * p.M * 8 / 4e6 / (tc ? 0.42 : 13.0));
-  p.tiles = tc ? cut.tiles : ((p.M + kT - 1) / kT) * ((p.K + kT - 1) / kT);
-  p.units = tc ? cut.units : sm_count() * 8;
+  // a partial product is written and read once, at about 4 TB/s; 64 rows of a tile take 0.42 us (the fp32 pipes: 3 us)
+  p.slot_cost = (float)((double)p.K * p.M * 8 / 4e6 / (tc ? 0.42 : 3.0));
+  p.tiles = tc ? cut.tiles : ((p.M + kTM - 1) / kTM) * ((p.K + kTN - 1) / kTN);
+  p.units = tc ? cut.units : sm_count() * 4;
   if (p.n > 0 && tc) return launch_linear_weights_tc(p, cut, s);
   if (p.n > 0) {
     const int grid = p.units;
     MT_LAUNCH("k_linear_weights", s);
-    if (dtype == MT_F32) k_linear_weights<float><<<grid, kThreadsL, weights_smem(p.groups), s>>>(p);
-    else k_linear_weights<__nv_bfloat16><<<grid, kThreadsL, weights_smem(p.groups), s>>>(p);
+    const size_t four = 4 * elem_bytes(dtype);
+    const bool vec = p.K % 4 == 0 && p.M % 4 == 0 && p.lddy % 4 == 0 && is_aligned(p.dy, four) &&
+                     (p.x.data == nullptr || (p.x.ld % 4 == 0 && is_aligned(p.x.data, four)));
+    if (dtype == MT_F32) {
+      if (vec) k_linear_weights<float, true><<<grid, kThreadsL, weights_smem(p.groups), s>>>(p);
+      else k_linear_weights<float, false><<<grid, kThreadsL, weights_smem(p.groups), s>>>(p);
+    } else {
+      if (vec) k_linear_weights<__nv_bfloat16, true><<<grid, kThreadsL, weights_smem(p.groups), s>>>(p);
+      else k_linear_weights<__nv_bfloat16, false><<<grid, kThreadsL, weights_smem(p.groups), s>>>(p);
+    }
   }
   return cudaGetLastError();
 }
