@@ -13,13 +13,15 @@ streams, each with its own workspace.
 """
 from __future__ import annotations
 
-import ctypes
 import dataclasses
+import importlib.util
+import ctypes
+import os
 import threading
 
 import torch
 
-from . import MT_BF16, MT_EINVAL, MT_F32, MTError, _check, load_library
+from . import LIB_PATH, MT_BF16, MT_EINVAL, MT_F32, MTError, load_library
 
 __all__ = ["Packed8", "pack8", "unpack8", "GroupedLinear", "GatedNorm", "NormParams", "NormForward", "NormGrads"]
 
@@ -29,97 +31,53 @@ PACK_BLOCK = 32
 _KINDS = {"rms": 0, "layer": 1}
 _GATES = {"none": 0, "linear": 1, "sigmoid": 2, "silu": 3}
 _DTYPES = {"f32": MT_F32, "bf16": MT_BF16}
-
-
-class _Rows(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64), ("codes", ctypes.c_void_p),
-                ("exps", ctypes.c_void_p)]
-
-
-class _GatedNorm(ctypes.Structure):
-    _fields_ = [("n", ctypes.c_int64), ("dim", ctypes.c_int32), ("groups", ctypes.c_int32),
-                ("dtype", ctypes.c_int32), ("kind", ctypes.c_int32), ("gate", ctypes.c_int32),
-                ("eps", ctypes.c_float), ("offsets", ctypes.c_void_p), ("status", ctypes.c_void_p),
-                ("post_weight", ctypes.c_void_p), ("post_bias", ctypes.c_void_p), ("scale", ctypes.c_void_p),
-                ("pre_weight", ctypes.c_void_p), ("pre_bias", ctypes.c_void_p)]
-
-
 _TORCH = {"f32": torch.float32, "bf16": torch.bfloat16}
 _CODES = {torch.float32: MT_F32, torch.bfloat16: MT_BF16}
 _current_device = torch.cuda.current_device
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _dtype_code(t):
-    code = _CODES.get(t)
-    if code is None:
-        raise TypeError("rows must be float32 or bfloat16")
-    return code
+def _load_native():
+    """The module that checks and marshals a call in one native step (built beside libmt.so)."""
+    lib = load_library()
+    path = os.path.join(os.path.dirname(LIB_PATH), "_mt_block.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"the Python module is not built: {path} is missing (run update_merged_table_gb300.build_lib.build())")
+    spec = importlib.util.spec_from_file_location("_mt_block", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    names = ("mt_pack8", "mt_unpack8", "mt_group_linear_forward", "mt_group_linear_backward", "mt_gated_norm_forward",
+             "mt_gated_norm_backward")
+    mod.init(*(ctypes.cast(getattr(lib, k), ctypes.c_void_p).value for k in names), MTError)
+    return mod
 
 
-def _rows_2d(t, what: str, width: int, n: int, dtype, device) -> int:
-    """The row stride of a row tensor: a CUDA tensor [n, width] of this dtype whose columns are contiguous and whose
-    rows do not overlap."""
-    try:
-        shape, (ld, step) = t.shape, t.stride()
-    except (AttributeError, ValueError):
-        raise (ValueError if torch.is_tensor(t) else TypeError)(f"{what} must be a 2-D CUDA tensor") from None
-    if shape[0] == n and shape[1] == width and step == 1 and ld >= width and t.dtype is dtype and t.device == device:
-        return ld
-    if t.dtype != dtype:
-        raise TypeError(f"{what} must be {dtype}")
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, not on {device}")
-    if tuple(shape) != (n, width):
-        raise ValueError(f"{what} must be [{n}, {width}], not {list(shape)}")
-    if width > 1 and step != 1:
-        raise ValueError(f"the columns of {what} must be contiguous")
-    if n <= 1:
-        return max(width, ld)
-    if ld < width:
-        raise ValueError(f"the rows of {what} overlap")
-    return ld
-
-
-def _count(t, what: str) -> int:
-    """Rows of a tensor that may be a row tensor (the rest is checked by _rows_2d)."""
-    if not torch.is_tensor(t):
-        raise TypeError(f"{what} must be a CUDA tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{what} must be a 2-D CUDA tensor")
-    return t.shape[0]
-
-
-def _cuda(t, what: str):
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
-    return t.device
+_native = _load_native()
 
 
 class _On:
-    """The stream a call runs on: its device made current, and torch allocating on it."""
+    """The stream a call runs on made current (and its device), so that torch allocates on it too."""
 
-    __slots__ = ("ctx", "index")
+    __slots__ = ("ctx",)
 
     def __init__(self, device, stream):
-        self.index = device.index
-        if stream is not None:
-            if stream.device.index != self.index:
-                raise ValueError(f"the stream is on {stream.device}, not on {device}")
-            self.ctx = torch.cuda.stream(stream)
-        elif _current_device() != self.index:
-            self.ctx = torch.cuda.device(device)
-        else:
-            self.ctx = None
+        if stream.device.index != device.index:
+            raise ValueError(f"the stream is on {stream.device}, not on {device}")
+        self.ctx = torch.cuda.stream(stream)
 
     def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return _raw_stream(self.index)
+        self.ctx.__enter__()
 
     def __exit__(self, *a):
-        if self.ctx is not None:
-            self.ctx.__exit__(*a)
+        self.ctx.__exit__(*a)
+
+
+def _on(device, stream, f, *args):
+    """f(*args) on the given stream, or on the current one."""
+    if stream is None:
+        return f(*args)
+    with _On(device, stream):
+        return f(*args)
 
 
 class Packed8:
@@ -152,56 +110,33 @@ class Packed8:
         return self.codes.numel() + self.exps.numel()
 
 
-def _new_packed(n: int, d: int, device) -> Packed8:
+def _packed(codes, exps) -> Packed8:
     p = Packed8.__new__(Packed8)
-    p.codes = torch.empty((n, d), dtype=torch.int8, device=device)
-    p.exps = torch.empty((n, -(-d // PACK_BLOCK)), dtype=torch.uint8, device=device)
+    p.codes, p.exps = codes, exps
     return p
-
-
-def _width_ok(d: int, what: str):
-    if not 1 <= d <= MAX_BLOCK_DIM:
-        raise ValueError(f"{what} must have 1 to {MAX_BLOCK_DIM} columns")
 
 
 def pack8(x, out: Packed8 | None = None, stream=None) -> Packed8:
     """The 8-bit form of the rows x [n, d] (float32 or bfloat16; rows may be strided)."""
-    n = _count(x, "x")
-    d, device = x.shape[1], _cuda(x, "x")
-    _width_ok(d, "x")
-    dt = _dtype_code(x.dtype)
-    ld = _rows_2d(x, "x", d, n, x.dtype, device)
-    with _On(device, stream) as s:
-        if out is None:
-            out = _new_packed(n, d, device)
-        elif out.shape != x.shape or out.device != device:
-            raise ValueError("out has another shape or device")
-        _check(load_library().mt_pack8(x.data_ptr(), ld, n, d, dt, out.codes.data_ptr(), out.exps.data_ptr(), s),
-               "mt_pack8")
-    return out
+    c, e = (None, None) if out is None else (out.codes, out.exps)
+    c, e = _native.pack8(x, c, e) if stream is None else _on(x.device, stream, _native.pack8, x, c, e)
+    return _packed(c, e) if out is None else out
 
 
 def unpack8(p: Packed8, dtype=None, out=None, stream=None):
     """The values p stands for, as rows of `dtype` (bfloat16 by default, which holds them exactly)."""
-    n, d = p.codes.shape
-    _width_ok(d, "p")
-    device = p.codes.device
-    if out is not None:
-        if dtype is not None and out.dtype != dtype:
-            raise TypeError("out has another dtype")
-        dtype = out.dtype
-    elif dtype is None:
-        dtype = torch.bfloat16
-    dt = _dtype_code(dtype)
-    with _On(device, stream) as s:
-        ld = d
-        if out is None:
-            out = torch.empty((n, d), dtype=dtype, device=device)
-        else:
-            ld = _rows_2d(out, "out", d, n, dtype, device)
-        _check(load_library().mt_unpack8(p.codes.data_ptr(), p.exps.data_ptr(), n, d, dt, out.data_ptr(), ld, s),
-               "mt_unpack8")
-    return out
+    if dtype is None:
+        dtype = torch.bfloat16 if out is None else out.dtype
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError("rows must be float32 or bfloat16")
+    if stream is None:
+        return _native.unpack8(p.codes, p.exps, code, out)
+    return _on(p.device, stream, _native.unpack8, p.codes, p.exps, code, out)
+
+
+def _plain_or_packed(t):
+    return (t.codes, t.exps) if isinstance(t, Packed8) else t
 
 
 # Status words of the handles: one zeroed buffer per device, a word (16 bytes apart) to each handle, so that making a
@@ -221,6 +156,12 @@ def _status_word(device):
     return buf[4 * used: 4 * used + 1]
 
 
+def _rows_of(t, what: str) -> int:
+    if not torch.is_tensor(t):
+        raise TypeError(f"{what} must be a CUDA tensor")
+    return t.shape[0] if t.dim() == 2 else 0  # anything but rows is refused by the call
+
+
 class _Handle:
     """What the block operators keep: their device, a status word and a workspace per stream."""
 
@@ -233,7 +174,9 @@ class _Handle:
         self._status_ptr = self._status.data_ptr()
         self._ws = {}
 
-    def _workspace(self, stream: int, nbytes: int):
+    def _workspace(self, nbytes: int):
+        """The workspace of the current stream."""
+        stream = _raw_stream(self.device.index)
         buf = self._ws.get(stream)
         if buf is None or buf.numel() < nbytes:
             if torch.cuda.is_current_stream_capturing():
@@ -243,12 +186,6 @@ class _Handle:
             buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
             self._ws[stream] = buf
         return buf
-
-    def _offsets(self, offsets, groups: int):
-        if not torch.is_tensor(offsets) or offsets.dtype is not torch.int64 or offsets.device != self.device \
-                or offsets.shape != (groups + 1,) or not offsets.is_contiguous():
-            raise TypeError(f"offsets must be a contiguous int64 CUDA tensor [{groups + 1}] on {self.device}")
-        return offsets.data_ptr()
 
     def error(self, clear: bool = False) -> int:
         """First error a call found on the device (MT_EINVAL: bad offsets), 0 if none; waits for the device."""
@@ -274,87 +211,33 @@ class GroupedLinear(_Handle):
         self.num_groups, self.in_dim, self.out_dim = num_groups, in_dim, out_dim
         self.dtype = dtype
         self.torch_dtype = _TORCH[dtype]
-        self._dt = _DTYPES[dtype]
-        self._w_shape = (num_groups, out_dim, in_dim)
-
-    def _weight(self, w):
-        if w.shape != self._w_shape or w.dtype is not self.torch_dtype or w.device != self.device \
-                or not w.is_contiguous():
-            raise ValueError(f"weight must be a contiguous {self.torch_dtype} CUDA tensor "
-                             f"[{self.num_groups}, {self.out_dim}, {self.in_dim}]")
-        return w.data_ptr()
+        self._cfg = (num_groups, in_dim, out_dim, _DTYPES[dtype], self.device.index, self._status_ptr)
 
     def forward(self, x, weight, offsets, out=None, stream=None):
         """y [n, out_dim] of x [n, in_dim], weight [num_groups, out_dim, in_dim] and offsets int64 CUDA
         [num_groups + 1]; rows in no group give zeros."""
-        n = _count(x, "x")
-        ldx = _rows_2d(x, "x", self.in_dim, n, self.torch_dtype, self.device)
-        w, off = self._weight(weight), self._offsets(offsets, self.num_groups)
-        with _On(self.device, stream) as s:
-            if out is None:
-                out = torch.empty((n, self.out_dim), dtype=self.torch_dtype, device=self.device)
-                ldy = self.out_dim
-            else:
-                ldy = _rows_2d(out, "out", self.out_dim, n, self.torch_dtype, self.device)
-            _check(self.lib.mt_group_linear_forward(x.data_ptr(), ldx, w, off, self.num_groups, n, self.in_dim,
-                                                    self.out_dim, self._dt, out.data_ptr(), ldy, self._status_ptr, s),
-                   "mt_group_linear_forward")
-        return out
+        if stream is None:
+            return _native.linear_forward(*self._cfg, x, weight, offsets, out)
+        return _on(self.device, stream, _native.linear_forward, *self._cfg, x, weight, offsets, out)
 
     def backward(self, dy, x, weight, offsets, want_dx: bool = True, want_dw: bool = True, out_dx=None, out_dw=None,
                  stream=None):
         """(dx [n, in_dim], dw fp32 [num_groups, out_dim, in_dim]) of dy [n, out_dim]; x: the forward's input, plain
         or ``Packed8`` (None without want_dw)."""
-        n = _count(dy, "dy")
-        lddy = _rows_2d(dy, "dy", self.out_dim, n, self.torch_dtype, self.device)
         if not want_dx and not want_dw:
             raise ValueError("nothing to compute")
-        w = self._weight(weight) if want_dx else None
-        off = self._offsets(offsets, self.num_groups)
-        rows = None
-        if want_dw:
-            if isinstance(x, Packed8):
-                if tuple(x.shape) != (n, self.in_dim) or x.device != self.device:
-                    raise ValueError(f"x must be [{n}, {self.in_dim}] on {self.device}")
-                rows = _Rows(None, 0, x.codes.data_ptr(), x.exps.data_ptr())
-            else:
-                ldx = _rows_2d(x, "x", self.in_dim, n, self.torch_dtype, self.device)
-                rows = _Rows(x.data_ptr(), ldx, None, None)
-        dx = dw = None
-        lddx = self.in_dim
-        with _On(self.device, stream) as s:
-            if want_dx:
-                dx = out_dx
-                if dx is None:
-                    dx = torch.empty((n, self.in_dim), dtype=self.torch_dtype, device=self.device)
-                else:
-                    lddx = _rows_2d(dx, "out_dx", self.in_dim, n, self.torch_dtype, self.device)
-                if n == 0 and not want_dw:
-                    return dx, None
-            ws_ptr, ws_len = None, 0
-            if want_dw:
-                shape = self._w_shape
-                dw = out_dw
-                if dw is None:
-                    dw = torch.empty(shape, dtype=torch.float32, device=self.device)
-                elif tuple(dw.shape) != shape or dw.dtype != torch.float32 or not dw.is_contiguous() \
-                        or dw.device != self.device:
-                    raise ValueError(f"out_dw must be a contiguous float32 CUDA tensor {list(shape)}")
-                ws = self._workspace(s, self.lib.mt_group_linear_workspace_bytes(n, self.num_groups, self.in_dim,
-                                                                                 self.out_dim))
-                ws_ptr, ws_len = ws.data_ptr(), ws.numel()
-            # an empty batch has no dx rows to point at: only dw is asked for
-            _check(self.lib.mt_group_linear_backward(
-                dy.data_ptr(), lddy, ctypes.byref(rows) if rows is not None else None, w, off, self.num_groups, n,
-                self.in_dim, self.out_dim, self._dt, dx.data_ptr() if want_dx and n else None, lddx,
-                dw.data_ptr() if want_dw else None, self._status_ptr, ws_ptr, ws_len, s), "mt_group_linear_backward")
-        return dx, dw
+        if stream is not None:
+            return _on(self.device, stream, self.backward, dy, x, weight, offsets, want_dx, want_dw, out_dx, out_dw)
+        ws = self._reserved(_rows_of(dy, "dy")) if want_dw else None
+        return _native.linear_backward(*self._cfg, dy, _plain_or_packed(x), weight, offsets, out_dx, out_dw, int(want_dx),
+                                       int(want_dw), ws)
+
+    def _reserved(self, n: int):
+        return self._workspace(self.lib.mt_group_linear_workspace_bytes(n, self.num_groups, self.in_dim, self.out_dim))
 
     def reserve_workspace(self, n: int, stream=None):
         """Allocate, on this stream, the workspace a backward over n rows needs (before a CUDA graph capture)."""
-        with _On(self.device, stream) as s:
-            self._workspace(s, self.lib.mt_group_linear_workspace_bytes(n, self.num_groups, self.in_dim,
-                                                                                 self.out_dim))
+        _on(self.device, stream, self._reserved, n)
 
 
 @dataclasses.dataclass
@@ -404,37 +287,7 @@ class GatedNorm(_Handle):
         super().__init__(device)
         self.dim, self.num_groups, self.kind, self.gate, self.eps, self.dtype = dim, num_groups, kind, gate, eps, dtype
         self.torch_dtype = _TORCH[dtype]
-        self._p_shapes = ((num_groups, dim), (dim,)) if num_groups == 1 else ((num_groups, dim),)
-        self._codes = (_DTYPES[dtype], _KINDS[kind], _GATES[gate])
-
-    def _config(self, n: int, params: NormParams, offsets) -> _GatedNorm:
-        c = _GatedNorm(n, self.dim, self.num_groups, *self._codes, self.eps, None, self._status_ptr)
-        if offsets is not None:
-            c.offsets = self._offsets(offsets, self.num_groups)
-        elif self.num_groups != 1:
-            raise ValueError("several groups need offsets")
-        for name in _PARAMS:
-            t = getattr(params, name)
-            if t is None:
-                continue
-            if t.dtype is not torch.float32 or t.device != self.device or t.shape not in self._p_shapes \
-                    or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous float32 CUDA tensor [{self.num_groups}, {self.dim}]")
-            setattr(c, name, t.data_ptr())
-        return c
-
-    def _plain(self, t, what: str, n: int):
-        if t is None:
-            return _Rows()
-        ld = _rows_2d(t, what, self.dim, n, self.torch_dtype, self.device)
-        return _Rows(t.data_ptr(), ld, None, None)
-
-    def _saved(self, t, what: str, n: int):
-        if isinstance(t, Packed8):
-            if tuple(t.shape) != (n, self.dim) or t.device != self.device:
-                raise ValueError(f"{what} must be [{n}, {self.dim}] on {self.device}")
-            return _Rows(None, 0, t.codes.data_ptr(), t.exps.data_ptr())
-        return self._plain(t, what, n)
+        self._cfg = (num_groups, dim, _DTYPES[dtype], _KINDS[kind], _GATES[gate], eps, self.device.index, self._status_ptr)
 
     def _parts(self, y, u, params: NormParams):
         """Which parts there are, checked against the parameters."""
@@ -455,42 +308,24 @@ class GatedNorm(_Handle):
         write, any of "yuzh" (``packed`` holds them by letter)."""
         params = params if params is not None else NormParams()
         self._parts(y, u, params)
-        n = _count(x, "x")
-        rx = self._plain(x, "x", n)
-        ry, ru = self._plain(y, "y", n), self._plain(u, "u", n)
-        c = self._config(n, params, offsets)
-        if y is None:
-            c.gate = 0
         has_h = params.pre_weight is not None
-        with _On(self.device, stream) as s:
-            z = x
-            rz, rh = _Rows(), _Rows()
-            if y is not None:
-                z = out_z if out_z is not None else torch.empty((n, self.dim), dtype=self.torch_dtype,
-                                                                device=self.device)
-                rz = self._plain(z, "out_z", n) if out_z is not None else _Rows(z.data_ptr(), self.dim)
-            elif out_z is not None:
-                raise ValueError("without y there is no z to write")
-            h = None
-            if has_h:
-                h = out_h if out_h is not None else torch.empty((n, self.dim), dtype=self.torch_dtype,
-                                                                device=self.device)
-                rh = self._plain(h, "out_h", n) if out_h is not None else _Rows(h.data_ptr(), self.dim)
-            elif out_h is not None:
-                raise ValueError("without pre_weight there is no h to write")
-            packed = {}
-            for name in pack:
-                there = {"y": y is not None, "u": u is not None, "z": True, "h": has_h}.get(name)
-                if not there:
-                    raise ValueError(f"there is no {name!r} to pack")
-                p = packed[name] = _new_packed(n, self.dim, self.device)
-                r = {"y": ry, "u": ru, "z": rz, "h": rh}[name]
-                r.codes, r.exps = p.codes.data_ptr(), p.exps.data_ptr()
-            if n:
-                _check(self.lib.mt_gated_norm_forward(ctypes.byref(c), ctypes.byref(rx), ctypes.byref(ry),
-                                                      ctypes.byref(ru), ctypes.byref(rz), ctypes.byref(rh), s),
-                       "mt_gated_norm_forward")
-        return NormForward(z, h, packed)
+        if y is None and out_z is not None:
+            raise ValueError("without y there is no z to write")
+        if not has_h and out_h is not None:
+            raise ValueError("without pre_weight there is no h to write")
+        bits = 0
+        for name in pack:
+            if not {"y": y is not None, "u": u is not None, "z": True, "h": has_h}.get(name):
+                raise ValueError(f"there is no {name!r} to pack")
+            bits |= 1 << "yuzh".index(name)
+        args = (*self._cfg, params.post_weight, params.post_bias, params.scale, params.pre_weight, params.pre_bias, offsets,
+                x, y, u, out_z, out_h, bits)
+        r = _native.norm_forward(*args) if stream is None else _on(self.device, stream, _native.norm_forward, *args)
+        packed = {}
+        if bits:
+            names = [k for i, k in enumerate("yuzh") if bits >> i & 1]
+            packed = {k: _packed(r[2 + 2 * i], r[3 + 2 * i]) for i, k in enumerate(names)}
+        return NormForward(r[0] if y is not None else x, r[1], packed)
 
     def backward(self, dz, dh, y=None, u=None, z=None, params: NormParams = None, offsets=None, out_dx=None,
                  out_dy=None, out_du=None, stream=None) -> NormGrads:
@@ -507,34 +342,17 @@ class GatedNorm(_Handle):
         lead = dh if has_h else dz
         if lead is None:
             raise ValueError("dz is needed without pre_weight")
-        n = _count(lead, "dh" if has_h else "dz")
-        rdz, rdh = self._plain(dz, "dz", n), self._plain(dh, "dh", n)
-        ry, ru, rz = self._saved(y, "y", n), self._saved(u, "u", n), self._saved(z if has_h else None, "z", n)
-        c = self._config(n, params, offsets)
-        if y is None:
-            c.gate = 0
-        with _On(self.device, stream) as s:
-            def rows(out, what):
-                if out is not None:
-                    return out, self._plain(out, what, n)
-                t = torch.empty((n, self.dim), dtype=self.torch_dtype, device=self.device)
-                return t, _Rows(t.data_ptr(), self.dim)
+        if stream is not None:
+            return _on(self.device, stream, self.backward, dz, dh, y, u, z, params, offsets, out_dx, out_dy, out_du)
+        ws = self._reserved(_rows_of(lead, "dh" if has_h else "dz"))
+        r = _native.norm_backward(*self._cfg, params.post_weight, params.post_bias, params.scale, params.pre_weight,
+                                  params.pre_bias, offsets, dz, dh, _plain_or_packed(y), _plain_or_packed(u),
+                                  _plain_or_packed(z), out_dx, out_dy, out_du, ws)
+        return NormGrads(r[0], r[1], r[2], NormParams(*r[3:]))
 
-            dx, rdx = rows(out_dx, "out_dx")
-            dy, rdy = rows(out_dy, "out_dy") if y is not None else (None, _Rows())
-            du, rdu = rows(out_du, "out_du") if u is not None else (None, _Rows())
-            there = [k for k in _PARAMS if getattr(params, k) is not None]
-            sums = torch.empty((len(there), self.num_groups, self.dim), dtype=torch.float32, device=self.device)
-            grads = dict(zip(there, sums.unbind(0)))
-            ws = self._workspace(s, self.lib.mt_gated_norm_workspace_bytes(n, self.dim, self.num_groups))
-            _check(self.lib.mt_gated_norm_backward(
-                ctypes.byref(c), ctypes.byref(rdz), ctypes.byref(rdh), ctypes.byref(ry), ctypes.byref(ru),
-                ctypes.byref(rz), ctypes.byref(rdx), ctypes.byref(rdy), ctypes.byref(rdu),
-                *(grads[k].data_ptr() if k in grads else None for k in _PARAMS), ws.data_ptr(), ws.numel(), s),
-                "mt_gated_norm_backward")
-        return NormGrads(dx, dy, du, NormParams(**grads))
+    def _reserved(self, n: int):
+        return self._workspace(self.lib.mt_gated_norm_workspace_bytes(n, self.dim, self.num_groups))
 
     def reserve_workspace(self, n: int, stream=None):
         """Allocate, on this stream, the workspace a backward over n rows needs (before a CUDA graph capture)."""
-        with _On(self.device, stream) as s:
-            self._workspace(s, self.lib.mt_gated_norm_workspace_bytes(n, self.dim, self.num_groups))
+        _on(self.device, stream, self._reserved, n)

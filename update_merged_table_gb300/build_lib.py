@@ -4,13 +4,19 @@ Each ``csrc/*.cu`` file is compiled by nvcc in parallel for
 ``-gencode arch=compute_103a,code=sm_103a`` and linked into
 ``update_merged_table_gb300/_build/libmt.so`` with the CUDA runtime linked
 statically, so the library depends on nothing but the driver.
+
+Beside it, ``csrc/py/mt_block_py.cpp`` becomes ``_build/_mt_block.so``, the
+Python module through which ``block.py`` calls the library (it needs torch's
+and Python's headers).
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,6 +24,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmt.so")
+BINDING_SRC = os.path.join(CSRC, "py", "mt_block_py.cpp")
+BINDING = os.path.join(BUILD, "_mt_block.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2", "-I", INCLUDE, "-I", CSRC]
@@ -34,11 +42,47 @@ def _newest(paths) -> float:
     return max(os.path.getmtime(p) for p in paths)
 
 
+def _start_binding(force: bool, verbose: bool):
+    """Start compiling the Python module if it is out of date; (process, file to rename) or None."""
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "mt.h"), __file__]
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= _newest(deps):
+        return None
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    lib = os.path.join(torch_dir, "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", BINDING_SRC, "-o", tmp, "-I", INCLUDE,
+           "-I", os.path.join(torch_dir, "include"), "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
+           "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd))
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT), tmp
+
+
+def _finish_binding(started):
+    if started is None:
+        return
+    proc, tmp = started
+    out, _ = proc.communicate()
+    if proc.returncode != 0:
+        raise RuntimeError("the Python module failed to compile:\n" + out.decode(errors="replace"))
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libmt.so if any source or header is newer than it; return its path."""
+    """Compile and link libmt.so and the Python module if any source or header is newer; return libmt.so's path."""
+    os.makedirs(BUILD, exist_ok=True)
+    binding = _start_binding(force, verbose)
+    try:
+        return _build_lib(force, verbose)
+    finally:
+        _finish_binding(binding)
+
+
+def _build_lib(force: bool, verbose: bool) -> str:
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     headers = sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")))
-    os.makedirs(BUILD, exist_ok=True)
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest(sources + headers + [__file__]):
         return LIB
     cc = nvcc()
