@@ -290,6 +290,10 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   return r;
 }
 __device__ __forceinline__ f32x2 both(float x) { return pk(x, x); }
+__device__ __forceinline__ float pair_sum(f32x2 a) {
+  const float2 f = upk(a);
+  return f.x + f.y;
+}
 
 template <typename T>
 __device__ __forceinline__ void widen8(const Raw8<T>& v, bool packed, f32x2 (&f)[4]) {

@@ -162,11 +162,6 @@ __device__ __forceinline__ void gate8(int gate, const f32x2 (&u)[4], f32x2 (&a)[
   }
 }
 
-__device__ __forceinline__ float pair_sum(f32x2 a) {
-  const float2 f = upk(a);
-  return f.x + f.y;
-}
-
 // A row v normalised is v * r + c: r its inverse deviation, c = -mean * r (0 for rms).  TWO rows v and w at once, or v
 // alone.  Columns past d hold zeros and stay out of the deviation.
 struct Stats {
