@@ -298,12 +298,18 @@ __device__ __forceinline__ float pair_sum(f32x2 a) {
 template <typename T>
 __device__ __forceinline__ void widen8(const Raw8<T>& v, bool packed, f32x2 (&f)[4]) {
   if (packed) {
-    const float s = pack_scale(v.a.z);
-    float g[8];
-    codes_f(v.a.x, s, g);
-    codes_f(v.a.y, s, g + 4);
+    // as codes_f does it, two columns an instruction
+    const f32x2 s = both(pack_scale(v.a.z)), off = both(-8388736.0f);
+    const uint32_t w[2] = {v.a.x ^ 0x80808080u, v.a.y ^ 0x80808080u};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = pk(g[2 * j], g[2 * j + 1]);
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t x = w[j >> 1];
+      const int b = (j & 1) * 2;
+      f[j] = mul2(add2(pk(__uint_as_float(__byte_perm(x, 0x4B000000u, 0x7540 + b)),
+                          __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7541 + b))),
+                       off),
+                  s);
+    }
   } else if constexpr (sizeof(T) == 4) {
     const uint32_t w[8] = {v.a.x, v.a.y, v.a.z, v.a.w, v.b.x, v.b.y, v.b.z, v.b.w};
 #pragma unroll

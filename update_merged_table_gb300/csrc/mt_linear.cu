@@ -313,10 +313,13 @@ __global__ void __launch_bounds__(kThreadsL) k_linear_weights(const LinearWeight
   }
 }
 
-constexpr int kSumSlices = 8;  // warps of a block
+constexpr int kSumSlices = 8;                 // warps of a block
+constexpr int kSumTask = 32 * kSumSlices * 4;  // values of dW a block sums at a time
+__host__ __device__ inline int sum_tasks(size_t size) { return (int)((size + kSumTask - 1) / kSumTask); }
 __global__ void __launch_bounds__(32 * kSumSlices) k_linear_sums(const LinearWeights p) {
   extern __shared__ long long s_off[];
   __shared__ float4 s_sum[kSumSlices][32];
+  __shared__ int s_active;
   int* s_cum = reinterpret_cast<int*>(s_off + p.groups + 1);
   int* s_slot = s_cum + p.groups + 1;
   load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
@@ -324,7 +327,6 @@ __global__ void __launch_bounds__(32 * kSumSlices) k_linear_sums(const LinearWei
   count_slots(s_cum, p.groups, s_slot);
   const size_t size = (size_t)p.M * p.K;
   const bool four = size % 4 == 0 && ((uintptr_t)p.dw & 15) == 0;  // four values at once
-  const size_t i0 = (size_t)blockIdx.x * blockDim.x + threadIdx.x, step = (size_t)gridDim.x * blockDim.x;
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   auto add4 = [](float4& s, const float4& v) {
     s.x += v.x;
@@ -332,36 +334,54 @@ __global__ void __launch_bounds__(32 * kSumSlices) k_linear_sums(const LinearWei
     s.z += v.z;
     s.w += v.w;
   };
-  for (int g = 0; g < p.groups; ++g) {
+  // the groups with work: all but those whose only chunk wrote dW itself
+  int* s_group = s_slot + p.groups + 1;
+  if (threadIdx.x < 32) {
+    int active = 0;
+    for (int g0 = 0; g0 < p.groups; g0 += 32) {
+      const int g = g0 + lane;
+      const bool on = g < p.groups && s_cum[g + 1] - s_cum[g] != 1;
+      const unsigned mask = __ballot_sync(kFull, on);
+      if (on) s_group[active + __popc(mask & ((1u << lane) - 1u))] = g;
+      active += __popc(mask);
+    }
+    if (lane == 0) s_active = active;
+  }
+  __syncthreads();
+  // a block's task: a group's next kSumTask values
+  const int per_group = sum_tasks(size);
+  for (long long t = blockIdx.x; t < (long long)s_active * per_group; t += gridDim.x) {
+    const int a = (int)(t / per_group), q = (int)(t - (long long)a * per_group), g = s_group[a];
     const int c = s_cum[g + 1] - s_cum[g];
-    if (c == 1) continue;  // written by its only chunk
     const float* part = p.part + (size_t)s_slot[g] * size;
     float* out = p.dw + (size_t)g * size;
+    const size_t end = size < (size_t)(q + 1) * kSumTask ? size : (size_t)(q + 1) * kSumTask;
     if (four && c >= 2 * kSumSlices) {  // many chunks: the block's warps take every kSumSlices-th, joined in their order
-      for (size_t b = blockIdx.x; b * 32 < size / 4; b += gridDim.x) {
-        const size_t i = b * 32 + lane;
+      for (size_t b = (size_t)q * kSumTask / 4; b < end / 4; b += 32) {
+        const size_t i = b + lane;
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (i < size / 4) {
+        if (i < end / 4) {
 #pragma unroll 4
           for (int k = slice; k < c; k += kSumSlices) add4(s, __ldg(reinterpret_cast<const float4*>(part + (size_t)k * size) + i));
         }
         s_sum[slice][lane] = s;
         __syncthreads();
-        if (slice == 0 && i < size / 4) {
+        if (slice == 0 && i < end / 4) {
           for (int k = 1; k < kSumSlices; ++k) add4(s, s_sum[k][lane]);
           reinterpret_cast<float4*>(out)[i] = s;
         }
         __syncthreads();
       }
     } else if (four) {
-      for (size_t i = i0; i < size / 4; i += step) {
+      const size_t i = (size_t)q * kSumTask / 4 + threadIdx.x;
+      if (i < end / 4) {
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
         for (int k = 0; k < c; ++k) add4(s, __ldg(reinterpret_cast<const float4*>(part + (size_t)k * size) + i));
         reinterpret_cast<float4*>(out)[i] = s;
       }
     } else {
-      for (size_t i = i0; i < size; i += step) {
+      for (size_t i = (size_t)q * kSumTask + threadIdx.x; i < end; i += blockDim.x) {
         float s = 0.0f;
 #pragma unroll 4
         for (int k = 0; k < c; ++k) s += __ldg(part + (size_t)k * size + i);
@@ -435,8 +455,12 @@ cudaError_t launch_linear_weights(LinearWeights& p, int dtype, cudaStream_t s) {
   Cut cut = cut_of(p.n, p.groups, p.K, p.M);
   const bool tc = dtype == MT_BF16 && linear_weights_fits_tc(p);
   p.slots = slots_of(p.n, p.groups, p.K, p.M);
-  // a partial product is written and read once, at about 4 TB/s; 64 rows of a tile take 0.42 us (the fp32 pipes: 3 us)
-  p.slot_cost = (float)((double)p.K * p.M * 8 / 4e6 / (tc ? 0.42 : 3.0));
+  // Measured: 64 rows of a tile take 0.42 us on the tensor cores and 6 us on the fp32 pipes, a tile's end 6 us, the sums'
+  // launch 5 us; a partial product is written and read once, at about 4 TB/s.
+  const float unit = tc ? 0.42f : 6.0f;
+  p.slot_cost = (float)((double)p.K * p.M * 8 / 4e6) / unit;
+  p.round_cost = 6.0f / unit;
+  p.sums_cost = 5.0f / unit;
   p.tiles = tc ? cut.tiles : ((p.M + kTM - 1) / kTM) * ((p.K + kTN - 1) / kTN);
   p.units = tc ? cut.units : sm_count() * 4;
   if (p.n > 0 && tc) return launch_linear_weights_tc(p, cut, s);
@@ -460,8 +484,8 @@ cudaError_t launch_linear_weights(LinearWeights& p, int dtype, cudaStream_t s) {
 cudaError_t launch_linear_sums(const LinearWeights& p, cudaStream_t s) {
   if (p.n == 0) return cudaMemsetAsync(p.dw, 0, (size_t)p.groups * p.M * p.K * 4, s);
   MT_LAUNCH("k_linear_sums", s);
-  const long long size = (long long)p.M * p.K;
-  k_linear_sums<<<grid_for((size + 3) / 4 * kSumSlices, 256, 4), 256, weights_smem(p.groups), s>>>(p);
+  const long long tasks = (long long)p.groups * sum_tasks((size_t)p.M * p.K);
+  k_linear_sums<<<grid_for(tasks * 256, 256, 8), 256, weights_smem(p.groups) + (size_t)p.groups * 4, s>>>(p);
   return cudaGetLastError();
 }
 

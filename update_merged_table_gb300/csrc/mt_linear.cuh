@@ -36,7 +36,8 @@ struct LinearWeights {
   int K, M;
   int tiles;        // tiles of dW (of the kernel that runs)
   int units;        // blocks (pairs) that walk over them
-  float slot_cost;  // what a partial product costs, in units of 64 rows of a tile
+  float slot_cost, round_cost, sums_cost;  // what a partial product, a tile's end and the sums' launch cost, in units of
+                                           // 64 rows of a tile
   int slots;        // partial products there is room for
   int* chosen;      // [1] workspace: the rows of a chunk, as the products chose them, for their sums
   float* part;    // [slots][M][K]: partial products of the groups that have several chunks
@@ -48,10 +49,8 @@ inline size_t weights_smem(int groups) { return (size_t)(groups + 1) * (8 + 4 + 
 // The rows of a chunk.  A group may be split into chunks whose products are summed afterwards, so that every block (pair)
 // gets about the same work however ragged the groups are; a partial product costs a write and a read of dW's size.  What
 // is weighed is the longest group in 1, 2, ... kSplits equal chunks, by the time of the last block in units of 64 rows:
-// rounds of tiles of that many rows, or what a block has on average plus one tile where the rounds differ in length,
-// and per round kRoundCost for the tile's last read-out and store (measured: 6 us against 0.42 us per 64 rows of a
-// 256 x 256 tile).  Every thread calls it, after load_offsets.
-constexpr float kRoundCost = 14.0f, kSumsCost = 12.0f;
+// rounds of tiles of that many rows, or what a block has on average plus one tile where the rounds differ in length, and
+// per round the tile's last read-out and store.  Every thread calls it, after load_offsets.
 struct ChunkChoice {
   int count[kSplits], split[kSplits];  // chunks; those of groups that have several
   int longest, rows, chunk;            // in units of 64 rows, and in rows
@@ -94,8 +93,8 @@ __device__ __forceinline__ int choose_chunk(const LinearWeights& p, const long l
     const float rounds = ceilf((float)c.count[lane] * (float)p.tiles / (float)p.units);
     const float mean = (float)c.rows * (float)p.tiles / (float)p.units;
     const int sp = c.split[lane];
-    float cost = fmaxf(mean, fminf(rounds * (float)s, mean + (float)s)) + rounds * kRoundCost + (float)sp * p.slot_cost +
-                 (sp > 0 ? kSumsCost : 0.0f);
+    float cost = fmaxf(mean, fminf(rounds * (float)s, mean + (float)s)) + rounds * p.round_cost +
+                 (float)sp * p.slot_cost + (sp > 0 ? p.sums_cost : 0.0f);
     if (sp > p.slots) cost = 3.0e38f;  // lane 0 splits nothing: it always has room
     int best = lane;
     for (int o = 16; o > 0; o >>= 1) {  // the cheapest, of equals the one that splits least

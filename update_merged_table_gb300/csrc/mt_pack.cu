@@ -17,10 +17,11 @@ struct PackParams {
   int d, vecs;     // vecs: vectors of eight columns per row (packing: rounded up to whole blocks of four)
 };
 
-constexpr int kUnroll = 4;  // vectors a lane has in flight
+// Vectors a lane has in flight.  Reading bf16 and writing codes gains from four (1.97M x 64: 72 us, one 78), reading codes
+// and writing bf16 is bound by its writes and loses by them (78 us, one 67).
+constexpr int kPackVecs = 4, kUnpackVecs = 1;
 
-// Vectors of a launch: lane `lane` of a warp takes the vectors it0 + 32 u + lane, u < kUnroll, so a warp covers 1024
-// neighbouring columns.  Where the rows follow one another without gaps and are whole blocks (FLAT), finding a vector
+// Vectors of a launch: lane `lane` of a warp takes the vectors it0 + 32 u + lane.  Where the rows follow one another without gaps and are whole blocks (FLAT), finding a vector
 // takes no division: everything is cut into rows of 2^20 vectors.
 struct Item {
   long long row;
@@ -38,17 +39,17 @@ __global__ void __launch_bounds__(256) k_pack8(const PackParams p) {
   const long long total = p.total;  // a multiple of four: a block's four lanes stay together
   const int lane = threadIdx.x & 31;
   const long long warp = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5, warps = ((long long)gridDim.x * blockDim.x) >> 5;
-  for (long long it0 = warp * 32 * kUnroll; it0 < total; it0 += warps * 32 * kUnroll) {
-    Raw8<T> v[kUnroll];
-    Item x[kUnroll];
+  for (long long it0 = warp * 32 * kPackVecs; it0 < total; it0 += warps * 32 * kPackVecs) {
+    Raw8<T> v[kPackVecs];
+    Item x[kPackVecs];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < kPackVecs; ++u) {
       const long long it = it0 + u * 32 + lane;
       x[u] = item_of<FLAT>(p, it < total ? it : 0);
       v[u] = it < total ? load8<T, AL>(p.r, x[u].row, x[u].vec, p.d) : Raw8<T>{};
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
+    for (int u = 0; u < kPackVecs; ++u)
       put_packed8<T, AL>(p.q, x[u].row, x[u].vec, p.d, v[u], it0 + u * 32 + lane < total);
   }
 }
@@ -58,17 +59,17 @@ __global__ void __launch_bounds__(256) k_unpack8(const PackParams p) {
   const long long total = p.total;
   const int lane = threadIdx.x & 31;
   const long long warp = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5, warps = ((long long)gridDim.x * blockDim.x) >> 5;
-  for (long long it0 = warp * 32 * kUnroll; it0 < total; it0 += warps * 32 * kUnroll) {
-    Raw8<T> v[kUnroll];
-    Item x[kUnroll];
+  for (long long it0 = warp * 32 * kUnpackVecs; it0 < total; it0 += warps * 32 * kUnpackVecs) {
+    Raw8<T> v[kUnpackVecs];
+    Item x[kUnpackVecs];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < kUnpackVecs; ++u) {
       const long long it = it0 + u * 32 + lane;
       x[u] = item_of<FLAT>(p, it < total ? it : 0);
       v[u] = it < total ? load8<T, AL>(p.q, x[u].row, x[u].vec, p.d) : Raw8<T>{};
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < kUnpackVecs; ++u) {
       f32x2 f[4];
       widen8<T>(v[u], true, f);
       if (it0 + u * 32 + lane < total) put8<T, AL>(p.r, x[u].row, x[u].vec, p.d, narrow8<T>(f));
@@ -112,7 +113,7 @@ int mt_pack8(const void* x, int64_t ldx, int64_t n, int32_t d, int dtype, int8_t
   if (rc != MT_OK || n == 0) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool wide = pack_wide(p, dtype), flat = pack_flat(p, wide, (d + kPackBlock - 1) / kPackBlock * 4);
-  const int grid = grid_for((p.total + kUnroll - 1) / kUnroll, 256, 8);
+  const int grid = grid_for((p.total + kPackVecs - 1) / kPackVecs, 256, 8);
   {
     MT_LAUNCH("k_pack8", s);
     if (dtype == MT_F32) {
@@ -140,7 +141,7 @@ int mt_unpack8(const int8_t* codes, const uint8_t* exps, int64_t n, int32_t d, i
   if (rc != MT_OK || n == 0) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool wide = pack_wide(p, dtype), flat = pack_flat(p, wide, (d + 7) / 8);
-  const int grid = grid_for((p.total + kUnroll - 1) / kUnroll, 256, 8);
+  const int grid = grid_for((p.total + kUnpackVecs - 1) / kUnpackVecs, 256, 8);
   {
     MT_LAUNCH("k_unpack8", s);
     if (dtype == MT_F32) {
