@@ -572,3 +572,13 @@ def test_refusals():
         mt.pack8(torch.zeros(2, 9000, **t))
     with pytest.raises(ValueError):
         mt.Packed8(torch.zeros(4, 33, device=DEV, dtype=torch.int8), torch.zeros(4, 1, device=DEV, dtype=torch.uint8))
+
+
+def test_example_trains_through_the_table():
+    """Lookup, tower, gradients from 8-bit checkpoints, sparse Adam: the loss falls; serving takes the same weights."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import dense_block
+    losses = dense_block.train(steps=25, users=24, width=64, verbose=False)
+    assert all(np.isfinite(losses)) and np.mean(losses[-5:]) < 0.9 * np.mean(losses[:5]), losses
