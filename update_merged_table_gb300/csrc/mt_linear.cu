@@ -231,25 +231,23 @@ __global__ void __launch_bounds__(kThreadsL) k_linear_weights(const LinearWeight
   extern __shared__ long long s_off[];
   __shared__ __align__(16) Steps s;
   __shared__ ChunkChoice s_choice;
-  int* s_cum = reinterpret_cast<int*>(s_off + p.groups + 1);
-  int* s_slot = s_cum + p.groups + 1;
   load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
-  const int chunk = choose_chunk(p, s_off, s_choice);
-  count_tiles(s_off, p.groups, chunk, s_cum);
-  count_slots(s_cum, p.groups, s_slot);
+  const Plan plan = plan_in(s_off, p.groups);
+  plan_chunks(p, plan, s_choice);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const T* DY = static_cast<const T*>(p.dy);
   const T* X = static_cast<const T*>(p.x.data);
   const int nb = (p.K + kPackBlock - 1) / kPackBlock;
   const bool is_wide = ((uintptr_t)p.dw & 15) == 0;  // (partial products always are)
   const int kt = (p.K + kTN - 1) / kTN, tiles = (p.M + kTM - 1) / kTM * kt;
-  const long long total = (long long)s_cum[p.groups] * tiles;
-  for (long long t = blockIdx.x; t < total; t += gridDim.x) {
+  const long long total = (long long)plan.ocum[p.groups] * tiles;
+  for (long long round = 0; round * gridDim.x < total; ++round) {
+    const long long t = dealt(round, blockIdx.x, gridDim.x);
+    if (t >= total) continue;
     const int c = (int)(t / tiles), q0 = (int)(t - (long long)c * tiles);
     const int m0 = q0 / kt * kTM, k0 = (q0 - q0 / kt * kt) * kTN;
-    const int g = tile_group(s_cum, p.groups, c);
-    const long long first = s_off[g] + (long long)(c - s_cum[g]) * chunk;
-    const long long last = min(first + chunk, s_off[g + 1]);
+    const Chunk x = chunk_of(plan, p.groups, c);
+    const long long first = x.first, last = x.last;
     // this thread's four-element pieces: two of dy (rows yr and yr + 8), one of x
     const int yr = tid >> 5, yc = (tid & 31) * 4, xr = tid >> 4, xc = (tid & 15) * 4;
     float4 ry[2], rx;
@@ -289,7 +287,7 @@ __global__ void __launch_bounds__(kThreadsL) k_linear_weights(const LinearWeight
       multiply(s, tx, ty, acc);
       __syncthreads();
     }
-    float* out = weights_out(p, s_cum, s_slot, g, c);
+    float* out = weights_out(p, plan, x);
     const int k = k0 + tx * 4;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {

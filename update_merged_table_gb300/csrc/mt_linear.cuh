@@ -44,13 +44,14 @@ struct LinearWeights {
   float* dw;      // [groups][M][K]
 };
 
-inline size_t weights_smem(int groups) { return (size_t)(groups + 1) * (8 + 4 + 4); }
+inline size_t weights_smem(int groups) { return (size_t)(groups + 1) * (8 + 4 * 4); }
 
 // The rows of a chunk.  A group may be split into chunks whose products are summed afterwards, so that every block (pair)
 // gets about the same work however ragged the groups are; a partial product costs a write and a read of dW's size.  What
 // is weighed is the longest group in 1, 2, ... kSplits equal chunks, by the time of the last block in units of 64 rows:
-// rounds of tiles of that many rows, or what a block has on average plus one tile where the rounds differ in length, and
-// per round the tile's last read-out and store.  Every thread calls it, after load_offsets.
+// rounds of tiles of that many rows, or what a block has on average plus a part of a tile where the rounds differ in
+// length (plan_chunks deals them out by length), and per round the tile's last read-out and store.  Every thread calls
+// it, after load_offsets.
 struct ChunkChoice {
   int count[kSplits], split[kSplits];  // chunks; those of groups that have several
   int longest, rows, chunk;            // in units of 64 rows, and in rows
@@ -93,7 +94,7 @@ __device__ __forceinline__ int choose_chunk(const LinearWeights& p, const long l
     const float rounds = ceilf((float)c.count[lane] * (float)p.tiles / (float)p.units);
     const float mean = (float)c.rows * (float)p.tiles / (float)p.units;
     const int sp = c.split[lane];
-    float cost = fmaxf(mean, fminf(rounds * (float)s, mean + (float)s)) + rounds * p.round_cost +
+    float cost = fmaxf(fmaxf(mean, (float)min(s, c.longest)), fminf(rounds * (float)s, mean + 0.35f * (float)s)) + rounds * p.round_cost +
                  (float)sp * p.slot_cost + (sp > 0 ? p.sums_cost : 0.0f);
     if (sp > p.slots) cost = 3.0e38f;  // lane 0 splits nothing: it always has room
     int best = lane;
@@ -133,11 +134,118 @@ __device__ __forceinline__ void count_slots(const int* s_cum, int G, int* s_slot
   __syncthreads();
 }
 
-// Where chunk c (of group g) puts its product: dW itself when the group has no other chunk, else its slot.
-__device__ __forceinline__ float* weights_out(const LinearWeights& p, const int* s_cum, const int* s_slot, int g, int c) {
+// The chunks of dW's rows and the order in which their tiles are dealt out.  A group's chunks are equal; the groups come
+// by the length of their chunks, longest first, and every other round of tiles is dealt backwards, so that the blocks'
+// sums come out near one another.
+constexpr int kSortGroups = 256;  // more groups than this make tiles enough to even out as they come
+struct Plan {
+  const long long* off;  // [groups + 1] rows
+  int* cum;              // [groups + 1] chunks before each group
+  int* slot;             // [groups + 1] partial products before each group
+  int* order;            // [groups] the groups as they are dealt
+  int* ocum;             // [groups + 1] chunks before each place of the order
+};
+struct Chunk {
+  int g, index;          // its group, and which of the group's chunks it is
+  long long first, last; // its rows
+};
+
+__device__ __forceinline__ Plan plan_in(long long* s_off, int G) {
+  int* p = reinterpret_cast<int*>(s_off + G + 1);
+  return Plan{s_off, p, p + (G + 1), p + 2 * (G + 1), p + 3 * (G + 1)};
+}
+// Units of 64 rows in each of group g's chunks.
+__device__ __forceinline__ int chunk_units(const Plan& q, int g) {
+  const int c = q.cum[g + 1] - q.cum[g], u = (int)((q.off[g + 1] - q.off[g] + 63) / 64);
+  return c > 0 ? (u + c - 1) / c : 0;
+}
+
+// Fills the plan (q.off is there already); every thread calls it.
+__device__ __forceinline__ void plan_chunks(const LinearWeights& p, const Plan& q, ChunkChoice& choice) {
+  const int G = p.groups, chunk = choose_chunk(p, q.off, choice);
+  if (G <= 32) {  // a lane per group: all in one warp, without waiting for the others in between
+    if (threadIdx.x < 32) {
+      const int lane = threadIdx.x;
+      const bool on = lane < G;
+      const int u = on ? (int)((q.off[lane + 1] - q.off[lane] + 63) / 64) : 0, s = chunk / 64;
+      const int c = (u + s - 1) / s, split = c > 1 ? c : 0;
+      const int before = warp_sum_scan(c, lane), slots = warp_sum_scan(split, lane);
+      const int e = on ? (c > 0 ? (u + c - 1) / c : 0) : -1;
+      int rank = 0;
+      for (int j = 0; j < G; ++j) {
+        const int ej = __shfl_sync(kFull, e, j);
+        rank += ej > e || (ej == e && j < lane);
+      }
+      if (on) {
+        q.cum[lane] = before - c;
+        q.slot[lane] = slots - split;
+        q.order[rank] = lane;
+        q.ocum[rank] = c;
+      }
+      if (lane == 31) {
+        q.cum[G] = q.ocum[G] = before;
+        q.slot[G] = slots;
+      }
+      __syncwarp();
+      const int oc = on ? q.ocum[lane] : 0, obefore = warp_sum_scan(oc, lane);
+      __syncwarp();
+      if (on) q.ocum[lane] = obefore - oc;
+    }
+    __syncthreads();
+    return;
+  }
+  count_tiles(q.off, G, chunk, q.cum);
+  count_slots(q.cum, G, q.slot);
+  if (G <= kSortGroups) {
+    for (int g = threadIdx.x; g < G; g += blockDim.x) q.ocum[g] = chunk_units(q, g);
+    __syncthreads();
+    for (int g = threadIdx.x; g < G; g += blockDim.x) {
+      const int e = q.ocum[g];
+      int rank = 0;
+      for (int j = 0; j < G; ++j) rank += q.ocum[j] > e || (q.ocum[j] == e && j < g);
+      q.order[rank] = g;
+    }
+  } else {
+    for (int g = threadIdx.x; g < G; g += blockDim.x) q.order[g] = g;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int carry = 0;
+    for (int i0 = 0; i0 < G; i0 += 32) {
+      const int i = i0 + lane, g = i < G ? q.order[i] : 0;
+      const int c = i < G ? q.cum[g + 1] - q.cum[g] : 0;
+      const int inc = warp_sum_scan(c, lane);
+      if (i < G) q.ocum[i] = carry + inc - c;
+      carry += __shfl_sync(kFull, inc, 31);
+    }
+    if (lane == 0) q.ocum[G] = carry;
+  }
+  __syncthreads();
+}
+
+// The c-th chunk as they are dealt.
+__device__ __forceinline__ Chunk chunk_of(const Plan& q, int G, int c) {
+  const int place = tile_group(q.ocum, G, c), g = q.order[place];
+  Chunk x;
+  x.g = g;
+  x.index = c - q.ocum[place];
+  const int rows = chunk_units(q, g) * 64;
+  x.first = q.off[g] + (long long)x.index * rows;
+  x.last = min(x.first + rows, q.off[g + 1]);
+  return x;
+}
+
+// The tile that block `unit` of `units` takes in round r (it may lie past the last one).
+__device__ __forceinline__ long long dealt(long long r, int unit, int units) {
+  return r * units + ((r & 1) != 0 ? units - 1 - unit : unit);
+}
+
+// Where a chunk puts its product: dW itself when the group has no other chunk, else its slot.
+__device__ __forceinline__ float* weights_out(const LinearWeights& p, const Plan& q, const Chunk& c) {
   const size_t size = (size_t)p.M * p.K;
-  if (s_cum[g + 1] - s_cum[g] == 1) return p.dw + (size_t)g * size;
-  return p.part + (size_t)(s_slot[g] + c - s_cum[g]) * size;
+  if (q.cum[c.g + 1] - q.cum[c.g] == 1) return p.dw + (size_t)c.g * size;
+  return p.part + (size_t)(q.slot[c.g] + c.index) * size;
 }
 
 // Zeros for the rows in no group, by the threads [0, threads) of every block.

@@ -394,34 +394,27 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
   __shared__ Barriers bar;
   uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)s_raw + 1023) & ~(uintptr_t)1023);
   long long* s_off = reinterpret_cast<long long*>(ring + R::kStages * R::kStage);
-  int* s_cum = reinterpret_cast<int*>(s_off + p.groups + 1);
-  int* s_slot = s_cum + p.groups + 1;
   __shared__ ChunkChoice s_choice;
   load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
-  const int chunk = choose_chunk(p, s_off, s_choice);
-  count_tiles(s_off, p.groups, chunk, s_cum);
-  count_slots(s_cum, p.groups, s_slot);
+  const Plan plan = plan_in(s_off, p.groups);
+  plan_chunks(p, plan, s_choice);
   const uint32_t tmem = tc_begin<BN, CG>(bar, kReadWarps / 2 * CG, kReadWarps);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = blockIdx.x % CG;
   const int mt = (p.M + BN - 1) / BN, tiles = (p.K + kRowsD - 1) / kRowsD * mt;
-  const long long total = (long long)s_cum[p.groups] * tiles;
-  const long long t0 = blockIdx.x / CG, tstep = gridDim.x / CG;
+  const long long total = (long long)plan.ocum[p.groups] * tiles;
+  const int unit = blockIdx.x / CG, units = gridDim.x / CG;
 
-  // tile t: chunk c of group g, the chunk's rows [first, last), dW's corner (m0, k0 of this block)
-  struct Tile {
-    int g, c, m0, k0, stages;
-    long long first, last;
+  // a tile: its chunk and dW's corner (m0, k0 of this block)
+  struct Tile : Chunk {
+    int m0, k0, stages;
   };
   auto tile_of = [&](long long t) {
+    const int c = (int)(t / tiles), q = (int)(t - (long long)c * tiles);
     Tile x;
-    x.c = (int)(t / tiles);
-    const int q = (int)(t - (long long)x.c * tiles);
+    static_cast<Chunk&>(x) = chunk_of(plan, p.groups, c);
     x.k0 = q / mt * kRowsD + rank * kBM;
     x.m0 = (q - q / mt * mt) * BN;
-    x.g = tile_group(s_cum, p.groups, x.c);
-    x.first = s_off[x.g] + (long long)(x.c - s_cum[x.g]) * chunk;
-    x.last = min(x.first + chunk, s_off[x.g + 1]);
     x.stages = (int)((x.last - x.first + kBK - 1) / kBK);
     return x;
   };
@@ -434,7 +427,9 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         Slot s;
         long long issued = 0;
         bool ok = true;
-        for (long long t = t0; t < total && ok; t += tstep) {
+        for (long long r0 = 0; r0 * units < total && ok; ++r0) {
+          const long long t = dealt(r0, unit, units);
+          if (t >= total) continue;
           const Tile x = tile_of(t);
           for (long long r = x.first; r < x.last; r += kBK) {
             ok = tc::mbar_wait(&bar.empty[s.stage], s.phase ^ 1);
@@ -484,7 +479,9 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
       bool ok = true;
       if (rank != 0) {
         uint32_t seq = 0;  // stages before this tile
-        for (long long t = t0; t < total && ok && !X8; t += tstep) {
+        for (long long r0 = 0; r0 * units < total && ok && !X8; ++r0) {
+          const long long t = dealt(r0, unit, units);
+          if (t >= total) continue;
           const Tile x = tile_of(t);
           const int left = (int)(x.last - x.first) & (kBK - 1);
           seq += x.stages;
@@ -497,7 +494,9 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
           if (lane == 0) arrive<CG>(&bar.tail_ready[stage]);
         }
       }
-      for (long long t = t0; rank == 0 && t < total && ok; t += tstep) {
+      for (long long r0 = 0; rank == 0 && r0 * units < total && ok; ++r0) {
+        const long long t = dealt(r0, unit, units);
+        if (t >= total) continue;
         const Tile x = tile_of(t);
         for (int k = 0; k < x.stages; ++k) {
           if (k % kPromote == 0) {
@@ -574,7 +573,9 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
       acc_phase ^= acc == 0;
     };
 
-    for (long long t = t0; t < total && ok; t += tstep) {
+    for (long long r0 = 0; r0 * units < total && ok; ++r0) {
+      const long long t = dealt(r0, unit, units);
+      if (t >= total) continue;
       const Tile x = tile_of(t);
       const int parts = (x.stages + kPromote - 1) / kPromote;
 #pragma unroll
@@ -653,7 +654,7 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
       if (!ok) break;
       // sum[j]: dW at column k0 + 32 quad + lane and row m0 + half kCols + j: 32 lanes write 128 bytes of a row
       const int k = x.k0 + quad * 32 + lane, m0 = x.m0 + half * kCols;
-      float* out = weights_out(p, s_cum, s_slot, x.g, x.c) + (size_t)m0 * p.K + k;
+      float* out = weights_out(p, plan, x) + (size_t)m0 * p.K + k;
       size_t ld = p.K;
       asm volatile("" : "+l"(ld));  // keeps the compiler from holding a register per row's offset across the tiles
       if (k < p.K) {
