@@ -493,6 +493,33 @@ def test_empty_batch():
     assert mt.unpack8(mt.pack8(e)).shape == (0, 64)
 
 
+def test_rows_past_32_bit_offsets():
+    """2.2e9 values: the last rows come out as they do on their own (elements, codes and exponents past 2^31)."""
+    n, d, tail = 4_300_000, 512, 300
+    x = torch.empty(n, d, device=DEV, dtype=torch.bfloat16).normal_(generator=torch.Generator(device=DEV).manual_seed(23))
+    last = x[-tail:].clone()
+    p, q = mt.pack8(x), mt.pack8(last)
+    assert torch.equal(p.codes[-tail:], q.codes) and torch.equal(p.exps[-tail:], q.exps)
+    assert torch.equal(mt.unpack8(p)[-tail:], mt.unpack8(q))
+    w = rand(torch.Generator(device=DEV).manual_seed(24), 2, 64, d, scale=d ** -0.5)
+    off, alone = offsets_of([n - 200, 200]), offsets_of([100, 200])
+    lin = mt.GroupedLinear(2, d, 64)
+    assert torch.equal(lin.forward(x, w, off)[-tail:], lin.forward(last, w, alone))
+    dy = torch.zeros(n, 64, device=DEV, dtype=torch.bfloat16)
+    dy[-200:] = rand(torch.Generator(device=DEV).manual_seed(25), 200, 64)
+    for saved, near_by in ((x, last), (p, q)):
+        dx, dw = lin.backward(dy, saved, w, off)
+        sdx, sdw = lin.backward(dy[-tail:], near_by, w, alone)
+        assert torch.equal(dx[-tail:], sdx)
+        near(dw[1], wide(sdw[1]), 216 * F * np.abs(wide(sdw[1])).max())
+        assert not dw[0].any()
+    nb = mt.GatedNorm(d, num_groups=2, kind="layer")
+    one = mt.NormParams(pre_weight=torch.ones(2, d, device=DEV))
+    assert torch.equal(nb.forward(x, params=one, offsets=off).h[-tail:], nb.forward(last, params=one, offsets=alone).h)
+    g = nb.backward(None, x, z=p, params=one, offsets=off)
+    assert torch.equal(g.dx[-tail:], nb.backward(None, last, z=q, params=one, offsets=alone).dx)
+
+
 # ---- streams, graphs, refusals -----------------------------------------------------------------------------------------
 
 def test_other_streams_and_graph_capture():

@@ -369,8 +369,8 @@ constexpr int kPromote = 8;   // stages (of kBK rows) an accumulator sums before
 constexpr int kReadWarps = 8;
 constexpr int kWarpsW = 4 + kReadWarps;  // a warpgroup for copies and products (two of its warps idle), two to read out
 // A read-out thread of the widest tile holds 128 sums beside its loads: the block's registers (384 threads x 168 at
-// launch = 64512) are split anew, 56 for a control thread and 224 for a read-out thread (128 x 56 + 256 x 224 = 64512).
-constexpr int kRegsLaunch = 168, kRegsControl = 56, kRegsRead = 224;
+// launch = 64512) are split anew, 72 for a control thread and 216 for a read-out thread (128 x 72 + 256 x 216 = 64512).
+constexpr int kRegsLaunch = 168, kRegsControl = 72, kRegsRead = 216;
 static_assert(128 * kRegsControl + 32 * kReadWarps * kRegsRead <= kWarpsW * 32 * kRegsLaunch, "the split fits the launch");
 
 // Rows [left, kBK) of `slabs` slabs become zero, by a warp.  Row i of a 64-column slab is the 128 bytes at i * 128,
@@ -576,8 +576,24 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     for (long long r0 = 0; r0 * units < total && ok; ++r0) {
       const long long t = dealt(r0, unit, units);
       if (t >= total) continue;
-      const Tile x = tile_of(t);
-      const int parts = (x.stages + kPromote - 1) / kPromote;
+      // what outlives the tile's stages is kept few: the registers go to the sums
+      float* out;
+      int stages, m_left, len;
+      bool k_in;
+      int kb;
+      const uint8_t* ex = nullptr;
+      {
+        const Tile x = tile_of(t);
+        stages = x.stages;
+        len = (int)(x.last - x.first);
+        const int k = x.k0 + quad * 32 + lane, m0 = x.m0 + half * kCols;
+        m_left = p.M - m0;
+        k_in = k < p.K;
+        out = weights_out(p, plan, x) + (size_t)m0 * p.K + k;
+        if constexpr (X8) ex = p.x.exps + row_offset(x.first + ((threadIdx.x & 127) >> 1), nb) + x.k0 / kPackBlock + (threadIdx.x & 1) * 2;
+        kb = x.k0 / kPackBlock + (threadIdx.x & 1) * 2;
+      }
+      const int parts = (stages + kPromote - 1) / kPromote;
 #pragma unroll
       for (int j = 0; j < kCols; ++j) sum[j] = 0.0f;
       if constexpr (X8) {
@@ -587,9 +603,7 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         constexpr int kOwn = kPromote / 2;
         const int tid = threadIdx.x & 127, crow = tid >> 1, ch = tid & 1;
         const int off = (half + seq) & 1;                 // this team's first stage of the tile
-        const int rows = (int)(x.last - x.first) - crow;  // rows of the chunk from this thread's first on
-        const int kb = x.k0 / kPackBlock + ch * 2;
-        const uint8_t* ex = p.x.exps + (x.first + crow) * nb + kb;
+        const int rows = len - crow;  // rows of the chunk from this thread's first on
         const bool has0 = kb < nb, has1 = kb + 1 < nb;
         const uint32_t ex_step = (uint32_t)(kBK * nb);
         uint32_t e0[kOwn], e1[kOwn];
@@ -604,7 +618,7 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
 #pragma unroll
           for (int i = 0; i < kOwn; ++i) {
             const int k = part * kPromote + off + 2 * i;
-            if (k >= x.stages) break;  // always for part = parts
+            if (k >= stages) break;  // always for part = parts
             const uint32_t b0 = e0[i], b1 = e1[i];
             exponents(i, k + kPromote);
             const uint32_t stage = (seq + k) % R::kStages, phase = (seq + k) / R::kStages & 1;
@@ -647,20 +661,18 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
           // the part before this one: its products are done or nearly so, and this part's go on meanwhile
           if (part > 0 && ok) read_out();
         }
-        seq += x.stages;
+        seq += stages;
       } else {
         for (int part = 0; part < parts && ok; ++part) read_out();
       }
       if (!ok) break;
       // sum[j]: dW at column k0 + 32 quad + lane and row m0 + half kCols + j: 32 lanes write 128 bytes of a row
-      const int k = x.k0 + quad * 32 + lane, m0 = x.m0 + half * kCols;
-      float* out = weights_out(p, plan, x) + (size_t)m0 * p.K + k;
       size_t ld = p.K;
       asm volatile("" : "+l"(ld));  // keeps the compiler from holding a register per row's offset across the tiles
-      if (k < p.K) {
+      if (k_in) {
 #pragma unroll
         for (int j = 0; j < kCols; ++j) {
-          if (m0 + j < p.M) *out = sum[j];
+          if (j < m_left) *out = sum[j];
           out += ld;
         }
       }
