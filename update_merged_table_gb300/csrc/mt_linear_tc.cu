@@ -20,10 +20,19 @@
 //                       smaller.
 //
 // The tensor core cuts its fp32 accumulator off towards zero at every step:
-// measured, a sum over r rows of unit normal products comes out 1.1e-9 * r short
-// (4.4e-6 at 4096 rows, where an fp32 chain is 2.5e-7 off).  dW is fp32 and sums
-// over many rows, so its accumulator starts anew every kPromote stages and the
-// read-out warps add it to registers, rounding to nearest.
+// measured, a sum over r rows of unit normal products has a relative error of
+// 1.1e-9 * r (4.4e-6 at 4096 rows, where fp32 sums on the pipes have 2.5e-7).  dW
+// is fp32 and sums over many rows, so its accumulator starts anew every kPromote
+// stages and the read-out warps add it to registers, rounding to nearest: 4.9e-7
+// at 700,000 rows, for 5% of the time of parts four times as long (65,536 x 1024
+// x 1024, one group: 115 against 110 us).
+//
+// Bound: the arithmetic where the contraction is long, HBM where it is short.
+// Measured, forward: 77,824 rows to 1024 columns 1.63 PFLOP/s from 1024 columns
+// and 1.91 from 4096 (the library's product 1.79 and 1.93); 1,970,003 x 64 to 256
+// 196 us, 95% of the copy bandwidth.  dx of 490,011 x 256 from 512 columns 122 us
+// (91% of it).  dW of 65,536 x 1024 x 1024 in 8 groups: 123 us and 9 us of sums
+// (1.12 PFLOP/s), from 8 bits 157 us, where the widening bounds it.
 #include <algorithm>
 #include <mutex>
 
@@ -685,7 +694,7 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
 
 // ---- host --------------------------------------------------------------------------------------------
 
-// Tile width of a product with J columns and `rows` row tiles: the widest that leaves no half of a tile idle and
+// Tile width of a product with J columns and `row_tiles` row tiles: the widest that leaves no half of a tile idle and
 // still gives every SM a tile.
 int tile_width(int J, long long row_tiles) {
   int bn = J <= 64 ? 64 : (J <= 128 || (J % 256 != 0 && J % 256 <= 128 && J < 512) ? 128 : 256);
@@ -752,12 +761,15 @@ bool linear_rows_fits_tc(const LinearRows& p) {
          is_aligned(p.w, 16);
 }
 
-// Pairs where the product is bound by its arithmetic (several stages per tile) and tiles of 256 rows neither waste rows
-// (groups of 512 and more on average) nor leave SMs without work.
+// Pairs where the product is bound by its arithmetic, and tiles of 256 rows neither waste rows nor leave SMs without work.
+// Measured, single blocks against pairs: one column tile (491,520 rows to 256 columns) from 256 columns 84 against 96 us,
+// 384 106 against 109, 448 117 against 108, 512 127 against 117; several (327,680 to 512) from 128 74 against 74, 192 87
+// against 83, 256 94 against 88.  Rows per group (65,536 x 1024 to 1024): 512 118 against 114, 256 144 against 141, 128
+// 208 against 210; in 32 groups 103 against 93.
 cudaError_t launch_linear_rows_tc(const LinearRows& p, cudaStream_t s) {
   const bool b_mn = p.wj == 1 && p.wi != 1;
   const int bn = tile_width(p.J, (p.n + kBM - 1) / kBM + p.groups - 1);
-  const bool pair = bn == 256 && p.I > 2 * kBK && p.n / p.groups >= 512 && p.n / 256 * ((p.J + 255) / 256) >= sm_count() / 2;
+  const bool pair = bn == 256 && p.I > (p.J > 256 ? 2 : 6) * kBK && p.n / p.groups >= 256 && p.n / 256 * ((p.J + 255) / 256) >= sm_count() / 2;
   CUtensorMap a, w;
   if (!tc::encode_bf16(&a, 2, p.a, p.I, p.n, p.lda, 1, 0, kBK, kBM)) return cudaErrorInvalidValue;
   if (b_mn ? !tc::encode_bf16(&w, 3, p.w, p.J, p.I, p.J, p.groups, (uint64_t)p.I * p.J, 64, kBK)
@@ -781,6 +793,8 @@ Cut cut_of(int64_t n, int32_t groups, int32_t k, int32_t m) {
   const long long chunks = groups + n / 4096;
   Cut c;
   c.bn = tile_width(m, chunks * ((k + kBM - 1) / kBM));
+  // Whole calls, single blocks against pairs: 490,011 x 256 x 512 from 8 bits 157 against 142 us, 114,468 x 728 x 720 124
+  // against 116, 65,536 x 1024 x 1024 in 8 groups 127 against 127.
   c.pair = c.bn == 256 && k > kBM && n / 512 * ((k + 255) / 256) * ((m + 255) / 256) >= sm_count() / 2;
   const int across = c.pair ? 2 * kBM : kBM;
   c.tiles = ((k + across - 1) / across) * ((m + c.bn - 1) / c.bn);
