@@ -19,7 +19,15 @@
 //                atomics, so the sums have one order).  With S1 = sum D a yh and
 //                S2 = sum D a, dwp = s S1, dbp = s S2 and ds = wp S1 + bp S2: two
 //                sums for three gradients, and one when there is no bp.
-//  k_norm_sums   the blocks' partial sums of each group.
+//  k_norm_sums   the blocks' partial sums of each group (9 to 17 us, latency).
+//
+// Measured, bf16, all parts, of the copy bandwidth: 490,011 x 512 rms forward 412
+// us (90%), with h in 8 bits as well 474 (86%); backward 629 (92%), from 8 bits
+// 689 (69%: widening three rows takes the issue slots).  200,003 x 1024 layer norm
+// with biases 558 forward (54%) and 851 backward (56%), bound by issue and by the
+// latency between dependent steps at 12 warps an SM; the same as rms without
+// biases 576 backward (82%).  Widths that are no multiple of 8 go an element at a
+// time: 200,003 x 777 backward 2.5 ms (15%).
 #include <algorithm>
 
 #include "mt_block.cuh"

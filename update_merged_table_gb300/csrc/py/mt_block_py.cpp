@@ -2,8 +2,8 @@
 // tensors and the call of the C ABI, in one step of native code.
 //
 // A call on a few rows (a token being served) takes a few microseconds on the
-// GPU; checked and marshalled from Python it cost 12 to 25 us of host time on
-// the Grace CPU, here 6 to 9.  Nothing is computed here: the functions of
+// GPU; checked and marshalled from Python it cost 12 to 34 us of host time on
+// the Grace CPU, here 4 to 7.  Nothing is computed here: the functions of
 // libmt.so arrive as addresses (init), and tensors are read and made with
 // torch's own C++ interface.
 #include <torch/csrc/autograd/python_variable.h>
