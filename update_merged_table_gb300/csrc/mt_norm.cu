@@ -54,9 +54,12 @@ struct NormParams {
   int wide;                      // parameters reached with 16-byte loads
 };
 
-// The rows of block b of B: an even run of the rows [off0, off0 + m) that lie in groups.
+// Runs that m rows are cut into for `blocks` blocks: no more than there are rows, so that no run is empty (a group's partial
+// sums are those of all runs from its first row's to its last row's).
+__device__ __forceinline__ int runs_of(long long m, int blocks) { return m < blocks ? (m > 0 ? (int)m : 1) : blocks; }
+// The rows of run b of B: an even share of the rows [off0, off0 + m) that lie in groups.
 __device__ __forceinline__ long long run_start(long long off0, long long m, int b, int B) { return off0 + m * b / B; }
-// The block whose run holds the row off0 + r (0 <= r < m).
+// The run that holds the row off0 + r (0 <= r < m).
 __device__ __forceinline__ int run_of(long long r, long long m, int B) { return (int)(((r + 1) * B - 1) / m); }
 
 // Sums a (and b, where TWO) over a team: shuffles inside a warp, shared memory across a team's warps.  A team of more than one
@@ -522,8 +525,9 @@ k_norm_bwd(const NormParams p) {
     }
   }
 
-  const long long end = run_start(off0, m, blockIdx.x + 1, gridDim.x);
-  long long first = run_start(off0, m, blockIdx.x, gridDim.x);
+  const int runs = runs_of(m, gridDim.x), run = min((int)blockIdx.x, runs);  // blocks past the runs: an empty one
+  const long long end = run_start(off0, m, min(run + 1, runs), runs);
+  long long first = run_start(off0, m, run, runs);
   for (int g = first < end ? row_group(s_off, p.groups, first) : 0; first < end; ++g) {
     const int last = (int)min(end, s_off[g + 1]);
     if (last <= first) continue;  // an empty group
@@ -702,10 +706,11 @@ __global__ void __launch_bounds__(32 * kSlices) k_norm_sums(const NormParams p) 
   if (post ? p.dwp == nullptr : p.dwq == nullptr) return;
   const bool second = post ? p.bp != nullptr : p.bq != nullptr;
   const long long off0 = s_off[0], m = s_off[p.groups] - off0;
+  const int runs = runs_of(m, p.blocks);
   for (int g = blockIdx.z; g < p.groups; g += gridDim.z) {
     float a = 0.0f, b = 0.0f;
     if (col < p.d && s_off[g] < s_off[g + 1]) {
-      const int b0 = run_of(s_off[g] - off0, m, p.blocks), b1 = run_of(s_off[g + 1] - 1 - off0, m, p.blocks);
+      const int b0 = run_of(s_off[g] - off0, m, runs), b1 = run_of(s_off[g + 1] - 1 - off0, m, runs);
       const float* base = p.part + (size_t)(post ? 0 : 2) * p.d + col;
 #pragma unroll 8
       for (int k = b0 + slice; k <= b1; k += kSlices) {
