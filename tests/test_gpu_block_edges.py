@@ -3,10 +3,11 @@ in a group, workspaces of captured graphs, calls from several threads, outputs t
 
 import numpy as np
 import pytest
+import torch
 
 import update_merged_table_gb300 as mt
 import block_reference as R
-from test_gpu_block import check_backward, norm_case, values, wide
+from test_gpu_block import DEV, F, check_backward, near, norm_case, offsets_of, rand, values, wide
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +32,25 @@ def test_norm_gradients_when_few_rows_are_in_groups(n, sizes, lead, d, kind):
     check_backward(nb, whole, ref, size, "bf16", max(sizes))
     for t in (got.dx, got.dy, got.du):
         assert not t[:a].any() and not t[b:].any()
+
+
+@pytest.mark.parametrize("n", [262_144 + 37])
+def test_a_launch_of_many_milliseconds_reports_no_error(n):
+    """Pairs of blocks at work for 20 ms and more: what a block waits for until the launch's end is no fault."""
+    k = m = 8192
+    gen = torch.Generator(device=DEV).manual_seed(41)
+    x, w, dy = rand(gen, n, k), rand(gen, 2, m, k, scale=k ** -0.5), rand(gen, n, m)
+    lin, off = mt.GroupedLinear(2, k, m), offsets_of([n - 101, 101])
+    y = lin.forward(x, w, off)
+    assert lin.error() == 0
+    at = [0, 1, 131_000, n - 102, n - 101, n - 1]
+    for g, rows in ((0, at[:4]), (1, at[4:])):
+        want, size = wide(x[rows]) @ wide(w[g, :64]).T, np.abs(wide(x[rows])) @ np.abs(wide(w[g, :64])).T
+        near(y[rows, :64], want, 2.0 ** -8 * np.abs(want) + (k + 16) * F * size)
+    del y
+    _, dw = lin.backward(dy, x, w, off, want_dx=False)
+    assert lin.error() == 0
+    for g, (a, b) in enumerate(((0, n - 101), (n - 101, n))):
+        want = (dy[a:b, -8:].double().T @ x[a:b, -8:].double()).cpu().numpy()
+        # sums of 512 rows are cut off at each step of 16 rows (2^-23 of the sum at most), and added up in fp32
+        near(dw[g, -8:, -8:], want, (32 + n / 512) * F * np.sqrt(n) * 4, "dw")

@@ -111,6 +111,8 @@ struct Barriers {
   uint64_t tail_full[8], tail_ready[8];
   uint64_t acc_full[2], acc_empty[2];  // an accumulator is finished; it has been read out
   uint64_t done;                 // every product issued is done
+  volatile uint32_t copied;      // stages whose copies this block has started (counted where a pair's second block waits
+                                 // for its next short stage)
   uint32_t tmem;
 };
 
@@ -135,6 +137,7 @@ __device__ __forceinline__ uint32_t tc_begin(Barriers& b, int ready_count, int r
       tc::mbar_init(&b.acc_empty[i], read_warps * CG);
     }
     tc::mbar_init(&b.done, 1);
+    b.copied = 0;
     tc::mbar_init_fence();
   }
   __syncwarp();
@@ -272,6 +275,8 @@ k_linear_rows_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         }
       }
       ok = ok && all_released<R::kStages>(bar, s, issued);
+      // what the first block signals of its last products has to have arrived here before this block ends
+      if (rank != 0) ok = tc::mbar_wait(&bar.done, 0) && ok;
       if (!ok) {
         latch_status(p.status, MT_ECUDA);
         if (rank == 0) drain<R::kStages>(bar, s, issued);
@@ -310,8 +315,6 @@ k_linear_rows_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constan
       tc::mma_commit<CG>(&bar.done);  // tensor memory is freed only when no product writes it, also after a wait ran out
       ok = tc::mbar_wait(&bar.done, 0) && ok;
       if (!ok) latch_status(p.status, MT_ECUDA);
-    } else if (lane == 0) {
-      if (!tc::mbar_wait(&bar.done, 0)) latch_status(p.status, MT_ECUDA);
     }
   } else {
     const int quad = warp & 3;  // the lanes of tensor memory this warp may read
@@ -467,10 +470,12 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
                 tc::tma_load_2d(st + R::kStageA + c * 8192, &map_dy, full, dy0 + c * 64, (int)r);
             }
             ++issued;
+            if (CG == 2 && !X8) bar.copied = (uint32_t)issued;
             s.next<R::kStages>();
           }
         }
         ok = ok && all_released<R::kStages>(bar, s, issued);
+        if (rank != 0) ok = tc::mbar_wait(&bar.done, 0) && ok;  // as in k_linear_rows_tc
         if (!ok) {
           latch_status(p.status, MT_ECUDA);
           if (X8 || rank == 0) drain<R::kStages>(bar, s, issued);
@@ -496,7 +501,8 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
           seq += x.stages;
           if (left == 0) continue;
           const uint32_t stage = (seq - 1) % R::kStages;
-          ok = __all_sync(kFull, tc::mbar_wait(&bar.tail_full[stage], tail_phase >> stage & 1));
+          // a whole chunk may lie between two short stages
+          ok = __all_sync(kFull, tc::mbar_wait_while(&bar.tail_full[stage], tail_phase >> stage & 1, &bar.copied));
           if (!ok) break;
           tail_phase ^= 1u << stage;
           zero_rows(ring + stage * R::kStage, (kBM + kColsB) / 64, left, lane);
@@ -545,8 +551,10 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
       }
       if (lane == 0) {
         // tensor memory is freed only when no product writes it, also after a wait ran out
-        if (rank == 0) tc::mma_commit<CG>(&bar.done);
-        ok = tc::mbar_wait(&bar.done, 0) && ok;
+        if (rank == 0) {
+          tc::mma_commit<CG>(&bar.done);
+          ok = tc::mbar_wait(&bar.done, 0) && ok;
+        }
         if (!ok) latch_status(p.status, MT_ECUDA);
       }
     }

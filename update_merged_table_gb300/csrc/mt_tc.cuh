@@ -27,23 +27,47 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// Waits until the barrier's phase of this parity is over; false when it is not after kWaitTries tries of up to about a
-// millisecond each (the hardware suspends the thread during a try), so no wait is endless.
-constexpr int kWaitTries = 2000;
+// Whether the barrier's phase of this parity is over.  The hardware suspends the thread for a while if it is not: some
+// microseconds, also where a try asks for a millisecond (2000 such tries were over within 21 ms), so tries measure no time.
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ uint64_t nanoseconds() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+
+// Waits until the barrier's phase of this parity is over; false when it is not after two seconds by the GPU's clock (and, were
+// that to stand still, after kWaitTries tries), so no wait is endless.  What is waited for takes microseconds.
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kWaitTries = 1 << 26;
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   const uint32_t a = smem_addr(bar);
+  if (mbar_try(a, parity)) return true;
+  const uint64_t start = nanoseconds();
   for (int i = 0; i < kWaitTries; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(a), "r"(parity), "r"(1000000u)
-        : "memory");
-    if (done) return true;
+    if (mbar_try(a, parity)) return true;
+    if (nanoseconds() - start > kWaitNs) return false;
   }
   return false;
+}
+// The same for what may come after any time, as long as `progress` goes on in every two seconds.
+__device__ __forceinline__ bool mbar_wait_while(uint64_t* bar, uint32_t parity, const volatile uint32_t* progress) {
+  for (uint32_t seen = *progress;;) {
+    if (mbar_wait(bar, parity)) return true;
+    const uint32_t now = *progress;
+    if (now == seen) return false;
+    seen = now;
+  }
 }
 
 // ---- pairs of blocks (clusters of two) ---------------------------------------------------
