@@ -12,6 +12,11 @@ from test_gpu_block import DEV, F, check_backward, near, norm_case, offsets_of, 
 pytestmark = pytest.mark.gpu
 
 
+def small_integers(gen, *shape, dtype=torch.bfloat16):
+    """Whole numbers in [-2, 2]: their products and the sums of up to four million of them are exact in fp32."""
+    return torch.randint(-2, 3, shape, generator=gen, device=DEV).to(dtype)
+
+
 # ---- few rows in groups -----------------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("n,sizes,lead", [(5000, [3], 0), (5000, [1, 0, 2], 4990), (100_000, [40, 0, 1, 300], 7), (70_000, [0, 0], 5)])
@@ -32,6 +37,61 @@ def test_norm_gradients_when_few_rows_are_in_groups(n, sizes, lead, d, kind):
     check_backward(nb, whole, ref, size, "bf16", max(sizes))
     for t in (got.dx, got.dy, got.du):
         assert not t[:a].any() and not t[b:].any()
+
+
+# ---- sums with one exact value ------------------------------------------------------------------------------------------
+
+EXACT = [
+    ("bf16", 512, 1024, [9001, 0, 3, 20000]),     # pairs of blocks, several chunks
+    ("bf16", 512, 1024, [7001, 12345, 654]),      # dx by pairs
+    ("bf16", 64, 64, [100_003]),                  # one narrow tile
+    ("bf16", 264, 272, [10000, 63, 129]),
+    ("bf16", 104, 200, [5001, 1, 4097]),          # 8-bit rows that are widened first
+    ("bf16", 33, 250, [6000, 5001]),              # fp32 pipes
+    ("f32", 32, 128, [8192, 1, 30011]),
+    ("f32", 129, 257, [3000, 5000]),
+    ("f32", 16, 16, [300_001, 5]),
+]
+
+
+@pytest.mark.parametrize("dtype,k,m,sizes", EXACT)
+def test_linear_sums_are_exact_on_whole_numbers(dtype, k, m, sizes):
+    """Every row is counted once: on small whole numbers every sum is exact in fp32, whatever its order."""
+    gen = torch.Generator(device=DEV).manual_seed(k + m)
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    n, lead = sum(sizes) + 12, 5
+    x, dy, w = small_integers(gen, n, k, dtype=t), small_integers(gen, n, m, dtype=t), small_integers(gen, len(sizes), m, k, dtype=t)
+    off = offsets_of(sizes, lead)
+    lin = mt.GroupedLinear(len(sizes), k, m, dtype=dtype)
+    lin.reserve_workspace(n)
+    for b in lin._ws.values():
+        b.fill_(255)
+    y, dx = torch.zeros(n, m, device=DEV, dtype=torch.float64), torch.zeros(n, k, device=DEV, dtype=torch.float64)
+    dw = torch.zeros(len(sizes), m, k, device=DEV, dtype=torch.float64)
+    for g, (a, b) in enumerate(R.spans(off.tolist())):
+        y[a:b], dx[a:b] = x[a:b].double() @ w[g].double().T, dy[a:b].double() @ w[g].double()
+        dw[g] = dy[a:b].double().T @ x[a:b].double()
+    assert torch.equal(lin.forward(x, w, off), y.float().to(t))
+    for saved in (x, mt.pack8(x)):
+        gx, gw = lin.backward(dy, saved, w, off)
+        assert torch.equal(gx, dx.float().to(t))
+        assert torch.equal(gw, dw.float())
+    assert lin.error() == 0
+
+
+@pytest.mark.parametrize("d,dtype,kind", [(64, "bf16", "layer"), (1024, "bf16", "rms"), (50, "f32", "layer"), (4096, "bf16", "rms")])
+def test_norm_bias_sums_are_exact_on_whole_numbers(d, dtype, kind):
+    """dpre_bias sums dh, dpost_bias (no gate, no scale, no next norm) sums dz: each row once."""
+    sizes = [9000, 1, 0, 12345] if d < 4096 else [700, 0, 1300]
+    rows, p, off = norm_case(32, sizes, 10, 20, d, dtype, "none")
+    gen = torch.Generator(device=DEV).manual_seed(33)
+    dv = small_integers(gen, rows["x"].shape[0], d, dtype=rows["x"].dtype)
+    want = torch.stack([dv[a:b].double().sum(0) for a, b in R.spans(off.tolist())]).float()
+    nb = mt.GatedNorm(d, num_groups=len(sizes), kind=kind, gate="none", dtype=dtype)
+    one = mt.NormParams(pre_weight=p.pre_weight, pre_bias=p.pre_bias)
+    assert torch.equal(nb.backward(None, dv, z=rows["z"], params=one, offsets=off).params.pre_bias, want)
+    one = mt.NormParams(post_weight=p.post_weight, post_bias=p.post_bias)
+    assert torch.equal(nb.backward(dv, None, y=rows["y"], params=one, offsets=off).params.post_bias, want)
 
 
 @pytest.mark.parametrize("n", [262_144 + 37])

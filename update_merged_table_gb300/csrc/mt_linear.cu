@@ -400,7 +400,7 @@ size_t rows_smem(int groups) { return (size_t)(groups + 1) * (8 + 4); }
 // (a split leaves chunks of kMinChunk rows and more, so a group of one more than that makes two).
 constexpr int kRounds = 4;
 int slots_of(int64_t n, int32_t groups, int32_t k, int32_t m) {
-  const Cut c = cut_of(n, groups, k, m);
+  const Cut c = cut_of(n, groups, k, m, true);
   const long long want = std::max<long long>(2, (long long)kRounds * c.units / c.tiles);
   return (int)std::min<long long>(want, 2 * (n / kMinChunk));
 }
@@ -455,7 +455,7 @@ cudaError_t launch_linear_rows(LinearRows p, int dtype, cudaStream_t s) {
 
 // The rest of p is filled in here: the sums go by it too.
 cudaError_t launch_linear_weights(LinearWeights& p, int dtype, cudaStream_t s) {
-  Cut cut = cut_of(p.n, p.groups, p.K, p.M);
+  const Cut cut = cut_of(p.n, p.groups, p.K, p.M, p.x.data != nullptr);
   const bool tc = dtype == MT_BF16 && linear_weights_fits_tc(p);
   p.slots = slots_of(p.n, p.groups, p.K, p.M);
   // Measured: 64 rows of a tile take 0.42 us on the tensor cores and 6 us on the fp32 pipes, a tile's end 6 us, the sums'

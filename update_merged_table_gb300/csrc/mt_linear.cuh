@@ -260,13 +260,13 @@ __device__ __forceinline__ void zero_outside(const long long* s_off, int G, long
   }
 }
 
-// How a dW of this shape is cut into tiles, and over how many blocks (pairs) they are dealt.
+// How a dW of this shape is cut into tiles, and over how many blocks (pairs, if it may be pairs) they are dealt.
 struct Cut {
   int bn;        // columns of dy in a tile (rows of dW)
   bool pair;     // tiles of 256 columns of x by pairs of blocks, else of 128
   int tiles, units;
 };
-Cut cut_of(int64_t n, int32_t groups, int32_t k, int32_t m);
+Cut cut_of(int64_t n, int32_t groups, int32_t k, int32_t m, bool pairs);
 
 // The tensor-core forms (mt_linear_tc.cu): bf16, widths and strides in multiples of 8, rows on 16 bytes.
 bool linear_rows_fits_tc(const LinearRows& p);

@@ -111,8 +111,7 @@ struct Barriers {
   uint64_t tail_full[8], tail_ready[8];
   uint64_t acc_full[2], acc_empty[2];  // an accumulator is finished; it has been read out
   uint64_t done;                 // every product issued is done
-  volatile uint32_t copied;      // stages whose copies this block has started (counted where a pair's second block waits
-                                 // for its next short stage)
+  volatile uint32_t copied;      // pairs: stages whose copies this block has started
   uint32_t tmem;
 };
 
@@ -396,7 +395,10 @@ __device__ __forceinline__ void zero_rows(uint8_t* st, int slabs, int left, int 
 }
 
 // CG = 2: a pair takes 256 columns of x, each block its 128 and half of the tile's columns of dy (the split of
-// k_linear_rows_tc, for the same reason).
+// k_linear_rows_tc, for the same reason).  Plain x only: the second block's widened rows would be ordinary writes that the
+// first block's products read, so each stage would have to be handed over across the pair, 1.4 us at a time.  490,011 x 256 x
+// 512 from 8 bits, whole calls: the hand-overs dealt over three warps 179 us, one warp's 289, by the widening warps 260;
+// single blocks 171.
 template <int BN, bool X8, int CG>
 __global__ void __launch_bounds__(kWarpsW * 32, 1)
 k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_dy, const LinearWeights p) {
@@ -410,7 +412,7 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
   load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
   const Plan plan = plan_in(s_off, p.groups);
   plan_chunks(p, plan, s_choice);
-  const uint32_t tmem = tc_begin<BN, CG>(bar, kReadWarps / 2 * CG, kReadWarps);
+  const uint32_t tmem = tc_begin<BN, CG>(bar, kReadWarps / 2, kReadWarps);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = blockIdx.x % CG;
   const int mt = (p.M + BN - 1) / BN, tiles = (p.K + kRowsD - 1) / kRowsD * mt;
@@ -448,7 +450,7 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
             if (!ok) break;
             uint8_t* st = ring + s.stage * R::kStage;
             const int dy0 = x.m0 + rank * kColsB;
-            if (CG == 2 && !X8 && x.last - r >= kBK) {  // both blocks' copies count on the first block's barrier
+            if (CG == 2 && x.last - r >= kBK) {  // both blocks' copies count on the first block's barrier
               const uint32_t full = tc::of_leader(&bar.full[s.stage]);
               if (rank == 0) tc::mbar_expect(&bar.full[s.stage], 2 * bytes);
 #pragma unroll
@@ -457,7 +459,7 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
               for (int c = 0; c < kColsB / 64; ++c)
                 tc::tma_load_2d_pair(st + R::kStageA + c * 8192, &map_dy, full, dy0 + c * 64, (int)r);
             } else {
-              uint64_t* full = CG == 2 && !X8 && rank != 0 ? &bar.tail_full[s.stage] : &bar.full[s.stage];
+              uint64_t* full = rank != 0 ? &bar.tail_full[s.stage] : &bar.full[s.stage];
               tc::mbar_expect(full, bytes);
               if constexpr (X8) {
                 tc::tma_load_2d(st, &map_x, full, x.k0, (int)r);
@@ -470,7 +472,7 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
                 tc::tma_load_2d(st + R::kStageA + c * 8192, &map_dy, full, dy0 + c * 64, (int)r);
             }
             ++issued;
-            if (CG == 2 && !X8) bar.copied = (uint32_t)issued;
+            if (CG == 2) bar.copied = (uint32_t)issued;
             s.next<R::kStages>();
           }
         }
@@ -478,13 +480,14 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         if (rank != 0) ok = tc::mbar_wait(&bar.done, 0) && ok;  // as in k_linear_rows_tc
         if (!ok) {
           latch_status(p.status, MT_ECUDA);
-          if (X8 || rank == 0) drain<R::kStages>(bar, s, issued);
+          if (rank == 0) drain<R::kStages>(bar, s, issued);
         }
       }
     }
     // Plain x: the rows past the chunk's end in its last stage belong to others; warp 1 zeroes them in both operands, so
     // that nothing of them (an infinity or NaN too) reaches the sum.  The second block of a pair does so for its own
-    // copies, which count on a barrier of its own in that stage, and tells the first.  8-bit x: the widening warps do it.
+    // copies, which count on a barrier of its own in that stage, and hands them over to the first.  8-bit x: the widening
+    // warps do it.
     if (warp == 1) {
       constexpr uint32_t instr = tc::instr_bf16(kRowsD, BN, true, true);
       Slot s;
@@ -493,7 +496,7 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
       bool ok = true;
       if (rank != 0) {
         uint32_t seq = 0;  // stages before this tile
-        for (long long r0 = 0; r0 * units < total && ok && !X8; ++r0) {
+        for (long long r0 = 0; r0 * units < total && ok; ++r0) {
           const long long t = dealt(r0, unit, units);
           if (t >= total) continue;
           const Tile x = tile_of(t);
@@ -506,7 +509,7 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
           if (!ok) break;
           tail_phase ^= 1u << stage;
           zero_rows(ring + stage * R::kStage, (kBM + kColsB) / 64, left, lane);
-          if (lane == 0) arrive<CG>(&bar.tail_ready[stage]);
+          if (lane == 0) tc::mbar_hand_over_at(tc::of_leader(&bar.tail_ready[stage]));
         }
       }
       for (long long r0 = 0; rank == 0 && r0 * units < total && ok; ++r0) {
@@ -525,7 +528,7 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
           if (!X8 && left < kBK) {
             zero_rows(st, (kBM + kColsB) / 64, left, lane);
             if constexpr (CG == 2) {
-              ok = __all_sync(kFull, tc::mbar_wait(&bar.tail_ready[s.stage], tail_phase >> s.stage & 1));
+              ok = __all_sync(kFull, tc::mbar_wait<true>(&bar.tail_ready[s.stage], tail_phase >> s.stage & 1));
               if (!ok) break;
               tail_phase ^= 1u << s.stage;
             }
@@ -673,7 +676,7 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
             }
             tc::fence_async_proxy();
             __syncwarp();
-            if (lane == 0) arrive<CG>(&bar.ready[stage]);
+            if (lane == 0) tc::mbar_arrive(&bar.ready[stage]);
           }
           // the part before this one: its products are done or nearly so, and this part's go on meanwhile
           if (part > 0 && ok) read_out();
@@ -757,7 +760,9 @@ cudaError_t weights_tc(const CUtensorMap& x, const CUtensorMap& dy, const Linear
 
 template <bool X8>
 cudaError_t weights_tc(const CUtensorMap& x, const CUtensorMap& dy, const LinearWeights& p, int bn, bool pair, cudaStream_t s) {
-  if (pair) return weights_tc<256, X8, 2>(x, dy, p, s);
+  if constexpr (!X8) {
+    if (pair) return weights_tc<256, X8, 2>(x, dy, p, s);
+  }
   return bn == 256 ? weights_tc<256, X8, 1>(x, dy, p, s) : bn == 128 ? weights_tc<128, X8, 1>(x, dy, p, s)
                                                                      : weights_tc<64, X8, 1>(x, dy, p, s);
 }
@@ -796,14 +801,14 @@ bool linear_weights_fits_tc(const LinearWeights& p) {
   return p.x.ld % 8 == 0 && is_aligned(p.x.data, 16);
 }
 
-Cut cut_of(int64_t n, int32_t groups, int32_t k, int32_t m) {
+Cut cut_of(int64_t n, int32_t groups, int32_t k, int32_t m, bool pairs) {
   // the tiles' width goes by the chunks that the rows may make
   const long long chunks = groups + n / 4096;
   Cut c;
   c.bn = tile_width(m, chunks * ((k + kBM - 1) / kBM));
-  // Whole calls, single blocks against pairs: 490,011 x 256 x 512 from 8 bits 157 against 142 us, 114,468 x 728 x 720 124
-  // against 116, 65,536 x 1024 x 1024 in 8 groups 127 against 127.
-  c.pair = c.bn == 256 && k > kBM && n / 512 * ((k + 255) / 256) * ((m + 255) / 256) >= sm_count() / 2;
+  // Whole calls, single blocks against pairs: 114,468 x 728 x 720 124 against 116 us, 65,536 x 1024 x 1024 in 8 groups 127
+  // against 127.
+  c.pair = pairs && c.bn == 256 && k > kBM && n / 512 * ((k + 255) / 256) * ((m + 255) / 256) >= sm_count() / 2;
   const int across = c.pair ? 2 * kBM : kBM;
   c.tiles = ((k + across - 1) / across) * ((m + c.bn - 1) / c.bn);
   c.units = std::max(1, sm_count() / (c.pair ? 2 : 1));

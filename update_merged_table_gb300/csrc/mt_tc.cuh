@@ -29,15 +29,27 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 
 // Whether the barrier's phase of this parity is over.  The hardware suspends the thread for a while if it is not: some
 // microseconds, also where a try asks for a millisecond (2000 such tries were over within 21 ms), so tries measure no time.
+// OF_PAIR: what the other block of a pair wrote before it arrived is seen afterwards.
+template <bool OF_PAIR>
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(bar), "r"(parity)
-      : "memory");
+  if constexpr (OF_PAIR) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  }
   return done != 0;
 }
 __device__ __forceinline__ uint64_t nanoseconds() {
@@ -50,12 +62,13 @@ __device__ __forceinline__ uint64_t nanoseconds() {
 // that to stand still, after kWaitTries tries), so no wait is endless.  What is waited for takes microseconds.
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kWaitTries = 1 << 26;
+template <bool OF_PAIR = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   const uint32_t a = smem_addr(bar);
-  if (mbar_try(a, parity)) return true;
+  if (mbar_try<OF_PAIR>(a, parity)) return true;
   const uint64_t start = nanoseconds();
   for (int i = 0; i < kWaitTries; ++i) {
-    if (mbar_try(a, parity)) return true;
+    if (mbar_try<OF_PAIR>(a, parity)) return true;
     if (nanoseconds() - start > kWaitNs) return false;
   }
   return false;
@@ -78,8 +91,15 @@ __device__ __forceinline__ uint32_t of_leader(const void* p) {
   asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_addr(p)));
   return r;
 }
+// An arrival at the other block's barrier that orders execution only (its release ends at this block): enough after a
+// tcgen05 fence, where the products that follow overwrite tensor memory that has been read out; no shared or global memory
+// passes through it.
 __device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// One that also hands over what this thread wrote, or saw written, in its block's shared memory (waited for with OF_PAIR).
+__device__ __forceinline__ void mbar_hand_over_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
