@@ -298,7 +298,8 @@ int mt_backward_adam_pooled(mt_table* t, const mt_lookup_result* res, int64_t n,
  * the backward.  Conventions of this section:
  *  - A row tensor is n rows of d columns of `dtype` (MT_F32 or MT_BF16), row i
  *    at data + i * ld elements, d <= ld < 2^31: a slice of columns of a wider
- *    tensor is a row tensor; n < 2^31.  Any element-aligned pointer and stride is taken; rows
+ *    tensor is a row tensor; n <= MT_MAX_BLOCK_ROWS (checkpoints on their own,
+ *    mt_pack8 and mt_unpack8: n < 2^31).  Any element-aligned pointer and stride is taken; rows
  *    that all start on 16 bytes, with widths that are multiples of 8, take
  *    faster kernels.
  *  - Group g holds the rows [offsets[g], offsets[g+1]); offsets is device
@@ -314,6 +315,7 @@ int mt_backward_adam_pooled(mt_table* t, const mt_lookup_result* res, int64_t n,
  *    once to `dtype`.  No atomics: the same call gives the same bits. */
 #define MT_MAX_GROUPS 1024
 #define MT_MAX_BLOCK_DIM 8192
+#define MT_MAX_BLOCK_ROWS 0x7FFFF000 /* 2^31 - 4096: a row's number plus a tile's rows fits 32 bits */
 #define MT_PACK_BLOCK 32
 
 /* A row tensor as plain rows (data, ld), in 8 bits (codes, exps; data NULL),

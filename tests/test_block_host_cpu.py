@@ -1,0 +1,25 @@
+"""The dense block's host side without a GPU: the limits of its calls, and what building and importing it needs."""
+import ctypes
+
+import pytest
+
+import update_merged_table_gb300 as mt
+from test_block_cpu import P, Rows, lib, norm_config  # noqa: F401 (lib: the built library)
+
+MOST_ROWS = (1 << 31) - 4096
+
+
+def test_row_numbers_leave_room_for_a_tile(lib):  # noqa: F811
+    """A kernel adds up to a few hundred rows to a row's number in 32 bits: batches that close to 2^31 are refused."""
+    x = Rows(P, 64, None, None)
+    packed = Rows(None, 0, P, P)
+    row = Rows(P, 64, None, None)
+    for n, code, size in ((MOST_ROWS, mt.MT_ENOSPACE, True), (MOST_ROWS + 1, mt.MT_EINVAL, False), ((1 << 31) - 1, mt.MT_EINVAL, False)):
+        assert (lib.mt_group_linear_workspace_bytes(n, 2, 64, 32) > 0) == size
+        assert (lib.mt_gated_norm_workspace_bytes(n, 64, 1) > 0) == size
+        assert lib.mt_group_linear_backward(P, 32, ctypes.byref(x), P, P, 2, n, 64, 32, mt.MT_BF16, None, 0, P, None, None, 0, None) == code
+        assert lib.mt_gated_norm_backward(ctypes.byref(norm_config(n=n)), *(ctypes.byref(r) for r in (row, row, packed, row, packed, row, row, row)),
+                                          P, None, P, P, None, None, 0, None) == code
+        if not size:
+            assert lib.mt_group_linear_forward(P, 64, P, P, 2, n, 64, 32, mt.MT_BF16, P, 32, None, None) == code
+            assert lib.mt_gated_norm_forward(ctypes.byref(norm_config(n=n)), *(ctypes.byref(row),) * 5, None) == code

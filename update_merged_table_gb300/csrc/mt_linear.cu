@@ -412,7 +412,7 @@ size_t partial_bytes(int64_t n, int32_t groups, int32_t k, int32_t m) {
 int linear_check(const int64_t* offsets, int32_t groups, int64_t n, int32_t k, int32_t m, int dtype,
                  const int32_t* status) {
   if (dtype != MT_F32 && dtype != MT_BF16) return MT_EINVAL;
-  if (n < 0 || n > 0x7FFFFFFF || groups < 1 || groups > MT_MAX_GROUPS) return MT_EINVAL;
+  if (n < 0 || n > MT_MAX_BLOCK_ROWS || groups < 1 || groups > MT_MAX_GROUPS) return MT_EINVAL;
   if (k < 1 || k > MT_MAX_BLOCK_DIM || m < 1 || m > MT_MAX_BLOCK_DIM) return MT_EINVAL;
   if (offsets == nullptr || !is_aligned(offsets, 8) || !is_aligned(status, 4)) return MT_EINVAL;
   return MT_OK;
@@ -530,7 +530,7 @@ int mt_group_linear_forward(const void* x, int64_t ldx, const void* w, const int
 
 size_t mt_group_linear_workspace_bytes(int64_t n, int32_t groups, int32_t in_dim, int32_t out_dim) {
   using namespace mt;
-  if (n < 0 || n > 0x7FFFFFFF || groups < 1 || groups > MT_MAX_GROUPS || in_dim < 1 || in_dim > MT_MAX_BLOCK_DIM || out_dim < 1 || out_dim > MT_MAX_BLOCK_DIM)
+  if (n < 0 || n > MT_MAX_BLOCK_ROWS || groups < 1 || groups > MT_MAX_GROUPS || in_dim < 1 || in_dim > MT_MAX_BLOCK_DIM || out_dim < 1 || out_dim > MT_MAX_BLOCK_DIM)
     return 0;
   return partial_bytes(n, groups, in_dim, out_dim) + (widened_first(in_dim) ? align_up((size_t)n * in_dim * 2, 256) : 0);
 }

@@ -760,7 +760,7 @@ int bwd_blocks(long long n, int d, int elem, bool bias) {
 
 int norm_params(const mt_gated_norm* c, NormParams& p) {
   if (c == nullptr) return MT_EINVAL;
-  if (c->n < 0 || c->n > 0x7FFFFFFF || c->dim < 1 || c->dim > MT_MAX_BLOCK_DIM) return MT_EINVAL;
+  if (c->n < 0 || c->n > MT_MAX_BLOCK_ROWS || c->dim < 1 || c->dim > MT_MAX_BLOCK_DIM) return MT_EINVAL;
   if (c->groups < 1 || c->groups > MT_MAX_GROUPS || (c->offsets == nullptr && c->groups != 1)) return MT_EINVAL;
   if (c->dtype != MT_F32 && c->dtype != MT_BF16) return MT_EINVAL;
   if (c->kind != MT_NORM_RMS && c->kind != MT_NORM_LAYER) return MT_EINVAL;
@@ -893,7 +893,7 @@ int mt_gated_norm_forward(const mt_gated_norm* cfg, const mt_rows* x, const mt_r
 
 size_t mt_gated_norm_workspace_bytes(int64_t n, int32_t dim, int32_t groups) {
   using namespace mt;
-  if (n < 0 || n > 0x7FFFFFFF || dim < 1 || dim > MT_MAX_BLOCK_DIM || groups < 1 || groups > MT_MAX_GROUPS) return 0;
+  if (n < 0 || n > MT_MAX_BLOCK_ROWS || dim < 1 || dim > MT_MAX_BLOCK_DIM || groups < 1 || groups > MT_MAX_GROUPS) return 0;
   return align_up(((size_t)bwd_blocks(n, dim, 2, false) + groups) * kSums * dim * 4, 256);
 }
 
