@@ -94,6 +94,62 @@ def test_norm_bias_sums_are_exact_on_whole_numbers(d, dtype, kind):
     assert torch.equal(nb.backward(dv, None, y=rows["y"], params=one, offsets=off).params.post_bias, want)
 
 
+# ---- graphs and threads ---------------------------------------------------------------------------------------------------
+
+def test_captured_calls_have_a_workspace_of_their_own(monkeypatch):
+    """A captured backward holds memory that lives as long as its graph: what the handle keeps for eager calls may grow
+    meanwhile, and a graph may be replayed on another stream beside them."""
+    gen = torch.Generator(device=DEV).manual_seed(34)
+    sizes, k, m = [500, 300], 64, 128
+    x, w, dy, off = rand(gen, 800, k), rand(gen, 2, m, k, scale=k ** -0.5), rand(gen, 800, m), offsets_of(sizes)
+    rows, p, noff = norm_case(35, sizes, 0, 0, 128, "bf16", "silu")
+    lin, nb = mt.GroupedLinear(2, k, m), mt.GatedNorm(128, num_groups=2)
+    args = (rows["dz"], rows["dh"], rows["y"], rows["u"], rows["z"])
+
+    def step():
+        g = nb.backward(*args, p, noff)
+        return [g.dx, g.params.scale, g.params.pre_weight, *lin.backward(dy, x, w, off)]
+
+    s = torch.cuda.Stream()
+    lin.reserve_workspace(800, stream=s)
+    nb.reserve_workspace(800, stream=s)
+    want = step()
+    torch.cuda.synchronize()
+    used = []
+    native = mt.block._native
+
+    class Seen:
+        def __getattr__(self, name):
+            f = getattr(native, name)
+            return lambda *a: (used.append(a[-1]), f(*a))[1]
+
+    monkeypatch.setattr(mt.block, "_native", Seen())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        held = step()
+    kept = {t.data_ptr() for h in (lin, nb) for t in h._ws.values()}
+    assert len(used) == 2 and not kept & {t.data_ptr() for t in used}
+    monkeypatch.undo()
+    used.clear()
+    lin.reserve_workspace(200_000, stream=s)
+    nb.reserve_workspace(200_000, stream=s)
+    other = torch.cuda.CUDAGraph()  # a capture begins by emptying the allocator's cache
+    with torch.cuda.graph(other, stream=s):
+        step()
+    for t in held:
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, held))
+    # nothing needs to be reserved before a capture
+    fresh, third = mt.GroupedLinear(2, k, m), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(third, stream=s):
+        got = fresh.backward(dy, x, w, off)
+    third.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[3]) and torch.equal(got[1], want[4])
+
+
 @pytest.mark.parametrize("n", [262_144 + 37])
 def test_a_launch_of_many_milliseconds_reports_no_error(n):
     """Pairs of blocks at work for 20 ms and more: what a block waits for until the launch's end is no fault."""

@@ -9,7 +9,11 @@ tokens sorted by expert.
 
 Outputs and workspaces are allocated on the stream the call runs on
 (``stream``, by default the current one); a handle may be used from several
-streams, each with its own workspace.
+streams, each with its own workspace.  A call captured in a CUDA graph takes
+its workspace from the graph's memory, like its outputs: nothing has to be
+reserved, and the graph may be replayed on any stream, beside other calls of
+the handle.  A graph writes errors to its handle's status word: keep the handle
+as long as the graph.
 """
 from __future__ import annotations
 
@@ -35,6 +39,14 @@ _TORCH = {"f32": torch.float32, "bf16": torch.bfloat16}
 _CODES = {torch.float32: MT_F32, torch.bfloat16: MT_BF16}
 _current_device = torch.cuda.current_device
 _raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _capturing(device) -> bool:
+    """Whether the device's current stream is being captured."""
+    if _current_device() == device.index:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(device):
+        return torch.cuda.is_current_stream_capturing()
 
 
 def _load_native():
@@ -175,14 +187,13 @@ class _Handle:
         self._ws = {}
 
     def _workspace(self, nbytes: int):
-        """The workspace of the current stream."""
+        """The workspace of the current stream; under capture one of the graph's own (a kept one may be replaced by a larger
+        one later, and its memory reused, while the graph still holds its address)."""
+        if _capturing(self.device):
+            return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
         stream = _raw_stream(self.device.index)
         buf = self._ws.get(stream)
         if buf is None or buf.numel() < nbytes:
-            if torch.cuda.is_current_stream_capturing():
-                # graphs captured earlier may hold the old buffer's address
-                raise RuntimeError("the workspace would have to grow during CUDA graph capture; call "
-                                   "reserve_workspace() on this stream with the largest batch before capturing")
             buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
             self._ws[stream] = buf
         return buf
@@ -236,7 +247,7 @@ class GroupedLinear(_Handle):
         return self._workspace(self.lib.mt_group_linear_workspace_bytes(n, self.num_groups, self.in_dim, self.out_dim))
 
     def reserve_workspace(self, n: int, stream=None):
-        """Allocate, on this stream, the workspace a backward over n rows needs (before a CUDA graph capture)."""
+        """Allocate, on this stream, the workspace a backward over n rows needs, so that calls up to that size do not."""
         _on(self.device, stream, self._reserved, n)
 
 
@@ -354,5 +365,5 @@ class GatedNorm(_Handle):
         return self._workspace(self.lib.mt_gated_norm_workspace_bytes(n, self.dim, self.num_groups))
 
     def reserve_workspace(self, n: int, stream=None):
-        """Allocate, on this stream, the workspace a backward over n rows needs (before a CUDA graph capture)."""
+        """Allocate, on this stream, the workspace a backward over n rows needs, so that calls up to that size do not."""
         _on(self.device, stream, self._reserved, n)
