@@ -277,6 +277,7 @@ class Table:
         self.dim = dim
         self.log2_slots = log2_slots
         self._ws = {}
+        self._captured = []  # workspaces whose addresses graphs hold: kept also when outgrown
 
     def __del__(self):
         h = getattr(self, "h", None)
@@ -295,14 +296,17 @@ class Table:
     def _workspace(self, kind: str, nbytes: int):
         torch = _torch()
         buf = self._ws.get(kind)
+        capturing = torch.cuda.is_current_stream_capturing()
         if buf is None or buf.numel() < nbytes:
-            if torch.cuda.is_current_stream_capturing():
+            if capturing:
                 # graphs captured earlier hold the old buffer's address, and a later capture may return the
                 # freed buffer to the driver: they would replay on unmapped memory
                 raise RuntimeError(f"the {kind} workspace would have to grow during CUDA graph capture; call "
                                    "reserve_workspaces() with the largest batch before capturing")
             buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
             self._ws[kind] = buf
+        if capturing and not any(b is buf for b in self._captured):
+            self._captured.append(buf)
         return buf
 
     def new_result(self, n: int, gather: bool = True, ranks: bool = True) -> LookupResult:
@@ -673,6 +677,7 @@ class MergedTables:
         self.device = self.tables[0].device
         self._pl = (_Placement * len(self.placement))(*[_Placement(g, t) for g, t in self.placement])
         self._ws = {}
+        self._captured = []  # workspaces whose addresses graphs hold: kept also when outgrown
 
     def group_sizes(self, feat_offsets):
         """IDs each merged table receives from a batch with these feature offsets."""
@@ -710,12 +715,15 @@ class MergedTables:
     def _workspace(self, kind: str, nbytes: int):
         torch = _torch()
         buf = self._ws.get(kind)
+        capturing = torch.cuda.is_current_stream_capturing()
         if buf is None or buf.numel() < nbytes:
-            if torch.cuda.is_current_stream_capturing():
+            if capturing:
                 raise RuntimeError(f"the grouped {kind} workspace would have to grow during CUDA graph capture; "
                                    "run one eager step with the largest batch before capturing")
             buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
             self._ws[kind] = buf
+        if capturing and not any(b is buf for b in self._captured):
+            self._captured.append(buf)
         return buf
 
     def backward_adam(self, results, grads, lr: float = 1e-3, beta1: float = 0.9, beta2: float = 0.999,
