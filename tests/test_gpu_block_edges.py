@@ -1,6 +1,9 @@
 """The dense block where rows are few, long, uneven or shared: sums that have one exact value, batches of which few rows are
 in a group, workspaces of captured graphs, calls from several threads, outputs that would overlap inputs."""
 
+import ctypes
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -148,6 +151,49 @@ def test_captured_calls_have_a_workspace_of_their_own(monkeypatch):
     third.replay()
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[3]) and torch.equal(got[1], want[4])
+
+
+def test_calls_from_several_threads_with_different_group_counts():
+    """One kernel launched with much and with little shared memory by threads of their own (the C calls run without the
+    interpreter's lock)."""
+    lib = mt.load_library()
+    gen = torch.Generator(device=DEV).manual_seed(36)
+    n, d = 64, 128
+    x = rand(gen, n, d)
+    bad = []
+
+    def worker(groups):
+        s = torch.cuda.Stream()
+        off = offsets_of([n] + [0] * (groups - 1))
+        w = torch.ones(groups, d, device=DEV)
+        h, y, weight = torch.empty_like(x), torch.empty_like(x), torch.zeros(groups, d, d, device=DEV, dtype=torch.bfloat16)
+        torch.cuda.synchronize()
+
+        class Rows(ctypes.Structure):
+            _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64), ("codes", ctypes.c_void_p), ("exps", ctypes.c_void_p)]
+
+        class Norm(ctypes.Structure):
+            _fields_ = [("n", ctypes.c_int64), ("dim", ctypes.c_int32), ("groups", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                        ("kind", ctypes.c_int32), ("gate", ctypes.c_int32), ("eps", ctypes.c_float), ("offsets", ctypes.c_void_p),
+                        ("status", ctypes.c_void_p)] + [(k, ctypes.c_void_p) for k in ("pw", "pb", "sc", "qw", "qb")]
+
+        c = Norm(n, d, groups, mt.MT_BF16, 0, 0, 1e-6, off.data_ptr(), None, None, None, None, w.data_ptr(), None)
+        rx, rh, none = Rows(x.data_ptr(), d), Rows(h.data_ptr(), d), Rows()
+        for _ in range(4000):
+            rc = lib.mt_gated_norm_forward(ctypes.byref(c), ctypes.byref(rx), ctypes.byref(none), ctypes.byref(none),
+                                           ctypes.byref(none), ctypes.byref(rh), s.cuda_stream)
+            rc2 = lib.mt_group_linear_forward(x.data_ptr(), d, weight.data_ptr(), off.data_ptr(), groups, n, d, d, mt.MT_BF16,
+                                              y.data_ptr(), d, None, s.cuda_stream) if groups < 32 else 0
+            if rc or rc2:
+                bad.append((groups, rc, rc2))
+        s.synchronize()
+
+    threads = [threading.Thread(target=worker, args=(g,)) for g in (1, 1024, 3, 700)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, (len(bad), bad[:5])
 
 
 @pytest.mark.parametrize("n", [262_144 + 37])

@@ -3,6 +3,8 @@
 // 8-bit form of a block of 32 columns.
 #pragma once
 
+#include <atomic>
+
 #include "mt_kernels.cuh"
 
 namespace mt {
@@ -401,6 +403,26 @@ __device__ __forceinline__ void put_packed8(const Rows& r, long long row, int ve
 // ---- host-side checks ------------------------------------------------------------------
 
 inline bool is_aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+// Lets a kernel have `most` bytes of dynamic shared memory, what its largest launch needs.  The limit belongs to the kernel
+// and the device, not to a launch: it is set once, to a constant, so that calls from several threads do not lower it for
+// one another.
+class SmemLimit {
+ public:
+  template <typename Kernel>
+  cudaError_t allow(Kernel kernel, size_t most) {
+    const int dev = current_device();
+    if (dev < 0) return cudaErrorInvalidDevice;
+    if (set_[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    if (e == cudaSuccess) set_[dev].store(true, std::memory_order_relaxed);
+    return e;
+  }
+
+ private:
+  std::atomic<bool> set_[kMaxDevices] = {};
+};
 
 inline size_t elem_bytes(int dtype) { return dtype == MT_F32 ? 4 : 2; }
 

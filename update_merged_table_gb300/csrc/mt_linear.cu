@@ -394,8 +394,6 @@ __global__ void __launch_bounds__(32 * kSumSlices) k_linear_sums(const LinearWei
   }
 }
 
-size_t rows_smem(int groups) { return (size_t)(groups + 1) * (8 + 4); }
-
 // Partial products of dW there is room for: as many as give every block (pair) kRounds tiles, if the rows allow any split
 // (a split leaves chunks of kMinChunk rows and more, so a group of one more than that makes two).
 constexpr int kRounds = 4;

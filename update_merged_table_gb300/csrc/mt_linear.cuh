@@ -44,6 +44,8 @@ struct LinearWeights {
   float* dw;      // [groups][M][K]
 };
 
+// Dynamic shared memory for the offsets and what is derived from them.
+inline size_t rows_smem(int groups) { return (size_t)(groups + 1) * (8 + 4); }
 inline size_t weights_smem(int groups) { return (size_t)(groups + 1) * (8 + 4 * 4); }
 
 // The rows of a chunk.  A group may be split into chunks whose products are summed afterwards, so that every block (pair)

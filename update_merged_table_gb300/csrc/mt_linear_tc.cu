@@ -34,7 +34,6 @@
 // (91% of it).  dW of 65,536 x 1024 x 1024 in 8 groups: 123 us and 9 us of sums
 // (1.12 PFLOP/s), from 8 bits 157 us, where the widening bounds it.
 #include <algorithm>
-#include <mutex>
 
 #include "mt_linear.cuh"
 #include "mt_tc.cuh"
@@ -713,13 +712,10 @@ int tile_width(int J, long long row_tiles) {
   return bn;
 }
 
-// Launches a kernel of 1024-aligned dynamic shared memory, in clusters of `pair` blocks.
+// Launches a kernel in clusters of `pair` blocks.
 template <typename Kernel, typename Params>
 cudaError_t launch_tc(Kernel kernel, int grid, int threads, size_t smem, int pair, cudaStream_t s, const CUtensorMap& a,
                       const CUtensorMap& b, const Params& p) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
@@ -740,9 +736,12 @@ template <int BN, bool B_MN, int CG>
 cudaError_t rows_tc(const CUtensorMap& a, const CUtensorMap& w, LinearRows p, cudaStream_t s) {
   p.jtiles = (p.J + BN - 1) / BN;
   const long long tiles = (p.n / (kBM * CG) + p.groups) * p.jtiles;
+  constexpr size_t ring = 1024 + Ring<BN, CG>::kBytes;  // the stages start on 1024 bytes
+  static SmemLimit limit;
+  const cudaError_t e = limit.allow(k_linear_rows_tc<BN, B_MN, CG>, ring + rows_smem(MT_MAX_GROUPS));
+  if (e != cudaSuccess) return e;
   MT_LAUNCH("k_linear_rows_tc", s);
-  return launch_tc(k_linear_rows_tc<BN, B_MN, CG>, tc_grid(tiles, CG), kWarpsTC * 32,
-                   1024 + Ring<BN, CG>::kBytes + (size_t)(p.groups + 1) * 12, CG, s, a, w, p);
+  return launch_tc(k_linear_rows_tc<BN, B_MN, CG>, tc_grid(tiles, CG), kWarpsTC * 32, ring + rows_smem(p.groups), CG, s, a, w, p);
 }
 
 template <int BN, bool X8, int CG>
@@ -753,9 +752,12 @@ cudaError_t weights_tc(const CUtensorMap& x, const CUtensorMap& dy, const Linear
     if (e != cudaSuccess) return e;
     if (a.numRegs < kRegsLaunch) return cudaErrorInvalidValue;
   }
+  constexpr size_t ring = 1024 + Ring<BN, CG>::kStages * Ring<BN, CG>::kStage;
+  static SmemLimit limit;
+  const cudaError_t e = limit.allow(k_linear_weights_tc<BN, X8, CG>, ring + weights_smem(MT_MAX_GROUPS));
+  if (e != cudaSuccess) return e;
   MT_LAUNCH("k_linear_weights_tc", s);
-  return launch_tc(k_linear_weights_tc<BN, X8, CG>, p.units * CG, kWarpsW * 32,
-                   1024 + Ring<BN, CG>::kStages * Ring<BN, CG>::kStage + weights_smem(p.groups), CG, s, x, dy, p);
+  return launch_tc(k_linear_weights_tc<BN, X8, CG>, p.units * CG, kWarpsW * 32, ring + weights_smem(p.groups), CG, s, x, dy, p);
 }
 
 template <bool X8>

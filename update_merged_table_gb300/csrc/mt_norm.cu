@@ -792,28 +792,26 @@ int norm_params(const mt_gated_norm* c, NormParams& p) {
 
 bool absent(const Rows& r) { return r.data == nullptr && r.codes == nullptr && r.exps == nullptr; }
 
-template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes) {
-  return cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
+size_t offsets_smem(int groups) { return (size_t)(groups + 1) * 8; }
 
 template <typename T, int MODE, int THREADS, int FORM>
 cudaError_t norm_fwd_as(const NormParams& p, cudaStream_t s) {
   const int teams = THREADS >> p.log_team;
   const int grid = grid_for((p.n + teams - 1) / teams * THREADS, THREADS, THREADS == 128 ? fwd_blocks_per_sm(sizeof(T)) : 1);
-  const size_t smem = (kStaged<T, MODE, THREADS> ? Stages<T, THREADS, 3>::kBytes : 0) + (size_t)(p.groups + 1) * 8;
-  const cudaError_t e = allow_smem(k_norm_fwd<T, MODE, THREADS, FORM>, smem);
+  constexpr size_t stages = kStaged<T, MODE, THREADS> ? Stages<T, THREADS, 3>::kBytes : 0;
+  static SmemLimit limit;
+  const cudaError_t e = limit.allow(k_norm_fwd<T, MODE, THREADS, FORM>, stages + offsets_smem(MT_MAX_GROUPS));
   if (e != cudaSuccess) return e;
-  k_norm_fwd<T, MODE, THREADS, FORM><<<grid, THREADS, smem, s>>>(p);
+  k_norm_fwd<T, MODE, THREADS, FORM><<<grid, THREADS, stages + offsets_smem(p.groups), s>>>(p);
   return cudaGetLastError();
 }
 template <typename T, int MODE, int THREADS, bool BIAS, int FORM>
 cudaError_t norm_bwd_as(const NormParams& p, cudaStream_t s) {
-  const size_t smem =
-      (kStaged<T, MODE, THREADS> ? Stages<T, THREADS, 5>::kBytes : 16 * THREADS * 4) + (size_t)(p.groups + 1) * 8;
-  const cudaError_t e = allow_smem(k_norm_bwd<T, MODE, THREADS, BIAS, FORM>, smem);
+  constexpr size_t stages = kStaged<T, MODE, THREADS> ? Stages<T, THREADS, 5>::kBytes : 16 * THREADS * 4;
+  static SmemLimit limit;
+  const cudaError_t e = limit.allow(k_norm_bwd<T, MODE, THREADS, BIAS, FORM>, stages + offsets_smem(MT_MAX_GROUPS));
   if (e != cudaSuccess) return e;
-  k_norm_bwd<T, MODE, THREADS, BIAS, FORM><<<p.blocks, THREADS, smem, s>>>(p);
+  k_norm_bwd<T, MODE, THREADS, BIAS, FORM><<<p.blocks, THREADS, stages + offsets_smem(p.groups), s>>>(p);
   return cudaGetLastError();
 }
 template <typename T, int MODE>
@@ -970,7 +968,7 @@ int mt_gated_norm_backward(const mt_gated_norm* cfg, const mt_rows* dz, const mt
   {
     MT_LAUNCH("k_norm_sums", s);
     const dim3 grid((p.d + 31) / 32, 2, p.groups);
-    k_norm_sums<<<grid, 32 * kSlices, (size_t)(p.groups + 1) * 8, s>>>(p);
+    k_norm_sums<<<grid, 32 * kSlices, offsets_smem(p.groups), s>>>(p);
   }
   return cudaGetLastError() == cudaSuccess ? MT_OK : MT_ECUDA;
 }
