@@ -196,6 +196,22 @@ def test_calls_from_several_threads_with_different_group_counts():
     assert not bad, (len(bad), bad[:5])
 
 
+# ---- long sums ---------------------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,n,k,m", [("f32", 1_970_003, 16, 16), ("bf16", 1_970_003, 24, 20), ("bf16", 1_970_003, 64, 64)])
+def test_weight_gradient_of_one_long_group(dtype, n, k, m):
+    """A chain of r adds of unit normal products is off by about 2^-24 * sqrt(r / 2) of its sum at most (each add by half a
+    unit in the last place of a partial sum that grows like the square root of the terms).  No chain has more than 1024
+    rows; the partial sums of those (at most n / 1024) make another."""
+    gen = torch.Generator(device=DEV).manual_seed(37)
+    x, dy = rand(gen, n, k, dtype=dtype), rand(gen, n, m, dtype=dtype)
+    off = offsets_of([n])
+    _, dw = mt.GroupedLinear(1, k, m, dtype=dtype).backward(dy, x, None, off, want_dx=False)
+    want = sum(dy[a:a + 65536].double().T @ x[a:a + 65536].double() for a in range(0, n, 65536))
+    off_by = (dw[0].double() - want).square().mean().sqrt() / want.square().mean().sqrt()
+    assert off_by <= 2.0 ** -24 * np.sqrt((1024 + n / 1024) / 2), float(off_by)
+
+
 @pytest.mark.parametrize("n", [262_144 + 37])
 def test_a_launch_of_many_milliseconds_reports_no_error(n):
     """Pairs of blocks at work for 20 ms and more: what a block waits for until the launch's end is no fault."""
