@@ -20,6 +20,19 @@ def small_integers(gen, *shape, dtype=torch.bfloat16):
     return torch.randint(-2, 3, shape, generator=gen, device=DEV).to(dtype)
 
 
+def time_of(f):
+    times = []
+    for _ in range(6):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda.synchronize()
+        a.record()
+        f()
+        b.record()
+        b.synchronize()
+        times.append(a.elapsed_time(b))
+    return min(times[1:])
+
+
 # ---- few rows in groups -----------------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("n,sizes,lead", [(5000, [3], 0), (5000, [1, 0, 2], 4990), (100_000, [40, 0, 1, 300], 7), (70_000, [0, 0], 5)])
@@ -232,3 +245,16 @@ def test_a_launch_of_many_milliseconds_reports_no_error(n):
         want = (dy[a:b, -8:].double().T @ x[a:b, -8:].double()).cpu().numpy()
         # sums of 512 rows are cut off at each step of 16 rows (2^-23 of the sum at most), and added up in fp32
         near(dw[g, -8:, -8:], want, (32 + n / 512) * F * np.sqrt(n) * 4, "dw")
+
+
+@pytest.mark.parametrize("dtype,k,m", [("bf16", 64, 64), ("f32", 16, 16)])
+def test_weight_gradient_of_one_long_group_takes_every_block(dtype, k, m):
+    """One group, or one beside a small one, in no more than twice the time of 61 equal ones."""
+    gen = torch.Generator(device=DEV).manual_seed(42)
+    n = 61 * 16000
+    x, dy = rand(gen, n, k, dtype=dtype), rand(gen, n, m, dtype=dtype)
+    times = []
+    for sizes in ([16000] * 61, [n], [100, n - 100]):
+        lin, off = mt.GroupedLinear(len(sizes), k, m, dtype=dtype), offsets_of(sizes)
+        times.append(time_of(lambda: lin.backward(dy, x, None, off, want_dx=False)))
+    assert max(times[1:]) <= 2 * times[0], times

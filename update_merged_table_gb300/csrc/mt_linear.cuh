@@ -6,7 +6,7 @@
 namespace mt {
 
 constexpr int kMinChunk = 256;  // fewest rows of a chunk that a group is split into
-constexpr int kSplits = 32;     // ways of splitting that choose_chunk weighs
+constexpr int kSplits = 32;     // ways of splitting that choose_chunk weighs at a time
 
 // C[row, j] = sum over i < I of A[row, i] * w[g * wg + i * wi + j * wj], for the rows of group g; rows in no group
 // become zeros.
@@ -52,11 +52,14 @@ inline size_t weights_smem(int groups) { return (size_t)(groups + 1) * (8 + 4 * 
 // gets about the same work however ragged the groups are; a partial product costs a write and a read of dW's size.  What
 // is weighed is the longest group in 1, 2, ... kSplits equal chunks, by the time of the last block in units of 64 rows:
 // rounds of tiles of that many rows, or what a block has on average plus a part of a tile where the rounds differ in
-// length (plan_chunks deals them out by length), and per round the tile's last read-out and store.  Every thread calls
-// it, after load_offsets.
+// length (plan_chunks deals them out by length), and per round the tile's last read-out and store.  Where kSplits chunks of
+// the longest group are still longer than that average (a long group, few tiles), as many finer splits follow, in even ratios
+// up to the partial products that there is room for: one group of 1,970,003 x 64 x 64 398 us with kSplits chunks, 128 with
+// these.  Every thread calls it, after load_offsets.
 struct ChunkChoice {
   int count[kSplits], split[kSplits];  // chunks; those of groups that have several
   int longest, rows, chunk;            // in units of 64 rows, and in rows
+  bool finer;
 };
 __device__ __forceinline__ int choose_chunk(const LinearWeights& p, const long long* s_off, ChunkChoice& c) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -76,45 +79,54 @@ __device__ __forceinline__ int choose_chunk(const LinearWeights& p, const long l
       c.rows = rows;
     }
   }
-  __syncthreads();
-  const int s = max(kMinChunk / 64, (c.longest + lane) / (lane + 1));  // this lane's chunk
-  const float inv = 1.0f / (float)s;
-  int count = 0, split = 0;
-  for (int g = warp; g < p.groups; g += warps) {
-    const int u = units_of(g);
-    int k = (int)((float)u * inv);  // within one of u / s
-    k += (k + 1) * s <= u;
-    k -= k * s > u;
-    k += k * s < u;  // rounded up
-    count += k;
-    split += k > 1 ? k : 0;
-  }
-  atomicAdd(&c.count[lane], count);  // integers: any order gives the same sum
-  atomicAdd(&c.split[lane], split);
-  __syncthreads();
-  if (warp == 0) {
-    const float rounds = ceilf((float)c.count[lane] * (float)p.tiles / (float)p.units);
-    const float mean = (float)c.rows * (float)p.tiles / (float)p.units;
-    const int sp = c.split[lane];
-    float cost = fmaxf(fmaxf(mean, (float)min(s, c.longest)), fminf(rounds * (float)s, mean + 0.35f * (float)s)) + rounds * p.round_cost +
-                 (float)sp * p.slot_cost + (sp > 0 ? p.sums_cost : 0.0f);
-    if (sp > p.slots) cost = 3.0e38f;  // lane 0 splits nothing: it always has room
-    int best = lane;
-    for (int o = 16; o > 0; o >>= 1) {  // the cheapest, of equals the one that splits least
-      const float oc = __shfl_xor_sync(kFull, cost, o);
-      const int ob = __shfl_xor_sync(kFull, best, o);
-      if (oc < cost || (oc == cost && ob < best)) {
-        cost = oc;
-        best = ob;
+  float least = 3.0e38f;  // what the chunk chosen so far costs
+  for (int pass = 0; pass < 2; ++pass) {
+    __syncthreads();
+    const int parts = pass == 0 ? lane + 1 : (int)(kSplits * exp2f(log2f((float)p.slots / kSplits) * (float)(lane + 1) / 32.0f));
+    const int s = max(kMinChunk / 64, (c.longest + parts - 1) / parts);  // this lane's chunk
+    const float inv = 1.0f / (float)s;
+    int count = 0, split = 0;
+    for (int g = warp; g < p.groups; g += warps) {
+      const int u = units_of(g);
+      int k = (int)((float)u * inv);  // within one of u / s
+      k += (k + 1) * s <= u;
+      k -= k * s > u;
+      k += k * s < u;  // rounded up
+      count += k;
+      split += k > 1 ? k : 0;
+    }
+    atomicAdd(&c.count[lane], count);  // integers: any order gives the same sum
+    atomicAdd(&c.split[lane], split);
+    __syncthreads();
+    if (warp == 0) {
+      const float rounds = ceilf((float)c.count[lane] * (float)p.tiles / (float)p.units);
+      const float mean = (float)c.rows * (float)p.tiles / (float)p.units;
+      const int sp = c.split[lane];
+      float cost = fmaxf(fmaxf(mean, (float)min(s, c.longest)), fminf(rounds * (float)s, mean + 0.35f * (float)s)) + rounds * p.round_cost +
+                   (float)sp * p.slot_cost + (sp > 0 ? p.sums_cost : 0.0f);
+      if (sp > p.slots) cost = 3.0e38f;  // lane 0 of the first pass splits nothing: it always has room
+      int best = lane;
+      for (int o = 16; o > 0; o >>= 1) {  // the cheapest, of equals the one that splits least
+        const float oc = __shfl_xor_sync(kFull, cost, o);
+        const int ob = __shfl_xor_sync(kFull, best, o);
+        if (oc < cost || (oc == cost && ob < best)) {
+          cost = oc;
+          best = ob;
+        }
       }
+      const int chosen = __shfl_sync(kFull, s, best) * 64;
+      const int finest = __shfl_sync(kFull, s, 31);
+      c.count[lane] = c.split[lane] = 0;
+      if (lane == 0) {
+        if (cost < least) c.chunk = chosen;
+        c.finer = p.slots > kSplits && finest > kMinChunk / 64 && (float)finest > mean;
+      }
+      least = fminf(least, cost);
     }
-    const int chosen = __shfl_sync(kFull, s, best) * 64;
-    if (lane == 0) {
-      c.chunk = chosen;
-      if (blockIdx.x == 0) *p.chosen = chosen;
-    }
+    __syncthreads();
+    if (!c.finer) break;
   }
-  __syncthreads();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.chosen = c.chunk;
   return c.chunk;
 }
 
