@@ -10,7 +10,7 @@ import torch
 
 import update_merged_table_gb300 as mt
 import block_reference as R
-from test_gpu_block import DEV, F, check_backward, near, norm_case, offsets_of, rand, values, wide
+from test_gpu_block import DEV, F, check_backward, near, norm_case, offsets_of, rand, rounding, values, wide
 
 pytestmark = pytest.mark.gpu
 
@@ -258,3 +258,21 @@ def test_weight_gradient_of_one_long_group_takes_every_block(dtype, k, m):
         lin, off = mt.GroupedLinear(len(sizes), k, m, dtype=dtype), offsets_of(sizes)
         times.append(time_of(lambda: lin.backward(dy, x, None, off, want_dx=False)))
     assert max(times[1:]) <= 2 * times[0], times
+
+
+# ---- one group has all the rows of a batch that is small for its groups ---------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,groups,n,k,m", [("bf16", 256, 512, 512, 256), ("bf16", 64, 128, 512, 64), ("f32", 64, 512, 256, 128)])
+def test_forward_of_few_rows_does_not_depend_on_their_group(dtype, groups, n, k, m):
+    """All rows in one group: the same values, in no more than a few times the time of rows spread over the groups."""
+    gen = torch.Generator(device=DEV).manual_seed(38)
+    x, w = rand(gen, n, k, dtype=dtype), rand(gen, groups, m, k, dtype=dtype, scale=k ** -0.5)
+    lin = mt.GroupedLinear(groups, k, m, dtype=dtype)
+    even = offsets_of([n // groups] * groups)
+    one = offsets_of([0] * 3 + [n] + [0] * (groups - 4))
+    for off in (even, one):
+        want, size = R.linear_forward(wide(x), wide(w), wide(off))
+        near(lin.forward(x, w, off), want, rounding(dtype) * np.abs(want) + (k + 16) * F * size)
+    out = torch.empty(n, m, device=DEV, dtype=x.dtype)
+    spread, alone = (time_of(lambda o=o: lin.forward(x, w, o, out=out)) for o in (even, one))
+    assert alone <= 4 * spread, (alone, spread)

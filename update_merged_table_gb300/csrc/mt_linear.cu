@@ -157,73 +157,61 @@ __global__ void __launch_bounds__(kThreadsL) k_linear_rows(const LinearRows p) {
 // A few tokens being served: every weight of the groups that have a row is read once and multiplied by a row or two, so
 // the weights' bytes and the latency of one load are all there is.  A warp takes kOuts neighbouring rows of W_g (32 lanes
 // by eight columns a step, the loads in flight together) against kFewRows rows of x at once; lanes then join by shuffles.
-// More rows at once take registers, and with them warps that keep loads in flight (eight rows: 6.1 us for 8 tokens on 8
-// experts of 512 x 1024, two rows: 4.7).
-constexpr int kFewRows = 2, kOuts = 4;
+// A group's further rows are tasks of their own, so a batch costs the same whichever groups its rows are in (512 rows to
+// 64 groups of 256 x 128 in fp32 10.4 us, all to one 10.0).  The SMs hold every block at once, three an SM: four would leave
+// 64 registers a thread and spills (8 tokens on 8 experts of 512 x 1024 in bf16 5.0 against 4.1 us), and more blocks than
+// fit would each read the offsets anew (128 tokens on 64 experts 21.0 against 18.4).
+constexpr int kFewRows = 2, kOuts = 4, kFewBlocks = 3;
 
 template <typename T>
-__global__ void __launch_bounds__(256, 4) k_linear_few(const LinearRows p) {
+__global__ void __launch_bounds__(256, kFewBlocks) k_linear_few(const LinearRows p) {
   extern __shared__ long long s_off[];
-  __shared__ int s_active;
-  int* s_group = reinterpret_cast<int*>(s_off + p.groups + 1);  // the groups that have rows
+  int* s_cum = reinterpret_cast<int*>(s_off + p.groups + 1);
   load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
+  count_tiles(s_off, p.groups, kFewRows, s_cum);
   const int lane = threadIdx.x & 31;
-  if (threadIdx.x < 32) {
-    int active = 0;
-    for (int g0 = 0; g0 < p.groups; g0 += 32) {
-      const int g = g0 + lane;
-      const bool on = g < p.groups && s_off[g] < s_off[g + 1];
-      const unsigned mask = __ballot_sync(kFull, on);
-      if (on) s_group[active + __popc(mask & ((1u << lane) - 1u))] = g;
-      active += __popc(mask);
-    }
-    if (lane == 0) s_active = active;
-  }
-  __syncthreads();
   T* C = static_cast<T*>(p.c);
   zero_outside<T>(s_off, p.groups, p.n, C, p.ldc, p.J, blockDim.x, threadIdx.x);
-  const int per_group = (p.J + kOuts - 1) / kOuts;
+  const int per_tile = (p.J + kOuts - 1) / kOuts;
   const int warps = (gridDim.x * blockDim.x) >> 5;
-  for (int t = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; t < s_active * per_group; t += warps) {
-    const int q = t / per_group, j0 = (t - q * per_group) * kOuts, g = s_group[q];
+  for (int t = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; t < s_cum[p.groups] * per_tile; t += warps) {
+    const int q = t / per_tile, j0 = (t - q * per_tile) * kOuts, g = tile_group(s_cum, p.groups, q);
     const T* W = static_cast<const T*>(p.w) + (size_t)g * p.wg + (size_t)j0 * p.wj;
     const int outs = min(kOuts, p.J - j0);
-    for (int r0 = (int)s_off[g]; r0 < (int)s_off[g + 1]; r0 += kFewRows) {
-      const int rows = min(kFewRows, (int)s_off[g + 1] - r0);
-      f32x2 acc[kFewRows][kOuts] = {};
+    const int r0 = (int)s_off[g] + (q - s_cum[g]) * kFewRows, rows = min(kFewRows, (int)s_off[g + 1] - r0);
+    f32x2 acc[kFewRows][kOuts] = {};
 #pragma unroll 2
-      for (int i = lane * 8; i < p.I; i += 256) {
-        Raw8<T> w[kOuts], x[kFewRows];  // every load of the step issued before the first is used
+    for (int i = lane * 8; i < p.I; i += 256) {
+      Raw8<T> w[kOuts], x[kFewRows];  // every load of the step issued before the first is used
 #pragma unroll
-        for (int o = 0; o < kOuts; ++o)
-          w[o] = load8<T, true>(Rows{const_cast<T*>(W), (int64_t)p.wj, nullptr, nullptr}, o < outs ? o : 0, i >> 3, p.I);
+      for (int o = 0; o < kOuts; ++o)
+        w[o] = load8<T, true>(Rows{const_cast<T*>(W), (int64_t)p.wj, nullptr, nullptr}, o < outs ? o : 0, i >> 3, p.I);
 #pragma unroll
-        for (int r = 0; r < kFewRows; ++r)
-          if (r < rows) x[r] = load8<T, true>(Rows{const_cast<void*>(p.a), p.lda, nullptr, nullptr}, r0 + r, i >> 3, p.I);
-#pragma unroll
-        for (int r = 0; r < kFewRows; ++r) {
-          if (r >= rows) break;
-          f32x2 v[4];
-          widen8<T>(x[r], false, v);
-#pragma unroll
-          for (int o = 0; o < kOuts; ++o) {
-            f32x2 f[4];
-            widen8<T>(w[o], false, f);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[r][o] = fma2(v[j], f[j], acc[r][o]);
-          }
-        }
-      }
+      for (int r = 0; r < kFewRows; ++r)
+        if (r < rows) x[r] = load8<T, true>(Rows{const_cast<void*>(p.a), p.lda, nullptr, nullptr}, r0 + r, i >> 3, p.I);
 #pragma unroll
       for (int r = 0; r < kFewRows; ++r) {
         if (r >= rows) break;
+        f32x2 v[4];
+        widen8<T>(x[r], false, v);
 #pragma unroll
         for (int o = 0; o < kOuts; ++o) {
-          float s = pair_sum(acc[r][o]);
+          f32x2 f[4];
+          widen8<T>(w[o], false, f);
 #pragma unroll
-          for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
-          if (lane == o && o < outs) C[row_offset(r0 + r, p.ldc) + j0 + o] = from_f<T>(s);
+          for (int j = 0; j < 4; ++j) acc[r][o] = fma2(v[j], f[j], acc[r][o]);
         }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kFewRows; ++r) {
+      if (r >= rows) break;
+#pragma unroll
+      for (int o = 0; o < kOuts; ++o) {
+        float s = pair_sum(acc[r][o]);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
+        if (lane == o && o < outs) C[row_offset(r0 + r, p.ldc) + j0 + o] = from_f<T>(s);
       }
     }
   }
@@ -429,18 +417,22 @@ int linear_check(const int64_t* offsets, int32_t groups, int64_t n, int32_t k, i
   return MT_OK;
 }
 
-// Rows per group, on average, up to which the forward goes to k_linear_few: each further pair of a group's rows reads its
-// weights again (from L2), where the tiles read them once.  Against the tensor cores two are the limit (512 x 1024, bf16:
-// 8 tokens on 8 experts 4.7 against 7.4 us, 32 tokens 8.9 against 7.3; one expert: 1 token 3.9 against 5.9, 4 tokens 6.5
-// against 5.8), against the fp32 pipes eight (fp32: 64 tokens on 8 experts 22 against 34 us, 128 tokens 40 against 35).
-constexpr int kFewTc = 2, kFewPipes = 8;
+// The forward of few rows goes to k_linear_few: of up to kFewTc rows per group on average (against the tensor cores) or
+// kFewPipes (against the fp32 pipes), as long as each warp that the SMs hold has no more than kTasksTc or kTasksPipes tasks.
+// Each further pair of a group's rows reads its weights again (from L2), where the tiles read them once.  Measured, warm and
+// with weights from HBM, against the tiles: bf16 512 x 1024, 8 tokens on 8 experts 4.1 and 10.2 us against 7.7 and 12.3, 64
+// on 32 (3.4 tasks a warp) 10.2 and 18.4 against 11.7 and 18.5, 128 on 64 (6.7) 18.4 and 26.7 against 10.8 and 24.6; 16 on 8
+// of 2048 x 2048 15.7 against 33.7.  fp32: 64 on 8 of 512 x 1024 14.2 against 34.4, 8192 on 1024 of 128 x 128 (40 tasks) 103
+// against 109.
+constexpr int kFewTc = 2, kFewPipes = 8, kTasksTc = 3, kTasksPipes = 12;
 
 cudaError_t launch_linear_rows(LinearRows p, int dtype, cudaStream_t s) {
   const bool tc = dtype == MT_BF16 && linear_rows_fits_tc(p);
-  if (p.n <= (long long)(tc ? kFewTc : kFewPipes) * p.groups && p.wi == 1 && p.I % 8 == 0 && (p.lda * elem_bytes(dtype)) % 16 == 0 && is_aligned(p.a, 16) &&
-      is_aligned(p.w, 16)) {
-    const long long tasks = std::min<long long>(p.n, p.groups) * ((p.J + kOuts - 1) / kOuts);
-    const int grid = grid_for(tasks * 32, 256, 8);
+  const long long few_tiles = (p.n + std::min<long long>(p.n, p.groups) * (kFewRows - 1)) / kFewRows;  // at most
+  const long long tasks = few_tiles * ((p.J + kOuts - 1) / kOuts), held = (long long)sm_count() * kFewBlocks * 8;
+  if (p.n <= (long long)(tc ? kFewTc : kFewPipes) * p.groups && tasks <= (tc ? kTasksTc : kTasksPipes) * held && p.wi == 1 &&
+      p.I % 8 == 0 && (p.lda * elem_bytes(dtype)) % 16 == 0 && is_aligned(p.a, 16) && is_aligned(p.w, 16)) {
+    const int grid = grid_for(tasks * 32, 256, kFewBlocks);
     MT_LAUNCH("k_linear_few", s);
     if (dtype == MT_F32) k_linear_few<float><<<grid, 256, rows_smem(p.groups), s>>>(p);
     else k_linear_few<__nv_bfloat16><<<grid, 256, rows_smem(p.groups), s>>>(p);
