@@ -276,3 +276,17 @@ def test_forward_of_few_rows_does_not_depend_on_their_group(dtype, groups, n, k,
     out = torch.empty(n, m, device=DEV, dtype=x.dtype)
     spread, alone = (time_of(lambda o=o: lin.forward(x, w, o, out=out)) for o in (even, one))
     assert alone <= 4 * spread, (alone, spread)
+
+
+def test_norm_gradients_of_many_groups_without_rows():
+    """One row and 1024 groups: as much as the groups' gradients take to write, not a launch of blocks for each."""
+    d = 2048
+    times = []
+    for groups in (8, 1024):
+        rows, p, off = norm_case(43, [1] + [0] * (groups - 1), 0, 0, d, "bf16", "silu")
+        nb = mt.GatedNorm(d, num_groups=groups)
+        args = (rows["dz"], rows["dh"], rows["y"], rows["u"], rows["z"])
+        got = nb.backward(*args, p, off).params
+        assert got.post_weight[0].any() and not any(t[1:].any() for t in (got.post_weight, got.post_bias, got.scale, got.pre_weight, got.pre_bias))
+        times.append(time_of(lambda: nb.backward(*args, p, off)))
+    assert times[1] <= 24 * times[0], times
