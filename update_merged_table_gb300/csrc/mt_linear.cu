@@ -471,7 +471,7 @@ cudaError_t launch_linear_weights(LinearWeights& p, int dtype, cudaStream_t s) {
   p.units = tc ? cut.units : sm_count() * 4;
   if (p.n > 0 && tc) return launch_linear_weights_tc(p, cut, s);
   if (p.n > 0) {
-    const int grid = p.units;
+    const int grid = weights_blocks(p);
     MT_LAUNCH("k_linear_weights", s);
     const size_t four = 4 * elem_bytes(dtype);
     const bool vec = p.K % 4 == 0 && p.M % 4 == 0 && p.lddy % 4 == 0 && is_aligned(p.dy, four) &&

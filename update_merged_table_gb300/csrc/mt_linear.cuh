@@ -35,7 +35,7 @@ struct LinearWeights {
   Rows x;
   int K, M;
   int tiles;        // tiles of dW (of the kernel that runs)
-  int units;        // blocks (pairs) that walk over them
+  int units;        // blocks (pairs) that there are to walk over them
   float slot_cost, round_cost, sums_cost;  // what a partial product, a tile's end and the sums' launch cost, in units of
                                            // 64 rows of a tile
   int slots;        // partial products there is room for
@@ -260,6 +260,12 @@ __device__ __forceinline__ float* weights_out(const LinearWeights& p, const Plan
   const size_t size = (size_t)p.M * p.K;
   if (q.cum[c.g + 1] - q.cum[c.g] == 1) return p.dw + (size_t)c.g * size;
   return p.part + (size_t)(q.slot[c.g] + c.index) * size;
+}
+
+// Blocks (pairs) of a launch: no more than there can be tiles (each then has one, as it would of a larger launch).
+inline int weights_blocks(const LinearWeights& p) {
+  const long long chunks = (p.n < p.groups ? p.n : p.groups) + p.n / kMinChunk;  // at most
+  return (int)(chunks * p.tiles < p.units ? chunks * p.tiles : p.units);
 }
 
 // Zeros for the rows in no group, by the threads [0, threads) of every block.

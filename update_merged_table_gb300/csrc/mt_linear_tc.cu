@@ -757,7 +757,7 @@ cudaError_t weights_tc(const CUtensorMap& x, const CUtensorMap& dy, const Linear
   const cudaError_t e = limit.allow(k_linear_weights_tc<BN, X8, CG>, ring + weights_smem(MT_MAX_GROUPS));
   if (e != cudaSuccess) return e;
   MT_LAUNCH("k_linear_weights_tc", s);
-  return launch_tc(k_linear_weights_tc<BN, X8, CG>, p.units * CG, kWarpsW * 32, ring + weights_smem(p.groups), CG, s, x, dy, p);
+  return launch_tc(k_linear_weights_tc<BN, X8, CG>, weights_blocks(p) * CG, kWarpsW * 32, ring + weights_smem(p.groups), CG, s, x, dy, p);
 }
 
 template <bool X8>
