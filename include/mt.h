@@ -309,8 +309,10 @@ int mt_backward_adam_pooled(mt_table* t, const mt_lookup_result* res, int64_t n,
  *    and raised to their running maximum, so every access stays in bounds.
  *  - status: device int32 or NULL; the first error found on the device is
  *    written there when it holds 0 (it is never cleared by a call).
- *  - Outputs must not overlap inputs or one another (two column slices of one
- *    buffer do not overlap).
+ *  - Outputs must not overlap inputs, the workspace or one another, and are
+ *    refused where they do (MT_EINVAL).  Rows equally far apart are compared
+ *    byte for byte (two column slices of one buffer do not overlap), others by
+ *    their address ranges.
  *  - Sums, statistics and accumulators are fp32 or wider; results are rounded
  *    once to `dtype`.  No atomics: the same call gives the same bits. */
 #define MT_MAX_GROUPS 1024

@@ -290,3 +290,43 @@ def test_norm_gradients_of_many_groups_without_rows():
         assert got.post_weight[0].any() and not any(t[1:].any() for t in (got.post_weight, got.post_bias, got.scale, got.pre_weight, got.pre_bias))
         times.append(time_of(lambda: nb.backward(*args, p, off)))
     assert times[1] <= 24 * times[0], times
+
+
+# ---- what a call refuses, and what it takes ---------------------------------------------------------------------------------------
+
+def refused(f, *a, **kw):
+    with pytest.raises(mt.MTError) as e:
+        f(*a, **kw)
+    assert e.value.code == mt.MT_EINVAL
+
+
+def test_outputs_that_overlap_are_refused():
+    t = dict(device=DEV, dtype=torch.bfloat16)
+    n, d = 40, 64
+    big = torch.zeros(n, 3 * d, **t)
+    x, y, off = torch.zeros(n, d, **t), torch.zeros(n, d, **t), offsets_of([15, 25])
+    w = torch.zeros(2, d, d, **t)
+    lin = mt.GroupedLinear(2, d, d)
+    refused(lin.forward, x, w, off, out=x)
+    refused(lin.forward, big[:, :d], w, off, out=big[:, d - 1:2 * d - 1])
+    refused(lin.forward, big[:-1, :d], w, offsets_of([15, 24]), out=big[1:, :d])
+    refused(lin.forward, x, w, off, out=w.view(-1, d)[:n])
+    refused(lin.backward, x, y, w, off, out_dx=x)
+    refused(lin.backward, x, y, w, off, out_dx=w.view(-1, d)[:n])
+    dw = torch.zeros(2, d, d, device=DEV)
+    refused(lin.backward, x, dw.view(-1).view(torch.bfloat16)[:n * d].view(n, d), w, off, out_dw=dw)
+    lin.forward(big[:, :d], w, off, out=big[:, d:2 * d])         # column slices of one tensor do not overlap
+    lin.backward(big[:, :d], big[:, 2 * d:], w, off, out_dx=big[:, d:2 * d])
+    lin.forward(big[0:20, :d], w, offsets_of([5, 15]), out=big[20:, :d])
+    both = torch.zeros(2 * n, d, **t)
+    lin.forward(both[0::2], w, off, out=both[1::2])              # nor do alternate rows
+    one = mt.NormParams(post_weight=torch.ones(d, device=DEV), pre_weight=torch.ones(d, device=DEV))
+    nb = mt.GatedNorm(d)
+    refused(nb.forward, x, y, y, one, out_h=y)
+    refused(nb.forward, x, y, y, one, out_z=big[:, :d], out_h=big[:, 8:8 + d])
+    refused(nb.backward, x, x, y, y, y, one, out_dx=big[:, :d], out_dy=big[:, d // 2:d // 2 + d])
+    refused(nb.backward, x, x, y, y, y, one, out_du=y)
+    nb.backward(x, x, y, y, y, one, out_dy=big[:, :d], out_du=big[:, d:2 * d])
+    p = mt.pack8(x)
+    refused(mt.pack8, x, out=mt.Packed8(x.view(torch.int8).view(-1, d)[:n], p.exps))
+    refused(mt.unpack8, mt.Packed8(x.view(torch.int8).view(-1, d)[:n], p.exps), out=x)

@@ -438,10 +438,71 @@ inline bool rows_wide(const Rows& r, int64_t d, int dtype) {
   return r.codes == nullptr || is_aligned(r.codes, 8);
 }
 
-// Whether [a, a + na) and [b, b + nb) meet.
-inline bool ranges_meet(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return a != nullptr && b != nullptr && x < y + nb && y < x + na;
+// Where a call reads or writes: n runs of `width` bytes, `step` bytes apart.
+struct Region {
+  uintptr_t at = 0;
+  long long n = 0, width = 0, step = 0;
+};
+inline Region whole_region(const void* p, size_t bytes) {
+  return p == nullptr ? Region{} : Region{(uintptr_t)p, bytes > 0, (long long)bytes, (long long)bytes};
 }
+
+// Whether two regions share a byte.  Runs equally far apart (column slices of one tensor, alternate rows): exactly, from the
+// runs of one that can reach a run of the other.  Otherwise: whether their address ranges meet.
+inline bool regions_meet(const Region& a, const Region& b) {
+  if (a.n == 0 || b.n == 0) return false;
+  const long long d = (long long)(b.at - a.at);
+  if (d >= (a.n - 1) * a.step + a.width || -d >= (b.n - 1) * b.step + b.width) return false;
+  if (a.n == 1 && b.n == 1) return true;
+  const long long step = a.n == 1 ? b.step : a.step;
+  if ((b.n > 1 && b.step != step) || a.width > step || b.width > step) return true;
+  long long k = d / step;  // b's first run starts k steps and r bytes (0 <= r < step) after a's
+  if (k * step > d) --k;
+  const long long r = d - k * step;
+  auto same = [&](long long i) { return i <= a.n - 1 && -i <= b.n - 1; };  // some run of b lies i steps after one of a
+  return (r < a.width && same(k)) || (r + b.width > step && same(k + 1));
+}
+
+// The inputs and outputs of a call, and whether an output shares a byte with an input or with another output.
+class Regions {
+ public:
+  void in(const Region& r) {
+    if (r.n > 0) in_[ins_++] = r;
+  }
+  void out(const Region& r) {
+    if (r.n > 0) out_[outs_++] = r;
+  }
+  // A row tensor of n rows: its plain rows and its checkpoint.
+  void in(const Rows& r, int64_t n, int64_t d, int dtype) {
+    in(plain(r, n, d, dtype));
+    in(whole_region(r.codes, (size_t)n * d));
+    in(whole_region(r.exps, (size_t)n * ((d + kPackBlock - 1) / kPackBlock)));
+  }
+  void out(const Rows& r, int64_t n, int64_t d, int dtype) {
+    out(plain(r, n, d, dtype));
+    out_packed(r, n, d);
+  }
+  void out_packed(const Rows& r, int64_t n, int64_t d) {
+    out(whole_region(r.codes, (size_t)n * d));
+    out(whole_region(r.exps, (size_t)n * ((d + kPackBlock - 1) / kPackBlock)));
+  }
+  static Region plain(const Rows& r, int64_t n, int64_t d, int dtype) {
+    const long long e = (long long)elem_bytes(dtype);
+    return r.data == nullptr ? Region{} : Region{(uintptr_t)r.data, n, d * e, r.ld * e};
+  }
+  bool clash() const {
+    for (int i = 0; i < outs_; ++i) {
+      for (int j = 0; j < ins_; ++j)
+        if (regions_meet(out_[i], in_[j])) return true;
+      for (int j = 0; j < i; ++j)
+        if (regions_meet(out_[i], out_[j])) return true;
+    }
+    return false;
+  }
+
+ private:
+  Region in_[24], out_[16];  // the norms' backward has the most: 21 and 9
+  int ins_ = 0, outs_ = 0;
+};
 
 }  // namespace mt

@@ -407,6 +407,8 @@ size_t partial_bytes(int64_t n, int32_t groups, int32_t k, int32_t m) {
   return align_up((size_t)slots_of(n, groups, k, m) * k * m * 4 + 256, 256);
 }
 
+size_t weights_bytes(int32_t groups, int32_t k, int32_t m, int dtype) { return (size_t)groups * k * m * elem_bytes(dtype); }
+
 // The shapes, offsets and types that both directions share.
 int linear_check(const int64_t* offsets, int32_t groups, int64_t n, int32_t k, int32_t m, int dtype,
                  const int32_t* status) {
@@ -513,6 +515,12 @@ int mt_group_linear_forward(const void* x, int64_t ldx, const void* w, const int
   if (w == nullptr || !is_aligned(w, elem_bytes(dtype))) return MT_EINVAL;
   if (n == 0) return MT_OK;
   if (!rows_ok(x, ldx, in_dim, dtype) || !rows_ok(y, ldy, out_dim, dtype)) return MT_EINVAL;
+  Regions all;
+  all.in(Rows{const_cast<void*>(x), ldx, nullptr, nullptr}, n, in_dim, dtype);
+  all.in(whole_region(w, weights_bytes(groups, in_dim, out_dim, dtype)));
+  all.in(whole_region(offsets, (size_t)(groups + 1) * 8));
+  all.out(Rows{y, ldy, nullptr, nullptr}, n, out_dim, dtype);
+  if (all.clash()) return MT_EINVAL;
   LinearRows p{};
   p.n = n;
   p.groups = groups;
@@ -558,6 +566,19 @@ int mt_group_linear_backward(const void* dy, int64_t lddy, const mt_rows* x, con
     if (ws == nullptr || !is_aligned(ws, 256) || ws_bytes < mt_group_linear_workspace_bytes(n, groups, in_dim, out_dim))
       return MT_ENOSPACE;
   }
+  Regions all;
+  all.in(Rows{const_cast<void*>(dy), lddy, nullptr, nullptr}, n, out_dim, dtype);
+  all.in(whole_region(offsets, (size_t)(groups + 1) * 8));
+  if (dx != nullptr) {
+    all.in(whole_region(w, weights_bytes(groups, in_dim, out_dim, dtype)));
+    all.out(Rows{dx, lddx, nullptr, nullptr}, n, in_dim, dtype);
+  }
+  if (dw != nullptr) {
+    all.in(x->data != nullptr ? Rows{x->data, x->ld, nullptr, nullptr} : *x, n, in_dim, dtype);
+    all.out(whole_region(dw, weights_bytes(groups, in_dim, out_dim, MT_F32)));
+    all.out(whole_region(ws, mt_group_linear_workspace_bytes(n, groups, in_dim, out_dim)));
+  }
+  if (all.clash()) return MT_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (dx != nullptr && n > 0) {

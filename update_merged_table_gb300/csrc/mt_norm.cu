@@ -852,6 +852,13 @@ bool packed_rows(const Rows& r) { return r.codes != nullptr && r.exps != nullptr
 bool half_packed(const Rows& r) { return (r.codes == nullptr) != (r.exps == nullptr); }
 Rows rows_of(const mt_rows* r) { return r != nullptr ? *r : Rows{nullptr, 0, nullptr, nullptr}; }
 
+// What both directions read beside rows.
+void common_inputs(Regions& all, const NormParams& p) {
+  const size_t bytes = (size_t)p.groups * p.d * 4;
+  for (const float* f : {p.wp, p.bp, p.sc, p.wq, p.bq}) all.in(whole_region(f, bytes));
+  all.in(whole_region(p.offsets, (size_t)(p.groups + 1) * 8));
+}
+
 }  // namespace
 }  // namespace mt
 
@@ -879,6 +886,14 @@ int mt_gated_norm_forward(const mt_gated_norm* cfg, const mt_rows* x, const mt_r
   if (has_u && !rows_ok(p.u.data, p.u.ld, p.d, cfg->dtype)) return MT_EINVAL;
   if (has_y ? !rows_ok(p.z.data, p.z.ld, p.d, cfg->dtype) : p.z.data != nullptr) return MT_EINVAL;
   if (p.wq != nullptr && !rows_ok(p.h.data, p.h.ld, p.d, cfg->dtype)) return MT_EINVAL;
+  Regions all;
+  common_inputs(all, p);
+  for (const Rows* r : {&p.x, &p.y, &p.u}) {
+    all.in(Regions::plain(*r, p.n, p.d, cfg->dtype));
+    all.out_packed(*r, p.n, p.d);
+  }
+  for (const Rows* r : {&p.z, &p.h}) all.out(*r, p.n, p.d, cfg->dtype);
+  if (all.clash()) return MT_EINVAL;
   bool wide = true;
   for (const Rows* r : {&p.x, &p.y, &p.u, &p.z, &p.h}) wide = wide && rows_wide(*r, p.d, cfg->dtype);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -954,6 +969,14 @@ int mt_gated_norm_backward(const mt_gated_norm* cfg, const mt_rows* dz, const mt
   }
   if (ws == nullptr || !is_aligned(ws, 256) || ws_bytes < mt_gated_norm_workspace_bytes(p.n, p.d, p.groups))
     return MT_ENOSPACE;
+  Regions all;
+  common_inputs(all, p);
+  for (const Rows* r : {&p.dz, &p.dh, &p.y, &p.u, &p.z})
+    all.in(r->data != nullptr ? Rows{r->data, r->ld, nullptr, nullptr} : *r, p.n, p.d, cfg->dtype);
+  for (const Rows* r : {&p.dx, &p.dy, &p.du}) all.out(*r, p.n, p.d, cfg->dtype);
+  for (const float* f : {p.dwp, p.dbp, p.dsc, p.dwq, p.dbq}) all.out(whole_region(f, (size_t)p.groups * p.d * 4));
+  all.out(whole_region(ws, mt_gated_norm_workspace_bytes(p.n, p.d, p.groups)));
+  if (all.clash()) return MT_EINVAL;
   p.part = static_cast<float*>(ws);
   p.blocks = bwd_blocks(p.n, p.d, (int)elem_bytes(cfg->dtype), p.bp != nullptr || p.bq != nullptr);
   bool wide = true;

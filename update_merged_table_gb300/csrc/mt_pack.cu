@@ -82,7 +82,10 @@ int pack_check(const PackParams& p, int dtype) {
   if (dtype != MT_F32 && dtype != MT_BF16) return MT_EINVAL;
   if (p.n < 0 || p.n > 0x7FFFFFFF || p.d < 1 || p.d > MT_MAX_BLOCK_DIM) return MT_EINVAL;
   if (p.n > 0 && (!rows_ok(p.r.data, p.r.ld, p.d, dtype) || p.q.codes == nullptr || p.q.exps == nullptr)) return MT_EINVAL;
-  return MT_OK;
+  Regions all;  // the rows and the two parts of the checkpoint: all apart, whichever is written
+  all.out(p.r, p.n, p.d, dtype);
+  all.out_packed(p.q, p.n, p.d);
+  return all.clash() ? MT_EINVAL : MT_OK;
 }
 
 bool pack_wide(const PackParams& p, int dtype) { return rows_wide(p.r, p.d, dtype) && rows_wide(p.q, p.d, dtype); }
