@@ -330,3 +330,13 @@ def test_outputs_that_overlap_are_refused():
     p = mt.pack8(x)
     refused(mt.pack8, x, out=mt.Packed8(x.view(torch.int8).view(-1, d)[:n], p.exps))
     refused(mt.unpack8, mt.Packed8(x.view(torch.int8).view(-1, d)[:n], p.exps), out=x)
+
+
+def test_one_row_of_any_stride():
+    """A batch of one row: the distance to a next row that is not there does not matter."""
+    gen = torch.Generator(device=DEV).manual_seed(39)
+    x, w, off = rand(gen, 1, 64), rand(gen, 1, 32, 64), offsets_of([1])
+    far = x.as_strided((1, 64), (1 << 31, 1))
+    lin = mt.GroupedLinear(1, 64, 32)
+    assert torch.equal(lin.forward(far, w, off), lin.forward(x, w, off))
+    assert torch.equal(mt.pack8(far).codes, mt.pack8(x).codes)

@@ -76,7 +76,7 @@ mt_rows rows(PyObject* o, const char* what, int64_t& n, int64_t d, at::ScalarTyp
   n = t.size(0);
   int64_t ld = t.stride(0);
   if (d > 1 && t.stride(1) != 1) raise(PyExc_ValueError, std::string("the columns of ") + what + " must be contiguous");
-  if (n <= 1) ld = std::max(ld, d);
+  if (n <= 1) ld = d;  // there is no next row
   else if (ld < d) raise(PyExc_ValueError, std::string("the rows of ") + what + " overlap");
   return mt_rows{t.data_ptr(), ld, nullptr, nullptr};
 }
