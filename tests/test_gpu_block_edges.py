@@ -340,3 +340,14 @@ def test_one_row_of_any_stride():
     lin = mt.GroupedLinear(1, 64, 32)
     assert torch.equal(lin.forward(far, w, off), lin.forward(x, w, off))
     assert torch.equal(mt.pack8(far).codes, mt.pack8(x).codes)
+
+
+def test_checkpoint_parts_that_do_not_belong_together_are_refused():
+    gen = torch.Generator(device=DEV).manual_seed(40)
+    p, q = mt.pack8(rand(gen, 50, 64)), mt.pack8(rand(gen, 5, 64))
+    p.exps = q.exps
+    with pytest.raises(ValueError):
+        mt.unpack8(p)
+    p.codes = p.codes[0]
+    with pytest.raises(ValueError):
+        mt.unpack8(p)

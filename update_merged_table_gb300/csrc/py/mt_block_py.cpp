@@ -146,15 +146,18 @@ PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F&& f) {
   }
 }
 
+// Both parts of a checkpoint of rows [n, d].
+mt_rows saved_parts(PyObject* codes, PyObject* exps, const char* what, int64_t n, int64_t d, int device) {
+  mt_rows r = none_rows();
+  r.codes = static_cast<int8_t*>(whole(codes, what, at::kChar, device, n, d));
+  r.exps = static_cast<uint8_t*>(whole(exps, what, at::kByte, device, n, (d + MT_PACK_BLOCK - 1) / MT_PACK_BLOCK));
+  return r;
+}
 // The saved rows of a backward: plain, or (codes, exps).
 mt_rows saved(PyObject* o, const char* what, int64_t& n, int64_t d, at::ScalarType type, int device) {
   if (o == Py_None) return none_rows();
   if (!PyTuple_Check(o)) return rows(o, what, n, d, type, device);
-  const int64_t nb = (d + MT_PACK_BLOCK - 1) / MT_PACK_BLOCK;
-  mt_rows r = none_rows();
-  r.codes = static_cast<int8_t*>(whole(PyTuple_GET_ITEM(o, 0), what, at::kChar, device, n, d));
-  r.exps = static_cast<uint8_t*>(whole(PyTuple_GET_ITEM(o, 1), what, at::kByte, device, n, nb));
-  return r;
+  return saved_parts(PyTuple_GET_ITEM(o, 0), PyTuple_GET_ITEM(o, 1), what, n, d, device);
 }
 
 // init(addresses of the six functions in order, MTError)
@@ -206,11 +209,13 @@ PyObject* pack8(PyObject*, PyObject* const* a, Py_ssize_t count) {
 // unpack8(codes, exps, dtype code, out or None) -> rows
 PyObject* unpack8(PyObject*, PyObject* const* a, Py_ssize_t count) {
   return guarded(count, 4, [&]() -> PyObject* {
-    const at::Tensor &codes = tensor(a[0], "p"), &exps = tensor(a[1], "p");
+    const at::Tensor& codes = tensor(a[0], "p");
+    if (codes.dim() != 2 || !codes.is_cuda()) raise(PyExc_ValueError, "the codes of p must be a 2-D CUDA tensor");
     const int device = codes.device().index();
     int64_t n = codes.size(0);
     const int64_t d = codes.size(1);
     if (d < 1 || d > MT_MAX_BLOCK_DIM) raise(PyExc_ValueError, "p must have 1 to 8192 columns");
+    const mt_rows p = saved_parts(a[0], a[1], "p", n, d, device);
     const int dtype = (int)integer(a[2]);
     On on(device);
     mt_rows r;
@@ -222,9 +227,7 @@ PyObject* unpack8(PyObject*, PyObject* const* a, Py_ssize_t count) {
       out = make({n, d}, type_of(dtype), device);
       r = mt_rows{out.data_ptr(), d, nullptr, nullptr};
     }
-    check(f_unpack8(static_cast<int8_t*>(codes.data_ptr()), static_cast<uint8_t*>(exps.data_ptr()), n, (int32_t)d, dtype,
-                    r.data, r.ld, on.stream),
-          "mt_unpack8");
+    check(f_unpack8(p.codes, p.exps, n, (int32_t)d, dtype, r.data, r.ld, on.stream), "mt_unpack8");
     return wrap(out);
   });
 }
