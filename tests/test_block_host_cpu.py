@@ -1,9 +1,10 @@
 """The dense block's host side without a GPU: the limits of its calls, and what building and importing it needs."""
 import ctypes
-
-import pytest
+import importlib.metadata
+import importlib.util
 
 import update_merged_table_gb300 as mt
+from update_merged_table_gb300 import build_lib
 from test_block_cpu import P, Rows, lib, norm_config  # noqa: F401 (lib: the built library)
 
 MOST_ROWS = (1 << 31) - 4096
@@ -23,3 +24,20 @@ def test_row_numbers_leave_room_for_a_tile(lib):  # noqa: F811
         if not size:
             assert lib.mt_group_linear_forward(P, 64, P, P, 2, n, 64, 32, mt.MT_BF16, P, 32, None, None) == code
             assert lib.mt_gated_norm_forward(ctypes.byref(norm_config(n=n)), *(ctypes.byref(row),) * 5, None) == code
+
+
+def test_library_builds_without_torch(monkeypatch, tmp_path, lib):  # noqa: F811
+    """The C library depends on nothing but CUDA: without torch only the Python module is left out."""
+    monkeypatch.setattr(build_lib, "BINDING", str(tmp_path / "_mt_block.so"))
+    find = importlib.util.find_spec
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: None if name == "torch" else find(name, *a))
+    assert build_lib.build() == build_lib.LIB
+    assert not (tmp_path / "_mt_block.so").exists()
+
+
+def test_python_module_is_built_anew_for_another_torch(monkeypatch, lib):  # noqa: F811
+    started = []
+    monkeypatch.setattr(build_lib.subprocess, "Popen", lambda cmd, **kw: started.append(cmd))
+    assert build_lib._start_binding(False, False) is None and not started
+    monkeypatch.setattr(importlib.metadata, "version", lambda name: "0.0")
+    assert build_lib._start_binding(False, False) is not None and len(started) == 1

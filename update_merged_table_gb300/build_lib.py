@@ -7,15 +7,17 @@ statically, so the library depends on nothing but the driver.
 
 Beside it, ``csrc/py/mt_block_py.cpp`` becomes ``_build/_mt_block.so``, the
 Python module through which ``block.py`` calls the library (it needs torch's
-and Python's headers).
+and Python's headers; without torch only the library is built).
 """
 from __future__ import annotations
 
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -26,6 +28,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmt.so")
 BINDING_SRC = os.path.join(CSRC, "py", "mt_block_py.cpp")
 BINDING = os.path.join(BUILD, "_mt_block.so")
+BINDING_FOR = os.path.join(BUILD, "_mt_block.for")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2", "-I", INCLUDE, "-I", CSRC]
@@ -42,12 +45,28 @@ def _newest(paths) -> float:
     return max(os.path.getmtime(p) for p in paths)
 
 
+def _made_for(torch_dir: str) -> str:
+    """What a Python module was compiled against: it fits this torch and this Python only."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "?"
+    return f"torch {version} in {torch_dir}\nPython {sys.version}\n"
+
+
 def _start_binding(force: bool, verbose: bool):
-    """Start compiling the Python module if it is out of date; (process, file to rename) or None."""
-    deps = [BINDING_SRC, os.path.join(INCLUDE, "mt.h"), __file__]
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= _newest(deps):
+    """Start compiling the Python module if it is out of date; (process, file to rename, what it is made for), or None
+    where there is nothing to do or no torch to make it for."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or spec.origin is None:
         return None
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    torch_dir = os.path.dirname(spec.origin)
+    made_for = _made_for(torch_dir)
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "mt.h"), __file__]
+    if not force and os.path.exists(BINDING) and os.path.exists(BINDING_FOR) and os.path.getmtime(BINDING) >= _newest(deps):
+        with open(BINDING_FOR) as f:
+            if f.read() == made_for:
+                return None
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     lib = os.path.join(torch_dir, "lib")
     tmp = BINDING + f".tmp{os.getpid()}"
@@ -57,17 +76,19 @@ def _start_binding(force: bool, verbose: bool):
            "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     if verbose:
         print(" ".join(cmd))
-    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT), tmp
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT), tmp, made_for
 
 
 def _finish_binding(started):
     if started is None:
         return
-    proc, tmp = started
+    proc, tmp, made_for = started
     out, _ = proc.communicate()
     if proc.returncode != 0:
         raise RuntimeError("the Python module failed to compile:\n" + out.decode(errors="replace"))
     os.replace(tmp, BINDING)
+    with open(BINDING_FOR, "w") as f:
+        f.write(made_for)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
