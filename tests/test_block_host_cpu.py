@@ -2,6 +2,10 @@
 import ctypes
 import importlib.metadata
 import importlib.util
+import os
+import shutil
+import subprocess
+import sys
 
 import update_merged_table_gb300 as mt
 from update_merged_table_gb300 import build_lib
@@ -41,3 +45,27 @@ def test_python_module_is_built_anew_for_another_torch(monkeypatch, lib):  # noq
     assert build_lib._start_binding(False, False) is None and not started
     monkeypatch.setattr(importlib.metadata, "version", lambda name: "0.0")
     assert build_lib._start_binding(False, False) is not None and len(started) == 1
+
+
+def test_all_names_import_without_a_library_or_torch(tmp_path):
+    """`from package import *` needs neither the built library nor torch; what does says so when it is used."""
+    shutil.copytree(os.path.dirname(build_lib.__file__), tmp_path / "update_merged_table_gb300",
+                    ignore=shutil.ignore_patterns("_build", "csrc", "__pycache__"))
+
+    def run(code):
+        r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True)
+        assert r.returncode == 0, r.stderr
+
+    run("""
+from update_merged_table_gb300 import *
+import torch
+assert Packed8 and Table
+for f in (lambda: pack8(torch.zeros(2, 32)), lambda: Table(10, 16, device="cpu")):
+    try:
+        f()
+    except RuntimeError as e:
+        assert "not built" in str(e), e
+    else:
+        raise SystemExit("no error")
+""")
+    run("import sys; sys.modules['torch'] = None\nfrom update_merged_table_gb300 import *\nassert plan_merge and 'Packed8' not in globals()")

@@ -16,14 +16,18 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import importlib.util
 import os
 
 import numpy as np
 
 __all__ = ["Table", "ShardGroup", "MergedTables", "plan_merge", "LookupResult", "load_library", "MTError", "MT_F32", "MT_BF16", "POOL_SUM", "POOL_MEAN",
            "KEY_EMPTY", "KEY_TOMBSTONE",
-           "Packed8", "pack8", "unpack8", "GroupedLinear", "GatedNorm", "NormParams", "NormForward", "NormGrads",
            "ABI_FUNCTIONS", "profile_enable", "profile_report", "kernel_launches"]
+
+_BLOCK = ("Packed8", "pack8", "unpack8", "GroupedLinear", "GatedNorm", "NormParams", "NormForward", "NormGrads")
+if importlib.util.find_spec("torch") is not None:  # the dense block's module is made of it
+    __all__ += _BLOCK
 
 MT_OK, MT_EINVAL, MT_ENOSPACE, MT_EFULL, MT_EKEY, MT_ECUDA, MT_ETOOBIG = 0, -1, -2, -3, -4, -5, -6
 ABI_VERSION = 3
@@ -755,9 +759,6 @@ class MergedTables:
                                                  ctypes.byref(hp), gs, ws.data_ptr(), ws.numel(), _stream(stream)),
                "mt_backward_adam_grouped")
         return gsums
-
-
-_BLOCK = frozenset(("Packed8", "pack8", "unpack8", "GroupedLinear", "GatedNorm", "NormParams", "NormForward", "NormGrads"))
 
 
 def __getattr__(name: str):

@@ -64,7 +64,16 @@ def _load_native():
     return mod
 
 
-_native = _load_native()
+class _Unloaded:
+    """Stands for the native module until its first use: the names of this one need no built library."""
+
+    def __getattr__(self, name):
+        global _native
+        _native = _load_native()
+        return getattr(_native, name)
+
+
+_native = _Unloaded()
 
 
 class _On:
