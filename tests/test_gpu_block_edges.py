@@ -10,7 +10,7 @@ import torch
 
 import update_merged_table_gb300 as mt
 import block_reference as R
-from test_gpu_block import DEV, F, check_backward, near, norm_case, offsets_of, rand, rounding, values, wide
+from test_gpu_block import DEV, F, check_backward, near, norm_case, offsets_of, rand, rounding, row_tol, values, wide
 
 pytestmark = pytest.mark.gpu
 
@@ -53,6 +53,32 @@ def test_norm_gradients_when_few_rows_are_in_groups(n, sizes, lead, d, kind):
     check_backward(nb, whole, ref, size, "bf16", max(sizes))
     for t in (got.dx, got.dy, got.du):
         assert not t[:a].any() and not t[b:].any()
+
+
+def test_norm_gradients_of_a_group_without_rows_are_zero():
+    """Also where that group's parameters are not finite."""
+    rows, p, off = norm_case(44, [20, 0, 13], 0, 0, 64, "bf16", "silu")
+    for t in (p.scale, p.post_weight, p.post_bias):
+        t[1] = float("inf")
+    nb = mt.GatedNorm(64, num_groups=3)
+    got = nb.backward(rows["dz"], rows["dh"], rows["y"], rows["u"], rows["z"], p, off).params
+    for t in (got.post_weight, got.post_bias, got.scale, got.pre_weight, got.pre_bias):
+        assert torch.equal(t[1], torch.zeros_like(t[1])) and torch.isfinite(t).all()
+
+
+@pytest.mark.parametrize("d", [4096, 5000, 8192])
+def test_norm_wide_rows_in_fp32(d):
+    """Teams of several warps, rows loaded when they are used."""
+    rows, p, off = norm_case(45, [5, 0, 70], 1, 2, d, "f32", "sigmoid")
+    nb = mt.GatedNorm(d, num_groups=3, kind="layer", gate="sigmoid", dtype="f32")
+    r = nb.forward(rows["x"], rows["y"], rows["u"], p, off)
+    z, h = R.norm_forward(wide(rows["x"]), wide(rows["y"]), wide(rows["u"]), values(p), wide(off), "layer", "sigmoid", 1e-6)
+    near(r.z, z, 4 * row_tol(z, "f32"))
+    near(r.h, h, 4 * row_tol(h, "f32"))
+    for saved in ((rows["y"], rows["u"], rows["z"]), tuple(mt.pack8(rows[k]) for k in ("y", "u", "z"))):
+        seen = [R.unpack(t.codes.cpu().numpy(), t.exps.cpu().numpy()) if isinstance(t, mt.Packed8) else wide(t) for t in saved]
+        ref, size = R.norm_backward(wide(rows["dz"]), wide(rows["dh"]), *seen, values(p), wide(off), "layer", "sigmoid", 1e-6)
+        check_backward(nb, nb.backward(rows["dz"], rows["dh"], *saved, p, off), ref, size, "f32", 70)
 
 
 # ---- sums with one exact value ------------------------------------------------------------------------------------------

@@ -737,7 +737,10 @@ __global__ void __launch_bounds__(32 * kSlices) k_norm_sums(const NormParams p) 
     }
     if (slice != turn || col >= p.d) continue;
     const size_t at = (size_t)g * p.d + col;
-    if (post) {
+    if (s_off[g] == s_off[g + 1]) {  // no rows: zeros, whatever the parameters are
+      for (float* f : {post ? p.dwp : p.dwq, post ? p.dbp : p.dbq, post ? p.dsc : nullptr})
+        if (f != nullptr) f[at] = 0.0f;
+    } else if (post) {
       const float s = p.sc != nullptr ? p.sc[at] : 1.0f;
       p.dwp[at] = s * a;
       if (p.dbp != nullptr) p.dbp[at] = s * b;
