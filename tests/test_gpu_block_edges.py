@@ -1,6 +1,5 @@
 """The dense block where rows are few, long, uneven or shared: sums that have one exact value, batches of which few rows are
 in a group, workspaces of captured graphs, calls from several threads, outputs that would overlap inputs."""
-
 import ctypes
 import threading
 
@@ -366,6 +365,13 @@ def test_one_row_of_any_stride():
     lin = mt.GroupedLinear(1, 64, 32)
     assert torch.equal(lin.forward(far, w, off), lin.forward(x, w, off))
     assert torch.equal(mt.pack8(far).codes, mt.pack8(x).codes)
+
+
+def test_out_of_memory_is_the_error_of_torch():
+    """Outputs that do not fit raise what torch raises, so that a caller can catch it."""
+    x, w, off = torch.zeros(20_000_000, 1, device=DEV), torch.zeros(1, 8192, 1, device=DEV), offsets_of([20_000_000])
+    with pytest.raises(torch.OutOfMemoryError):
+        mt.GroupedLinear(1, 1, 8192, dtype="f32").forward(x, w, off)
 
 
 def test_checkpoint_parts_that_do_not_belong_together_are_refused():

@@ -60,7 +60,7 @@ def _load_native():
     spec.loader.exec_module(mod)
     names = ("mt_pack8", "mt_unpack8", "mt_group_linear_forward", "mt_group_linear_backward", "mt_gated_norm_forward",
              "mt_gated_norm_backward")
-    mod.init(*(ctypes.cast(getattr(lib, k), ctypes.c_void_p).value for k in names), MTError)
+    mod.init(*(ctypes.cast(getattr(lib, k), ctypes.c_void_p).value for k in names), MTError, torch.OutOfMemoryError)
     return mod
 
 

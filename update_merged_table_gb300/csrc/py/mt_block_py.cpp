@@ -25,7 +25,8 @@ decltype(&mt_group_linear_forward) f_linear_forward;
 decltype(&mt_group_linear_backward) f_linear_backward;
 decltype(&mt_gated_norm_forward) f_norm_forward;
 decltype(&mt_gated_norm_backward) f_norm_backward;
-PyObject* g_mt_error;  // the MTError class
+PyObject* g_mt_error;       // the MTError class
+PyObject* g_out_of_memory;  // torch's
 
 // Thrown where a Python error has been set.
 struct Raised {};
@@ -137,6 +138,9 @@ PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F&& f) {
     return f();
   } catch (const Raised&) {
     return nullptr;
+  } catch (const c10::OutOfMemoryError& e) {
+    PyErr_SetString(g_out_of_memory, e.what_without_backtrace());
+    return nullptr;
   } catch (const c10::Error& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
     return nullptr;
@@ -160,9 +164,9 @@ mt_rows saved(PyObject* o, const char* what, int64_t& n, int64_t d, at::ScalarTy
   return saved_parts(PyTuple_GET_ITEM(o, 0), PyTuple_GET_ITEM(o, 1), what, n, d, device);
 }
 
-// init(addresses of the six functions in order, MTError)
+// init(addresses of the six functions in order, MTError, torch.OutOfMemoryError)
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 7, [&]() -> PyObject* {
+  return guarded(n, 8, [&]() -> PyObject* {
     f_pack8 = reinterpret_cast<decltype(f_pack8)>(integer(a[0]));
     f_unpack8 = reinterpret_cast<decltype(f_unpack8)>(integer(a[1]));
     f_linear_forward = reinterpret_cast<decltype(f_linear_forward)>(integer(a[2]));
@@ -171,6 +175,8 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
     f_norm_backward = reinterpret_cast<decltype(f_norm_backward)>(integer(a[5]));
     Py_INCREF(a[6]);
     g_mt_error = a[6];
+    Py_INCREF(a[7]);
+    g_out_of_memory = a[7];
     Py_RETURN_NONE;
   });
 }
