@@ -292,7 +292,7 @@ k_linear_rows_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constan
         if (!ok) break;
         tc::fence_after();
         for (int k = 0; k < steps; ++k) {
-          ok = tc::mbar_wait(&bar.full[s.stage], s.phase);
+          ok = tc::mbar_wait<CG == 2>(&bar.full[s.stage], s.phase);  // a pair's copies into both blocks
           if (!ok) break;
           tc::fence_after();
           const uint32_t a = tc::smem_addr(ring + s.stage * R::kStage), b = a + R::kStageA;
@@ -521,7 +521,7 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
             if (!ok) break;
           }
           uint8_t* st = ring + s.stage * R::kStage;
-          ok = __all_sync(kFull, tc::mbar_wait(X8 ? &bar.ready[s.stage] : &bar.full[s.stage], s.phase));
+          ok = __all_sync(kFull, tc::mbar_wait<CG == 2>(X8 ? &bar.ready[s.stage] : &bar.full[s.stage], s.phase));
           if (!ok) break;
           const int left = (int)min((long long)kBK, x.last - x.first - (long long)k * kBK);
           if (!X8 && left < kBK) {
