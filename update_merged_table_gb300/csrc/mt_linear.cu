@@ -15,10 +15,10 @@
 //                    from the chunks' partial products in chunk order (no
 //                    atomics: the sum has one order), and zeros for empty groups.
 //
-// The fp32 pipes bound the tiles (200,000 x 128 to 256 in fp32: 298 us, 44
-// TFLOP/s; dW 271 us, 48), latency where the contraction is short (65,536 x 32 to
-// 128: 28 us over uneven groups).  Alignment chooses the VEC form: 53,166 rows to
-// 207 columns 46 us, to 208 columns 37.
+// The fp32 pipes bound the tiles (200,000 x 128 to 256 in fp32: 305 us, 43
+// TFLOP/s; dW 260 us, 50, and 35 of sums), shared memory and its latency where
+// the contraction is short (65,536 x 32 to 128: 22 us).  Alignment chooses the VEC
+// form: 53,166 x 32 to 207 columns 45 us, to 208 columns 31.
 #include <algorithm>
 
 #include "mt_linear.cuh"

@@ -30,9 +30,10 @@
 // Bound: the arithmetic where the contraction is long, HBM where it is short.
 // Measured, forward: 77,824 rows to 1024 columns 1.63 PFLOP/s from 1024 columns
 // and 1.91 from 4096 (the library's product 1.79 and 1.93); 1,970,003 x 64 to 256
-// 196 us, 95% of the copy bandwidth.  dx of 490,011 x 256 from 512 columns 122 us
-// (91% of it).  dW of 65,536 x 1024 x 1024 in 8 groups: 123 us and 9 us of sums
-// (1.12 PFLOP/s), from 8 bits 157 us, where the widening bounds it.
+// 196 us, 95% of the copy bandwidth.  dx of 490,011 x 256 from 512 columns 121 us
+// (91% of it).  dW of 65,536 x 1024 x 1024 in 8 groups: 123 us and 8 us of sums
+// (1.12 PFLOP/s), from 8 bits 178 us, where the widening and one block's shared
+// memory bound it.
 #include <algorithm>
 
 #include "mt_linear.cuh"

@@ -19,15 +19,20 @@
 //                atomics, so the sums have one order).  With S1 = sum D a yh and
 //                S2 = sum D a, dwp = s S1, dbp = s S2 and ds = wp S1 + bp S2: two
 //                sums for three gradients, and one when there is no bp.
-//  k_norm_sums   the blocks' partial sums of each group (9 to 17 us, latency).
+//  k_norm_sums   the runs' partial sums of each group (8 to 12 us, latency).
 //
-// Measured, bf16, all parts, of the copy bandwidth: 490,011 x 512 rms forward 412
-// us (90%), with h in 8 bits as well 474 (86%); backward 629 (92%), from 8 bits
-// 689 (69%: widening three rows takes the issue slots).  200,003 x 1024 layer norm
-// with biases 558 forward (54%) and 851 backward (56%), bound by issue and by the
-// latency between dependent steps at 12 warps an SM; the same as rms without
-// biases 576 backward (82%).  Widths that are no multiple of 8 go an element at a
-// time: 200,003 x 777 backward 2.5 ms (15%).
+// Measured, all parts, with the sums, of the copy bandwidth.  bf16, 490,011 x 512
+// rms: forward 405 us (91%), with h in 8 bits as well 467 (87%), with all four
+// checkpoints of y and u side by side 680 (77%); backward 639 (93%), from 8 bits 698
+// (69%: issue at 57%, three rows widened and their exponent bytes loaded one by one
+// between dependent steps).  200,003 x 1024 layer norm with biases: forward 555 (54%;
+// 24 warps an SM, issue at 57% and shared memory's pipe at 60%, most stalls on
+// loads: five rows of fp32 parameters come through L1 for every row, and each
+// statistic waits for two reductions in a row) and backward 850 (57%; 12 warps an SM,
+// bound by issue and by the latency between dependent steps); the same as rms without
+// biases 379 (80%) and 594 (81%).  fp32, 245,003 x 512 rms: 461 (80%) and 666 (89%).
+// Widths that are no multiple of 8 go an element at a time: 200,003 x 777 rms 1.1 ms
+// forward (21%) and 2.0 backward (19%).
 #include <algorithm>
 
 #include "mt_block.cuh"
