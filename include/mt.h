@@ -422,6 +422,99 @@ int mt_gated_norm_backward(const mt_gated_norm* cfg, const mt_rows* dz, const mt
                            const mt_rows* dgate, float* dpost_weight, float* dpost_bias, float* dscale,
                            float* dpre_weight, float* dpre_bias, void* ws, size_t ws_bytes, mt_stream stream);
 
+#define MT_GATE_GELU 4 /* mt_gated_linear only: a = u / (1 + exp(-2 sqrt(2/pi) (u + 0.044715 u^3))), the tanh form */
+
+/* The gated feed-forward part of a block: both projections, the activation and
+ * the product in one pass over the rows,
+ *   y = Wy x, u = Wu x, h = y * act(u)
+ * for the rows x of group g.  w is device [groups, 2 * out_dim, in_dim] of
+ * dtype, contiguous: a group's Wy above its Wu. */
+typedef struct {
+  int64_t n;
+  int32_t in_dim;
+  int32_t out_dim;
+  int32_t groups;
+  int32_t dtype;
+  int32_t gate; /* MT_GATE_LINEAR, _SIGMOID, _SILU or _GELU */
+  int32_t reserved;
+  const int64_t* offsets;
+  int32_t* status;
+  const void* x; /* row tensor [n, in_dim] */
+  int64_t ldx;
+  const void* w;
+} mt_gated_linear;
+
+/* Workspace bytes of a call on these arguments (256-byte aligned; 0: none is
+ * needed, or the arguments are refused).  The forward of bf16 rows and weights
+ * on 16 bytes with widths that are multiples of 8 needs none; others are copied
+ * into a form that the tensor cores take. */
+size_t mt_gated_linear_workspace_bytes(const mt_gated_linear* cfg, int backward);
+/* h: row tensor [n, out_dim], written. */
+int mt_gated_linear_forward(const mt_gated_linear* cfg, void* h, int64_t ldh, void* ws, size_t ws_bytes, mt_stream stream);
+/* Backward from dh: nothing of the forward is kept but x, y and u are computed
+ * again.
+ *  dx  row tensor [n, in_dim], written, or NULL.
+ *  dw  device [groups, 2 * out_dim, in_dim] of dtype, written (zeros for an
+ *      empty group), or NULL.
+ * With bf16 rows the gradients of y and u are rounded to bf16 on the way. */
+int mt_gated_linear_backward(const mt_gated_linear* cfg, const void* dh, int64_t lddh, void* dx, int64_t lddx, void* dw,
+                             void* ws, size_t ws_bytes, mt_stream stream);
+
+/* ---- losses over a vocabulary ------------------------------------------------- */
+
+/* Rows x_i [dim] against a vocabulary of rows w_v (items, or a table's rows of
+ * some keys): logits z_iv = scale * (x_i . w_v), never kept in memory as a
+ * whole, and
+ *   lse_i = log sum over v of exp z_iv.
+ * Cross entropy (top = 0) with target t_i:
+ *   loss_i = lse_i - (1 - smoothing) z_it - smoothing / vocab * sum over v of z_iv + z_loss * lse_i^2
+ * A row whose target is negative takes no part.
+ * Distillation (top = K > 0) from a teacher known by K (id, logit) pairs a row:
+ *   t_ik = softmax over the row's pairs of scale * logit_ik
+ *   loss_i = sum over k of t_ik (log t_ik - z_i,id_k) + lse_i
+ * A pair whose id is negative, or whose logit is -inf, is not there; an id may
+ * come twice (both count); a row without any pair takes no part.
+ * A row that takes no part has loss 0, lse 0 and a zero gradient, and nothing of
+ * it reaches dw, whatever it holds.  A target or id of vocab or more latches
+ * MT_EINVAL into *status and counts as negative.  Row tensors, status, overlap
+ * and determinism as for the dense block above; all sums and statistics are
+ * fp32 or wider. */
+#define MT_MAX_TOP 1024
+typedef struct {
+  int64_t n;
+  int32_t vocab; /* 1 .. MT_MAX_BLOCK_ROWS */
+  int32_t dim;   /* 1 .. MT_MAX_BLOCK_DIM */
+  int32_t dtype; /* of x, w, dx and dw */
+  int32_t top;   /* 0: cross entropy; else K <= MT_MAX_TOP */
+  float scale;   /* > 0 */
+  float smoothing; /* [0, 1); with top: 0 */
+  float z_loss;    /* >= 0; with top: 0 */
+  int32_t id_bytes;      /* 4 or 8: int32 or int64 targets and ids */
+  int32_t teacher_dtype; /* of the teacher's logits: MT_F32 or MT_BF16 */
+  int32_t reserved;
+  const void* x; /* row tensor [n, dim] */
+  int64_t ldx;
+  const void* w; /* row tensor [vocab, dim] */
+  int64_t ldw;
+  const void* targets; /* device [n], or ids [n, top], contiguous */
+  const void* teacher; /* device [n, top], contiguous; NULL for cross entropy */
+  int32_t* status;
+} mt_vocab_loss;
+
+/* Workspace bytes of a call on these arguments (256-byte aligned; 0: refused). */
+size_t mt_vocab_loss_workspace_bytes(const mt_vocab_loss* cfg, int backward);
+/* loss, lse: device fp32 [n], written. */
+int mt_vocab_loss_forward(const mt_vocab_loss* cfg, float* loss, float* lse, void* ws, size_t ws_bytes, mt_stream stream);
+/* Gradients of sum over i of dloss_i loss_i.
+ *  dloss  device fp32 [n].
+ *  lse    device fp32 [n], the forward's.
+ *  dx     row tensor [n, dim], written, or NULL.
+ *  dw     device [vocab, dim] of dtype, contiguous, written, or NULL.
+ * The logits are computed again, a piece of the vocabulary at a time; with bf16
+ * rows a piece's gradient is rounded to bf16 before it is multiplied. */
+int mt_vocab_loss_backward(const mt_vocab_loss* cfg, const float* dloss, const float* lse, void* dx, int64_t lddx, void* dw,
+                           void* ws, size_t ws_bytes, mt_stream stream);
+
 /* ---- automatic table merging ------------------------------------------------ */
 
 /* Feature tables merged into shared tables (MTGenRec TL;DR and abstract:

@@ -25,9 +25,10 @@ __all__ = ["Table", "ShardGroup", "MergedTables", "plan_merge", "LookupResult", 
            "KEY_EMPTY", "KEY_TOMBSTONE",
            "ABI_FUNCTIONS", "profile_enable", "profile_report", "kernel_launches"]
 
-_BLOCK = ("Packed8", "pack8", "unpack8", "GroupedLinear", "GatedNorm", "NormParams", "NormForward", "NormGrads")
+_BLOCK = ("Packed8", "pack8", "unpack8", "GroupedLinear", "GatedNorm", "NormParams", "NormForward", "NormGrads", "GatedLinear")
+_LOSS = ("CrossEntropy", "Distillation", "LossForward")
 if importlib.util.find_spec("torch") is not None:  # the dense block's module is made of it
-    __all__ += _BLOCK
+    __all__ += _BLOCK + _LOSS
 
 MT_OK, MT_EINVAL, MT_ENOSPACE, MT_EFULL, MT_EKEY, MT_ECUDA, MT_ETOOBIG = 0, -1, -2, -3, -4, -5, -6
 ABI_VERSION = 3
@@ -115,6 +116,12 @@ ABI_FUNCTIONS = {
     "mt_gated_norm_forward": (_I32, [_P, _P, _P, _P, _P, _P, _P]),
     "mt_gated_norm_workspace_bytes": (_SZ, [_I64, _C32, _C32]),
     "mt_gated_norm_backward": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "mt_gated_linear_workspace_bytes": (_SZ, [_P, _I32]),
+    "mt_gated_linear_forward": (_I32, [_P, _P, _I64, _P, _SZ, _P]),
+    "mt_gated_linear_backward": (_I32, [_P, _P, _I64, _P, _I64, _P, _P, _SZ, _P]),
+    "mt_vocab_loss_workspace_bytes": (_SZ, [_P, _I32]),
+    "mt_vocab_loss_forward": (_I32, [_P, _P, _P, _P, _SZ, _P]),
+    "mt_vocab_loss_backward": (_I32, [_P, _P, _P, _P, _I64, _P, _P, _SZ, _P]),
     "mt_erase_workspace_bytes": (_SZ, [_I64]),
     "mt_erase": (_I32, [_P, _P, _I64, _P, _P, _SZ, _P]),
     "mt_compact_workspace_bytes": (_SZ, [_P]),
@@ -762,10 +769,13 @@ class MergedTables:
 
 
 def __getattr__(name: str):
-    # the dense block's operators import torch, which importing this package alone does not
-    if name in _BLOCK:
-        from . import block
-        value = getattr(block, name)
+    # the dense block's operators and the losses import torch, which importing this package alone does not
+    if name in _BLOCK or name in _LOSS:
+        if name in _BLOCK:
+            from . import block as module
+        else:
+            from . import loss as module
+        value = getattr(module, name)
         globals()[name] = value
         return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,9 +1,10 @@
 """The dense block between a lookup and its gradient, over ragged groups of rows.
 
 ``GroupedLinear`` (matrix products whose weights differ by row segment),
-``GatedNorm`` (the norm after a block with its gate and residual scale, the
-residual sum and the next block's norm) and ``Packed8`` (activations kept in
-8 bits for the backward) marshal their arguments to the calls of the same
+``GatedLinear`` (the gated feed-forward part: two such products, an activation
+and their product in one pass), ``GatedNorm`` (the norm after a block with its
+gate and residual scale, the residual sum and the next block's norm) and
+``Packed8`` (activations kept in 8 bits for the backward) marshal their arguments to the calls of the same
 names in ``include/mt.h``.  Groups are runs of rows: a batch's feature segments, or the
 tokens sorted by expert.
 
@@ -27,13 +28,14 @@ import torch
 
 from . import LIB_PATH, MT_BF16, MT_EINVAL, MT_F32, MTError, load_library
 
-__all__ = ["Packed8", "pack8", "unpack8", "GroupedLinear", "GatedNorm", "NormParams", "NormForward", "NormGrads"]
+__all__ = ["Packed8", "pack8", "unpack8", "GroupedLinear", "GatedNorm", "NormParams", "NormForward", "NormGrads", "GatedLinear"]
 
 MAX_GROUPS = 1024
 MAX_BLOCK_DIM = 8192
 PACK_BLOCK = 32
 _KINDS = {"rms": 0, "layer": 1}
 _GATES = {"none": 0, "linear": 1, "sigmoid": 2, "silu": 3}
+_FEED_GATES = {"linear": 1, "sigmoid": 2, "silu": 3, "gelu": 4}
 _DTYPES = {"f32": MT_F32, "bf16": MT_BF16}
 _TORCH = {"f32": torch.float32, "bf16": torch.bfloat16}
 _CODES = {torch.float32: MT_F32, torch.bfloat16: MT_BF16}
@@ -59,7 +61,8 @@ def _load_native():
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)
     names = ("mt_pack8", "mt_unpack8", "mt_group_linear_forward", "mt_group_linear_backward", "mt_gated_norm_forward",
-             "mt_gated_norm_backward")
+             "mt_gated_norm_backward", "mt_gated_linear_workspace_bytes", "mt_gated_linear_forward", "mt_gated_linear_backward",
+             "mt_vocab_loss_workspace_bytes", "mt_vocab_loss_forward", "mt_vocab_loss_backward")
     mod.init(*(ctypes.cast(getattr(lib, k), ctypes.c_void_p).value for k in names), MTError, torch.OutOfMemoryError)
     return mod
 
@@ -258,6 +261,44 @@ class GroupedLinear(_Handle):
     def reserve_workspace(self, n: int, stream=None):
         """Allocate, on this stream, the workspace a backward over n rows needs, so that calls up to that size do not."""
         _on(self.device, stream, self._reserved, n)
+
+
+class GatedLinear(_Handle):
+    """The gated feed-forward part of a block, grouped by row segment::
+
+        y_i = Wy_g x_i,  u_i = Wu_g x_i,  h_i = y_i * act(u_i)      for the rows i of group g
+
+    weight is [num_groups, 2 * out_dim, in_dim], a group's Wy above its Wu (what ``GroupedLinear`` takes to make y and u
+    side by side).  One pass makes h; the backward keeps nothing but x and makes y and u again.
+
+    num_groups: 1 to 1024; in_dim, out_dim: 1 to 8192; gate: "linear" (act(u) = u), "sigmoid", "silu" or "gelu" (the
+    tanh form); dtype of x, weight, h and the gradients: "bf16" or "f32"."""
+
+    def __init__(self, num_groups: int, in_dim: int, out_dim: int, gate: str = "silu", dtype: str = "bf16", device=None):
+        if dtype not in _DTYPES or gate not in _FEED_GATES:
+            raise ValueError("unknown gate or dtype")
+        if not 1 <= num_groups <= MAX_GROUPS or not 1 <= in_dim <= MAX_BLOCK_DIM or not 1 <= out_dim <= MAX_BLOCK_DIM:
+            raise MTError(MT_EINVAL, "GatedLinear")
+        super().__init__(device)
+        self.num_groups, self.in_dim, self.out_dim, self.gate, self.dtype = num_groups, in_dim, out_dim, gate, dtype
+        self.torch_dtype = _TORCH[dtype]
+        self._cfg = (num_groups, in_dim, out_dim, _DTYPES[dtype], _FEED_GATES[gate], self.device.index, self._status_ptr)
+
+    def forward(self, x, weight, offsets, out=None, stream=None):
+        """h [n, out_dim] of x [n, in_dim], weight [num_groups, 2 * out_dim, in_dim] and offsets int64 CUDA
+        [num_groups + 1]; rows in no group give zeros."""
+        if stream is None:
+            return _native.gated_forward(*self._cfg, x, weight, offsets, out)
+        return _on(self.device, stream, _native.gated_forward, *self._cfg, x, weight, offsets, out)
+
+    def backward(self, dh, x, weight, offsets, want_dx: bool = True, want_dw: bool = True, out_dx=None, out_dw=None,
+                 stream=None):
+        """(dx [n, in_dim], dw [num_groups, 2 * out_dim, in_dim]), both in the handle's dtype, of dh [n, out_dim] and the
+        forward's input x."""
+        if not want_dx and not want_dw:
+            raise ValueError("nothing to compute")
+        args = (*self._cfg, dh, x, weight, offsets, out_dx, out_dw, int(want_dx), int(want_dw))
+        return _native.gated_backward(*args) if stream is None else _on(self.device, stream, _native.gated_backward, *args)
 
 
 @dataclasses.dataclass

@@ -1,0 +1,380 @@
+// The gated feed-forward part of a block over ragged groups of rows:
+//
+//   forward   y = Wy x, u = Wu x, h = y act(u)          W [groups, Wy over Wu: 2 out, in]
+//   backward  dy = dh act(u), du = dh y act'(u), dx = Wy^T dy + Wu^T du, dW = [dy | du]^T x
+//
+// Forward: one product of both projections.  A tile holds 128 columns of y and
+// the same 128 of u side by side (a pair of blocks: one block copies Wy's rows,
+// the other Wu's), so the epilogue has both in registers and only h is written.
+// Backward: the same product again, y and u meet dh in the epilogue and leave as
+// dt = [dy | du] in the rows' type; then the grouped products of mt_linear*.cu make
+// dx and dW from it.  Nothing but x is kept between the two: y and u would be 4 n out
+// bytes written and read against 4 n in out operations.
+//
+// dt is rounded to bf16 (with bf16 rows) because the tensor cores take it so: each
+// dx and dW is then about as far from the exact value as its own rounding puts it.
+#include <algorithm>
+
+#include "mt_linear.cuh"
+#include "mt_parts.cuh"
+#include "mt_tiles.cuh"
+
+namespace mt {
+namespace {
+
+using tiles::Acc;
+using tiles::Unit;
+
+// The gate's factor and its derivative.  bf16 rows: by the hardware's exponential and reciprocal (2^-22 off).
+template <typename T>
+__device__ __forceinline__ float sigmoid_of(float u) {
+  if constexpr (sizeof(T) == 4) {
+    return 1.0f / (1.0f + expf(-u));
+  } else {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(u * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+  }
+}
+constexpr float kGelu = 1.5957691216057308f, kCube = 0.044715f;  // 2 sqrt(2 / pi)
+
+template <typename T>
+__device__ __forceinline__ float gate_of(int gate, float u) {
+  if (gate == MT_GATE_LINEAR) return u;
+  if (gate == MT_GATE_SIGMOID) return sigmoid_of<T>(u);
+  if (gate == MT_GATE_SILU) return u * sigmoid_of<T>(u);
+  return u * sigmoid_of<T>(kGelu * fmaf(kCube * u * u, u, u));
+}
+template <typename T>
+__device__ __forceinline__ float2 gate_grad(int gate, float u) {
+  if (gate == MT_GATE_LINEAR) return make_float2(u, 1.0f);
+  if (gate == MT_GATE_SIGMOID) {
+    const float p = sigmoid_of<T>(u);
+    return make_float2(p, p * (1.0f - p));
+  }
+  if (gate == MT_GATE_SILU) {
+    const float p = sigmoid_of<T>(u), a = u * p;
+    return make_float2(a, fmaf(a, 1.0f - p, p));
+  }
+  const float uu = u * u, p = sigmoid_of<T>(kGelu * fmaf(kCube * uu, u, u)), a = u * p;
+  return make_float2(a, fmaf(a * (1.0f - p), kGelu * fmaf(3.0f * kCube, uu, 1.0f), p));
+}
+
+struct GatedParams {
+  long long n;
+  const long long* offsets;
+  int32_t* status;
+  const void* dh;
+  void* out;  // h, or dt
+  long long lddh, ldo;
+  int groups, out_dim, jtiles;
+  int u_col;  // dt: the column of du's first
+  int gate;
+  int steps;  // of the contraction, per pass
+  int passes, a_part, b_part, b_second, promote;
+  bool wide, wide_dh;
+};
+
+// T: the rows' type.  BACKWARD: dt instead of h.
+template <typename T, bool BACKWARD>
+struct Gated {
+  using Params = GatedParams;
+  static constexpr int kBN = 256;
+  static constexpr bool kAMN = false, kBMN = false, kTwoB = true;
+  const Params& p;
+  const long long* off;
+  const int* cum;
+  int rank, rows_per_tile, quad, half, lane;
+  uint8_t* stage;
+
+  __device__ Gated(const Params& params, uint8_t* mem, int r) : p(params), rank(r) {
+    long long* s_off = reinterpret_cast<long long*>(mem);
+    int* s_cum = reinterpret_cast<int*>(s_off + p.groups + 1);
+    load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
+    rows_per_tile = tiles::kBM * cluster();
+    count_tiles(s_off, p.groups, rows_per_tile, s_cum);
+    off = s_off;
+    cum = s_cum;
+  }
+  static __device__ __forceinline__ int cluster() {
+    int c;
+    asm("mov.u32 %0, %cluster_nctaid.x;" : "=r"(c));
+    return c;
+  }
+  __device__ long long units() const { return (long long)cum[p.groups] * p.jtiles; }
+  __device__ Unit unit(long long u) const {
+    const int rt = (int)(u / p.jtiles), j = (int)(u - (long long)rt * p.jtiles);
+    Unit x;
+    x.g = tile_group(cum, p.groups, rt);
+    x.row0 = (int)off[x.g] + (rt - cum[x.g]) * rows_per_tile;
+    x.end = (int)off[x.g + 1];
+    x.ct0 = j;
+    x.ct1 = j + 1;
+    x.k0 = 0;
+    x.k1 = p.steps;
+    x.slot = 0;
+    return x;
+  }
+  __device__ void warp(uint8_t* s, int q, int h, int l) {
+    stage = s;
+    quad = q;
+    half = h;
+    lane = l;
+    const int J = BACKWARD ? 2 * p.u_col : p.out_dim;
+    zero_outside<T>(off, p.groups, p.n, static_cast<T*>(p.out), p.ldo, J, tiles::kEpiWarps * 32, (h * 4 + q) * 32 + l);
+  }
+  __device__ void begin(const Unit&) {}
+  __device__ void end(const Unit&) {}
+
+  template <int CG>
+  __device__ __forceinline__ void tile(const Unit& x, int ct, const Acc& acc, bool, bool) {
+    const long long r0 = x.row0 + rank * tiles::kBM + quad * 32;
+    const int rows = min(32, x.end - (int)r0);  // <= 0: none of this warp's rows is in the group
+    T* out = static_cast<T*>(p.out);
+#pragma unroll
+    for (int c = 0; c < 64; c += 32) {
+      const int col = ct * 128 + half * 64 + c;
+      uint32_t y[32], u[32];
+      acc.load(half * 64 + c, y);
+      acc.load(128 + half * 64 + c, u);
+      float d[BACKWARD ? 32 : 1];
+      if constexpr (BACKWARD) {
+        if (col < p.out_dim) tiles::load_rows<T>(stage, lane, d, static_cast<const T*>(p.dh), p.lddh, r0, rows, col, p.out_dim, p.wide_dh);
+      }
+      tc::tmem_load_wait(y);
+      tc::tmem_loaded(u);
+      if (c == 32) acc.release<CG>(lane);
+      float f[32];
+      if constexpr (!BACKWARD) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(y[j]) * gate_of<T>(p.gate, __uint_as_float(u[j]));
+        tiles::store32<T>(stage, lane, f, out, p.ldo, r0, rows, col, p.out_dim, p.wide);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float2 a = gate_grad<T>(p.gate, __uint_as_float(u[j]));
+          u[j] = __float_as_uint(d[j] * __uint_as_float(y[j]) * a.y);
+          f[j] = d[j] * a.x;
+        }
+        tiles::store32<T>(stage, lane, f, out, p.ldo, r0, rows, col, p.out_dim, p.wide);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(u[j]);
+        tiles::store32<T>(stage, lane, f, out + p.u_col, p.ldo, r0, rows, col, p.out_dim, p.wide);
+      }
+    }
+  }
+};
+
+// ---- host --------------------------------------------------------------------------------------
+
+// How a call's operands reach the tensor cores.
+struct Layout {
+  bool copies;     // x and W are copied first: fp32 in three parts, bf16 padded to multiples of 8
+  int parts;
+  int64_t k, m;    // in_dim of a part and out_dim, padded
+  size_t x, w, dt, dx, dw, partial, total;  // where the workspace has them
+};
+
+bool fits(const mt_gated_linear& c) {
+  return c.in_dim % 8 == 0 && c.out_dim % 8 == 0 && (c.n <= 1 || c.ldx % 8 == 0) && is_aligned(c.x, 16) && is_aligned(c.w, 16);
+}
+
+Layout layout_of(const mt_gated_linear& c, bool backward) {
+  Layout l{};
+  l.parts = c.dtype == MT_F32 ? 3 : 1;
+  l.copies = c.dtype == MT_F32 || !fits(c);
+  l.k = part_columns(c.in_dim, l.parts);
+  l.m = c.dtype == MT_F32 ? c.out_dim : (c.out_dim + 7) / 8 * 8;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align_up(bytes, 256);
+    return here;
+  };
+  const size_t e = elem_bytes(c.dtype);
+  if (l.copies) {
+    l.x = take((size_t)c.n * l.parts * l.k * 2);
+    l.w = take((size_t)c.groups * 2 * l.m * l.parts * l.k * 2);
+  }
+  if (backward) {
+    l.dt = take((size_t)c.n * 2 * l.m * e);
+    const bool padded = l.copies && c.dtype == MT_BF16;
+    if (padded) {
+      l.dx = take((size_t)c.n * l.k * 2);
+      l.dw = take((size_t)c.groups * 2 * l.m * l.k * 2);
+    }
+    l.partial = take(partial_bytes(c.n, c.groups, padded ? (int32_t)l.k : c.in_dim, (int32_t)(2 * l.m)));
+  }
+  l.total = at;
+  return l;
+}
+
+int check(const mt_gated_linear* c) {
+  if (c == nullptr || (c->dtype != MT_F32 && c->dtype != MT_BF16)) return MT_EINVAL;
+  if (c->gate < MT_GATE_LINEAR || c->gate > MT_GATE_GELU) return MT_EINVAL;
+  if (c->n < 0 || c->n > MT_MAX_BLOCK_ROWS || c->groups < 1 || c->groups > MT_MAX_GROUPS) return MT_EINVAL;
+  if (c->in_dim < 1 || c->in_dim > MT_MAX_BLOCK_DIM || c->out_dim < 1 || c->out_dim > MT_MAX_BLOCK_DIM) return MT_EINVAL;
+  if (c->offsets == nullptr || !is_aligned(c->offsets, 8) || !is_aligned(c->status, 4)) return MT_EINVAL;
+  if (c->w == nullptr || !is_aligned(c->w, elem_bytes(c->dtype))) return MT_EINVAL;
+  if (c->n > 0 && !rows_ok(c->x, c->ldx, c->in_dim, c->dtype)) return MT_EINVAL;
+  return MT_OK;
+}
+
+template <typename T, bool BACKWARD>
+cudaError_t launch_product(const mt_gated_linear& c, const Layout& l, GatedParams p, char* ws, cudaStream_t s) {
+  const void* x = l.copies ? ws + l.x : c.x;
+  const void* w = l.copies ? ws + l.w : c.w;
+  if (l.copies) {
+    cudaError_t e = launch_parts(c.x, c.ldx, 1, c.n, c.n, c.in_dim, c.dtype, reinterpret_cast<__nv_bfloat16*>(ws + l.x), s);
+    if (e == cudaSuccess)
+      e = launch_parts(c.w, c.in_dim, (int64_t)c.groups * 2, c.out_dim, l.m, c.in_dim, c.dtype, reinterpret_cast<__nv_bfloat16*>(ws + l.w), s);
+    if (e != cudaSuccess) return e;
+  }
+  p.n = c.n;
+  p.offsets = reinterpret_cast<const long long*>(c.offsets);
+  p.status = c.status;
+  p.groups = c.groups;
+  p.out_dim = c.out_dim;
+  p.jtiles = (c.out_dim + 127) / 128;
+  p.gate = c.gate;
+  p.steps = (int)((l.k + tiles::kBK - 1) / tiles::kBK);
+  p.passes = l.parts == 3 ? 6 : 1;
+  p.a_part = p.b_part = (int)l.k;
+  p.b_second = (int)l.m;
+  p.promote = 1 << 30;
+  const bool pair = sizeof(T) == 2 && l.k > 2 * tiles::kBK && c.n / c.groups >= 256 && c.n / 256 * p.jtiles >= sm_count() / 2;
+  CUtensorMap a, b;
+  const uint64_t width = (uint64_t)l.parts * l.k;
+  if (!tc::encode_bf16(&a, 2, x, width, c.n, l.copies ? width : (c.n <= 1 ? width : c.ldx), 1, 0, tiles::kBK, tiles::kBM)) return cudaErrorInvalidValue;
+  if (!tc::encode_bf16(&b, 3, w, width, 2 * l.m, width, c.groups, width * 2 * l.m, tiles::kBK, 128)) return cudaErrorInvalidValue;
+  const size_t extra = rows_smem(c.groups), most = rows_smem(MT_MAX_GROUPS);
+  const char* name = BACKWARD ? "k_gated_backward" : "k_gated_forward";
+  if constexpr (sizeof(T) == 2) {
+    if (pair) return tiles::launch<Gated<T, BACKWARD>, 2>(name, a, b, p, (c.n / 256 + c.groups) * p.jtiles, extra, most, s);
+  }
+  return tiles::launch<Gated<T, BACKWARD>, 1>(name, a, b, p, (c.n / 128 + c.groups) * p.jtiles, extra, most, s);
+}
+
+}  // namespace
+}  // namespace mt
+
+extern "C" {
+
+size_t mt_gated_linear_workspace_bytes(const mt_gated_linear* c, int backward) {
+  using namespace mt;
+  if (check(c) != MT_OK) return 0;
+  return layout_of(*c, backward != 0).total;
+}
+
+int mt_gated_linear_forward(const mt_gated_linear* c, void* h, int64_t ldh, void* ws, size_t ws_bytes, mt_stream stream) {
+  using namespace mt;
+  const int rc = check(c);
+  if (rc != MT_OK) return rc;
+  if (c->n == 0) return MT_OK;
+  if (!rows_ok(h, ldh, c->out_dim, c->dtype)) return MT_EINVAL;
+  const Layout l = layout_of(*c, false);
+  if (l.total > 0 && (ws == nullptr || !is_aligned(ws, 256) || ws_bytes < l.total)) return MT_ENOSPACE;
+  Regions all;
+  all.in(Rows{const_cast<void*>(c->x), c->ldx, nullptr, nullptr}, c->n, c->in_dim, c->dtype);
+  all.in(whole_region(c->w, (size_t)c->groups * 2 * c->out_dim * c->in_dim * elem_bytes(c->dtype)));
+  all.in(whole_region(c->offsets, (size_t)(c->groups + 1) * 8));
+  all.out(Rows{h, ldh, nullptr, nullptr}, c->n, c->out_dim, c->dtype);
+  if (l.total > 0) all.out(whole_region(ws, l.total));
+  if (all.clash()) return MT_EINVAL;
+  GatedParams p{};
+  p.out = h;
+  p.ldo = ldh;
+  p.wide = is_aligned(h, 16) && ldh * elem_bytes(c->dtype) % 16 == 0 && c->out_dim * elem_bytes(c->dtype) % 16 == 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* w = static_cast<char*>(ws);
+  const cudaError_t e = c->dtype == MT_F32 ? launch_product<float, false>(*c, l, p, w, s) : launch_product<__nv_bfloat16, false>(*c, l, p, w, s);
+  return e == cudaSuccess ? MT_OK : MT_ECUDA;
+}
+
+int mt_gated_linear_backward(const mt_gated_linear* c, const void* dh, int64_t lddh, void* dx, int64_t lddx, void* dw, void* ws,
+                             size_t ws_bytes, mt_stream stream) {
+  using namespace mt;
+  const int rc = check(c);
+  if (rc != MT_OK) return rc;
+  if (dx == nullptr && dw == nullptr) return MT_EINVAL;
+  if (c->n > 0 && !rows_ok(dh, lddh, c->out_dim, c->dtype)) return MT_EINVAL;
+  if (c->n > 0 && dx != nullptr && !rows_ok(dx, lddx, c->in_dim, c->dtype)) return MT_EINVAL;
+  if (!is_aligned(dw, elem_bytes(c->dtype))) return MT_EINVAL;
+  const Layout l = layout_of(*c, true);
+  if (ws == nullptr || !is_aligned(ws, 256) || ws_bytes < l.total) return MT_ENOSPACE;
+  const size_t e = elem_bytes(c->dtype), weights = (size_t)c->groups * 2 * c->out_dim * c->in_dim * e;
+  Regions all;
+  if (c->n > 0) {
+    all.in(Rows{const_cast<void*>(dh), lddh, nullptr, nullptr}, c->n, c->out_dim, c->dtype);
+    all.in(Rows{const_cast<void*>(c->x), c->ldx, nullptr, nullptr}, c->n, c->in_dim, c->dtype);
+    if (dx != nullptr) all.out(Rows{dx, lddx, nullptr, nullptr}, c->n, c->in_dim, c->dtype);
+  }
+  all.in(whole_region(c->w, weights));
+  all.in(whole_region(c->offsets, (size_t)(c->groups + 1) * 8));
+  if (dw != nullptr) all.out(whole_region(dw, weights));
+  all.out(whole_region(ws, l.total));
+  if (all.clash()) return MT_EINVAL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (c->n == 0) {
+    if (dw == nullptr) return MT_OK;
+    return cudaMemsetAsync(dw, 0, weights, s) == cudaSuccess ? MT_OK : MT_ECUDA;
+  }
+  char* base = static_cast<char*>(ws);
+  const bool padded = l.copies && c->dtype == MT_BF16;
+  GatedParams p{};
+  p.dh = dh;
+  p.lddh = lddh;
+  p.out = base + l.dt;
+  p.ldo = 2 * l.m;
+  p.u_col = (int)l.m;
+  p.wide = l.m * e % 16 == 0;
+  p.wide_dh = is_aligned(dh, 16) && (c->n <= 1 || lddh * e % 16 == 0) && c->out_dim * e % 16 == 0;
+  cudaError_t err = cudaSuccess;
+  err = c->dtype == MT_F32 ? launch_product<float, true>(*c, l, p, base, s) : launch_product<__nv_bfloat16, true>(*c, l, p, base, s);
+  const int32_t k = padded ? (int32_t)l.k : c->in_dim, m2 = (int32_t)(2 * l.m);
+  if (dx != nullptr && err == cudaSuccess) {
+    LinearRows r{};
+    r.n = c->n;
+    r.groups = c->groups;
+    r.offsets = reinterpret_cast<const long long*>(c->offsets);
+    r.a = base + l.dt;
+    r.lda = 2 * l.m;
+    r.w = padded ? base + l.w : c->w;
+    r.wg = (size_t)k * m2;
+    r.wi = k;
+    r.wj = 1;
+    r.c = padded ? static_cast<void*>(base + l.dx) : dx;
+    r.ldc = padded ? l.k : lddx;
+    r.I = m2;
+    r.J = k;
+    r.status = c->status;
+    err = launch_linear_rows(r, c->dtype, s);
+    if (padded && err == cudaSuccess)
+      err = launch_unpad(reinterpret_cast<__nv_bfloat16*>(base + l.dx), l.k, 1, c->n, c->n, c->in_dim, static_cast<__nv_bfloat16*>(dx), lddx, s);
+  }
+  if (dw != nullptr && err == cudaSuccess) {
+    LinearWeights q{};
+    q.n = c->n;
+    q.groups = c->groups;
+    q.offsets = reinterpret_cast<const long long*>(c->offsets);
+    q.status = c->status;
+    q.dy = base + l.dt;
+    q.lddy = 2 * l.m;
+    q.x = padded ? Rows{base + l.x, l.k, nullptr, nullptr} : Rows{const_cast<void*>(c->x), c->n <= 1 ? c->in_dim : c->ldx, nullptr, nullptr};
+    q.K = k;
+    q.M = m2;
+    q.chosen = reinterpret_cast<int*>(base + l.partial);
+    q.part = reinterpret_cast<float*>(base + l.partial) + 64;
+    if (c->dtype == MT_F32) q.dw = static_cast<float*>(dw);
+    else q.dw16 = padded ? reinterpret_cast<__nv_bfloat16*>(base + l.dw) : static_cast<__nv_bfloat16*>(dw);
+    err = launch_linear_weights(q, c->dtype, s);
+    if (err == cudaSuccess) err = launch_linear_sums(q, s);
+    if (padded && err == cudaSuccess)
+      err = launch_unpad(reinterpret_cast<__nv_bfloat16*>(base + l.dw), l.k, (int64_t)c->groups * 2, c->out_dim, l.m, c->in_dim,
+                         static_cast<__nv_bfloat16*>(dw), c->in_dim, s);
+  }
+  return err == cudaSuccess ? MT_OK : MT_ECUDA;
+}
+
+}  // extern "C"

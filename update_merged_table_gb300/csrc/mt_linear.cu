@@ -326,6 +326,11 @@ __global__ void __launch_bounds__(kThreadsL) k_linear_weights(const LinearWeight
 constexpr int kSumSlices = 8;                 // warps of a block
 constexpr int kSumTask = 32 * kSumSlices * 4;  // values of dW a block sums at a time
 __host__ __device__ inline int sum_tasks(size_t size) { return (int)((size + kSumTask - 1) / kSumTask); }
+// The i-th four values of a sum, as fp32 or (out16) rounded to bf16.
+__device__ __forceinline__ void put4(float* out, __nv_bfloat16* out16, size_t i, const float4& s) {
+  if (out16 != nullptr) reinterpret_cast<uint2*>(out16)[i] = make_uint2(bf16x2_of(s.x, s.y), bf16x2_of(s.z, s.w));
+  else reinterpret_cast<float4*>(out)[i] = s;
+}
 __global__ void __launch_bounds__(32 * kSumSlices) k_linear_sums(const LinearWeights p) {
   extern __shared__ long long s_off[];
   __shared__ float4 s_sum[kSumSlices][32];
@@ -336,7 +341,7 @@ __global__ void __launch_bounds__(32 * kSumSlices) k_linear_sums(const LinearWei
   count_tiles(s_off, p.groups, *p.chosen, s_cum);
   count_slots(s_cum, p.groups, s_slot);
   const size_t size = (size_t)p.M * p.K;
-  const bool four = size % 4 == 0 && ((uintptr_t)p.dw & 15) == 0;  // four values at once
+  const bool four = size % 4 == 0 && ((uintptr_t)p.dw & 15) == 0 && ((uintptr_t)p.dw16 & 7) == 0;  // four values at once
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   // the groups with work: all but those whose only chunk wrote dW itself
   int* s_group = s_slot + p.groups + 1;
@@ -359,6 +364,7 @@ __global__ void __launch_bounds__(32 * kSumSlices) k_linear_sums(const LinearWei
     const int c = s_cum[g + 1] - s_cum[g];
     const float* part = p.part + (size_t)s_slot[g] * size;
     float* out = p.dw + (size_t)g * size;
+    __nv_bfloat16* out16 = p.dw16 != nullptr ? p.dw16 + (size_t)g * size : nullptr;
     const size_t end = size < (size_t)(q + 1) * kSumTask ? size : (size_t)(q + 1) * kSumTask;
     if (four && c >= 2 * kSumSlices) {  // many chunks: the block's warps take every kSumSlices-th, joined in their order
       for (size_t b = (size_t)q * kSumTask / 4; b < end / 4; b += 32) {
@@ -372,7 +378,7 @@ __global__ void __launch_bounds__(32 * kSumSlices) k_linear_sums(const LinearWei
         __syncthreads();
         if (slice == 0 && i < end / 4) {
           for (int k = 1; k < kSumSlices; ++k) add4(s, s_sum[k][lane]);
-          reinterpret_cast<float4*>(out)[i] = s;
+          put4(out, out16, i, s);
         }
         __syncthreads();
       }
@@ -382,14 +388,15 @@ __global__ void __launch_bounds__(32 * kSumSlices) k_linear_sums(const LinearWei
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
         for (int k = 0; k < c; ++k) add4(s, __ldg(reinterpret_cast<const float4*>(part + (size_t)k * size) + i));
-        reinterpret_cast<float4*>(out)[i] = s;
+        put4(out, out16, i, s);
       }
     } else {
       for (size_t i = (size_t)q * kSumTask + threadIdx.x; i < end; i += blockDim.x) {
         float s = 0.0f;
 #pragma unroll 4
         for (int k = 0; k < c; ++k) s += __ldg(part + (size_t)k * size + i);
-        out[i] = s;
+        if (out16 != nullptr) out16[i] = __float2bfloat16_rn(s);
+        else out[i] = s;
       }
     }
   }
@@ -403,9 +410,13 @@ int slots_of(int64_t n, int32_t groups, int32_t k, int32_t m) {
   const long long want = std::max<long long>(2, (long long)kRounds * c.units / c.tiles);
   return (int)std::min<long long>(want, 2 * (n / kMinChunk));
 }
+}  // namespace
+
 size_t partial_bytes(int64_t n, int32_t groups, int32_t k, int32_t m) {
   return align_up((size_t)slots_of(n, groups, k, m) * k * m * 4 + 256, 256);
 }
+
+namespace {
 
 size_t weights_bytes(int32_t groups, int32_t k, int32_t m, int dtype) { return (size_t)groups * k * m * elem_bytes(dtype); }
 
@@ -427,6 +438,8 @@ int linear_check(const int64_t* offsets, int32_t groups, int64_t n, int32_t k, i
 // of 2048 x 2048 15.7 against 33.7.  fp32: 64 on 8 of 512 x 1024 14.2 against 34.4, 8192 on 1024 of 128 x 128 (40 tasks) 103
 // against 109.
 constexpr int kFewTc = 2, kFewPipes = 8, kTasksTc = 3, kTasksPipes = 12;
+
+}  // namespace
 
 cudaError_t launch_linear_rows(LinearRows p, int dtype, cudaStream_t s) {
   const bool tc = dtype == MT_BF16 && linear_rows_fits_tc(p);
@@ -472,6 +485,7 @@ cudaError_t launch_linear_weights(LinearWeights& p, int dtype, cudaStream_t s) {
   p.tiles = tc ? cut.tiles : ((p.M + kTM - 1) / kTM) * ((p.K + kTN - 1) / kTN);
   p.units = tc ? cut.units : sm_count() * 4;
   if (p.n > 0 && tc) return launch_linear_weights_tc(p, cut, s);
+  if (p.dw16 != nullptr) return p.n > 0 ? cudaErrorInvalidValue : cudaSuccess;
   if (p.n > 0) {
     const int grid = weights_blocks(p);
     MT_LAUNCH("k_linear_weights", s);
@@ -490,12 +504,15 @@ cudaError_t launch_linear_weights(LinearWeights& p, int dtype, cudaStream_t s) {
 }
 
 cudaError_t launch_linear_sums(const LinearWeights& p, cudaStream_t s) {
-  if (p.n == 0) return cudaMemsetAsync(p.dw, 0, (size_t)p.groups * p.M * p.K * 4, s);
+  const size_t values = (size_t)p.groups * p.M * p.K;
+  if (p.n == 0) return p.dw16 != nullptr ? cudaMemsetAsync(p.dw16, 0, values * 2, s) : cudaMemsetAsync(p.dw, 0, values * 4, s);
   MT_LAUNCH("k_linear_sums", s);
   const long long tasks = (long long)p.groups * sum_tasks((size_t)p.M * p.K);
   k_linear_sums<<<grid_for(tasks * 256, 256, 8), 256, weights_smem(p.groups) + (size_t)p.groups * 4, s>>>(p);
   return cudaGetLastError();
 }
+
+namespace {
 
 // 8-bit x whose rows do not lie a multiple of 16 bytes apart cannot be copied as it is: it is widened to bf16 rows in
 // the workspace first (one more pass over x, 3 bytes per value).

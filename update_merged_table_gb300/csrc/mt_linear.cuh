@@ -42,6 +42,7 @@ struct LinearWeights {
   int* chosen;      // [1] workspace: the rows of a chunk, as the products chose them, for their sums
   float* part;    // [slots][M][K]: partial products of the groups that have several chunks
   float* dw;      // [groups][M][K]
+  __nv_bfloat16* dw16;  // the same rounded to bf16 in its place (NULL: dw); tensor-core form only
 };
 
 // Dynamic shared memory for the offsets and what is derived from them.
@@ -261,6 +262,10 @@ __device__ __forceinline__ float* weights_out(const LinearWeights& p, const Plan
   if (q.cum[c.g + 1] - q.cum[c.g] == 1) return p.dw + (size_t)c.g * size;
   return p.part + (size_t)(q.slot[c.g] + c.index) * size;
 }
+// The same where dW is bf16: NULL when the chunk's product goes to a slot.
+__device__ __forceinline__ __nv_bfloat16* weights_out16(const LinearWeights& p, const Plan& q, const Chunk& c) {
+  return p.dw16 != nullptr && q.cum[c.g + 1] - q.cum[c.g] == 1 ? p.dw16 + (size_t)c.g * p.M * p.K : nullptr;
+}
 
 // Blocks (pairs) of a launch: no more than there can be tiles (each then has one, as it would of a larger launch).
 inline int weights_blocks(const LinearWeights& p) {
@@ -287,6 +292,13 @@ struct Cut {
   int tiles, units;
 };
 Cut cut_of(int64_t n, int32_t groups, int32_t k, int32_t m, bool pairs);
+
+// What the entry points run (mt_linear.cu), for the operators built on them.  dW: launch_linear_weights fills in the rest of
+// p, the sums go by it; the workspace p.chosen and p.part lies in has partial_bytes().
+cudaError_t launch_linear_rows(LinearRows p, int dtype, cudaStream_t s);
+cudaError_t launch_linear_weights(LinearWeights& p, int dtype, cudaStream_t s);
+cudaError_t launch_linear_sums(const LinearWeights& p, cudaStream_t s);
+size_t partial_bytes(int64_t n, int32_t groups, int32_t k, int32_t m);
 
 // The tensor-core forms (mt_linear_tc.cu): bf16, widths and strides in multiples of 8, rows on 16 bytes.
 bool linear_rows_fits_tc(const LinearRows& p);

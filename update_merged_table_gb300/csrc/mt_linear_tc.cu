@@ -88,6 +88,12 @@ bool encode_u8(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uin
 
 namespace {
 
+using tc::all_released;
+using tc::arrive;
+using tc::drain;
+using tc::latch_status;
+using tc::Slot;
+
 constexpr int kBM = 128;         // tile rows: the lanes of tensor memory
 constexpr int kBK = 64;          // contraction per stage: one 128-byte swizzled row of bf16
 constexpr int kWarpsTC = 6;      // copies, products, four to read out
@@ -114,10 +120,6 @@ struct Barriers {
   volatile uint32_t copied;      // pairs: stages whose copies this block has started
   uint32_t tmem;
 };
-
-__device__ __forceinline__ void latch_status(int32_t* status, int code) {
-  if (status != nullptr) atomicCAS(status, 0, code);
-}
 
 // Set-up that both kernels share: barriers, tensor memory.  Every thread calls it; ends with the block (the pair)
 // synchronised.
@@ -156,56 +158,6 @@ __device__ __forceinline__ void tc_end(uint32_t tmem) {
   else __syncthreads();
   tc::fence_after();
   if (threadIdx.x >> 5 == 1) tc::tmem_free<CG>(tmem, 2 * BN);
-}
-
-// Arrives at a barrier of the block that issues the products.
-template <int CG>
-__device__ __forceinline__ void arrive(uint64_t* bar) {
-  if constexpr (CG == 2) tc::mbar_arrive_at(tc::of_leader(bar));
-  else tc::mbar_arrive(bar);
-}
-
-// The ring's position: stage and the parity of its current use.
-struct Slot {
-  int stage = 0;
-  uint32_t phase = 0;
-  template <int STAGES>
-  __device__ __forceinline__ void next() {
-    if (++stage == STAGES) {
-      stage = 0;
-      phase ^= 1;
-    }
-  }
-};
-
-// The last stages' products are done, and what a pair's first block signals of them has arrived here.
-template <int STAGES>
-__device__ __forceinline__ bool all_released(Barriers& b, Slot s, long long issued) {
-  const long long k = issued < STAGES ? issued : STAGES;
-  for (long long i = 0; i < k; ++i) {
-    if (s.stage == 0) {
-      s.stage = STAGES;
-      s.phase ^= 1;
-    }
-    --s.stage;
-    if (!tc::mbar_wait(&b.empty[s.stage], s.phase)) return false;
-  }
-  return true;
-}
-
-// After a wait ran out: the copies already issued are waited for (again with a limit) so that none lands in a block
-// that has ended.
-template <int STAGES>
-__device__ __forceinline__ void drain(Barriers& b, Slot s, long long issued) {
-  const long long k = issued < STAGES ? issued : STAGES;
-  for (long long i = 0; i < k; ++i) {
-    if (s.stage == 0) {
-      s.stage = STAGES;
-      s.phase ^= 1;
-    }
-    --s.stage;
-    if (!tc::mbar_wait(&b.full[s.stage], s.phase)) return;
-  }
 }
 
 // ---- forward and dx ------------------------------------------------------------------------
@@ -598,6 +550,7 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
       if (t >= total) continue;
       // what outlives the tile's stages is kept few: the registers go to the sums
       float* out;
+      __nv_bfloat16* out16;  // not NULL: dW is bf16, at `out`
       int stages, m_left, len;
       bool k_in;
       int kb;
@@ -610,6 +563,11 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         m_left = p.M - m0;
         k_in = k < p.K;
         out = weights_out(p, plan, x) + (size_t)m0 * p.K + k;
+        out16 = nullptr;
+        if constexpr (!X8) {  // (a bf16 dW from 8 bits is not asked for)
+          out16 = weights_out16(p, plan, x);
+          if (out16 != nullptr) out = reinterpret_cast<float*>(out16 + (size_t)m0 * p.K + k);
+        }
         if constexpr (X8) ex = p.x.exps + row_offset(x.first + ((threadIdx.x & 127) >> 1), nb) + x.k0 / kPackBlock + (threadIdx.x & 1) * 2;
         kb = x.k0 / kPackBlock + (threadIdx.x & 1) * 2;
       }
@@ -689,7 +647,14 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
       // sum[j]: dW at column k0 + 32 quad + lane and row m0 + half kCols + j: 32 lanes write 128 bytes of a row
       size_t ld = p.K;
       asm volatile("" : "+l"(ld));  // keeps the compiler from holding a register per row's offset across the tiles
-      if (k_in) {
+      if (k_in && out16 != nullptr) {
+        out16 = reinterpret_cast<__nv_bfloat16*>(out);
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+          if (j < m_left) *out16 = __float2bfloat16_rn(sum[j]);
+          out16 += ld;
+        }
+      } else if (k_in) {
 #pragma unroll
         for (int j = 0; j < kCols; ++j) {
           if (j < m_left) *out = sum[j];

@@ -176,6 +176,21 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
       : "r"(addr));
 }
 __device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The same, and no use of these registers is moved before it.
+__device__ __forceinline__ void tmem_loaded(uint32_t (&r)[32]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_load_wait(uint32_t (&r)[32]) {
+  tmem_load_wait();
+  tmem_loaded(r);
+}
 
 // ---- products --------------------------------------------------------------------------
 
@@ -229,6 +244,62 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
             smem_addr(bar))
         : "memory");
   }
+}
+
+// ---- rings of stages ------------------------------------------------------------------------
+
+// The ring's position: stage and the parity of its current use.
+struct Slot {
+  int stage = 0;
+  uint32_t phase = 0;
+  template <int STAGES>
+  __device__ __forceinline__ void next() {
+    if (++stage == STAGES) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// Arrives at a barrier of the block that issues the products.
+template <int CG>
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  if constexpr (CG == 2) mbar_arrive_at(of_leader(bar));
+  else mbar_arrive(bar);
+}
+
+// The last stages' products are done, and what a pair's first block signals of them has arrived here.
+template <int STAGES, typename Barriers>
+__device__ __forceinline__ bool all_released(Barriers& b, Slot s, long long issued) {
+  const long long k = issued < STAGES ? issued : STAGES;
+  for (long long i = 0; i < k; ++i) {
+    if (s.stage == 0) {
+      s.stage = STAGES;
+      s.phase ^= 1;
+    }
+    --s.stage;
+    if (!mbar_wait(&b.empty[s.stage], s.phase)) return false;
+  }
+  return true;
+}
+
+// After a wait ran out: the copies already issued are waited for (again with a limit) so that none lands in a block
+// that has ended.
+template <int STAGES, typename Barriers>
+__device__ __forceinline__ void drain(Barriers& b, Slot s, long long issued) {
+  const long long k = issued < STAGES ? issued : STAGES;
+  for (long long i = 0; i < k; ++i) {
+    if (s.stage == 0) {
+      s.stage = STAGES;
+      s.phase ^= 1;
+    }
+    --s.stage;
+    if (!mbar_wait(&b.full[s.stage], s.phase)) return;
+  }
+}
+
+__device__ __forceinline__ void latch_status(int32_t* status, int code) {
+  if (status != nullptr) atomicCAS(status, 0, code);
 }
 
 // 32 bits of two signed bytes each: the pair at bytes 2 * h and 2 * h + 1 of w as two bf16 times `scale` (two equal bf16

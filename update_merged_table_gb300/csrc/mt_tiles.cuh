@@ -1,0 +1,408 @@
+// Tiles of a bf16 matrix product on the tensor cores whose epilogue is the
+// operator: the loop that the gated feed-forward part (mt_gated.cu) and the
+// losses over a vocabulary (mt_vocab*.cu) share.
+//
+// C(i, j) = sum over k of A(i, k) B(j, k), 128 rows i (256 by a pair of blocks)
+// and BN columns j per tile.  One persistent block per SM walks the units that
+// its operator deals out (a row tile and a run of column tiles); one thread
+// keeps a ring of stages filled by TMA, one issues the products into one of two
+// accumulators in tensor memory, and eight warps, two for each 32 lanes, hand
+// finished tiles to the operator while the next tile's products run.
+//
+// An operand lies with its contraction contiguous, or with its rows contiguous
+// (A_MN, B_MN).  fp32 operands come as three bf16 parts side by side whose sum
+// is the value (24 bits in three times 8); a tile then sums the six products of
+// parts that reach 2^-24 of the whole, the small ones first, since the tensor
+// core cuts its accumulator off towards zero at every step and the error goes by
+// the accumulator's size (1.1e-9 of it per 16 products).
+#pragma once
+
+#include "mt_block.cuh"
+#include "mt_tc.cuh"
+
+namespace mt {
+namespace tiles {
+
+constexpr int kBM = 128;        // tile rows of a block: the lanes of tensor memory
+constexpr int kBK = 64;         // contraction per stage: one 128-byte swizzled row of bf16
+constexpr int kEpiWarps = 8;    // two for each 32 lanes of tensor memory, half of a tile's columns each
+constexpr int kWarps = 4 + kEpiWarps;  // copies, products, two idle, epilogue
+constexpr int kThreadsT = kWarps * 32;
+constexpr int kStageOut = 2048;  // bytes per epilogue warp: 32 rows x 64 bytes
+
+template <int BN, int CG>
+struct Ring {
+  static constexpr int kStageA = kBM * kBK * 2, kStageB = BN / CG * kBK * 2;
+  static constexpr int kStage = kStageA + kStageB;
+  static constexpr int kStages = 196608 / kStage;
+  static constexpr int kBytes = kStages * kStage + kEpiWarps * kStageOut;
+};
+
+struct Barriers {
+  uint64_t full[8], empty[8];          // a stage's copies have landed; its products are done
+  uint64_t acc_full[2], acc_empty[2];  // an accumulator is finished; it has been read out
+  uint64_t done;                       // every product issued is done
+  uint32_t tmem;
+};
+
+// The parts that pass q of six multiplies, the smallest products first; of one pass, the only parts.
+__device__ __forceinline__ int part_a(int passes, int q) { return passes == 1 ? 0 : (0x010120 >> (4 * q)) & 3; }
+__device__ __forceinline__ int part_b(int passes, int q) { return passes == 1 ? 0 : (0x001102 >> (4 * q)) & 3; }
+
+// A unit of work: a row tile, column tiles [ct0, ct1) one after the other, contraction steps [k0, k1) of each pass.
+struct Unit {
+  int row0;  // first row of the (pair's) tile
+  int end;   // rows of the tile end here
+  int g;     // group (third coordinate of B)
+  int ct0, ct1;
+  int k0, k1;
+  int slot;  // the operator's
+};
+
+// A finished accumulator as an epilogue warp sees it: its 32 lanes.
+struct Acc {
+  uint32_t from;
+  uint64_t* empty;
+  bool live;  // false: the contraction is empty, everything is zero
+  // 32 columns from c on; tc::tmem_load_wait() before they are used
+  __device__ __forceinline__ void load(int c, uint32_t (&v)[32]) const {
+    if (live) {
+      tc::tmem_load32(from + c, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = 0u;
+    }
+  }
+  // every load is done: the accumulator may be written again
+  template <int CG>
+  __device__ __forceinline__ void release(int lane) const {
+    if (!live) return;
+    tc::fence_before();
+    __syncwarp();
+    if (lane == 0) tc::arrive<CG>(empty);
+  }
+};
+
+// Op: what is computed.
+//   kBN, kAMN, kBMN            tile columns; operands whose rows are contiguous
+//   kTwoB                      (where B's contraction is contiguous) half of the columns b_second rows of B after the others
+//   Params                     passes, a_part, b_part (columns between the parts), promote (stages an accumulator sums
+//                              before it is handed over), status
+//   Op(p, dynamic memory)      every thread; may synchronise the block
+//   units(), unit(u)           the work
+//   warp(stage, quad, half, lane)   once, epilogue warps
+//   begin(x), tile(x, ct, acc, first, last), end(x)   a unit; a column tile's accumulator, or (promote) the parts of it
+template <class Op, int CG>
+__global__ void __launch_bounds__(kThreadsT, 1)
+k_tiles(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+        const __grid_constant__ typename Op::Params p) {
+  constexpr int BN = Op::kBN;
+  using R = Ring<BN, CG>;
+  constexpr int kCols = BN / CG;  // columns of B that a block copies
+  extern __shared__ uint8_t s_raw[];
+  __shared__ Barriers bar;
+  uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)s_raw + 1023) & ~(uintptr_t)1023);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x % CG;  // in the pair
+  Op op(p, ring + R::kBytes, rank);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < R::kStages; ++i) {
+      tc::mbar_init(&bar.full[i], 1);
+      tc::mbar_init(&bar.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&bar.acc_full[i], 1);
+      tc::mbar_init(&bar.acc_empty[i], kEpiWarps * CG);
+    }
+    tc::mbar_init(&bar.done, 1);
+    tc::mbar_init_fence();
+  }
+  __syncwarp();
+  if (warp == 1) tc::tmem_alloc<CG>(&bar.tmem, 2 * BN);
+  tc::fence_before();
+  if constexpr (CG == 2) tc::cluster_sync();
+  else __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = bar.tmem;
+  const long long units = op.units(), u0 = blockIdx.x / CG, ustep = gridDim.x / CG;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tc::Slot s;
+      long long issued = 0;
+      bool ok = true;
+      for (long long u = u0; u < units && ok; u += ustep) {
+        const Unit x = op.unit(u);
+        const int r0 = x.row0 + rank * kBM;
+        for (int ct = x.ct0; ct < x.ct1 && ok; ++ct) {
+          for (int q = 0; q < p.passes && ok; ++q) {
+            const int ap = part_a(p.passes, q) * p.a_part, bp = part_b(p.passes, q) * p.b_part;
+            for (int k = x.k0; k < x.k1; ++k) {
+              ok = tc::mbar_wait(&bar.empty[s.stage], s.phase ^ 1);
+              if (!ok) break;
+              uint8_t* st = ring + s.stage * R::kStage;
+              uint8_t* sb = st + R::kStageA;
+              if constexpr (CG == 2) {  // both blocks' copies count on the first block's barrier
+                const uint32_t full = tc::of_leader(&bar.full[s.stage]);
+                if (rank == 0) tc::mbar_expect(&bar.full[s.stage], 2 * R::kStage);
+                if constexpr (Op::kAMN) {
+#pragma unroll
+                  for (int c = 0; c < kBM / 64; ++c) tc::tma_load_2d_pair(st + c * 8192, &map_a, full, ap + r0 + c * 64, k * kBK);
+                } else {
+                  tc::tma_load_2d_pair(st, &map_a, full, ap + k * kBK, r0);
+                }
+                if constexpr (Op::kBMN) {
+#pragma unroll
+                  for (int c = 0; c < kCols / 64; ++c)
+                    tc::tma_load_2d_pair(sb + c * 8192, &map_b, full, bp + ct * BN + rank * kCols + c * 64, k * kBK);
+                } else if constexpr (Op::kTwoB) {  // the first block copies the first weights' columns, the second the second's
+                  tc::tma_load_3d_pair(sb, &map_b, full, bp + k * kBK, ct * kCols + rank * p.b_second, x.g);
+                } else {
+                  tc::tma_load_2d_pair(sb, &map_b, full, bp + k * kBK, ct * BN + rank * kCols);
+                }
+              } else {
+                uint64_t* full = &bar.full[s.stage];
+                tc::mbar_expect(full, R::kStage);
+                if constexpr (Op::kAMN) {
+#pragma unroll
+                  for (int c = 0; c < kBM / 64; ++c) tc::tma_load_2d(st + c * 8192, &map_a, full, ap + r0 + c * 64, k * kBK);
+                } else {
+                  tc::tma_load_2d(st, &map_a, full, ap + k * kBK, r0);
+                }
+                if constexpr (Op::kBMN) {
+#pragma unroll
+                  for (int c = 0; c < kCols / 64; ++c) tc::tma_load_2d(sb + c * 8192, &map_b, full, bp + ct * BN + c * 64, k * kBK);
+                } else if constexpr (Op::kTwoB) {
+                  tc::tma_load_3d(sb, &map_b, full, bp + k * kBK, ct * (BN / 2), x.g);
+                  tc::tma_load_3d(sb + R::kStageB / 2, &map_b, full, bp + k * kBK, ct * (BN / 2) + p.b_second, x.g);
+                } else {
+                  tc::tma_load_2d(sb, &map_b, full, bp + k * kBK, ct * BN);
+                }
+              }
+              ++issued;
+              s.next<R::kStages>();
+            }
+          }
+        }
+      }
+      ok = ok && tc::all_released<R::kStages>(bar, s, issued);
+      // what the first block signals of its last products has to have arrived here before this block ends
+      if (rank != 0) ok = tc::mbar_wait(&bar.done, 0) && ok;
+      if (!ok) {
+        tc::latch_status(p.status, MT_ECUDA);
+        if (rank == 0) tc::drain<R::kStages>(bar, s, issued);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t instr = tc::instr_bf16(kBM * CG, BN, Op::kAMN, Op::kBMN);
+      tc::Slot s;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true;
+      for (long long u = u0; u < units && ok; u += ustep) {
+        const Unit x = op.unit(u);
+        const int steps = (x.k1 - x.k0) * p.passes;
+        for (int ct = x.ct0; ct < x.ct1 && ok; ++ct) {
+          int part = 0;  // stages that the accumulator has
+          for (int k = 0; k < steps; ++k) {
+            if (part == 0) {
+              ok = tc::mbar_wait(&bar.acc_empty[acc], acc_phase ^ 1);
+              if (!ok) break;
+              tc::fence_after();
+            }
+            ok = tc::mbar_wait<CG == 2>(&bar.full[s.stage], s.phase);
+            if (!ok) break;
+            tc::fence_after();
+            const uint32_t a = tc::smem_addr(ring + s.stage * R::kStage), b = a + R::kStageA;
+#pragma unroll
+            for (int i = 0; i < kBK / 16; ++i) {
+              const uint64_t da = Op::kAMN ? tc::smem_desc(a + i * 2048, 8192) : tc::smem_desc(a + i * 32, 16);
+              const uint64_t db = Op::kBMN ? tc::smem_desc(b + i * 2048, 8192) : tc::smem_desc(b + i * 32, 16);
+              tc::mma_bf16<CG>(tmem + acc * BN, da, db, instr, part > 0 || i > 0);
+            }
+            tc::mma_commit<CG>(&bar.empty[s.stage]);
+            s.next<R::kStages>();
+            if (++part == p.promote || k + 1 == steps) {
+              tc::mma_commit<CG>(&bar.acc_full[acc]);
+              acc ^= 1;
+              acc_phase ^= acc == 0;
+              part = 0;
+            }
+          }
+        }
+      }
+      tc::mma_commit<CG>(&bar.done);  // tensor memory is freed only when no product writes it, also after a wait ran out
+      ok = tc::mbar_wait(&bar.done, 0) && ok;
+      if (!ok) tc::latch_status(p.status, MT_ECUDA);
+    }
+  } else if (warp >= 4) {
+    const int quad = warp & 3, half = (warp - 4) >> 2;
+    op.warp(ring + R::kStages * R::kStage + (warp - 4) * kStageOut, quad, half, lane);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (long long u = u0; u < units && ok; u += ustep) {
+      const Unit x = op.unit(u);
+      op.begin(x);
+      const int steps = (x.k1 - x.k0) * p.passes;
+      for (int ct = x.ct0; ct < x.ct1 && ok; ++ct) {
+        const int parts = steps == 0 ? 1 : (steps + p.promote - 1) / p.promote;
+        for (int part = 0; part < parts; ++part) {
+          if (steps > 0) {
+            ok = __all_sync(kFull, tc::mbar_wait(&bar.acc_full[acc], acc_phase));
+            if (!ok) break;
+            tc::fence_after();
+          }
+          const Acc a{tmem + acc * BN + ((uint32_t)(quad * 32) << 16), &bar.acc_empty[acc], steps > 0};
+          op.template tile<CG>(x, ct, a, part == 0, part + 1 == parts);
+          if (steps > 0) {
+            acc ^= 1;
+            acc_phase ^= acc == 0;
+          }
+        }
+      }
+      if (ok) op.end(x);
+    }
+    if (!ok) tc::latch_status(p.status, MT_ECUDA);
+  }
+  __syncwarp();
+  tc::fence_before();
+  if constexpr (CG == 2) tc::cluster_sync();
+  else __syncthreads();
+  tc::fence_after();
+  if (warp == 1) tc::tmem_free<CG>(tmem, 2 * BN);
+}
+
+// ---- rows through an epilogue warp's shared memory -------------------------------------------
+//
+// A lane holds its row's columns; global memory wants neighbouring lanes on
+// neighbouring columns.  64 bytes of each of 32 rows go through shared memory as
+// four 16-byte pieces, piece c of row r at c ^ ((r >> 1) & 3): writes and reads of
+// eight neighbouring lanes then meet all banks.
+
+__device__ __forceinline__ uint32_t piece_at(int row, int c) { return (uint32_t)(row * 64 + ((c ^ ((row >> 1) & 3)) << 4)); }
+
+// Stores 64 bytes of each lane's row (w: 16 words; element j of the row is column col + j): rows [0, rows) of C from r0 on,
+// columns below J.  WIDE: C's rows lie on 16 bytes and J ends on them.
+template <typename T>
+__device__ __forceinline__ void store_rows(uint8_t* stage, int lane, const uint32_t (&w)[16], T* C, size_t ldc, long long r0,
+                                           int rows, int col, int J, bool wide) {
+  constexpr int kPer = 64 / sizeof(T);  // columns
+  if (col >= J) return;
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<uint4*>(stage + piece_at(lane, c)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+  __syncwarp();
+  if (wide) {
+    const int c = lane & 3, at = col + c * (16 / (int)sizeof(T));
+    T* to = C + (size_t)r0 * ldc + at;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int r = q * 8 + (lane >> 2);
+      if (r < rows && at < J) *reinterpret_cast<uint4*>(to + (size_t)r * ldc) = *reinterpret_cast<const uint4*>(stage + piece_at(r, c));
+    }
+  } else {
+    for (int i = lane; i < 32 * kPer; i += 32) {
+      const int r = i / kPer, j = i % kPer;
+      if (r < rows && col + j < J)
+        C[(size_t)(r0 + r) * ldc + col + j] = *reinterpret_cast<const T*>(stage + piece_at(r, j * (int)sizeof(T) / 16) + j * (int)sizeof(T) % 16);
+    }
+  }
+}
+
+// Loads 32 columns of each lane's row as fp32 (zeros outside): the reverse.
+template <typename T>
+__device__ __forceinline__ void load_rows(uint8_t* stage, int lane, float (&f)[32], const T* C, size_t ldc, long long r0, int rows,
+                                          int col, int J, bool wide) {
+  if (wide) {
+    const T* p = C + (size_t)(r0 + lane) * ldc + col;
+    constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+    for (int c = 0; c < 32 / kPer; ++c) {
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (lane < rows && col + c * kPer < J) v = __ldg(reinterpret_cast<const uint4*>(p) + c);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 4) {
+          f[c * 4 + j] = __uint_as_float(w[j]);
+        } else {
+          f[c * 8 + 2 * j] = __uint_as_float(w[j] << 16);
+          f[c * 8 + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        }
+      }
+    }
+    return;
+  }
+  constexpr int kPer = 64 / sizeof(T);  // columns through the stage at a time
+#pragma unroll
+  for (int h = 0; h < 32 / kPer; ++h) {
+    __syncwarp();
+    for (int i = lane; i < 32 * kPer; i += 32) {
+      const int r = i / kPer, j = i % kPer, at = col + h * kPer + j;
+      T v = from_f<T>(0.0f);
+      if (r < rows && at < J) v = C[(size_t)(r0 + r) * ldc + at];
+      *reinterpret_cast<T*>(stage + piece_at(r, j * (int)sizeof(T) / 16) + j * (int)sizeof(T) % 16) = v;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      f[h * kPer + j] = to_f<T>(*reinterpret_cast<const T*>(stage + piece_at(lane, j * (int)sizeof(T) / 16) + j * (int)sizeof(T) % 16));
+  }
+}
+
+// The same words of 32 fp32 columns: rounded to bf16 (16 words), or half of them as they are.
+__device__ __forceinline__ void narrow32(const float (&f)[32], uint32_t (&w)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) w[j] = bf16x2_of(f[2 * j], f[2 * j + 1]);
+}
+
+// Stores 32 fp32 columns of each lane's row as T.
+template <typename T>
+__device__ __forceinline__ void store32(uint8_t* stage, int lane, const float (&f)[32], T* C, size_t ldc, long long r0, int rows,
+                                        int col, int J, bool wide) {
+  uint32_t w[16];
+  if constexpr (sizeof(T) == 2) {
+    narrow32(f, w);
+    store_rows<T>(stage, lane, w, C, ldc, r0, rows, col, J, wide);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(f[h * 16 + j]);
+      store_rows<T>(stage, lane, w, C, ldc, r0, rows, col + h * 16, J, wide);
+    }
+  }
+}
+
+// ---- host ----------------------------------------------------------------------------------------
+
+// Launches an operator over `units` units (at most), in clusters of CG blocks, with `extra` bytes of its own shared
+// memory of at most `most`.
+template <class Op, int CG>
+cudaError_t launch(const char* name, const CUtensorMap& a, const CUtensorMap& b, const typename Op::Params& p, long long units,
+                   size_t extra, size_t most, cudaStream_t s) {
+  constexpr size_t ring = 1024 + Ring<Op::kBN, CG>::kBytes;  // the stages start on 1024 bytes
+  static SmemLimit limit;
+  const cudaError_t e = limit.allow(k_tiles<Op, CG>, ring + most);
+  if (e != cudaSuccess) return e;
+  const int blocks = sm_count() / CG;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((units < blocks ? (units > 0 ? units : 1) : blocks) * CG));
+  cfg.blockDim = dim3(kThreadsT);
+  cfg.dynamicSmemBytes = ring + extra;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG > 1 ? 1 : 0;
+  MT_LAUNCH(name, s);
+  return cudaLaunchKernelEx(&cfg, k_tiles<Op, CG>, a, b, p);
+}
+
+}  // namespace tiles
+}  // namespace mt

@@ -1,0 +1,622 @@
+// Losses of rows against a vocabulary whose logits are never kept: cross entropy,
+// and distillation from a teacher's top logits.
+//
+//   k_vocab_mark   which rows take part (one bit each)
+//   k_vocab_rows   the rows that do, one after the other: their values as the
+//                  tensor cores take them (bf16; fp32 in three parts), their targets
+//                  in ascending order with their shares, for the backward the row's
+//                  factors.  Rows that take no part cost nothing afterwards, and
+//                  nothing of them can reach a sum.
+//   k_logit_stats  (mt_vocab_logits.cu) largest logit, sum of exponentials, targets'
+//                  logits, per row and run of the vocabulary
+//   k_vocab_loss   joins the runs: lse and loss
+//   k_logit_grad   the gradient of a piece of the logits
+//   k_vocab_dx, k_vocab_dw  (mt_vocab_sums.cu) the products of that piece
+//   k_vocab_dx_sum, k_vocab_dw_sum  partial products joined, rounded, put in place
+#include <algorithm>
+
+#include "mt_tc.cuh"
+#include "mt_vocab.cuh"
+
+namespace mt {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct VocabRows {
+  long long n;
+  int vocab, dim, top;  // top: entries of a row's list (1: cross entropy)
+  bool distill, wide_ids, teacher16;
+  const void* targets;
+  const void* teacher;
+  int32_t* status;
+  float scale, smoothing, z_loss;
+  const void* x;
+  int64_t ldx;
+  // made here
+  uint32_t* mask;   // [ceil(n / 32)]
+  int* live;        // [1]
+  int* pos;         // [n] a row's place among the live ones, -1
+  __nv_bfloat16* xs;  // [n][parts][dp]
+  int dp;
+  int* ids;
+  float* share;
+  float* entropy;   // [n] sum of share log share
+  // backward
+  const float* dloss;
+  const float* lse;
+  float4* coef;
+};
+
+__device__ __forceinline__ long long id_at(const VocabRows& p, long long i) {
+  return p.wide_ids ? static_cast<const long long*>(p.targets)[i] : static_cast<const int*>(p.targets)[i];
+}
+__device__ __forceinline__ float teacher_at(const VocabRows& p, long long i) {
+  return p.teacher16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.teacher)[i]) : static_cast<const float*>(p.teacher)[i];
+}
+__device__ __forceinline__ bool pair_there(const VocabRows& p, long long i, long long id) {
+  return id >= 0 && id < p.vocab && (!p.distill || !(teacher_at(p, i) == -INFINITY));
+}
+
+// A warp per 32 rows.
+__global__ void __launch_bounds__(256) k_vocab_mark(const VocabRows p) {
+  const int lane = threadIdx.x & 31;
+  const long long words = (p.n + 31) / 32;
+  for (long long w = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5; w < words; w += ((long long)gridDim.x * blockDim.x) >> 5) {
+    const long long row = w * 32 + lane;
+    bool there = false, bad = false;
+    if (row < p.n) {
+      for (int k = 0; k < p.top; ++k) {
+        const long long id = id_at(p, row * p.top + k);
+        bad |= id >= p.vocab;
+        there |= pair_there(p, row * p.top + k, id);
+      }
+    }
+    if (bad && p.status != nullptr) atomicCAS(p.status, 0, MT_EINVAL);
+    const unsigned bits = __ballot_sync(kFull, there);
+    if (lane == 0) p.mask[w] = bits;
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+
+// A block per 32 rows, a warp per live row; the last block writes how many there are and puts zeros behind them up to the
+// next 64 rows (a step of dW's contraction).  T: the rows' type; AL: they can be read in 16-byte vectors.
+template <typename T, bool AL>
+__global__ void __launch_bounds__(256) k_vocab_rows(const VocabRows p) {
+  constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
+  extern __shared__ uint8_t s_mem[];
+  __shared__ int s_base;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long words = (p.n + 31) / 32;
+  for (long long w = blockIdx.x; w < words; w += gridDim.x) {
+    if (threadIdx.x == 0) s_base = 0;
+    __syncthreads();
+    int before = 0;
+    for (long long i = threadIdx.x; i < w; i += blockDim.x) before += __popc(p.mask[i]);
+    before = __reduce_add_sync(kFull, before);
+    if (lane == 0) atomicAdd(&s_base, before);
+    __syncthreads();
+    const int base = s_base;
+    const uint32_t bits = p.mask[w];
+    const int own = __popc(bits);
+    if (threadIdx.x < 32 && w * 32 + lane < p.n)
+      p.pos[w * 32 + lane] = bits >> lane & 1 ? base + __popc(bits & ((1u << lane) - 1u)) : -1;
+    for (int k = warp; k < own; k += 8) {
+      const long long row = w * 32 + __fns(bits, 0, k + 1);
+      const size_t at = (size_t)base + k;
+      // the row's values
+      __nv_bfloat16* to = p.xs + at * ((size_t)kParts * p.dp);
+      const Rows x{const_cast<T*>(static_cast<const T*>(p.x) + row * p.ldx), 0, nullptr, nullptr};
+      for (int v = lane; v < p.dp / 8; v += 32) {
+        const Raw8<T> raw = load8<T, AL>(x, 0, v, p.dim);
+        if constexpr (kParts == 1) {
+          *reinterpret_cast<uint4*>(to + v * 8) = raw.a;
+        } else {
+          float f[8];
+          widen8<T>(raw, false, f);
+          uint32_t q[3][4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            __nv_bfloat16 a[3], b[3];
+            split3(f[2 * j], a[0], a[1], a[2]);
+            split3(f[2 * j + 1], b[0], b[1], b[2]);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) q[i][j] = bf16_bits(a[i], b[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < 3; ++i) *reinterpret_cast<uint4*>(to + (size_t)i * p.dp + v * 8) = make_uint4(q[i][0], q[i][1], q[i][2], q[i][3]);
+        }
+      }
+      // its targets and their shares
+      if (!p.distill) {
+        if (lane == 0) {
+          p.ids[at] = (int)id_at(p, row);
+          p.share[at] = 1.0f - p.smoothing;
+        }
+      } else {
+        // ids that are not there come last, with a share of zero
+        int* s_id = reinterpret_cast<int*>(s_mem) + warp * p.top;
+        float* s_t = reinterpret_cast<float*>(s_mem + (size_t)8 * p.top * 4) + warp * p.top;
+        float top = -INFINITY;
+        for (int j = lane; j < p.top; j += 32) {
+          const long long id = id_at(p, row * p.top + j);
+          const bool there = pair_there(p, row * p.top + j, id);
+          s_id[j] = there ? (int)id : 0x7FFFFFFF;
+          s_t[j] = there ? p.scale * teacher_at(p, row * p.top + j) : -INFINITY;
+          top = fmaxf(top, s_t[j]);
+        }
+        top = warp_max(top);
+        float sum = 0.0f;
+        for (int j = lane; j < p.top; j += 32) sum += expf(s_t[j] - top);
+        sum = warp_sum(sum);
+        const float inv = 1.0f / sum, log_sum = logf(sum);
+        float entropy = 0.0f;
+        __syncwarp();
+        for (int j = lane; j < p.top; j += 32) {
+          const int id = s_id[j];
+          int rank = 0;
+          for (int i = 0; i < p.top; ++i) rank += s_id[i] < id || (s_id[i] == id && i < j);
+          const float d = s_t[j] - top, t = expf(d) * inv;
+          p.ids[at * p.top + rank] = id;
+          p.share[at * p.top + rank] = t;
+          if (t != 0.0f) entropy += t * (d - log_sum);
+        }
+        entropy = warp_sum(entropy);
+        if (lane == 0) p.entropy[at] = entropy;
+        __syncwarp();
+      }
+      if (p.coef != nullptr && lane == 0) {
+        const float lse = p.lse[row], g = p.dloss[row] * p.scale;
+        p.coef[at] = make_float4(lse * kLog2e, g * (1.0f + 2.0f * p.z_loss * lse), g * p.smoothing / (float)p.vocab, g);
+      }
+    }
+    if (w + 1 == words) {
+      const int live = base + own;
+      if (threadIdx.x == 0) *p.live = live;
+      const size_t width = (size_t)kParts * p.dp;
+      const size_t first = (size_t)live * width, last = (size_t)((live + 63) / 64 * 64) * width;
+      for (size_t i = first / 8 + threadIdx.x; i < last / 8; i += blockDim.x) reinterpret_cast<uint4*>(p.xs)[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __syncthreads();
+  }
+}
+
+struct VocabLoss {
+  long long n;
+  int vocab, top;
+  const int* pos;
+  const float2* part;
+  const float* sum_z;
+  size_t stride;
+  const int* chunks;
+  const float* picked;
+  const float* share;
+  const float* entropy;  // NULL: cross entropy
+  float scale, smoothing, z_loss;
+  float* loss;
+  float* lse;
+};
+
+// A warp per row: the runs' statistics joined.
+__global__ void __launch_bounds__(256) k_vocab_loss(const VocabLoss p) {
+  const int lane = threadIdx.x & 31;
+  const int slots = 2 * *p.chunks;
+  for (long long row = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5; row < p.n; row += ((long long)gridDim.x * blockDim.x) >> 5) {
+    const int at = p.pos[row];
+    if (at < 0) {
+      if (lane == 0) p.loss[row] = p.lse[row] = 0.0f;
+      continue;
+    }
+    float top = -INFINITY, sum = 0.0f, z = 0.0f;
+    for (int k = lane; k < slots; k += 32) {
+      const float2 q = p.part[(size_t)k * p.stride + at];
+      const float now = fmaxf(top, q.x), off = now == -INFINITY ? 0.0f : now;
+      sum = sum * exp2f(top - off) + q.y * exp2f(q.x - off);
+      top = now;
+      if (p.sum_z != nullptr) z += p.sum_z[(size_t)k * p.stride + at];
+    }
+    const float all = warp_max(top), off = all == -INFINITY ? 0.0f : all;
+    sum = warp_sum(sum * exp2f(top - off));
+    // the largest exponent is whole bits and a fraction: both logarithms in double, so that lse is rounded once
+    const float lse = (float)(((double)all + log2((double)sum)) * 0.69314718055994530942);
+    double loss = lse;
+    if (p.sum_z != nullptr) loss -= (double)p.smoothing / p.vocab * p.scale * (double)warp_sum(z);
+    float told = 0.0f;
+    for (int k = lane; k < p.top; k += 32) {
+      const float t = p.share[(size_t)at * p.top + k];
+      if (t != 0.0f) told += t * p.picked[(size_t)at * p.top + k];
+    }
+    told = warp_sum(told);
+    if (lane == 0) {
+      loss += (double)p.z_loss * lse * lse - (double)p.scale * told;
+      if (p.entropy != nullptr) loss += p.entropy[at];
+      p.loss[row] = (float)loss;
+      p.lse[row] = lse;
+    }
+  }
+}
+
+// dx in its rows' places from the runs' partial products; zeros for rows that take no part.
+template <typename T>
+__global__ void __launch_bounds__(256) k_vocab_dx_sum(const float* part, size_t stride, int splits, const int* pos, long long n, int d, T* dx,
+                                                      int64_t lddx) {
+  const long long total = n * d;
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (long long)gridDim.x * blockDim.x) {
+    const long long row = i / d;
+    const int j = (int)(i - row * d), at = pos[row];
+    float s = 0.0f;
+    if (at >= 0)
+      for (int k = 0; k < splits; ++k) s += part[((size_t)k * stride + at) * d + j];
+    dx[row * lddx + j] = from_f<T>(s);
+  }
+}
+template <typename T>
+__global__ void __launch_bounds__(256) k_vocab_dw_sum(const float* part, size_t stride, int splits, long long values, int d, T* dw) {
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < values; i += (long long)gridDim.x * blockDim.x) {
+    float s = 0.0f;
+    for (int k = 0; k < splits; ++k) s += part[(size_t)k * stride * d + i];
+    dw[i] = from_f<T>(s);
+  }
+}
+
+// ---- host --------------------------------------------------------------------------------------
+
+constexpr size_t kPieceBytes = (size_t)512 << 20;  // of dz at a time
+
+struct Layout {
+  int parts, dp, wp;          // parts of an operand; columns of a part of x and of W
+  bool copy_w;
+  int64_t rows;               // n in multiples of 256
+  int top, max_chunks;
+  int64_t piece;              // entries of the vocabulary at a time, a multiple of 256
+  int dx_splits, dw_splits;
+  size_t mask, live, chunks, pos, xs, ids, share, entropy, w, picked, part, sum_z, coef, dz, dx, dw, total;
+};
+
+int64_t tiles_of(int64_t n, int64_t of) { return (n + of - 1) / of; }
+
+// Pairs of blocks where the product is bound by its arithmetic and there are tiles enough for every pair.
+bool pair_rows(int64_t n, int64_t tiles, int64_t steps) { return steps > 2 && n >= 256 && n / 256 * tiles >= sm_count() / 2; }
+
+Layout layout_of(const mt_vocab_loss& c, bool backward) {
+  Layout l{};
+  l.parts = c.dtype == MT_F32 ? 3 : 1;
+  l.dp = l.wp = (int)part_columns(c.dim, l.parts);
+  l.copy_w = c.dtype == MT_F32 || c.dim % 8 != 0 || (c.vocab > 1 && c.ldw % 8 != 0) || !is_aligned(c.w, 16);
+  l.rows = tiles_of(c.n, 256) * 256;
+  l.top = c.top > 0 ? c.top : 1;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align_up(bytes, 256);
+    return here;
+  };
+  l.mask = take((size_t)tiles_of(c.n, 32) * 4);
+  l.live = take(4);
+  l.chunks = take(4);
+  l.pos = take((size_t)c.n * 4);
+  l.xs = take((size_t)l.rows * l.parts * l.dp * 2);
+  l.ids = take((size_t)c.n * l.top * 4);
+  l.share = take((size_t)c.n * l.top * 4);
+  l.entropy = take(c.top > 0 ? (size_t)c.n * 4 : 0);
+  if (l.copy_w) l.w = take((size_t)c.vocab * l.parts * l.wp * 2);
+  const int sms = std::max(1, sm_count());
+  if (!backward) {
+    l.max_chunks = (int)(16 * sms / (l.rows / 128) + 1);
+    l.picked = take((size_t)c.n * l.top * 4);
+    l.part = take((size_t)2 * l.max_chunks * l.rows * 8);
+    if (c.smoothing > 0.0f) l.sum_z = take((size_t)2 * l.max_chunks * l.rows * 4);
+  } else {
+    l.max_chunks = 1 << 30;
+    const int64_t most = std::max<int64_t>(1, (int64_t)(kPieceBytes / ((size_t)l.rows * l.parts * 512)));
+    const int64_t pieces = tiles_of(tiles_of(c.vocab, 256), most);
+    l.piece = tiles_of(tiles_of(c.vocab, 256), pieces) * 256;
+    l.coef = take((size_t)c.n * 16);
+    l.dz = take((size_t)l.rows * l.parts * l.piece * 2);
+    const int bn = sum_width(c.dim, c.dtype == MT_F32);
+    const int64_t ct = tiles_of(c.dim, bn);
+    // runs of the contraction: enough units of work for every SM, none shorter than 8 steps
+    l.dx_splits = (int)std::max<int64_t>(1, std::min<int64_t>(tiles_of(2 * sms, l.rows / 128 * ct), l.piece / 512));
+    l.dx = take((size_t)l.dx_splits * l.rows * c.dim * 4);
+    l.dw_splits = (int)std::max<int64_t>(1, std::min<int64_t>(sms / std::max<int64_t>(1, l.piece / 128 * ct), tiles_of(c.n, 512)));
+    if (l.dw_splits > 1) l.dw = take((size_t)l.dw_splits * l.piece * c.dim * 4);
+  }
+  l.total = at;
+  return l;
+}
+
+int check(const mt_vocab_loss* c) {
+  if (c == nullptr || (c->dtype != MT_F32 && c->dtype != MT_BF16)) return MT_EINVAL;
+  if (c->n < 0 || c->n > MT_MAX_BLOCK_ROWS || c->vocab < 1 || c->vocab > MT_MAX_BLOCK_ROWS) return MT_EINVAL;
+  if (c->dim < 1 || c->dim > MT_MAX_BLOCK_DIM || c->top < 0 || c->top > MT_MAX_TOP) return MT_EINVAL;
+  if (!(c->scale > 0.0f && c->scale <= 1e30f) || !(c->smoothing >= 0.0f && c->smoothing < 1.0f) || !(c->z_loss >= 0.0f && c->z_loss <= 1e30f))
+    return MT_EINVAL;
+  if (c->top > 0 && (c->smoothing != 0.0f || c->z_loss != 0.0f)) return MT_EINVAL;
+  if (c->id_bytes != 4 && c->id_bytes != 8) return MT_EINVAL;
+  if (c->top > 0 && c->teacher_dtype != MT_F32 && c->teacher_dtype != MT_BF16) return MT_EINVAL;
+  if (!is_aligned(c->status, 4) || !rows_ok(c->w, c->ldw, c->dim, c->dtype)) return MT_EINVAL;
+  if (c->n > 0) {
+    if (!rows_ok(c->x, c->ldx, c->dim, c->dtype) || c->targets == nullptr || !is_aligned(c->targets, c->id_bytes)) return MT_EINVAL;
+    if (c->top > 0 && (c->teacher == nullptr || !is_aligned(c->teacher, elem_bytes(c->teacher_dtype)))) return MT_EINVAL;
+  }
+  return MT_OK;
+}
+
+void inputs_of(const mt_vocab_loss& c, Regions& all) {
+  all.in(Rows{const_cast<void*>(c.x), c.ldx, nullptr, nullptr}, c.n, c.dim, c.dtype);
+  all.in(Rows{const_cast<void*>(c.w), c.ldw, nullptr, nullptr}, c.vocab, c.dim, c.dtype);
+  const size_t pairs = (size_t)c.n * (c.top > 0 ? c.top : 1);
+  all.in(whole_region(c.targets, pairs * c.id_bytes));
+  if (c.top > 0) all.in(whole_region(c.teacher, pairs * elem_bytes(c.teacher_dtype)));
+}
+
+// The rows that take part, and W as the tensor cores take it.
+cudaError_t launch_rows(const mt_vocab_loss& c, const Layout& l, char* ws, const float* dloss, const float* lse, cudaStream_t s) {
+  VocabRows r{};
+  r.n = c.n;
+  r.vocab = c.vocab;
+  r.dim = c.dim;
+  r.top = l.top;
+  r.distill = c.top > 0;
+  r.wide_ids = c.id_bytes == 8;
+  r.teacher16 = c.teacher_dtype == MT_BF16;
+  r.targets = c.targets;
+  r.teacher = c.teacher;
+  r.status = c.status;
+  r.scale = c.scale;
+  r.smoothing = c.smoothing;
+  r.z_loss = c.z_loss;
+  r.x = c.x;
+  r.ldx = c.ldx;
+  r.mask = reinterpret_cast<uint32_t*>(ws + l.mask);
+  r.live = reinterpret_cast<int*>(ws + l.live);
+  r.pos = reinterpret_cast<int*>(ws + l.pos);
+  r.xs = reinterpret_cast<__nv_bfloat16*>(ws + l.xs);
+  r.dp = l.dp;
+  r.ids = reinterpret_cast<int*>(ws + l.ids);
+  r.share = reinterpret_cast<float*>(ws + l.share);
+  r.entropy = reinterpret_cast<float*>(ws + l.entropy);
+  r.dloss = dloss;
+  r.lse = lse;
+  r.coef = dloss != nullptr ? reinterpret_cast<float4*>(ws + l.coef) : nullptr;
+  {
+    MT_LAUNCH("k_vocab_mark", s);
+    k_vocab_mark<<<grid_for(c.n, 256, 8), 256, 0, s>>>(r);
+  }
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  {
+    const bool al = rows_wide(Rows{const_cast<void*>(c.x), c.n <= 1 ? c.dim : c.ldx, nullptr, nullptr}, c.dim, c.dtype);
+    const size_t smem = c.top > 0 ? (size_t)8 * c.top * 8 : 0;
+    const int grid = grid_for(tiles_of(c.n, 32) * 256, 256, 8);
+    auto go = [&](auto kernel, SmemLimit& limit) {
+      const cudaError_t le = limit.allow(kernel, (size_t)8 * MT_MAX_TOP * 8);
+      if (le != cudaSuccess) return le;
+      MT_LAUNCH("k_vocab_rows", s);
+      kernel<<<grid, 256, smem, s>>>(r);
+      return cudaGetLastError();
+    };
+    static SmemLimit limit[4];
+    if (c.dtype == MT_F32) e = al ? go(k_vocab_rows<float, true>, limit[0]) : go(k_vocab_rows<float, false>, limit[1]);
+    else e = al ? go(k_vocab_rows<__nv_bfloat16, true>, limit[2]) : go(k_vocab_rows<__nv_bfloat16, false>, limit[3]);
+  }
+  if (e == cudaSuccess && l.copy_w)
+    e = launch_parts(c.w, c.vocab <= 1 ? c.dim : c.ldw, 1, c.vocab, c.vocab, c.dim, c.dtype, reinterpret_cast<__nv_bfloat16*>(ws + l.w), s);
+  return e;
+}
+
+struct Weights {
+  const char* data;
+  uint64_t width, ld;  // columns and stride, elements
+};
+Weights weights_of(const mt_vocab_loss& c, const Layout& l, const char* ws) {
+  const uint64_t width = (uint64_t)l.parts * l.wp;
+  if (l.copy_w) return {ws + l.w, width, width};
+  return {static_cast<const char*>(c.w), width, c.vocab <= 1 ? width : (uint64_t)c.ldw};
+}
+
+LogitParams logits_of(const mt_vocab_loss& c, const Layout& l, char* ws) {
+  LogitParams p{};
+  p.passes = l.parts == 3 ? 6 : 1;
+  p.a_part = l.dp;
+  p.b_part = l.wp;
+  p.promote = 1 << 30;
+  p.steps = (int)tiles_of(l.dp, 64);
+  p.status = c.status;
+  p.rows = LiveRows{reinterpret_cast<int*>(ws + l.live), reinterpret_cast<int*>(ws + l.ids), reinterpret_cast<float*>(ws + l.share), l.top};
+  p.max_chunks = l.max_chunks;
+  p.scale2 = c.scale * kLog2e;
+  p.stride = l.rows;
+  return p;
+}
+
+}  // namespace
+}  // namespace mt
+
+extern "C" {
+
+size_t mt_vocab_loss_workspace_bytes(const mt_vocab_loss* c, int backward) {
+  using namespace mt;
+  if (check(c) != MT_OK) return 0;
+  if (c->n == 0) return 256;
+  return layout_of(*c, backward != 0).total;
+}
+
+int mt_vocab_loss_forward(const mt_vocab_loss* c, float* loss, float* lse, void* ws, size_t ws_bytes, mt_stream stream) {
+  using namespace mt;
+  const int rc = check(c);
+  if (rc != MT_OK) return rc;
+  if (c->n == 0) return MT_OK;
+  if (loss == nullptr || lse == nullptr || !is_aligned(loss, 4) || !is_aligned(lse, 4)) return MT_EINVAL;
+  const Layout l = layout_of(*c, false);
+  if (ws == nullptr || !is_aligned(ws, 256) || ws_bytes < l.total) return MT_ENOSPACE;
+  Regions all;
+  inputs_of(*c, all);
+  all.out(whole_region(loss, (size_t)c->n * 4));
+  all.out(whole_region(lse, (size_t)c->n * 4));
+  all.out(whole_region(ws, l.total));
+  if (all.clash()) return MT_EINVAL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* base = static_cast<char*>(ws);
+  cudaError_t e = launch_rows(*c, l, base, nullptr, nullptr, s);
+  if (e != cudaSuccess) return MT_ECUDA;
+  LogitParams p = logits_of(*c, l, base);
+  p.v0 = 0;
+  p.columns = c->vocab;
+  p.tiles = (int)tiles_of(c->vocab, 256);
+  p.part = reinterpret_cast<float2*>(base + l.part);
+  p.sum_z = c->smoothing > 0.0f ? reinterpret_cast<float*>(base + l.sum_z) : nullptr;
+  p.picked = reinterpret_cast<float*>(base + l.picked);
+  p.chunks = reinterpret_cast<int*>(base + l.chunks);
+  const bool pair = c->dtype == MT_BF16 && pair_rows(c->n, p.tiles, p.steps);
+  const Weights w = weights_of(*c, l, base);
+  CUtensorMap a, b;
+  const uint64_t width = (uint64_t)l.parts * l.dp;
+  if (!tc::encode_bf16(&a, 2, base + l.xs, width, l.rows, width, 1, 0, 64, 128)) return MT_ECUDA;
+  if (!tc::encode_bf16(&b, 2, w.data, w.width, c->vocab, w.ld, 1, 0, 64, pair ? 128 : 256)) return MT_ECUDA;
+  e = launch_logit_stats(p, a, b, tiles_of(c->n, pair ? 256 : 128), pair, s);
+  if (e != cudaSuccess) return MT_ECUDA;
+  VocabLoss q{};
+  q.n = c->n;
+  q.vocab = c->vocab;
+  q.top = l.top;
+  q.pos = reinterpret_cast<int*>(base + l.pos);
+  q.part = p.part;
+  q.sum_z = p.sum_z;
+  q.stride = l.rows;
+  q.chunks = p.chunks;
+  q.picked = p.picked;
+  q.share = p.rows.share;
+  q.entropy = c->top > 0 ? reinterpret_cast<float*>(base + l.entropy) : nullptr;
+  q.scale = c->scale;
+  q.smoothing = c->smoothing;
+  q.z_loss = c->z_loss;
+  q.loss = loss;
+  q.lse = lse;
+  MT_LAUNCH("k_vocab_loss", s);
+  k_vocab_loss<<<grid_for(c->n * 32, 256, 8), 256, 0, s>>>(q);
+  return cudaGetLastError() == cudaSuccess ? MT_OK : MT_ECUDA;
+}
+
+int mt_vocab_loss_backward(const mt_vocab_loss* c, const float* dloss, const float* lse, void* dx, int64_t lddx, void* dw, void* ws,
+                           size_t ws_bytes, mt_stream stream) {
+  using namespace mt;
+  const int rc = check(c);
+  if (rc != MT_OK) return rc;
+  if (dx == nullptr && dw == nullptr) return MT_EINVAL;
+  if (c->n > 0) {
+    if (dloss == nullptr || lse == nullptr || !is_aligned(dloss, 4) || !is_aligned(lse, 4)) return MT_EINVAL;
+    if (dx != nullptr && !rows_ok(dx, lddx, c->dim, c->dtype)) return MT_EINVAL;
+  }
+  const size_t el = elem_bytes(c->dtype), weights = (size_t)c->vocab * c->dim * el;
+  if (!is_aligned(dw, el)) return MT_EINVAL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (c->n == 0) {
+    if (dw == nullptr) return MT_OK;
+    Regions all;
+    inputs_of(*c, all);
+    all.out(whole_region(dw, weights));
+    if (all.clash()) return MT_EINVAL;
+    return cudaMemsetAsync(dw, 0, weights, s) == cudaSuccess ? MT_OK : MT_ECUDA;
+  }
+  const Layout l = layout_of(*c, true);
+  if (ws == nullptr || !is_aligned(ws, 256) || ws_bytes < l.total) return MT_ENOSPACE;
+  Regions all;
+  inputs_of(*c, all);
+  all.in(whole_region(dloss, (size_t)c->n * 4));
+  all.in(whole_region(lse, (size_t)c->n * 4));
+  if (dx != nullptr) all.out(Rows{dx, lddx, nullptr, nullptr}, c->n, c->dim, c->dtype);
+  if (dw != nullptr) all.out(whole_region(dw, weights));
+  all.out(whole_region(ws, l.total));
+  if (all.clash()) return MT_EINVAL;
+  char* base = static_cast<char*>(ws);
+  cudaError_t e = launch_rows(*c, l, base, dloss, lse, s);
+  const bool fp32 = c->dtype == MT_F32;
+  const Weights w = weights_of(*c, l, base);
+  const uint64_t xw = (uint64_t)l.parts * l.dp;
+  const int bn = sum_width(c->dim, fp32);
+  const int ct = (int)tiles_of(c->dim, bn);
+  const bool wide = c->dim * el % 16 == 0 && is_aligned(dw, 16);
+  for (int64_t v0 = 0; v0 < c->vocab && e == cudaSuccess; v0 += l.piece) {
+    const int64_t columns = std::min<int64_t>(l.piece, c->vocab - v0);
+    const char* wv = w.data + (size_t)v0 * w.ld * 2;
+    LogitParams p = logits_of(*c, l, base);
+    p.v0 = (int)v0;
+    p.columns = (int)columns;
+    p.tiles = (int)tiles_of(columns, 256);
+    p.coef = reinterpret_cast<float4*>(base + l.coef);
+    p.dz = reinterpret_cast<__nv_bfloat16*>(base + l.dz);
+    p.width = (int)(tiles_of(columns, 64) * 64);
+    const uint64_t zw = (uint64_t)l.parts * p.width;
+    CUtensorMap a, b;
+    {
+      const bool pair = !fp32 && pair_rows(c->n, p.tiles, p.steps);
+      if (!tc::encode_bf16(&a, 2, base + l.xs, xw, l.rows, xw, 1, 0, 64, 128)) return MT_ECUDA;
+      if (!tc::encode_bf16(&b, 2, wv, w.width, columns, w.ld, 1, 0, 64, pair ? 128 : 256)) return MT_ECUDA;
+      e = launch_logit_grad(p, l.parts, a, b, tiles_of(c->n, pair ? 256 : 128), pair, s);
+    }
+    SumParams q{};
+    q.passes = p.passes;
+    q.promote = fp32 ? 8 : 1 << 30;
+    q.status = c->status;
+    q.live = p.rows.count;
+    q.a_part = p.width;
+    q.columns = c->dim;
+    q.ctiles = ct;
+    if (dx != nullptr && e == cudaSuccess) {
+      const bool pair = bn == 256 && pair_rows(c->n, (int64_t)ct * l.dx_splits, p.width / 64);
+      if (!tc::encode_bf16(&a, 2, base + l.dz, zw, l.rows, zw, 1, 0, 64, 128)) return MT_ECUDA;
+      if (!tc::encode_bf16(&b, 2, wv, w.width, columns, w.ld, 1, 0, 64, 64)) return MT_ECUDA;
+      q.b_part = l.wp;
+      q.steps = p.width / 64;
+      q.splits = l.dx_splits;
+      q.part = reinterpret_cast<float*>(base + l.dx);
+      q.stride = l.rows;
+      q.add = v0 > 0;
+      e = launch_rows_sum(q, fp32, a, b, tiles_of(c->n, pair ? 256 : 128), pair, s);
+    }
+    if (dw != nullptr && e == cudaSuccess) {
+      const bool pair = bn == 256 && pair_rows(columns, (int64_t)ct * l.dw_splits, tiles_of(c->n, 64));
+      if (!tc::encode_bf16(&a, 2, base + l.dz, zw, l.rows, zw, 1, 0, 64, 64)) return MT_ECUDA;
+      if (!tc::encode_bf16(&b, 2, base + l.xs, xw, l.rows, xw, 1, 0, 64, 64)) return MT_ECUDA;
+      q.b_part = l.dp;
+      q.rows = (int)columns;
+      q.splits = l.dw_splits;
+      q.part = l.dw_splits > 1 ? reinterpret_cast<float*>(base + l.dw) : nullptr;
+      q.stride = l.piece;
+      q.add = false;
+      q.wide = wide;
+      q.out = static_cast<char*>(dw) + (size_t)v0 * c->dim * el;
+      e = launch_vocab_sum(q, fp32, a, b, tiles_of(columns, pair ? 256 : 128), pair, s);
+      if (e == cudaSuccess && l.dw_splits > 1) {
+        const long long values = columns * c->dim;
+        MT_LAUNCH("k_vocab_dw_sum", s);
+        if (fp32) k_vocab_dw_sum<float><<<grid_for(values, 256, 8), 256, 0, s>>>(q.part, q.stride, q.splits, values, c->dim, static_cast<float*>(q.out));
+        else k_vocab_dw_sum<__nv_bfloat16><<<grid_for(values, 256, 8), 256, 0, s>>>(q.part, q.stride, q.splits, values, c->dim, static_cast<__nv_bfloat16*>(q.out));
+        e = cudaGetLastError();
+      }
+    }
+  }
+  if (dx != nullptr && e == cudaSuccess) {
+    const float* part = reinterpret_cast<const float*>(base + l.dx);
+    const int* pos = reinterpret_cast<const int*>(base + l.pos);
+    const int grid = grid_for(c->n * c->dim, 256, 8);
+    MT_LAUNCH("k_vocab_dx_sum", s);
+    if (fp32) k_vocab_dx_sum<float><<<grid, 256, 0, s>>>(part, l.rows, l.dx_splits, pos, c->n, c->dim, static_cast<float*>(dx), lddx);
+    else k_vocab_dx_sum<__nv_bfloat16><<<grid, 256, 0, s>>>(part, l.rows, l.dx_splits, pos, c->n, c->dim, static_cast<__nv_bfloat16*>(dx), lddx);
+    e = cudaGetLastError();
+  }
+  return e == cudaSuccess ? MT_OK : MT_ECUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,69 @@
+// The losses over a vocabulary: what their files share (mt_vocab.cu: entry points
+// and the kernels around the products; mt_vocab_logits.cu: the tiles of logits;
+// mt_vocab_sums.cu: the gradients' products).
+#pragma once
+
+#include <cuda.h>
+
+#include "mt_parts.cuh"
+
+namespace mt {
+
+// The rows that take part, one after the other: "live" rows below.  Everything is sized for n rows; how many are live is
+// known on the device only.
+struct LiveRows {
+  const int* count;     // [1]
+  const int* ids;       // [n][top] a live row's targets in ascending order (top = 1: its target)
+  const float* share;   // [n][top] what each of them has of the target distribution
+  int top;
+};
+
+// The products x W^T of a piece of the vocabulary, as both kernels of logits see them.
+struct LogitParams {
+  int passes, a_part, b_part, promote, steps;
+  int32_t* status;
+  LiveRows rows;
+  int v0, columns;      // the piece: its first entry of the vocabulary, how many it has
+  int tiles;            // of 256 columns
+  int max_chunks;       // runs of tiles that the statistics have room for
+  float scale2;         // scale * log2(e)
+  // statistics
+  float2* part;         // [2 max_chunks][stride]: per run and half of a tile's columns, the largest z and sum of 2^(z - that)
+  float* sum_z;         // the same shape: sums of the logits before the scale (smoothing), or NULL
+  float* picked;        // [n][top] the logits of the row's targets, before the scale
+  size_t stride;
+  int* chunks;          // [1] how many runs the statistics were taken in
+  // gradient of the logits
+  const float4* coef;   // [n] {lse * log2(e), factor of p, what is taken off everywhere, factor of the targets' shares}
+  __nv_bfloat16* dz;    // [stride][parts][width]
+  int width;            // columns of a part of dz: those of the piece in multiples of 64, zeros behind them
+};
+cudaError_t launch_logit_stats(const LogitParams& p, const CUtensorMap& a, const CUtensorMap& b, long long row_tiles, bool pair,
+                               cudaStream_t s);
+cudaError_t launch_logit_grad(const LogitParams& p, int parts, const CUtensorMap& a, const CUtensorMap& b, long long row_tiles, bool pair,
+                              cudaStream_t s);
+
+// C = A B over a contraction that may be cut into `splits` runs, each with its own fp32 partial product (dx), or C itself
+// rounded to its type (dW where splits = 1).
+struct SumParams {
+  int passes, a_part, b_part, promote;
+  int32_t* status;
+  const int* live;      // [1]: rows of C (dx), or the contraction's length (dW)
+  int rows;             // rows of C that are stored (dW)
+  int steps;            // of the contraction (dx)
+  int columns, ctiles;  // of C
+  int splits;
+  float* part;          // [splits][stride][columns], or NULL
+  size_t stride;
+  bool add;             // to what is there
+  bool wide;            // C's rows lie on 16 bytes and end on them
+  void* out;            // [rows][columns]
+};
+// Columns of a tile of C with this many columns.
+inline int sum_width(int64_t columns, bool fp32) { return columns <= 64 ? 64 : columns <= 128 || fp32 ? 128 : 256; }
+cudaError_t launch_rows_sum(const SumParams& p, bool fp32, const CUtensorMap& a, const CUtensorMap& b, long long row_tiles, bool pair,
+                            cudaStream_t s);
+cudaError_t launch_vocab_sum(const SumParams& p, bool fp32, const CUtensorMap& a, const CUtensorMap& b, long long row_tiles, bool pair,
+                             cudaStream_t s);
+
+}  // namespace mt

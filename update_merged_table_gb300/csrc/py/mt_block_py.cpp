@@ -25,6 +25,12 @@ decltype(&mt_group_linear_forward) f_linear_forward;
 decltype(&mt_group_linear_backward) f_linear_backward;
 decltype(&mt_gated_norm_forward) f_norm_forward;
 decltype(&mt_gated_norm_backward) f_norm_backward;
+decltype(&mt_gated_linear_workspace_bytes) f_gated_bytes;
+decltype(&mt_gated_linear_forward) f_gated_forward;
+decltype(&mt_gated_linear_backward) f_gated_backward;
+decltype(&mt_vocab_loss_workspace_bytes) f_vocab_bytes;
+decltype(&mt_vocab_loss_forward) f_vocab_forward;
+decltype(&mt_vocab_loss_backward) f_vocab_backward;
 PyObject* g_mt_error;       // the MTError class
 PyObject* g_out_of_memory;  // torch's
 
@@ -164,19 +170,25 @@ mt_rows saved(PyObject* o, const char* what, int64_t& n, int64_t d, at::ScalarTy
   return saved_parts(PyTuple_GET_ITEM(o, 0), PyTuple_GET_ITEM(o, 1), what, n, d, device);
 }
 
-// init(addresses of the six functions in order, MTError, torch.OutOfMemoryError)
+// init(addresses of the twelve functions in order, MTError, torch.OutOfMemoryError)
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 8, [&]() -> PyObject* {
+  return guarded(n, 14, [&]() -> PyObject* {
     f_pack8 = reinterpret_cast<decltype(f_pack8)>(integer(a[0]));
     f_unpack8 = reinterpret_cast<decltype(f_unpack8)>(integer(a[1]));
     f_linear_forward = reinterpret_cast<decltype(f_linear_forward)>(integer(a[2]));
     f_linear_backward = reinterpret_cast<decltype(f_linear_backward)>(integer(a[3]));
     f_norm_forward = reinterpret_cast<decltype(f_norm_forward)>(integer(a[4]));
     f_norm_backward = reinterpret_cast<decltype(f_norm_backward)>(integer(a[5]));
-    Py_INCREF(a[6]);
-    g_mt_error = a[6];
-    Py_INCREF(a[7]);
-    g_out_of_memory = a[7];
+    f_gated_bytes = reinterpret_cast<decltype(f_gated_bytes)>(integer(a[6]));
+    f_gated_forward = reinterpret_cast<decltype(f_gated_forward)>(integer(a[7]));
+    f_gated_backward = reinterpret_cast<decltype(f_gated_backward)>(integer(a[8]));
+    f_vocab_bytes = reinterpret_cast<decltype(f_vocab_bytes)>(integer(a[9]));
+    f_vocab_forward = reinterpret_cast<decltype(f_vocab_forward)>(integer(a[10]));
+    f_vocab_backward = reinterpret_cast<decltype(f_vocab_backward)>(integer(a[11]));
+    Py_INCREF(a[12]);
+    g_mt_error = a[12];
+    Py_INCREF(a[13]);
+    g_out_of_memory = a[13];
     Py_RETURN_NONE;
   });
 }
@@ -442,9 +454,181 @@ PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
   });
 }
 
+// ---- the gated feed-forward part and the losses -----------------------------------------
+//
+// Their workspaces are made here, on the call's stream, and go back to torch's allocator with the call: work that follows
+// on the stream may use the memory, and a captured call's lies in its graph's own.
+
+struct Workspace {
+  at::Tensor t;
+  Workspace(size_t bytes, int device) {
+    if (bytes > 0) t = make({(int64_t)bytes}, at::kByte, device);
+  }
+  void* data() const { return t.defined() ? t.data_ptr() : nullptr; }
+  size_t size() const { return t.defined() ? (size_t)t.numel() : 0; }
+};
+
+// groups, in, out, dtype, gate, device, status
+constexpr int kGatedArgs = 7;
+mt_gated_linear gated_config(PyObject* const* a, PyObject* x, PyObject* w, PyObject* offsets, int64_t& n) {
+  mt_gated_linear c{};
+  c.groups = (int32_t)integer(a[0]);
+  c.in_dim = (int32_t)integer(a[1]);
+  c.out_dim = (int32_t)integer(a[2]);
+  c.dtype = (int32_t)integer(a[3]);
+  c.gate = (int32_t)integer(a[4]);
+  const int device = (int)integer(a[5]);
+  c.status = reinterpret_cast<int32_t*>(integer(a[6]));
+  const mt_rows r = rows(x, "x", n, c.in_dim, type_of(c.dtype), device);
+  c.n = n;
+  c.x = r.data;
+  c.ldx = r.ld;
+  c.w = whole(w, "weight", type_of(c.dtype), device, c.groups, 2 * (int64_t)c.out_dim, c.in_dim);
+  c.offsets = offsets_of(offsets, c.groups, device);
+  return c;
+}
+
+// gated_forward(config..., x, w, offsets, h or None) -> h
+PyObject* gated_forward(PyObject*, PyObject* const* a, Py_ssize_t count) {
+  return guarded(count, kGatedArgs + 4, [&]() -> PyObject* {
+    PyObject* const* b = a + kGatedArgs;
+    int64_t n = -1;
+    const mt_gated_linear c = gated_config(a, b[0], b[1], b[2], n);
+    const int device = (int)integer(a[5]);
+    On on(device);
+    std::optional<at::Tensor> h;
+    const mt_rows r = output(b[3], "out", n, c.out_dim, type_of(c.dtype), device, h);
+    if (n > 0) {
+      const Workspace ws(f_gated_bytes(&c, 0), device);
+      check(f_gated_forward(&c, r.data, r.ld, ws.data(), ws.size(), on.stream), "mt_gated_linear_forward");
+    }
+    return wrap(*h);
+  });
+}
+
+// A gradient of the weights: the caller's, or a new one.
+void* weights_out(PyObject* given, at::ScalarType type, int device, at::IntArrayRef size, std::optional<at::Tensor>& t) {
+  if (given != Py_None) {
+    void* p = whole(given, "out_dw", type, device, size[0], size[1], size.size() > 2 ? size[2] : -1);
+    t = THPVariable_Unpack(given);
+    return p;
+  }
+  t = make(size, type, device);
+  return t->data_ptr();
+}
+
+// gated_backward(config..., dh, x, w, offsets, dx or None, dw or None, want_dx, want_dw) -> (dx, dw)
+PyObject* gated_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
+  return guarded(count, kGatedArgs + 8, [&]() -> PyObject* {
+    PyObject* const* b = a + kGatedArgs;
+    int64_t n = -1;
+    const mt_gated_linear c = gated_config(a, b[1], b[2], b[3], n);
+    const int device = (int)integer(a[5]);
+    const at::ScalarType type = type_of(c.dtype);
+    const mt_rows dh = rows(b[0], "dh", n, c.out_dim, type, device);
+    const bool want_dx = integer(b[6]) != 0, want_dw = integer(b[7]) != 0;
+    On on(device);
+    std::optional<at::Tensor> dx, dw;
+    const mt_rows rdx = want_dx ? output(b[4], "out_dx", n, c.in_dim, type, device, dx) : none_rows();
+    void* pdw = want_dw ? weights_out(b[5], type, device, {c.groups, 2 * (int64_t)c.out_dim, c.in_dim}, dw) : nullptr;
+    if (n > 0 || want_dw) {
+      const Workspace ws(f_gated_bytes(&c, 1), device);
+      check(f_gated_backward(&c, dh.data, dh.ld, n > 0 ? rdx.data : nullptr, rdx.ld, pdw, ws.data(), ws.size(), on.stream),
+            "mt_gated_linear_backward");
+    }
+    return Py_BuildValue("(NN)", wrap_or_none(dx), wrap_or_none(dw));
+  });
+}
+
+// vocab, dim, dtype, top, scale, smoothing, z_loss, device, status
+constexpr int kVocabArgs = 9;
+mt_vocab_loss vocab_config(PyObject* const* a, PyObject* x, PyObject* w, PyObject* targets, PyObject* teacher, int64_t& n) {
+  mt_vocab_loss c{};
+  c.vocab = (int32_t)integer(a[0]);
+  c.dim = (int32_t)integer(a[1]);
+  c.dtype = (int32_t)integer(a[2]);
+  c.top = (int32_t)integer(a[3]);
+  c.scale = (float)PyFloat_AsDouble(a[4]);
+  c.smoothing = (float)PyFloat_AsDouble(a[5]);
+  c.z_loss = (float)PyFloat_AsDouble(a[6]);
+  const int device = (int)integer(a[7]);
+  c.status = reinterpret_cast<int32_t*>(integer(a[8]));
+  const mt_rows r = rows(x, "x", n, c.dim, type_of(c.dtype), device);
+  c.n = n;
+  c.x = r.data;
+  c.ldx = r.ld;
+  int64_t v = c.vocab;
+  const mt_rows rw = rows(w, "weight", v, c.dim, type_of(c.dtype), device);
+  c.w = rw.data;
+  c.ldw = rw.ld;
+  const char* what = c.top > 0 ? "ids" : "targets";
+  const at::ScalarType id = tensor(targets, what).scalar_type();
+  if (id != at::kInt && id != at::kLong) raise(PyExc_TypeError, std::string(what) + " must be int32 or int64");
+  c.id_bytes = id == at::kInt ? 4 : 8;
+  c.targets = c.top > 0 ? whole(targets, what, id, device, n, c.top) : whole(targets, what, id, device, n, -1);
+  if (c.top > 0) {
+    const at::ScalarType t = tensor(teacher, "logits").scalar_type();
+    if (t != at::kFloat && t != at::kBFloat16) raise(PyExc_TypeError, "logits must be float32 or bfloat16");
+    c.teacher_dtype = t == at::kFloat ? MT_F32 : MT_BF16;
+    c.teacher = whole(teacher, "logits", t, device, n, c.top);
+  }
+  return c;
+}
+
+// vocab_forward(config..., x, w, targets, teacher or None, loss or None, lse or None) -> (loss, lse)
+PyObject* vocab_forward(PyObject*, PyObject* const* a, Py_ssize_t count) {
+  return guarded(count, kVocabArgs + 6, [&]() -> PyObject* {
+    PyObject* const* b = a + kVocabArgs;
+    int64_t n = -1;
+    const mt_vocab_loss c = vocab_config(a, b[0], b[1], b[2], b[3], n);
+    const int device = (int)integer(a[7]);
+    On on(device);
+    at::Tensor out[2];
+    static const char* const names[] = {"out_loss", "out_lse"};
+    for (int i = 0; i < 2; ++i) {
+      if (b[4 + i] != Py_None) {
+        whole(b[4 + i], names[i], at::kFloat, device, n, -1);
+        out[i] = THPVariable_Unpack(b[4 + i]);
+      } else {
+        out[i] = make({n}, at::kFloat, device);
+      }
+    }
+    if (n > 0) {
+      const Workspace ws(f_vocab_bytes(&c, 0), device);
+      check(f_vocab_forward(&c, static_cast<float*>(out[0].data_ptr()), static_cast<float*>(out[1].data_ptr()), ws.data(), ws.size(), on.stream),
+            "mt_vocab_loss_forward");
+    }
+    return Py_BuildValue("(NN)", wrap(out[0]), wrap(out[1]));
+  });
+}
+
+// vocab_backward(config..., dloss, lse, x, w, targets, teacher or None, dx or None, dw or None, want_dx, want_dw) -> (dx, dw)
+PyObject* vocab_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
+  return guarded(count, kVocabArgs + 10, [&]() -> PyObject* {
+    PyObject* const* b = a + kVocabArgs;
+    int64_t n = -1;
+    const mt_vocab_loss c = vocab_config(a, b[2], b[3], b[4], b[5], n);
+    const int device = (int)integer(a[7]);
+    const at::ScalarType type = type_of(c.dtype);
+    const float* dloss = static_cast<const float*>(whole(b[0], "dloss", at::kFloat, device, n, -1));
+    const float* lse = static_cast<const float*>(whole(b[1], "lse", at::kFloat, device, n, -1));
+    const bool want_dx = integer(b[8]) != 0, want_dw = integer(b[9]) != 0;
+    On on(device);
+    std::optional<at::Tensor> dx, dw;
+    const mt_rows rdx = want_dx ? output(b[6], "out_dx", n, c.dim, type, device, dx) : none_rows();
+    void* pdw = want_dw ? weights_out(b[7], type, device, {c.vocab, c.dim}, dw) : nullptr;
+    if (n > 0 || want_dw) {
+      const Workspace ws(f_vocab_bytes(&c, 1), device);
+      check(f_vocab_backward(&c, dloss, lse, n > 0 ? rdx.data : nullptr, rdx.ld, pdw, ws.data(), ws.size(), on.stream), "mt_vocab_loss_backward");
+    }
+    return Py_BuildValue("(NN)", wrap_or_none(dx), wrap_or_none(dw));
+  });
+}
+
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(init),           FAST(pack8),        FAST(unpack8),       FAST(linear_forward),
-                         FAST(linear_backward), FAST(norm_forward), FAST(norm_backward), {nullptr, nullptr, 0, nullptr}};
+                         FAST(linear_backward), FAST(norm_forward), FAST(norm_backward), FAST(gated_forward),
+                         FAST(gated_backward), FAST(vocab_forward), FAST(vocab_backward), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mt_block", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
