@@ -12,6 +12,7 @@
 //   k_vocab_loss   joins the runs: lse and loss
 //   k_logit_grad   the gradient of a piece of the logits
 //   k_vocab_dx, k_vocab_dw  (mt_vocab_sums.cu) the products of that piece
+//   k_vocab_fused_dx, k_vocab_fused_dw  (mt_vocab_fused.cu) both without the piece in memory, for narrow rows
 //   k_vocab_dx_sum, k_vocab_dw_sum  partial products joined, rounded, put in place
 #include <algorithm>
 
@@ -90,7 +91,7 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 
 // A block per 32 rows, a warp per live row; the last block writes how many there are and puts zeros behind them up to the
-// next 64 rows (a step of dW's contraction).  T: the rows' type; AL: they can be read in 16-byte vectors.
+// next 128 rows (steps of dW's contraction).  T: the rows' type; AL: they can be read in 16-byte vectors.
 template <typename T, bool AL>
 __global__ void __launch_bounds__(256) k_vocab_rows(const VocabRows p) {
   constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const VocabRows p) {
       const int live = base + own;
       if (threadIdx.x == 0) *p.live = live;
       const size_t width = (size_t)kParts * p.dp;
-      const size_t first = (size_t)live * width, last = (size_t)((live + 63) / 64 * 64) * width;
+      const size_t first = (size_t)live * width, last = (size_t)((live + 127) / 128 * 128) * width;
       for (size_t i = first / 8 + threadIdx.x; i < last / 8; i += blockDim.x) reinterpret_cast<uint4*>(p.xs)[i] = make_uint4(0u, 0u, 0u, 0u);
     }
     __syncthreads();
@@ -217,51 +218,72 @@ __global__ void __launch_bounds__(256) k_vocab_loss(const VocabLoss p) {
       if (lane == 0) p.loss[row] = p.lse[row] = 0.0f;
       continue;
     }
-    float top = -INFINITY, sum = 0.0f, z = 0.0f;
+    // the runs' largest logit first (their loads do not wait for one another), then their sums brought to it
+    float top = -INFINITY;
+#pragma unroll 4
+    for (int k = lane; k < slots; k += 32) top = fmaxf(top, p.part[(size_t)k * p.stride + at].x);
+    top = warp_max(top);
+    const float off = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f, z = 0.0f, told = 0.0f;
+#pragma unroll 4
     for (int k = lane; k < slots; k += 32) {
       const float2 q = p.part[(size_t)k * p.stride + at];
-      const float now = fmaxf(top, q.x), off = now == -INFINITY ? 0.0f : now;
-      sum = sum * exp2f(top - off) + q.y * exp2f(q.x - off);
-      top = now;
+      sum += q.y * exp2f(q.x - off);
       if (p.sum_z != nullptr) z += p.sum_z[(size_t)k * p.stride + at];
     }
-    const float all = warp_max(top), off = all == -INFINITY ? 0.0f : all;
-    sum = warp_sum(sum * exp2f(top - off));
-    // the largest exponent is whole bits and a fraction: both logarithms in double, so that lse is rounded once
-    const float lse = (float)(((double)all + log2((double)sum)) * 0.69314718055994530942);
-    double loss = lse;
-    if (p.sum_z != nullptr) loss -= (double)p.smoothing / p.vocab * p.scale * (double)warp_sum(z);
-    float told = 0.0f;
     for (int k = lane; k < p.top; k += 32) {
       const float t = p.share[(size_t)at * p.top + k];
       if (t != 0.0f) told += t * p.picked[(size_t)at * p.top + k];
     }
+    sum = warp_sum(sum);
     told = warp_sum(told);
+    const float lse = fmaf(top, 0.693147181f, logf(sum));
+    float loss = fmaf(-p.scale, told, lse);
+    if (p.sum_z != nullptr) loss = fmaf(-p.smoothing / (float)p.vocab * p.scale, warp_sum(z), loss);
     if (lane == 0) {
-      loss += (double)p.z_loss * lse * lse - (double)p.scale * told;
       if (p.entropy != nullptr) loss += p.entropy[at];
-      p.loss[row] = (float)loss;
+      p.loss[row] = fmaf(p.z_loss * lse, lse, loss);
       p.lse[row] = lse;
     }
   }
 }
 
-// dx in its rows' places from the runs' partial products; zeros for rows that take no part.
-template <typename T>
+// dx in its rows' places from the runs' partial products; zeros for rows that take no part.  FOUR: four columns a thread.
+// cut: NULL, or where only the live rows from cut[0] on come in several runs, cut[1] of them.
+template <typename T, bool FOUR>
 __global__ void __launch_bounds__(256) k_vocab_dx_sum(const float* part, size_t stride, int splits, const int* pos, long long n, int d, T* dx,
-                                                      int64_t lddx) {
-  const long long total = n * d;
+                                                      int64_t lddx, const int* cut) {
+  constexpr int kPer = FOUR ? 4 : 1;
+  const int per_row = d / kPer;
+  const long long total = n * per_row;
   for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (long long)gridDim.x * blockDim.x) {
-    const long long row = i / d;
-    const int j = (int)(i - row * d), at = pos[row];
-    float s = 0.0f;
-    if (at >= 0)
-      for (int k = 0; k < splits; ++k) s += part[((size_t)k * stride + at) * d + j];
-    dx[row * lddx + j] = from_f<T>(s);
+    const long long row = i / per_row;
+    const int j = (int)(i - row * per_row) * kPer, at = pos[row];
+    const float* from = part + (size_t)at * d + j;
+    const int runs = cut == nullptr ? splits : at >= cut[0] ? cut[1] : 1;
+    T* to = dx + row * lddx + j;
+    if constexpr (FOUR) {
+      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (at >= 0) {
+#pragma unroll 4
+        for (int k = 0; k < runs; ++k) {
+          const float4 v = __ldg(reinterpret_cast<const float4*>(from + (size_t)k * stride * d));
+          s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+        }
+      }
+      if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(to) = s;
+      else *reinterpret_cast<uint2*>(to) = make_uint2(bf16x2_of(s.x, s.y), bf16x2_of(s.z, s.w));
+    } else {
+      float s = 0.0f;
+      if (at >= 0)
+        for (int k = 0; k < runs; ++k) s += from[(size_t)k * stride * d];
+      *to = from_f<T>(s);
+    }
   }
 }
 template <typename T>
-__global__ void __launch_bounds__(256) k_vocab_dw_sum(const float* part, size_t stride, int splits, long long values, int d, T* dw) {
+__global__ void __launch_bounds__(256) k_vocab_dw_sum(const float* part, size_t stride, int splits, long long values, int d, T* dw, const int* cut) {
+  if (cut != nullptr) splits = cut[1];
   for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < values; i += (long long)gridDim.x * blockDim.x) {
     float s = 0.0f;
     for (int k = 0; k < splits; ++k) s += part[(size_t)k * stride * d + i];
@@ -275,12 +297,13 @@ constexpr size_t kPieceBytes = (size_t)512 << 20;  // of dz at a time
 
 struct Layout {
   int parts, dp, wp;          // parts of an operand; columns of a part of x and of W
-  bool copy_w;
+  bool copy_w, fused;         // fused: the gradients without dz in memory
+  int whole, runs_dx, runs_dw;  // fused: dW's tiles that need no partial products; room for runs of the others
   int64_t rows;               // n in multiples of 256
   int top, max_chunks;
   int64_t piece;              // entries of the vocabulary at a time, a multiple of 256
   int dx_splits, dw_splits;
-  size_t mask, live, chunks, pos, xs, ids, share, entropy, w, picked, part, sum_z, coef, dz, dx, dw, total;
+  size_t mask, live, chunks, cut, pos, xs, ids, share, entropy, w, picked, part, sum_z, coef, dz, dx, dw, total;
 };
 
 int64_t tiles_of(int64_t n, int64_t of) { return (n + of - 1) / of; }
@@ -316,6 +339,17 @@ Layout layout_of(const mt_vocab_loss& c, bool backward) {
     l.picked = take((size_t)c.n * l.top * 4);
     l.part = take((size_t)2 * l.max_chunks * l.rows * 8);
     if (c.smoothing > 0.0f) l.sum_z = take((size_t)2 * l.max_chunks * l.rows * 4);
+  } else if (c.dtype == MT_BF16 && c.dim <= kFusedColumns) {
+    // room for as many runs as give every block eight units, of the tiles that are cut at all
+    l.fused = true;
+    const int64_t rt = tiles_of(c.n, kFusedTile), vt = tiles_of(c.vocab, kFusedTile);
+    l.cut = take(16);
+    l.coef = take((size_t)c.n * 16);
+    l.runs_dx = (int)std::min<int64_t>(vt, rt < sms ? 8 * sms / rt + 1 : 4);
+    l.dx = take((size_t)l.runs_dx * l.rows * c.dim * 4);
+    l.whole = (int)(vt / sms * sms);
+    l.runs_dw = vt > l.whole ? (int)std::min<int64_t>(rt, 8 * sms / (vt - l.whole) + 1) : 0;
+    l.dw = take((size_t)l.runs_dw * (vt - l.whole) * kFusedTile * c.dim * 4);
   } else {
     l.max_chunks = 1 << 30;
     const int64_t most = std::max<int64_t>(1, (int64_t)(kPieceBytes / ((size_t)l.rows * l.parts * 512)));
@@ -547,7 +581,44 @@ int mt_vocab_loss_backward(const mt_vocab_loss* c, const float* dloss, const flo
   const int bn = sum_width(c->dim, fp32);
   const int ct = (int)tiles_of(c->dim, bn);
   const bool wide = c->dim * el % 16 == 0 && is_aligned(dw, 16);
-  for (int64_t v0 = 0; v0 < c->vocab && e == cudaSuccess; v0 += l.piece) {
+  if (l.fused && e == cudaSuccess) {
+    FusedParams f{};
+    f.status = c->status;
+    f.rows = logits_of(*c, l, base).rows;
+    f.vocab = c->vocab;
+    f.columns = c->dim;
+    f.scale2 = c->scale * kLog2e;
+    f.coef = reinterpret_cast<float4*>(base + l.coef);
+    f.wide = wide;
+    f.out = static_cast<__nv_bfloat16*>(dw);
+    CUtensorMap a, b;
+    if (!tc::encode_bf16(&a, 2, base + l.xs, xw, l.rows, xw, 1, 0, 64, kFusedTile)) return MT_ECUDA;
+    if (!tc::encode_bf16(&b, 2, w.data, w.width, c->vocab, w.ld, 1, 0, 64, kFusedTile)) return MT_ECUDA;
+    const int64_t rt = tiles_of(c->n, kFusedTile), vt = tiles_of(c->vocab, kFusedTile);
+    if (dx != nullptr) {
+      f.max_chunks = l.runs_dx;
+      f.cut = reinterpret_cast<int*>(base + l.cut);
+      f.part = reinterpret_cast<float*>(base + l.dx);
+      f.stride = l.rows;
+      e = launch_fused(false, f, a, b, rt * l.runs_dx, s);
+    }
+    if (dw != nullptr && e == cudaSuccess) {
+      f.max_chunks = std::max(1, l.runs_dw);
+      f.whole = l.whole;
+      f.cut = reinterpret_cast<int*>(base + l.cut) + 2;
+      f.part = reinterpret_cast<float*>(base + l.dw);
+      f.stride = (size_t)(vt - l.whole) * kFusedTile;
+      e = launch_fused(true, f, a, b, l.whole + (vt - l.whole) * l.runs_dw, s);
+      const int64_t first = (int64_t)l.whole * kFusedTile;
+      const long long values = (c->vocab - first) * c->dim;
+      if (values > 0 && e == cudaSuccess) {
+        MT_LAUNCH("k_vocab_dw_sum", s);
+        k_vocab_dw_sum<__nv_bfloat16><<<grid_for(values, 256, 8), 256, 0, s>>>(f.part, f.stride, 0, values, c->dim, f.out + first * c->dim, f.cut);
+        e = cudaGetLastError();
+      }
+    }
+  }
+  for (int64_t v0 = 0; !l.fused && v0 < c->vocab && e == cudaSuccess; v0 += l.piece) {
     const int64_t columns = std::min<int64_t>(l.piece, c->vocab - v0);
     const char* wv = w.data + (size_t)v0 * w.ld * 2;
     LogitParams p = logits_of(*c, l, base);
@@ -601,8 +672,8 @@ int mt_vocab_loss_backward(const mt_vocab_loss* c, const float* dloss, const flo
       if (e == cudaSuccess && l.dw_splits > 1) {
         const long long values = columns * c->dim;
         MT_LAUNCH("k_vocab_dw_sum", s);
-        if (fp32) k_vocab_dw_sum<float><<<grid_for(values, 256, 8), 256, 0, s>>>(q.part, q.stride, q.splits, values, c->dim, static_cast<float*>(q.out));
-        else k_vocab_dw_sum<__nv_bfloat16><<<grid_for(values, 256, 8), 256, 0, s>>>(q.part, q.stride, q.splits, values, c->dim, static_cast<__nv_bfloat16*>(q.out));
+        if (fp32) k_vocab_dw_sum<float><<<grid_for(values, 256, 8), 256, 0, s>>>(q.part, q.stride, q.splits, values, c->dim, static_cast<float*>(q.out), nullptr);
+        else k_vocab_dw_sum<__nv_bfloat16><<<grid_for(values, 256, 8), 256, 0, s>>>(q.part, q.stride, q.splits, values, c->dim, static_cast<__nv_bfloat16*>(q.out), nullptr);
         e = cudaGetLastError();
       }
     }
@@ -610,10 +681,13 @@ int mt_vocab_loss_backward(const mt_vocab_loss* c, const float* dloss, const flo
   if (dx != nullptr && e == cudaSuccess) {
     const float* part = reinterpret_cast<const float*>(base + l.dx);
     const int* pos = reinterpret_cast<const int*>(base + l.pos);
-    const int grid = grid_for(c->n * c->dim, 256, 8);
+    const int* cut = reinterpret_cast<const int*>(base + l.cut);
+    const bool four = c->dim % 4 == 0 && (c->n <= 1 || lddx % 4 == 0) && is_aligned(dx, 4 * el);
+    const int grid = grid_for(c->n * (four ? c->dim / 4 : c->dim), 256, 8);
+    auto go = [&](auto kernel, auto* to) { kernel<<<grid, 256, 0, s>>>(part, l.rows, l.dx_splits, pos, c->n, c->dim, to, lddx, l.fused ? cut : nullptr); };
     MT_LAUNCH("k_vocab_dx_sum", s);
-    if (fp32) k_vocab_dx_sum<float><<<grid, 256, 0, s>>>(part, l.rows, l.dx_splits, pos, c->n, c->dim, static_cast<float*>(dx), lddx);
-    else k_vocab_dx_sum<__nv_bfloat16><<<grid, 256, 0, s>>>(part, l.rows, l.dx_splits, pos, c->n, c->dim, static_cast<__nv_bfloat16*>(dx), lddx);
+    if (fp32) four ? go(k_vocab_dx_sum<float, true>, static_cast<float*>(dx)) : go(k_vocab_dx_sum<float, false>, static_cast<float*>(dx));
+    else four ? go(k_vocab_dx_sum<__nv_bfloat16, true>, static_cast<__nv_bfloat16*>(dx)) : go(k_vocab_dx_sum<__nv_bfloat16, false>, static_cast<__nv_bfloat16*>(dx));
     e = cudaGetLastError();
   }
   return e == cudaSuccess ? MT_OK : MT_ECUDA;

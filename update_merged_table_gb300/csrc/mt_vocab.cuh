@@ -66,4 +66,22 @@ cudaError_t launch_rows_sum(const SumParams& p, bool fp32, const CUtensorMap& a,
 cudaError_t launch_vocab_sum(const SumParams& p, bool fp32, const CUtensorMap& a, const CUtensorMap& b, long long row_tiles, bool pair,
                              cudaStream_t s);
 
+// The gradients for narrow rows, without a dz in memory (mt_vocab_fused.cu): bf16, up to 128 columns.
+struct FusedParams {
+  int32_t* status;
+  LiveRows rows;
+  int vocab, columns;
+  int max_chunks;      // runs of the streamed tiles that there is room for
+  int whole;           // dW: kept tiles that go over all streamed tiles, and to `out`
+  int* cut;            // [2] the rows of such tiles, and the runs that the others are cut into
+  float scale2;
+  const float4* coef;
+  float* part;         // [max_chunks][stride][columns]: dx of all rows (of a whole tile in the first run), dW of those behind the whole tiles
+  size_t stride;
+  bool wide;
+  __nv_bfloat16* out;  // dW
+};
+constexpr int kFusedColumns = 128, kFusedTile = 128;
+cudaError_t launch_fused(bool vocab, const FusedParams& p, const CUtensorMap& x, const CUtensorMap& w, long long units, cudaStream_t s);
+
 }  // namespace mt

@@ -1,0 +1,354 @@
+// The gradients of the losses over a vocabulary for narrow rows (up to 128 columns
+// of bf16): the gradient of the logits never leaves the chip.
+//
+// With few columns a logit is a few products and one exponential, and writing its
+// gradient out (2 bytes) and reading it back twice costs more than making it
+// again.  So there are two passes over the tiles of 128 rows by 128 entries, each
+// with its own sum:
+//
+//   dx  a block keeps 128 rows of x and goes over entries of W
+//   dW  a block keeps 128 entries of W and goes over rows of x
+//
+//   S = x W^T into tensor memory; dz from S by eight warps, rounded to bf16, into
+//   shared memory (64 entries of a row are one 128-byte swizzled row); then
+//   dx += dz W or dW += dz^T x with the same tile of dz, read along its rows or
+//   across them, and the same tile of W or x that made S, read across.
+//
+// The products of the next tile are issued before those that wait for this tile's
+// dz, so the tensor core works while the warps do.
+#include "mt_tiles.cuh"
+#include "mt_vocab.cuh"
+#include "mt_vocab_rows.cuh"
+
+namespace mt {
+namespace {
+
+constexpr int kT = 128;                  // rows and entries of a tile
+constexpr int kSlab = kT * 128;          // 128 rows of 64 columns
+constexpr int kDz = 2 * kSlab;           // a tile of dz
+constexpr int kAccAt = 2 * kT;           // tensor memory: two S, then the sum
+
+struct FusedBarriers {
+  uint64_t full[8], empty[8];        // a streamed tile has landed; its products are done
+  uint64_t s_full[2], s_empty[2];    // S is finished; it has been read
+  uint64_t dz_full[2], dz_empty[2];  // dz is in shared memory; its products are done
+  uint64_t kept_full, kept_empty;    // the kept tile has landed; its products are done
+  uint64_t acc_full, acc_empty;      // a unit's sum is finished; it has been read
+  uint64_t done;
+  uint32_t tmem;
+};
+
+template <int KS>
+struct FusedRing {  // KS: slabs of 64 columns
+  static constexpr int kTile = KS * kSlab;
+  static constexpr int kStages = KS == 1 ? 4 : 3;
+  static constexpr int kBytes = (1 + kStages) * kTile + 2 * kDz + tiles::kEpiWarps * tiles::kStageOut;
+};
+
+// A unit: a kept tile and streamed tiles [t0, t1).
+struct FusedUnit {
+  int kept, t0, t1, slot;
+};
+// The kept tiles that make whole rounds of the blocks go over all streamed tiles; the rest are cut into `chunks` runs, so
+// that the last round is a full one too (766 kept tiles on 152 blocks: five rounds and a 25th, not six).
+struct FusedWork {
+  int live, kept_tiles, streamed, whole, chunks;
+  __device__ __forceinline__ int units() const { return whole + (kept_tiles - whole) * chunks; }
+  __device__ __forceinline__ FusedUnit unit(int u) const {  // kept tiles fastest: blocks at work together read the same streamed tiles
+    if (u < whole) return {u, 0, streamed, 0};
+    const int rest = kept_tiles - whole, c = (u - whole) / rest;
+    return {whole + (u - whole) - c * rest, (int)((long long)c * streamed / chunks), (int)((long long)(c + 1) * streamed / chunks), c};
+  }
+};
+
+template <int KS, bool VOCAB>
+__global__ void __launch_bounds__(tiles::kThreadsT, 1)
+k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ FusedParams p) {
+  using R = FusedRing<KS>;
+  extern __shared__ uint8_t s_raw[];
+  __shared__ FusedBarriers bar;
+  uint8_t* base = reinterpret_cast<uint8_t*>(((uintptr_t)s_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* s_kept = base;
+  uint8_t* s_ring = base + R::kTile;
+  uint8_t* s_dz = s_ring + R::kStages * R::kTile;
+  uint8_t* s_out = s_dz + 2 * kDz;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  FusedWork work;
+  work.live = *p.rows.count;
+  {
+    const int rt = (work.live + kT - 1) / kT, vt = (p.vocab + kT - 1) / kT;
+    work.kept_tiles = VOCAB ? vt : rt;
+    work.streamed = VOCAB ? rt : vt;
+    work.whole = VOCAB ? p.whole : work.kept_tiles / (int)gridDim.x * (int)gridDim.x;
+    work.chunks = choose_chunks(work.kept_tiles - work.whole, work.streamed, p.max_chunks, gridDim.x, 4);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      p.cut[0] = work.whole * kT;
+      p.cut[1] = work.chunks;
+    }
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < R::kStages; ++i) {
+      tc::mbar_init(&bar.full[i], 1);
+      tc::mbar_init(&bar.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&bar.s_full[i], 1);
+      tc::mbar_init(&bar.s_empty[i], tiles::kEpiWarps);
+      tc::mbar_init(&bar.dz_full[i], tiles::kEpiWarps);
+      tc::mbar_init(&bar.dz_empty[i], 1);
+    }
+    tc::mbar_init(&bar.kept_full, 1);
+    tc::mbar_init(&bar.kept_empty, 1);
+    tc::mbar_init(&bar.acc_full, 1);
+    tc::mbar_init(&bar.acc_empty, tiles::kEpiWarps);
+    tc::mbar_init(&bar.done, 1);
+    tc::mbar_init_fence();
+  }
+  __syncwarp();
+  if (warp == 1) tc::tmem_alloc<1>(&bar.tmem, 512);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = bar.tmem;
+  const int units = work.units();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tc::Slot s;
+      long long issued = 0;
+      uint32_t kept_phase = 0;
+      bool ok = true, any = false;
+      const CUtensorMap* kept_map = VOCAB ? &map_w : &map_x;
+      const CUtensorMap* ring_map = VOCAB ? &map_x : &map_w;
+      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+        const FusedUnit x = work.unit(u);
+        if (x.t0 == x.t1) continue;
+        ok = tc::mbar_wait(&bar.kept_empty, kept_phase ^ 1);
+        if (!ok) break;
+        kept_phase ^= 1;
+        any = true;
+        tc::mbar_expect(&bar.kept_full, R::kTile);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) tc::tma_load_2d(s_kept + k * kSlab, kept_map, &bar.kept_full, k * 64, x.kept * kT);
+        for (int t = x.t0; t < x.t1; ++t) {
+          ok = tc::mbar_wait(&bar.empty[s.stage], s.phase ^ 1);
+          if (!ok) break;
+          uint8_t* st = s_ring + s.stage * R::kTile;
+          tc::mbar_expect(&bar.full[s.stage], R::kTile);
+#pragma unroll
+          for (int k = 0; k < KS; ++k) tc::tma_load_2d(st + k * kSlab, ring_map, &bar.full[s.stage], k * 64, t * kT);
+          ++issued;
+          s.next<R::kStages>();
+        }
+      }
+      ok = ok && tc::all_released<R::kStages>(bar, s, issued);
+      if (!ok) {
+        tc::latch_status(p.status, MT_ECUDA);
+        tc::drain<R::kStages>(bar, s, issued);
+        if (any) tc::mbar_wait(&bar.kept_full, kept_phase ^ 1);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t instr_s = tc::instr_bf16(kT, kT, false, false), instr_sum = tc::instr_bf16(kT, KS * 64, VOCAB, true);
+      tc::Slot s, d;   // the streamed tile of the next S; of the next sum
+      uint32_t n_s = 0, n_sum = 0, kept_phase = 0, acc_phase = 0;  // tiles so far
+      bool ok = true;
+      // S of the next tile
+      auto make_s = [&]() {
+        const int b = n_s & 1;
+        ok = tc::mbar_wait(&bar.s_empty[b], (n_s >> 1 & 1) ^ 1) && tc::mbar_wait(&bar.full[s.stage], s.phase);
+        if (!ok) return;
+        tc::fence_after();
+        const uint32_t kept = tc::smem_addr(s_kept), ring = tc::smem_addr(s_ring + s.stage * R::kTile);
+        const uint32_t ax = VOCAB ? ring : kept, aw = VOCAB ? kept : ring;
+#pragma unroll
+        for (int i = 0; i < KS * 4; ++i)
+          tc::mma_bf16<1>(tmem + b * kT, tc::smem_desc(ax + (i >> 2) * kSlab + (i & 3) * 32, 16),
+                          tc::smem_desc(aw + (i >> 2) * kSlab + (i & 3) * 32, 16), instr_s, i > 0);
+        tc::mma_commit<1>(&bar.s_full[b]);
+        ++n_s;
+        s.next<R::kStages>();
+      };
+      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+        const FusedUnit x = work.unit(u);
+        if (x.t0 == x.t1) continue;
+        ok = tc::mbar_wait(&bar.kept_full, kept_phase);
+        kept_phase ^= 1;
+        if (!ok) break;
+        make_s();
+        for (int t = x.t0; t < x.t1 && ok; ++t) {
+          if (t + 1 < x.t1) make_s();
+          if (!ok) break;
+          const int b = n_sum & 1;
+          if (t == x.t0) ok = tc::mbar_wait(&bar.acc_empty, acc_phase ^ 1);
+          ok = ok && tc::mbar_wait(&bar.dz_full[b], n_sum >> 1 & 1);
+          if (!ok) break;
+          tc::fence_after();
+          const uint32_t dz = tc::smem_addr(s_dz + b * kDz), ring = tc::smem_addr(s_ring + d.stage * R::kTile);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint64_t a = VOCAB ? tc::smem_desc(dz + i * 2048, kSlab) : tc::smem_desc(dz + (i >> 2) * kSlab + (i & 3) * 32, 16);
+            tc::mma_bf16<1>(tmem + kAccAt, a, tc::smem_desc(ring + i * 2048, kSlab), instr_sum, t > x.t0 || i > 0);
+          }
+          tc::mma_commit<1>(&bar.empty[d.stage]);
+          tc::mma_commit<1>(&bar.dz_empty[b]);
+          ++n_sum;
+          d.next<R::kStages>();
+        }
+        if (!ok) break;
+        tc::mma_commit<1>(&bar.kept_empty);
+        tc::mma_commit<1>(&bar.acc_full);
+        acc_phase ^= 1;
+      }
+      tc::mma_commit<1>(&bar.done);  // tensor memory is freed only when no product writes it, also after a wait ran out
+      ok = tc::mbar_wait(&bar.done, 0) && ok;
+      if (!ok) tc::latch_status(p.status, MT_ECUDA);
+    }
+  } else if (warp >= 4) {
+    const int quad = warp & 3, half = (warp - 4) >> 2;
+    uint8_t* stage = s_out + (warp - 4) * tiles::kStageOut;
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    const f32x2 s2 = both(p.scale2);
+    uint32_t n = 0, acc_phase = 0;
+    bool ok = true;
+    RowTargets to;
+    float4 k = make_float4(0.0f, 0.0f, 0.0f, 0.0f), k_next = k;
+    int id_next = 0x7FFFFFFF;  // a row's only target
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const FusedUnit x = work.unit(u);
+      if (x.t0 < x.t1) {
+        auto row_at = [&](int tile) { return tile * kT + quad * 32 + lane; };
+        auto id_at = [&](int row) { return p.rows.top == 1 && row < work.live ? __ldg(p.rows.ids + row) : 0x7FFFFFFF; };
+        auto coef_at = [&](int row) { return row < work.live ? __ldg(p.coef + row) : make_float4(0.0f, 0.0f, 0.0f, 0.0f); };
+        if (VOCAB) {
+          k_next = coef_at(row_at(x.t0));
+          id_next = id_at(row_at(x.t0));
+        } else {
+          k = coef_at(row_at(x.kept));
+          to.start(p.rows, row_at(x.kept), work.live, x.t0 * kT);
+        }
+        for (int t = x.t0; t < x.t1; ++t, ++n) {
+          const int b = n & 1, parity = n >> 1 & 1;
+          const int row = row_at(VOCAB ? t : x.kept), v0 = (VOCAB ? x.kept : t) * kT + half * 64;
+          if (VOCAB) {
+            k = k_next;
+            if (p.rows.top == 1) {
+              to.row = row;
+              to.pos = 0;
+              to.next = id_next >= x.kept * kT ? id_next : 0x7FFFFFFF;
+            } else {
+              to.start(p.rows, row, work.live, x.kept * kT);
+            }
+            if (t + 1 < x.t1) {
+              k_next = coef_at(row_at(t + 1));
+              id_next = id_at(row_at(t + 1));
+            }
+          }
+          ok = __all_sync(kFull, tc::mbar_wait(&bar.s_full[b], parity) && tc::mbar_wait(&bar.dz_empty[b], parity ^ 1));
+          if (!ok) break;
+          tc::fence_after();
+          uint32_t v[2][32];
+          tc::tmem_load32(tmem + b * kT + half * 64 + lanes, v[0]);
+          tc::tmem_load32(tmem + b * kT + half * 64 + 32 + lanes, v[1]);
+          tc::tmem_load_wait(v[0]);
+          tc::tmem_loaded(v[1]);
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&bar.s_empty[b]);
+          // dz of 64 entries of the thread's row: eight 16-byte pieces of a swizzled 128-byte row
+          uint8_t* dz = s_dz + b * kDz + half * kSlab + (quad * 32 + lane) * 128;
+          const f32x2 x2 = both(-k.x), y2 = both(k.y), z2 = both(-k.z);
+          const int left = p.vocab - v0;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float f[32];
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const float2 e = upk(fma2(pk(__uint_as_float(v[c][j]), __uint_as_float(v[c][j + 1])), s2, x2));
+              const float2 g = upk(fma2(pk(exp2_of(e.x), exp2_of(e.y)), y2, z2));
+              f[j] = g.x;
+              f[j + 1] = g.y;
+            }
+            to.take(p.rows, v0 + c * 32, k.w, f);
+            const uint32_t there = row < work.live ? below(left - c * 32) : 0u;
+            if (there != kFull) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!(there >> j & 1)) f[j] = 0.0f;
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<uint4*>(dz + (((c * 4 + q) ^ (lane & 7)) << 4)) =
+                  make_uint4(bf16x2_of(f[q * 8], f[q * 8 + 1]), bf16x2_of(f[q * 8 + 2], f[q * 8 + 3]), bf16x2_of(f[q * 8 + 4], f[q * 8 + 5]),
+                             bf16x2_of(f[q * 8 + 6], f[q * 8 + 7]));
+          }
+          tc::fence_async_proxy();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&bar.dz_full[b]);
+        }
+        if (!ok) break;
+        ok = __all_sync(kFull, tc::mbar_wait(&bar.acc_full, acc_phase));
+        if (!ok) break;
+        acc_phase ^= 1;
+        tc::fence_after();
+      }
+      // the unit's sum: 32 columns at a time
+      const int c0 = half * KS * 32;
+      const int rows = min(32, (VOCAB ? p.vocab : work.live) - (x.kept * kT + quad * 32));
+      const long long r0 = x.kept * kT + quad * 32;
+#pragma unroll
+      for (int c = 0; c < KS; ++c) {
+        uint32_t v[32];
+        if (x.t0 < x.t1) {
+          tc::tmem_load32(tmem + kAccAt + c0 + c * 32 + lanes, v);
+          tc::tmem_load_wait(v);
+          if (c + 1 == KS) {
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bar.acc_empty);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0u;
+        }
+        float f[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
+        if (VOCAB && x.kept < work.whole)
+          tiles::store32<__nv_bfloat16>(stage, lane, f, p.out, p.columns, r0, rows, c0 + c * 32, p.columns, p.wide);
+        else
+          tiles::store32<float>(stage, lane, f, p.part + (size_t)x.slot * p.stride * p.columns, p.columns, VOCAB ? r0 - work.whole * kT : r0,
+                                rows, c0 + c * 32, p.columns, p.columns % 4 == 0);
+      }
+    }
+    if (!ok) tc::latch_status(p.status, MT_ECUDA);
+  }
+  __syncwarp();
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 1) tc::tmem_free<1>(tmem, 512);
+}
+
+template <int KS, bool VOCAB>
+cudaError_t launch(const char* name, const CUtensorMap& x, const CUtensorMap& w, const FusedParams& p, long long units, cudaStream_t s) {
+  constexpr size_t bytes = 1024 + FusedRing<KS>::kBytes;
+  static SmemLimit limit;
+  const cudaError_t e = limit.allow(k_vocab_fused<KS, VOCAB>, bytes);
+  if (e != cudaSuccess) return e;
+  const int blocks = sm_count();
+  MT_LAUNCH(name, s);
+  k_vocab_fused<KS, VOCAB><<<(int)(units < blocks ? (units > 0 ? units : 1) : blocks), tiles::kThreadsT, bytes, s>>>(x, w, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_fused(bool vocab, const FusedParams& p, const CUtensorMap& x, const CUtensorMap& w, long long units, cudaStream_t s) {
+  const char* name = vocab ? "k_vocab_fused_dw" : "k_vocab_fused_dx";
+  if (p.columns <= 64) return vocab ? launch<1, true>(name, x, w, p, units, s) : launch<1, false>(name, x, w, p, units, s);
+  return vocab ? launch<2, true>(name, x, w, p, units, s) : launch<2, false>(name, x, w, p, units, s);
+}
+
+}  // namespace mt

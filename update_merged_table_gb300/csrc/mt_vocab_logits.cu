@@ -12,6 +12,7 @@
 //                   of the vocabulary at a time.
 #include "mt_tiles.cuh"
 #include "mt_vocab.cuh"
+#include "mt_vocab_rows.cuh"
 
 namespace mt {
 namespace {
@@ -19,29 +20,11 @@ namespace {
 using tiles::Acc;
 using tiles::Unit;
 
-__device__ __forceinline__ float exp2_of(float x) {
+__device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-
-// Runs of column tiles for `rt` row tiles on `blocks` blocks (pairs): as many as end the last block soonest, a run's start
-// counted as half a tile.  Every thread calls it.
-__device__ __forceinline__ int choose_chunks(int rt, int tiles, int most, int blocks) {
-  __shared__ unsigned long long s_best;
-  if (threadIdx.x == 0) s_best = ~0ull;
-  __syncthreads();
-  unsigned long long best = ~0ull;
-  for (int c = threadIdx.x + 1; c <= min(most, tiles); c += blockDim.x) {
-    const long long rounds = ((long long)rt * c + blocks - 1) / blocks;
-    const unsigned long long cost = (unsigned long long)rounds * (2 * ((tiles + c - 1) / c) + 1);
-    best = min(best, cost << 32 | (unsigned)c);
-  }
-  if (best != ~0ull) atomicMin(&s_best, best);
-  __syncthreads();
-  return (int)(uint32_t)s_best;
-}
-
 // What both kernels share: rows tiles fastest, so that blocks at work at the same time read the same entries of W.
 template <int CG>
 struct Logits {
@@ -51,12 +34,13 @@ struct Logits {
   const Params& p;
   int rank, live, rt, chunks;
   uint8_t* stage;
-  int half, lane, row, pos, next;  // the thread's row; its next target
+  int quad, half, lane, row;  // the thread's row
+  RowTargets to;
 
   __device__ Logits(const Params& params, uint8_t*, int r) : p(params), rank(r) {
     live = *p.rows.count;
     rt = (live + tiles::kBM * CG - 1) / (tiles::kBM * CG);
-    chunks = choose_chunks(rt, p.tiles, p.max_chunks, gridDim.x / CG);
+    chunks = choose_chunks(rt, p.tiles, p.max_chunks, gridDim.x / CG, 1);
   }
   __device__ long long units() const { return (long long)rt * chunks; }
   __device__ Unit unit(long long u) const {
@@ -72,7 +56,6 @@ struct Logits {
     x.slot = c;
     return x;
   }
-  int quad;
   __device__ void warp(uint8_t* s, int q, int h, int l) {
     stage = s;
     quad = q;
@@ -81,23 +64,7 @@ struct Logits {
   }
   __device__ void start(const Unit& x) {
     row = x.row0 + rank * tiles::kBM + quad * 32 + lane;
-    pos = 0;
-    next = 0x7FFFFFFF;
-    if (row >= live) return;
-    const int first = p.v0 + x.ct0 * kBN;
-    const int* ids = p.rows.ids + (size_t)row * p.rows.top;
-    int lo = 0, hi = p.rows.top;  // targets before `lo` are below `first`, those from `hi` on are not
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (ids[mid] < first) lo = mid + 1;
-      else hi = mid;
-    }
-    pos = lo;
-    if (pos < p.rows.top) next = ids[pos];
-  }
-  __device__ __forceinline__ void advance() {
-    ++pos;
-    next = pos < p.rows.top ? p.rows.ids[(size_t)row * p.rows.top + pos] : 0x7FFFFFFF;
+    to.start(p.rows, row, live, p.v0 + x.ct0 * kBN);
   }
 };
 
@@ -119,56 +86,55 @@ struct Stats : Logits<CG> {
     this->p.part[at] = make_float2(top, sum);
     if constexpr (SMOOTH) this->p.sum_z[at] = total;
   }
+  // 32 columns: their largest, then one exponential each.  The next columns' load is on its way meanwhile.
+  __device__ __forceinline__ void columns(uint32_t (&v)[32], int col, int left) {
+    const LogitParams& p = this->p;
+    this->to.pick(p.rows, col, v, p.picked);
+    if constexpr (SMOOTH) {
+      f32x2 t[2] = {0ull, 0ull};
+#pragma unroll
+      for (int j = 0; j < 32; j += 2)  // (columns that are not there are zero)
+        t[j >> 1 & 1] = add2(t[j >> 1 & 1], pk(__uint_as_float(v[j]), __uint_as_float(v[j + 1])));
+      total += pair_sum(add2(t[0], t[1]));
+    }
+    if (left < 32) {
+      const uint32_t there = below(left);
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (!(there >> j & 1)) v[j] = 0xFF800000u;
+    }
+    float m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = __uint_as_float(v[i * 8]);
+#pragma unroll
+      for (int j = 1; j < 7; j += 2) m[i] = max3(m[i], __uint_as_float(v[i * 8 + j]), __uint_as_float(v[i * 8 + j + 1]));
+      m[i] = fmaxf(m[i], __uint_as_float(v[i * 8 + 7]));
+    }
+    const float now = max3(top, fmaxf(m[0], m[1]) * p.scale2, fmaxf(m[2], m[3]) * p.scale2);
+    const float off = now == -INFINITY ? 0.0f : now;
+    const f32x2 s2 = both(p.scale2), o2 = both(-off);
+    f32x2 s[2] = {0ull, 0ull};
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      const float2 e = upk(fma2(pk(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), s2, o2));
+      s[j >> 1 & 1] = add2(s[j >> 1 & 1], pk(exp2_of(e.x), exp2_of(e.y)));
+    }
+    sum = fmaf(sum, exp2_of(top - off), pair_sum(add2(s[0], s[1])));
+    top = now;
+  }
   template <int G>
   __device__ __forceinline__ void tile(const Unit&, int ct, const Acc& acc, bool, bool) {
     const LogitParams& p = this->p;
-    const int left = p.columns - ct * 256 - this->half * 128;  // columns of this half that there are
-#pragma unroll 1
-    for (int c = 0; c < 128; c += 32) {
-      uint32_t v[32];
-      acc.load(this->half * 128 + c, v);
-      tc::tmem_load_wait(v);
-      if (c == 96) acc.release<G>(this->lane);
-      const int col = p.v0 + ct * 256 + this->half * 128 + c;
-      while (__any_sync(kFull, this->next < col + 32)) {
-        if (this->next < col + 32) {
-          if (this->next >= col) {
-            const int at = this->next - col;
-            uint32_t z = v[0];
+    const int from = this->half * 128, at = ct * 256 + from, left = p.columns - at;
+    uint32_t v[2][32];
+    acc.load(from, v[0]);
 #pragma unroll
-            for (int j = 1; j < 32; ++j) z = at == j ? v[j] : z;
-            p.picked[(size_t)this->row * p.rows.top + this->pos] = __uint_as_float(z);
-          }
-          this->advance();
-        }
-      }
-      if (left < c + 32) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (c + j >= left) v[j] = 0xFF800000u;
-      }
-      float m = __uint_as_float(v[0]);
-#pragma unroll
-      for (int j = 1; j < 32; ++j) m = fmaxf(m, __uint_as_float(v[j]));
-      const float now = fmaxf(top, m * p.scale2);
-      const float off = now == -INFINITY ? 0.0f : now;
-      const f32x2 s2 = both(p.scale2), o2 = both(-off);
-      float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        const float2 e = upk(fma2(pk(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), s2, o2));
-        s[j & 2] += exp2_of(e.x);
-        s[(j & 2) + 1] += exp2_of(e.y);
-      }
-      sum = fmaf(sum, exp2_of(top - off), (s[0] + s[1]) + (s[2] + s[3]));
-      top = now;
-      if constexpr (SMOOTH) {
-        float t = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (c + j < left) t += __uint_as_float(v[j]);
-        total += t;
-      }
+    for (int c = 0; c < 4; ++c) {
+      tc::tmem_load_wait(v[c & 1]);
+      if (c < 3) acc.load(from + (c + 1) * 32, v[(c + 1) & 1]);
+      else acc.release<G>(this->lane);
+      columns(v[c & 1], p.v0 + at + c * 32, left - c * 32);
     }
   }
 };
@@ -183,54 +149,55 @@ struct Grad : Logits<CG> {
     k = this->row < this->live ? this->p.coef[this->row] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   }
   __device__ void end(const Unit&) {}
+  __device__ __forceinline__ void columns(uint32_t (&v)[32], int at0, int left, long long r0) {
+    const LogitParams& p = this->p;
+    const int col = p.v0 + at0;
+    float f[32];
+    const f32x2 s2 = both(p.scale2), x2 = both(-k.x), y2 = both(k.y), z2 = both(-k.z);
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      const float2 e = upk(fma2(pk(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), s2, x2));
+      const float2 d = upk(fma2(pk(exp2_of(e.x), exp2_of(e.y)), y2, z2));
+      f[j] = d.x;
+      f[j + 1] = d.y;
+    }
+    this->to.take(p.rows, col, k.w, f);
+    // zeros behind the piece's last column, and in a row behind the last, whatever it holds
+    const uint32_t there = this->row < this->live ? below(left) : 0u;
+    if (there != kFull) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (!(there >> j & 1)) f[j] = 0.0f;
+    }
+    if constexpr (PARTS == 1) {
+      tiles::store32<__nv_bfloat16>(this->stage, this->lane, f, p.dz, p.width, r0, 32, at0, p.width, true);
+    } else {
+      uint32_t w[3][16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        __nv_bfloat16 a[3], b[3];
+        split3(f[2 * j], a[0], a[1], a[2]);
+        split3(f[2 * j + 1], b[0], b[1], b[2]);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) w[q][j] = bf16_bits(a[q], b[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+        tiles::store_rows<__nv_bfloat16>(this->stage, this->lane, w[q], p.dz + (size_t)q * p.width, (size_t)3 * p.width, r0, 32, at0, p.width, true);
+    }
+  }
   template <int G>
   __device__ __forceinline__ void tile(const Unit& x, int ct, const Acc& acc, bool, bool) {
-    const LogitParams& p = this->p;
-    const int left = p.columns - ct * 256 - this->half * 128;
-    const bool dead = this->row >= this->live;  // a row behind the last: whatever it holds, zeros
-#pragma unroll 1
-    for (int c = 0; c < 128; c += 32) {
-      uint32_t v[32];
-      acc.load(this->half * 128 + c, v);
-      tc::tmem_load_wait(v);
-      if (c == 96) acc.release<G>(this->lane);
-      const int at0 = ct * 256 + this->half * 128 + c, col = p.v0 + at0;
-      float f[32];
+    const int from = this->half * 128, at = ct * 256 + from, left = this->p.columns - at;
+    const long long r0 = x.row0 + this->rank * tiles::kBM + this->quad * 32;
+    uint32_t v[2][32];
+    acc.load(from, v[0]);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) f[j] = fmaf(exp2_of(fmaf(__uint_as_float(v[j]), p.scale2, -k.x)), k.y, -k.z);
-      while (__any_sync(kFull, this->next < col + 32)) {
-        if (this->next < col + 32) {
-          if (this->next >= col) {
-            const int at = this->next - col;
-            const float take = k.w * p.rows.share[(size_t)this->row * p.rows.top + this->pos];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) f[j] -= at == j ? take : 0.0f;
-          }
-          this->advance();
-        }
-      }
-      if (dead || left < c + 32) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (dead || c + j >= left) f[j] = 0.0f;
-      }
-      const long long r0 = x.row0 + this->rank * tiles::kBM + this->quad * 32;
-      if constexpr (PARTS == 1) {
-        tiles::store32<__nv_bfloat16>(this->stage, this->lane, f, p.dz, p.width, r0, 32, at0, p.width, true);
-      } else {
-        uint32_t w[3][16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          __nv_bfloat16 a[3], b[3];
-          split3(f[2 * j], a[0], a[1], a[2]);
-          split3(f[2 * j + 1], b[0], b[1], b[2]);
-#pragma unroll
-          for (int q = 0; q < 3; ++q) w[q][j] = bf16_bits(a[q], b[q]);
-        }
-#pragma unroll
-        for (int q = 0; q < 3; ++q)
-          tiles::store_rows<__nv_bfloat16>(this->stage, this->lane, w[q], p.dz + (size_t)q * p.width, (size_t)3 * p.width, r0, 32, at0, p.width, true);
-      }
+    for (int c = 0; c < 4; ++c) {
+      tc::tmem_load_wait(v[c & 1]);
+      if (c < 3) acc.load(from + (c + 1) * 32, v[(c + 1) & 1]);
+      else acc.release<G>(this->lane);
+      columns(v[c & 1], at + c * 32, left - c * 32, r0);
     }
   }
 };
