@@ -81,11 +81,11 @@ template <typename T, bool BACKWARD>
 struct Gated {
   using Params = GatedParams;
   static constexpr int kBN = 256;
-  static constexpr bool kAMN = false, kBMN = false, kTwoB = true;
+  static constexpr bool kAMN = false, kBMN = false, kTwoB = true, kTeams = true, kKeep = false;
   const Params& p;
   const long long* off;
   const int* cum;
-  int rank, rows_per_tile, quad, half, lane;
+  int rank, rows_per_tile, quad, lane;
   uint8_t* stage;
 
   __device__ Gated(const Params& params, uint8_t* mem, int r) : p(params), rank(r) {
@@ -119,7 +119,6 @@ struct Gated {
   __device__ void warp(uint8_t* s, int q, int h, int l) {
     stage = s;
     quad = q;
-    half = h;
     lane = l;
     const int J = BACKWARD ? 2 * p.u_col : p.out_dim;
     zero_outside<T>(off, p.groups, p.n, static_cast<T*>(p.out), p.ldo, J, tiles::kEpiWarps * 32, (h * 4 + q) * 32 + l);
@@ -132,19 +131,19 @@ struct Gated {
     const long long r0 = x.row0 + rank * tiles::kBM + quad * 32;
     const int rows = min(32, x.end - (int)r0);  // <= 0: none of this warp's rows is in the group
     T* out = static_cast<T*>(p.out);
-#pragma unroll
-    for (int c = 0; c < 64; c += 32) {
-      const int col = ct * 128 + half * 64 + c;
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+      const int col = ct * 128 + c;
       uint32_t y[32], u[32];
-      acc.load(half * 64 + c, y);
-      acc.load(128 + half * 64 + c, u);
+      acc.load(c, y);
+      acc.load(128 + c, u);
       float d[BACKWARD ? 32 : 1];
       if constexpr (BACKWARD) {
         if (col < p.out_dim) tiles::load_rows<T>(stage, lane, d, static_cast<const T*>(p.dh), p.lddh, r0, rows, col, p.out_dim, p.wide_dh);
       }
       tc::tmem_load_wait(y);
       tc::tmem_loaded(u);
-      if (c == 32) acc.release<CG>(lane);
+      if (c == 96) acc.release<CG>(lane);
       float f[32];
       if constexpr (!BACKWARD) {
 #pragma unroll

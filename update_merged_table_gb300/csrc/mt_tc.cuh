@@ -83,6 +83,24 @@ __device__ __forceinline__ bool mbar_wait_while(uint64_t* bar, uint32_t parity, 
   }
 }
 
+// A whole warp waits; true for every lane or for none.
+template <bool OF_PAIR = false>
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait<OF_PAIR>(bar, parity));
+}
+// True for one lane of a warp, always the same one.  A warp that copies or multiplies stays together and lets one lane issue:
+// what the instructions take (descriptors, coordinates, barriers) is then the same in every lane and is worked out once per
+// warp; under `lane == 0` each of them took a single thread's chain of dependent instructions.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(is));
+  return is != 0;
+}
+
 // ---- pairs of blocks (clusters of two) ---------------------------------------------------
 
 // Where the first block of the pair has what this block has at p.
@@ -210,6 +228,10 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
          (1ull << 46) | (2ull << 61);
 }
 
+// The low word of such a descriptor, to which a step of 16 of the contraction adds a constant; the high word is kDescHigh.
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lead) { return ((addr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16); }
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+
 // D (tensor memory) = A * B, or D + A * B; one thread issues it.  For a pair (the first block's thread) each block holds
 // half of A's rows, half of B's rows and its half of D's rows, at the same addresses.
 template <int CG>
@@ -227,6 +249,29 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
         "setp.ne.u32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(instr), "r"(add ? 1u : 0u)
+        : "memory");
+  }
+}
+// The same from the descriptors' low words.
+template <int CG>
+__device__ __forceinline__ void mma_low(uint32_t d, uint32_t a, uint32_t b, uint32_t instr, bool add) {
+  if constexpr (CG == 1) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "mov.b64 x, {%1, %5};\n\t"
+        "mov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(instr), "r"(add ? 1u : 0u), "n"(kDescHigh)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "mov.b64 x, {%1, %5};\n\t"
+        "mov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(instr), "r"(add ? 1u : 0u), "n"(kDescHigh)
         : "memory");
   }
 }
@@ -254,10 +299,20 @@ struct Slot {
   uint32_t phase = 0;
   template <int STAGES>
   __device__ __forceinline__ void next() {
-    if (++stage == STAGES) {
+    next(STAGES);
+  }
+  __device__ __forceinline__ void next(int stages) {
+    if (++stage == stages) {
       stage = 0;
       phase ^= 1;
     }
+  }
+  __device__ __forceinline__ void back(int stages) {
+    if (stage == 0) {
+      stage = stages;
+      phase ^= 1;
+    }
+    --stage;
   }
 };
 
@@ -269,33 +324,33 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
 }
 
 // The last stages' products are done, and what a pair's first block signals of them has arrived here.
-template <int STAGES, typename Barriers>
-__device__ __forceinline__ bool all_released(Barriers& b, Slot s, long long issued) {
-  const long long k = issued < STAGES ? issued : STAGES;
+template <typename Barriers>
+__device__ __forceinline__ bool all_released(Barriers& b, Slot s, long long issued, int stages) {
+  const long long k = issued < stages ? issued : stages;
   for (long long i = 0; i < k; ++i) {
-    if (s.stage == 0) {
-      s.stage = STAGES;
-      s.phase ^= 1;
-    }
-    --s.stage;
+    s.back(stages);
     if (!mbar_wait(&b.empty[s.stage], s.phase)) return false;
   }
   return true;
 }
+template <int STAGES, typename Barriers>
+__device__ __forceinline__ bool all_released(Barriers& b, Slot s, long long issued) {
+  return all_released(b, s, issued, STAGES);
+}
 
 // After a wait ran out: the copies already issued are waited for (again with a limit) so that none lands in a block
 // that has ended.
-template <int STAGES, typename Barriers>
-__device__ __forceinline__ void drain(Barriers& b, Slot s, long long issued) {
-  const long long k = issued < STAGES ? issued : STAGES;
+template <typename Barriers>
+__device__ __forceinline__ void drain(Barriers& b, Slot s, long long issued, int stages) {
+  const long long k = issued < stages ? issued : stages;
   for (long long i = 0; i < k; ++i) {
-    if (s.stage == 0) {
-      s.stage = STAGES;
-      s.phase ^= 1;
-    }
-    --s.stage;
+    s.back(stages);
     if (!mbar_wait(&b.full[s.stage], s.phase)) return;
   }
+}
+template <int STAGES, typename Barriers>
+__device__ __forceinline__ void drain(Barriers& b, Slot s, long long issued) {
+  drain(b, s, issued, STAGES);
 }
 
 __device__ __forceinline__ void latch_status(int32_t* status, int code) {

@@ -5,9 +5,11 @@
 // C(i, j) = sum over k of A(i, k) B(j, k), 128 rows i (256 by a pair of blocks)
 // and BN columns j per tile.  One persistent block per SM walks the units that
 // its operator deals out (a row tile and a run of column tiles); one thread
-// keeps a ring of stages filled by TMA, one issues the products into one of two
-// accumulators in tensor memory, and eight warps, two for each 32 lanes, hand
-// finished tiles to the operator while the next tile's products run.
+// keeps a ring of stages filled by TMA, one issues the products into one of two or
+// four accumulators in tensor memory, and two teams of four warps hand finished tiles
+// to the operator while the next tile's products run: a team takes every other
+// tile, so that one's loads and waits overlap the other's arithmetic (or, where an
+// operator adds tiles up in registers, half of each tile's columns).
 //
 // An operand lies with its contraction contiguous, or with its rows contiguous
 // (A_MN, B_MN).  fp32 operands come as three bf16 parts side by side whose sum
@@ -25,22 +27,31 @@ namespace tiles {
 
 constexpr int kBM = 128;        // tile rows of a block: the lanes of tensor memory
 constexpr int kBK = 64;         // contraction per stage: one 128-byte swizzled row of bf16
-constexpr int kEpiWarps = 8;    // two for each 32 lanes of tensor memory, half of a tile's columns each
+constexpr int kEpiWarps = 8;    // two for each 32 lanes of tensor memory: two teams
 constexpr int kWarps = 4 + kEpiWarps;  // copies, products, two idle, epilogue
 constexpr int kThreadsT = kWarps * 32;
 constexpr int kStageOut = 2048;  // bytes per epilogue warp: 32 rows x 64 bytes
 
-template <int BN, int CG>
+// Shared memory of a block: stages of both operands (of a pair's block: its half of the columns), and where the epilogue
+// turns its rows.  KEEP: A's tile (all of its contraction, up to kKept steps) is copied once per unit and stays, and the
+// stages hold B alone.
+constexpr int kKept = 8;
+template <int BN, int CG, bool KEEP>
 struct Ring {
   static constexpr int kStageA = kBM * kBK * 2, kStageB = BN / CG * kBK * 2;
-  static constexpr int kStage = kStageA + kStageB;
-  static constexpr int kStages = 196608 / kStage;
-  static constexpr int kBytes = kStages * kStage + kEpiWarps * kStageOut;
+  static constexpr int kStage = kStageB + (KEEP ? 0 : kStageA);
+  static constexpr int kTotal = 196608;
+  static constexpr int kBytes = kTotal + kEpiWarps * kStageOut;
+  static __host__ __device__ constexpr int stages(int kept) {
+    const int n = (kTotal - kept * kStageA) / kStage;
+    return n < 8 ? n : 8;
+  }
 };
 
 struct Barriers {
   uint64_t full[8], empty[8];          // a stage's copies have landed; its products are done
-  uint64_t acc_full[2], acc_empty[2];  // an accumulator is finished; it has been read out
+  uint64_t acc_full[4], acc_empty[4];  // an accumulator is finished; it has been read out
+  uint64_t a_full, a_empty;            // a unit's kept A has landed; its products are done
   uint64_t done;                       // every product issued is done
   uint32_t tmem;
 };
@@ -83,8 +94,17 @@ struct Acc {
   }
 };
 
+// Steps of A (of all parts) that stay.
+template <class Op>
+__device__ __forceinline__ int kept_of(const typename Op::Params& p) {
+  if constexpr (Op::kKeep) return p.kept;
+  else return 0;
+}
+
 // Op: what is computed.
 //   kBN, kAMN, kBMN            tile columns; operands whose rows are contiguous
+//   kTeams                     a team of epilogue warps takes every other tile (else half of the columns of each)
+//   kKeep                      A's tile stays for the unit: parts x steps <= kKept
 //   kTwoB                      (where B's contraction is contiguous) half of the columns b_second rows of B after the others
 //   Params                     passes, a_part, b_part (columns between the parts), promote (stages an accumulator sums
 //                              before it is handed over), status
@@ -97,28 +117,34 @@ __global__ void __launch_bounds__(kThreadsT, 1)
 k_tiles(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
         const __grid_constant__ typename Op::Params p) {
   constexpr int BN = Op::kBN;
-  using R = Ring<BN, CG>;
+  using R = Ring<BN, CG, Op::kKeep>;
   constexpr int kCols = BN / CG;  // columns of B that a block copies
+  constexpr int kAccs = BN >= 256 ? 2 : 4;
   extern __shared__ uint8_t s_raw[];
   __shared__ Barriers bar;
   uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)s_raw + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = blockIdx.x % CG;  // in the pair
   Op op(p, ring + R::kBytes, rank);
+  const int kept = kept_of<Op>(p);
+  const int stages = R::stages(kept);
+  uint8_t* stages_at = ring + kept * R::kStageA;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < R::kStages; ++i) {
+    for (int i = 0; i < 8; ++i) {
       tc::mbar_init(&bar.full[i], 1);
       tc::mbar_init(&bar.empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    tc::mbar_init(&bar.a_full, 1);
+    tc::mbar_init(&bar.a_empty, 1);
+    for (int i = 0; i < kAccs; ++i) {
       tc::mbar_init(&bar.acc_full[i], 1);
-      tc::mbar_init(&bar.acc_empty[i], kEpiWarps * CG);
+      tc::mbar_init(&bar.acc_empty[i], (Op::kTeams ? kEpiWarps / 2 : kEpiWarps) * CG);
     }
     tc::mbar_init(&bar.done, 1);
     tc::mbar_init_fence();
   }
   __syncwarp();
-  if (warp == 1) tc::tmem_alloc<CG>(&bar.tmem, 2 * BN);
+  if (warp == 1) tc::tmem_alloc<CG>(&bar.tmem, kAccs * BN);
   tc::fence_before();
   if constexpr (CG == 2) tc::cluster_sync();
   else __syncthreads();
@@ -127,48 +153,68 @@ k_tiles(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
   const long long units = op.units(), u0 = blockIdx.x / CG, ustep = gridDim.x / CG;
 
   if (warp == 0) {
-    if (lane == 0) {
-      tc::Slot s;
-      long long issued = 0;
-      bool ok = true;
-      for (long long u = u0; u < units && ok; u += ustep) {
-        const Unit x = op.unit(u);
-        const int r0 = x.row0 + rank * kBM;
-        for (int ct = x.ct0; ct < x.ct1 && ok; ++ct) {
-          for (int q = 0; q < p.passes && ok; ++q) {
-            const int ap = part_a(p.passes, q) * p.a_part, bp = part_b(p.passes, q) * p.b_part;
-            for (int k = x.k0; k < x.k1; ++k) {
-              ok = tc::mbar_wait(&bar.empty[s.stage], s.phase ^ 1);
-              if (!ok) break;
-              uint8_t* st = ring + s.stage * R::kStage;
-              uint8_t* sb = st + R::kStageA;
-              if constexpr (CG == 2) {  // both blocks' copies count on the first block's barrier
-                const uint32_t full = tc::of_leader(&bar.full[s.stage]);
-                if (rank == 0) tc::mbar_expect(&bar.full[s.stage], 2 * R::kStage);
-                if constexpr (Op::kAMN) {
+    const bool one = tc::elect_one();
+    tc::Slot s;
+    long long issued = 0;
+    uint32_t a_phase = 0;
+    bool ok = true;
+    // one step of A into `to`
+    auto load_a = [&](uint8_t* to, uint64_t* full, int x, int r0, int k) {
+      if constexpr (CG == 2) {
+        const uint32_t at = tc::of_leader(full);
+        if constexpr (Op::kAMN) {
 #pragma unroll
-                  for (int c = 0; c < kBM / 64; ++c) tc::tma_load_2d_pair(st + c * 8192, &map_a, full, ap + r0 + c * 64, k * kBK);
-                } else {
-                  tc::tma_load_2d_pair(st, &map_a, full, ap + k * kBK, r0);
-                }
+          for (int c = 0; c < kBM / 64; ++c) tc::tma_load_2d_pair(to + c * 8192, &map_a, at, x + r0 + c * 64, k * kBK);
+        } else {
+          tc::tma_load_2d_pair(to, &map_a, at, x + k * kBK, r0);
+        }
+      } else {
+        if constexpr (Op::kAMN) {
+#pragma unroll
+          for (int c = 0; c < kBM / 64; ++c) tc::tma_load_2d(to + c * 8192, &map_a, full, x + r0 + c * 64, k * kBK);
+        } else {
+          tc::tma_load_2d(to, &map_a, full, x + k * kBK, r0);
+        }
+      }
+    };
+    for (long long u = u0; u < units && ok; u += ustep) {
+      const Unit x = op.unit(u);
+      const int r0 = x.row0 + rank * kBM;
+      if constexpr (Op::kKeep) {
+        ok = tc::warp_wait(&bar.a_empty, a_phase ^ 1);
+        if (!ok) break;
+        a_phase ^= 1;
+        if (one) {  // a pair's copies count on the first block's barrier
+          if (rank == 0) tc::mbar_expect(&bar.a_full, CG * kept * R::kStageA);
+          const int steps = x.k1 - x.k0;
+          for (int i = 0; i < kept; ++i) load_a(ring + i * R::kStageA, &bar.a_full, i / steps * p.a_part, r0, x.k0 + i % steps);
+        }
+        __syncwarp();
+      }
+      for (int ct = x.ct0; ct < x.ct1 && ok; ++ct) {
+        for (int q = 0; q < p.passes && ok; ++q) {
+          const int ap = part_a(p.passes, q) * p.a_part, bp = part_b(p.passes, q) * p.b_part;
+          for (int k = x.k0; k < x.k1; ++k) {
+            ok = tc::warp_wait(&bar.empty[s.stage], s.phase ^ 1);
+            if (!ok) break;
+            uint8_t* st = stages_at + s.stage * R::kStage;
+            uint8_t* sb = st + (Op::kKeep ? 0 : R::kStageA);
+            if (one) {
+              uint64_t* full = &bar.full[s.stage];
+              if (rank == 0) tc::mbar_expect(full, CG * R::kStage);
+              if constexpr (!Op::kKeep) load_a(st, full, ap, r0, k);
+              if constexpr (CG == 2) {
+                const uint32_t at = tc::of_leader(full);
                 if constexpr (Op::kBMN) {
 #pragma unroll
                   for (int c = 0; c < kCols / 64; ++c)
-                    tc::tma_load_2d_pair(sb + c * 8192, &map_b, full, bp + ct * BN + rank * kCols + c * 64, k * kBK);
+                    tc::tma_load_2d_pair(sb + c * 8192, &map_b, at, bp + ct * BN + rank * kCols + c * 64, k * kBK);
                 } else if constexpr (Op::kTwoB) {  // the first block copies the first weights' columns, the second the second's
-                  tc::tma_load_3d_pair(sb, &map_b, full, bp + k * kBK, ct * kCols + rank * p.b_second, x.g);
+                  tc::tma_load_3d_pair(sb, &map_b, at, bp + k * kBK, ct * kCols + rank * p.b_second, x.g);
                 } else {
-                  tc::tma_load_2d_pair(sb, &map_b, full, bp + k * kBK, ct * BN + rank * kCols);
+                  tc::tma_load_2d_pair(sb, &map_b, at, bp + k * kBK, ct * BN + rank * kCols);
                 }
               } else {
-                uint64_t* full = &bar.full[s.stage];
-                tc::mbar_expect(full, R::kStage);
-                if constexpr (Op::kAMN) {
-#pragma unroll
-                  for (int c = 0; c < kBM / 64; ++c) tc::tma_load_2d(st + c * 8192, &map_a, full, ap + r0 + c * 64, k * kBK);
-                } else {
-                  tc::tma_load_2d(st, &map_a, full, ap + k * kBK, r0);
-                }
                 if constexpr (Op::kBMN) {
 #pragma unroll
                   for (int c = 0; c < kCols / 64; ++c) tc::tma_load_2d(sb + c * 8192, &map_b, full, bp + ct * BN + c * 64, k * kBK);
@@ -179,68 +225,94 @@ k_tiles(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
                   tc::tma_load_2d(sb, &map_b, full, bp + k * kBK, ct * BN);
                 }
               }
-              ++issued;
-              s.next<R::kStages>();
             }
+            __syncwarp();
+            ++issued;
+            s.next(stages);
           }
         }
       }
-      ok = ok && tc::all_released<R::kStages>(bar, s, issued);
-      // what the first block signals of its last products has to have arrived here before this block ends
-      if (rank != 0) ok = tc::mbar_wait(&bar.done, 0) && ok;
-      if (!ok) {
-        tc::latch_status(p.status, MT_ECUDA);
-        if (rank == 0) tc::drain<R::kStages>(bar, s, issued);
+    }
+    ok = ok && tc::all_released(bar, s, issued, stages);
+    // what the first block signals of its last products has to have arrived here before this block ends
+    if (rank != 0) ok = tc::mbar_wait(&bar.done, 0) && ok;
+    if (!ok) {
+      if (one) tc::latch_status(p.status, MT_ECUDA);
+      if (rank == 0) {
+        tc::drain(bar, s, issued, stages);
+        if (Op::kKeep && (issued > 0 || a_phase != 0)) tc::mbar_wait(&bar.a_full, a_phase ^ 1);
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       constexpr uint32_t instr = tc::instr_bf16(kBM * CG, BN, Op::kAMN, Op::kBMN);
+      // descriptors' low words: of the ring's (and the kept A's) first stage, from one stage to the next, from one 16 of the
+      // contraction to the next
+      constexpr uint32_t kLeadA = Op::kAMN ? 8192 : 16, kLeadB = Op::kBMN ? 8192 : 16;
+      constexpr uint32_t kStepA = Op::kAMN ? 2048 >> 4 : 32 >> 4, kStepB = Op::kBMN ? 2048 >> 4 : 32 >> 4;
+      const bool one = tc::elect_one();
+      const uint32_t a0 = tc::desc_low(tc::smem_addr(Op::kKeep ? ring : stages_at), kLeadA);
+      const uint32_t b0 = tc::desc_low(tc::smem_addr(stages_at + (Op::kKeep ? 0 : R::kStageA)), kLeadB);
       tc::Slot s;
       int acc = 0;
-      uint32_t acc_phase = 0;
+      uint32_t acc_phase = 0, a_phase = 0;
       bool ok = true;
       for (long long u = u0; u < units && ok; u += ustep) {
         const Unit x = op.unit(u);
-        const int steps = (x.k1 - x.k0) * p.passes;
+        const int per_pass = x.k1 - x.k0;
+        if constexpr (Op::kKeep) {
+          ok = tc::warp_wait<CG == 2>(&bar.a_full, a_phase);
+          a_phase ^= 1;
+          if (!ok) break;
+        }
         for (int ct = x.ct0; ct < x.ct1 && ok; ++ct) {
           int part = 0;  // stages that the accumulator has
-          for (int k = 0; k < steps; ++k) {
-            if (part == 0) {
-              ok = tc::mbar_wait(&bar.acc_empty[acc], acc_phase ^ 1);
+          for (int q = 0; q < p.passes && ok; ++q) {
+            uint32_t a_at = a0 + part_a(p.passes, q) * per_pass * (R::kStageA >> 4);  // (kept A)
+            for (int k = 0; k < per_pass; ++k) {
+              if (part == 0) {
+                ok = tc::warp_wait(&bar.acc_empty[acc], acc_phase ^ 1);
+                if (!ok) break;
+                tc::fence_after();
+              }
+              ok = tc::warp_wait<CG == 2>(&bar.full[s.stage], s.phase);
               if (!ok) break;
               tc::fence_after();
-            }
-            ok = tc::mbar_wait<CG == 2>(&bar.full[s.stage], s.phase);
-            if (!ok) break;
-            tc::fence_after();
-            const uint32_t a = tc::smem_addr(ring + s.stage * R::kStage), b = a + R::kStageA;
+              const uint32_t b = b0 + s.stage * (R::kStage >> 4), a = Op::kKeep ? a_at : a0 + s.stage * (R::kStage >> 4);
+              const bool closes = part + 1 == p.promote || (k + 1 == per_pass && q + 1 == p.passes);
+              if (one) {
 #pragma unroll
-            for (int i = 0; i < kBK / 16; ++i) {
-              const uint64_t da = Op::kAMN ? tc::smem_desc(a + i * 2048, 8192) : tc::smem_desc(a + i * 32, 16);
-              const uint64_t db = Op::kBMN ? tc::smem_desc(b + i * 2048, 8192) : tc::smem_desc(b + i * 32, 16);
-              tc::mma_bf16<CG>(tmem + acc * BN, da, db, instr, part > 0 || i > 0);
-            }
-            tc::mma_commit<CG>(&bar.empty[s.stage]);
-            s.next<R::kStages>();
-            if (++part == p.promote || k + 1 == steps) {
-              tc::mma_commit<CG>(&bar.acc_full[acc]);
-              acc ^= 1;
-              acc_phase ^= acc == 0;
-              part = 0;
+                for (int i = 0; i < kBK / 16; ++i)
+                  tc::mma_low<CG>(tmem + acc * BN, a + i * kStepA, b + i * kStepB, instr, part > 0 || i > 0);
+                tc::mma_commit<CG>(&bar.empty[s.stage]);
+                if (closes) tc::mma_commit<CG>(&bar.acc_full[acc]);
+              }
+              __syncwarp();
+              a_at += R::kStageA >> 4;
+              s.next(stages);
+              ++part;
+              if (closes) {
+                if (++acc == kAccs) {
+                  acc = 0;
+                  acc_phase ^= 1;
+                }
+                part = 0;
+              }
             }
           }
         }
+        if (Op::kKeep && ok && one) tc::mma_commit<CG>(&bar.a_empty);
+        __syncwarp();
       }
-      tc::mma_commit<CG>(&bar.done);  // tensor memory is freed only when no product writes it, also after a wait ran out
+      if (one) tc::mma_commit<CG>(&bar.done);  // tensor memory is freed only when no product writes it, also after a wait ran out
+      __syncwarp();
       ok = tc::mbar_wait(&bar.done, 0) && ok;
-      if (!ok) tc::latch_status(p.status, MT_ECUDA);
+      if (!ok && one) tc::latch_status(p.status, MT_ECUDA);
     }
   } else if (warp >= 4) {
-    const int quad = warp & 3, half = (warp - 4) >> 2;
-    op.warp(ring + R::kStages * R::kStage + (warp - 4) * kStageOut, quad, half, lane);
-    int acc = 0;
-    uint32_t acc_phase = 0;
+    const int quad = warp & 3, team = (warp - 4) >> 2;
+    op.warp(ring + R::kTotal + (warp - 4) * kStageOut, quad, team, lane);
+    uint32_t seq = 0;  // accumulators so far
     bool ok = true;
     for (long long u = u0; u < units && ok; u += ustep) {
       const Unit x = op.unit(u);
@@ -249,17 +321,19 @@ k_tiles(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
       for (int ct = x.ct0; ct < x.ct1 && ok; ++ct) {
         const int parts = steps == 0 ? 1 : (steps + p.promote - 1) / p.promote;
         for (int part = 0; part < parts; ++part) {
+          const uint32_t b = seq % kAccs, parity = seq / kAccs & 1;
+          if (Op::kTeams && (steps > 0 ? seq & 1 : 0) != team) {
+            seq += steps > 0;
+            continue;
+          }
+          seq += steps > 0;
           if (steps > 0) {
-            ok = __all_sync(kFull, tc::mbar_wait(&bar.acc_full[acc], acc_phase));
+            ok = __all_sync(kFull, tc::mbar_wait(&bar.acc_full[b], parity));
             if (!ok) break;
             tc::fence_after();
           }
-          const Acc a{tmem + acc * BN + ((uint32_t)(quad * 32) << 16), &bar.acc_empty[acc], steps > 0};
+          const Acc a{tmem + b * BN + ((uint32_t)(quad * 32) << 16), &bar.acc_empty[b], steps > 0};
           op.template tile<CG>(x, ct, a, part == 0, part + 1 == parts);
-          if (steps > 0) {
-            acc ^= 1;
-            acc_phase ^= acc == 0;
-          }
         }
       }
       if (ok) op.end(x);
@@ -271,7 +345,7 @@ k_tiles(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
   if constexpr (CG == 2) tc::cluster_sync();
   else __syncthreads();
   tc::fence_after();
-  if (warp == 1) tc::tmem_free<CG>(tmem, 2 * BN);
+  if (warp == 1) tc::tmem_free<CG>(tmem, kAccs * BN);
 }
 
 // ---- rows through an epilogue warp's shared memory -------------------------------------------
@@ -384,7 +458,7 @@ __device__ __forceinline__ void store32(uint8_t* stage, int lane, const float (&
 template <class Op, int CG>
 cudaError_t launch(const char* name, const CUtensorMap& a, const CUtensorMap& b, const typename Op::Params& p, long long units,
                    size_t extra, size_t most, cudaStream_t s) {
-  constexpr size_t ring = 1024 + Ring<Op::kBN, CG>::kBytes;  // the stages start on 1024 bytes
+  constexpr size_t ring = 1024 + Ring<Op::kBN, CG, Op::kKeep>::kBytes;  // the stages start on 1024 bytes
   static SmemLimit limit;
   const cudaError_t e = limit.allow(k_tiles<Op, CG>, ring + most);
   if (e != cudaSuccess) return e;

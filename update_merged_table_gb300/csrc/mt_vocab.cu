@@ -466,6 +466,7 @@ LogitParams logits_of(const mt_vocab_loss& c, const Layout& l, char* ws) {
   p.b_part = l.wp;
   p.promote = 1 << 30;
   p.steps = (int)tiles_of(l.dp, 64);
+  p.kept = l.parts * p.steps <= kLogitKept ? l.parts * p.steps : 0;
   p.status = c.status;
   p.rows = LiveRows{reinterpret_cast<int*>(ws + l.live), reinterpret_cast<int*>(ws + l.ids), reinterpret_cast<float*>(ws + l.share), l.top};
   p.max_chunks = l.max_chunks;
@@ -512,7 +513,7 @@ int mt_vocab_loss_forward(const mt_vocab_loss* c, float* loss, float* lse, void*
   p.sum_z = c->smoothing > 0.0f ? reinterpret_cast<float*>(base + l.sum_z) : nullptr;
   p.picked = reinterpret_cast<float*>(base + l.picked);
   p.chunks = reinterpret_cast<int*>(base + l.chunks);
-  const bool pair = c->dtype == MT_BF16 && pair_rows(c->n, p.tiles, p.steps);
+  const bool pair = c->dtype == MT_BF16 && pair_rows(c->n, tiles_of(c->vocab, 256), p.steps);
   const Weights w = weights_of(*c, l, base);
   CUtensorMap a, b;
   const uint64_t width = (uint64_t)l.parts * l.dp;
@@ -631,7 +632,7 @@ int mt_vocab_loss_backward(const mt_vocab_loss* c, const float* dloss, const flo
     const uint64_t zw = (uint64_t)l.parts * p.width;
     CUtensorMap a, b;
     {
-      const bool pair = !fp32 && pair_rows(c->n, p.tiles, p.steps);
+      const bool pair = !fp32 && pair_rows(c->n, tiles_of(columns, 256), p.steps);
       if (!tc::encode_bf16(&a, 2, base + l.xs, xw, l.rows, xw, 1, 0, 64, 128)) return MT_ECUDA;
       if (!tc::encode_bf16(&b, 2, wv, w.width, columns, w.ld, 1, 0, 64, pair ? 128 : 256)) return MT_ECUDA;
       e = launch_logit_grad(p, l.parts, a, b, tiles_of(c->n, pair ? 256 : 128), pair, s);

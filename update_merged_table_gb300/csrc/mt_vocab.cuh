@@ -24,11 +24,12 @@ struct LogitParams {
   int32_t* status;
   LiveRows rows;
   int v0, columns;      // the piece: its first entry of the vocabulary, how many it has
-  int tiles;            // of 256 columns
+  int kept;             // steps of x (of all parts) that a block keeps, 0: none
+  int tiles;            // of 128 columns (kept) or 256
   int max_chunks;       // runs of tiles that the statistics have room for
   float scale2;         // scale * log2(e)
   // statistics
-  float2* part;         // [2 max_chunks][stride]: per run and half of a tile's columns, the largest z and sum of 2^(z - that)
+  float2* part;         // [2 max_chunks][stride]: per run and team, the largest z and sum of 2^(z - that)
   float* sum_z;         // the same shape: sums of the logits before the scale (smoothing), or NULL
   float* picked;        // [n][top] the logits of the row's targets, before the scale
   size_t stride;
@@ -38,6 +39,7 @@ struct LogitParams {
   __nv_bfloat16* dz;    // [stride][parts][width]
   int width;            // columns of a part of dz: those of the piece in multiples of 64, zeros behind them
 };
+constexpr int kLogitKept = 8;  // steps of 64 columns
 cudaError_t launch_logit_stats(const LogitParams& p, const CUtensorMap& a, const CUtensorMap& b, long long row_tiles, bool pair,
                                cudaStream_t s);
 cudaError_t launch_logit_grad(const LogitParams& p, int parts, const CUtensorMap& a, const CUtensorMap& b, long long row_tiles, bool pair,

@@ -14,8 +14,9 @@
 //   dx += dz W or dW += dz^T x with the same tile of dz, read along its rows or
 //   across them, and the same tile of W or x that made S, read across.
 //
-// The products of the next tile are issued before those that wait for this tile's
-// dz, so the tensor core works while the warps do.
+// The products of the next two tiles are issued before those that wait for this
+// tile's dz, so the tensor core works while the warps do; two teams of four warps take
+// every other tile, so that one's loads and waits overlap the other's arithmetic.
 #include "mt_tiles.cuh"
 #include "mt_vocab.cuh"
 #include "mt_vocab_rows.cuh"
@@ -26,11 +27,12 @@ namespace {
 constexpr int kT = 128;                  // rows and entries of a tile
 constexpr int kSlab = kT * 128;          // 128 rows of 64 columns
 constexpr int kDz = 2 * kSlab;           // a tile of dz
-constexpr int kAccAt = 2 * kT;           // tensor memory: two S, then the sum
+constexpr int kS = 3;                    // S under way
+constexpr int kAccAt = kS * kT;          // tensor memory: these, then the sum
 
 struct FusedBarriers {
   uint64_t full[8], empty[8];        // a streamed tile has landed; its products are done
-  uint64_t s_full[2], s_empty[2];    // S is finished; it has been read
+  uint64_t s_full[kS], s_empty[kS];  // S is finished; it has been read
   uint64_t dz_full[2], dz_empty[2];  // dz is in shared memory; its products are done
   uint64_t kept_full, kept_empty;    // the kept tile has landed; its products are done
   uint64_t acc_full, acc_empty;      // a unit's sum is finished; it has been read
@@ -91,10 +93,12 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
       tc::mbar_init(&bar.full[i], 1);
       tc::mbar_init(&bar.empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kS; ++i) {
       tc::mbar_init(&bar.s_full[i], 1);
-      tc::mbar_init(&bar.s_empty[i], tiles::kEpiWarps);
-      tc::mbar_init(&bar.dz_full[i], tiles::kEpiWarps);
+      tc::mbar_init(&bar.s_empty[i], tiles::kEpiWarps / 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&bar.dz_full[i], tiles::kEpiWarps / 2);
       tc::mbar_init(&bar.dz_empty[i], 1);
     }
     tc::mbar_init(&bar.kept_full, 1);
@@ -156,8 +160,8 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
       bool ok = true;
       // S of the next tile
       auto make_s = [&]() {
-        const int b = n_s & 1;
-        ok = tc::mbar_wait(&bar.s_empty[b], (n_s >> 1 & 1) ^ 1) && tc::mbar_wait(&bar.full[s.stage], s.phase);
+        const int b = n_s % kS;
+        ok = tc::mbar_wait(&bar.s_empty[b], (n_s / kS & 1) ^ 1) && tc::mbar_wait(&bar.full[s.stage], s.phase);
         if (!ok) return;
         tc::fence_after();
         const uint32_t kept = tc::smem_addr(s_kept), ring = tc::smem_addr(s_ring + s.stage * R::kTile);
@@ -177,8 +181,9 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         kept_phase ^= 1;
         if (!ok) break;
         make_s();
+        if (ok && x.t0 + 1 < x.t1) make_s();
         for (int t = x.t0; t < x.t1 && ok; ++t) {
-          if (t + 1 < x.t1) make_s();
+          if (t + 2 < x.t1) make_s();
           if (!ok) break;
           const int b = n_sum & 1;
           if (t == x.t0) ok = tc::mbar_wait(&bar.acc_empty, acc_phase ^ 1);
@@ -206,95 +211,102 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
       if (!ok) tc::latch_status(p.status, MT_ECUDA);
     }
   } else if (warp >= 4) {
-    const int quad = warp & 3, half = (warp - 4) >> 2;
+    const int quad = warp & 3, team = (warp - 4) >> 2;
     uint8_t* stage = s_out + (warp - 4) * tiles::kStageOut;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    uint8_t* dz = s_dz + team * kDz + (quad * 32 + lane) * 128;  // the thread's row of dz: two halves of 64 entries
     const f32x2 s2 = both(p.scale2);
-    uint32_t n = 0, acc_phase = 0;
+    uint32_t n = 0, acc_phase = 0;  // tiles so far
     bool ok = true;
     RowTargets to;
     float4 k = make_float4(0.0f, 0.0f, 0.0f, 0.0f), k_next = k;
     int id_next = 0x7FFFFFFF;  // a row's only target
+    // dz of 32 entries from their logits, four 16-byte pieces of a swizzled 128-byte row
+    auto columns = [&](const uint32_t (&v)[32], int c, int row, int v0, bool some) {
+      float f[32];
+      const f32x2 x2 = both(-k.x), y2 = both(k.y), z2 = both(-k.z);
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        const float2 e = upk(fma2(pk(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), s2, x2));
+        const float2 g = upk(fma2(pk(exp2_of(e.x), exp2_of(e.y)), y2, z2));
+        f[j] = g.x;
+        f[j + 1] = g.y;
+      }
+      if (some) {  // targets, or entries or rows that are not there
+        to.take(p.rows, v0 + c, k.w, f);
+        const uint32_t there = row < work.live ? below(p.vocab - v0 - c) : 0u;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (!(there >> j & 1)) f[j] = 0.0f;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint4*>(dz + (c >> 6) * kSlab + (((((c >> 5) & 1) * 4 + q) ^ (lane & 7)) << 4)) =
+            make_uint4(bf16x2_of(f[q * 8], f[q * 8 + 1]), bf16x2_of(f[q * 8 + 2], f[q * 8 + 3]), bf16x2_of(f[q * 8 + 4], f[q * 8 + 5]),
+                       bf16x2_of(f[q * 8 + 6], f[q * 8 + 7]));
+    };
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const FusedUnit x = work.unit(u);
       if (x.t0 < x.t1) {
         auto row_at = [&](int tile) { return tile * kT + quad * 32 + lane; };
         auto id_at = [&](int row) { return p.rows.top == 1 && row < work.live ? __ldg(p.rows.ids + row) : 0x7FFFFFFF; };
         auto coef_at = [&](int row) { return row < work.live ? __ldg(p.coef + row) : make_float4(0.0f, 0.0f, 0.0f, 0.0f); };
+        const int first = x.t0 + ((n & 1) != team);  // this team's first tile
         if (VOCAB) {
-          k_next = coef_at(row_at(x.t0));
-          id_next = id_at(row_at(x.t0));
+          k_next = coef_at(row_at(first));
+          id_next = id_at(row_at(first));
         } else {
           k = coef_at(row_at(x.kept));
           to.start(p.rows, row_at(x.kept), work.live, x.t0 * kT);
         }
-        for (int t = x.t0; t < x.t1; ++t, ++n) {
-          const int b = n & 1, parity = n >> 1 & 1;
-          const int row = row_at(VOCAB ? t : x.kept), v0 = (VOCAB ? x.kept : t) * kT + half * 64;
+        for (int t = first; t < x.t1; t += 2) {
+          const uint32_t of = n + (t - x.t0), b = of % kS, from = tmem + b * kT + lanes;
+          const int row = row_at(VOCAB ? t : x.kept), v0 = (VOCAB ? x.kept : t) * kT;
           if (VOCAB) {
             k = k_next;
             if (p.rows.top == 1) {
               to.row = row;
               to.pos = 0;
-              to.next = id_next >= x.kept * kT ? id_next : 0x7FFFFFFF;
+              to.next = id_next >= v0 ? id_next : 0x7FFFFFFF;
             } else {
-              to.start(p.rows, row, work.live, x.kept * kT);
+              to.start(p.rows, row, work.live, v0);
             }
-            if (t + 1 < x.t1) {
-              k_next = coef_at(row_at(t + 1));
-              id_next = id_at(row_at(t + 1));
+            if (t + 2 < x.t1) {
+              k_next = coef_at(row_at(t + 2));
+              id_next = id_at(row_at(t + 2));
             }
           }
-          ok = __all_sync(kFull, tc::mbar_wait(&bar.s_full[b], parity) && tc::mbar_wait(&bar.dz_empty[b], parity ^ 1));
+          const bool some = __any_sync(kFull, to.next < v0 + kT || row >= work.live) || v0 + kT > p.vocab;
+          ok = __all_sync(kFull, tc::mbar_wait(&bar.s_full[b], of / kS & 1) && tc::mbar_wait(&bar.dz_empty[team], (of >> 1 & 1) ^ 1));
           if (!ok) break;
           tc::fence_after();
           uint32_t v[2][32];
-          tc::tmem_load32(tmem + b * kT + half * 64 + lanes, v[0]);
-          tc::tmem_load32(tmem + b * kT + half * 64 + 32 + lanes, v[1]);
-          tc::tmem_load_wait(v[0]);
-          tc::tmem_loaded(v[1]);
-          tc::fence_before();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&bar.s_empty[b]);
-          // dz of 64 entries of the thread's row: eight 16-byte pieces of a swizzled 128-byte row
-          uint8_t* dz = s_dz + b * kDz + half * kSlab + (quad * 32 + lane) * 128;
-          const f32x2 x2 = both(-k.x), y2 = both(k.y), z2 = both(-k.z);
-          const int left = p.vocab - v0;
+          tc::tmem_load32(from, v[0]);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float f[32];
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const float2 e = upk(fma2(pk(__uint_as_float(v[c][j]), __uint_as_float(v[c][j + 1])), s2, x2));
-              const float2 g = upk(fma2(pk(exp2_of(e.x), exp2_of(e.y)), y2, z2));
-              f[j] = g.x;
-              f[j + 1] = g.y;
+          for (int c = 0; c < kT; c += 32) {
+            tc::tmem_load_wait(v[c >> 5 & 1]);
+            if (c + 32 < kT) {
+              tc::tmem_load32(from + c + 32, v[(c >> 5 & 1) ^ 1]);
+            } else {
+              tc::fence_before();
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive(&bar.s_empty[b]);
             }
-            to.take(p.rows, v0 + c * 32, k.w, f);
-            const uint32_t there = row < work.live ? below(left - c * 32) : 0u;
-            if (there != kFull) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!(there >> j & 1)) f[j] = 0.0f;
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<uint4*>(dz + (((c * 4 + q) ^ (lane & 7)) << 4)) =
-                  make_uint4(bf16x2_of(f[q * 8], f[q * 8 + 1]), bf16x2_of(f[q * 8 + 2], f[q * 8 + 3]), bf16x2_of(f[q * 8 + 4], f[q * 8 + 5]),
-                             bf16x2_of(f[q * 8 + 6], f[q * 8 + 7]));
+            columns(v[c >> 5 & 1], c, row, v0, some);
           }
           tc::fence_async_proxy();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&bar.dz_full[b]);
+          if (lane == 0) tc::mbar_arrive(&bar.dz_full[team]);
         }
         if (!ok) break;
+        n += x.t1 - x.t0;
         ok = __all_sync(kFull, tc::mbar_wait(&bar.acc_full, acc_phase));
         if (!ok) break;
         acc_phase ^= 1;
         tc::fence_after();
       }
       // the unit's sum: 32 columns at a time
-      const int c0 = half * KS * 32;
+      const int c0 = team * KS * 32;  // half of the columns each team
       const int rows = min(32, (VOCAB ? p.vocab : work.live) - (x.kept * kT + quad * 32));
       const long long r0 = x.kept * kT + quad * 32;
 #pragma unroll

@@ -1,15 +1,20 @@
 // Tiles of logits x W^T, 128 rows (256 by a pair of blocks) by 256 entries of the
-// vocabulary, that never leave the chip:
+// vocabulary, that never leave the chip.  Where the rows are short (KEEP) a block
+// keeps its rows of x for a whole run of the vocabulary, which halves what it reads
+// from L2, and takes 128 entries at a time, so that four tiles are under way and no
+// team waits for the products of its next.
 //
-//  the statistics   a thread has one row and half of a tile's columns.  It keeps
-//                   the largest logit so far and the sum of 2^(z - largest) over a
-//                   run of tiles (an online softmax in base 2, one exponential a
+//
+//  the statistics   a thread has one row of every other tile.  It keeps the largest
+//                   logit so far and the sum of 2^(z - largest) over a run of tiles (an online softmax in base 2, one exponential a
 //                   logit), and picks the logits of the row's targets as they come
 //                   by: the targets lie in ascending order, so one comparison per
 //                   32 columns finds them.
 //  their gradient   with the row's log sum known, dz = a p - b less the targets'
 //                   shares, rounded to bf16 (fp32 rows: three bf16 parts), a piece
 //                   of the vocabulary at a time.
+#include <algorithm>
+
 #include "mt_tiles.cuh"
 #include "mt_vocab.cuh"
 #include "mt_vocab_rows.cuh"
@@ -26,21 +31,21 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 // What both kernels share: rows tiles fastest, so that blocks at work at the same time read the same entries of W.
-template <int CG>
+template <int CG, bool KEEP>
 struct Logits {
   using Params = LogitParams;
   static constexpr int kBN = 256;
-  static constexpr bool kAMN = false, kBMN = false, kTwoB = false;
+  static constexpr bool kAMN = false, kBMN = false, kTwoB = false, kTeams = true, kKeep = KEEP;
   const Params& p;
   int rank, live, rt, chunks;
   uint8_t* stage;
-  int quad, half, lane, row;  // the thread's row
+  int quad, team, lane, row;  // the thread's row
   RowTargets to;
 
   __device__ Logits(const Params& params, uint8_t*, int r) : p(params), rank(r) {
     live = *p.rows.count;
     rt = (live + tiles::kBM * CG - 1) / (tiles::kBM * CG);
-    chunks = choose_chunks(rt, p.tiles, p.max_chunks, gridDim.x / CG, 1);
+    chunks = choose_chunks(rt, p.tiles, p.max_chunks, gridDim.x / CG, KEEP ? 6 : 1);
   }
   __device__ long long units() const { return (long long)rt * chunks; }
   __device__ Unit unit(long long u) const {
@@ -59,7 +64,7 @@ struct Logits {
   __device__ void warp(uint8_t* s, int q, int h, int l) {
     stage = s;
     quad = q;
-    half = h;
+    team = h;
     lane = l;
   }
   __device__ void start(const Unit& x) {
@@ -68,9 +73,9 @@ struct Logits {
   }
 };
 
-template <bool SMOOTH, int CG>
-struct Stats : Logits<CG> {
-  using Base = Logits<CG>;
+template <bool SMOOTH, int CG, bool KEEP>
+struct Stats : Logits<CG, KEEP> {
+  using Base = Logits<CG, KEEP>;
   float top, sum, total;
   __device__ Stats(const LogitParams& p, uint8_t* mem, int r) : Base(p, mem, r) {
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.chunks = this->chunks;
@@ -82,7 +87,7 @@ struct Stats : Logits<CG> {
   }
   __device__ void end(const Unit& x) {
     if (this->row >= this->live) return;
-    const size_t at = (size_t)(x.slot * 2 + this->half) * this->p.stride + this->row;
+    const size_t at = (size_t)(x.slot * 2 + this->team) * this->p.stride + this->row;
     this->p.part[at] = make_float2(top, sum);
     if constexpr (SMOOTH) this->p.sum_z[at] = total;
   }
@@ -126,22 +131,26 @@ struct Stats : Logits<CG> {
   template <int G>
   __device__ __forceinline__ void tile(const Unit&, int ct, const Acc& acc, bool, bool) {
     const LogitParams& p = this->p;
-    const int from = this->half * 128, at = ct * 256 + from, left = p.columns - at;
+    constexpr int kBN = Base::kBN;
+    const int at = ct * kBN, left = p.columns - at;
     uint32_t v[2][32];
-    acc.load(from, v[0]);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      tc::tmem_load_wait(v[c & 1]);
-      if (c < 3) acc.load(from + (c + 1) * 32, v[(c + 1) & 1]);
+    acc.load(0, v[0]);
+#pragma unroll 1
+    for (int c = 0; c < kBN; c += 64) {
+      tc::tmem_load_wait(v[0]);
+      acc.load(c + 32, v[1]);
+      columns(v[0], p.v0 + at + c, left - c);
+      tc::tmem_load_wait(v[1]);
+      if (c + 64 < kBN) acc.load(c + 64, v[0]);
       else acc.release<G>(this->lane);
-      columns(v[c & 1], p.v0 + at + c * 32, left - c * 32);
+      columns(v[1], p.v0 + at + c + 32, left - c - 32);
     }
   }
 };
 
-template <int PARTS, int CG>
-struct Grad : Logits<CG> {
-  using Base = Logits<CG>;
+template <bool SPLIT, int CG, bool KEEP>  // SPLIT: dz in three bf16 parts
+struct Grad : Logits<CG, KEEP> {
+  using Base = Logits<CG, KEEP>;
   float4 k;
   __device__ Grad(const LogitParams& p, uint8_t* mem, int r) : Base(p, mem, r) {}
   __device__ void begin(const Unit& x) {
@@ -169,7 +178,7 @@ struct Grad : Logits<CG> {
       for (int j = 0; j < 32; ++j)
         if (!(there >> j & 1)) f[j] = 0.0f;
     }
-    if constexpr (PARTS == 1) {
+    if constexpr (!SPLIT) {
       tiles::store32<__nv_bfloat16>(this->stage, this->lane, f, p.dz, p.width, r0, 32, at0, p.width, true);
     } else {
       uint32_t w[3][16];
@@ -188,37 +197,52 @@ struct Grad : Logits<CG> {
   }
   template <int G>
   __device__ __forceinline__ void tile(const Unit& x, int ct, const Acc& acc, bool, bool) {
-    const int from = this->half * 128, at = ct * 256 + from, left = this->p.columns - at;
+    constexpr int kBN = Base::kBN;
+    const int at = ct * kBN, left = this->p.columns - at;
     const long long r0 = x.row0 + this->rank * tiles::kBM + this->quad * 32;
     uint32_t v[2][32];
-    acc.load(from, v[0]);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      tc::tmem_load_wait(v[c & 1]);
-      if (c < 3) acc.load(from + (c + 1) * 32, v[(c + 1) & 1]);
+    acc.load(0, v[0]);
+#pragma unroll 1
+    for (int c = 0; c < kBN; c += 64) {
+      tc::tmem_load_wait(v[0]);
+      acc.load(c + 32, v[1]);
+      columns(v[0], at + c, left - c, r0);
+      tc::tmem_load_wait(v[1]);
+      if (c + 64 < kBN) acc.load(c + 64, v[0]);
       else acc.release<G>(this->lane);
-      columns(v[c & 1], at + c * 32, left - c * 32, r0);
+      columns(v[1], at + c + 32, left - c - 32, r0);
     }
   }
 };
 
 }  // namespace
 
+namespace {
+template <class Op, int CG>
+cudaError_t launch_op(const char* name, const LogitParams& p, const CUtensorMap& a, const CUtensorMap& b, long long row_tiles, cudaStream_t s) {
+  return tiles::launch<Op, CG>(name, a, b, p, row_tiles * std::min(p.tiles, p.max_chunks), 0, 0, s);
+}
+}  // namespace
+
 cudaError_t launch_logit_stats(const LogitParams& p, const CUtensorMap& a, const CUtensorMap& b, long long row_tiles, bool pair,
                                cudaStream_t s) {
-  const long long units = row_tiles * (p.tiles < p.max_chunks ? p.tiles : p.max_chunks);
   const char* name = "k_logit_stats";
-  if (p.sum_z != nullptr)
-    return pair ? tiles::launch<Stats<true, 2>, 2>(name, a, b, p, units, 0, 0, s) : tiles::launch<Stats<true, 1>, 1>(name, a, b, p, units, 0, 0, s);
-  return pair ? tiles::launch<Stats<false, 2>, 2>(name, a, b, p, units, 0, 0, s) : tiles::launch<Stats<false, 1>, 1>(name, a, b, p, units, 0, 0, s);
+  auto go = [&](auto smooth) {
+    constexpr bool S = decltype(smooth)::value;
+    if (p.kept > 0)
+      return pair ? launch_op<Stats<S, 2, true>, 2>(name, p, a, b, row_tiles, s) : launch_op<Stats<S, 1, true>, 1>(name, p, a, b, row_tiles, s);
+    return pair ? launch_op<Stats<S, 2, false>, 2>(name, p, a, b, row_tiles, s) : launch_op<Stats<S, 1, false>, 1>(name, p, a, b, row_tiles, s);
+  };
+  return p.sum_z != nullptr ? go(std::true_type{}) : go(std::false_type{});
 }
-
 cudaError_t launch_logit_grad(const LogitParams& p, int parts, const CUtensorMap& a, const CUtensorMap& b, long long row_tiles, bool pair,
                               cudaStream_t s) {
-  const long long units = row_tiles * (p.tiles < p.max_chunks ? p.tiles : p.max_chunks);
   const char* name = "k_logit_grad";
-  if (parts == 3) return tiles::launch<Grad<3, 1>, 1>(name, a, b, p, units, 0, 0, s);
-  return pair ? tiles::launch<Grad<1, 2>, 2>(name, a, b, p, units, 0, 0, s) : tiles::launch<Grad<1, 1>, 1>(name, a, b, p, units, 0, 0, s);
+  if (parts == 3)
+    return p.kept > 0 ? launch_op<Grad<true, 1, true>, 1>(name, p, a, b, row_tiles, s) : launch_op<Grad<true, 1, false>, 1>(name, p, a, b, row_tiles, s);
+  if (p.kept > 0)
+    return pair ? launch_op<Grad<false, 2, true>, 2>(name, p, a, b, row_tiles, s) : launch_op<Grad<false, 1, true>, 1>(name, p, a, b, row_tiles, s);
+  return pair ? launch_op<Grad<false, 2, false>, 2>(name, p, a, b, row_tiles, s) : launch_op<Grad<false, 1, false>, 1>(name, p, a, b, row_tiles, s);
 }
 
 }  // namespace mt

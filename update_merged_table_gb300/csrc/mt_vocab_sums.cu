@@ -25,7 +25,7 @@ template <int BN, bool FP32, bool VOCAB, int CG>
 struct Sum {
   using Params = SumParams;
   static constexpr int kBN = BN;
-  static constexpr bool kAMN = VOCAB, kBMN = true;
+  static constexpr bool kAMN = VOCAB, kBMN = true, kTeams = !FP32, kKeep = false;
   const Params& p;
   int rank, rows, rt, steps, quad, half, lane;
   uint8_t* stage;
@@ -119,14 +119,14 @@ struct Sum {
 
   template <int G>
   __device__ __forceinline__ void tile(const Unit& x, int ct, const Acc& acc, bool first, bool last) {
-    constexpr int kHalf = BN / 2;
-    const int col0 = ct * BN + half * kHalf;
+    constexpr int kMine = kTeams ? BN : BN / 2;  // columns of this warp
+    const int from = kTeams ? 0 : half * kMine, col0 = ct * BN + from;
 #pragma unroll
-    for (int c = 0; c < kHalf; c += 32) {
+    for (int c = 0; c < kMine; c += 32) {
       uint32_t v[32];
-      acc.load(half * kHalf + c, v);
+      acc.load(from + c, v);
       tc::tmem_load_wait(v);
-      if (c + 32 == kHalf) acc.release<G>(lane);
+      if (c + 32 == kMine) acc.release<G>(lane);
       if constexpr (FP32) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) sum[c + j] = first ? __uint_as_float(v[j]) : sum[c + j] + __uint_as_float(v[j]);
@@ -140,7 +140,7 @@ struct Sum {
     if constexpr (FP32) {
       if (last) {
 #pragma unroll
-        for (int c = 0; c < kHalf; c += 32) {
+        for (int c = 0; c < kMine; c += 32) {
           float f[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) f[j] = sum[c + j];
