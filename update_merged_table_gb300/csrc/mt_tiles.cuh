@@ -76,7 +76,9 @@ struct Acc {
   uint64_t* empty;
   bool live;  // false: the contraction is empty, everything is zero
   // 32 columns from c on; tc::tmem_load_wait() before they are used
-  __device__ __forceinline__ void load(int c, uint32_t (&v)[32]) const {
+  __device__ __forceinline__ void load(int c, uint32_t (&v)[32]) const { tc::tmem_load32(from + c, v); }
+  // the same where the contraction may be empty
+  __device__ __forceinline__ void load_or_zero(int c, uint32_t (&v)[32]) const {
     if (live) {
       tc::tmem_load32(from + c, v);
     } else {

@@ -117,99 +117,118 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   const int units = work.units();
 
   if (warp == 0) {
-    if (lane == 0) {
-      tc::Slot s;
-      long long issued = 0;
-      uint32_t kept_phase = 0;
-      bool ok = true, any = false;
-      const CUtensorMap* kept_map = VOCAB ? &map_w : &map_x;
-      const CUtensorMap* ring_map = VOCAB ? &map_x : &map_w;
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-        const FusedUnit x = work.unit(u);
-        if (x.t0 == x.t1) continue;
-        ok = tc::mbar_wait(&bar.kept_empty, kept_phase ^ 1);
-        if (!ok) break;
-        kept_phase ^= 1;
-        any = true;
+    const bool one = tc::elect_one();
+    tc::Slot s;
+    long long issued = 0;
+    uint32_t kept_phase = 0;
+    bool ok = true, any = false;
+    const CUtensorMap* kept_map = VOCAB ? &map_w : &map_x;
+    const CUtensorMap* ring_map = VOCAB ? &map_x : &map_w;
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const FusedUnit x = work.unit(u);
+      if (x.t0 == x.t1) continue;
+      ok = tc::warp_wait(&bar.kept_empty, kept_phase ^ 1);
+      if (!ok) break;
+      kept_phase ^= 1;
+      any = true;
+      if (one) {
         tc::mbar_expect(&bar.kept_full, R::kTile);
 #pragma unroll
         for (int k = 0; k < KS; ++k) tc::tma_load_2d(s_kept + k * kSlab, kept_map, &bar.kept_full, k * 64, x.kept * kT);
-        for (int t = x.t0; t < x.t1; ++t) {
-          ok = tc::mbar_wait(&bar.empty[s.stage], s.phase ^ 1);
-          if (!ok) break;
+      }
+      __syncwarp();
+      for (int t = x.t0; t < x.t1; ++t) {
+        ok = tc::warp_wait(&bar.empty[s.stage], s.phase ^ 1);
+        if (!ok) break;
+        if (one) {
           uint8_t* st = s_ring + s.stage * R::kTile;
           tc::mbar_expect(&bar.full[s.stage], R::kTile);
 #pragma unroll
           for (int k = 0; k < KS; ++k) tc::tma_load_2d(st + k * kSlab, ring_map, &bar.full[s.stage], k * 64, t * kT);
-          ++issued;
-          s.next<R::kStages>();
         }
+        __syncwarp();
+        ++issued;
+        s.next<R::kStages>();
       }
-      ok = ok && tc::all_released<R::kStages>(bar, s, issued);
-      if (!ok) {
-        tc::latch_status(p.status, MT_ECUDA);
-        tc::drain<R::kStages>(bar, s, issued);
-        if (any) tc::mbar_wait(&bar.kept_full, kept_phase ^ 1);
-      }
+    }
+    ok = ok && tc::all_released<R::kStages>(bar, s, issued);
+    if (!ok) {
+      if (one) tc::latch_status(p.status, MT_ECUDA);
+      tc::drain<R::kStages>(bar, s, issued);
+      if (any) tc::mbar_wait(&bar.kept_full, kept_phase ^ 1);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t instr_s = tc::instr_bf16(kT, kT, false, false), instr_sum = tc::instr_bf16(kT, KS * 64, VOCAB, true);
-      tc::Slot s, d;   // the streamed tile of the next S; of the next sum
-      uint32_t n_s = 0, n_sum = 0, kept_phase = 0, acc_phase = 0;  // tiles so far
-      bool ok = true;
-      // S of the next tile
-      auto make_s = [&]() {
-        const int b = n_s % kS;
-        ok = tc::mbar_wait(&bar.s_empty[b], (n_s / kS & 1) ^ 1) && tc::mbar_wait(&bar.full[s.stage], s.phase);
-        if (!ok) return;
-        tc::fence_after();
-        const uint32_t kept = tc::smem_addr(s_kept), ring = tc::smem_addr(s_ring + s.stage * R::kTile);
-        const uint32_t ax = VOCAB ? ring : kept, aw = VOCAB ? kept : ring;
+    constexpr uint32_t instr_s = tc::instr_bf16(kT, kT, false, false), instr_sum = tc::instr_bf16(kT, KS * 64, VOCAB, true);
+    const bool one = tc::elect_one();
+    // descriptors' low words: rows along the contraction (S, and dz for dx), rows across it (the sums' others)
+    const uint32_t kept_s = tc::desc_low(tc::smem_addr(s_kept), 16), ring_s = tc::desc_low(tc::smem_addr(s_ring), 16);
+    const uint32_t ring_sum = tc::desc_low(tc::smem_addr(s_ring), kSlab), dz_sum = tc::desc_low(tc::smem_addr(s_dz), VOCAB ? kSlab : 16);
+    tc::Slot s, d;   // the streamed tile of the next S; of the next sum
+    uint32_t b_s = 0, phase_s = 0, n_sum = 0, kept_phase = 0, acc_phase = 0;
+    bool ok = true;
+    // S of the next tile
+    auto make_s = [&]() {
+      ok = tc::warp_wait(&bar.s_empty[b_s], phase_s ^ 1) && tc::warp_wait(&bar.full[s.stage], s.phase);
+      if (!ok) return;
+      tc::fence_after();
+      const uint32_t at = ring_s + s.stage * (R::kTile >> 4);
+      const uint32_t ax = VOCAB ? at : kept_s, aw = VOCAB ? kept_s : at;
+      if (one) {
 #pragma unroll
-        for (int i = 0; i < KS * 4; ++i)
-          tc::mma_bf16<1>(tmem + b * kT, tc::smem_desc(ax + (i >> 2) * kSlab + (i & 3) * 32, 16),
-                          tc::smem_desc(aw + (i >> 2) * kSlab + (i & 3) * 32, 16), instr_s, i > 0);
-        tc::mma_commit<1>(&bar.s_full[b]);
-        ++n_s;
-        s.next<R::kStages>();
-      };
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-        const FusedUnit x = work.unit(u);
-        if (x.t0 == x.t1) continue;
-        ok = tc::mbar_wait(&bar.kept_full, kept_phase);
-        kept_phase ^= 1;
+        for (int i = 0; i < KS * 4; ++i) {
+          const uint32_t o = ((i >> 2) * kSlab + (i & 3) * 32) >> 4;
+          tc::mma_low<1>(tmem + b_s * kT, ax + o, aw + o, instr_s, i > 0);
+        }
+        tc::mma_commit<1>(&bar.s_full[b_s]);
+      }
+      __syncwarp();
+      if (++b_s == kS) {
+        b_s = 0;
+        phase_s ^= 1;
+      }
+      s.next<R::kStages>();
+    };
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const FusedUnit x = work.unit(u);
+      if (x.t0 == x.t1) continue;
+      ok = tc::warp_wait(&bar.kept_full, kept_phase);
+      kept_phase ^= 1;
+      if (!ok) break;
+      make_s();
+      if (ok && x.t0 + 1 < x.t1) make_s();
+      for (int t = x.t0; t < x.t1 && ok; ++t) {
+        if (t + 2 < x.t1) make_s();
         if (!ok) break;
-        make_s();
-        if (ok && x.t0 + 1 < x.t1) make_s();
-        for (int t = x.t0; t < x.t1 && ok; ++t) {
-          if (t + 2 < x.t1) make_s();
-          if (!ok) break;
-          const int b = n_sum & 1;
-          if (t == x.t0) ok = tc::mbar_wait(&bar.acc_empty, acc_phase ^ 1);
-          ok = ok && tc::mbar_wait(&bar.dz_full[b], n_sum >> 1 & 1);
-          if (!ok) break;
-          tc::fence_after();
-          const uint32_t dz = tc::smem_addr(s_dz + b * kDz), ring = tc::smem_addr(s_ring + d.stage * R::kTile);
+        const uint32_t b = n_sum & 1;
+        if (t == x.t0) ok = tc::warp_wait(&bar.acc_empty, acc_phase ^ 1);
+        ok = ok && tc::warp_wait(&bar.dz_full[b], n_sum >> 1 & 1);
+        if (!ok) break;
+        tc::fence_after();
+        const uint32_t dz = dz_sum + b * (kDz >> 4), ring = ring_sum + d.stage * (R::kTile >> 4);
+        if (one) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint64_t a = VOCAB ? tc::smem_desc(dz + i * 2048, kSlab) : tc::smem_desc(dz + (i >> 2) * kSlab + (i & 3) * 32, 16);
-            tc::mma_bf16<1>(tmem + kAccAt, a, tc::smem_desc(ring + i * 2048, kSlab), instr_sum, t > x.t0 || i > 0);
-          }
+          for (int i = 0; i < 8; ++i)
+            tc::mma_low<1>(tmem + kAccAt, dz + ((VOCAB ? i * 2048 : (i >> 2) * kSlab + (i & 3) * 32) >> 4), ring + (i * 2048 >> 4), instr_sum,
+                           t > x.t0 || i > 0);
           tc::mma_commit<1>(&bar.empty[d.stage]);
           tc::mma_commit<1>(&bar.dz_empty[b]);
-          ++n_sum;
-          d.next<R::kStages>();
         }
-        if (!ok) break;
+        __syncwarp();
+        ++n_sum;
+        d.next<R::kStages>();
+      }
+      if (!ok) break;
+      if (one) {
         tc::mma_commit<1>(&bar.kept_empty);
         tc::mma_commit<1>(&bar.acc_full);
-        acc_phase ^= 1;
       }
-      tc::mma_commit<1>(&bar.done);  // tensor memory is freed only when no product writes it, also after a wait ran out
-      ok = tc::mbar_wait(&bar.done, 0) && ok;
-      if (!ok) tc::latch_status(p.status, MT_ECUDA);
+      __syncwarp();
+      acc_phase ^= 1;
     }
+    if (one) tc::mma_commit<1>(&bar.done);  // tensor memory is freed only when no product writes it, also after a wait ran out
+    __syncwarp();
+    ok = tc::mbar_wait(&bar.done, 0) && ok;
+    if (!ok && one) tc::latch_status(p.status, MT_ECUDA);
   } else if (warp >= 4) {
     const int quad = warp & 3, team = (warp - 4) >> 2;
     uint8_t* stage = s_out + (warp - 4) * tiles::kStageOut;

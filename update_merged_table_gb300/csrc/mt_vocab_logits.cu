@@ -1,8 +1,7 @@
 // Tiles of logits x W^T, 128 rows (256 by a pair of blocks) by 256 entries of the
 // vocabulary, that never leave the chip.  Where the rows are short (KEEP) a block
 // keeps its rows of x for a whole run of the vocabulary, which halves what it reads
-// from L2, and takes 128 entries at a time, so that four tiles are under way and no
-// team waits for the products of its next.
+// from L2.
 //
 //
 //  the statistics   a thread has one row of every other tile.  It keeps the largest
@@ -91,10 +90,11 @@ struct Stats : Logits<CG, KEEP> {
     this->p.part[at] = make_float2(top, sum);
     if constexpr (SMOOTH) this->p.sum_z[at] = total;
   }
-  // 32 columns: their largest, then one exponential each.  The next columns' load is on its way meanwhile.
-  __device__ __forceinline__ void columns(uint32_t (&v)[32], int col, int left) {
+  // 32 columns: their largest, then one exponential each.  The next columns' load is on its way meanwhile.  some: there may
+  // be targets among them, or columns that are not there.
+  __device__ __forceinline__ void columns(uint32_t (&v)[32], int col, int left, bool some) {
     const LogitParams& p = this->p;
-    this->to.pick(p.rows, col, v, p.picked);
+    if (some) this->to.pick(p.rows, col, v, p.picked);
     if constexpr (SMOOTH) {
       f32x2 t[2] = {0ull, 0ull};
 #pragma unroll
@@ -102,7 +102,7 @@ struct Stats : Logits<CG, KEEP> {
         t[j >> 1 & 1] = add2(t[j >> 1 & 1], pk(__uint_as_float(v[j]), __uint_as_float(v[j + 1])));
       total += pair_sum(add2(t[0], t[1]));
     }
-    if (left < 32) {
+    if (some && left < 32) {
       const uint32_t there = below(left);
 #pragma unroll
       for (int j = 0; j < 32; ++j)
@@ -133,17 +133,18 @@ struct Stats : Logits<CG, KEEP> {
     const LogitParams& p = this->p;
     constexpr int kBN = Base::kBN;
     const int at = ct * kBN, left = p.columns - at;
+    const bool some = left < kBN || __any_sync(kFull, this->to.next < p.v0 + at + kBN);
     uint32_t v[2][32];
     acc.load(0, v[0]);
 #pragma unroll 1
     for (int c = 0; c < kBN; c += 64) {
       tc::tmem_load_wait(v[0]);
       acc.load(c + 32, v[1]);
-      columns(v[0], p.v0 + at + c, left - c);
+      columns(v[0], p.v0 + at + c, left - c, some);
       tc::tmem_load_wait(v[1]);
       if (c + 64 < kBN) acc.load(c + 64, v[0]);
       else acc.release<G>(this->lane);
-      columns(v[1], p.v0 + at + c + 32, left - c - 32);
+      columns(v[1], p.v0 + at + c + 32, left - c - 32, some);
     }
   }
 };
@@ -158,7 +159,7 @@ struct Grad : Logits<CG, KEEP> {
     k = this->row < this->live ? this->p.coef[this->row] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   }
   __device__ void end(const Unit&) {}
-  __device__ __forceinline__ void columns(uint32_t (&v)[32], int at0, int left, long long r0) {
+  __device__ __forceinline__ void columns(uint32_t (&v)[32], int at0, int left, long long r0, bool some) {
     const LogitParams& p = this->p;
     const int col = p.v0 + at0;
     float f[32];
@@ -170,10 +171,10 @@ struct Grad : Logits<CG, KEEP> {
       f[j] = d.x;
       f[j + 1] = d.y;
     }
-    this->to.take(p.rows, col, k.w, f);
-    // zeros behind the piece's last column, and in a row behind the last, whatever it holds
-    const uint32_t there = this->row < this->live ? below(left) : 0u;
-    if (there != kFull) {
+    if (some) {
+      this->to.take(p.rows, col, k.w, f);
+      // zeros behind the piece's last column, and in a row behind the last, whatever it holds
+      const uint32_t there = this->row < this->live ? below(left) : 0u;
 #pragma unroll
       for (int j = 0; j < 32; ++j)
         if (!(there >> j & 1)) f[j] = 0.0f;
@@ -200,17 +201,18 @@ struct Grad : Logits<CG, KEEP> {
     constexpr int kBN = Base::kBN;
     const int at = ct * kBN, left = this->p.columns - at;
     const long long r0 = x.row0 + this->rank * tiles::kBM + this->quad * 32;
+    const bool some = left < kBN || __any_sync(kFull, this->to.next < this->p.v0 + at + kBN || this->row >= this->live);
     uint32_t v[2][32];
     acc.load(0, v[0]);
 #pragma unroll 1
     for (int c = 0; c < kBN; c += 64) {
       tc::tmem_load_wait(v[0]);
       acc.load(c + 32, v[1]);
-      columns(v[0], at + c, left - c, r0);
+      columns(v[0], at + c, left - c, r0, some);
       tc::tmem_load_wait(v[1]);
       if (c + 64 < kBN) acc.load(c + 64, v[0]);
       else acc.release<G>(this->lane);
-      columns(v[1], at + c + 32, left - c - 32, r0);
+      columns(v[1], at + c + 32, left - c - 32, r0, some);
     }
   }
 };

@@ -124,7 +124,7 @@ struct Sum {
 #pragma unroll
     for (int c = 0; c < kMine; c += 32) {
       uint32_t v[32];
-      acc.load(from + c, v);
+      acc.load_or_zero(from + c, v);
       tc::tmem_load_wait(v);
       if (c + 32 == kMine) acc.release<G>(lane);
       if constexpr (FP32) {
