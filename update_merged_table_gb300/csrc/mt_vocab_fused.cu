@@ -14,8 +14,8 @@
 //   dx += dz W or dW += dz^T x with the same tile of dz, read along its rows or
 //   across them, and the same tile of W or x that made S, read across.
 //
-// The products of the next two tiles are issued before those that wait for this
-// tile's dz, so the tensor core works while the warps do; two teams of four warps take
+// The products of the next tiles are issued before those that wait for this tile's
+// dz, so the tensor core works while the warps do; two teams of four warps take
 // every other tile, so that one's loads and waits overlap the other's arithmetic.
 #include "mt_tiles.cuh"
 #include "mt_vocab.cuh"
@@ -33,18 +33,19 @@ constexpr int kAccAt = kS * kT;          // tensor memory: these, then the sum
 struct FusedBarriers {
   uint64_t full[8], empty[8];        // a streamed tile has landed; its products are done
   uint64_t s_full[kS], s_empty[kS];  // S is finished; it has been read
-  uint64_t dz_full[2], dz_empty[2];  // dz is in shared memory; its products are done
+  uint64_t dz_full[4], dz_empty[4];  // dz is in shared memory; its products are done
   uint64_t kept_full, kept_empty;    // the kept tile has landed; its products are done
   uint64_t acc_full, acc_empty;      // a unit's sum is finished; it has been read
   uint64_t done;
   uint32_t tmem;
 };
 
+// KS: slabs of 64 columns.  Tiles of dz under way, streamed tiles, and S issued ahead of the tile whose dz is waited for.
 template <int KS>
-struct FusedRing {  // KS: slabs of 64 columns
+struct FusedRing {
   static constexpr int kTile = KS * kSlab;
-  static constexpr int kStages = KS == 1 ? 4 : 3;
-  static constexpr int kBytes = (1 + kStages) * kTile + 2 * kDz + tiles::kEpiWarps * tiles::kStageOut;
+  static constexpr int kDzs = KS == 1 ? 4 : 2, kStages = KS == 1 ? 5 : 4, kAhead = KS == 1 ? 2 : 1;
+  static constexpr int kBytes = (1 + kStages) * kTile + kDzs * kDz;
 };
 
 // A unit: a kept tile and streamed tiles [t0, t1).
@@ -73,7 +74,6 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   uint8_t* s_kept = base;
   uint8_t* s_ring = base + R::kTile;
   uint8_t* s_dz = s_ring + R::kStages * R::kTile;
-  uint8_t* s_out = s_dz + 2 * kDz;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   FusedWork work;
   work.live = *p.rows.count;
@@ -97,7 +97,7 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
       tc::mbar_init(&bar.s_full[i], 1);
       tc::mbar_init(&bar.s_empty[i], tiles::kEpiWarps / 2);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < R::kDzs; ++i) {
       tc::mbar_init(&bar.dz_full[i], tiles::kEpiWarps / 2);
       tc::mbar_init(&bar.dz_empty[i], 1);
     }
@@ -194,14 +194,12 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
       ok = tc::warp_wait(&bar.kept_full, kept_phase);
       kept_phase ^= 1;
       if (!ok) break;
-      make_s();
-      if (ok && x.t0 + 1 < x.t1) make_s();
-      for (int t = x.t0; t < x.t1 && ok; ++t) {
-        if (t + 2 < x.t1) make_s();
-        if (!ok) break;
-        const uint32_t b = n_sum & 1;
+      for (int t = x.t0; t <= x.t0 + R::kAhead && t < x.t1 && ok; ++t) make_s();
+      if (!ok) break;
+      for (int t = x.t0; t < x.t1; ++t) {
+        const uint32_t b = n_sum % R::kDzs;
         if (t == x.t0) ok = tc::warp_wait(&bar.acc_empty, acc_phase ^ 1);
-        ok = ok && tc::warp_wait(&bar.dz_full[b], n_sum >> 1 & 1);
+        ok = ok && tc::warp_wait(&bar.dz_full[b], n_sum / R::kDzs & 1);
         if (!ok) break;
         tc::fence_after();
         const uint32_t dz = dz_sum + b * (kDz >> 4), ring = ring_sum + d.stage * (R::kTile >> 4);
@@ -216,6 +214,8 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         __syncwarp();
         ++n_sum;
         d.next<R::kStages>();
+        if (t + R::kAhead + 1 < x.t1) make_s();
+        if (!ok) break;
       }
       if (!ok) break;
       if (one) {
@@ -231,9 +231,9 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     if (!ok && one) tc::latch_status(p.status, MT_ECUDA);
   } else if (warp >= 4) {
     const int quad = warp & 3, team = (warp - 4) >> 2;
-    uint8_t* stage = s_out + (warp - 4) * tiles::kStageOut;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    uint8_t* dz = s_dz + team * kDz + (quad * 32 + lane) * 128;  // the thread's row of dz: two halves of 64 entries
+    uint8_t* const dz_row = s_dz + (quad * 32 + lane) * 128;  // the thread's row of the first dz: two halves of 64 entries
+    uint8_t* const stage = s_dz + team * kDz + quad * 4096;   // (the sum goes out through the warp's own rows)
     const f32x2 s2 = both(p.scale2);
     uint32_t n = 0, acc_phase = 0;  // tiles so far
     bool ok = true;
@@ -241,7 +241,7 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     float4 k = make_float4(0.0f, 0.0f, 0.0f, 0.0f), k_next = k;
     int id_next = 0x7FFFFFFF;  // a row's only target
     // dz of 32 entries from their logits, four 16-byte pieces of a swizzled 128-byte row
-    auto columns = [&](const uint32_t (&v)[32], int c, int row, int v0, bool some) {
+    auto columns = [&](const uint32_t (&v)[32], uint8_t* dz, int c, int row, int v0, bool some) {
       float f[32];
       const f32x2 x2 = both(-k.x), y2 = both(k.y), z2 = both(-k.z);
 #pragma unroll
@@ -279,7 +279,7 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
           to.start(p.rows, row_at(x.kept), work.live, x.t0 * kT);
         }
         for (int t = first; t < x.t1; t += 2) {
-          const uint32_t of = n + (t - x.t0), b = of % kS, from = tmem + b * kT + lanes;
+          const uint32_t of = n + (t - x.t0), b = of % kS, d = of % R::kDzs, from = tmem + b * kT + lanes;
           const int row = row_at(VOCAB ? t : x.kept), v0 = (VOCAB ? x.kept : t) * kT;
           if (VOCAB) {
             k = k_next;
@@ -296,7 +296,7 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             }
           }
           const bool some = __any_sync(kFull, to.next < v0 + kT || row >= work.live) || v0 + kT > p.vocab;
-          ok = __all_sync(kFull, tc::mbar_wait(&bar.s_full[b], of / kS & 1) && tc::mbar_wait(&bar.dz_empty[team], (of >> 1 & 1) ^ 1));
+          ok = __all_sync(kFull, tc::mbar_wait(&bar.s_full[b], of / kS & 1) && tc::mbar_wait(&bar.dz_empty[d], (of / R::kDzs & 1) ^ 1));
           if (!ok) break;
           tc::fence_after();
           uint32_t v[2][32];
@@ -311,11 +311,11 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
               __syncwarp();
               if (lane == 0) tc::mbar_arrive(&bar.s_empty[b]);
             }
-            columns(v[c >> 5 & 1], c, row, v0, some);
+            columns(v[c >> 5 & 1], dz_row + d * kDz, c, row, v0, some);
           }
           tc::fence_async_proxy();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&bar.dz_full[team]);
+          if (lane == 0) tc::mbar_arrive(&bar.dz_full[d]);
         }
         if (!ok) break;
         n += x.t1 - x.t0;
