@@ -14,8 +14,8 @@
 //   dx += dz W or dW += dz^T x with the same tile of dz, read along its rows or
 //   across them, and the same tile of W or x that made S, read across.
 //
-// The products of the next tiles are issued before those that wait for this tile's
-// dz, so the tensor core works while the warps do; two teams of four warps take
+// One warp issues the products of S, as far ahead as there is room, another those
+// of the sums as their dz comes, so neither waits for what the other waits for; two teams of four warps take
 // every other tile, so that one's loads and waits overlap the other's arithmetic.
 #include "mt_tiles.cuh"
 #include "mt_vocab.cuh"
@@ -36,15 +36,15 @@ struct FusedBarriers {
   uint64_t dz_full[4], dz_empty[4];  // dz is in shared memory; its products are done
   uint64_t kept_full, kept_empty;    // the kept tile has landed; its products are done
   uint64_t acc_full, acc_empty;      // a unit's sum is finished; it has been read
-  uint64_t done;
+  uint64_t s_done, done;             // every product issued is done
   uint32_t tmem;
 };
 
-// KS: slabs of 64 columns.  Tiles of dz under way, streamed tiles, and S issued ahead of the tile whose dz is waited for.
+// KS: slabs of 64 columns.  Tiles of dz under way, and streamed tiles.
 template <int KS>
 struct FusedRing {
   static constexpr int kTile = KS * kSlab;
-  static constexpr int kDzs = KS == 1 ? 4 : 2, kStages = KS == 1 ? 5 : 4, kAhead = KS == 1 ? 2 : 1;
+  static constexpr int kDzs = KS == 1 ? 4 : 2, kStages = KS == 1 ? 5 : 4;
   static constexpr int kBytes = (1 + kStages) * kTile + kDzs * kDz;
 };
 
@@ -105,6 +105,7 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     tc::mbar_init(&bar.kept_empty, 1);
     tc::mbar_init(&bar.acc_full, 1);
     tc::mbar_init(&bar.acc_empty, tiles::kEpiWarps);
+    tc::mbar_init(&bar.s_done, 1);
     tc::mbar_init(&bar.done, 1);
     tc::mbar_init_fence();
   }
@@ -158,64 +159,74 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
       if (any) tc::mbar_wait(&bar.kept_full, kept_phase ^ 1);
     }
   } else if (warp == 1) {
-    constexpr uint32_t instr_s = tc::instr_bf16(kT, kT, false, false), instr_sum = tc::instr_bf16(kT, KS * 64, VOCAB, true);
+    // S: as far ahead as there is room
+    constexpr uint32_t instr = tc::instr_bf16(kT, kT, false, false);
     const bool one = tc::elect_one();
-    // descriptors' low words: rows along the contraction (S, and dz for dx), rows across it (the sums' others)
-    const uint32_t kept_s = tc::desc_low(tc::smem_addr(s_kept), 16), ring_s = tc::desc_low(tc::smem_addr(s_ring), 16);
-    const uint32_t ring_sum = tc::desc_low(tc::smem_addr(s_ring), kSlab), dz_sum = tc::desc_low(tc::smem_addr(s_dz), VOCAB ? kSlab : 16);
-    tc::Slot s, d;   // the streamed tile of the next S; of the next sum
-    uint32_t b_s = 0, phase_s = 0, n_sum = 0, kept_phase = 0, acc_phase = 0;
+    const uint32_t kept = tc::desc_low(tc::smem_addr(s_kept), 16), ring = tc::desc_low(tc::smem_addr(s_ring), 16);
+    tc::Slot s;
+    uint32_t b = 0, phase = 0, kept_phase = 0;
     bool ok = true;
-    // S of the next tile
-    auto make_s = [&]() {
-      ok = tc::warp_wait(&bar.s_empty[b_s], phase_s ^ 1) && tc::warp_wait(&bar.full[s.stage], s.phase);
-      if (!ok) return;
-      tc::fence_after();
-      const uint32_t at = ring_s + s.stage * (R::kTile >> 4);
-      const uint32_t ax = VOCAB ? at : kept_s, aw = VOCAB ? kept_s : at;
-      if (one) {
-#pragma unroll
-        for (int i = 0; i < KS * 4; ++i) {
-          const uint32_t o = ((i >> 2) * kSlab + (i & 3) * 32) >> 4;
-          tc::mma_low<1>(tmem + b_s * kT, ax + o, aw + o, instr_s, i > 0);
-        }
-        tc::mma_commit<1>(&bar.s_full[b_s]);
-      }
-      __syncwarp();
-      if (++b_s == kS) {
-        b_s = 0;
-        phase_s ^= 1;
-      }
-      s.next<R::kStages>();
-    };
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const FusedUnit x = work.unit(u);
       if (x.t0 == x.t1) continue;
       ok = tc::warp_wait(&bar.kept_full, kept_phase);
       kept_phase ^= 1;
-      if (!ok) break;
-      for (int t = x.t0; t <= x.t0 + R::kAhead && t < x.t1 && ok; ++t) make_s();
-      if (!ok) break;
-      for (int t = x.t0; t < x.t1; ++t) {
-        const uint32_t b = n_sum % R::kDzs;
-        if (t == x.t0) ok = tc::warp_wait(&bar.acc_empty, acc_phase ^ 1);
-        ok = ok && tc::warp_wait(&bar.dz_full[b], n_sum / R::kDzs & 1);
+      for (int t = x.t0; t < x.t1 && ok; ++t) {
+        ok = tc::warp_wait(&bar.s_empty[b], phase ^ 1) && tc::warp_wait(&bar.full[s.stage], s.phase);
         if (!ok) break;
         tc::fence_after();
-        const uint32_t dz = dz_sum + b * (kDz >> 4), ring = ring_sum + d.stage * (R::kTile >> 4);
+        const uint32_t at = ring + s.stage * (R::kTile >> 4);
+        const uint32_t ax = VOCAB ? at : kept, aw = VOCAB ? kept : at;
+        if (one) {
+#pragma unroll
+          for (int i = 0; i < KS * 4; ++i) {
+            const uint32_t o = ((i >> 2) * kSlab + (i & 3) * 32) >> 4;
+            tc::mma_low<1>(tmem + b * kT, ax + o, aw + o, instr, i > 0);
+          }
+          tc::mma_commit<1>(&bar.s_full[b]);
+        }
+        __syncwarp();
+        if (++b == kS) {
+          b = 0;
+          phase ^= 1;
+        }
+        s.next<R::kStages>();
+      }
+    }
+    if (one) tc::mma_commit<1>(&bar.s_done);  // tensor memory is freed only when no product writes it, also after a wait ran out
+    __syncwarp();
+    ok = tc::mbar_wait(&bar.s_done, 0) && ok;
+    if (!ok && one) tc::latch_status(p.status, MT_ECUDA);
+  } else if (warp == 2) {
+    // the sums.  A tile's S is done before its dz is, so what this warp signals of a sum holds for its S too.
+    constexpr uint32_t instr = tc::instr_bf16(kT, KS * 64, VOCAB, true);
+    const bool one = tc::elect_one();
+    const uint32_t ring = tc::desc_low(tc::smem_addr(s_ring), kSlab), dz = tc::desc_low(tc::smem_addr(s_dz), VOCAB ? kSlab : 16);
+    tc::Slot s;
+    uint32_t n = 0, acc_phase = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const FusedUnit x = work.unit(u);
+      if (x.t0 == x.t1) continue;
+      ok = tc::warp_wait(&bar.acc_empty, acc_phase ^ 1);
+      acc_phase ^= 1;
+      for (int t = x.t0; t < x.t1 && ok; ++t) {
+        const uint32_t b = n % R::kDzs;
+        ok = tc::warp_wait(&bar.dz_full[b], n / R::kDzs & 1);
+        if (!ok) break;
+        tc::fence_after();
+        const uint32_t from = dz + b * (kDz >> 4), with = ring + s.stage * (R::kTile >> 4);
         if (one) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            tc::mma_low<1>(tmem + kAccAt, dz + ((VOCAB ? i * 2048 : (i >> 2) * kSlab + (i & 3) * 32) >> 4), ring + (i * 2048 >> 4), instr_sum,
+            tc::mma_low<1>(tmem + kAccAt, from + ((VOCAB ? i * 2048 : (i >> 2) * kSlab + (i & 3) * 32) >> 4), with + (i * 2048 >> 4), instr,
                            t > x.t0 || i > 0);
-          tc::mma_commit<1>(&bar.empty[d.stage]);
+          tc::mma_commit<1>(&bar.empty[s.stage]);
           tc::mma_commit<1>(&bar.dz_empty[b]);
         }
         __syncwarp();
-        ++n_sum;
-        d.next<R::kStages>();
-        if (t + R::kAhead + 1 < x.t1) make_s();
-        if (!ok) break;
+        ++n;
+        s.next<R::kStages>();
       }
       if (!ok) break;
       if (one) {
@@ -223,9 +234,8 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         tc::mma_commit<1>(&bar.acc_full);
       }
       __syncwarp();
-      acc_phase ^= 1;
     }
-    if (one) tc::mma_commit<1>(&bar.done);  // tensor memory is freed only when no product writes it, also after a wait ran out
+    if (one) tc::mma_commit<1>(&bar.done);
     __syncwarp();
     ok = tc::mbar_wait(&bar.done, 0) && ok;
     if (!ok && one) tc::latch_status(p.status, MT_ECUDA);
