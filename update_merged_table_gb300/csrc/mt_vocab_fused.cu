@@ -15,8 +15,8 @@
 //   across them, and the same tile of W or x that made S, read across.
 //
 // One warp issues the products of S, as far ahead as there is room, another those
-// of the sums as their dz comes, so neither waits for what the other waits for; two teams of four warps take
-// every other tile, so that one's loads and waits overlap the other's arithmetic.
+// of the sums as their dz comes, so neither waits for what the other waits for; teams of four warps take the
+// tiles in turn, so that one's loads and waits overlap the others' arithmetic.
 #include "mt_tiles.cuh"
 #include "mt_vocab.cuh"
 #include "mt_vocab_rows.cuh"
@@ -33,18 +33,19 @@ constexpr int kAccAt = kS * kT;          // tensor memory: these, then the sum
 struct FusedBarriers {
   uint64_t full[8], empty[8];        // a streamed tile has landed; its products are done
   uint64_t s_full[kS], s_empty[kS];  // S is finished; it has been read
-  uint64_t dz_full[4], dz_empty[4];  // dz is in shared memory; its products are done
+  uint64_t dz_full[3], dz_empty[3];  // dz is in shared memory; its products are done
   uint64_t kept_full, kept_empty;    // the kept tile has landed; its products are done
   uint64_t acc_full, acc_empty;      // a unit's sum is finished; it has been read
   uint64_t s_done, done;             // every product issued is done
   uint32_t tmem;
 };
 
-// KS: slabs of 64 columns.  Tiles of dz under way, and streamed tiles.
+// KS: slabs of 64 columns.  Teams of four warps, each with a tile of dz of its own, and streamed tiles.
 template <int KS>
 struct FusedRing {
   static constexpr int kTile = KS * kSlab;
-  static constexpr int kDzs = KS == 1 ? 4 : 2, kStages = KS == 1 ? 5 : 4;
+  static constexpr int kTeams = KS == 1 ? 3 : 2, kThreads = (4 + kTeams * 4) * 32;
+  static constexpr int kDzs = kTeams, kStages = KS == 1 ? 6 : 4;
   static constexpr int kBytes = (1 + kStages) * kTile + kDzs * kDz;
 };
 
@@ -65,7 +66,7 @@ struct FusedWork {
 };
 
 template <int KS, bool VOCAB>
-__global__ void __launch_bounds__(tiles::kThreadsT, 1)
+__global__ void __launch_bounds__(FusedRing<KS>::kThreads, 1)
 k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ FusedParams p) {
   using R = FusedRing<KS>;
   extern __shared__ uint8_t s_raw[];
@@ -95,16 +96,16 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     }
     for (int i = 0; i < kS; ++i) {
       tc::mbar_init(&bar.s_full[i], 1);
-      tc::mbar_init(&bar.s_empty[i], tiles::kEpiWarps / 2);
+      tc::mbar_init(&bar.s_empty[i], 4);
     }
     for (int i = 0; i < R::kDzs; ++i) {
-      tc::mbar_init(&bar.dz_full[i], tiles::kEpiWarps / 2);
+      tc::mbar_init(&bar.dz_full[i], 4);
       tc::mbar_init(&bar.dz_empty[i], 1);
     }
     tc::mbar_init(&bar.kept_full, 1);
     tc::mbar_init(&bar.kept_empty, 1);
     tc::mbar_init(&bar.acc_full, 1);
-    tc::mbar_init(&bar.acc_empty, tiles::kEpiWarps);
+    tc::mbar_init(&bar.acc_empty, 8);
     tc::mbar_init(&bar.s_done, 1);
     tc::mbar_init(&bar.done, 1);
     tc::mbar_init_fence();
@@ -242,8 +243,8 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   } else if (warp >= 4) {
     const int quad = warp & 3, team = (warp - 4) >> 2;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    uint8_t* const dz_row = s_dz + (quad * 32 + lane) * 128;  // the thread's row of the first dz: two halves of 64 entries
-    uint8_t* const stage = s_dz + team * kDz + quad * 4096;   // (the sum goes out through the warp's own rows)
+    uint8_t* const stage = s_dz + team * kDz + quad * 4096;  // the warp's rows of dz; the sum goes out through them
+    uint8_t* const dz = stage + lane * 128;                  // the thread's row: two halves of 64 entries
     const f32x2 s2 = both(p.scale2);
     uint32_t n = 0, acc_phase = 0;  // tiles so far
     bool ok = true;
@@ -251,7 +252,7 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     float4 k = make_float4(0.0f, 0.0f, 0.0f, 0.0f), k_next = k;
     int id_next = 0x7FFFFFFF;  // a row's only target
     // dz of 32 entries from their logits, four 16-byte pieces of a swizzled 128-byte row
-    auto columns = [&](const uint32_t (&v)[32], uint8_t* dz, int c, int row, int v0, bool some) {
+    auto columns = [&](const uint32_t (&v)[32], int c, int row, int v0, bool some) {
       float f[32];
       const f32x2 x2 = both(-k.x), y2 = both(k.y), z2 = both(-k.z);
 #pragma unroll
@@ -280,7 +281,7 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         auto row_at = [&](int tile) { return tile * kT + quad * 32 + lane; };
         auto id_at = [&](int row) { return p.rows.top == 1 && row < work.live ? __ldg(p.rows.ids + row) : 0x7FFFFFFF; };
         auto coef_at = [&](int row) { return row < work.live ? __ldg(p.coef + row) : make_float4(0.0f, 0.0f, 0.0f, 0.0f); };
-        const int first = x.t0 + ((n & 1) != team);  // this team's first tile
+        const int first = x.t0 + (team + R::kTeams - (int)(n % R::kTeams)) % R::kTeams;  // this team's first tile
         if (VOCAB) {
           k_next = coef_at(row_at(first));
           id_next = id_at(row_at(first));
@@ -288,8 +289,8 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
           k = coef_at(row_at(x.kept));
           to.start(p.rows, row_at(x.kept), work.live, x.t0 * kT);
         }
-        for (int t = first; t < x.t1; t += 2) {
-          const uint32_t of = n + (t - x.t0), b = of % kS, d = of % R::kDzs, from = tmem + b * kT + lanes;
+        for (int t = first; t < x.t1; t += R::kTeams) {
+          const uint32_t of = n + (t - x.t0), b = of % kS, from = tmem + b * kT + lanes;
           const int row = row_at(VOCAB ? t : x.kept), v0 = (VOCAB ? x.kept : t) * kT;
           if (VOCAB) {
             k = k_next;
@@ -300,32 +301,36 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             } else {
               to.start(p.rows, row, work.live, v0);
             }
-            if (t + 2 < x.t1) {
-              k_next = coef_at(row_at(t + 2));
-              id_next = id_at(row_at(t + 2));
+            if (t + R::kTeams < x.t1) {
+              k_next = coef_at(row_at(t + R::kTeams));
+              id_next = id_at(row_at(t + R::kTeams));
             }
           }
           const bool some = __any_sync(kFull, to.next < v0 + kT || row >= work.live) || v0 + kT > p.vocab;
-          ok = __all_sync(kFull, tc::mbar_wait(&bar.s_full[b], of / kS & 1) && tc::mbar_wait(&bar.dz_empty[d], (of / R::kDzs & 1) ^ 1));
+          ok = __all_sync(kFull, tc::mbar_wait(&bar.s_full[b], of / kS & 1) && tc::mbar_wait(&bar.dz_empty[team], (of / R::kTeams & 1) ^ 1));
           if (!ok) break;
           tc::fence_after();
-          uint32_t v[2][32];
-          tc::tmem_load32(from, v[0]);
+          // two teams: the next columns' load is on its way meanwhile (three have no registers for it, and overlap more)
+          constexpr bool kTwo = R::kTeams == 2;
+          uint32_t v[kTwo ? 2 : 1][32];
+          if (kTwo) tc::tmem_load32(from, v[0]);
 #pragma unroll
           for (int c = 0; c < kT; c += 32) {
-            tc::tmem_load_wait(v[c >> 5 & 1]);
-            if (c + 32 < kT) {
-              tc::tmem_load32(from + c + 32, v[(c >> 5 & 1) ^ 1]);
-            } else {
+            uint32_t (&now)[32] = v[kTwo ? c >> 5 & 1 : 0];
+            if (!kTwo) tc::tmem_load32(from + c, now);
+            tc::tmem_load_wait(now);
+            if (c + 32 == kT) {
               tc::fence_before();
               __syncwarp();
               if (lane == 0) tc::mbar_arrive(&bar.s_empty[b]);
+            } else if (kTwo) {
+              tc::tmem_load32(from + c + 32, v[(c >> 5 & 1) ^ 1]);
             }
-            columns(v[c >> 5 & 1], dz_row + d * kDz, c, row, v0, some);
+            columns(now, c, row, v0, some);
           }
           tc::fence_async_proxy();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&bar.dz_full[d]);
+          if (lane == 0) tc::mbar_arrive(&bar.dz_full[team]);
         }
         if (!ok) break;
         n += x.t1 - x.t0;
@@ -334,7 +339,8 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         acc_phase ^= 1;
         tc::fence_after();
       }
-      // the unit's sum: 32 columns at a time
+      // the unit's sum, by the first two teams: 32 columns at a time
+      if (team >= 2) continue;
       const int c0 = team * KS * 32;  // half of the columns each team
       const int rows = min(32, (VOCAB ? p.vocab : work.live) - (x.kept * kT + quad * 32));
       const long long r0 = x.kept * kT + quad * 32;
@@ -380,7 +386,7 @@ cudaError_t launch(const char* name, const CUtensorMap& x, const CUtensorMap& w,
   if (e != cudaSuccess) return e;
   const int blocks = sm_count();
   MT_LAUNCH(name, s);
-  k_vocab_fused<KS, VOCAB><<<(int)(units < blocks ? (units > 0 ? units : 1) : blocks), tiles::kThreadsT, bytes, s>>>(x, w, p);
+  k_vocab_fused<KS, VOCAB><<<(int)(units < blocks ? (units > 0 ? units : 1) : blocks), FusedRing<KS>::kThreads, bytes, s>>>(x, w, p);
   return cudaGetLastError();
 }
 
