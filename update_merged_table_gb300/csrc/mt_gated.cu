@@ -73,7 +73,7 @@ struct GatedParams {
   int gate;
   int steps;  // of the contraction, per pass
   int passes, a_part, b_part, b_second, promote;
-  bool wide, wide_dh;
+  int reach, reach_dh;  // of out's rows and dh's
 };
 
 // T: the rows' type.  BACKWARD: dt instead of h.
@@ -139,7 +139,7 @@ struct Gated {
       acc.load(128 + c, u);
       float d[BACKWARD ? 32 : 1];
       if constexpr (BACKWARD) {
-        if (col < p.out_dim) tiles::load_rows<T>(stage, lane, d, static_cast<const T*>(p.dh), p.lddh, r0, rows, col, p.out_dim, p.wide_dh);
+        if (col < p.out_dim) tiles::load_rows<T>(stage, lane, d, static_cast<const T*>(p.dh), p.lddh, r0, rows, col, p.out_dim, p.reach_dh);
       }
       tc::tmem_load_wait(y);
       tc::tmem_loaded(u);
@@ -148,7 +148,7 @@ struct Gated {
       if constexpr (!BACKWARD) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(y[j]) * gate_of<T>(p.gate, __uint_as_float(u[j]));
-        tiles::store32<T>(stage, lane, f, out, p.ldo, r0, rows, col, p.out_dim, p.wide);
+        tiles::store32<T>(stage, lane, f, out, p.ldo, r0, rows, col, p.out_dim, p.reach);
       } else {
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
@@ -156,10 +156,10 @@ struct Gated {
           u[j] = __float_as_uint(d[j] * __uint_as_float(y[j]) * a.y);
           f[j] = d[j] * a.x;
         }
-        tiles::store32<T>(stage, lane, f, out, p.ldo, r0, rows, col, p.out_dim, p.wide);
+        tiles::store32<T>(stage, lane, f, out, p.ldo, r0, rows, col, p.out_dim, p.reach);
 #pragma unroll
         for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(u[j]);
-        tiles::store32<T>(stage, lane, f, out + p.u_col, p.ldo, r0, rows, col, p.out_dim, p.wide);
+        tiles::store32<T>(stage, lane, f, out + p.u_col, p.ldo, r0, rows, col, p.out_dim, p.reach);
       }
     }
   }
@@ -284,7 +284,7 @@ int mt_gated_linear_forward(const mt_gated_linear* c, void* h, int64_t ldh, void
   GatedParams p{};
   p.out = h;
   p.ldo = ldh;
-  p.wide = is_aligned(h, 16) && ldh * elem_bytes(c->dtype) % 16 == 0 && c->out_dim * elem_bytes(c->dtype) % 16 == 0;
+  p.reach = tiles::reach_of(h, ldh, c->out_dim, elem_bytes(c->dtype));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* w = static_cast<char*>(ws);
   const cudaError_t e = c->dtype == MT_F32 ? launch_product<float, false>(*c, l, p, w, s) : launch_product<__nv_bfloat16, false>(*c, l, p, w, s);
@@ -327,8 +327,8 @@ int mt_gated_linear_backward(const mt_gated_linear* c, const void* dh, int64_t l
   p.out = base + l.dt;
   p.ldo = 2 * l.m;
   p.u_col = (int)l.m;
-  p.wide = l.m * e % 16 == 0;
-  p.wide_dh = is_aligned(dh, 16) && (c->n <= 1 || lddh * e % 16 == 0) && c->out_dim * e % 16 == 0;
+  p.reach = tiles::reach_of(p.out, l.m, l.m, e);  // (dt's own rows: no column behind the last is the user's)
+  p.reach_dh = tiles::reach_of(dh, c->n <= 1 ? c->out_dim : lddh, c->out_dim, e);
   cudaError_t err = cudaSuccess;
   err = c->dtype == MT_F32 ? launch_product<float, true>(*c, l, p, base, s) : launch_product<__nv_bfloat16, true>(*c, l, p, base, s);
   const int32_t k = padded ? (int32_t)l.k : c->in_dim, m2 = (int32_t)(2 * l.m);

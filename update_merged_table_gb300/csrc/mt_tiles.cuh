@@ -359,19 +359,36 @@ k_tiles(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
 
 __device__ __forceinline__ uint32_t piece_at(int row, int c) { return (uint32_t)(row * 64 + ((c ^ ((row >> 1) & 3)) << 4)); }
 
+// How rows may be reached: by elements, in 16-byte pieces turned in shared memory, or in 32-byte sectors as they are.
+enum Reach { kElements = 0, kPieces = 1, kSectors = 2 };
+inline int reach_of(const void* data, int64_t ld, int64_t columns, size_t bytes) {
+  const auto on = [&](size_t a) { return is_aligned(data, a) && ld * bytes % a == 0 && columns * bytes % a == 0; };
+  return on(32) ? kSectors : on(16) ? kPieces : kElements;
+}
+__device__ __forceinline__ void store_sector(void* to, const uint32_t* w);
+
 // Stores 64 bytes of each lane's row (w: 16 words; element j of the row is column col + j): rows [0, rows) of C from r0 on,
-// columns below J.  WIDE: C's rows lie on 16 bytes and J ends on them.
+// columns below J.  In sectors the shared memory's bandwidth stays with the products' operands (8192 rows x 20,000 entries
+// x 512: TODO).
 template <typename T>
 __device__ __forceinline__ void store_rows(uint8_t* stage, int lane, const uint32_t (&w)[16], T* C, size_t ldc, long long r0,
-                                           int rows, int col, int J, bool wide) {
+                                           int rows, int col, int J, int reach) {
   constexpr int kPer = 64 / sizeof(T);  // columns
   if (col >= J) return;
+  if (reach == kSectors) {
+    T* to = C + (size_t)(r0 + lane) * ldc + col;
+    if (lane < rows) {
+      store_sector(to, w);
+      if (col + kPer / 2 < J) store_sector(to + kPer / 2, w + 8);
+    }
+    return;
+  }
   __syncwarp();
 #pragma unroll
   for (int c = 0; c < 4; ++c)
     *reinterpret_cast<uint4*>(stage + piece_at(lane, c)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
   __syncwarp();
-  if (wide) {
+  if (reach == kPieces) {
     const int c = lane & 3, at = col + c * (16 / (int)sizeof(T));
     T* to = C + (size_t)r0 * ldc + at;
 #pragma unroll
@@ -388,11 +405,18 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, int lane, const uint3
   }
 }
 
+// 32 bytes of a lane's row at once (sm_100 and later): a whole sector of global memory, so rows need no turning.
+__device__ __forceinline__ void store_sector(void* to, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+               "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // Loads 32 columns of each lane's row as fp32 (zeros outside): the reverse.
 template <typename T>
 __device__ __forceinline__ void load_rows(uint8_t* stage, int lane, float (&f)[32], const T* C, size_t ldc, long long r0, int rows,
-                                          int col, int J, bool wide) {
-  if (wide) {
+                                          int col, int J, int reach) {
+  if (reach != kElements) {
     const T* p = C + (size_t)(r0 + lane) * ldc + col;
     constexpr int kPer = 16 / sizeof(T);
 #pragma unroll
@@ -438,17 +462,17 @@ __device__ __forceinline__ void narrow32(const float (&f)[32], uint32_t (&w)[16]
 // Stores 32 fp32 columns of each lane's row as T.
 template <typename T>
 __device__ __forceinline__ void store32(uint8_t* stage, int lane, const float (&f)[32], T* C, size_t ldc, long long r0, int rows,
-                                        int col, int J, bool wide) {
+                                        int col, int J, int reach) {
   uint32_t w[16];
   if constexpr (sizeof(T) == 2) {
     narrow32(f, w);
-    store_rows<T>(stage, lane, w, C, ldc, r0, rows, col, J, wide);
+    store_rows<T>(stage, lane, w, C, ldc, r0, rows, col, J, reach);
   } else {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
       for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(f[h * 16 + j]);
-      store_rows<T>(stage, lane, w, C, ldc, r0, rows, col + h * 16, J, wide);
+      store_rows<T>(stage, lane, w, C, ldc, r0, rows, col + h * 16, J, reach);
     }
   }
 }

@@ -16,7 +16,7 @@
 //   k_vocab_dx_sum, k_vocab_dw_sum  partial products joined, rounded, put in place
 #include <algorithm>
 
-#include "mt_tc.cuh"
+#include "mt_tiles.cuh"
 #include "mt_vocab.cuh"
 
 namespace mt {
@@ -248,10 +248,10 @@ __global__ void __launch_bounds__(256) k_vocab_loss(const VocabLoss p) {
   }
 }
 
-// dx in its rows' places from the runs' partial products; zeros for rows that take no part.  FOUR: four columns a thread.
-// cut: NULL, or where only the live rows from cut[0] on come in several runs, cut[1] of them.
+// dx in its rows' places; zeros for rows that take no part.  The live rows from cut[0] on come in cut[1] runs.  FOUR: four
+// columns a thread.
 template <typename T, bool FOUR>
-__global__ void __launch_bounds__(256) k_vocab_dx_sum(const float* part, size_t stride, int splits, const int* pos, long long n, int d, T* dx,
+__global__ void __launch_bounds__(256) k_vocab_dx_sum(const float* part, size_t stride, const int* pos, long long n, int d, T* dx,
                                                       int64_t lddx, const int* cut) {
   constexpr int kPer = FOUR ? 4 : 1;
   const int per_row = d / kPer;
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(256) k_vocab_dx_sum(const float* part, size_t 
     const long long row = i / per_row;
     const int j = (int)(i - row * per_row) * kPer, at = pos[row];
     const float* from = part + (size_t)at * d + j;
-    const int runs = cut == nullptr ? splits : at >= cut[0] ? cut[1] : 1;
+    const int runs = at >= cut[0] ? cut[1] : 1;
     T* to = dx + row * lddx + j;
     if constexpr (FOUR) {
       float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -281,28 +281,60 @@ __global__ void __launch_bounds__(256) k_vocab_dx_sum(const float* part, size_t 
     }
   }
 }
-template <typename T>
-__global__ void __launch_bounds__(256) k_vocab_dw_sum(const float* part, size_t stride, int splits, long long values, int d, T* dw, const int* cut) {
-  if (cut != nullptr) splits = cut[1];
+// The rows of dW from cut[0] on, which came in cut[1] runs.  FOUR: four values a thread.
+template <typename T, bool FOUR>
+__global__ void __launch_bounds__(256) k_vocab_dw_sum(const float* part, size_t stride, const int* cut, long long rows, int d, T* dw) {
+  constexpr int kPer = FOUR ? 4 : 1;
+  const int runs = cut[1];
+  const size_t first = (size_t)cut[0] * d;
+  const long long values = (rows * d - (long long)first) / kPer;
   for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < values; i += (long long)gridDim.x * blockDim.x) {
-    float s = 0.0f;
-    for (int k = 0; k < splits; ++k) s += part[(size_t)k * stride * d + i];
-    dw[i] = from_f<T>(s);
+    if constexpr (FOUR) {
+      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+      for (int k = 0; k < runs; ++k) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(part + (size_t)k * stride * d) + i);
+        s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+      }
+      if constexpr (sizeof(T) == 4) reinterpret_cast<float4*>(dw + first)[i] = s;
+      else reinterpret_cast<uint2*>(dw + first)[i] = make_uint2(bf16x2_of(s.x, s.y), bf16x2_of(s.z, s.w));
+    } else {
+      float s = 0.0f;
+      for (int k = 0; k < runs; ++k) s += part[(size_t)k * stride * d + i];
+      dw[first + i] = from_f<T>(s);
+    }
   }
+}
+
+// `rows` rows of dW, at most `tail` of them in runs.
+cudaError_t launch_dw_sum(const float* part, size_t stride, const int* cut, long long rows, long long tail, int d, int dtype, void* dw,
+                          cudaStream_t s) {
+  const bool four = d % 4 == 0 && is_aligned(dw, 4 * elem_bytes(dtype));
+  const int grid = grid_for(tail * d / (four ? 4 : 1), 256, 8);
+  MT_LAUNCH("k_vocab_dw_sum", s);
+  if (dtype == MT_F32) {
+    if (four) k_vocab_dw_sum<float, true><<<grid, 256, 0, s>>>(part, stride, cut, rows, d, static_cast<float*>(dw));
+    else k_vocab_dw_sum<float, false><<<grid, 256, 0, s>>>(part, stride, cut, rows, d, static_cast<float*>(dw));
+  } else {
+    if (four) k_vocab_dw_sum<__nv_bfloat16, true><<<grid, 256, 0, s>>>(part, stride, cut, rows, d, static_cast<__nv_bfloat16*>(dw));
+    else k_vocab_dw_sum<__nv_bfloat16, false><<<grid, 256, 0, s>>>(part, stride, cut, rows, d, static_cast<__nv_bfloat16*>(dw));
+  }
+  return cudaGetLastError();
 }
 
 // ---- host --------------------------------------------------------------------------------------
 
-constexpr size_t kPieceBytes = (size_t)512 << 20;  // of dz at a time
+constexpr size_t kPieceBytes = (size_t)1 << 30;  // of dz at a time
 
 struct Layout {
   int parts, dp, wp;          // parts of an operand; columns of a part of x and of W
   bool copy_w, fused;         // fused: the gradients without dz in memory
-  int whole, runs_dx, runs_dw;  // fused: dW's tiles that need no partial products; room for runs of the others
+  int whole;                  // fused: dW's tiles that need no partial products
+  int runs_dx, runs_dw;       // room for runs
   int64_t rows;               // n in multiples of 256
   int top, max_chunks;
   int64_t piece;              // entries of the vocabulary at a time, a multiple of 256
-  int dx_splits, dw_splits;
+  int64_t dw_rows;            // rows of dW's partial products
   size_t mask, live, chunks, cut, pos, xs, ids, share, entropy, w, picked, part, sum_z, coef, dz, dx, dw, total;
 };
 
@@ -327,6 +359,7 @@ Layout layout_of(const mt_vocab_loss& c, bool backward) {
   l.mask = take((size_t)tiles_of(c.n, 32) * 4);
   l.live = take(4);
   l.chunks = take(4);
+  l.cut = take(16);
   l.pos = take((size_t)c.n * 4);
   l.xs = take((size_t)l.rows * l.parts * l.dp * 2);
   l.ids = take((size_t)c.n * l.top * 4);
@@ -343,7 +376,6 @@ Layout layout_of(const mt_vocab_loss& c, bool backward) {
     // room for as many runs as give every block eight units, of the tiles that are cut at all
     l.fused = true;
     const int64_t rt = tiles_of(c.n, kFusedTile), vt = tiles_of(c.vocab, kFusedTile);
-    l.cut = take(16);
     l.coef = take((size_t)c.n * 16);
     l.runs_dx = (int)std::min<int64_t>(vt, rt < sms ? 8 * sms / rt + 1 : 4);
     l.dx = take((size_t)l.runs_dx * l.rows * c.dim * 4);
@@ -359,11 +391,15 @@ Layout layout_of(const mt_vocab_loss& c, bool backward) {
     l.dz = take((size_t)l.rows * l.parts * l.piece * 2);
     const int bn = sum_width(c.dim, c.dtype == MT_F32);
     const int64_t ct = tiles_of(c.dim, bn);
-    // runs of the contraction: enough units of work for every SM, none shorter than 8 steps
-    l.dx_splits = (int)std::max<int64_t>(1, std::min<int64_t>(tiles_of(2 * sms, l.rows / 128 * ct), l.piece / 512));
-    l.dx = take((size_t)l.dx_splits * l.rows * c.dim * 4);
-    l.dw_splits = (int)std::max<int64_t>(1, std::min<int64_t>(sms / std::max<int64_t>(1, l.piece / 128 * ct), tiles_of(c.n, 512)));
-    if (l.dw_splits > 1) l.dw = take((size_t)l.dw_splits * l.piece * c.dim * 4);
+    // room for runs of the contraction: eight units a block, no run shorter than 8 steps, 256 MiB of dx
+    const int64_t rt = l.rows / 128;
+    l.runs_dx = (int)std::max<int64_t>(1, std::min({8 * sms / (rt * ct) + 1, l.piece / 512, (int64_t)((256 << 20) / ((size_t)l.rows * c.dim * 4))}));
+    l.dx = take((size_t)l.runs_dx * l.rows * c.dim * 4);
+    // dW: only of the tiles behind the whole rounds, fewer than there are blocks
+    const int64_t tail = std::min<int64_t>(l.piece / 128 * ct, sms + ct);
+    l.runs_dw = (int)std::max<int64_t>(1, std::min<int64_t>(8 * sms / tail + 1, tiles_of(c.n, 512)));
+    l.dw_rows = std::min<int64_t>(l.piece, tiles_of(tail, ct) * 256);
+    l.dw = take((size_t)l.runs_dw * l.dw_rows * c.dim * 4);
   }
   l.total = at;
   return l;
@@ -581,7 +617,8 @@ int mt_vocab_loss_backward(const mt_vocab_loss* c, const float* dloss, const flo
   const uint64_t xw = (uint64_t)l.parts * l.dp;
   const int bn = sum_width(c->dim, fp32);
   const int ct = (int)tiles_of(c->dim, bn);
-  const bool wide = c->dim * el % 16 == 0 && is_aligned(dw, 16);
+  const int reach = dw != nullptr ? tiles::reach_of(dw, c->dim, c->dim, el) : 0, reach_part = tiles::reach_of(base, c->dim, c->dim, 4);
+  int* cut = reinterpret_cast<int*>(base + l.cut);  // of dx, of dW
   if (l.fused && e == cudaSuccess) {
     FusedParams f{};
     f.status = c->status;
@@ -590,7 +627,8 @@ int mt_vocab_loss_backward(const mt_vocab_loss* c, const float* dloss, const flo
     f.columns = c->dim;
     f.scale2 = c->scale * kLog2e;
     f.coef = reinterpret_cast<float4*>(base + l.coef);
-    f.wide = wide;
+    f.reach = reach;
+    f.reach_part = reach_part;
     f.out = static_cast<__nv_bfloat16*>(dw);
     CUtensorMap a, b;
     if (!tc::encode_bf16(&a, 2, base + l.xs, xw, l.rows, xw, 1, 0, 64, kFusedTile)) return MT_ECUDA;
@@ -598,7 +636,7 @@ int mt_vocab_loss_backward(const mt_vocab_loss* c, const float* dloss, const flo
     const int64_t rt = tiles_of(c->n, kFusedTile), vt = tiles_of(c->vocab, kFusedTile);
     if (dx != nullptr) {
       f.max_chunks = l.runs_dx;
-      f.cut = reinterpret_cast<int*>(base + l.cut);
+      f.cut = cut;
       f.part = reinterpret_cast<float*>(base + l.dx);
       f.stride = l.rows;
       e = launch_fused(false, f, a, b, rt * l.runs_dx, s);
@@ -606,17 +644,12 @@ int mt_vocab_loss_backward(const mt_vocab_loss* c, const float* dloss, const flo
     if (dw != nullptr && e == cudaSuccess) {
       f.max_chunks = std::max(1, l.runs_dw);
       f.whole = l.whole;
-      f.cut = reinterpret_cast<int*>(base + l.cut) + 2;
+      f.cut = cut + 2;
       f.part = reinterpret_cast<float*>(base + l.dw);
       f.stride = (size_t)(vt - l.whole) * kFusedTile;
       e = launch_fused(true, f, a, b, l.whole + (vt - l.whole) * l.runs_dw, s);
-      const int64_t first = (int64_t)l.whole * kFusedTile;
-      const long long values = (c->vocab - first) * c->dim;
-      if (values > 0 && e == cudaSuccess) {
-        MT_LAUNCH("k_vocab_dw_sum", s);
-        k_vocab_dw_sum<__nv_bfloat16><<<grid_for(values, 256, 8), 256, 0, s>>>(f.part, f.stride, 0, values, c->dim, f.out + first * c->dim, f.cut);
-        e = cudaGetLastError();
-      }
+      const int64_t tail = c->vocab - (int64_t)l.whole * kFusedTile;
+      if (tail > 0 && e == cudaSuccess) e = launch_dw_sum(f.part, f.stride, f.cut, c->vocab, tail, c->dim, c->dtype, dw, s);
     }
   }
   for (int64_t v0 = 0; !l.fused && v0 < c->vocab && e == cudaSuccess; v0 += l.piece) {
@@ -645,47 +678,44 @@ int mt_vocab_loss_backward(const mt_vocab_loss* c, const float* dloss, const flo
     q.a_part = p.width;
     q.columns = c->dim;
     q.ctiles = ct;
+    q.reach = reach;
+    q.reach_part = reach_part;
     if (dx != nullptr && e == cudaSuccess) {
-      const bool pair = bn == 256 && pair_rows(c->n, (int64_t)ct * l.dx_splits, p.width / 64);
+      const bool pair = bn == 256 && pair_rows(c->n, (int64_t)ct * l.runs_dx, l.piece / 64);  // (the same for every piece)
       if (!tc::encode_bf16(&a, 2, base + l.dz, zw, l.rows, zw, 1, 0, 64, 128)) return MT_ECUDA;
       if (!tc::encode_bf16(&b, 2, wv, w.width, columns, w.ld, 1, 0, 64, 64)) return MT_ECUDA;
       q.b_part = l.wp;
       q.steps = p.width / 64;
-      q.splits = l.dx_splits;
+      q.usual = (int)(l.piece / 64);
+      q.max_runs = l.runs_dx;
+      q.cut = cut;
       q.part = reinterpret_cast<float*>(base + l.dx);
       q.stride = l.rows;
       q.add = v0 > 0;
       e = launch_rows_sum(q, fp32, a, b, tiles_of(c->n, pair ? 256 : 128), pair, s);
     }
     if (dw != nullptr && e == cudaSuccess) {
-      const bool pair = bn == 256 && pair_rows(columns, (int64_t)ct * l.dw_splits, tiles_of(c->n, 64));
+      const bool pair = bn == 256 && pair_rows(columns, (int64_t)ct * l.runs_dw, tiles_of(c->n, 64));
       if (!tc::encode_bf16(&a, 2, base + l.dz, zw, l.rows, zw, 1, 0, 64, 64)) return MT_ECUDA;
       if (!tc::encode_bf16(&b, 2, base + l.xs, xw, l.rows, xw, 1, 0, 64, 64)) return MT_ECUDA;
       q.b_part = l.dp;
       q.rows = (int)columns;
-      q.splits = l.dw_splits;
-      q.part = l.dw_splits > 1 ? reinterpret_cast<float*>(base + l.dw) : nullptr;
-      q.stride = l.piece;
+      q.max_runs = l.runs_dw;
+      q.cut = cut + 2;
+      q.part = reinterpret_cast<float*>(base + l.dw);
+      q.stride = l.dw_rows;
       q.add = false;
-      q.wide = wide;
       q.out = static_cast<char*>(dw) + (size_t)v0 * c->dim * el;
       e = launch_vocab_sum(q, fp32, a, b, tiles_of(columns, pair ? 256 : 128), pair, s);
-      if (e == cudaSuccess && l.dw_splits > 1) {
-        const long long values = columns * c->dim;
-        MT_LAUNCH("k_vocab_dw_sum", s);
-        if (fp32) k_vocab_dw_sum<float><<<grid_for(values, 256, 8), 256, 0, s>>>(q.part, q.stride, q.splits, values, c->dim, static_cast<float*>(q.out), nullptr);
-        else k_vocab_dw_sum<__nv_bfloat16><<<grid_for(values, 256, 8), 256, 0, s>>>(q.part, q.stride, q.splits, values, c->dim, static_cast<__nv_bfloat16*>(q.out), nullptr);
-        e = cudaGetLastError();
-      }
+      if (e == cudaSuccess) e = launch_dw_sum(q.part, q.stride, q.cut, columns, std::min<int64_t>(columns, l.dw_rows), c->dim, c->dtype, q.out, s);
     }
   }
   if (dx != nullptr && e == cudaSuccess) {
     const float* part = reinterpret_cast<const float*>(base + l.dx);
     const int* pos = reinterpret_cast<const int*>(base + l.pos);
-    const int* cut = reinterpret_cast<const int*>(base + l.cut);
     const bool four = c->dim % 4 == 0 && (c->n <= 1 || lddx % 4 == 0) && is_aligned(dx, 4 * el);
     const int grid = grid_for(c->n * (four ? c->dim / 4 : c->dim), 256, 8);
-    auto go = [&](auto kernel, auto* to) { kernel<<<grid, 256, 0, s>>>(part, l.rows, l.dx_splits, pos, c->n, c->dim, to, lddx, l.fused ? cut : nullptr); };
+    auto go = [&](auto kernel, auto* to) { kernel<<<grid, 256, 0, s>>>(part, l.rows, pos, c->n, c->dim, to, lddx, cut); };
     MT_LAUNCH("k_vocab_dx_sum", s);
     if (fp32) four ? go(k_vocab_dx_sum<float, true>, static_cast<float*>(dx)) : go(k_vocab_dx_sum<float, false>, static_cast<float*>(dx));
     else four ? go(k_vocab_dx_sum<__nv_bfloat16, true>, static_cast<__nv_bfloat16*>(dx)) : go(k_vocab_dx_sum<__nv_bfloat16, false>, static_cast<__nv_bfloat16*>(dx));

@@ -45,21 +45,23 @@ cudaError_t launch_logit_stats(const LogitParams& p, const CUtensorMap& a, const
 cudaError_t launch_logit_grad(const LogitParams& p, int parts, const CUtensorMap& a, const CUtensorMap& b, long long row_tiles, bool pair,
                               cudaStream_t s);
 
-// C = A B over a contraction that may be cut into `splits` runs, each with its own fp32 partial product (dx), or C itself
-// rounded to its type (dW where splits = 1).
+// C = A B.  The tiles that make whole rounds of the blocks have the whole contraction; that of the rest (all of them where
+// there are few) is cut into runs, each with its own fp32 partial product, so that the last round is a full one too.
 struct SumParams {
   int passes, a_part, b_part, promote;
   int32_t* status;
   const int* live;      // [1]: rows of C (dx), or the contraction's length (dW)
-  int rows;             // rows of C that are stored (dW)
+  int rows;             // rows of C (dW)
   int steps;            // of the contraction (dx)
+  int usual;            // steps of a whole piece (dx): by these the runs are chosen, the same ones for every piece
   int columns, ctiles;  // of C
-  int splits;
-  float* part;          // [splits][stride][columns], or NULL
+  int max_runs;         // that there is room for
+  int* cut;             // [2] the rows of C before those that come in runs, and the runs
+  float* part;          // [max_runs][stride][columns]: dx of all rows (one run: the first), dW of the rows behind cut[0]
   size_t stride;
   bool add;             // to what is there
-  bool wide;            // C's rows lie on 16 bytes and end on them
-  void* out;            // [rows][columns]
+  int reach, reach_part;
+  void* out;            // dW [rows][columns]
 };
 // Columns of a tile of C with this many columns.
 inline int sum_width(int64_t columns, bool fp32) { return columns <= 64 ? 64 : columns <= 128 || fp32 ? 128 : 256; }
@@ -80,7 +82,7 @@ struct FusedParams {
   const float4* coef;
   float* part;         // [max_chunks][stride][columns]: dx of all rows (of a whole tile in the first run), dW of those behind the whole tiles
   size_t stride;
-  bool wide;
+  int reach, reach_part;  // of out's rows and part's
   __nv_bfloat16* out;  // dW
 };
 constexpr int kFusedColumns = 128, kFusedTile = 128;

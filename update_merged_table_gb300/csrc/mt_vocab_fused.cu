@@ -363,10 +363,10 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
 #pragma unroll
         for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
         if (VOCAB && x.kept < work.whole)
-          tiles::store32<__nv_bfloat16>(stage, lane, f, p.out, p.columns, r0, rows, c0 + c * 32, p.columns, p.wide);
+          tiles::store32<__nv_bfloat16>(stage, lane, f, p.out, p.columns, r0, rows, c0 + c * 32, p.columns, p.reach);
         else
           tiles::store32<float>(stage, lane, f, p.part + (size_t)x.slot * p.stride * p.columns, p.columns, VOCAB ? r0 - work.whole * kT : r0,
-                                rows, c0 + c * 32, p.columns, p.columns % 4 == 0);
+                                rows, c0 + c * 32, p.columns, p.reach_part);
       }
     }
     if (!ok) tc::latch_status(p.status, MT_ECUDA);

@@ -180,7 +180,7 @@ struct Grad : Logits<CG, KEEP> {
         if (!(there >> j & 1)) f[j] = 0.0f;
     }
     if constexpr (!SPLIT) {
-      tiles::store32<__nv_bfloat16>(this->stage, this->lane, f, p.dz, p.width, r0, 32, at0, p.width, true);
+      tiles::store32<__nv_bfloat16>(this->stage, this->lane, f, p.dz, p.width, r0, 32, at0, p.width, tiles::kSectors);
     } else {
       uint32_t w[3][16];
 #pragma unroll
@@ -193,7 +193,7 @@ struct Grad : Logits<CG, KEEP> {
       }
 #pragma unroll
       for (int q = 0; q < 3; ++q)
-        tiles::store_rows<__nv_bfloat16>(this->stage, this->lane, w[q], p.dz + (size_t)q * p.width, (size_t)3 * p.width, r0, 32, at0, p.width, true);
+        tiles::store_rows<__nv_bfloat16>(this->stage, this->lane, w[q], p.dz + (size_t)q * p.width, (size_t)3 * p.width, r0, 32, at0, p.width, tiles::kSectors);
     }
   }
   template <int G>

@@ -1,17 +1,17 @@
 // The gradients of the losses over a vocabulary from a piece of dz, the gradient
 // of its logits:
 //
-//   dx = dz W    rows of x by columns of W, the contraction over the piece, cut into
-//                runs where there are few rows; fp32 partial products, one per run,
-//                which the next pieces add to
+//   dx = dz W    rows of x by columns of W, the contraction over the piece; fp32
+//                sums, which the next pieces add to
 //   dW = dz^T x  entries of the piece by columns of x, the contraction over the live
-//                rows; the only product where the piece has entries enough, else cut
+//                rows, rounded and done
 //
 // fp32 rows: the accumulator starts anew every 512 products (`promote`) and is
 // added up in registers, rounding to nearest, since the tensor core cuts it off
 // towards zero at every step.
 #include "mt_tiles.cuh"
 #include "mt_vocab.cuh"
+#include "mt_vocab_rows.cuh"
 
 namespace mt {
 namespace {
@@ -27,7 +27,7 @@ struct Sum {
   static constexpr int kBN = BN;
   static constexpr bool kAMN = VOCAB, kBMN = true, kTeams = !FP32, kKeep = false;
   const Params& p;
-  int rank, rows, rt, steps, quad, half, lane;
+  int rank, rows, rt, steps, whole, runs, quad, half, lane;  // whole: row tiles with the whole contraction
   uint8_t* stage;
   float sum[FP32 ? BN / 2 : 1];
 
@@ -36,20 +36,32 @@ struct Sum {
     rows = VOCAB ? p.rows : live;
     steps = VOCAB ? (live + tiles::kBK - 1) / tiles::kBK : p.steps;
     rt = (rows + tiles::kBM * CG - 1) / (tiles::kBM * CG);
+    const int blocks = gridDim.x / CG;
+    whole = rt * p.ctiles / blocks * blocks / p.ctiles;
+    runs = choose_chunks((rt - whole) * p.ctiles, VOCAB ? steps : p.usual, p.max_runs, blocks, 8);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      p.cut[0] = whole * (tiles::kBM * CG);
+      p.cut[1] = runs;
+    }
   }
-  __device__ long long units() const { return (long long)rt * p.ctiles * p.splits; }
+  __device__ long long units() const { return ((long long)whole + (long long)(rt - whole) * runs) * p.ctiles; }
   __device__ Unit unit(long long u) const {  // columns fastest: the tiles of a row tile read the same rows of dz
     const int c = (int)(u % p.ctiles);
-    const long long q = u / p.ctiles;
-    const int r = (int)(q % rt), s = (int)(q / rt);
+    int r = (int)(u / p.ctiles), s = 0, n = 1;
+    if (r >= whole) {
+      const int rest = rt - whole;
+      s = (r - whole) / rest;
+      r = whole + (r - whole) - s * rest;
+      n = runs;
+    }
     Unit x;
     x.g = 0;
     x.row0 = r * (tiles::kBM * CG);
     x.end = rows;
     x.ct0 = c;
     x.ct1 = c + 1;
-    x.k0 = (int)((long long)s * steps / p.splits);
-    x.k1 = (int)((long long)(s + 1) * steps / p.splits);
+    x.k0 = (int)((long long)s * steps / n);
+    x.k1 = (int)((long long)(s + 1) * steps / n);
     x.slot = s;
     return x;
   }
@@ -62,59 +74,28 @@ struct Sum {
   __device__ void begin(const Unit&) {}
   __device__ void end(const Unit&) {}
 
-  // 16 columns of each lane's row, added to what is there where p.add
-  __device__ __forceinline__ void put(const float (&f)[32], const Unit& x, int col, bool first_half) {
-    const long long r0 = x.row0 + rank * tiles::kBM + quad * 32;
-    const int n = min(32, x.end - (int)r0);
+  // 32 columns of each lane's row to the unit's partial product, or added to it
+  __device__ __forceinline__ void put(float (&f)[32], const Unit& x, int col) {
+    const long long r0 = x.row0 - (VOCAB ? whole * (tiles::kBM * CG) : 0) + rank * tiles::kBM + quad * 32;
+    const int n = min(32, x.end - (x.row0 + rank * tiles::kBM + quad * 32));
     float* C = p.part + (size_t)x.slot * p.stride * p.columns;
-    uint32_t w[16];
+    if (!VOCAB && p.add) {
+      float old[32];
+      tiles::load_rows<float>(stage, lane, old, C, p.columns, r0, n, col, p.columns, p.reach_part);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(first_half ? f[j] : f[16 + j]);
-    if (!p.add) {
-      tiles::store_rows<float>(stage, lane, w, C, p.columns, r0, n, col, p.columns, p.columns % 4 == 0);
-      return;
+      for (int j = 0; j < 32; ++j) f[j] += old[j];
     }
-    if (col >= p.columns) return;
-    __syncwarp();
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      *reinterpret_cast<uint4*>(stage + tiles::piece_at(lane, c)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-    __syncwarp();
-    if (p.columns % 4 == 0) {
-      const int c = lane & 3, at = col + c * 4;
-      float4 old[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int r = q * 8 + (lane >> 2);
-        if (r < n && at < p.columns) old[q] = *reinterpret_cast<const float4*>(C + (size_t)(r0 + r) * p.columns + at);
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int r = q * 8 + (lane >> 2);
-        if (r < n && at < p.columns) {
-          const float4 v = *reinterpret_cast<const float4*>(stage + tiles::piece_at(r, c));
-          *reinterpret_cast<float4*>(C + (size_t)(r0 + r) * p.columns + at) =
-              make_float4(old[q].x + v.x, old[q].y + v.y, old[q].z + v.z, old[q].w + v.w);
-        }
-      }
-    } else {
-      for (int i = lane; i < 512; i += 32) {
-        const int r = i / 16, j = i % 16;
-        if (r < n && col + j < p.columns)
-          C[(size_t)(r0 + r) * p.columns + col + j] += *reinterpret_cast<const float*>(stage + tiles::piece_at(r, j / 4) + j % 4 * 4);
-      }
-    }
+    tiles::store32<float>(stage, lane, f, C, p.columns, r0, n, col, p.columns, p.reach_part);
   }
 
-  __device__ __forceinline__ void store(const float (&f)[32], const Unit& x, int col) {
-    if (!VOCAB || p.part != nullptr) {
-      put(f, x, col, true);
-      put(f, x, col + 16, false);
+  __device__ __forceinline__ void store(float (&f)[32], const Unit& x, int col) {
+    if (!VOCAB || x.row0 >= whole * (tiles::kBM * CG)) {
+      put(f, x, col);
       return;
     }
     using T = std::conditional_t<FP32, float, __nv_bfloat16>;
-    const long long r0 = x.row0 + rank * tiles::kBM + quad * 32;
-    tiles::store32<T>(stage, lane, f, static_cast<T*>(p.out), p.columns, r0, min(32, x.end - (int)r0), col, p.columns, p.wide);
+    const int r0 = x.row0 + rank * tiles::kBM + quad * 32;
+    tiles::store32<T>(stage, lane, f, static_cast<T*>(p.out), p.columns, r0, min(32, x.end - r0), col, p.columns, p.reach);
   }
 
   template <int G>
@@ -154,7 +135,7 @@ struct Sum {
 template <bool VOCAB>
 cudaError_t launch_sum(const char* name, const SumParams& p, bool fp32, const CUtensorMap& a, const CUtensorMap& b, long long row_tiles,
                        bool pair, cudaStream_t s) {
-  const long long units = row_tiles * p.ctiles * p.splits;
+  const long long units = row_tiles * p.ctiles * p.max_runs;
   const int bn = sum_width(p.columns, fp32);
   if (fp32)
     return bn == 64 ? tiles::launch<Sum<64, true, VOCAB, 1>, 1>(name, a, b, p, units, 0, 0, s)
