@@ -1,8 +1,8 @@
 // Grouped matrix products in bf16 on the tensor cores (tcgen05): forward, dx and dW.
 //
 // One persistent block per SM walks the output tiles of all groups; inside it
-// one thread keeps a ring of shared-memory stages filled by TMA, one thread
-// issues the products into tensor memory, and four warps read finished tiles
+// one warp keeps a ring of shared-memory stages filled by TMA, one warp issues the
+// products into tensor memory, and four warps read finished tiles
 // out while the next tile's products run (two accumulators).
 //
 //  k_linear_rows_tc     forward and dx: 128 rows of one group x BN columns.  The
@@ -187,18 +187,19 @@ k_linear_rows_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constan
   const long long t0 = blockIdx.x / CG, tstep = gridDim.x / CG;
 
   if (warp == 0) {
-    if (lane == 0) {
-      Slot s;
-      long long issued = 0;
-      bool ok = true;
-      for (long long t = t0; t < total && ok; t += tstep) {
-        const int rt = (int)(t / p.jtiles), j0 = (int)(t - (long long)rt * p.jtiles) * BN + rank * kCols;
-        const int g = tile_group(s_cum, p.groups, rt);
-        const int r0 = (int)(s_off[g] + (long long)(rt - s_cum[g]) * kRows) + rank * kBM;
-        for (int k = 0; k < steps; ++k) {
-          ok = tc::mbar_wait(&bar.empty[s.stage], s.phase ^ 1);
-          if (!ok) break;
-          uint8_t* st = ring + s.stage * R::kStage;
+    const bool one = tc::elect_one();
+    Slot s;
+    long long issued = 0;
+    bool ok = true;
+    for (long long t = t0; t < total && ok; t += tstep) {
+      const int rt = (int)(t / p.jtiles), j0 = (int)(t - (long long)rt * p.jtiles) * BN + rank * kCols;
+      const int g = tile_group(s_cum, p.groups, rt);
+      const int r0 = (int)(s_off[g] + (long long)(rt - s_cum[g]) * kRows) + rank * kBM;
+      for (int k = 0; k < steps; ++k) {
+        ok = tc::warp_wait(&bar.empty[s.stage], s.phase ^ 1);
+        if (!ok) break;
+        uint8_t* st = ring + s.stage * R::kStage;
+        if (one) {
           if constexpr (CG == 2) {  // both blocks' copies count on the first block's barrier
             const uint32_t full = tc::of_leader(&bar.full[s.stage]);
             if (rank == 0) tc::mbar_expect(&bar.full[s.stage], 2 * R::kStage);
@@ -221,51 +222,55 @@ k_linear_rows_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constan
               tc::tma_load_3d(st + R::kStageA, &map_w, &bar.full[s.stage], k * kBK, j0, g);
             }
           }
-          ++issued;
-          s.next<R::kStages>();
         }
-      }
-      ok = ok && all_released<R::kStages>(bar, s, issued);
-      // what the first block signals of its last products has to have arrived here before this block ends
-      if (rank != 0) ok = tc::mbar_wait(&bar.done, 0) && ok;
-      if (!ok) {
-        latch_status(p.status, MT_ECUDA);
-        if (rank == 0) drain<R::kStages>(bar, s, issued);
+        __syncwarp();
+        ++issued;
+        s.next<R::kStages>();
       }
     }
+    ok = ok && all_released<R::kStages>(bar, s, issued);
+    // what the first block signals of its last products has to have arrived here before this block ends
+    if (rank != 0) ok = tc::mbar_wait(&bar.done, 0) && ok;
+    if (!ok) {
+      if (one) latch_status(p.status, MT_ECUDA);
+      if (rank == 0) drain<R::kStages>(bar, s, issued);
+    }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       constexpr uint32_t instr = tc::instr_bf16(kRows, BN, false, B_MN);
+      constexpr uint32_t kStepB = (B_MN ? 2048 : 32) >> 4;  // 16 of the contraction further on, as descriptors count
+      const bool one = tc::elect_one();
+      const uint32_t a0 = tc::desc_low(tc::smem_addr(ring), 16), b0 = tc::desc_low(tc::smem_addr(ring + R::kStageA), B_MN ? 8192 : 16);
       Slot s;
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true;
       for (long long t = t0; t < total && ok; t += tstep) {
-        ok = tc::mbar_wait(&bar.acc_empty[acc], acc_phase ^ 1);
+        ok = tc::warp_wait(&bar.acc_empty[acc], acc_phase ^ 1);
         if (!ok) break;
         tc::fence_after();
         for (int k = 0; k < steps; ++k) {
-          ok = tc::mbar_wait<CG == 2>(&bar.full[s.stage], s.phase);  // a pair's copies into both blocks
+          ok = tc::warp_wait<CG == 2>(&bar.full[s.stage], s.phase);  // a pair's copies into both blocks
           if (!ok) break;
           tc::fence_after();
-          const uint32_t a = tc::smem_addr(ring + s.stage * R::kStage), b = a + R::kStageA;
+          const uint32_t a = a0 + s.stage * (R::kStage >> 4), b = b0 + s.stage * (R::kStage >> 4);
+          if (one) {
 #pragma unroll
-          for (int i = 0; i < kBK / 16; ++i) {
-            const uint64_t da = tc::smem_desc(a + i * 32, 16);
-            const uint64_t db = B_MN ? tc::smem_desc(b + i * 2048, 8192) : tc::smem_desc(b + i * 32, 16);
-            tc::mma_bf16<CG>(tmem + acc * BN, da, db, instr, k > 0 || i > 0);
+            for (int i = 0; i < kBK / 16; ++i) tc::mma_bf16<CG>(tmem + acc * BN, a + i * (32 >> 4), b + i * kStepB, instr, k > 0 || i > 0);
+            tc::mma_commit<CG>(&bar.empty[s.stage]);
+            if (k + 1 == steps) tc::mma_commit<CG>(&bar.acc_full[acc]);
           }
-          tc::mma_commit<CG>(&bar.empty[s.stage]);
+          __syncwarp();
           s.next<R::kStages>();
         }
         if (!ok) break;
-        tc::mma_commit<CG>(&bar.acc_full[acc]);
         acc ^= 1;
         acc_phase ^= acc == 0;
       }
-      tc::mma_commit<CG>(&bar.done);  // tensor memory is freed only when no product writes it, also after a wait ran out
+      if (one) tc::mma_commit<CG>(&bar.done);  // tensor memory is freed only when no product writes it, also after a wait ran out
+      __syncwarp();
       ok = tc::mbar_wait(&bar.done, 0) && ok;
-      if (!ok) latch_status(p.status, MT_ECUDA);
+      if (!ok && one) latch_status(p.status, MT_ECUDA);
     }
   } else {
     const int quad = warp & 3;  // the lanes of tensor memory this warp may read
@@ -388,20 +393,21 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
   if (warp < 4) {
     if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
     if (warp == 0) {
-      if (lane == 0) {
-        constexpr uint32_t bytes = (X8 ? kBM * kBK : R::kStageA) + R::kStageB;
-        Slot s;
-        long long issued = 0;
-        bool ok = true;
-        for (long long r0 = 0; r0 * units < total && ok; ++r0) {
-          const long long t = dealt(r0, unit, units);
-          if (t >= total) continue;
-          const Tile x = tile_of(t);
-          for (long long r = x.first; r < x.last; r += kBK) {
-            ok = tc::mbar_wait(&bar.empty[s.stage], s.phase ^ 1);
-            if (!ok) break;
-            uint8_t* st = ring + s.stage * R::kStage;
-            const int dy0 = x.m0 + rank * kColsB;
+      constexpr uint32_t bytes = (X8 ? kBM * kBK : R::kStageA) + R::kStageB;
+      const bool one = tc::elect_one();
+      Slot s;
+      long long issued = 0;
+      bool ok = true;
+      for (long long r0 = 0; r0 * units < total && ok; ++r0) {
+        const long long t = dealt(r0, unit, units);
+        if (t >= total) continue;
+        const Tile x = tile_of(t);
+        for (long long r = x.first; r < x.last; r += kBK) {
+          ok = tc::warp_wait(&bar.empty[s.stage], s.phase ^ 1);
+          if (!ok) break;
+          uint8_t* st = ring + s.stage * R::kStage;
+          const int dy0 = x.m0 + rank * kColsB;
+          if (one) {
             if (CG == 2 && x.last - r >= kBK) {  // both blocks' copies count on the first block's barrier
               const uint32_t full = tc::of_leader(&bar.full[s.stage]);
               if (rank == 0) tc::mbar_expect(&bar.full[s.stage], 2 * bytes);
@@ -423,17 +429,18 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
               for (int c = 0; c < kColsB / 64; ++c)
                 tc::tma_load_2d(st + R::kStageA + c * 8192, &map_dy, full, dy0 + c * 64, (int)r);
             }
-            ++issued;
-            if (CG == 2) bar.copied = (uint32_t)issued;
-            s.next<R::kStages>();
           }
+          __syncwarp();
+          ++issued;
+          if (CG == 2 && one) bar.copied = (uint32_t)issued;
+          s.next<R::kStages>();
         }
-        ok = ok && all_released<R::kStages>(bar, s, issued);
-        if (rank != 0) ok = tc::mbar_wait(&bar.done, 0) && ok;  // as in k_linear_rows_tc
-        if (!ok) {
-          latch_status(p.status, MT_ECUDA);
-          if (rank == 0) drain<R::kStages>(bar, s, issued);
-        }
+      }
+      ok = ok && all_released<R::kStages>(bar, s, issued);
+      if (rank != 0) ok = tc::mbar_wait(&bar.done, 0) && ok;  // as in k_linear_rows_tc
+      if (!ok) {
+        if (one) latch_status(p.status, MT_ECUDA);
+        if (rank == 0) drain<R::kStages>(bar, s, issued);
       }
     }
     // Plain x: the rows past the chunk's end in its last stage belong to others; warp 1 zeroes them in both operands, so
@@ -442,6 +449,8 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     // warps do it.
     if (warp == 1) {
       constexpr uint32_t instr = tc::instr_bf16(kRowsD, BN, true, true);
+      const bool one = tc::elect_one();
+      const uint32_t a0 = tc::desc_low(tc::smem_addr(ring), 8192);
       Slot s;
       int acc = 0;
       uint32_t acc_phase = 0, tail_phase = 0;  // tail_phase: a bit per stage
@@ -487,12 +496,11 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
           }
           tc::fence_after();
           const bool closes = k % kPromote == kPromote - 1 || k + 1 == x.stages;
-          if (lane == 0) {
-            const uint32_t a = tc::smem_addr(st), b = a + R::kStageA;
+          const uint32_t a = a0 + s.stage * (R::kStage >> 4), b = a + (R::kStageA >> 4);
+          if (one) {
 #pragma unroll
             for (int i = 0; i < kBK / 16; ++i)
-              tc::mma_bf16<CG>(tmem + acc * BN, tc::smem_desc(a + i * 2048, 8192), tc::smem_desc(b + i * 2048, 8192), instr,
-                               k % kPromote > 0 || i > 0);
+              tc::mma_bf16<CG>(tmem + acc * BN, a + i * (2048 >> 4), b + i * (2048 >> 4), instr, k % kPromote > 0 || i > 0);
             tc::mma_commit<CG>(&bar.empty[s.stage]);
             if (closes) tc::mma_commit<CG>(&bar.acc_full[acc]);
           }
@@ -504,14 +512,13 @@ k_linear_weights_tc(const __grid_constant__ CUtensorMap map_x, const __grid_cons
           s.next<R::kStages>();
         }
       }
-      if (lane == 0) {
-        // tensor memory is freed only when no product writes it, also after a wait ran out
-        if (rank == 0) {
-          tc::mma_commit<CG>(&bar.done);
-          ok = tc::mbar_wait(&bar.done, 0) && ok;
-        }
-        if (!ok) latch_status(p.status, MT_ECUDA);
+      // tensor memory is freed only when no product writes it, also after a wait ran out
+      if (rank == 0) {
+        if (one) tc::mma_commit<CG>(&bar.done);
+        __syncwarp();
+        ok = tc::mbar_wait(&bar.done, 0) && ok;
       }
+      if (!ok && one) latch_status(p.status, MT_ECUDA);
     }
   } else {
     if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRead));

@@ -223,38 +223,16 @@ __host__ __device__ constexpr uint32_t instr_bf16(int M, int N, bool a_mn, bool 
 //  contraction contiguous: 8-row groups of 128-byte rows lie 1024 bytes apart; 64 bf16 of the contraction per row.
 //  rows contiguous: 64 rows (128 bytes) per contraction step, 8 steps lie 1024 bytes apart; the next 64 rows `lead`
 //  bytes on.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
-         (1ull << 46) | (2ull << 61);
-}
-
-// The low word of such a descriptor, to which a step of 16 of the contraction adds a constant; the high word is kDescHigh.
+// Its low word, to which a step of 16 of the contraction adds 32 >> 4 or 2048 >> 4; the high word is the same for all.
 __device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lead) { return ((addr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16); }
 constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 
-// D (tensor memory) = A * B, or D + A * B; one thread issues it.  For a pair (the first block's thread) each block holds
-// half of A's rows, half of B's rows and its half of D's rows, at the same addresses.
+// D (tensor memory) = A * B, or D + A * B, operands by their descriptors' low words; one thread issues it (elect_one: the
+// 100 dependent instructions that a thread by itself needed for four of them took longer than the products, 690 clocks
+// against 512).  For a pair (the first block's thread) each block holds half of A's rows, half of B's rows and its half of
+// D's rows, at the same addresses.
 template <int CG>
-__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, bool add) {
-  if constexpr (CG == 1) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(instr), "r"(add ? 1u : 0u)
-        : "memory");
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(instr), "r"(add ? 1u : 0u)
-        : "memory");
-  }
-}
-// The same from the descriptors' low words.
-template <int CG>
-__device__ __forceinline__ void mma_low(uint32_t d, uint32_t a, uint32_t b, uint32_t instr, bool add) {
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint32_t a, uint32_t b, uint32_t instr, bool add) {
   if constexpr (CG == 1) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"

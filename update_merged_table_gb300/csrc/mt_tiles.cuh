@@ -285,7 +285,7 @@ k_tiles(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
               if (one) {
 #pragma unroll
                 for (int i = 0; i < kBK / 16; ++i)
-                  tc::mma_low<CG>(tmem + acc * BN, a + i * kStepA, b + i * kStepB, instr, part > 0 || i > 0);
+                  tc::mma_bf16<CG>(tmem + acc * BN, a + i * kStepA, b + i * kStepB, instr, part > 0 || i > 0);
                 tc::mma_commit<CG>(&bar.empty[s.stage]);
                 if (closes) tc::mma_commit<CG>(&bar.acc_full[acc]);
               }

@@ -182,7 +182,7 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
 #pragma unroll
           for (int i = 0; i < KS * 4; ++i) {
             const uint32_t o = ((i >> 2) * kSlab + (i & 3) * 32) >> 4;
-            tc::mma_low<1>(tmem + b * kT, ax + o, aw + o, instr, i > 0);
+            tc::mma_bf16<1>(tmem + b * kT, ax + o, aw + o, instr, i > 0);
           }
           tc::mma_commit<1>(&bar.s_full[b]);
         }
@@ -220,7 +220,7 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         if (one) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            tc::mma_low<1>(tmem + kAccAt, from + ((VOCAB ? i * 2048 : (i >> 2) * kSlab + (i & 3) * 32) >> 4), with + (i * 2048 >> 4), instr,
+            tc::mma_bf16<1>(tmem + kAccAt, from + ((VOCAB ? i * 2048 : (i >> 2) * kSlab + (i & 3) * 32) >> 4), with + (i * 2048 >> 4), instr,
                            t > x.t0 || i > 0);
           tc::mma_commit<1>(&bar.empty[s.stage]);
           tc::mma_commit<1>(&bar.dz_empty[b]);
