@@ -424,6 +424,26 @@ class SmemLimit {
   std::atomic<bool> set_[kMaxDevices] = {};
 };
 
+// A kernel that starts while the one before it on the stream ends: its blocks set themselves up and then wait (follow()) until
+// that one is done and its writes are seen.  Every block calls follow() before it touches global memory, and lead() once it
+// runs, which lets the next kernel's blocks in.
+__device__ __forceinline__ void follow() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void lead() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_following(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 inline size_t elem_bytes(int dtype) { return dtype == MT_F32 ? 4 : 2; }
 
 // A plain row tensor: pointer, element alignment, row stride of at least d and below 2^31.

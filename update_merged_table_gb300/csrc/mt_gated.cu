@@ -165,7 +165,97 @@ struct Gated {
   }
 };
 
+// ---- forward of a few rows --------------------------------------------------------------
+//
+// A few tokens being served: the weights' bytes and the latency of one load are all there is.  A warp takes two
+// neighbouring rows of Wy and the same two of Wu (32 lanes by eight columns a step, the loads in flight together) against
+// two rows of x; lanes then join by shuffles and h is made in registers.  A group's further rows are tasks of their own, so
+// a batch costs the same whichever groups its rows are in.
+constexpr int kFewRows = 2, kFewOuts = 2, kFewBlocks = 3;
+
+struct FewParams {
+  long long n;
+  const long long* offsets;
+  int32_t* status;
+  const void* x;
+  long long ldx;
+  const void* w;
+  void* h;
+  long long ldh;
+  int groups, in_dim, out_dim, gate;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(256, kFewBlocks) k_gated_few(const FewParams p) {
+  extern __shared__ long long s_off[];
+  int* s_cum = reinterpret_cast<int*>(s_off + p.groups + 1);
+  load_offsets(p.offsets, p.groups, p.n, s_off, p.status);
+  count_tiles(s_off, p.groups, kFewRows, s_cum);
+  const int lane = threadIdx.x & 31;
+  T* H = static_cast<T*>(p.h);
+  zero_outside<T>(s_off, p.groups, p.n, H, p.ldh, p.out_dim, blockDim.x, threadIdx.x);
+  const int per_tile = (p.out_dim + kFewOuts - 1) / kFewOuts;
+  const int warps = (gridDim.x * blockDim.x) >> 5;
+  for (int t = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; t < s_cum[p.groups] * per_tile; t += warps) {
+    const int q = t / per_tile, j0 = (t - q * per_tile) * kFewOuts, g = tile_group(s_cum, p.groups, q);
+    const int outs = min(kFewOuts, p.out_dim - j0);
+    const int r0 = (int)s_off[g] + (q - s_cum[g]) * kFewRows, rows = min(kFewRows, (int)s_off[g + 1] - r0);
+    const T* W = static_cast<const T*>(p.w) + ((size_t)g * 2 * p.out_dim + j0) * p.in_dim;
+    f32x2 acc[kFewRows][2 * kFewOuts] = {};
+#pragma unroll 2
+    for (int i = lane * 8; i < p.in_dim; i += 256) {
+      Raw8<T> w[2 * kFewOuts], x[kFewRows];  // every load of the step issued before the first is used
+#pragma unroll
+      for (int o = 0; o < 2 * kFewOuts; ++o) {  // the rows of Wy, then those of Wu
+        const int row = (o % kFewOuts < outs ? o % kFewOuts : 0) + (o < kFewOuts ? 0 : p.out_dim);
+        w[o] = load8<T, true>(Rows{const_cast<T*>(W), (int64_t)p.in_dim, nullptr, nullptr}, row, i >> 3, p.in_dim);
+      }
+#pragma unroll
+      for (int r = 0; r < kFewRows; ++r)
+        if (r < rows) x[r] = load8<T, true>(Rows{const_cast<void*>(p.x), p.ldx, nullptr, nullptr}, r0 + r, i >> 3, p.in_dim);
+#pragma unroll
+      for (int r = 0; r < kFewRows; ++r) {
+        if (r >= rows) break;
+        f32x2 v[4];
+        widen8<T>(x[r], false, v);
+#pragma unroll
+        for (int o = 0; o < 2 * kFewOuts; ++o) {
+          f32x2 f[4];
+          widen8<T>(w[o], false, f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[r][o] = fma2(v[j], f[j], acc[r][o]);
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kFewRows; ++r) {
+      if (r >= rows) break;
+      float s[2 * kFewOuts];
+#pragma unroll
+      for (int o = 0; o < 2 * kFewOuts; ++o) {
+        s[o] = pair_sum(acc[r][o]);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) s[o] += __shfl_xor_sync(kFull, s[o], d);
+      }
+#pragma unroll
+      for (int o = 0; o < kFewOuts; ++o)
+        if (lane == o && o < outs) H[row_offset(r0 + r, p.ldh) + j0 + o] = from_f<T>(s[o] * gate_of<T>(p.gate, s[kFewOuts + o]));
+    }
+  }
+}
+
 // ---- host --------------------------------------------------------------------------------------
+
+// The forward of few rows goes to k_gated_few: up to kFewTc rows per group on average (bf16) or kFewParts (fp32, whose weights
+// would be copied first), as long as each warp that the SMs hold has no more than kFewTasks tasks.  (As for the grouped
+// products, whose rule has both sides' times.)
+constexpr int kFewTc = 2, kFewParts = 8, kFewTasks = 6;
+bool few(const mt_gated_linear& c) {
+  const long long tiles = (c.n + std::min<long long>(c.n, c.groups) * (kFewRows - 1)) / kFewRows;  // at most
+  const long long tasks = tiles * ((c.out_dim + kFewOuts - 1) / kFewOuts), held = (long long)sm_count() * kFewBlocks * 8;
+  return c.n <= (long long)(c.dtype == MT_BF16 ? kFewTc : kFewParts) * c.groups && tasks <= kFewTasks * held && c.in_dim % 8 == 0 &&
+         (c.n <= 1 || c.ldx * elem_bytes(c.dtype) % 16 == 0) && is_aligned(c.x, 16) && is_aligned(c.w, 16);
+}
 
 // How a call's operands reach the tensor cores.
 struct Layout {
@@ -182,6 +272,7 @@ bool fits(const mt_gated_linear& c) {
 Layout layout_of(const mt_gated_linear& c, bool backward) {
   Layout l{};
   l.parts = c.dtype == MT_F32 ? 3 : 1;
+  if (!backward && few(c)) return l;
   l.copies = c.dtype == MT_F32 || !fits(c);
   l.k = part_columns(c.in_dim, l.parts);
   l.m = c.dtype == MT_F32 ? c.out_dim : (c.out_dim + 7) / 8 * 8;
@@ -281,6 +372,17 @@ int mt_gated_linear_forward(const mt_gated_linear* c, void* h, int64_t ldh, void
   all.out(Rows{h, ldh, nullptr, nullptr}, c->n, c->out_dim, c->dtype);
   if (l.total > 0) all.out(whole_region(ws, l.total));
   if (all.clash()) return MT_EINVAL;
+  if (few(*c)) {
+    const FewParams f{c->n, reinterpret_cast<const long long*>(c->offsets), c->status, c->x, c->n <= 1 ? c->in_dim : c->ldx, c->w, h, ldh,
+                      c->groups, c->in_dim, c->out_dim, c->gate};
+    const long long tasks = (c->n + std::min<long long>(c->n, c->groups) * (kFewRows - 1)) / kFewRows * ((c->out_dim + kFewOuts - 1) / kFewOuts);
+    const int grid = grid_for(tasks * 32, 256, kFewBlocks);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    MT_LAUNCH("k_gated_few", s);
+    if (c->dtype == MT_F32) k_gated_few<float><<<grid, 256, rows_smem(c->groups), s>>>(f);
+    else k_gated_few<__nv_bfloat16><<<grid, 256, rows_smem(c->groups), s>>>(f);
+    return cudaGetLastError() == cudaSuccess ? MT_OK : MT_ECUDA;
+  }
   GatedParams p{};
   p.out = h;
   p.ldo = ldh;

@@ -127,7 +127,6 @@ k_tiles(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
   uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)s_raw + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = blockIdx.x % CG;  // in the pair
-  Op op(p, ring + R::kBytes, rank);
   const int kept = kept_of<Op>(p);
   const int stages = R::stages(kept);
   uint8_t* stages_at = ring + kept * R::kStageA;
@@ -152,6 +151,9 @@ k_tiles(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
   else __syncthreads();
   tc::fence_after();
   const uint32_t tmem = bar.tmem;
+  lead();
+  follow();
+  Op op(p, ring + R::kBytes, rank);
   const long long units = op.units(), u0 = blockIdx.x / CG, ustep = gridDim.x / CG;
 
   if (warp == 0) {
@@ -479,7 +481,7 @@ __device__ __forceinline__ void store32(uint8_t* stage, int lane, const float (&
 
 // ---- host ----------------------------------------------------------------------------------------
 
-// Launches an operator over `units` units (at most), in clusters of CG blocks, with `extra` bytes of its own shared
+// Launches an operator over `units` units (at most), in clusters of CG blocks, following the kernel before it, with `extra` bytes of its own shared
 // memory of at most `most`.
 template <class Op, int CG>
 cudaError_t launch(const char* name, const CUtensorMap& a, const CUtensorMap& b, const typename Op::Params& p, long long units,
@@ -494,12 +496,14 @@ cudaError_t launch(const char* name, const CUtensorMap& a, const CUtensorMap& b,
   cfg.blockDim = dim3(kThreadsT);
   cfg.dynamicSmemBytes = ring + extra;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CG;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = CG > 1 ? 1 : 0;
+  cfg.numAttrs = CG > 1 ? 2 : 1;
   MT_LAUNCH(name, s);
   return cudaLaunchKernelEx(&cfg, k_tiles<Op, CG>, a, b, p);
 }

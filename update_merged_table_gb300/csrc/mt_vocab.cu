@@ -1,7 +1,7 @@
 // Losses of rows against a vocabulary whose logits are never kept: cross entropy,
 // and distillation from a teacher's top logits.
 //
-//   k_vocab_mark   which rows take part (one bit each)
+//   k_vocab_mark   which rows take part (one bit each; few rows: k_vocab_rows sees to it)
 //   k_vocab_rows   the rows that do, one after the other: their values as the
 //                  tensor cores take them (bf16; fp32 in three parts), their targets
 //                  in ascending order with their shares, for the backward the row's
@@ -59,21 +59,26 @@ __device__ __forceinline__ bool pair_there(const VocabRows& p, long long i, long
   return id >= 0 && id < p.vocab && (!p.distill || !(teacher_at(p, i) == -INFINITY));
 }
 
+// Whether a row takes part; what is outside the vocabulary is latched.
+__device__ __forceinline__ bool row_there(const VocabRows& p, long long row) {
+  bool there = false, bad = false;
+  for (int k = 0; k < p.top; ++k) {
+    const long long id = id_at(p, row * p.top + k);
+    bad |= id >= p.vocab;
+    there |= pair_there(p, row * p.top + k, id);
+  }
+  if (bad && p.status != nullptr) atomicCAS(p.status, 0, MT_EINVAL);
+  return there;
+}
+
 // A warp per 32 rows.
 __global__ void __launch_bounds__(256) k_vocab_mark(const VocabRows p) {
+  lead();
   const int lane = threadIdx.x & 31;
   const long long words = (p.n + 31) / 32;
   for (long long w = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5; w < words; w += ((long long)gridDim.x * blockDim.x) >> 5) {
     const long long row = w * 32 + lane;
-    bool there = false, bad = false;
-    if (row < p.n) {
-      for (int k = 0; k < p.top; ++k) {
-        const long long id = id_at(p, row * p.top + k);
-        bad |= id >= p.vocab;
-        there |= pair_there(p, row * p.top + k, id);
-      }
-    }
-    if (bad && p.status != nullptr) atomicCAS(p.status, 0, MT_EINVAL);
+    const bool there = row < p.n && row_there(p, row);
     const unsigned bits = __ballot_sync(kFull, there);
     if (lane == 0) p.mask[w] = bits;
   }
@@ -90,10 +95,15 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// MARK: few rows, which every block looks through itself (no k_vocab_mark before it).
+constexpr int kMarkPairs = 8192;  // targets, or pairs, of so few rows
+
 // A block per 32 rows, a warp per live row; the last block writes how many there are and puts zeros behind them up to the
 // next 128 rows (steps of dW's contraction).  T: the rows' type; AL: they can be read in 16-byte vectors.
-template <typename T, bool AL>
+template <typename T, bool AL, bool MARK>
 __global__ void __launch_bounds__(256) k_vocab_rows(const VocabRows p) {
+  lead();
+  if (!MARK) follow();
   constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
   extern __shared__ uint8_t s_mem[];
   __shared__ int s_base;
@@ -103,12 +113,19 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const VocabRows p) {
     if (threadIdx.x == 0) s_base = 0;
     __syncthreads();
     int before = 0;
-    for (long long i = threadIdx.x; i < w; i += blockDim.x) before += __popc(p.mask[i]);
+    uint32_t bits;
+    if constexpr (MARK) {
+      for (long long i = threadIdx.x; i < w * 32; i += blockDim.x) before += row_there(p, i);
+      __syncwarp();
+      bits = __ballot_sync(kFull, w * 32 + lane < p.n && row_there(p, w * 32 + lane));
+    } else {
+      for (long long i = threadIdx.x; i < w; i += blockDim.x) before += __popc(p.mask[i]);
+      bits = p.mask[w];
+    }
     before = __reduce_add_sync(kFull, before);
     if (lane == 0) atomicAdd(&s_base, before);
     __syncthreads();
     const int base = s_base;
-    const uint32_t bits = p.mask[w];
     const int own = __popc(bits);
     if (threadIdx.x < 32 && w * 32 + lane < p.n)
       p.pos[w * 32 + lane] = bits >> lane & 1 ? base + __popc(bits & ((1u << lane) - 1u)) : -1;
@@ -210,6 +227,8 @@ struct VocabLoss {
 
 // A warp per row: the runs' statistics joined.
 __global__ void __launch_bounds__(256) k_vocab_loss(const VocabLoss p) {
+  lead();
+  follow();
   const int lane = threadIdx.x & 31;
   const int slots = 2 * *p.chunks;
   for (long long row = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5; row < p.n; row += ((long long)gridDim.x * blockDim.x) >> 5) {
@@ -253,6 +272,8 @@ __global__ void __launch_bounds__(256) k_vocab_loss(const VocabLoss p) {
 template <typename T, bool FOUR>
 __global__ void __launch_bounds__(256) k_vocab_dx_sum(const float* part, size_t stride, const int* pos, long long n, int d, T* dx,
                                                       int64_t lddx, const int* cut) {
+  lead();
+  follow();
   constexpr int kPer = FOUR ? 4 : 1;
   const int per_row = d / kPer;
   const long long total = n * per_row;
@@ -284,6 +305,8 @@ __global__ void __launch_bounds__(256) k_vocab_dx_sum(const float* part, size_t 
 // The rows of dW from cut[0] on, which came in cut[1] runs.  FOUR: four values a thread.
 template <typename T, bool FOUR>
 __global__ void __launch_bounds__(256) k_vocab_dw_sum(const float* part, size_t stride, const int* cut, long long rows, int d, T* dw) {
+  lead();
+  follow();
   constexpr int kPer = FOUR ? 4 : 1;
   const int runs = cut[1];
   const size_t first = (size_t)cut[0] * d;
@@ -312,14 +335,10 @@ cudaError_t launch_dw_sum(const float* part, size_t stride, const int* cut, long
   const bool four = d % 4 == 0 && is_aligned(dw, 4 * elem_bytes(dtype));
   const int grid = grid_for(tail * d / (four ? 4 : 1), 256, 8);
   MT_LAUNCH("k_vocab_dw_sum", s);
-  if (dtype == MT_F32) {
-    if (four) k_vocab_dw_sum<float, true><<<grid, 256, 0, s>>>(part, stride, cut, rows, d, static_cast<float*>(dw));
-    else k_vocab_dw_sum<float, false><<<grid, 256, 0, s>>>(part, stride, cut, rows, d, static_cast<float*>(dw));
-  } else {
-    if (four) k_vocab_dw_sum<__nv_bfloat16, true><<<grid, 256, 0, s>>>(part, stride, cut, rows, d, static_cast<__nv_bfloat16*>(dw));
-    else k_vocab_dw_sum<__nv_bfloat16, false><<<grid, 256, 0, s>>>(part, stride, cut, rows, d, static_cast<__nv_bfloat16*>(dw));
-  }
-  return cudaGetLastError();
+  auto go = [&](auto kernel, auto* to) { return launch_following(kernel, grid, 256, 0, s, part, stride, cut, rows, d, to); };
+  if (dtype == MT_F32) return four ? go(k_vocab_dw_sum<float, true>, static_cast<float*>(dw)) : go(k_vocab_dw_sum<float, false>, static_cast<float*>(dw));
+  return four ? go(k_vocab_dw_sum<__nv_bfloat16, true>, static_cast<__nv_bfloat16*>(dw))
+              : go(k_vocab_dw_sum<__nv_bfloat16, false>, static_cast<__nv_bfloat16*>(dw));
 }
 
 // ---- host --------------------------------------------------------------------------------------
@@ -459,26 +478,33 @@ cudaError_t launch_rows(const mt_vocab_loss& c, const Layout& l, char* ws, const
   r.dloss = dloss;
   r.lse = lse;
   r.coef = dloss != nullptr ? reinterpret_cast<float4*>(ws + l.coef) : nullptr;
-  {
+  const bool mark = c.n * l.top <= kMarkPairs;
+  cudaError_t e = cudaSuccess;
+  if (!mark) {
     MT_LAUNCH("k_vocab_mark", s);
     k_vocab_mark<<<grid_for(c.n, 256, 8), 256, 0, s>>>(r);
+    e = cudaGetLastError();
   }
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   {
     const bool al = rows_wide(Rows{const_cast<void*>(c.x), c.n <= 1 ? c.dim : c.ldx, nullptr, nullptr}, c.dim, c.dtype);
     const size_t smem = c.top > 0 ? (size_t)8 * c.top * 8 : 0;
     const int grid = grid_for(tiles_of(c.n, 32) * 256, 256, 8);
-    auto go = [&](auto kernel, SmemLimit& limit) {
-      const cudaError_t le = limit.allow(kernel, (size_t)8 * MT_MAX_TOP * 8);
+    static SmemLimit limit[8];
+    auto go = [&](auto kernel, int i) {
+      const cudaError_t le = limit[i].allow(kernel, (size_t)8 * MT_MAX_TOP * 8);
       if (le != cudaSuccess) return le;
       MT_LAUNCH("k_vocab_rows", s);
+      if (!mark) return launch_following(kernel, grid, 256, smem, s, r);
       kernel<<<grid, 256, smem, s>>>(r);
       return cudaGetLastError();
     };
-    static SmemLimit limit[4];
-    if (c.dtype == MT_F32) e = al ? go(k_vocab_rows<float, true>, limit[0]) : go(k_vocab_rows<float, false>, limit[1]);
-    else e = al ? go(k_vocab_rows<__nv_bfloat16, true>, limit[2]) : go(k_vocab_rows<__nv_bfloat16, false>, limit[3]);
+    auto of = [&](auto few) {
+      constexpr bool M = decltype(few)::value;
+      if (c.dtype == MT_F32) return al ? go(k_vocab_rows<float, true, M>, M) : go(k_vocab_rows<float, false, M>, 2 + M);
+      return al ? go(k_vocab_rows<__nv_bfloat16, true, M>, 4 + M) : go(k_vocab_rows<__nv_bfloat16, false, M>, 6 + M);
+    };
+    e = mark ? of(std::true_type{}) : of(std::false_type{});
   }
   if (e == cudaSuccess && l.copy_w)
     e = launch_parts(c.w, c.vocab <= 1 ? c.dim : c.ldw, 1, c.vocab, c.vocab, c.dim, c.dtype, reinterpret_cast<__nv_bfloat16*>(ws + l.w), s);
@@ -575,8 +601,7 @@ int mt_vocab_loss_forward(const mt_vocab_loss* c, float* loss, float* lse, void*
   q.loss = loss;
   q.lse = lse;
   MT_LAUNCH("k_vocab_loss", s);
-  k_vocab_loss<<<grid_for(c->n * 32, 256, 8), 256, 0, s>>>(q);
-  return cudaGetLastError() == cudaSuccess ? MT_OK : MT_ECUDA;
+  return launch_following(k_vocab_loss, grid_for(c->n * 32, 256, 8), 256, 0, s, q) == cudaSuccess ? MT_OK : MT_ECUDA;
 }
 
 int mt_vocab_loss_backward(const mt_vocab_loss* c, const float* dloss, const float* lse, void* dx, int64_t lddx, void* dw, void* ws,
@@ -715,11 +740,10 @@ int mt_vocab_loss_backward(const mt_vocab_loss* c, const float* dloss, const flo
     const int* pos = reinterpret_cast<const int*>(base + l.pos);
     const bool four = c->dim % 4 == 0 && (c->n <= 1 || lddx % 4 == 0) && is_aligned(dx, 4 * el);
     const int grid = grid_for(c->n * (four ? c->dim / 4 : c->dim), 256, 8);
-    auto go = [&](auto kernel, auto* to) { kernel<<<grid, 256, 0, s>>>(part, l.rows, pos, c->n, c->dim, to, lddx, cut); };
+    auto go = [&](auto kernel, auto* to) { return launch_following(kernel, grid, 256, 0, s, part, l.rows, pos, c->n, c->dim, to, lddx, cut); };
     MT_LAUNCH("k_vocab_dx_sum", s);
-    if (fp32) four ? go(k_vocab_dx_sum<float, true>, static_cast<float*>(dx)) : go(k_vocab_dx_sum<float, false>, static_cast<float*>(dx));
-    else four ? go(k_vocab_dx_sum<__nv_bfloat16, true>, static_cast<__nv_bfloat16*>(dx)) : go(k_vocab_dx_sum<__nv_bfloat16, false>, static_cast<__nv_bfloat16*>(dx));
-    e = cudaGetLastError();
+    if (fp32) e = four ? go(k_vocab_dx_sum<float, true>, static_cast<float*>(dx)) : go(k_vocab_dx_sum<float, false>, static_cast<float*>(dx));
+    else e = four ? go(k_vocab_dx_sum<__nv_bfloat16, true>, static_cast<__nv_bfloat16*>(dx)) : go(k_vocab_dx_sum<__nv_bfloat16, false>, static_cast<__nv_bfloat16*>(dx));
   }
   return e == cudaSuccess ? MT_OK : MT_ECUDA;
 }

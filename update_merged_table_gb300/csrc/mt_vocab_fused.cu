@@ -76,19 +76,6 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   uint8_t* s_ring = base + R::kTile;
   uint8_t* s_dz = s_ring + R::kStages * R::kTile;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  FusedWork work;
-  work.live = *p.rows.count;
-  {
-    const int rt = (work.live + kT - 1) / kT, vt = (p.vocab + kT - 1) / kT;
-    work.kept_tiles = VOCAB ? vt : rt;
-    work.streamed = VOCAB ? rt : vt;
-    work.whole = VOCAB ? p.whole : work.kept_tiles / (int)gridDim.x * (int)gridDim.x;
-    work.chunks = choose_chunks(work.kept_tiles - work.whole, work.streamed, p.max_chunks, gridDim.x, 4);
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-      p.cut[0] = work.whole * kT;
-      p.cut[1] = work.chunks;
-    }
-  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < R::kStages; ++i) {
       tc::mbar_init(&bar.full[i], 1);
@@ -116,6 +103,21 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = bar.tmem;
+  lead();
+  follow();
+  FusedWork work;
+  work.live = *p.rows.count;
+  {
+    const int rt = (work.live + kT - 1) / kT, vt = (p.vocab + kT - 1) / kT;
+    work.kept_tiles = VOCAB ? vt : rt;
+    work.streamed = VOCAB ? rt : vt;
+    work.whole = VOCAB ? p.whole : work.kept_tiles / (int)gridDim.x * (int)gridDim.x;
+    work.chunks = choose_chunks(work.kept_tiles - work.whole, work.streamed, p.max_chunks, gridDim.x, 4);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      p.cut[0] = work.whole * kT;
+      p.cut[1] = work.chunks;
+    }
+  }
   const int units = work.units();
 
   if (warp == 0) {
@@ -386,8 +388,7 @@ cudaError_t launch(const char* name, const CUtensorMap& x, const CUtensorMap& w,
   if (e != cudaSuccess) return e;
   const int blocks = sm_count();
   MT_LAUNCH(name, s);
-  k_vocab_fused<KS, VOCAB><<<(int)(units < blocks ? (units > 0 ? units : 1) : blocks), FusedRing<KS>::kThreads, bytes, s>>>(x, w, p);
-  return cudaGetLastError();
+  return launch_following(k_vocab_fused<KS, VOCAB>, (int)(units < blocks ? (units > 0 ? units : 1) : blocks), FusedRing<KS>::kThreads, bytes, s, x, w, p);
 }
 
 }  // namespace
