@@ -39,26 +39,38 @@ __device__ __forceinline__ float sigmoid_of(float u) {
 }
 constexpr float kGelu = 1.5957691216057308f, kCube = 0.044715f;  // 2 sqrt(2 / pi)
 
-template <typename T>
-__device__ __forceinline__ float gate_of(int gate, float u) {
-  if (gate == MT_GATE_LINEAR) return u;
-  if (gate == MT_GATE_SIGMOID) return sigmoid_of<T>(u);
-  if (gate == MT_GATE_SILU) return u * sigmoid_of<T>(u);
+template <typename T, int GATE>
+__device__ __forceinline__ float gate_of(float u) {
+  if constexpr (GATE == MT_GATE_LINEAR) return u;
+  if constexpr (GATE == MT_GATE_SIGMOID) return sigmoid_of<T>(u);
+  if constexpr (GATE == MT_GATE_SILU) return u * sigmoid_of<T>(u);
   return u * sigmoid_of<T>(kGelu * fmaf(kCube * u * u, u, u));
 }
-template <typename T>
-__device__ __forceinline__ float2 gate_grad(int gate, float u) {
-  if (gate == MT_GATE_LINEAR) return make_float2(u, 1.0f);
-  if (gate == MT_GATE_SIGMOID) {
+template <typename T, int GATE>
+__device__ __forceinline__ float2 gate_grad(float u) {
+  if constexpr (GATE == MT_GATE_LINEAR) return make_float2(u, 1.0f);
+  if constexpr (GATE == MT_GATE_SIGMOID) {
     const float p = sigmoid_of<T>(u);
     return make_float2(p, p * (1.0f - p));
   }
-  if (gate == MT_GATE_SILU) {
+  if constexpr (GATE == MT_GATE_SILU) {
     const float p = sigmoid_of<T>(u), a = u * p;
     return make_float2(a, fmaf(a, 1.0f - p, p));
   }
   const float uu = u * u, p = sigmoid_of<T>(kGelu * fmaf(kCube * uu, u, u)), a = u * p;
   return make_float2(a, fmaf(a * (1.0f - p), kGelu * fmaf(3.0f * kCube, uu, 1.0f), p));
+}
+template <int GATE>
+struct GateIs {
+  static constexpr int value = GATE;
+};
+// f(GateIs<gate>): the gate is known where the columns are gone through.
+template <typename F>
+__host__ __device__ __forceinline__ void by_gate(int gate, F&& f) {
+  if (gate == MT_GATE_SILU) f(GateIs<MT_GATE_SILU>{});
+  else if (gate == MT_GATE_GELU) f(GateIs<MT_GATE_GELU>{});
+  else if (gate == MT_GATE_SIGMOID) f(GateIs<MT_GATE_SIGMOID>{});
+  else f(GateIs<MT_GATE_LINEAR>{});
 }
 
 struct GatedParams {
@@ -82,11 +94,14 @@ struct Gated {
   using Params = GatedParams;
   static constexpr int kBN = 256;
   static constexpr bool kAMN = false, kBMN = false, kTwoB = true, kTeams = true, kKeep = false;
+  static constexpr bool kSplit = BACKWARD && sizeof(T) == 2;
+  static constexpr bool kAhead = BACKWARD && sizeof(T) == 2;  // dh of a tile's first columns is on its way before the tile
   const Params& p;
   const long long* off;
   const int* cum;
   int rank, rows_per_tile, quad, lane;
   uint8_t* stage;
+  uint4 dh[4];
 
   __device__ Gated(const Params& params, uint8_t* mem, int r) : p(params), rank(r) {
     long long* s_off = reinterpret_cast<long long*>(mem);
@@ -103,14 +118,14 @@ struct Gated {
     return c;
   }
   __device__ long long units() const { return (long long)cum[p.groups] * p.jtiles; }
-  __device__ Unit unit(long long u) const {
-    const int rt = (int)(u / p.jtiles), j = (int)(u - (long long)rt * p.jtiles);
+  __device__ Unit unit(long long u) const {  // columns fastest: a row tile's products read the same rows of x
+    const int rt = (int)(u / p.jtiles), c = (int)(u - (long long)rt * p.jtiles);
     Unit x;
     x.g = tile_group(cum, p.groups, rt);
     x.row0 = (int)off[x.g] + (rt - cum[x.g]) * rows_per_tile;
     x.end = (int)off[x.g + 1];
-    x.ct0 = j;
-    x.ct1 = j + 1;
+    x.ct0 = c;
+    x.ct1 = c + 1;
     x.k0 = 0;
     x.k1 = p.steps;
     x.slot = 0;
@@ -126,8 +141,26 @@ struct Gated {
   __device__ void begin(const Unit&) {}
   __device__ void end(const Unit&) {}
 
+  // 32 columns of dh as they lie, where they lie on 16 bytes
+  __device__ __forceinline__ void fetch(const Unit& x, int col) {
+    const long long r0 = x.row0 + rank * tiles::kBM + quad * 32;
+    const T* from = static_cast<const T*>(p.dh) + (size_t)(r0 + lane) * p.lddh + col;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      dh[c] = make_uint4(0u, 0u, 0u, 0u);
+      if (r0 + lane < x.end && col + c * 8 < p.out_dim) dh[c] = __ldg(reinterpret_cast<const uint4*>(from) + c);
+    }
+  }
+  __device__ __forceinline__ void ahead(const Unit& x, int ct) {
+    if (p.reach_dh != tiles::kElements) fetch(x, ct * 128);
+  }
+
   template <int CG>
   __device__ __forceinline__ void tile(const Unit& x, int ct, const Acc& acc, bool, bool) {
+    by_gate(p.gate, [&](auto gate) { columns<CG, decltype(gate)::value>(x, ct, acc); });
+  }
+  template <int CG, int GATE>
+  __device__ __forceinline__ void columns(const Unit& x, int ct, const Acc& acc) {
     const long long r0 = x.row0 + rank * tiles::kBM + quad * 32;
     const int rows = min(32, x.end - (int)r0);  // <= 0: none of this warp's rows is in the group
     T* out = static_cast<T*>(p.out);
@@ -137,29 +170,77 @@ struct Gated {
       uint32_t y[32], u[32];
       acc.load(c, y);
       acc.load(128 + c, u);
-      float d[BACKWARD ? 32 : 1];
+      uint32_t d[BACKWARD ? 32 : 1];  // dh: bf16 pairs as they lie in the first 16, or fp32
       if constexpr (BACKWARD) {
-        if (col < p.out_dim) tiles::load_rows<T>(stage, lane, d, static_cast<const T*>(p.dh), p.lddh, r0, rows, col, p.out_dim, p.reach_dh);
+        if constexpr (sizeof(T) == 2) {
+          if (p.reach_dh != tiles::kElements) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              d[4 * j] = dh[j].x;
+              d[4 * j + 1] = dh[j].y;
+              d[4 * j + 2] = dh[j].z;
+              d[4 * j + 3] = dh[j].w;
+            }
+            if (c < 96) fetch(x, col + 32);
+          }
+        }
+        if (sizeof(T) == 4 || p.reach_dh == tiles::kElements) {
+          float f[32];
+          tiles::load_rows<T>(stage, lane, f, static_cast<const T*>(p.dh), p.lddh, r0, col < p.out_dim ? rows : 0, col, p.out_dim, p.reach_dh);
+          if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) d[j] = bf16x2_of(f[2 * j], f[2 * j + 1]);  // (bf16 already)
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) d[j] = __float_as_uint(f[j]);
+          }
+        }
       }
       tc::tmem_load_wait(y);
       tc::tmem_loaded(u);
       if (c == 96) acc.release<CG>(lane);
-      float f[32];
-      if constexpr (!BACKWARD) {
+      // y becomes h, or dy; u du.  bf16: two columns to a word
+      constexpr int kWords = sizeof(T) == 2 ? 16 : 32;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(y[j]) * gate_of<T>(p.gate, __uint_as_float(u[j]));
-        tiles::store32<T>(stage, lane, f, out, p.ldo, r0, rows, col, p.out_dim, p.reach);
-      } else {
+      for (int j = 0; j < 16; ++j) {
+        float a[2], b[2];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float2 a = gate_grad<T>(p.gate, __uint_as_float(u[j]));
-          u[j] = __float_as_uint(d[j] * __uint_as_float(y[j]) * a.y);
-          f[j] = d[j] * a.x;
+        for (int i = 0; i < 2; ++i) {
+          const float yy = __uint_as_float(y[2 * j + i]), uu = __uint_as_float(u[2 * j + i]);
+          if constexpr (BACKWARD) {
+            float g;
+            if constexpr (sizeof(T) == 2) g = __uint_as_float(i == 0 ? d[j] << 16 : d[j] & 0xFFFF0000u);
+            else g = __uint_as_float(d[2 * j + i]);
+            const float2 t = gate_grad<T, GATE>(uu);
+            a[i] = g * t.x;
+            b[i] = g * yy * t.y;
+          } else {
+            a[i] = yy * gate_of<T, GATE>(uu);
+          }
         }
-        tiles::store32<T>(stage, lane, f, out, p.ldo, r0, rows, col, p.out_dim, p.reach);
+        if constexpr (sizeof(T) == 2) {
+          y[j] = bf16x2_of(a[0], a[1]);
+          if constexpr (BACKWARD) u[j] = bf16x2_of(b[0], b[1]);
+        } else {
+          y[2 * j] = __float_as_uint(a[0]);
+          y[2 * j + 1] = __float_as_uint(a[1]);
+          if constexpr (BACKWARD) {
+            u[2 * j] = __float_as_uint(b[0]);
+            u[2 * j + 1] = __float_as_uint(b[1]);
+          }
+        }
+      }
 #pragma unroll
-        for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(u[j]);
-        tiles::store32<T>(stage, lane, f, out + p.u_col, p.ldo, r0, rows, col, p.out_dim, p.reach);
+      for (int h = 0; h < kWords / 16; ++h) {
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) w[j] = y[h * 16 + j];
+        tiles::store_rows<T>(stage, lane, w, out, p.ldo, r0, rows, col + h * 16, p.out_dim, p.reach);
+        if constexpr (BACKWARD) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) w[j] = u[h * 16 + j];
+          tiles::store_rows<T>(stage, lane, w, out + p.u_col, p.ldo, r0, rows, col + h * 16, p.out_dim, p.reach);
+        }
       }
     }
   }
@@ -239,7 +320,8 @@ __global__ void __launch_bounds__(256, kFewBlocks) k_gated_few(const FewParams p
       }
 #pragma unroll
       for (int o = 0; o < kFewOuts; ++o)
-        if (lane == o && o < outs) H[row_offset(r0 + r, p.ldh) + j0 + o] = from_f<T>(s[o] * gate_of<T>(p.gate, s[kFewOuts + o]));
+        if (lane == o && o < outs)
+          by_gate(p.gate, [&](auto gate) { H[row_offset(r0 + r, p.ldh) + j0 + o] = from_f<T>(s[o] * gate_of<T, decltype(gate)::value>(s[kFewOuts + o])); });
     }
   }
 }
@@ -340,10 +422,11 @@ cudaError_t launch_product(const mt_gated_linear& c, const Layout& l, GatedParam
   if (!tc::encode_bf16(&b, 3, w, width, 2 * l.m, width, c.groups, width * 2 * l.m, tiles::kBK, 128)) return cudaErrorInvalidValue;
   const size_t extra = rows_smem(c.groups), most = rows_smem(MT_MAX_GROUPS);
   const char* name = BACKWARD ? "k_gated_backward" : "k_gated_forward";
+  const long long units1 = (c.n / 128 + c.groups) * p.jtiles, units2 = (c.n / 256 + c.groups) * p.jtiles;  // at most
   if constexpr (sizeof(T) == 2) {
-    if (pair) return tiles::launch<Gated<T, BACKWARD>, 2>(name, a, b, p, (c.n / 256 + c.groups) * p.jtiles, extra, most, s);
+    if (pair) return tiles::launch<Gated<T, BACKWARD>, 2>(name, a, b, p, units2, extra, most, s);
   }
-  return tiles::launch<Gated<T, BACKWARD>, 1>(name, a, b, p, (c.n / 128 + c.groups) * p.jtiles, extra, most, s);
+  return tiles::launch<Gated<T, BACKWARD>, 1>(name, a, b, p, units1, extra, most, s);
 }
 
 }  // namespace

@@ -30,6 +30,10 @@ constexpr int kBK = 64;         // contraction per stage: one 128-byte swizzled 
 constexpr int kEpiWarps = 8;    // two for each 32 lanes of tensor memory: two teams
 constexpr int kWarps = 4 + kEpiWarps;  // copies, products, two idle, epilogue
 constexpr int kThreadsT = kWarps * 32;
+// Where an epilogue needs more registers than the launch gives a thread (Op::kSplit), the block's (384 threads x 168 at launch
+// = 64512) are split anew: 72 for a thread of the first four warps and 216 for one of the epilogue (128 x 72 + 256 x 216).
+constexpr int kRegsLaunch = 168, kRegsControl = 72, kRegsEpi = 216;
+static_assert(128 * kRegsControl + kEpiWarps * 32 * kRegsEpi <= kThreadsT * kRegsLaunch, "the split fits the launch");
 constexpr int kStageOut = 2048;  // bytes per epilogue warp: 32 rows x 64 bytes
 
 // Shared memory of a block: stages of both operands (of a pair's block: its half of the columns), and where the epilogue
@@ -113,6 +117,8 @@ __device__ __forceinline__ int kept_of(const typename Op::Params& p) {
 //   Op(p, dynamic memory)      every thread; may synchronise the block
 //   units(), unit(u)           the work
 //   warp(stage, quad, half, lane)   once, epilogue warps
+//   kAhead, ahead(x, ct)       before a tile is waited for
+//   kSplit                     more registers for the epilogue
 //   begin(x), tile(x, ct, acc, first, last), end(x)   a unit; a column tile's accumulator, or (promote) the parts of it
 template <class Op, int CG>
 __global__ void __launch_bounds__(kThreadsT, 1)
@@ -156,164 +162,168 @@ k_tiles(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
   Op op(p, ring + R::kBytes, rank);
   const long long units = op.units(), u0 = blockIdx.x / CG, ustep = gridDim.x / CG;
 
-  if (warp == 0) {
-    const bool one = tc::elect_one();
-    tc::Slot s;
-    long long issued = 0;
-    uint32_t a_phase = 0;
-    bool ok = true;
-    // one step of A into `to`
-    auto load_a = [&](uint8_t* to, uint64_t* full, int x, int r0, int k) {
-      if constexpr (CG == 2) {
-        const uint32_t at = tc::of_leader(full);
-        if constexpr (Op::kAMN) {
+  if (warp < 4) {
+    if constexpr (Op::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+    if (warp == 0) {
+      const bool one = tc::elect_one();
+      tc::Slot s;
+      long long issued = 0;
+      uint32_t a_phase = 0;
+      bool ok = true;
+      // one step of A into `to`
+      auto load_a = [&](uint8_t* to, uint64_t* full, int x, int r0, int k) {
+        if constexpr (CG == 2) {
+          const uint32_t at = tc::of_leader(full);
+          if constexpr (Op::kAMN) {
 #pragma unroll
-          for (int c = 0; c < kBM / 64; ++c) tc::tma_load_2d_pair(to + c * 8192, &map_a, at, x + r0 + c * 64, k * kBK);
+            for (int c = 0; c < kBM / 64; ++c) tc::tma_load_2d_pair(to + c * 8192, &map_a, at, x + r0 + c * 64, k * kBK);
+          } else {
+            tc::tma_load_2d_pair(to, &map_a, at, x + k * kBK, r0);
+          }
         } else {
-          tc::tma_load_2d_pair(to, &map_a, at, x + k * kBK, r0);
-        }
-      } else {
-        if constexpr (Op::kAMN) {
+          if constexpr (Op::kAMN) {
 #pragma unroll
-          for (int c = 0; c < kBM / 64; ++c) tc::tma_load_2d(to + c * 8192, &map_a, full, x + r0 + c * 64, k * kBK);
-        } else {
-          tc::tma_load_2d(to, &map_a, full, x + k * kBK, r0);
-        }
-      }
-    };
-    for (long long u = u0; u < units && ok; u += ustep) {
-      const Unit x = op.unit(u);
-      const int r0 = x.row0 + rank * kBM;
-      if constexpr (Op::kKeep) {
-        ok = tc::warp_wait(&bar.a_empty, a_phase ^ 1);
-        if (!ok) break;
-        a_phase ^= 1;
-        if (one) {  // a pair's copies count on the first block's barrier
-          if (rank == 0) tc::mbar_expect(&bar.a_full, CG * kept * R::kStageA);
-          const int steps = x.k1 - x.k0;
-          for (int i = 0; i < kept; ++i) load_a(ring + i * R::kStageA, &bar.a_full, i / steps * p.a_part, r0, x.k0 + i % steps);
-        }
-        __syncwarp();
-      }
-      for (int ct = x.ct0; ct < x.ct1 && ok; ++ct) {
-        for (int q = 0; q < p.passes && ok; ++q) {
-          const int ap = part_a(p.passes, q) * p.a_part, bp = part_b(p.passes, q) * p.b_part;
-          for (int k = x.k0; k < x.k1; ++k) {
-            ok = tc::warp_wait(&bar.empty[s.stage], s.phase ^ 1);
-            if (!ok) break;
-            uint8_t* st = stages_at + s.stage * R::kStage;
-            uint8_t* sb = st + (Op::kKeep ? 0 : R::kStageA);
-            if (one) {
-              uint64_t* full = &bar.full[s.stage];
-              if (rank == 0) tc::mbar_expect(full, CG * R::kStage);
-              if constexpr (!Op::kKeep) load_a(st, full, ap, r0, k);
-              if constexpr (CG == 2) {
-                const uint32_t at = tc::of_leader(full);
-                if constexpr (Op::kBMN) {
-#pragma unroll
-                  for (int c = 0; c < kCols / 64; ++c)
-                    tc::tma_load_2d_pair(sb + c * 8192, &map_b, at, bp + ct * BN + rank * kCols + c * 64, k * kBK);
-                } else if constexpr (Op::kTwoB) {  // the first block copies the first weights' columns, the second the second's
-                  tc::tma_load_3d_pair(sb, &map_b, at, bp + k * kBK, ct * kCols + rank * p.b_second, x.g);
-                } else {
-                  tc::tma_load_2d_pair(sb, &map_b, at, bp + k * kBK, ct * BN + rank * kCols);
-                }
-              } else {
-                if constexpr (Op::kBMN) {
-#pragma unroll
-                  for (int c = 0; c < kCols / 64; ++c) tc::tma_load_2d(sb + c * 8192, &map_b, full, bp + ct * BN + c * 64, k * kBK);
-                } else if constexpr (Op::kTwoB) {
-                  tc::tma_load_3d(sb, &map_b, full, bp + k * kBK, ct * (BN / 2), x.g);
-                  tc::tma_load_3d(sb + R::kStageB / 2, &map_b, full, bp + k * kBK, ct * (BN / 2) + p.b_second, x.g);
-                } else {
-                  tc::tma_load_2d(sb, &map_b, full, bp + k * kBK, ct * BN);
-                }
-              }
-            }
-            __syncwarp();
-            ++issued;
-            s.next(stages);
+            for (int c = 0; c < kBM / 64; ++c) tc::tma_load_2d(to + c * 8192, &map_a, full, x + r0 + c * 64, k * kBK);
+          } else {
+            tc::tma_load_2d(to, &map_a, full, x + k * kBK, r0);
           }
         }
-      }
-    }
-    ok = ok && tc::all_released(bar, s, issued, stages);
-    // what the first block signals of its last products has to have arrived here before this block ends
-    if (rank != 0) ok = tc::mbar_wait(&bar.done, 0) && ok;
-    if (!ok) {
-      if (one) tc::latch_status(p.status, MT_ECUDA);
-      if (rank == 0) {
-        tc::drain(bar, s, issued, stages);
-        if (Op::kKeep && (issued > 0 || a_phase != 0)) tc::mbar_wait(&bar.a_full, a_phase ^ 1);
-      }
-    }
-  } else if (warp == 1) {
-    if (rank == 0) {
-      constexpr uint32_t instr = tc::instr_bf16(kBM * CG, BN, Op::kAMN, Op::kBMN);
-      // descriptors' low words: of the ring's (and the kept A's) first stage, from one stage to the next, from one 16 of the
-      // contraction to the next
-      constexpr uint32_t kLeadA = Op::kAMN ? 8192 : 16, kLeadB = Op::kBMN ? 8192 : 16;
-      constexpr uint32_t kStepA = Op::kAMN ? 2048 >> 4 : 32 >> 4, kStepB = Op::kBMN ? 2048 >> 4 : 32 >> 4;
-      const bool one = tc::elect_one();
-      const uint32_t a0 = tc::desc_low(tc::smem_addr(Op::kKeep ? ring : stages_at), kLeadA);
-      const uint32_t b0 = tc::desc_low(tc::smem_addr(stages_at + (Op::kKeep ? 0 : R::kStageA)), kLeadB);
-      tc::Slot s;
-      int acc = 0;
-      uint32_t acc_phase = 0, a_phase = 0;
-      bool ok = true;
+      };
       for (long long u = u0; u < units && ok; u += ustep) {
         const Unit x = op.unit(u);
-        const int per_pass = x.k1 - x.k0;
+        const int r0 = x.row0 + rank * kBM;
         if constexpr (Op::kKeep) {
-          ok = tc::warp_wait<CG == 2>(&bar.a_full, a_phase);
-          a_phase ^= 1;
+          ok = tc::warp_wait(&bar.a_empty, a_phase ^ 1);
           if (!ok) break;
+          a_phase ^= 1;
+          if (one) {  // a pair's copies count on the first block's barrier
+            if (rank == 0) tc::mbar_expect(&bar.a_full, CG * kept * R::kStageA);
+            const int steps = x.k1 - x.k0;
+            for (int i = 0; i < kept; ++i) load_a(ring + i * R::kStageA, &bar.a_full, i / steps * p.a_part, r0, x.k0 + i % steps);
+          }
+          __syncwarp();
         }
         for (int ct = x.ct0; ct < x.ct1 && ok; ++ct) {
-          int part = 0;  // stages that the accumulator has
           for (int q = 0; q < p.passes && ok; ++q) {
-            uint32_t a_at = a0 + part_a(p.passes, q) * per_pass * (R::kStageA >> 4);  // (kept A)
-            for (int k = 0; k < per_pass; ++k) {
-              if (part == 0) {
-                ok = tc::warp_wait(&bar.acc_empty[acc], acc_phase ^ 1);
-                if (!ok) break;
-                tc::fence_after();
-              }
-              ok = tc::warp_wait<CG == 2>(&bar.full[s.stage], s.phase);
+            const int ap = part_a(p.passes, q) * p.a_part, bp = part_b(p.passes, q) * p.b_part;
+            for (int k = x.k0; k < x.k1; ++k) {
+              ok = tc::warp_wait(&bar.empty[s.stage], s.phase ^ 1);
               if (!ok) break;
-              tc::fence_after();
-              const uint32_t b = b0 + s.stage * (R::kStage >> 4), a = Op::kKeep ? a_at : a0 + s.stage * (R::kStage >> 4);
-              const bool closes = part + 1 == p.promote || (k + 1 == per_pass && q + 1 == p.passes);
+              uint8_t* st = stages_at + s.stage * R::kStage;
+              uint8_t* sb = st + (Op::kKeep ? 0 : R::kStageA);
               if (one) {
+                uint64_t* full = &bar.full[s.stage];
+                if (rank == 0) tc::mbar_expect(full, CG * R::kStage);
+                if constexpr (!Op::kKeep) load_a(st, full, ap, r0, k);
+                if constexpr (CG == 2) {
+                  const uint32_t at = tc::of_leader(full);
+                  if constexpr (Op::kBMN) {
 #pragma unroll
-                for (int i = 0; i < kBK / 16; ++i)
-                  tc::mma_bf16<CG>(tmem + acc * BN, a + i * kStepA, b + i * kStepB, instr, part > 0 || i > 0);
-                tc::mma_commit<CG>(&bar.empty[s.stage]);
-                if (closes) tc::mma_commit<CG>(&bar.acc_full[acc]);
+                    for (int c = 0; c < kCols / 64; ++c)
+                      tc::tma_load_2d_pair(sb + c * 8192, &map_b, at, bp + ct * BN + rank * kCols + c * 64, k * kBK);
+                  } else if constexpr (Op::kTwoB) {  // the first block copies the first weights' columns, the second the second's
+                    tc::tma_load_3d_pair(sb, &map_b, at, bp + k * kBK, ct * kCols + rank * p.b_second, x.g);
+                  } else {
+                    tc::tma_load_2d_pair(sb, &map_b, at, bp + k * kBK, ct * BN + rank * kCols);
+                  }
+                } else {
+                  if constexpr (Op::kBMN) {
+#pragma unroll
+                    for (int c = 0; c < kCols / 64; ++c) tc::tma_load_2d(sb + c * 8192, &map_b, full, bp + ct * BN + c * 64, k * kBK);
+                  } else if constexpr (Op::kTwoB) {
+                    tc::tma_load_3d(sb, &map_b, full, bp + k * kBK, ct * (BN / 2), x.g);
+                    tc::tma_load_3d(sb + R::kStageB / 2, &map_b, full, bp + k * kBK, ct * (BN / 2) + p.b_second, x.g);
+                  } else {
+                    tc::tma_load_2d(sb, &map_b, full, bp + k * kBK, ct * BN);
+                  }
+                }
               }
               __syncwarp();
-              a_at += R::kStageA >> 4;
+              ++issued;
               s.next(stages);
-              ++part;
-              if (closes) {
-                if (++acc == kAccs) {
-                  acc = 0;
-                  acc_phase ^= 1;
-                }
-                part = 0;
-              }
             }
           }
         }
-        if (Op::kKeep && ok && one) tc::mma_commit<CG>(&bar.a_empty);
-        __syncwarp();
       }
-      if (one) tc::mma_commit<CG>(&bar.done);  // tensor memory is freed only when no product writes it, also after a wait ran out
-      __syncwarp();
-      ok = tc::mbar_wait(&bar.done, 0) && ok;
-      if (!ok && one) tc::latch_status(p.status, MT_ECUDA);
+      ok = ok && tc::all_released(bar, s, issued, stages);
+      // what the first block signals of its last products has to have arrived here before this block ends
+      if (rank != 0) ok = tc::mbar_wait(&bar.done, 0) && ok;
+      if (!ok) {
+        if (one) tc::latch_status(p.status, MT_ECUDA);
+        if (rank == 0) {
+          tc::drain(bar, s, issued, stages);
+          if (Op::kKeep && (issued > 0 || a_phase != 0)) tc::mbar_wait(&bar.a_full, a_phase ^ 1);
+        }
+      }
+    } else if (warp == 1) {
+      if (rank == 0) {
+        constexpr uint32_t instr = tc::instr_bf16(kBM * CG, BN, Op::kAMN, Op::kBMN);
+        // descriptors' low words: of the ring's (and the kept A's) first stage, from one stage to the next, from one 16 of the
+        // contraction to the next
+        constexpr uint32_t kLeadA = Op::kAMN ? 8192 : 16, kLeadB = Op::kBMN ? 8192 : 16;
+        constexpr uint32_t kStepA = Op::kAMN ? 2048 >> 4 : 32 >> 4, kStepB = Op::kBMN ? 2048 >> 4 : 32 >> 4;
+        const bool one = tc::elect_one();
+        const uint32_t a0 = tc::desc_low(tc::smem_addr(Op::kKeep ? ring : stages_at), kLeadA);
+        const uint32_t b0 = tc::desc_low(tc::smem_addr(stages_at + (Op::kKeep ? 0 : R::kStageA)), kLeadB);
+        tc::Slot s;
+        int acc = 0;
+        uint32_t acc_phase = 0, a_phase = 0;
+        bool ok = true;
+        for (long long u = u0; u < units && ok; u += ustep) {
+          const Unit x = op.unit(u);
+          const int per_pass = x.k1 - x.k0;
+          if constexpr (Op::kKeep) {
+            ok = tc::warp_wait<CG == 2>(&bar.a_full, a_phase);
+            a_phase ^= 1;
+            if (!ok) break;
+          }
+          for (int ct = x.ct0; ct < x.ct1 && ok; ++ct) {
+            int part = 0;  // stages that the accumulator has
+            for (int q = 0; q < p.passes && ok; ++q) {
+              uint32_t a_at = a0 + part_a(p.passes, q) * per_pass * (R::kStageA >> 4);  // (kept A)
+              for (int k = 0; k < per_pass; ++k) {
+                if (part == 0) {
+                  ok = tc::warp_wait(&bar.acc_empty[acc], acc_phase ^ 1);
+                  if (!ok) break;
+                  tc::fence_after();
+                }
+                ok = tc::warp_wait<CG == 2>(&bar.full[s.stage], s.phase);
+                if (!ok) break;
+                tc::fence_after();
+                const uint32_t b = b0 + s.stage * (R::kStage >> 4), a = Op::kKeep ? a_at : a0 + s.stage * (R::kStage >> 4);
+                const bool closes = part + 1 == p.promote || (k + 1 == per_pass && q + 1 == p.passes);
+                if (one) {
+#pragma unroll
+                  for (int i = 0; i < kBK / 16; ++i)
+                    tc::mma_bf16<CG>(tmem + acc * BN, a + i * kStepA, b + i * kStepB, instr, part > 0 || i > 0);
+                  tc::mma_commit<CG>(&bar.empty[s.stage]);
+                  if (closes) tc::mma_commit<CG>(&bar.acc_full[acc]);
+                }
+                __syncwarp();
+                a_at += R::kStageA >> 4;
+                s.next(stages);
+                ++part;
+                if (closes) {
+                  if (++acc == kAccs) {
+                    acc = 0;
+                    acc_phase ^= 1;
+                  }
+                  part = 0;
+                }
+              }
+            }
+          }
+          if (Op::kKeep && ok && one) tc::mma_commit<CG>(&bar.a_empty);
+          __syncwarp();
+        }
+        if (one) tc::mma_commit<CG>(&bar.done);  // tensor memory is freed only when no product writes it, also after a wait ran out
+        __syncwarp();
+        ok = tc::mbar_wait(&bar.done, 0) && ok;
+        if (!ok && one) tc::latch_status(p.status, MT_ECUDA);
+      }
     }
-  } else if (warp >= 4) {
+  } else {
+    if constexpr (Op::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
     const int quad = warp & 3, team = (warp - 4) >> 2;
     op.warp(ring + R::kTotal + (warp - 4) * kStageOut, quad, team, lane);
     uint32_t seq = 0;  // accumulators so far
@@ -331,6 +341,7 @@ k_tiles(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
             continue;
           }
           seq += steps > 0;
+          if constexpr (Op::kAhead) op.ahead(x, ct);
           if (steps > 0) {
             ok = __all_sync(kFull, tc::mbar_wait(&bar.acc_full[b], parity));
             if (!ok) break;
@@ -490,6 +501,12 @@ cudaError_t launch(const char* name, const CUtensorMap& a, const CUtensorMap& b,
   static SmemLimit limit;
   const cudaError_t e = limit.allow(k_tiles<Op, CG>, ring + most);
   if (e != cudaSuccess) return e;
+  if constexpr (Op::kSplit) {  // the split of the registers needs the launch to bring them
+    cudaFuncAttributes f;
+    const cudaError_t fe = cudaFuncGetAttributes(&f, reinterpret_cast<const void*>(k_tiles<Op, CG>));
+    if (fe != cudaSuccess) return fe;
+    if (f.numRegs < kRegsLaunch) return cudaErrorInvalidValue;
+  }
   const int blocks = sm_count() / CG;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((units < blocks ? (units > 0 ? units : 1) : blocks) * CG));

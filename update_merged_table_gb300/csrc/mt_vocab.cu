@@ -71,16 +71,38 @@ __device__ __forceinline__ bool row_there(const VocabRows& p, long long row) {
   return there;
 }
 
-// A warp per 32 rows.
+// A block per 32 rows: a thread per row where it has one target, else a warp.
 __global__ void __launch_bounds__(256) k_vocab_mark(const VocabRows p) {
   lead();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long words = (p.n + 31) / 32;
-  for (long long w = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5; w < words; w += ((long long)gridDim.x * blockDim.x) >> 5) {
-    const long long row = w * 32 + lane;
-    const bool there = row < p.n && row_there(p, row);
-    const unsigned bits = __ballot_sync(kFull, there);
-    if (lane == 0) p.mask[w] = bits;
+  if (!p.distill) {
+    for (long long w = (long long)blockIdx.x * 8 + warp; w < words; w += (long long)gridDim.x * 8) {
+      const unsigned bits = __ballot_sync(kFull, w * 32 + lane < p.n && row_there(p, w * 32 + lane));
+      if (lane == 0) p.mask[w] = bits;
+    }
+    return;
+  }
+  __shared__ uint32_t s_bits;
+  for (long long w = blockIdx.x; w < words; w += gridDim.x) {
+    if (threadIdx.x == 0) s_bits = 0u;
+    __syncthreads();
+    for (int r = warp; r < 32; r += 8) {
+      const long long row = w * 32 + r;
+      bool there = false, bad = false;
+      if (row < p.n) {
+        for (int k = lane; k < p.top; k += 32) {
+          const long long id = id_at(p, row * p.top + k);
+          bad |= id >= p.vocab;
+          there |= pair_there(p, row * p.top + k, id);
+        }
+      }
+      if (bad && p.status != nullptr) atomicCAS(p.status, 0, MT_EINVAL);
+      if (__any_sync(kFull, there) && lane == 0) atomicOr(&s_bits, 1u << r);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) p.mask[w] = s_bits;
+    __syncthreads();
   }
 }
 
@@ -96,9 +118,11 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 
 // MARK: few rows, which every block looks through itself (no k_vocab_mark before it).
-constexpr int kMarkPairs = 8192;  // targets, or pairs, of so few rows
+constexpr int kMarkPairs = 2048;  // targets, or pairs, of so few rows
 
-// A block per 32 rows, a warp per live row; the last block writes how many there are and puts zeros behind them up to the
+constexpr int kRowBlocks = 4;  // blocks to 32 rows: a warp has one row at most
+
+// A quarter of 32 rows' live ones per block, a warp each; the last block writes how many there are and puts zeros behind them up to the
 // next 128 rows (steps of dW's contraction).  T: the rows' type; AL: they can be read in 16-byte vectors.
 template <typename T, bool AL, bool MARK>
 __global__ void __launch_bounds__(256) k_vocab_rows(const VocabRows p) {
@@ -109,7 +133,9 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const VocabRows p) {
   __shared__ int s_base;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long words = (p.n + 31) / 32;
-  for (long long w = blockIdx.x; w < words; w += gridDim.x) {
+  for (long long q = blockIdx.x; q < words * kRowBlocks; q += gridDim.x) {
+    const long long w = q / kRowBlocks;
+    const int share = (int)(q % kRowBlocks);
     if (threadIdx.x == 0) s_base = 0;
     __syncthreads();
     int before = 0;
@@ -127,9 +153,9 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const VocabRows p) {
     __syncthreads();
     const int base = s_base;
     const int own = __popc(bits);
-    if (threadIdx.x < 32 && w * 32 + lane < p.n)
+    if (share == 0 && threadIdx.x < 32 && w * 32 + lane < p.n)
       p.pos[w * 32 + lane] = bits >> lane & 1 ? base + __popc(bits & ((1u << lane) - 1u)) : -1;
-    for (int k = warp; k < own; k += 8) {
+    for (int k = share * 8 + warp; k < own; k += 8 * kRowBlocks) {
       const long long row = w * 32 + __fns(bits, 0, k + 1);
       const size_t at = (size_t)base + k;
       // the row's values
@@ -198,7 +224,7 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const VocabRows p) {
         p.coef[at] = make_float4(lse * kLog2e, g * (1.0f + 2.0f * p.z_loss * lse), g * p.smoothing / (float)p.vocab, g);
       }
     }
-    if (w + 1 == words) {
+    if (q + 1 == words * kRowBlocks) {
       const int live = base + own;
       if (threadIdx.x == 0) *p.live = live;
       const size_t width = (size_t)kParts * p.dp;
@@ -482,14 +508,14 @@ cudaError_t launch_rows(const mt_vocab_loss& c, const Layout& l, char* ws, const
   cudaError_t e = cudaSuccess;
   if (!mark) {
     MT_LAUNCH("k_vocab_mark", s);
-    k_vocab_mark<<<grid_for(c.n, 256, 8), 256, 0, s>>>(r);
+    k_vocab_mark<<<grid_for(c.top > 0 ? tiles_of(c.n, 32) * 256 : c.n, 256, 8), 256, 0, s>>>(r);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
   {
     const bool al = rows_wide(Rows{const_cast<void*>(c.x), c.n <= 1 ? c.dim : c.ldx, nullptr, nullptr}, c.dim, c.dtype);
     const size_t smem = c.top > 0 ? (size_t)8 * c.top * 8 : 0;
-    const int grid = grid_for(tiles_of(c.n, 32) * 256, 256, 8);
+    const int grid = grid_for(tiles_of(c.n, 32) * kRowBlocks * 256, 256, 8);
     static SmemLimit limit[8];
     auto go = [&](auto kernel, int i) {
       const cudaError_t le = limit[i].allow(kernel, (size_t)8 * MT_MAX_TOP * 8);

@@ -34,7 +34,7 @@ template <int CG, bool KEEP>
 struct Logits {
   using Params = LogitParams;
   static constexpr int kBN = 256;
-  static constexpr bool kAMN = false, kBMN = false, kTwoB = false, kTeams = true, kKeep = KEEP;
+  static constexpr bool kAMN = false, kBMN = false, kTwoB = false, kTeams = true, kKeep = KEEP, kAhead = false, kSplit = false;
   const Params& p;
   int rank, live, rt, chunks;
   uint8_t* stage;

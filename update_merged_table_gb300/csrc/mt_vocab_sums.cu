@@ -25,7 +25,7 @@ template <int BN, bool FP32, bool VOCAB, int CG>
 struct Sum {
   using Params = SumParams;
   static constexpr int kBN = BN;
-  static constexpr bool kAMN = VOCAB, kBMN = true, kTeams = !FP32, kKeep = false;
+  static constexpr bool kAMN = VOCAB, kBMN = true, kTeams = !FP32, kKeep = false, kAhead = false, kSplit = false;
   const Params& p;
   int rank, rows, rt, steps, whole, runs, quad, half, lane;  // whole: row tiles with the whole contraction
   uint8_t* stage;
