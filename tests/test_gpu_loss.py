@@ -122,7 +122,7 @@ def test_scale_smoothing_and_z_loss(scale, smoothing, z_loss, dtype):
 
 
 @pytest.mark.parametrize("n,v,d,top", [(2048, 20000, 256, 0), (4096, 5000, 512, 0), (2048, 20000, 256, 16), (65537, 4500, 16, 0), (3, 100003, 256, 0),
-                                       (20000, 300, 64, 0)])
+                                       (20000, 300, 64, 0), (5000, 30000, 200, 0), (700, 40000, 130, 3), (20000, 2500, 100, 0), (9000, 9000, 264, 0)])
 def test_long(n, v, d, top):
     """Pairs of blocks, vocabularies in several pieces and runs, few rows and few entries."""
     check_all(make(4, n, v, d, "bf16", top=top), "bf16")

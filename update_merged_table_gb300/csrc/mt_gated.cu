@@ -93,13 +93,14 @@ template <typename T, bool BACKWARD>
 struct Gated {
   using Params = GatedParams;
   static constexpr int kBN = 256;
-  static constexpr bool kAMN = false, kBMN = false, kTwoB = true, kTeams = true, kKeep = false;
+  static constexpr bool kAMN = false, kBMN = false, kTwoB = true, kTeams = true, kKeep = false, kSingle = true;
+  static constexpr int kStageOut = 2048;  // 32 rows x 64 bytes
   static constexpr bool kSplit = BACKWARD && sizeof(T) == 2;
   static constexpr bool kAhead = BACKWARD && sizeof(T) == 2;  // dh of a tile's first columns is on its way before the tile
   const Params& p;
   const long long* off;
   const int* cum;
-  int rank, rows_per_tile, quad, lane;
+  int rank, rows_per_tile, quad, lane, group = 0;
   uint8_t* stage;
   uint4 dh[4];
 
@@ -118,11 +119,15 @@ struct Gated {
     return c;
   }
   __device__ long long units() const { return (long long)cum[p.groups] * p.jtiles; }
-  __device__ Unit unit(long long u) const {  // columns fastest: a row tile's products read the same rows of x
-    const int rt = (int)(u / p.jtiles), c = (int)(u - (long long)rt * p.jtiles);
+  // Units come in ascending order: the group is looked for from the last one's on.  Columns fastest: a row tile's products
+  // read the same rows of x.
+  __device__ Unit unit(long long u) {
+    const unsigned rt = u <= 0xFFFFFFFFll ? (unsigned)u / (unsigned)p.jtiles : (unsigned)(u / p.jtiles);
+    const int c = (int)(u - (long long)rt * p.jtiles);
+    while (cum[group + 1] <= (int)rt) ++group;
     Unit x;
-    x.g = tile_group(cum, p.groups, rt);
-    x.row0 = (int)off[x.g] + (rt - cum[x.g]) * rows_per_tile;
+    x.g = group;
+    x.row0 = (int)off[x.g] + ((int)rt - cum[x.g]) * rows_per_tile;
     x.end = (int)off[x.g + 1];
     x.ct0 = c;
     x.ct1 = c + 1;
@@ -139,6 +144,7 @@ struct Gated {
     zero_outside<T>(off, p.groups, p.n, static_cast<T*>(p.out), p.ldo, J, tiles::kEpiWarps * 32, (h * 4 + q) * 32 + l);
   }
   __device__ void begin(const Unit&) {}
+  __device__ void finish() {}
   __device__ void end(const Unit&) {}
 
   // 32 columns of dh as they lie, where they lie on 16 bytes

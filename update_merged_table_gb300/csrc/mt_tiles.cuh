@@ -34,7 +34,6 @@ constexpr int kThreadsT = kWarps * 32;
 // = 64512) are split anew: 72 for a thread of the first four warps and 216 for one of the epilogue (128 x 72 + 256 x 216).
 constexpr int kRegsLaunch = 168, kRegsControl = 72, kRegsEpi = 216;
 static_assert(128 * kRegsControl + kEpiWarps * 32 * kRegsEpi <= kThreadsT * kRegsLaunch, "the split fits the launch");
-constexpr int kStageOut = 2048;  // bytes per epilogue warp: 32 rows x 64 bytes
 
 // Shared memory of a block: stages of both operands (of a pair's block: its half of the columns), and where the epilogue
 // turns its rows.  KEEP: A's tile (all of its contraction, up to kKept steps) is copied once per unit and stays, and the
@@ -45,7 +44,6 @@ struct Ring {
   static constexpr int kStageA = kBM * kBK * 2, kStageB = BN / CG * kBK * 2;
   static constexpr int kStage = kStageB + (KEEP ? 0 : kStageA);
   static constexpr int kTotal = 196608;
-  static constexpr int kBytes = kTotal + kEpiWarps * kStageOut;
   static __host__ __device__ constexpr int stages(int kept) {
     const int n = (kTotal - kept * kStageA) / kStage;
     return n < 8 ? n : 8;
@@ -116,9 +114,11 @@ __device__ __forceinline__ int kept_of(const typename Op::Params& p) {
 //                              before it is handed over), status
 //   Op(p, dynamic memory)      every thread; may synchronise the block
 //   units(), unit(u)           the work
-//   warp(stage, quad, half, lane)   once, epilogue warps
+//   kStageOut                  bytes of shared memory for each epilogue warp (on 1024 bytes where they are a multiple of it)
+//   warp(stage, quad, team, lane), finish()   once, epilogue warps: before the first unit, after the last
 //   kAhead, ahead(x, ct)       before a tile is waited for
 //   kSplit                     more registers for the epilogue
+//   kSingle                    every unit is one tile with one accumulator (and teams take turns)
 //   begin(x), tile(x, ct, acc, first, last), end(x)   a unit; a column tile's accumulator, or (promote) the parts of it
 template <class Op, int CG>
 __global__ void __launch_bounds__(kThreadsT, 1)
@@ -159,7 +159,7 @@ k_tiles(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
   const uint32_t tmem = bar.tmem;
   lead();
   follow();
-  Op op(p, ring + R::kBytes, rank);
+  Op op(p, ring + R::kTotal + kEpiWarps * Op::kStageOut, rank);
   const long long units = op.units(), u0 = blockIdx.x / CG, ustep = gridDim.x / CG;
 
   if (warp < 4) {
@@ -325,15 +325,19 @@ k_tiles(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
   } else {
     if constexpr (Op::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
     const int quad = warp & 3, team = (warp - 4) >> 2;
-    op.warp(ring + R::kTotal + (warp - 4) * kStageOut, quad, team, lane);
+    op.warp(ring + R::kTotal + (warp - 4) * Op::kStageOut, quad, team, lane);
     uint32_t seq = 0;  // accumulators so far
     bool ok = true;
     for (long long u = u0; u < units && ok; u += ustep) {
+      if (Op::kSingle && (seq & 1) != team) {  // the other team's
+        ++seq;
+        continue;
+      }
       const Unit x = op.unit(u);
       op.begin(x);
       const int steps = (x.k1 - x.k0) * p.passes;
+      const int parts = steps <= p.promote ? 1 : (steps + p.promote - 1) / p.promote;
       for (int ct = x.ct0; ct < x.ct1 && ok; ++ct) {
-        const int parts = steps == 0 ? 1 : (steps + p.promote - 1) / p.promote;
         for (int part = 0; part < parts; ++part) {
           const uint32_t b = seq % kAccs, parity = seq / kAccs & 1;
           if (Op::kTeams && (steps > 0 ? seq & 1 : 0) != team) {
@@ -353,6 +357,7 @@ k_tiles(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
       }
       if (ok) op.end(x);
     }
+    op.finish();
     if (!ok) tc::latch_status(p.status, MT_ECUDA);
   }
   __syncwarp();
@@ -497,7 +502,7 @@ __device__ __forceinline__ void store32(uint8_t* stage, int lane, const float (&
 template <class Op, int CG>
 cudaError_t launch(const char* name, const CUtensorMap& a, const CUtensorMap& b, const typename Op::Params& p, long long units,
                    size_t extra, size_t most, cudaStream_t s) {
-  constexpr size_t ring = 1024 + Ring<Op::kBN, CG, Op::kKeep>::kBytes;  // the stages start on 1024 bytes
+  constexpr size_t ring = 1024 + Ring<Op::kBN, CG, Op::kKeep>::kTotal + kEpiWarps * Op::kStageOut;  // the stages start on 1024 bytes
   static SmemLimit limit;
   const cudaError_t e = limit.allow(k_tiles<Op, CG>, ring + most);
   if (e != cudaSuccess) return e;

@@ -719,6 +719,7 @@ int mt_vocab_loss_backward(const mt_vocab_loss* c, const float* dloss, const flo
       const bool pair = !fp32 && pair_rows(c->n, tiles_of(columns, 256), p.steps);
       if (!tc::encode_bf16(&a, 2, base + l.xs, xw, l.rows, xw, 1, 0, 64, 128)) return MT_ECUDA;
       if (!tc::encode_bf16(&b, 2, wv, w.width, columns, w.ld, 1, 0, 64, pair ? 128 : 256)) return MT_ECUDA;
+      if (!fp32 && !tc::encode_bf16(&p.map_dz, 2, p.dz, zw, l.rows, zw, 1, 0, 64, 32)) return MT_ECUDA;
       e = launch_logit_grad(p, l.parts, a, b, tiles_of(c->n, pair ? 256 : 128), pair, s);
     }
     SumParams q{};

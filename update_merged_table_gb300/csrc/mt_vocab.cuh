@@ -38,6 +38,7 @@ struct LogitParams {
   const float4* coef;   // [n] {lse * log2(e), factor of p, what is taken off everywhere, factor of the targets' shares}
   __nv_bfloat16* dz;    // [stride][parts][width]
   int width;            // columns of a part of dz: those of the piece in multiples of 64, zeros behind them
+  CUtensorMap map_dz;   // dz in boxes of 64 columns by 32 rows
 };
 constexpr int kLogitKept = 8;  // steps of 64 columns
 cudaError_t launch_logit_stats(const LogitParams& p, const CUtensorMap& a, const CUtensorMap& b, long long row_tiles, bool pair,
@@ -70,7 +71,9 @@ cudaError_t launch_rows_sum(const SumParams& p, bool fp32, const CUtensorMap& a,
 cudaError_t launch_vocab_sum(const SumParams& p, bool fp32, const CUtensorMap& a, const CUtensorMap& b, long long row_tiles, bool pair,
                              cudaStream_t s);
 
-// The gradients for narrow rows, without a dz in memory (mt_vocab_fused.cu): bf16, up to 128 columns.
+// The gradients for narrow rows, without a dz in memory (mt_vocab_fused.cu): bf16, up to 128 columns.  Measured, backward
+// of 16,384 rows x 50,000 entries, without dz against with: 64 columns 527 against 950 us, 128 693 against 1013, 192 1336
+// against 1067; of 2048 x 100,003: 156 / 263, 203 / 281, 361 / 295.
 struct FusedParams {
   int32_t* status;
   LiveRows rows;

@@ -32,8 +32,9 @@ constexpr int kAccAt = kS * kT;          // tensor memory: these, then the sum
 
 struct FusedBarriers {
   uint64_t full[8], empty[8];        // a streamed tile has landed; its products are done
-  uint64_t s_full[kS], s_empty[kS];  // S is finished; it has been read
-  uint64_t dz_full[3], dz_empty[3];  // dz is in shared memory; its products are done
+  uint64_t s_full[3], s_empty[3];    // S is finished; it has been read
+  uint64_t dz_full[3];               // dz is in shared memory
+  uint64_t dz_empty[3];              // the products of a team's last tile of dz are done
   uint64_t kept_full, kept_empty;    // the kept tile has landed; its products are done
   uint64_t acc_full, acc_empty;      // a unit's sum is finished; it has been read
   uint64_t s_done, done;             // every product issued is done
@@ -45,8 +46,8 @@ template <int KS>
 struct FusedRing {
   static constexpr int kTile = KS * kSlab;
   static constexpr int kTeams = KS == 1 ? 3 : 2, kThreads = (4 + kTeams * 4) * 32;
-  static constexpr int kDzs = kTeams, kStages = KS == 1 ? 6 : 4;
-  static constexpr int kBytes = (1 + kStages) * kTile + kDzs * kDz;
+  static constexpr int kStages = KS == 1 ? 6 : 4;
+  static constexpr int kBytes = (1 + kStages) * kTile + kTeams * kDz;
 };
 
 // A unit: a kept tile and streamed tiles [t0, t1).
@@ -85,7 +86,7 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
       tc::mbar_init(&bar.s_full[i], 1);
       tc::mbar_init(&bar.s_empty[i], 4);
     }
-    for (int i = 0; i < R::kDzs; ++i) {
+    for (int i = 0; i < 3; ++i) {
       tc::mbar_init(&bar.dz_full[i], 4);
       tc::mbar_init(&bar.dz_empty[i], 1);
     }
@@ -214,8 +215,8 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
       ok = tc::warp_wait(&bar.acc_empty, acc_phase ^ 1);
       acc_phase ^= 1;
       for (int t = x.t0; t < x.t1 && ok; ++t) {
-        const uint32_t b = n % R::kDzs;
-        ok = tc::warp_wait(&bar.dz_full[b], n / R::kDzs & 1);
+        const uint32_t b = n % R::kTeams;
+        ok = tc::warp_wait(&bar.dz_full[b], n / R::kTeams & 1);
         if (!ok) break;
         tc::fence_after();
         const uint32_t from = dz + b * (kDz >> 4), with = ring + s.stage * (R::kTile >> 4);
@@ -225,7 +226,7 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             tc::mma_bf16<1>(tmem + kAccAt, from + ((VOCAB ? i * 2048 : (i >> 2) * kSlab + (i & 3) * 32) >> 4), with + (i * 2048 >> 4), instr,
                            t > x.t0 || i > 0);
           tc::mma_commit<1>(&bar.empty[s.stage]);
-          tc::mma_commit<1>(&bar.dz_empty[b]);
+          tc::mma_commit<1>(&bar.dz_empty[n % R::kTeams]);
         }
         __syncwarp();
         ++n;
@@ -292,6 +293,7 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
           to.start(p.rows, row_at(x.kept), work.live, x.t0 * kT);
         }
         for (int t = first; t < x.t1; t += R::kTeams) {
+          // (a team sees every third S or so of a buffer: its tiles' S come in order, so that one of an earlier turn is done)
           const uint32_t of = n + (t - x.t0), b = of % kS, from = tmem + b * kT + lanes;
           const int row = row_at(VOCAB ? t : x.kept), v0 = (VOCAB ? x.kept : t) * kT;
           if (VOCAB) {

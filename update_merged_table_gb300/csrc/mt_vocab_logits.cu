@@ -34,7 +34,8 @@ template <int CG, bool KEEP>
 struct Logits {
   using Params = LogitParams;
   static constexpr int kBN = 256;
-  static constexpr bool kAMN = false, kBMN = false, kTwoB = false, kTeams = true, kKeep = KEEP, kAhead = false, kSplit = false;
+  static constexpr bool kAMN = false, kBMN = false, kTwoB = false, kTeams = true, kKeep = KEEP, kAhead = false, kSplit = false, kSingle = false;
+  static constexpr int kStageOut = 4096;  // 32 rows x 128 bytes
   const Params& p;
   int rank, live, rt, chunks;
   uint8_t* stage;
@@ -128,6 +129,7 @@ struct Stats : Logits<CG, KEEP> {
     sum = fmaf(sum, exp2_of(top - off), pair_sum(add2(s[0], s[1])));
     top = now;
   }
+  __device__ void finish() {}
   template <int G>
   __device__ __forceinline__ void tile(const Unit&, int ct, const Acc& acc, bool, bool) {
     const LogitParams& p = this->p;
@@ -159,10 +161,13 @@ struct Grad : Logits<CG, KEEP> {
     k = this->row < this->live ? this->p.coef[this->row] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   }
   __device__ void end(const Unit&) {}
-  __device__ __forceinline__ void columns(uint32_t (&v)[32], int at0, int left, long long r0, bool some) {
+  __device__ void finish() {
+    if (!SPLIT && this->lane == 0) tc::bulk_done();
+  }
+  // dz of 32 columns
+  __device__ __forceinline__ void columns(const uint32_t (&v)[32], int at0, int left, bool some, float (&f)[32]) {
     const LogitParams& p = this->p;
     const int col = p.v0 + at0;
-    float f[32];
     const f32x2 s2 = both(p.scale2), x2 = both(-k.x), y2 = both(k.y), z2 = both(-k.z);
 #pragma unroll
     for (int j = 0; j < 32; j += 2) {
@@ -179,40 +184,64 @@ struct Grad : Logits<CG, KEEP> {
       for (int j = 0; j < 32; ++j)
         if (!(there >> j & 1)) f[j] = 0.0f;
     }
-    if constexpr (!SPLIT) {
-      tiles::store32<__nv_bfloat16>(this->stage, this->lane, f, p.dz, p.width, r0, 32, at0, p.width, tiles::kSectors);
-    } else {
-      uint32_t w[3][16];
+  }
+  // bf16: 32 columns into their half of the warp's 32 rows x 128 bytes (piece c of row r at c ^ (r & 7), as copies with the
+  // 128-byte swizzle have it), which leave by one copy: the warps neither turn rows nor wait for their stores.
+  __device__ __forceinline__ void to_stage(const float (&f)[32], int half) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        __nv_bfloat16 a[3], b[3];
-        split3(f[2 * j], a[0], a[1], a[2]);
-        split3(f[2 * j + 1], b[0], b[1], b[2]);
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<uint4*>(this->stage + this->lane * 128 + (((half * 4 + q) ^ (this->lane & 7)) << 4)) =
+          make_uint4(bf16x2_of(f[q * 8], f[q * 8 + 1]), bf16x2_of(f[q * 8 + 2], f[q * 8 + 3]), bf16x2_of(f[q * 8 + 4], f[q * 8 + 5]),
+                     bf16x2_of(f[q * 8 + 6], f[q * 8 + 7]));
+  }
+  __device__ __forceinline__ void put_split(const float (&f)[32], int at0, long long r0) {
+    const LogitParams& p = this->p;
+    uint32_t w[3][16];
 #pragma unroll
-        for (int q = 0; q < 3; ++q) w[q][j] = bf16_bits(a[q], b[q]);
-      }
+    for (int j = 0; j < 16; ++j) {
+      __nv_bfloat16 a[3], b[3];
+      split3(f[2 * j], a[0], a[1], a[2]);
+      split3(f[2 * j + 1], b[0], b[1], b[2]);
 #pragma unroll
-      for (int q = 0; q < 3; ++q)
-        tiles::store_rows<__nv_bfloat16>(this->stage, this->lane, w[q], p.dz + (size_t)q * p.width, (size_t)3 * p.width, r0, 32, at0, p.width, tiles::kSectors);
+      for (int q = 0; q < 3; ++q) w[q][j] = bf16_bits(a[q], b[q]);
     }
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+      tiles::store_rows<__nv_bfloat16>(this->stage, this->lane, w[q], p.dz + (size_t)q * p.width, (size_t)3 * p.width, r0, 32, at0, p.width, tiles::kSectors);
   }
   template <int G>
   __device__ __forceinline__ void tile(const Unit& x, int ct, const Acc& acc, bool, bool) {
     constexpr int kBN = Base::kBN;
     const int at = ct * kBN, left = this->p.columns - at;
-    const long long r0 = x.row0 + this->rank * tiles::kBM + this->quad * 32;
+    const int r0 = x.row0 + this->rank * tiles::kBM + this->quad * 32;
     const bool some = left < kBN || __any_sync(kFull, this->to.next < this->p.v0 + at + kBN || this->row >= this->live);
     uint32_t v[2][32];
+    float f[32];
     acc.load(0, v[0]);
 #pragma unroll 1
     for (int c = 0; c < kBN; c += 64) {
       tc::tmem_load_wait(v[0]);
       acc.load(c + 32, v[1]);
-      columns(v[0], at + c, left - c, r0, some);
+      columns(v[0], at + c, left - c, some, f);
+      if constexpr (SPLIT) {
+        put_split(f, at + c, r0);
+      } else {
+        if (this->lane == 0) tc::bulk_read();  // the last 64 columns' copy has read them
+        __syncwarp();
+        to_stage(f, 0);
+      }
       tc::tmem_load_wait(v[1]);
       if (c + 64 < kBN) acc.load(c + 64, v[0]);
       else acc.release<G>(this->lane);
-      columns(v[1], at + c + 32, left - c - 32, r0, some);
+      columns(v[1], at + c + 32, left - c - 32, some, f);
+      if constexpr (SPLIT) {
+        put_split(f, at + c + 32, r0);
+      } else {
+        to_stage(f, 1);
+        tc::fence_async_proxy();
+        __syncwarp();
+        if (this->lane == 0 && at + c < this->p.width) tc::tma_store_2d(&this->p.map_dz, this->stage, at + c, r0);
+      }
     }
   }
 };

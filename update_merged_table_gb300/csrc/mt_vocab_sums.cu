@@ -25,7 +25,8 @@ template <int BN, bool FP32, bool VOCAB, int CG>
 struct Sum {
   using Params = SumParams;
   static constexpr int kBN = BN;
-  static constexpr bool kAMN = VOCAB, kBMN = true, kTeams = !FP32, kKeep = false, kAhead = false, kSplit = false;
+  static constexpr bool kAMN = VOCAB, kBMN = true, kTeams = !FP32, kKeep = false, kAhead = false, kSplit = false, kSingle = false;
+  static constexpr int kStageOut = 2048;  // 32 rows x 64 bytes
   const Params& p;
   int rank, rows, rt, steps, whole, runs, quad, half, lane;  // whole: row tiles with the whole contraction
   uint8_t* stage;
@@ -46,8 +47,9 @@ struct Sum {
   }
   __device__ long long units() const { return ((long long)whole + (long long)(rt - whole) * runs) * p.ctiles; }
   __device__ Unit unit(long long u) const {  // columns fastest: the tiles of a row tile read the same rows of dz
-    const int c = (int)(u % p.ctiles);
-    int r = (int)(u / p.ctiles), s = 0, n = 1;
+    const unsigned q = (unsigned)u / (unsigned)p.ctiles;  // (fewer than 2^32: at most eight a block beside the whole tiles)
+    const int c = (int)((unsigned)u - q * (unsigned)p.ctiles);
+    int r = (int)q, s = 0, n = 1;
     if (r >= whole) {
       const int rest = rt - whole;
       s = (r - whole) / rest;
@@ -72,6 +74,7 @@ struct Sum {
     lane = l;
   }
   __device__ void begin(const Unit&) {}
+  __device__ void finish() {}
   __device__ void end(const Unit&) {}
 
   // 32 columns of each lane's row to the unit's partial product, or added to it
