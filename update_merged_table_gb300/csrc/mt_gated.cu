@@ -93,7 +93,7 @@ template <typename T, bool BACKWARD>
 struct Gated {
   using Params = GatedParams;
   static constexpr int kBN = 256;
-  static constexpr bool kAMN = false, kBMN = false, kTwoB = true, kTeams = true, kKeep = false, kSingle = true;
+  static constexpr bool kAMN = false, kBMN = false, kTwoB = true, kTeams = true, kKeep = false, kSingle = true, kTri = false;
   static constexpr int kStageOut = 2048;  // 32 rows x 64 bytes
   static constexpr bool kSplit = BACKWARD && sizeof(T) == 2;
   static constexpr bool kAhead = BACKWARD && sizeof(T) == 2;  // dh of a tile's first columns is on its way before the tile

@@ -22,6 +22,16 @@ __device__ __forceinline__ uint32_t bf16_bits(__nv_bfloat16 a, __nv_bfloat16 b) 
   return (uint32_t)__bfloat16_as_ushort(a) | (uint32_t)__bfloat16_as_ushort(b) << 16;
 }
 
+// The same of two values into pairs, where none is near the largest number (one that is, or an infinity, becomes NaN).
+__device__ __forceinline__ void split3_pair(float x, float y, uint32_t (&w)[3]) {
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    w[q] = bf16x2_of(x, y);
+    x -= __uint_as_float(w[q] << 16);
+    y -= __uint_as_float(w[q] & 0xFFFF0000u);
+  }
+}
+
 // Columns of a part of a padded copy: a multiple of 8 (the copies' strides), of 64 where several parts lie side by side (a
 // step of the contraction must not reach into the next part).
 inline int64_t part_columns(int64_t d, int parts) { return parts == 1 ? (d + 7) / 8 * 8 : (d + 63) / 64 * 64; }

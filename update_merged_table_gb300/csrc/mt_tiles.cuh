@@ -39,10 +39,11 @@ static_assert(128 * kRegsControl + kEpiWarps * 32 * kRegsEpi <= kThreadsT * kReg
 // turns its rows.  KEEP: A's tile (all of its contraction, up to kKept steps) is copied once per unit and stays, and the
 // stages hold B alone.
 constexpr int kKept = 8;
-template <int BN, int CG, bool KEEP>
+template <int BN, int CG, bool KEEP, bool TRI>  // TRI: a stage holds all three parts of both operands
 struct Ring {
   static constexpr int kStageA = kBM * kBK * 2, kStageB = BN / CG * kBK * 2;
-  static constexpr int kStage = kStageB + (KEEP ? 0 : kStageA);
+  static constexpr int kParts = TRI ? 3 : 1;
+  static constexpr int kStage = kParts * (kStageB + (KEEP ? 0 : kStageA));
   static constexpr int kTotal = 196608;
   static __host__ __device__ constexpr int stages(int kept) {
     const int n = (kTotal - kept * kStageA) / kStage;
@@ -109,6 +110,7 @@ __device__ __forceinline__ int kept_of(const typename Op::Params& p) {
 //   kBN, kAMN, kBMN            tile columns; operands whose rows are contiguous
 //   kTeams                     a team of epilogue warps takes every other tile (else half of the columns of each)
 //   kKeep                      A's tile stays for the unit: parts x steps <= kKept
+//   kTri                       every stage brings three parts of A and of B (passes is 1) and makes their six products
 //   kTwoB                      (where B's contraction is contiguous) half of the columns b_second rows of B after the others
 //   Params                     passes, a_part, b_part (columns between the parts), promote (stages an accumulator sums
 //                              before it is handed over), status
@@ -125,7 +127,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
 k_tiles(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
         const __grid_constant__ typename Op::Params p) {
   constexpr int BN = Op::kBN;
-  using R = Ring<BN, CG, Op::kKeep>;
+  using R = Ring<BN, CG, Op::kKeep, Op::kTri>;
   constexpr int kCols = BN / CG;  // columns of B that a block copies
   constexpr int kAccs = BN >= 256 ? 2 : 4;
   extern __shared__ uint8_t s_raw[];
@@ -210,10 +212,20 @@ k_tiles(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
               ok = tc::warp_wait(&bar.empty[s.stage], s.phase ^ 1);
               if (!ok) break;
               uint8_t* st = stages_at + s.stage * R::kStage;
-              uint8_t* sb = st + (Op::kKeep ? 0 : R::kStageA);
+              uint8_t* sb = st + (Op::kKeep ? 0 : R::kParts * R::kStageA);
               if (one) {
                 uint64_t* full = &bar.full[s.stage];
                 if (rank == 0) tc::mbar_expect(full, CG * R::kStage);
+                if constexpr (Op::kTri) {
+                  static_assert(!Op::kTri || (CG == 1 && Op::kBMN && !Op::kKeep), "the only form with three parts at once");
+#pragma unroll
+                  for (int i = 0; i < 3; ++i) {
+                    load_a(st + i * R::kStageA, full, i * p.a_part, r0, k);
+#pragma unroll
+                    for (int c = 0; c < kCols / 64; ++c)
+                      tc::tma_load_2d(sb + i * R::kStageB + c * 8192, &map_b, full, i * p.b_part + ct * BN + c * 64, k * kBK);
+                  }
+                } else {
                 if constexpr (!Op::kKeep) load_a(st, full, ap, r0, k);
                 if constexpr (CG == 2) {
                   const uint32_t at = tc::of_leader(full);
@@ -236,6 +248,7 @@ k_tiles(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
                   } else {
                     tc::tma_load_2d(sb, &map_b, full, bp + k * kBK, ct * BN);
                   }
+                }
                 }
               }
               __syncwarp();
@@ -264,7 +277,7 @@ k_tiles(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
         constexpr uint32_t kStepA = Op::kAMN ? 2048 >> 4 : 32 >> 4, kStepB = Op::kBMN ? 2048 >> 4 : 32 >> 4;
         const bool one = tc::elect_one();
         const uint32_t a0 = tc::desc_low(tc::smem_addr(Op::kKeep ? ring : stages_at), kLeadA);
-        const uint32_t b0 = tc::desc_low(tc::smem_addr(stages_at + (Op::kKeep ? 0 : R::kStageA)), kLeadB);
+        const uint32_t b0 = tc::desc_low(tc::smem_addr(stages_at + (Op::kKeep ? 0 : R::kParts * R::kStageA)), kLeadB);
         tc::Slot s;
         int acc = 0;
         uint32_t acc_phase = 0, a_phase = 0;
@@ -294,8 +307,12 @@ k_tiles(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
                 const bool closes = part + 1 == p.promote || (k + 1 == per_pass && q + 1 == p.passes);
                 if (one) {
 #pragma unroll
-                  for (int i = 0; i < kBK / 16; ++i)
-                    tc::mma_bf16<CG>(tmem + acc * BN, a + i * kStepA, b + i * kStepB, instr, part > 0 || i > 0);
+                  for (int q3 = 0; q3 < (Op::kTri ? 6 : 1); ++q3) {
+                    const uint32_t aq = a + (Op::kTri ? part_a(6, q3) * (R::kStageA >> 4) : 0), bq = b + (Op::kTri ? part_b(6, q3) * (R::kStageB >> 4) : 0);
+#pragma unroll
+                    for (int i = 0; i < kBK / 16; ++i)
+                      tc::mma_bf16<CG>(tmem + acc * BN, aq + i * kStepA, bq + i * kStepB, instr, part > 0 || i > 0 || q3 > 0);
+                  }
                   tc::mma_commit<CG>(&bar.empty[s.stage]);
                   if (closes) tc::mma_commit<CG>(&bar.acc_full[acc]);
                 }
@@ -415,10 +432,12 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, int lane, const uint3
       if (r < rows && at < J) *reinterpret_cast<uint4*>(to + (size_t)r * ldc) = *reinterpret_cast<const uint4*>(stage + piece_at(r, c));
     }
   } else {
-    for (int i = lane; i < 32 * kPer; i += 32) {
-      const int r = i / kPer, j = i % kPer;
+    const int j = lane % kPer;
+    T* to = C + (size_t)(r0 + lane / kPer) * ldc + col + j;
+#pragma unroll 8
+    for (int r = lane / kPer; r < 32; r += 32 / kPer, to += (size_t)(32 / kPer) * ldc) {
       if (r < rows && col + j < J)
-        C[(size_t)(r0 + r) * ldc + col + j] = *reinterpret_cast<const T*>(stage + piece_at(r, j * (int)sizeof(T) / 16) + j * (int)sizeof(T) % 16);
+        *to = *reinterpret_cast<const T*>(stage + piece_at(r, j * (int)sizeof(T) / 16) + j * (int)sizeof(T) % 16);
     }
   }
 }
@@ -458,10 +477,12 @@ __device__ __forceinline__ void load_rows(uint8_t* stage, int lane, float (&f)[3
 #pragma unroll
   for (int h = 0; h < 32 / kPer; ++h) {
     __syncwarp();
-    for (int i = lane; i < 32 * kPer; i += 32) {
-      const int r = i / kPer, j = i % kPer, at = col + h * kPer + j;
+    const int j = lane % kPer, at = col + h * kPer + j;
+    const T* from = C + (size_t)(r0 + lane / kPer) * ldc + at;
+#pragma unroll 8
+    for (int r = lane / kPer; r < 32; r += 32 / kPer, from += (size_t)(32 / kPer) * ldc) {
       T v = from_f<T>(0.0f);
-      if (r < rows && at < J) v = C[(size_t)(r0 + r) * ldc + at];
+      if (r < rows && at < J) v = *from;
       *reinterpret_cast<T*>(stage + piece_at(r, j * (int)sizeof(T) / 16) + j * (int)sizeof(T) % 16) = v;
     }
     __syncwarp();
@@ -502,7 +523,7 @@ __device__ __forceinline__ void store32(uint8_t* stage, int lane, const float (&
 template <class Op, int CG>
 cudaError_t launch(const char* name, const CUtensorMap& a, const CUtensorMap& b, const typename Op::Params& p, long long units,
                    size_t extra, size_t most, cudaStream_t s) {
-  constexpr size_t ring = 1024 + Ring<Op::kBN, CG, Op::kKeep>::kTotal + kEpiWarps * Op::kStageOut;  // the stages start on 1024 bytes
+  constexpr size_t ring = 1024 + Ring<Op::kBN, CG, Op::kKeep, Op::kTri>::kTotal + kEpiWarps * Op::kStageOut;  // the stages start on 1024 bytes
   static SmemLimit limit;
   const cudaError_t e = limit.allow(k_tiles<Op, CG>, ring + most);
   if (e != cudaSuccess) return e;

@@ -708,6 +708,7 @@ int mt_vocab_loss_backward(const mt_vocab_loss* c, const float* dloss, const flo
     const char* wv = w.data + (size_t)v0 * w.ld * 2;
     LogitParams p = logits_of(*c, l, base);
     p.v0 = (int)v0;
+    if (p.kept > kGradKept) p.kept = 0;
     p.columns = (int)columns;
     p.tiles = (int)tiles_of(columns, 256);
     p.coef = reinterpret_cast<float4*>(base + l.coef);
@@ -723,8 +724,8 @@ int mt_vocab_loss_backward(const mt_vocab_loss* c, const float* dloss, const flo
       e = launch_logit_grad(p, l.parts, a, b, tiles_of(c->n, pair ? 256 : 128), pair, s);
     }
     SumParams q{};
-    q.passes = p.passes;
-    q.promote = fp32 ? 8 : 1 << 30;
+    q.passes = 1;
+    q.promote = fp32 ? 1 : 1 << 30;
     q.status = c->status;
     q.live = p.rows.count;
     q.a_part = p.width;

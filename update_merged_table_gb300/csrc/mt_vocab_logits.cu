@@ -34,7 +34,7 @@ template <int CG, bool KEEP>
 struct Logits {
   using Params = LogitParams;
   static constexpr int kBN = 256;
-  static constexpr bool kAMN = false, kBMN = false, kTwoB = false, kTeams = true, kKeep = KEEP, kAhead = false, kSplit = false, kSingle = false;
+  static constexpr bool kAMN = false, kBMN = false, kTwoB = false, kTeams = true, kKeep = KEEP, kAhead = false, kSplit = false, kSingle = false, kTri = false;
   static constexpr int kStageOut = 4096;  // 32 rows x 128 bytes
   const Params& p;
   int rank, live, rt, chunks;
@@ -199,11 +199,10 @@ struct Grad : Logits<CG, KEEP> {
     uint32_t w[3][16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      __nv_bfloat16 a[3], b[3];
-      split3(f[2 * j], a[0], a[1], a[2]);
-      split3(f[2 * j + 1], b[0], b[1], b[2]);
+      uint32_t t[3];
+      split3_pair(f[2 * j], f[2 * j + 1], t);
 #pragma unroll
-      for (int q = 0; q < 3; ++q) w[q][j] = bf16_bits(a[q], b[q]);
+      for (int q = 0; q < 3; ++q) w[q][j] = t[q];
     }
 #pragma unroll
     for (int q = 0; q < 3; ++q)

@@ -6,9 +6,11 @@
 //   dW = dz^T x  entries of the piece by columns of x, the contraction over the live
 //                rows, rounded and done
 //
-// fp32 rows: the accumulator starts anew every 512 products (`promote`) and is
-// added up in registers, rounding to nearest, since the tensor core cuts it off
-// towards zero at every step.
+// fp32 rows: a step brings all parts of both operands and makes their six products
+// (part by part, each pass over the operands again was bound by L2: dW of 10,007 x
+// 128 from 1639 rows 42 us, TODO with all at once).  The accumulator starts anew
+// every step (`promote`) and is added up in registers, rounding to nearest, since the
+// tensor core cuts it off towards zero at every product.
 #include "mt_tiles.cuh"
 #include "mt_vocab.cuh"
 #include "mt_vocab_rows.cuh"
@@ -25,7 +27,7 @@ template <int BN, bool FP32, bool VOCAB, int CG>
 struct Sum {
   using Params = SumParams;
   static constexpr int kBN = BN;
-  static constexpr bool kAMN = VOCAB, kBMN = true, kTeams = !FP32, kKeep = false, kAhead = false, kSplit = false, kSingle = false;
+  static constexpr bool kAMN = VOCAB, kBMN = true, kTeams = !FP32, kKeep = false, kAhead = false, kSplit = false, kSingle = false, kTri = FP32;
   static constexpr int kStageOut = 2048;  // 32 rows x 64 bytes
   const Params& p;
   int rank, rows, rt, steps, whole, runs, quad, half, lane;  // whole: row tiles with the whole contraction
