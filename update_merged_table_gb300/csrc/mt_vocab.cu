@@ -132,26 +132,29 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const VocabRows p) {
   extern __shared__ uint8_t s_mem[];
   __shared__ int s_base;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long words = (p.n + 31) / 32;
-  for (long long q = blockIdx.x; q < words * kRowBlocks; q += gridDim.x) {
+  const long long words = (p.n + 31) / 32, all = words * kRowBlocks, per = (all + gridDim.x - 1) / gridDim.x;
+  const long long q0 = blockIdx.x * per, q1 = min(q0 + per, all);  // a block's quarters lie one after the other
+  if (q0 >= q1) return;
+  // the live rows before the block's first word
+  int before = 0;
+  if (threadIdx.x == 0) s_base = 0;
+  __syncthreads();
+  if constexpr (MARK) {
+    for (long long i = threadIdx.x; i < q0 / kRowBlocks * 32; i += blockDim.x) before += row_there(p, i);
+    __syncwarp();
+  } else {
+    for (long long i = threadIdx.x; i < q0 / kRowBlocks; i += blockDim.x) before += __popc(p.mask[i]);
+  }
+  before = __reduce_add_sync(kFull, before);
+  if (lane == 0) atomicAdd(&s_base, before);
+  __syncthreads();
+  int base = s_base;
+  for (long long q = q0; q < q1; ++q) {
     const long long w = q / kRowBlocks;
     const int share = (int)(q % kRowBlocks);
-    if (threadIdx.x == 0) s_base = 0;
-    __syncthreads();
-    int before = 0;
     uint32_t bits;
-    if constexpr (MARK) {
-      for (long long i = threadIdx.x; i < w * 32; i += blockDim.x) before += row_there(p, i);
-      __syncwarp();
-      bits = __ballot_sync(kFull, w * 32 + lane < p.n && row_there(p, w * 32 + lane));
-    } else {
-      for (long long i = threadIdx.x; i < w; i += blockDim.x) before += __popc(p.mask[i]);
-      bits = p.mask[w];
-    }
-    before = __reduce_add_sync(kFull, before);
-    if (lane == 0) atomicAdd(&s_base, before);
-    __syncthreads();
-    const int base = s_base;
+    if constexpr (MARK) bits = __ballot_sync(kFull, w * 32 + lane < p.n && row_there(p, w * 32 + lane));
+    else bits = p.mask[w];
     const int own = __popc(bits);
     if (share == 0 && threadIdx.x < 32 && w * 32 + lane < p.n)
       p.pos[w * 32 + lane] = bits >> lane & 1 ? base + __popc(bits & ((1u << lane) - 1u)) : -1;
@@ -224,14 +227,14 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const VocabRows p) {
         p.coef[at] = make_float4(lse * kLog2e, g * (1.0f + 2.0f * p.z_loss * lse), g * p.smoothing / (float)p.vocab, g);
       }
     }
-    if (q + 1 == words * kRowBlocks) {
+    if (q + 1 == all) {
       const int live = base + own;
       if (threadIdx.x == 0) *p.live = live;
       const size_t width = (size_t)kParts * p.dp;
       const size_t first = (size_t)live * width, last = (size_t)((live + 127) / 128 * 128) * width;
       for (size_t i = first / 8 + threadIdx.x; i < last / 8; i += blockDim.x) reinterpret_cast<uint4*>(p.xs)[i] = make_uint4(0u, 0u, 0u, 0u);
     }
-    __syncthreads();
+    if (share == kRowBlocks - 1) base += own;
   }
 }
 
@@ -243,6 +246,7 @@ struct VocabLoss {
   const float* sum_z;
   size_t stride;
   const int* chunks;
+  int teams;             // partial statistics of a run
   const float* picked;
   const float* share;
   const float* entropy;  // NULL: cross entropy
@@ -256,7 +260,7 @@ __global__ void __launch_bounds__(256) k_vocab_loss(const VocabLoss p) {
   lead();
   follow();
   const int lane = threadIdx.x & 31;
-  const int slots = 2 * *p.chunks;
+  const int slots = p.teams * *p.chunks;
   for (long long row = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5; row < p.n; row += ((long long)gridDim.x * blockDim.x) >> 5) {
     const int at = p.pos[row];
     if (at < 0) {
@@ -403,7 +407,7 @@ Layout layout_of(const mt_vocab_loss& c, bool backward) {
   };
   l.mask = take((size_t)tiles_of(c.n, 32) * 4);
   l.live = take(4);
-  l.chunks = take(4);
+  l.chunks = take(8);
   l.cut = take(16);
   l.pos = take((size_t)c.n * 4);
   l.xs = take((size_t)l.rows * l.parts * l.dp * 2);
@@ -415,8 +419,8 @@ Layout layout_of(const mt_vocab_loss& c, bool backward) {
   if (!backward) {
     l.max_chunks = (int)(16 * sms / (l.rows / 128) + 1);
     l.picked = take((size_t)c.n * l.top * 4);
-    l.part = take((size_t)2 * l.max_chunks * l.rows * 8);
-    if (c.smoothing > 0.0f) l.sum_z = take((size_t)2 * l.max_chunks * l.rows * 4);
+    l.part = take((size_t)kNarrowTeams * l.max_chunks * l.rows * 8);
+    if (c.smoothing > 0.0f) l.sum_z = take((size_t)kNarrowTeams * l.max_chunks * l.rows * 4);
   } else if (c.dtype == MT_BF16 && c.dim <= kFusedColumns) {
     // room for as many runs as give every block eight units, of the tiles that are cut at all
     l.fused = true;
@@ -601,13 +605,30 @@ int mt_vocab_loss_forward(const mt_vocab_loss* c, float* loss, float* lse, void*
   p.sum_z = c->smoothing > 0.0f ? reinterpret_cast<float*>(base + l.sum_z) : nullptr;
   p.picked = reinterpret_cast<float*>(base + l.picked);
   p.chunks = reinterpret_cast<int*>(base + l.chunks);
-  const bool pair = c->dtype == MT_BF16 && pair_rows(c->n, tiles_of(c->vocab, 256), p.steps);
+  const bool narrow = c->dtype == MT_BF16 && c->dim <= kFusedColumns;
+  const bool pair = !narrow && c->dtype == MT_BF16 && pair_rows(c->n, tiles_of(c->vocab, 256), p.steps);
   const Weights w = weights_of(*c, l, base);
   CUtensorMap a, b;
   const uint64_t width = (uint64_t)l.parts * l.dp;
   if (!tc::encode_bf16(&a, 2, base + l.xs, width, l.rows, width, 1, 0, 64, 128)) return MT_ECUDA;
-  if (!tc::encode_bf16(&b, 2, w.data, w.width, c->vocab, w.ld, 1, 0, 64, pair ? 128 : 256)) return MT_ECUDA;
-  e = launch_logit_stats(p, a, b, tiles_of(c->n, pair ? 256 : 128), pair, s);
+  if (!tc::encode_bf16(&b, 2, w.data, w.width, c->vocab, w.ld, 1, 0, 64, pair || narrow ? 128 : 256)) return MT_ECUDA;
+  if (narrow) {
+    FusedParams f{};
+    f.status = c->status;
+    f.rows = p.rows;
+    f.vocab = c->vocab;
+    f.columns = c->dim;
+    f.max_chunks = l.max_chunks;
+    f.scale2 = p.scale2;
+    f.stats = p.part;
+    f.sum_z = p.sum_z;
+    f.picked = p.picked;
+    f.stride = l.rows;
+    f.cut = p.chunks;
+    e = launch_narrow_stats(f, a, b, tiles_of(c->n, kFusedTile) * std::min<int64_t>(l.max_chunks, tiles_of(c->vocab, kFusedTile)), s);
+  } else {
+    e = launch_logit_stats(p, a, b, tiles_of(c->n, pair ? 256 : 128), pair, s);
+  }
   if (e != cudaSuccess) return MT_ECUDA;
   VocabLoss q{};
   q.n = c->n;
@@ -618,6 +639,7 @@ int mt_vocab_loss_forward(const mt_vocab_loss* c, float* loss, float* lse, void*
   q.sum_z = p.sum_z;
   q.stride = l.rows;
   q.chunks = p.chunks;
+  q.teams = narrow ? kNarrowTeams : 2;
   q.picked = p.picked;
   q.share = p.rows.share;
   q.entropy = c->top > 0 ? reinterpret_cast<float*>(base + l.entropy) : nullptr;

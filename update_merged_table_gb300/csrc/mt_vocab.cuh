@@ -74,7 +74,7 @@ cudaError_t launch_rows_sum(const SumParams& p, bool fp32, const CUtensorMap& a,
 cudaError_t launch_vocab_sum(const SumParams& p, bool fp32, const CUtensorMap& a, const CUtensorMap& b, long long row_tiles, bool pair,
                              cudaStream_t s);
 
-// The gradients for narrow rows, without a dz in memory (mt_vocab_fused.cu): bf16, up to 128 columns.  Measured, backward
+// The statistics and gradients for narrow rows, without a dz in memory (mt_vocab_fused.cu): bf16, up to 128 columns.  Measured, backward
 // of 16,384 rows x 50,000 entries, without dz against with: 64 columns 527 against 950 us, 128 693 against 1013, 192 1336
 // against 1067; of 2048 x 100,003: 156 / 263, 203 / 281, 361 / 295.
 struct FusedParams {
@@ -90,7 +90,13 @@ struct FusedParams {
   size_t stride;
   int reach, reach_part;  // of out's rows and part's
   __nv_bfloat16* out;  // dW
+  // statistics: as in LogitParams, kNarrowTeams to a run
+  float2* stats;
+  float* sum_z;
+  float* picked;
 };
+constexpr int kNarrowTeams = 3;
+cudaError_t launch_narrow_stats(const FusedParams& p, const CUtensorMap& x, const CUtensorMap& w, long long units, cudaStream_t s);
 constexpr int kFusedColumns = 128, kFusedTile = 128;
 cudaError_t launch_fused(bool vocab, const FusedParams& p, const CUtensorMap& x, const CUtensorMap& w, long long units, cudaStream_t s);
 

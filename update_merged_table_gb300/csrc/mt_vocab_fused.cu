@@ -1,5 +1,6 @@
-// The gradients of the losses over a vocabulary for narrow rows (up to 128 columns
-// of bf16): the gradient of the logits never leaves the chip.
+// The losses over a vocabulary for narrow rows (up to 128 columns of bf16): their
+// statistics, and gradients for which the gradient of the logits never leaves the
+// chip.
 //
 // With few columns a logit is a few products and one exponential, and writing its
 // gradient out (2 bytes) and reading it back twice costs more than making it
@@ -27,12 +28,11 @@ namespace {
 constexpr int kT = 128;                  // rows and entries of a tile
 constexpr int kSlab = kT * 128;          // 128 rows of 64 columns
 constexpr int kDz = 2 * kSlab;           // a tile of dz
-constexpr int kS = 3;                    // S under way
-constexpr int kAccAt = kS * kT;          // tensor memory: these, then the sum
+constexpr int kAccAt = 3 * kT;           // tensor memory: S, then the sum
 
 struct FusedBarriers {
   uint64_t full[8], empty[8];        // a streamed tile has landed; its products are done
-  uint64_t s_full[3], s_empty[3];    // S is finished; it has been read
+  uint64_t s_full[4], s_empty[4];    // S is finished; it has been read
   uint64_t dz_full[3];               // dz is in shared memory
   uint64_t dz_empty[3];              // the products of a team's last tile of dz are done
   uint64_t kept_full, kept_empty;    // the kept tile has landed; its products are done
@@ -42,12 +42,13 @@ struct FusedBarriers {
 };
 
 // KS: slabs of 64 columns.  Teams of four warps, each with a tile of dz of its own, and streamed tiles.
-template <int KS>
+template <int KS, bool STATS>
 struct FusedRing {
   static constexpr int kTile = KS * kSlab;
-  static constexpr int kTeams = KS == 1 ? 3 : 2, kThreads = (4 + kTeams * 4) * 32;
+  static constexpr int kTeams = STATS ? kNarrowTeams : KS == 1 ? 3 : 2, kThreads = (4 + kTeams * 4) * 32;
   static constexpr int kStages = KS == 1 ? 6 : 4;
-  static constexpr int kBytes = (1 + kStages) * kTile + kTeams * kDz;
+  static constexpr int kS = STATS ? 4 : 3;  // S under way
+  static constexpr int kBytes = (1 + kStages) * kTile + (STATS ? 0 : kTeams * kDz);
 };
 
 // A unit: a kept tile and streamed tiles [t0, t1).
@@ -66,10 +67,15 @@ struct FusedWork {
   }
 };
 
-template <int KS, bool VOCAB>
-__global__ void __launch_bounds__(FusedRing<KS>::kThreads, 1)
+// What a launch computes: dx, dW, or the rows' statistics (with smoothing: the sums of their logits too).
+enum Fused { kDx, kDw, kStats, kStatsSmooth };
+
+template <int KS, int WHAT>
+__global__ void __launch_bounds__(FusedRing<KS, (WHAT >= kStats)>::kThreads, 1)
 k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ FusedParams p) {
-  using R = FusedRing<KS>;
+  constexpr bool VOCAB = WHAT == kDw, STATS = WHAT >= kStats;
+  using R = FusedRing<KS, STATS>;
+  constexpr int kS = R::kS;
   extern __shared__ uint8_t s_raw[];
   __shared__ FusedBarriers bar;
   uint8_t* base = reinterpret_cast<uint8_t*>(((uintptr_t)s_raw + 1023) & ~(uintptr_t)1023);
@@ -112,10 +118,10 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     const int rt = (work.live + kT - 1) / kT, vt = (p.vocab + kT - 1) / kT;
     work.kept_tiles = VOCAB ? vt : rt;
     work.streamed = VOCAB ? rt : vt;
-    work.whole = VOCAB ? p.whole : work.kept_tiles / (int)gridDim.x * (int)gridDim.x;
+    work.whole = VOCAB ? p.whole : STATS ? 0 : work.kept_tiles / (int)gridDim.x * (int)gridDim.x;
     work.chunks = choose_chunks(work.kept_tiles - work.whole, work.streamed, p.max_chunks, gridDim.x, 4);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
-      p.cut[0] = work.whole * kT;
+      p.cut[0] = STATS ? work.chunks : work.whole * kT;
       p.cut[1] = work.chunks;
     }
   }
@@ -187,7 +193,9 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             const uint32_t o = ((i >> 2) * kSlab + (i & 3) * 32) >> 4;
             tc::mma_bf16<1>(tmem + b * kT, ax + o, aw + o, instr, i > 0);
           }
+          if (STATS) tc::mma_commit<1>(&bar.empty[s.stage]);
           tc::mma_commit<1>(&bar.s_full[b]);
+          if (STATS && t + 1 == x.t1) tc::mma_commit<1>(&bar.kept_empty);
         }
         __syncwarp();
         if (++b == kS) {
@@ -201,7 +209,7 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     __syncwarp();
     ok = tc::mbar_wait(&bar.s_done, 0) && ok;
     if (!ok && one) tc::latch_status(p.status, MT_ECUDA);
-  } else if (warp == 2) {
+  } else if (!STATS && warp == 2) {
     // the sums.  A tile's S is done before its dz is, so what this warp signals of a sum holds for its S too.
     constexpr uint32_t instr = tc::instr_bf16(kT, KS * 64, VOCAB, true);
     const bool one = tc::elect_one();
@@ -243,7 +251,50 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     __syncwarp();
     ok = tc::mbar_wait(&bar.done, 0) && ok;
     if (!ok && one) tc::latch_status(p.status, MT_ECUDA);
-  } else if (warp >= 4) {
+  } else if (STATS && warp >= 4) {
+    const int quad = warp & 3, team = (warp - 4) >> 2;
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    uint32_t n = 0;  // tiles so far
+    bool ok = true;
+    RowTargets to;
+    RowStats<WHAT == kStatsSmooth> stats;
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const FusedUnit x = work.unit(u);
+      const int row = x.kept * kT + quad * 32 + lane;
+      to.start(p.rows, row, work.live, x.t0 * kT);
+      stats.clear();
+      for (int t = x.t0 + (team + R::kTeams - (int)(n % R::kTeams)) % R::kTeams; t < x.t1; t += R::kTeams) {
+        // (a team sees every third S or so of a buffer: the S before are done before its own is)
+        const uint32_t of = n + (t - x.t0), b = of % kS, from = tmem + b * kT + lanes;
+        const int v0 = t * kT, left = p.vocab - v0;
+        const bool some = left < kT || __any_sync(kFull, to.next < v0 + kT);
+        ok = tc::warp_wait(&bar.s_full[b], of / kS & 1);
+        if (!ok) break;
+        tc::fence_after();
+#pragma unroll
+        for (int c = 0; c < kT; c += 32) {
+          uint32_t v[32];
+          tc::tmem_load32(from + c, v);
+          tc::tmem_load_wait(v);
+          if (c + 32 == kT) {
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bar.s_empty[b]);
+          }
+          if (some) to.pick(p.rows, v0 + c, v, p.picked);
+          stats.add(v, p.scale2, some ? left - c : 32);
+        }
+      }
+      if (!ok) break;
+      n += x.t1 - x.t0;
+      if (row < work.live) {
+        const size_t at = (size_t)(x.slot * R::kTeams + team) * p.stride + row;
+        p.stats[at] = make_float2(stats.top, stats.sum);
+        if (WHAT == kStatsSmooth) p.sum_z[at] = stats.total;
+      }
+    }
+    if (!ok) tc::latch_status(p.status, MT_ECUDA);
+  } else if (!STATS && warp >= 4) {
     const int quad = warp & 3, team = (warp - 4) >> 2;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     uint8_t* const stage = s_dz + team * kDz + quad * 4096;  // the warp's rows of dz; the sum goes out through them
@@ -382,23 +433,30 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   if (warp == 1) tc::tmem_free<1>(tmem, 512);
 }
 
-template <int KS, bool VOCAB>
+template <int KS, int WHAT>
 cudaError_t launch(const char* name, const CUtensorMap& x, const CUtensorMap& w, const FusedParams& p, long long units, cudaStream_t s) {
-  constexpr size_t bytes = 1024 + FusedRing<KS>::kBytes;
+  using R = FusedRing<KS, (WHAT >= kStats)>;
+  constexpr size_t bytes = 1024 + R::kBytes;
   static SmemLimit limit;
-  const cudaError_t e = limit.allow(k_vocab_fused<KS, VOCAB>, bytes);
+  const cudaError_t e = limit.allow(k_vocab_fused<KS, WHAT>, bytes);
   if (e != cudaSuccess) return e;
   const int blocks = sm_count();
   MT_LAUNCH(name, s);
-  return launch_following(k_vocab_fused<KS, VOCAB>, (int)(units < blocks ? (units > 0 ? units : 1) : blocks), FusedRing<KS>::kThreads, bytes, s, x, w, p);
+  return launch_following(k_vocab_fused<KS, WHAT>, (int)(units < blocks ? (units > 0 ? units : 1) : blocks), R::kThreads, bytes, s, x, w, p);
+}
+
+template <int WHAT>
+cudaError_t launch_of(const char* name, const CUtensorMap& x, const CUtensorMap& w, const FusedParams& p, long long units, cudaStream_t s) {
+  return p.columns <= 64 ? launch<1, WHAT>(name, x, w, p, units, s) : launch<2, WHAT>(name, x, w, p, units, s);
 }
 
 }  // namespace
 
 cudaError_t launch_fused(bool vocab, const FusedParams& p, const CUtensorMap& x, const CUtensorMap& w, long long units, cudaStream_t s) {
-  const char* name = vocab ? "k_vocab_fused_dw" : "k_vocab_fused_dx";
-  if (p.columns <= 64) return vocab ? launch<1, true>(name, x, w, p, units, s) : launch<1, false>(name, x, w, p, units, s);
-  return vocab ? launch<2, true>(name, x, w, p, units, s) : launch<2, false>(name, x, w, p, units, s);
+  return vocab ? launch_of<kDw>("k_vocab_fused_dw", x, w, p, units, s) : launch_of<kDx>("k_vocab_fused_dx", x, w, p, units, s);
+}
+cudaError_t launch_narrow_stats(const FusedParams& p, const CUtensorMap& x, const CUtensorMap& w, long long units, cudaStream_t s) {
+  return p.sum_z != nullptr ? launch_of<kStatsSmooth>("k_vocab_fused_stats", x, w, p, units, s) : launch_of<kStats>("k_vocab_fused_stats", x, w, p, units, s);
 }
 
 }  // namespace mt

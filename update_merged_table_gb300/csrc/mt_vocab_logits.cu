@@ -24,11 +24,6 @@ namespace {
 using tiles::Acc;
 using tiles::Unit;
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 // What both kernels share: rows tiles fastest, so that blocks at work at the same time read the same entries of W.
 template <int CG, bool KEEP>
 struct Logits {
@@ -76,58 +71,25 @@ struct Logits {
 template <bool SMOOTH, int CG, bool KEEP>
 struct Stats : Logits<CG, KEEP> {
   using Base = Logits<CG, KEEP>;
-  float top, sum, total;
+  RowStats<SMOOTH> stats;
   __device__ Stats(const LogitParams& p, uint8_t* mem, int r) : Base(p, mem, r) {
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.chunks = this->chunks;
   }
   __device__ void begin(const Unit& x) {
     this->start(x);
-    top = -INFINITY;
-    sum = total = 0.0f;
+    stats.clear();
   }
   __device__ void end(const Unit& x) {
     if (this->row >= this->live) return;
     const size_t at = (size_t)(x.slot * 2 + this->team) * this->p.stride + this->row;
-    this->p.part[at] = make_float2(top, sum);
-    if constexpr (SMOOTH) this->p.sum_z[at] = total;
+    this->p.part[at] = make_float2(stats.top, stats.sum);
+    if constexpr (SMOOTH) this->p.sum_z[at] = stats.total;
   }
-  // 32 columns: their largest, then one exponential each.  The next columns' load is on its way meanwhile.  some: there may
-  // be targets among them, or columns that are not there.
+  // 32 columns; the next columns' load is on its way meanwhile.  some: there may be targets among them, or columns that are
+  // not there.
   __device__ __forceinline__ void columns(uint32_t (&v)[32], int col, int left, bool some) {
-    const LogitParams& p = this->p;
-    if (some) this->to.pick(p.rows, col, v, p.picked);
-    if constexpr (SMOOTH) {
-      f32x2 t[2] = {0ull, 0ull};
-#pragma unroll
-      for (int j = 0; j < 32; j += 2)  // (columns that are not there are zero)
-        t[j >> 1 & 1] = add2(t[j >> 1 & 1], pk(__uint_as_float(v[j]), __uint_as_float(v[j + 1])));
-      total += pair_sum(add2(t[0], t[1]));
-    }
-    if (some && left < 32) {
-      const uint32_t there = below(left);
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (!(there >> j & 1)) v[j] = 0xFF800000u;
-    }
-    float m[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      m[i] = __uint_as_float(v[i * 8]);
-#pragma unroll
-      for (int j = 1; j < 7; j += 2) m[i] = max3(m[i], __uint_as_float(v[i * 8 + j]), __uint_as_float(v[i * 8 + j + 1]));
-      m[i] = fmaxf(m[i], __uint_as_float(v[i * 8 + 7]));
-    }
-    const float now = max3(top, fmaxf(m[0], m[1]) * p.scale2, fmaxf(m[2], m[3]) * p.scale2);
-    const float off = now == -INFINITY ? 0.0f : now;
-    const f32x2 s2 = both(p.scale2), o2 = both(-off);
-    f32x2 s[2] = {0ull, 0ull};
-#pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      const float2 e = upk(fma2(pk(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), s2, o2));
-      s[j >> 1 & 1] = add2(s[j >> 1 & 1], pk(exp2_of(e.x), exp2_of(e.y)));
-    }
-    sum = fmaf(sum, exp2_of(top - off), pair_sum(add2(s[0], s[1])));
-    top = now;
+    if (some) this->to.pick(this->p.rows, col, v, this->p.picked);
+    stats.add(v, this->p.scale2, some ? left : 32);
   }
   __device__ void finish() {}
   template <int G>

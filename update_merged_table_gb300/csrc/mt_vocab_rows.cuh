@@ -86,4 +86,57 @@ struct RowTargets {
   }
 };
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// A row's statistics over the columns it has seen: the largest logit (in base 2) and the sum of 2^(z - that), and (SMOOTH) the
+// sum of the logits before the scale.
+template <bool SMOOTH>
+struct RowStats {
+  float top, sum, total;
+
+  __device__ __forceinline__ void clear() {
+    top = -INFINITY;
+    sum = total = 0.0f;
+  }
+  // 32 columns: their largest, then one exponential each; only the first `left` count.
+  __device__ __forceinline__ void add(uint32_t (&v)[32], float scale2, int left) {
+    if constexpr (SMOOTH) {
+      f32x2 t[2] = {0ull, 0ull};
+#pragma unroll
+      for (int j = 0; j < 32; j += 2)  // (columns that are not there are zero)
+        t[j >> 1 & 1] = add2(t[j >> 1 & 1], pk(__uint_as_float(v[j]), __uint_as_float(v[j + 1])));
+      total += pair_sum(add2(t[0], t[1]));
+    }
+    if (left < 32) {
+      const uint32_t there = below(left);
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (!(there >> j & 1)) v[j] = 0xFF800000u;
+    }
+    float m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = __uint_as_float(v[i * 8]);
+#pragma unroll
+      for (int j = 1; j < 7; j += 2) m[i] = max3(m[i], __uint_as_float(v[i * 8 + j]), __uint_as_float(v[i * 8 + j + 1]));
+      m[i] = fmaxf(m[i], __uint_as_float(v[i * 8 + 7]));
+    }
+    const float now = max3(top, fmaxf(m[0], m[1]) * scale2, fmaxf(m[2], m[3]) * scale2);
+    const float off = now == -INFINITY ? 0.0f : now;
+    const f32x2 s2 = both(scale2), o2 = both(-off);
+    f32x2 s[2] = {0ull, 0ull};
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      const float2 e = upk(fma2(pk(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), s2, o2));
+      s[j >> 1 & 1] = add2(s[j >> 1 & 1], pk(exp2_of(e.x), exp2_of(e.y)));
+    }
+    sum = fmaf(sum, exp2_of(top - off), pair_sum(add2(s[0], s[1])));
+    top = now;
+  }
+};
+
 }  // namespace mt

@@ -41,7 +41,8 @@ struct Sum {
     rt = (rows + tiles::kBM * CG - 1) / (tiles::kBM * CG);
     const int blocks = gridDim.x / CG;
     whole = rt * p.ctiles / blocks * blocks / p.ctiles;
-    runs = choose_chunks((rt - whole) * p.ctiles, VOCAB ? steps : p.usual, p.max_runs, blocks, 8);
+    // (a partial product is written and read again, which takes about as long as 24 steps, or 4 of six products each)
+    runs = choose_chunks((rt - whole) * p.ctiles, VOCAB ? steps : p.usual, p.max_runs, blocks, FP32 ? 8 : 48);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
       p.cut[0] = whole * (tiles::kBM * CG);
       p.cut[1] = runs;
