@@ -120,7 +120,7 @@ __device__ __forceinline__ int kept_of(const typename Op::Params& p) {
 //   warp(stage, quad, team, lane), finish()   once, epilogue warps: before the first unit, after the last
 //   kAhead, ahead(x, ct)       before a tile is waited for
 //   kSplit                     more registers for the epilogue
-//   kSingle                    every unit is one tile with one accumulator (and teams take turns)
+//   kSingle                    every unit is one tile of p.steps with one accumulator (and teams take turns)
 //   begin(x), tile(x, ct, acc, first, last), end(x)   a unit; a column tile's accumulator, or (promote) the parts of it
 template <class Op, int CG>
 __global__ void __launch_bounds__(kThreadsT, 1)
@@ -283,7 +283,14 @@ k_tiles(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
         uint32_t acc_phase = 0, a_phase = 0;
         bool ok = true;
         for (long long u = u0; u < units && ok; u += ustep) {
-          const Unit x = op.unit(u);
+          Unit x;
+          if constexpr (Op::kSingle) {  // nothing of a unit has to be found: it would hold the products up
+            x.k0 = x.ct0 = 0;
+            x.k1 = p.steps;
+            x.ct1 = 1;
+          } else {
+            x = op.unit(u);
+          }
           const int per_pass = x.k1 - x.k0;
           if constexpr (Op::kKeep) {
             ok = tc::warp_wait<CG == 2>(&bar.a_full, a_phase);
