@@ -265,6 +265,71 @@ def test_streams_and_graphs():
             assert torch.equal(a, b)
 
 
+def test_replayed_graphs_follow_their_inputs():
+    """How many rows take part is found on the device: a replay with other targets in place is right too."""
+    s = make(17, 300, 900, 64, "bf16", masked=0.2)
+    handle = mt.CrossEntropy(900, 64)
+    handle.forward(s["x"], s["w"], s["targets"])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        r = handle.forward(s["x"], s["w"], s["targets"])
+        dx, dw = handle.backward(s["dloss"], s["x"], s["w"], s["targets"], r.lse)
+    for masked in (0.9, 0.0, 1.1):
+        t = make(18 + int(10 * masked), 300, 900, 64, "bf16", masked=masked)
+        for k in ("x", "w", "targets", "dloss"):
+            s[k].copy_(t[k])
+        g.replay()
+        check_all(t, "bf16", handle=handle, forward=r, grads=(dx, dw))
+
+
+def test_threads_and_streams_side_by_side():
+    import threading
+    cases = [make(20 + i, 400 + 100 * i, 2000 + 500 * i, 64 + 72 * i, "bf16", top=i) for i in range(4)]
+    want, got = [], [None] * 4
+    handles = [mt.CrossEntropy(s["w"].shape[0], s["x"].shape[1]) if "targets" in s else mt.Distillation(s["w"].shape[0], s["x"].shape[1], s["ids"].shape[1])
+               for s in cases]
+    for s, h in zip(cases, handles):
+        r = h.forward(s["x"], s["w"], *given(s))
+        want.append((r.loss, *h.backward(s["dloss"], s["x"], s["w"], *given(s), r.lse)))
+    torch.cuda.synchronize()
+
+    def work(i):
+        st = torch.cuda.Stream()
+        s, h = cases[i], handles[i]
+        for _ in range(5):
+            r = h.forward(s["x"], s["w"], *given(s), stream=st)
+            g = h.backward(s["dloss"], s["x"], s["w"], *given(s), r.lse, stream=st)
+        st.synchronize()
+        got[i] = (r.loss, *g)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for a, b in zip(want, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.slow
+def test_offsets_past_32_bits():
+    """Rows of x, W and dx more than 2^31 elements apart from their first."""
+    n, v, d, ld = 70000, 70000, 32, 40000
+    s = make(30, n, v, d, "bf16", masked=0.98)  # (about 1400 rows take part: the last ones among them)
+    s["targets"][-3:] = torch.tensor([v - 1, 0, v // 2], dtype=torch.int32, device=DEV)
+    big = torch.empty(n, ld, device=DEV, dtype=torch.bfloat16)
+    big[:, :d], big[:, 64:64 + d] = s["x"], s["w"]
+    t = {**s, "x": big[:, :d], "w": big[:, 64:64 + d]}
+    handle = mt.CrossEntropy(v, d)
+    r = handle.forward(t["x"], t["w"], t["targets"])
+    dx, dw = handle.backward(t["dloss"], t["x"], t["w"], t["targets"], r.lse, out_dx=big[:, 128:128 + d])
+    # the rows that take part, against the definition (the sums' runs go by n, so another n need not give the same bits)
+    live = s["targets"] >= 0
+    assert not r.loss[~live].any() and not r.lse[~live].any() and not dx[~live].any()
+    c = {**s, "x": s["x"][live], "targets": s["targets"][live], "dloss": s["dloss"][live]}
+    check_all(c, "bf16", handle=handle, forward=mt.LossForward(r.loss[live], r.lse[live]), grads=(dx[live], dw))
+
+
 def test_gradients_against_differences():
     """fp32, along random directions; differences of the library's own losses."""
     for top in (0, 5):
