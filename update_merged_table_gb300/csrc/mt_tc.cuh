@@ -220,6 +220,16 @@ __device__ __forceinline__ void tmem_load_wait(uint32_t (&r)[32]) {
   tmem_loaded(r);
 }
 
+// 16 columns of the warp's 32 lanes: the reverse.  tmem_store_wait() before what reads them is told.
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // ---- products --------------------------------------------------------------------------
 
 // Instruction descriptor of a bf16 product with fp32 accumulator, M x N; a_mn / b_mn: the operand's rows (M or N) are
@@ -262,6 +272,16 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint32_t a, uint32_t b, uin
         "r"(a), "r"(b), "r"(instr), "r"(add ? 1u : 0u), "n"(kDescHigh)
         : "memory");
   }
+}
+// D = A * B or D + A * B with A's 128 rows in tensor memory, two bf16 of the contraction to a column (16 take 8 columns).
+__device__ __forceinline__ void mma_bf16_tmem(uint32_t d, uint32_t a, uint32_t b, uint32_t instr, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "mov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(instr), "r"(add ? 1u : 0u), "n"(kDescHigh)
+      : "memory");
 }
 // The barrier (of both blocks of a pair) is arrived at when every product issued so far by this thread is done.
 template <int CG>

@@ -59,9 +59,10 @@ struct Barriers {
   uint32_t tmem;
 };
 
-// The parts that pass q of six multiplies, the smallest products first; of one pass, the only parts.
-__device__ __forceinline__ int part_a(int passes, int q) { return passes == 1 ? 0 : (0x010120 >> (4 * q)) & 3; }
-__device__ __forceinline__ int part_b(int passes, int q) { return passes == 1 ? 0 : (0x001102 >> (4 * q)) & 3; }
+// The parts that pass q of `passes` multiplies, the smallest products first: of one pass the only parts, of two A's two parts
+// with B's only one, of six those of three.
+__device__ __forceinline__ int part_a(int passes, int q) { return passes == 1 ? 0 : passes == 2 ? 1 - q : (0x010120 >> (4 * q)) & 3; }
+__device__ __forceinline__ int part_b(int passes, int q) { return passes <= 2 ? 0 : (0x001102 >> (4 * q)) & 3; }
 
 // A unit of work: a row tile, column tiles [ct0, ct1) one after the other, contraction steps [k0, k1) of each pass.
 struct Unit {

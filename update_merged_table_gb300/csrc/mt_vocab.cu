@@ -377,6 +377,7 @@ constexpr size_t kPieceBytes = (size_t)1 << 30;  // of dz at a time
 
 struct Layout {
   int parts, dp, wp;          // parts of an operand; columns of a part of x and of W
+  int dz_parts;
   bool copy_w, fused;         // fused: the gradients without dz in memory
   int whole;                  // fused: dW's tiles that need no partial products
   int runs_dx, runs_dw;       // room for runs
@@ -386,6 +387,12 @@ struct Layout {
   int64_t dw_rows;            // rows of dW's partial products
   size_t mask, live, chunks, cut, pos, xs, ids, share, entropy, w, picked, part, sum_z, coef, dz, dx, dw, total;
 };
+
+// dz of up to this many bf16 rows comes in two bf16 parts.  Its rounding (2^-9 of a value) is one of many terms of dx and dw and
+// adds about what their own rounding does; with few rows single terms show (one row: dw's row of the target is one product).
+// Measured, relative error of dw with one part and with two: 2 rows 0.0029 and 0.0014 (its rounding alone 0.0014), 200 rows
+// 0.0022 and 0.0016; backward of 16 x 100,003 x 256 102 and 119 us, of 200 x 100,003 x 64 57 and 105.
+constexpr int64_t kFewRowsTwice = 64;
 
 int64_t tiles_of(int64_t n, int64_t of) { return (n + of - 1) / of; }
 
@@ -421,7 +428,7 @@ Layout layout_of(const mt_vocab_loss& c, bool backward) {
     l.picked = take((size_t)c.n * l.top * 4);
     l.part = take((size_t)kNarrowTeams * l.max_chunks * l.rows * 8);
     if (c.smoothing > 0.0f) l.sum_z = take((size_t)kNarrowTeams * l.max_chunks * l.rows * 4);
-  } else if (c.dtype == MT_BF16 && c.dim <= kFusedColumns) {
+  } else if (c.dtype == MT_BF16 && c.dim <= kFusedColumns && c.n > kFewRowsTwice) {
     // room for as many runs as give every block eight units, of the tiles that are cut at all
     l.fused = true;
     const int64_t rt = tiles_of(c.n, kFusedTile), vt = tiles_of(c.vocab, kFusedTile);
@@ -432,12 +439,13 @@ Layout layout_of(const mt_vocab_loss& c, bool backward) {
     l.runs_dw = vt > l.whole ? (int)std::min<int64_t>(rt, 8 * sms / (vt - l.whole) + 1) : 0;
     l.dw = take((size_t)l.runs_dw * (vt - l.whole) * kFusedTile * c.dim * 4);
   } else {
+    l.dz_parts = c.dtype == MT_F32 ? 3 : c.n <= kFewRowsTwice ? 2 : 1;
     l.max_chunks = 1 << 30;
-    const int64_t most = std::max<int64_t>(1, (int64_t)(kPieceBytes / ((size_t)l.rows * l.parts * 512)));
+    const int64_t most = std::max<int64_t>(1, (int64_t)(kPieceBytes / ((size_t)l.rows * l.dz_parts * 512)));
     const int64_t pieces = tiles_of(tiles_of(c.vocab, 256), most);
     l.piece = tiles_of(tiles_of(c.vocab, 256), pieces) * 256;
     l.coef = take((size_t)c.n * 16);
-    l.dz = take((size_t)l.rows * l.parts * l.piece * 2);
+    l.dz = take((size_t)l.rows * l.dz_parts * l.piece * 2);
     const int bn = sum_width(c.dim, c.dtype == MT_F32);
     const int64_t ct = tiles_of(c.dim, bn);
     // room for runs of the contraction: eight units a block, no run shorter than 8 steps, 256 MiB of dx
@@ -736,17 +744,17 @@ int mt_vocab_loss_backward(const mt_vocab_loss* c, const float* dloss, const flo
     p.coef = reinterpret_cast<float4*>(base + l.coef);
     p.dz = reinterpret_cast<__nv_bfloat16*>(base + l.dz);
     p.width = (int)(tiles_of(columns, 64) * 64);
-    const uint64_t zw = (uint64_t)l.parts * p.width;
+    const uint64_t zw = (uint64_t)l.dz_parts * p.width;
     CUtensorMap a, b;
     {
-      const bool pair = !fp32 && pair_rows(c->n, tiles_of(columns, 256), p.steps);
+      const bool pair = l.dz_parts == 1 && pair_rows(c->n, tiles_of(columns, 256), p.steps);
       if (!tc::encode_bf16(&a, 2, base + l.xs, xw, l.rows, xw, 1, 0, 64, 128)) return MT_ECUDA;
       if (!tc::encode_bf16(&b, 2, wv, w.width, columns, w.ld, 1, 0, 64, pair ? 128 : 256)) return MT_ECUDA;
-      if (!fp32 && !tc::encode_bf16(&p.map_dz, 2, p.dz, zw, l.rows, zw, 1, 0, 64, 32)) return MT_ECUDA;
-      e = launch_logit_grad(p, l.parts, a, b, tiles_of(c->n, pair ? 256 : 128), pair, s);
+      if (l.dz_parts == 1 && !tc::encode_bf16(&p.map_dz, 2, p.dz, zw, l.rows, zw, 1, 0, 64, 32)) return MT_ECUDA;
+      e = launch_logit_grad(p, l.dz_parts, a, b, tiles_of(c->n, pair ? 256 : 128), pair, s);
     }
     SumParams q{};
-    q.passes = 1;
+    q.passes = l.dz_parts == 2 ? 2 : 1;
     q.promote = fp32 ? 1 : 1 << 30;
     q.status = c->status;
     q.live = p.rows.count;

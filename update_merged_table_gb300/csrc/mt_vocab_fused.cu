@@ -10,10 +10,11 @@
 //   dx  a block keeps 128 rows of x and goes over entries of W
 //   dW  a block keeps 128 entries of W and goes over rows of x
 //
-//   S = x W^T into tensor memory; dz from S by eight warps, rounded to bf16, into
-//   shared memory (64 entries of a row are one 128-byte swizzled row); then
-//   dx += dz W or dW += dz^T x with the same tile of dz, read along its rows or
-//   across them, and the same tile of W or x that made S, read across.
+//   S = x W^T into tensor memory; dz from S by teams of four warps, rounded to bf16;
+//   then dx += dz W, dz in tensor memory in the place of S (its rows are the
+//   operand's), or dW += dz^T x, dz in shared memory (64 entries of a row are one
+//   128-byte swizzled row) and read across; with the same tile of W or x that made
+//   S, read across.
 //
 // One warp issues the products of S, as far ahead as there is room, another those
 // of the sums as their dz comes, so neither waits for what the other waits for; teams of four warps take the
@@ -33,7 +34,7 @@ constexpr int kAccAt = 3 * kT;           // tensor memory: S, then the sum
 struct FusedBarriers {
   uint64_t full[8], empty[8];        // a streamed tile has landed; its products are done
   uint64_t s_full[4], s_empty[4];    // S is finished; it has been read
-  uint64_t dz_full[3];               // dz is in shared memory
+  uint64_t dz_full[3];               // a team's dz is in its place
   uint64_t dz_empty[3];              // the products of a team's last tile of dz are done
   uint64_t kept_full, kept_empty;    // the kept tile has landed; its products are done
   uint64_t acc_full, acc_empty;      // a unit's sum is finished; it has been read
@@ -41,14 +42,19 @@ struct FusedBarriers {
   uint32_t tmem;
 };
 
-// KS: slabs of 64 columns.  Teams of four warps, each with a tile of dz of its own, and streamed tiles.
-template <int KS, bool STATS>
+// What a launch computes: dx, dW, or the rows' statistics (with smoothing: the sums of their logits too).
+enum Fused { kDx, kDw, kStats, kStatsSmooth };
+
+// KS: slabs of 64 columns.  Teams of four warps, streamed tiles, S under way, and (dW) a tile of dz for each team.
+template <int KS, int WHAT>
 struct FusedRing {
   static constexpr int kTile = KS * kSlab;
-  static constexpr int kTeams = STATS ? kNarrowTeams : KS == 1 ? 3 : 2, kThreads = (4 + kTeams * 4) * 32;
-  static constexpr int kStages = KS == 1 ? 6 : 4;
-  static constexpr int kS = STATS ? 4 : 3;  // S under way
-  static constexpr int kBytes = (1 + kStages) * kTile + (STATS ? 0 : kTeams * kDz);
+  static constexpr int kTeams = WHAT >= kStats ? kNarrowTeams : KS == 1 ? 3 : 2, kThreads = (4 + kTeams * 4) * 32;
+  static constexpr int kStages = KS == 1 ? 6 : WHAT == kDx ? 5 : 4;
+  static constexpr int kS = WHAT >= kStats ? 4 : 3;  // S under way
+  static constexpr int kDzAt = (1 + kStages) * kTile;
+  // behind the tiles: dz (dW), or where the sum's rows are turned (dx)
+  static constexpr int kBytes = kDzAt + (WHAT == kDw ? kTeams * kDz : WHAT == kDx ? 8 * 2048 : 0);
 };
 
 // A unit: a kept tile and streamed tiles [t0, t1).
@@ -67,21 +73,21 @@ struct FusedWork {
   }
 };
 
-// What a launch computes: dx, dW, or the rows' statistics (with smoothing: the sums of their logits too).
-enum Fused { kDx, kDw, kStats, kStatsSmooth };
-
 template <int KS, int WHAT>
-__global__ void __launch_bounds__(FusedRing<KS, (WHAT >= kStats)>::kThreads, 1)
+__global__ void __launch_bounds__(FusedRing<KS, WHAT>::kThreads, 1)
 k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ FusedParams p) {
   constexpr bool VOCAB = WHAT == kDw, STATS = WHAT >= kStats;
-  using R = FusedRing<KS, STATS>;
+  using R = FusedRing<KS, WHAT>;
   constexpr int kS = R::kS;
+  // a team's next tile waits for the products of its last: dW, whose dz has one place for each team; dx where there are more S
+  // than teams (else the team's next S waits for them)
+  constexpr bool kWaits = VOCAB || (WHAT == kDx && R::kTeams < kS);
   extern __shared__ uint8_t s_raw[];
   __shared__ FusedBarriers bar;
   uint8_t* base = reinterpret_cast<uint8_t*>(((uintptr_t)s_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* s_kept = base;
   uint8_t* s_ring = base + R::kTile;
-  uint8_t* s_dz = s_ring + R::kStages * R::kTile;
+  uint8_t* s_dz = base + R::kDzAt;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < R::kStages; ++i) {
@@ -90,7 +96,7 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     }
     for (int i = 0; i < kS; ++i) {
       tc::mbar_init(&bar.s_full[i], 1);
-      tc::mbar_init(&bar.s_empty[i], 4);
+      tc::mbar_init(&bar.s_empty[i], WHAT == kDx ? 1 : 4);
     }
     for (int i = 0; i < 3; ++i) {
       tc::mbar_init(&bar.dz_full[i], 4);
@@ -213,7 +219,7 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     // the sums.  A tile's S is done before its dz is, so what this warp signals of a sum holds for its S too.
     constexpr uint32_t instr = tc::instr_bf16(kT, KS * 64, VOCAB, true);
     const bool one = tc::elect_one();
-    const uint32_t ring = tc::desc_low(tc::smem_addr(s_ring), kSlab), dz = tc::desc_low(tc::smem_addr(s_dz), VOCAB ? kSlab : 16);
+    const uint32_t ring = tc::desc_low(tc::smem_addr(s_ring), kSlab), dz = tc::desc_low(tc::smem_addr(s_dz), kSlab);
     tc::Slot s;
     uint32_t n = 0, acc_phase = 0;
     bool ok = true;
@@ -230,11 +236,13 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         const uint32_t from = dz + b * (kDz >> 4), with = ring + s.stage * (R::kTile >> 4);
         if (one) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            tc::mma_bf16<1>(tmem + kAccAt, from + ((VOCAB ? i * 2048 : (i >> 2) * kSlab + (i & 3) * 32) >> 4), with + (i * 2048 >> 4), instr,
-                           t > x.t0 || i > 0);
+          for (int i = 0; i < 8; ++i) {
+            if (VOCAB) tc::mma_bf16<1>(tmem + kAccAt, from + (i * 2048 >> 4), with + (i * 2048 >> 4), instr, t > x.t0 || i > 0);
+            else tc::mma_bf16_tmem(tmem + kAccAt, tmem + n % kS * kT + i * 8, with + (i * 2048 >> 4), instr, t > x.t0 || i > 0);
+          }
           tc::mma_commit<1>(&bar.empty[s.stage]);
-          tc::mma_commit<1>(&bar.dz_empty[n % R::kTeams]);
+          if (!VOCAB) tc::mma_commit<1>(&bar.s_empty[n % kS]);
+          if (kWaits) tc::mma_commit<1>(&bar.dz_empty[b]);
         }
         __syncwarp();
         ++n;
@@ -297,16 +305,18 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   } else if (!STATS && warp >= 4) {
     const int quad = warp & 3, team = (warp - 4) >> 2;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    uint8_t* const stage = s_dz + team * kDz + quad * 4096;  // the warp's rows of dz; the sum goes out through them
-    uint8_t* const dz = stage + lane * 128;                  // the thread's row: two halves of 64 entries
+    // dW: the warp's rows of dz, through which the sum goes out too; the thread's row: two halves of 64 entries
+    uint8_t* const stage = VOCAB ? s_dz + team * kDz + quad * 4096 : s_dz + (team & 1) * 8192 + quad * 2048;
+    uint8_t* const dz = stage + lane * 128;
     const f32x2 s2 = both(p.scale2);
     uint32_t n = 0, acc_phase = 0;  // tiles so far
     bool ok = true;
     RowTargets to;
     float4 k = make_float4(0.0f, 0.0f, 0.0f, 0.0f), k_next = k;
     int id_next = 0x7FFFFFFF;  // a row's only target
-    // dz of 32 entries from their logits, four 16-byte pieces of a swizzled 128-byte row
-    auto columns = [&](const uint32_t (&v)[32], int c, int row, int v0, bool some) {
+    // dz of 32 entries from their logits: four 16-byte pieces of a swizzled 128-byte row (dW), or 16 columns of tensor memory in
+    // the place of S, whose columns up to there have been read (dx)
+    auto columns = [&](const uint32_t (&v)[32], uint32_t from, int c, int row, int v0, bool some) {
       float f[32];
       const f32x2 x2 = both(-k.x), y2 = both(k.y), z2 = both(-k.z);
 #pragma unroll
@@ -323,11 +333,17 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         for (int j = 0; j < 32; ++j)
           if (!(there >> j & 1)) f[j] = 0.0f;
       }
+      if constexpr (!VOCAB) {
+        uint32_t w[16];
+        tiles::narrow32(f, w);
+        tc::tmem_store16(from + (c >> 1), w);
+      } else {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<uint4*>(dz + (c >> 6) * kSlab + (((((c >> 5) & 1) * 4 + q) ^ (lane & 7)) << 4)) =
-            make_uint4(bf16x2_of(f[q * 8], f[q * 8 + 1]), bf16x2_of(f[q * 8 + 2], f[q * 8 + 3]), bf16x2_of(f[q * 8 + 4], f[q * 8 + 5]),
-                       bf16x2_of(f[q * 8 + 6], f[q * 8 + 7]));
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint4*>(dz + (c >> 6) * kSlab + (((((c >> 5) & 1) * 4 + q) ^ (lane & 7)) << 4)) =
+              make_uint4(bf16x2_of(f[q * 8], f[q * 8 + 1]), bf16x2_of(f[q * 8 + 2], f[q * 8 + 3]), bf16x2_of(f[q * 8 + 4], f[q * 8 + 5]),
+                         bf16x2_of(f[q * 8 + 6], f[q * 8 + 7]));
+      }
     };
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const FusedUnit x = work.unit(u);
@@ -362,7 +378,7 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             }
           }
           const bool some = __any_sync(kFull, to.next < v0 + kT || row >= work.live) || v0 + kT > p.vocab;
-          ok = __all_sync(kFull, tc::mbar_wait(&bar.s_full[b], of / kS & 1) && tc::mbar_wait(&bar.dz_empty[team], (of / R::kTeams & 1) ^ 1));
+          ok = __all_sync(kFull, tc::mbar_wait(&bar.s_full[b], of / kS & 1) && (!kWaits || tc::mbar_wait(&bar.dz_empty[team], (of / R::kTeams & 1) ^ 1)));
           if (!ok) break;
           tc::fence_after();
           // two teams: the next columns' load is on its way meanwhile (three have no registers for it, and overlap more)
@@ -374,16 +390,21 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             uint32_t (&now)[32] = v[kTwo ? c >> 5 & 1 : 0];
             if (!kTwo) tc::tmem_load32(from + c, now);
             tc::tmem_load_wait(now);
-            if (c + 32 == kT) {
+            if (c + 32 < kT) {
+              if (kTwo) tc::tmem_load32(from + c + 32, v[(c >> 5 & 1) ^ 1]);
+            } else if (VOCAB) {
               tc::fence_before();
               __syncwarp();
               if (lane == 0) tc::mbar_arrive(&bar.s_empty[b]);
-            } else if (kTwo) {
-              tc::tmem_load32(from + c + 32, v[(c >> 5 & 1) ^ 1]);
             }
-            columns(now, c, row, v0, some);
+            columns(now, from, c, row, v0, some);
           }
-          tc::fence_async_proxy();
+          if (VOCAB) {
+            tc::fence_async_proxy();
+          } else {
+            tc::tmem_store_wait();
+            tc::fence_before();
+          }
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&bar.dz_full[team]);
         }
@@ -435,7 +456,7 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
 
 template <int KS, int WHAT>
 cudaError_t launch(const char* name, const CUtensorMap& x, const CUtensorMap& w, const FusedParams& p, long long units, cudaStream_t s) {
-  using R = FusedRing<KS, (WHAT >= kStats)>;
+  using R = FusedRing<KS, WHAT>;
   constexpr size_t bytes = 1024 + R::kBytes;
   static SmemLimit limit;
   const cudaError_t e = limit.allow(k_vocab_fused<KS, WHAT>, bytes);

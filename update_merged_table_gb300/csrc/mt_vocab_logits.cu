@@ -10,8 +10,8 @@
 //                   by: the targets lie in ascending order, so one comparison per
 //                   32 columns finds them.
 //  their gradient   with the row's log sum known, dz = a p - b less the targets'
-//                   shares, rounded to bf16 (fp32 rows: three bf16 parts), a piece
-//                   of the vocabulary at a time.
+//                   shares, rounded to bf16 (few rows: two bf16 parts, fp32 rows:
+//                   three), a piece of the vocabulary at a time.
 #include <algorithm>
 
 #include "mt_tiles.cuh"
@@ -113,7 +113,7 @@ struct Stats : Logits<CG, KEEP> {
   }
 };
 
-template <bool SPLIT, int CG, bool KEEP>  // SPLIT: dz in three bf16 parts
+template <int PARTS, int CG, bool KEEP>  // of dz, bf16 each
 struct Grad : Logits<CG, KEEP> {
   using Base = Logits<CG, KEEP>;
   float4 k;
@@ -124,7 +124,7 @@ struct Grad : Logits<CG, KEEP> {
   }
   __device__ void end(const Unit&) {}
   __device__ void finish() {
-    if (!SPLIT && this->lane == 0) tc::bulk_done();
+    if (PARTS == 1 && this->lane == 0) tc::bulk_done();
   }
   // dz of 32 columns
   __device__ __forceinline__ void columns(const uint32_t (&v)[32], int at0, int left, bool some, float (&f)[32]) {
@@ -156,7 +156,7 @@ struct Grad : Logits<CG, KEEP> {
           make_uint4(bf16x2_of(f[q * 8], f[q * 8 + 1]), bf16x2_of(f[q * 8 + 2], f[q * 8 + 3]), bf16x2_of(f[q * 8 + 4], f[q * 8 + 5]),
                      bf16x2_of(f[q * 8 + 6], f[q * 8 + 7]));
   }
-  __device__ __forceinline__ void put_split(const float (&f)[32], int at0, long long r0) {
+  __device__ __forceinline__ void put_parts(const float (&f)[32], int at0, long long r0) {
     const LogitParams& p = this->p;
     uint32_t w[3][16];
 #pragma unroll
@@ -167,8 +167,8 @@ struct Grad : Logits<CG, KEEP> {
       for (int q = 0; q < 3; ++q) w[q][j] = t[q];
     }
 #pragma unroll
-    for (int q = 0; q < 3; ++q)
-      tiles::store_rows<__nv_bfloat16>(this->stage, this->lane, w[q], p.dz + (size_t)q * p.width, (size_t)3 * p.width, r0, 32, at0, p.width, tiles::kSectors);
+    for (int q = 0; q < PARTS; ++q)
+      tiles::store_rows<__nv_bfloat16>(this->stage, this->lane, w[q], p.dz + (size_t)q * p.width, (size_t)PARTS * p.width, r0, 32, at0, p.width, tiles::kSectors);
   }
   template <int G>
   __device__ __forceinline__ void tile(const Unit& x, int ct, const Acc& acc, bool, bool) {
@@ -184,8 +184,8 @@ struct Grad : Logits<CG, KEEP> {
       tc::tmem_load_wait(v[0]);
       acc.load(c + 32, v[1]);
       columns(v[0], at + c, left - c, some, f);
-      if constexpr (SPLIT) {
-        put_split(f, at + c, r0);
+      if constexpr (PARTS > 1) {
+        put_parts(f, at + c, r0);
       } else {
         if (this->lane == 0) tc::bulk_read();  // the last 64 columns' copy has read them
         __syncwarp();
@@ -195,8 +195,8 @@ struct Grad : Logits<CG, KEEP> {
       if (c + 64 < kBN) acc.load(c + 64, v[0]);
       else acc.release<G>(this->lane);
       columns(v[1], at + c + 32, left - c - 32, some, f);
-      if constexpr (SPLIT) {
-        put_split(f, at + c + 32, r0);
+      if constexpr (PARTS > 1) {
+        put_parts(f, at + c + 32, r0);
       } else {
         to_stage(f, 1);
         tc::fence_async_proxy();
@@ -230,11 +230,14 @@ cudaError_t launch_logit_stats(const LogitParams& p, const CUtensorMap& a, const
 cudaError_t launch_logit_grad(const LogitParams& p, int parts, const CUtensorMap& a, const CUtensorMap& b, long long row_tiles, bool pair,
                               cudaStream_t s) {
   const char* name = "k_logit_grad";
-  if (parts == 3)
-    return p.kept > 0 ? launch_op<Grad<true, 1, true>, 1>(name, p, a, b, row_tiles, s) : launch_op<Grad<true, 1, false>, 1>(name, p, a, b, row_tiles, s);
-  if (p.kept > 0)
-    return pair ? launch_op<Grad<false, 2, true>, 2>(name, p, a, b, row_tiles, s) : launch_op<Grad<false, 1, true>, 1>(name, p, a, b, row_tiles, s);
-  return pair ? launch_op<Grad<false, 2, false>, 2>(name, p, a, b, row_tiles, s) : launch_op<Grad<false, 1, false>, 1>(name, p, a, b, row_tiles, s);
+  auto single = [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    return p.kept > 0 ? launch_op<Grad<N, 1, true>, 1>(name, p, a, b, row_tiles, s) : launch_op<Grad<N, 1, false>, 1>(name, p, a, b, row_tiles, s);
+  };
+  if (parts == 3) return single(std::integral_constant<int, 3>{});
+  if (parts == 2) return single(std::integral_constant<int, 2>{});
+  if (!pair) return single(std::integral_constant<int, 1>{});
+  return p.kept > 0 ? launch_op<Grad<1, 2, true>, 2>(name, p, a, b, row_tiles, s) : launch_op<Grad<1, 2, false>, 2>(name, p, a, b, row_tiles, s);
 }
 
 }  // namespace mt
