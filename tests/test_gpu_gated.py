@@ -112,6 +112,16 @@ def test_gates(gate, dtype):
     check_all(x, w, dh, off, dtype, gate)
 
 
+@pytest.mark.parametrize("gate", ["linear", "sigmoid", "silu", "gelu"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_large_gates(gate, dtype):
+    """u of 1e20 to 1e22 either way: its square is no fp32 number, everything that is asked for is one."""
+    x, w, dh, off = make(13, [40, 5], 0, 0, dtype, 24, 40)
+    w[:, 40:] *= 1e21
+    _, h, (dx, dw) = check_all(x, w, dh, off, dtype, gate)
+    assert bool(torch.isfinite(h).all()) and bool(torch.isfinite(dx).all()) and bool(torch.isfinite(dw).all())
+
+
 @pytest.mark.parametrize("sizes,k,m", [([9001, 0, 3, 20000], 256, 512), ([300, 700, 40], 1024, 2048), ([129, 2], 2048, 1032),
                                        ([2000] * 8, 512, 1024), ([6000, 5001], 33, 250)])
 def test_long_groups(sizes, k, m):

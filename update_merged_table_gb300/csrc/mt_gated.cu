@@ -57,7 +57,8 @@ __device__ __forceinline__ float2 gate_grad(float u) {
     const float p = sigmoid_of<T>(u), a = u * p;
     return make_float2(a, fmaf(a, 1.0f - p, p));
   }
-  const float uu = u * u, p = sigmoid_of<T>(kGelu * fmaf(kCube * uu, u, u)), a = u * p;
+  // (p is 0 or 1 long before the limit on u u, which keeps 0 from meeting infinity)
+  const float uu = fminf(u * u, 1e30f), p = sigmoid_of<T>(kGelu * fmaf(kCube * uu, u, u)), a = u * p;
   return make_float2(a, fmaf(a * (1.0f - p), kGelu * fmaf(3.0f * kCube, uu, 1.0f), p));
 }
 template <int GATE>
