@@ -311,6 +311,20 @@ def test_threads_and_streams_side_by_side():
         assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+@pytest.mark.parametrize("n,v,d,dtype,top", [(70000, 40000, 136, "bf16", 0), (70000, 12001, 40, "f32", 0), (66001, 36000, 520, "bf16", 3)])
+def test_vocabulary_in_pieces(n, v, d, dtype, top):
+    """More of dz than there is room for: the vocabulary comes in two pieces (few rows take part)."""
+    s = make(31, n, v, d, dtype, top=top, masked=0.99)
+    live = (s["ids"] >= 0).any(1) if top else s["targets"] >= 0
+    handle = mt.Distillation(v, d, top, dtype=dtype) if top else mt.CrossEntropy(v, d, dtype=dtype)
+    args = (s["ids"], s["logits"]) if top else (s["targets"],)
+    r = handle.forward(s["x"], s["w"], *args)
+    dx, dw = handle.backward(s["dloss"], s["x"], s["w"], *args, r.lse)
+    assert not r.loss[~live].any() and not r.lse[~live].any() and not dx[~live].any()
+    c = {k: t if k == "w" else t[live] for k, t in s.items()}
+    check_all(c, dtype, handle=handle, forward=mt.LossForward(r.loss[live], r.lse[live]), grads=(dx[live], dw))
+
+
 @pytest.mark.slow
 def test_offsets_past_32_bits():
     """Rows of x, W and dx more than 2^31 elements apart from their first."""
