@@ -411,8 +411,8 @@ inline int reach_of(const void* data, int64_t ld, int64_t columns, size_t bytes)
 __device__ __forceinline__ void store_sector(void* to, const uint32_t* w);
 
 // Stores 64 bytes of each lane's row (w: 16 words; element j of the row is column col + j): rows [0, rows) of C from r0 on,
-// columns below J.  In sectors the shared memory's bandwidth stays with the products' operands (8192 rows x 20,000 entries
-// x 512: TODO).
+// columns below J.  In sectors where rows allow it: nothing passes through shared memory, whose bandwidth the products
+// need.
 template <typename T>
 __device__ __forceinline__ void store_rows(uint8_t* stage, int lane, const uint32_t (&w)[16], T* C, size_t ldc, long long r0,
                                            int rows, int col, int J, int reach) {
