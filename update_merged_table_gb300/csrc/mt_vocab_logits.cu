@@ -3,8 +3,7 @@
 // keeps its rows of x for a whole run of the vocabulary, which halves what it reads
 // from L2.
 //
-//
-//  the statistics   a thread has one row of every other tile.  It keeps the largest
+//  the statistics   a thread has one row of half of each tile.  It keeps the largest
 //                   logit so far and the sum of 2^(z - largest) over a run of tiles (an online softmax in base 2, one exponential a
 //                   logit), and picks the logits of the row's targets as they come
 //                   by: the targets lie in ascending order, so one comparison per
@@ -24,12 +23,18 @@ namespace {
 using tiles::Acc;
 using tiles::Unit;
 
+// Columns of a tile that a team of epilogue warps has.  Both teams at one tile leave its accumulator twice as soon as teams in
+// turns, and all columns of a row in registers have one largest value and one chain of sums.  Measured with teams in turns and
+// 32 columns at a time, with halves, and with halves at once: 32,769 of 65,537 rows x 16,384 x 256 statistics 214, 190 and 170 us,
+// gradient 284, 252 and 244; 4096 x 131,072 x 1024, bound by the products, 609, 609 and 630, and 719, 633 and 654.
+constexpr int kHalf = 128;
+
 // What both kernels share: rows tiles fastest, so that blocks at work at the same time read the same entries of W.
 template <int CG, bool KEEP>
 struct Logits {
   using Params = LogitParams;
   static constexpr int kBN = 256;
-  static constexpr bool kAMN = false, kBMN = false, kTwoB = false, kTeams = true, kKeep = KEEP, kAhead = false, kSplit = false, kSingle = false, kTri = false;
+  static constexpr bool kAMN = false, kBMN = false, kTwoB = false, kTeams = false, kKeep = KEEP, kAhead = false, kSplit = true, kSingle = false, kTri = false;
   static constexpr int kStageOut = 4096;  // 32 rows x 128 bytes
   const Params& p;
   int rank, live, rt, chunks;
@@ -62,6 +67,16 @@ struct Logits {
     team = h;
     lane = l;
   }
+  // A warp's columns of a tile, all at once: the accumulator is free for the next products before the arithmetic begins.
+  template <int G>
+  __device__ __forceinline__ void load(const Acc& acc, uint32_t (&v)[kHalf / 32][32]) const {
+#pragma unroll
+    for (int i = 0; i < kHalf / 32; ++i) acc.load(team * kHalf + i * 32, v[i]);
+    tc::tmem_load_wait(v[0]);
+#pragma unroll
+    for (int i = 1; i < kHalf / 32; ++i) tc::tmem_loaded(v[i]);
+    acc.release<G>(lane);
+  }
   __device__ void start(const Unit& x) {
     row = x.row0 + rank * tiles::kBM + quad * 32 + lane;
     to.start(p.rows, row, live, p.v0 + x.ct0 * kBN);
@@ -85,31 +100,20 @@ struct Stats : Logits<CG, KEEP> {
     this->p.part[at] = make_float2(stats.top, stats.sum);
     if constexpr (SMOOTH) this->p.sum_z[at] = stats.total;
   }
-  // 32 columns; the next columns' load is on its way meanwhile.  some: there may be targets among them, or columns that are
-  // not there.
-  __device__ __forceinline__ void columns(uint32_t (&v)[32], int col, int left, bool some) {
-    if (some) this->to.pick(this->p.rows, col, v, this->p.picked);
-    stats.add(v, this->p.scale2, some ? left : 32);
-  }
   __device__ void finish() {}
   template <int G>
   __device__ __forceinline__ void tile(const Unit&, int ct, const Acc& acc, bool, bool) {
     const LogitParams& p = this->p;
-    constexpr int kBN = Base::kBN;
-    const int at = ct * kBN, left = p.columns - at;
-    const bool some = left < kBN || __any_sync(kFull, this->to.next < p.v0 + at + kBN);
-    uint32_t v[2][32];
-    acc.load(0, v[0]);
-#pragma unroll 1
-    for (int c = 0; c < kBN; c += 64) {
-      tc::tmem_load_wait(v[0]);
-      acc.load(c + 32, v[1]);
-      columns(v[0], p.v0 + at + c, left - c, some);
-      tc::tmem_load_wait(v[1]);
-      if (c + 64 < kBN) acc.load(c + 64, v[0]);
-      else acc.release<G>(this->lane);
-      columns(v[1], p.v0 + at + c + 32, left - c - 32, some);
+    const int at = ct * Base::kBN + this->team * kHalf, left = p.columns - at;
+    // there may be targets among the columns, or columns that are not there
+    const bool some = left < kHalf || __any_sync(kFull, this->to.next < p.v0 + at + kHalf);
+    uint32_t v[kHalf / 32][32];
+    this->template load<G>(acc, v);
+    if (some) {
+#pragma unroll
+      for (int i = 0; i < kHalf / 32; ++i) this->to.pick(p.rows, p.v0 + at + i * 32, v[i], p.picked);
     }
+    stats.add(v, p.scale2, some ? left : kHalf);
   }
 };
 
@@ -172,36 +176,29 @@ struct Grad : Logits<CG, KEEP> {
   }
   template <int G>
   __device__ __forceinline__ void tile(const Unit& x, int ct, const Acc& acc, bool, bool) {
-    constexpr int kBN = Base::kBN;
-    const int at = ct * kBN, left = this->p.columns - at;
+    const int at = ct * Base::kBN + this->team * kHalf, left = this->p.columns - at;
     const int r0 = x.row0 + this->rank * tiles::kBM + this->quad * 32;
-    const bool some = left < kBN || __any_sync(kFull, this->to.next < this->p.v0 + at + kBN || this->row >= this->live);
-    uint32_t v[2][32];
-    float f[32];
-    acc.load(0, v[0]);
-#pragma unroll 1
-    for (int c = 0; c < kBN; c += 64) {
-      tc::tmem_load_wait(v[0]);
-      acc.load(c + 32, v[1]);
-      columns(v[0], at + c, left - c, some, f);
+    const bool some = left < kHalf || __any_sync(kFull, this->to.next < this->p.v0 + at + kHalf || this->row >= this->live);
+    uint32_t v[kHalf / 32][32];
+    this->template load<G>(acc, v);
+#pragma unroll
+    for (int i = 0; i < kHalf / 32; ++i) {
+      float f[32];
+      const int c = i * 32;
+      columns(v[i], at + c, left - c, some, f);
       if constexpr (PARTS > 1) {
         put_parts(f, at + c, r0);
       } else {
-        if (this->lane == 0) tc::bulk_read();  // the last 64 columns' copy has read them
-        __syncwarp();
-        to_stage(f, 0);
-      }
-      tc::tmem_load_wait(v[1]);
-      if (c + 64 < kBN) acc.load(c + 64, v[0]);
-      else acc.release<G>(this->lane);
-      columns(v[1], at + c + 32, left - c - 32, some, f);
-      if constexpr (PARTS > 1) {
-        put_parts(f, at + c + 32, r0);
-      } else {
-        to_stage(f, 1);
-        tc::fence_async_proxy();
-        __syncwarp();
-        if (this->lane == 0 && at + c < this->p.width) tc::tma_store_2d(&this->p.map_dz, this->stage, at + c, r0);
+        if (i % 2 == 0) {
+          if (this->lane == 0) tc::bulk_read();  // the last 64 columns' copy has read them
+          __syncwarp();
+        }
+        to_stage(f, i % 2);
+        if (i % 2 == 1) {
+          tc::fence_async_proxy();
+          __syncwarp();
+          if (this->lane == 0 && at + c - 32 < this->p.width) tc::tma_store_2d(&this->p.map_dz, this->stage, at + c - 32, r0);
+        }
       }
     }
   }

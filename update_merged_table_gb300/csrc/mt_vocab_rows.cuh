@@ -102,40 +102,55 @@ struct RowStats {
     top = -INFINITY;
     sum = total = 0.0f;
   }
-  // 32 columns: their largest, then one exponential each; only the first `left` count.
-  __device__ __forceinline__ void add(uint32_t (&v)[32], float scale2, int left) {
+  // N x 32 columns: their largest, then one exponential each; only the first `left` count.
+  template <int N>
+  __device__ __forceinline__ void add(uint32_t (&v)[N][32], float scale2, int left) {
     if constexpr (SMOOTH) {
       f32x2 t[2] = {0ull, 0ull};
 #pragma unroll
-      for (int j = 0; j < 32; j += 2)  // (columns that are not there are zero)
-        t[j >> 1 & 1] = add2(t[j >> 1 & 1], pk(__uint_as_float(v[j]), __uint_as_float(v[j + 1])));
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < 32; j += 2)  // (columns that are not there are zero)
+          t[j >> 1 & 1] = add2(t[j >> 1 & 1], pk(__uint_as_float(v[i][j]), __uint_as_float(v[i][j + 1])));
       total += pair_sum(add2(t[0], t[1]));
     }
-    if (left < 32) {
-      const uint32_t there = below(left);
+    if (left < N * 32) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (!(there >> j & 1)) v[j] = 0xFF800000u;
+      for (int i = 0; i < N; ++i) {
+        const uint32_t there = below(left - i * 32);
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (!(there >> j & 1)) v[i][j] = 0xFF800000u;
+      }
     }
     float m[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      m[i] = __uint_as_float(v[i * 8]);
+      m[i] = __uint_as_float(v[0][i * 8]);
 #pragma unroll
-      for (int j = 1; j < 7; j += 2) m[i] = max3(m[i], __uint_as_float(v[i * 8 + j]), __uint_as_float(v[i * 8 + j + 1]));
-      m[i] = fmaxf(m[i], __uint_as_float(v[i * 8 + 7]));
+      for (int j = 1; j < 7; j += 2) m[i] = max3(m[i], __uint_as_float(v[0][i * 8 + j]), __uint_as_float(v[0][i * 8 + j + 1]));
+      m[i] = fmaxf(m[i], __uint_as_float(v[0][i * 8 + 7]));
+#pragma unroll
+      for (int n = 1; n < N; ++n)
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) m[i] = max3(m[i], __uint_as_float(v[n][i * 8 + j]), __uint_as_float(v[n][i * 8 + j + 1]));
     }
     const float now = max3(top, fmaxf(m[0], m[1]) * scale2, fmaxf(m[2], m[3]) * scale2);
     const float off = now == -INFINITY ? 0.0f : now;
     const f32x2 s2 = both(scale2), o2 = both(-off);
     f32x2 s[2] = {0ull, 0ull};
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      const float2 e = upk(fma2(pk(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), s2, o2));
-      s[j >> 1 & 1] = add2(s[j >> 1 & 1], pk(exp2_of(e.x), exp2_of(e.y)));
-    }
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        const float2 e = upk(fma2(pk(__uint_as_float(v[i][j]), __uint_as_float(v[i][j + 1])), s2, o2));
+        s[j >> 1 & 1] = add2(s[j >> 1 & 1], pk(exp2_of(e.x), exp2_of(e.y)));
+      }
     sum = fmaf(sum, exp2_of(top - off), pair_sum(add2(s[0], s[1])));
     top = now;
+  }
+  __device__ __forceinline__ void add(uint32_t (&v)[32], float scale2, int left) {
+    add<1>(reinterpret_cast<uint32_t(&)[1][32]>(v), scale2, left);
   }
 };
 
