@@ -280,17 +280,22 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         if (!ok) break;
         tc::fence_after();
 #pragma unroll
-        for (int c = 0; c < kT; c += 32) {
-          uint32_t v[32];
-          tc::tmem_load32(from + c, v);
-          tc::tmem_load_wait(v);
-          if (c + 32 == kT) {
+        for (int c = 0; c < kT; c += 64) {
+          uint32_t v[2][32];
+          tc::tmem_load32(from + c, v[0]);
+          tc::tmem_load32(from + c + 32, v[1]);
+          tc::tmem_load_wait(v[0]);
+          tc::tmem_loaded(v[1]);
+          if (c + 64 == kT) {
             tc::fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bar.s_empty[b]);
           }
-          if (some) to.pick(p.rows, v0 + c, v, p.picked);
-          stats.add(v, p.scale2, some ? left - c : 32);
+          if (some) {
+            to.pick(p.rows, v0 + c, v[0], p.picked);
+            to.pick(p.rows, v0 + c + 32, v[1], p.picked);
+          }
+          stats.add(v, p.scale2, some ? left - c : 64);
         }
       }
       if (!ok) break;
@@ -381,23 +386,20 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
           ok = __all_sync(kFull, tc::mbar_wait(&bar.s_full[b], of / kS & 1) && (!kWaits || tc::mbar_wait(&bar.dz_empty[team], (of / R::kTeams & 1) ^ 1)));
           if (!ok) break;
           tc::fence_after();
-          // two teams: the next columns' load is on its way meanwhile (three have no registers for it, and overlap more)
-          constexpr bool kTwo = R::kTeams == 2;
-          uint32_t v[kTwo ? 2 : 1][32];
-          if (kTwo) tc::tmem_load32(from, v[0]);
 #pragma unroll
-          for (int c = 0; c < kT; c += 32) {
-            uint32_t (&now)[32] = v[kTwo ? c >> 5 & 1 : 0];
-            if (!kTwo) tc::tmem_load32(from + c, now);
-            tc::tmem_load_wait(now);
-            if (c + 32 < kT) {
-              if (kTwo) tc::tmem_load32(from + c + 32, v[(c >> 5 & 1) ^ 1]);
-            } else if (VOCAB) {
+          for (int c = 0; c < kT; c += 64) {
+            uint32_t v[2][32];
+            tc::tmem_load32(from + c, v[0]);
+            tc::tmem_load32(from + c + 32, v[1]);
+            tc::tmem_load_wait(v[0]);
+            tc::tmem_loaded(v[1]);
+            if (VOCAB && c + 64 == kT) {
               tc::fence_before();
               __syncwarp();
               if (lane == 0) tc::mbar_arrive(&bar.s_empty[b]);
             }
-            columns(now, from, c, row, v0, some);
+            columns(v[0], from, c, row, v0, some);
+            columns(v[1], from, c + 32, row, v0, some);
           }
           if (VOCAB) {
             tc::fence_async_proxy();
