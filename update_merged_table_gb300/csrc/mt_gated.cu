@@ -94,14 +94,14 @@ template <typename T, bool BACKWARD>
 struct Gated {
   using Params = GatedParams;
   static constexpr int kBN = 256;
-  static constexpr bool kAMN = false, kBMN = false, kTwoB = true, kTeams = true, kKeep = false, kSingle = true, kTri = false;
+  static constexpr bool kAMN = false, kBMN = false, kTwoB = true, kTeams = false, kKeep = false, kSingle = true, kTri = false;
   static constexpr int kStageOut = 2048;  // 32 rows x 64 bytes
-  static constexpr bool kSplit = BACKWARD && sizeof(T) == 2;
+  static constexpr bool kSplit = !BACKWARD || sizeof(T) == 2;
   static constexpr bool kAhead = BACKWARD && sizeof(T) == 2;  // dh of a tile's first columns is on its way before the tile
   const Params& p;
   const long long* off;
   const int* cum;
-  int rank, rows_per_tile, quad, lane, group = 0;
+  int rank, rows_per_tile, quad, team, lane, group = 0;
   uint8_t* stage;
   uint4 dh[4];
 
@@ -140,6 +140,7 @@ struct Gated {
   __device__ void warp(uint8_t* s, int q, int h, int l) {
     stage = s;
     quad = q;
+    team = h;
     lane = l;
     const int J = BACKWARD ? 2 * p.u_col : p.out_dim;
     zero_outside<T>(off, p.groups, p.n, static_cast<T*>(p.out), p.ldo, J, tiles::kEpiWarps * 32, (h * 4 + q) * 32 + l);
@@ -159,7 +160,7 @@ struct Gated {
     }
   }
   __device__ __forceinline__ void ahead(const Unit& x, int ct) {
-    if (p.reach_dh != tiles::kElements) fetch(x, ct * 128);
+    if (p.reach_dh != tiles::kElements) fetch(x, ct * 128 + team * 64);
   }
 
   template <int CG>
@@ -171,12 +172,22 @@ struct Gated {
     const long long r0 = x.row0 + rank * tiles::kBM + quad * 32;
     const int rows = min(32, x.end - (int)r0);  // <= 0: none of this warp's rows is in the group
     T* out = static_cast<T*>(p.out);
-#pragma unroll 1
-    for (int c = 0; c < 128; c += 32) {
-      const int col = ct * 128 + c;
-      uint32_t y[32], u[32];
-      acc.load(c, y);
-      acc.load(128 + c, u);
+    // Of the team's 64 columns the forward loads all at once: the accumulator is free for the next products before the
+    // arithmetic begins.  (The backward has registers for 32.)
+    constexpr int kOnce = BACKWARD ? 1 : 2;
+    uint32_t ys[kOnce][32], us[kOnce][32];
+#pragma unroll(kOnce)
+    for (int i = 0; i < 2; ++i) {
+      const int col = ct * 128 + team * 64 + i * 32;
+      uint32_t (&y)[32] = ys[BACKWARD ? 0 : i];
+      uint32_t (&u)[32] = us[BACKWARD ? 0 : i];
+      if (BACKWARD || i == 0) {
+#pragma unroll
+        for (int k = 0; k < kOnce; ++k) {
+          acc.load(team * 64 + (i + k) * 32, ys[k]);
+          acc.load(128 + team * 64 + (i + k) * 32, us[k]);
+        }
+      }
       uint32_t d[BACKWARD ? 32 : 1];  // dh: bf16 pairs as they lie in the first 16, or fp32
       if constexpr (BACKWARD) {
         if constexpr (sizeof(T) == 2) {
@@ -188,7 +199,7 @@ struct Gated {
               d[4 * j + 2] = dh[j].z;
               d[4 * j + 3] = dh[j].w;
             }
-            if (c < 96) fetch(x, col + 32);
+            if (i == 0) fetch(x, col + 32);
           }
         }
         if (sizeof(T) == 4 || p.reach_dh == tiles::kElements) {
@@ -203,26 +214,32 @@ struct Gated {
           }
         }
       }
-      tc::tmem_load_wait(y);
-      tc::tmem_loaded(u);
-      if (c == 96) acc.release<CG>(lane);
+      if (BACKWARD || i == 0) {
+        tc::tmem_load_wait();
+#pragma unroll
+        for (int k = 0; k < kOnce; ++k) {
+          tc::tmem_loaded(ys[k]);
+          tc::tmem_loaded(us[k]);
+        }
+        if (!BACKWARD || i == 1) acc.release<CG>(lane);
+      }
       // y becomes h, or dy; u du.  bf16: two columns to a word
       constexpr int kWords = sizeof(T) == 2 ? 16 : 32;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         float a[2], b[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float yy = __uint_as_float(y[2 * j + i]), uu = __uint_as_float(u[2 * j + i]);
+        for (int e = 0; e < 2; ++e) {
+          const float yy = __uint_as_float(y[2 * j + e]), uu = __uint_as_float(u[2 * j + e]);
           if constexpr (BACKWARD) {
             float g;
-            if constexpr (sizeof(T) == 2) g = __uint_as_float(i == 0 ? d[j] << 16 : d[j] & 0xFFFF0000u);
-            else g = __uint_as_float(d[2 * j + i]);
+            if constexpr (sizeof(T) == 2) g = __uint_as_float(e == 0 ? d[j] << 16 : d[j] & 0xFFFF0000u);
+            else g = __uint_as_float(d[2 * j + e]);
             const float2 t = gate_grad<T, GATE>(uu);
-            a[i] = g * t.x;
-            b[i] = g * yy * t.y;
+            a[e] = g * t.x;
+            b[e] = g * yy * t.y;
           } else {
-            a[i] = yy * gate_of<T, GATE>(uu);
+            a[e] = yy * gate_of<T, GATE>(uu);
           }
         }
         if constexpr (sizeof(T) == 2) {

@@ -121,7 +121,7 @@ __device__ __forceinline__ int kept_of(const typename Op::Params& p) {
 //   warp(stage, quad, team, lane), finish()   once, epilogue warps: before the first unit, after the last
 //   kAhead, ahead(x, ct)       before a tile is waited for
 //   kSplit                     more registers for the epilogue
-//   kSingle                    every unit is one tile of p.steps with one accumulator (and teams take turns)
+//   kSingle                    every unit is one tile of p.steps with one accumulator
 //   begin(x), tile(x, ct, acc, first, last), end(x)   a unit; a column tile's accumulator, or (promote) the parts of it
 template <class Op, int CG>
 __global__ void __launch_bounds__(kThreadsT, 1)
@@ -354,7 +354,7 @@ k_tiles(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
     uint32_t seq = 0;  // accumulators so far
     bool ok = true;
     for (long long u = u0; u < units && ok; u += ustep) {
-      if (Op::kSingle && (seq & 1) != team) {  // the other team's
+      if (Op::kSingle && Op::kTeams && (seq & 1) != team) {  // the other team's
         ++seq;
         continue;
       }
