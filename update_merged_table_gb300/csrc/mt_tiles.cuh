@@ -7,9 +7,15 @@
 // its operator deals out (a row tile and a run of column tiles); one thread
 // keeps a ring of stages filled by TMA, one issues the products into one of two or
 // four accumulators in tensor memory, and two teams of four warps hand finished tiles
-// to the operator while the next tile's products run: a team takes every other
-// tile, so that one's loads and waits overlap the other's arithmetic (or, where an
-// operator adds tiles up in registers, half of each tile's columns).
+// to the operator while the next tile's products run: half of a tile's columns each,
+// which leaves the accumulator soonest (the losses: 214 to 190 us, see there), or
+// (kTeams) every other tile each.
+//
+// Bound: by the products from 512 columns of contraction on (7373 rows x 100,003
+// entries x 512: 400 to 450 us, 1.7 to 1.9 PFLOP/s, the clock held down by power);
+// shorter ones by what their epilogue does with a tile.  All of a warp issues
+// products and copies by an elected lane: by lane 0 four products took 690 clocks,
+// so 512.
 //
 // An operand lies with its contraction contiguous, or with its rows contiguous
 // (A_MN, B_MN).  fp32 operands come as three bf16 parts side by side whose sum
@@ -354,10 +360,6 @@ k_tiles(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUten
     uint32_t seq = 0;  // accumulators so far
     bool ok = true;
     for (long long u = u0; u < units && ok; u += ustep) {
-      if (Op::kSingle && Op::kTeams && (seq & 1) != team) {  // the other team's
-        ++seq;
-        continue;
-      }
       const Unit x = op.unit(u);
       op.begin(x);
       const int steps = (x.k1 - x.k0) * p.passes;

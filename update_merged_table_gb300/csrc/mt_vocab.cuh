@@ -75,7 +75,7 @@ cudaError_t launch_vocab_sum(const SumParams& p, bool fp32, const CUtensorMap& a
                              cudaStream_t s);
 
 // The statistics and gradients for narrow rows, without a dz in memory (mt_vocab_fused.cu): bf16, up to 128 columns.  Measured, backward
-// of 16,384 rows x 50,000 entries, without dz against with: 64 columns 527 against 950 us, 128 693 against 1013, 192 1336
+// of 16,384 rows x 50,000 entries, without dz against with: 64 columns 487 against 950 us, 128 604 against 1013, 192 1336
 // against 1067; of 2048 x 100,003: 156 / 263, 203 / 281, 361 / 295.
 struct FusedParams {
   int32_t* status;

@@ -19,6 +19,10 @@
 // One warp issues the products of S, as far ahead as there is room, another those
 // of the sums as their dz comes, so neither waits for what the other waits for; teams of four warps take the
 // tiles in turn, so that one's loads and waits overlap the others' arithmetic.
+//
+// Bound: by the latency from S to dz to the sum, three tiles of it under way, which tensor memory and shared memory have room
+// for (16,384 rows x 98,001 x 64: statistics 295 us, dx 410, dW 425, about 1200 clocks a tile against 512 of exponentials and
+// 690 of products).
 #include "mt_tiles.cuh"
 #include "mt_vocab.cuh"
 #include "mt_vocab_rows.cuh"

@@ -11,6 +11,10 @@
 //  their gradient   with the row's log sum known, dz = a p - b less the targets'
 //                   shares, rounded to bf16 (few rows: two bf16 parts, fp32 rows:
 //                   three), a piece of the vocabulary at a time.
+//
+// Bound: by the tensor cores from 512 columns on (7373 live rows x 100,003 x 512: statistics 400 to 450 us, 1.7 to 1.9
+// PFLOP/s; gradient 545, with 1.5 GB written), below by exponentials and their latency (32,769 live rows x 16,384 x 256:
+// 170 us, 1.6 PFLOP/s, and 244 us).
 #include <algorithm>
 
 #include "mt_tiles.cuh"
