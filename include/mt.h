@@ -444,8 +444,8 @@ typedef struct {
   const void* w;
 } mt_gated_linear;
 
-/* Workspace bytes of a call on these arguments (256-byte aligned; 0: none is
- * needed, or the arguments are refused).  The forward of bf16 rows and weights
+/* Workspace bytes of a call on these arguments on the current device (256-byte
+ * aligned; 0: none is needed, or the arguments are refused).  The forward of bf16 rows and weights
  * on 16 bytes with widths that are multiples of 8 needs none; others are copied
  * into a form that the tensor cores take. */
 size_t mt_gated_linear_workspace_bytes(const mt_gated_linear* cfg, int backward);
@@ -501,7 +501,9 @@ typedef struct {
   int32_t* status;
 } mt_vocab_loss;
 
-/* Workspace bytes of a call on these arguments (256-byte aligned; 0: refused). */
+/* Workspace bytes of a call on these arguments on the current device (256-byte
+ * aligned; 0: refused).  A backward of rows of more than 128 columns, or of
+ * fp32, holds up to 4 GiB of the logits' gradient at a time. */
 size_t mt_vocab_loss_workspace_bytes(const mt_vocab_loss* cfg, int backward);
 /* loss, lse: device fp32 [n], written. */
 int mt_vocab_loss_forward(const mt_vocab_loss* cfg, float* loss, float* lse, void* ws, size_t ws_bytes, mt_stream stream);
