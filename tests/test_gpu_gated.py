@@ -160,6 +160,19 @@ def test_strided_rows_and_outputs(dtype):
         assert (big_dx[:, :lo] == 7).all() and (big_dx[:, lo + k:] == 7).all()
 
 
+@pytest.mark.parametrize("dtype,k,m", [("bf16", 64, 128), ("bf16", 50, 33), ("f32", 64, 128)])
+def test_outputs_on_one_element(dtype, k, m):
+    """Outputs that start on one element only, with rows of several parts of dw."""
+    x, w, dh, off = make(14, [700, 0, 90], 2, 3, dtype, k, m)
+    lin, h, (dx, dw) = check_all(x, w, dh, off, dtype, "silu")
+    flat = [torch.full((t.numel() + 2,), 7.0, device=DEV, dtype=TORCH[dtype]) for t in (h, dx, dw)]
+    out = [f[1:-1].view(t.shape) for f, t in zip(flat, (h, dx, dw))]
+    assert torch.equal(lin.forward(x, w, off, out=out[0]), h)
+    got = lin.backward(dh, x, w, off, out_dx=out[1], out_dw=out[2])
+    assert torch.equal(got[0], dx) and torch.equal(got[1], dw)
+    assert all(float(f[0]) == 7 and float(f[-1]) == 7 for f in flat)
+
+
 def test_single_gradients_and_empty_batches():
     x, w, dh, off = make(7, [30, 50], 0, 0, "bf16", 64, 64)
     lin = mt.GatedLinear(2, 64, 64)

@@ -225,6 +225,23 @@ def test_strided_rows_and_outputs(dtype):
         assert (big_dx[:, :lo] == 7).all() and (big_dx[:, lo + 64:] == 7).all()
 
 
+@pytest.mark.parametrize("n,v,d,dtype", [(300, 600, 64, "bf16"), (300, 600, 200, "bf16"), (3000, 20000, 264, "bf16"), (300, 600, 72, "f32")])
+def test_unaligned_outputs_and_no_row(n, v, d, dtype):
+    """Gradients that start on one element only; then no row at all that takes part."""
+    s = make(15, n, v, d, dtype)
+    handle, r, (dx, dw) = check_all(s, dtype)
+    flat = [torch.full((k * d + 2,), 7.0, device=DEV, dtype=TORCH[dtype]) for k in (n, v)]
+    out = [f[1:-1].view(-1, d) for f in flat]
+    got = handle.backward(s["dloss"], s["x"], s["w"], s["targets"], r.lse, out_dx=out[0], out_dw=out[1])
+    assert torch.equal(got[0], dx) and torch.equal(got[1], dw)
+    none = torch.full_like(s["targets"], -1)
+    r = handle.forward(s["x"], s["w"], none)
+    assert not r.loss.any() and not r.lse.any()
+    got = handle.backward(s["dloss"], s["x"], s["w"], none, r.lse, out_dx=out[0], out_dw=out[1])
+    assert not got[0].any() and not got[1].any()
+    assert all(float(f[0]) == 7 and float(f[-1]) == 7 for f in flat) and handle.error() == 0
+
+
 def test_single_gradients_and_empty_batches():
     s = make(12, 60, 90, 64, "bf16")
     handle, r, (dx, dw) = check_all(s, "bf16")

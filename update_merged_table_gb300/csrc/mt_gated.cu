@@ -12,7 +12,7 @@
 // bytes written and read against 4 n in out operations.
 //
 // Bound: by the tensor cores where rows are long (40,009 rows on 32 uneven experts, 1024 -> 2048, backward's product 250 us:
-// 1.34 PFLOP/s; forward of 122,880 x 1024 -> 512 1.73), else by the epilogue (122,880 x 256 -> 512 57 us: 1.12 PFLOP/s and 49%
+// 1.34 PFLOP/s; forward of 122,880 x 1024 -> 512 1.78), else by the epilogue (122,880 x 256 -> 512 59 us: 1.09 PFLOP/s and 48%
 // of the copy bandwidth; half of the rest is the stores, 3 to 8 us the gate).
 //
 // dt is rounded to bf16 (with bf16 rows) because the tensor cores take it so: each
@@ -49,6 +49,23 @@ __device__ __forceinline__ float gate_of(float u) {
   if constexpr (GATE == MT_GATE_SIGMOID) return sigmoid_of<T>(u);
   if constexpr (GATE == MT_GATE_SILU) return u * sigmoid_of<T>(u);
   return u * sigmoid_of<T>(kGelu * fmaf(kCube * u * u, u, u));
+}
+// The factors of two bf16 columns (one column at a time: forward of 122,880 x 512 -> 512 85 us, two 82.5).
+template <int GATE>
+__device__ __forceinline__ f32x2 gate_of2(f32x2 u) {
+  if constexpr (GATE == MT_GATE_LINEAR) return u;
+  constexpr float kLog2e = 1.4426950408889634f;
+  f32x2 t;
+  if constexpr (GATE == MT_GATE_GELU) t = mul2(u, fma2(mul2(u, u), both(-kLog2e * kGelu * kCube), both(-kLog2e * kGelu)));
+  else t = mul2(u, both(-kLog2e));
+  float2 e = upk(t), r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(e.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(e.y));
+  e = upk(add2(pk(e.x, e.y), both(1.0f)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+  if constexpr (GATE == MT_GATE_SIGMOID) return pk(r.x, r.y);
+  return mul2(u, pk(r.x, r.y));
 }
 template <typename T, int GATE>
 __device__ __forceinline__ float2 gate_grad(float u) {
@@ -232,6 +249,12 @@ struct Gated {
       constexpr int kWords = sizeof(T) == 2 ? 16 : 32;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
+        if constexpr (!BACKWARD && sizeof(T) == 2) {
+          const float2 h = upk(mul2(pk(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1])),
+                                    gate_of2<GATE>(pk(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1])))));
+          y[j] = bf16x2_of(h.x, h.y);
+          continue;
+        }
         float a[2], b[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -358,8 +381,10 @@ __global__ void __launch_bounds__(256, kFewBlocks) k_gated_few(const FewParams p
 // ---- host --------------------------------------------------------------------------------------
 
 // The forward of few rows goes to k_gated_few: up to kFewTc rows per group on average (bf16) or kFewParts (fp32, whose weights
-// would be copied first), as long as each warp that the SMs hold has no more than kFewTasks tasks.  (As for the grouped
-// products, whose rule has both sides' times.)
+// would be copied first), as long as each warp that the SMs hold has no more than kFewTasks tasks.  Measured
+// against the tiles: bf16, 512 -> 1024, 8 tokens on 8 experts 6.4 and 8.6 us, 16 on 8 7.6 and 8.5, 24 on 8 10.7 and 8.5, 64 on 32
+// (more tasks) 19.8 and 16.6; 1 token, 1024 -> 4096, 5.8 and 9.8; 16 on 8, 2048 -> 2048, 31.8 and 30.3.  fp32: 64 on 8, 512 ->
+// 1024, 25.3 and 39.0, 128 on 8 46.3 and 39.1.
 constexpr int kFewTc = 2, kFewParts = 8, kFewTasks = 6;
 bool few(const mt_gated_linear& c) {
   const long long tiles = (c.n + std::min<long long>(c.n, c.groups) * (kFewRows - 1)) / kFewRows;  // at most
