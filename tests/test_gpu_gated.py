@@ -169,7 +169,7 @@ def test_outputs_on_one_element(dtype, k, m):
     out = [f[1:-1].view(t.shape) for f, t in zip(flat, (h, dx, dw))]
     assert torch.equal(lin.forward(x, w, off, out=out[0]), h)
     got = lin.backward(dh, x, w, off, out_dx=out[1], out_dw=out[2])
-    assert torch.equal(got[0], dx) and torch.equal(got[1], dw)
+    check_all(x, w, dh, off, dtype, "silu", lin=lin, h=out[0], grads=got)  # (dx by the fp32 pipes: not the same bits)
     assert all(float(f[0]) == 7 and float(f[-1]) == 7 for f in flat)
 
 
