@@ -1,0 +1,19 @@
+"""The losses over a vocabulary where a call's shape or values leave the common path; tolerances as in test_gpu_loss."""
+import pytest
+import torch
+
+import update_merged_table_gb300 as mt
+from test_gpu_loss import DEV, check_all, given, make
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("n,v,d,top", [(100, 30000, 64, 0), (65, 40001, 16, 0), (128, 30000, 64, 3), (30000, 100, 64, 0), (25000, 128, 40, 0)])
+def test_sums_of_one_tile(n, v, d, top):
+    """Narrow rows whose gradients' sums have one tile of logits each and several to a block: teams without a tile in a sum."""
+    s = make(41, n, v, d, "bf16", top=top, masked=0.0)
+    handle, r, (dx, dw) = check_all(s, "bf16")
+    for _ in range(30):
+        ax, aw = handle.backward(s["dloss"], s["x"], s["w"], *given(s), r.lse)
+        assert torch.equal(ax, dx) and torch.equal(aw, dw)
+    assert handle.error() == 0

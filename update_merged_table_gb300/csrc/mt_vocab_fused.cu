@@ -416,13 +416,18 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         }
         if (!ok) break;
         n += x.t1 - x.t0;
+      }
+      // The unit's sum, by the first two teams: 32 columns at a time.  A third neither reads it nor waits for it: it has no tile
+      // in some units of one or two, acc_empty does not count it, so sums could be two phases ahead of a wait here, which a
+      // parity cannot tell from none.  Its next dz waits for what it needs: dx for S (free again once the sum has had the dz
+      // there), dW for dz_empty.
+      if (team >= 2) continue;
+      if (x.t0 < x.t1) {
         ok = __all_sync(kFull, tc::mbar_wait(&bar.acc_full, acc_phase));
         if (!ok) break;
         acc_phase ^= 1;
         tc::fence_after();
       }
-      // the unit's sum, by the first two teams: 32 columns at a time
-      if (team >= 2) continue;
       const int c0 = team * KS * 32;  // half of the columns each team
       const int rows = min(32, (VOCAB ? p.vocab : work.live) - (x.kept * kT + quad * 32));
       const long long r0 = x.kept * kT + quad * 32;
