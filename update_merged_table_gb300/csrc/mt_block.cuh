@@ -50,7 +50,7 @@ __device__ __forceinline__ void load_offsets(const long long* offsets, int G, lo
     __syncthreads();
     return;
   }
-  for (int i = threadIdx.x; i <= G; i += blockDim.x) s_off[i] = __ldg(&offsets[i]);
+  for (int i = threadIdx.x; i <= G; i += blockDim.x) s_off[i] = offsets[i];
   __syncthreads();
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
@@ -426,7 +426,9 @@ class SmemLimit {
 
 // A kernel that starts while the one before it on the stream ends: its blocks set themselves up and then wait (follow()) until
 // that one is done and its writes are seen.  Every block calls follow() before it touches global memory, and lead() once it
-// runs, which lets the next kernel's blocks in.
+// runs, which lets the next kernel's blocks in.  It is resident while the one before it (the caller's, or another call's) still
+// writes, so it reads by ordinary loads: the read-only path is for memory that nothing writes during a kernel's whole life.
+// (k_vocab_rows may read its caller's rows so: k_vocab_mark before it waited for everything in front of the call.)
 __device__ __forceinline__ void follow() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void lead() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 template <typename... P, typename... A>

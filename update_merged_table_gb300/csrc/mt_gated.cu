@@ -177,7 +177,7 @@ struct Gated {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       dh[c] = make_uint4(0u, 0u, 0u, 0u);
-      if (r0 + lane < x.end && col + c * 8 < p.out_dim) dh[c] = __ldg(reinterpret_cast<const uint4*>(from) + c);
+      if (r0 + lane < x.end && col + c * 8 < p.out_dim) dh[c] = reinterpret_cast<const uint4*>(from)[c];
     }
   }
   __device__ __forceinline__ void ahead(const Unit& x, int ct) {

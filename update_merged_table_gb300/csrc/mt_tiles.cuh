@@ -469,7 +469,7 @@ __device__ __forceinline__ void load_rows(uint8_t* stage, int lane, float (&f)[3
 #pragma unroll
     for (int c = 0; c < 32 / kPer; ++c) {
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (lane < rows && col + c * kPer < J) v = __ldg(reinterpret_cast<const uint4*>(p) + c);
+      if (lane < rows && col + c * kPer < J) v = reinterpret_cast<const uint4*>(p)[c];
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {

@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(256) k_vocab_dx_sum(const float* part, size_t 
       if (at >= 0) {
 #pragma unroll 4
         for (int k = 0; k < runs; ++k) {
-          const float4 v = __ldg(reinterpret_cast<const float4*>(from + (size_t)k * stride * d));
+          const float4 v = *reinterpret_cast<const float4*>(from + (size_t)k * stride * d);
           s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
         }
       }
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(256) k_vocab_dw_sum(const float* part, size_t 
       float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
       for (int k = 0; k < runs; ++k) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(part + (size_t)k * stride * d) + i);
+        const float4 v = reinterpret_cast<const float4*>(part + (size_t)k * stride * d)[i];
         s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
       }
       if constexpr (sizeof(T) == 4) reinterpret_cast<float4*>(dw + first)[i] = s;

@@ -358,8 +358,8 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
       const FusedUnit x = work.unit(u);
       if (x.t0 < x.t1) {
         auto row_at = [&](int tile) { return tile * kT + quad * 32 + lane; };
-        auto id_at = [&](int row) { return p.rows.top == 1 && row < work.live ? __ldg(p.rows.ids + row) : 0x7FFFFFFF; };
-        auto coef_at = [&](int row) { return row < work.live ? __ldg(p.coef + row) : make_float4(0.0f, 0.0f, 0.0f, 0.0f); };
+        auto id_at = [&](int row) { return p.rows.top == 1 && row < work.live ? p.rows.ids[row] : 0x7FFFFFFF; };
+        auto coef_at = [&](int row) { return row < work.live ? p.coef[row] : make_float4(0.0f, 0.0f, 0.0f, 0.0f); };
         const int first = x.t0 + (team + R::kTeams - (int)(n % R::kTeams)) % R::kTeams;  // this team's first tile
         if (VOCAB) {
           k_next = coef_at(row_at(first));
