@@ -17,3 +17,15 @@ def test_sums_of_one_tile(n, v, d, top):
         ax, aw = handle.backward(s["dloss"], s["x"], s["w"], *given(s), r.lse)
         assert torch.equal(ax, dx) and torch.equal(aw, dw)
     assert handle.error() == 0
+
+
+@pytest.mark.parametrize("n,v,d", [(100, 700, 200), (2048, 20000, 256), (4096, 5000, 512), (2048, 20000, 640), (300, 2500, 1032)])
+@pytest.mark.parametrize("scale,smoothing,z_loss", [(1.5, 0.3, 1e-3), (0.5, 0.1, 0.0)])
+def test_smoothing_and_z_loss_of_wide_rows(n, v, d, scale, smoothing, z_loss):
+    """Tiles of 256 entries, by blocks and by pairs, whose rows of x stay with the block and whose do not."""
+    check_all(make(42, n, v, d, "bf16"), "bf16", scale, smoothing, z_loss)
+
+
+@pytest.mark.parametrize("n,v,d,top", [(2048, 20000, 256, 16), (2048, 20000, 640, 5), (100, 700, 200, 8)])
+def test_scale_of_distillation_over_wide_rows(n, v, d, top):
+    check_all(make(43, n, v, d, "bf16", top=top), "bf16", scale=0.5)
