@@ -29,3 +29,18 @@ def test_smoothing_and_z_loss_of_wide_rows(n, v, d, scale, smoothing, z_loss):
 @pytest.mark.parametrize("n,v,d,top", [(2048, 20000, 256, 16), (2048, 20000, 640, 5), (100, 700, 200, 8)])
 def test_scale_of_distillation_over_wide_rows(n, v, d, top):
     check_all(make(43, n, v, d, "bf16", top=top), "bf16", scale=0.5)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kept", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("scale", [0.5, 2.0, 3.0])
+def test_teachers_of_the_largest_and_lowest_logits(scale, kept, dtype):
+    """A kept logit of the type's lowest value (a mask of the teacher's) is a pair like others: equal ones share, and beside any
+    other it has nothing; times the scale it is no fp32 number."""
+    low = torch.finfo(kept).min
+    s = make(44, 6, 50, 32, dtype, top=4, masked=0.0)
+    s["ids"] = torch.tensor([[3, 9, 4, 7], [1, 2, 0, 4], [9, 9, 8, 7], [5, 6, -1, -1], [8, 0, 49, 8], [-1, 6, 6, -1]], dtype=torch.int32, device=DEV)
+    s["logits"] = torch.tensor([[low, low, low, low], [1.0, low, 2.0, low], [-low, low, 0.0, -low], [-low, -low, low, 0.0],
+                                [low, low / 2, low, low], [0.0, low, low, -low]], device=DEV).to(kept)
+    _, r, (dx, dw) = check_all(s, dtype, scale=scale)
+    assert bool(torch.isfinite(r.loss).all()) and bool(torch.isfinite(dx).all()) and bool(torch.isfinite(dw).all())

@@ -199,12 +199,13 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const VocabRows p) {
           const long long id = id_at(p, row * p.top + j);
           const bool there = pair_there(p, row * p.top + j, id);
           s_id[j] = there ? (int)id : 0x7FFFFFFF;
-          s_t[j] = there ? p.scale * teacher_at(p, row * p.top + j) : -INFINITY;
+          s_t[j] = there ? teacher_at(p, row * p.top + j) : -INFINITY;
           top = fmaxf(top, s_t[j]);
         }
         top = warp_max(top);
+        // (the differences are scaled, not the logits: a type's lowest or largest value times the scale may be no number)
         float sum = 0.0f;
-        for (int j = lane; j < p.top; j += 32) sum += expf(s_t[j] - top);
+        for (int j = lane; j < p.top; j += 32) sum += expf(p.scale * (s_t[j] - top));
         sum = warp_sum(sum);
         const float inv = 1.0f / sum, log_sum = logf(sum);
         float entropy = 0.0f;
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const VocabRows p) {
           const int id = s_id[j];
           int rank = 0;
           for (int i = 0; i < p.top; ++i) rank += s_id[i] < id || (s_id[i] == id && i < j);
-          const float d = s_t[j] - top, t = expf(d) * inv;
+          const float d = p.scale * (s_t[j] - top), t = expf(d) * inv;
           p.ids[at * p.top + rank] = id;
           p.share[at * p.top + rank] = t;
           if (t != 0.0f) entropy += t * (d - log_sum);
