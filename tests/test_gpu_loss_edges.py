@@ -44,3 +44,12 @@ def test_teachers_of_the_largest_and_lowest_logits(scale, kept, dtype):
                                 [low, low / 2, low, low], [0.0, low, low, -low]], device=DEV).to(kept)
     _, r, (dx, dw) = check_all(s, dtype, scale=scale)
     assert bool(torch.isfinite(r.loss).all()) and bool(torch.isfinite(dx).all()) and bool(torch.isfinite(dw).all())
+
+
+@pytest.mark.parametrize("n,top", [(2, 1024), (300, 1024), (40, 1023), (3, 513), (70, 129), (70, 128), (70, 127), (70, 65), (70, 64), (70, 63), (9, 33)])
+def test_long_lists_of_a_teacher(n, top):
+    """Lists sorted in every way there is; many of the same id, and ids in descending order."""
+    s = make(47, n, 200, 24, "f32", top=top, masked=0.1)
+    s["ids"][0] = torch.arange(top, 0, -1, device=DEV, dtype=torch.int32) % 200
+    s["ids"][-1] = 7
+    check_all(s, "f32")
