@@ -53,3 +53,29 @@ def test_long_lists_of_a_teacher(n, top):
     s["ids"][0] = torch.arange(top, 0, -1, device=DEV, dtype=torch.int32) % 200
     s["ids"][-1] = 7
     check_all(s, "f32")
+
+
+@pytest.mark.parametrize("n,top", [(2, 1024), (1, 1024), (16, 128), (15, 130), (64, 32), (33, 62), (255, 8), (256, 8), (257, 8), (1024, 2), (1025, 2)])
+def test_rows_marked_by_their_pairs(n, top):
+    """Up to 2048 pairs a block looks through all of them; rows whose only pair comes last, rows without any, and pairs outside
+    the vocabulary in rows that take part and in rows that do not."""
+    v, d = 700, 24
+    s = make(45, n, v, d, "f32", top=top, masked=0.0)
+    for i in range(0, n, 3):
+        s["ids"][i] = -1
+        if i % 2 == 0:
+            s["ids"][i, -1] = i % v
+    check_all(s, "f32")
+    handle = mt.Distillation(v, d, top, dtype="f32")
+    bad = s["ids"].clone()
+    bad[0], bad[-1, -1] = v, 2 ** 31 - 1
+    safe = torch.where(bad >= v, -1, bad)
+    r = handle.forward(s["x"], s["w"], bad, s["logits"])
+    assert handle.error(clear=True) == mt.MT_EINVAL
+    want = handle.forward(s["x"], s["w"], safe, s["logits"])
+    assert torch.equal(r.loss, want.loss) and torch.equal(r.lse, want.lse) and float(r.loss[0]) == 0 and handle.error() == 0
+
+
+@pytest.mark.parametrize("n", [2047, 2048, 2049])
+def test_rows_marked_by_their_targets(n):
+    check_all(make(46, n, 300, 24, "bf16", masked=0.5), "bf16")

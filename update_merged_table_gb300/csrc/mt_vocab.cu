@@ -59,10 +59,10 @@ __device__ __forceinline__ bool pair_there(const VocabRows& p, long long i, long
   return id >= 0 && id < p.vocab && (!p.distill || !(teacher_at(p, i) == -INFINITY));
 }
 
-// Whether a row takes part; what is outside the vocabulary is latched.
-__device__ __forceinline__ bool row_there(const VocabRows& p, long long row) {
+// Whether a row has a pair that is there among every step-th from `first` on; what is outside the vocabulary is latched.
+__device__ __forceinline__ bool row_there(const VocabRows& p, long long row, int first = 0, int step = 1) {
   bool there = false, bad = false;
-  for (int k = 0; k < p.top; ++k) {
+  for (int k = first; k < p.top; k += step) {
     const long long id = id_at(p, row * p.top + k);
     bad |= id >= p.vocab;
     there |= pair_there(p, row * p.top + k, id);
@@ -160,8 +160,12 @@ __device__ __forceinline__ void warp_sort(unsigned long long* s, int size, int l
   __syncwarp();
 }
 
-// MARK: few rows, which every block looks through itself (no k_vocab_mark before it).
-constexpr int kMarkPairs = 2048;  // targets, or pairs, of so few rows
+// MARK: few rows, of up to kMarkPairs targets or pairs, which every block looks through itself (no k_vocab_mark before it): a
+// thread to a row of up to kLanePairs, else eight lanes, or 32 from 65 on.  Forward in us, so, with k_vocab_mark, and by a
+// thread to any row: against 32,771 x 320, 37 rows of 8 pairs 16.9, 19.0 and 16.9, 200 of 9 24 (thread) or 27 (lanes) and 26,
+// 64 of 32 18.8, 20.4 and 28.3, 16 of 128 23.8, 25.0 and 38, 2 of 1024 56, 63 and 111; targets against 8192 x 64, 2048 17.6
+// and 16.2, 8192 46 and 31.
+constexpr int kMarkPairs = 2048, kLanePairs = 16;
 
 constexpr int kRowBlocks = 4;  // blocks to 32 rows: a warp has one row at most
 
@@ -174,15 +178,32 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const VocabRows p) {
   constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
   extern __shared__ uint8_t s_mem[];
   __shared__ int s_base;
+  __shared__ uint32_t s_mask[MARK ? kMarkPairs / (kLanePairs + 1) / 32 + 1 : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long words = (p.n + 31) / 32, all = words * kRowBlocks, per = (all + gridDim.x - 1) / gridDim.x;
   const long long q0 = blockIdx.x * per, q1 = min(q0 + per, all);  // a block's quarters lie one after the other
   if (q0 >= q1) return;
   // the live rows before the block's first word
   int before = 0;
+  const bool wide = MARK && p.top > kLanePairs;
   if (threadIdx.x == 0) s_base = 0;
+  if (wide) {
+    if (threadIdx.x < words) s_mask[threadIdx.x] = 0u;
+    __syncthreads();
+    const int rows = (int)min(p.n, ((q1 - 1) / kRowBlocks + 1) * 32);  // up to the block's last one
+    const int shift = p.top > 64 ? 5 : 3;
+    for (int r0 = 0; r0 < rows; r0 += 256 >> shift) {
+      const int row = r0 + ((int)threadIdx.x >> shift);
+      const bool there = row < rows && row_there(p, row, threadIdx.x & ((1 << shift) - 1), 1 << shift);
+      const unsigned bits = __reduce_or_sync(kFull, there ? 1u << (row & 31) : 0u);  // a warp's rows are of one word
+      if (lane == 0 && bits != 0u) atomicOr(&s_mask[row >> 5], bits);
+    }
+  }
   __syncthreads();
-  if constexpr (MARK) {
+  if (wide) {
+    for (long long i = threadIdx.x; i < q0 / kRowBlocks; i += blockDim.x) before += __popc(s_mask[i]);
+    __syncwarp();
+  } else if constexpr (MARK) {
     for (long long i = threadIdx.x; i < q0 / kRowBlocks * 32; i += blockDim.x) before += row_there(p, i);
     __syncwarp();
   } else {
@@ -196,7 +217,7 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const VocabRows p) {
     const long long w = q / kRowBlocks;
     const int share = (int)(q % kRowBlocks);
     uint32_t bits;
-    if constexpr (MARK) bits = __ballot_sync(kFull, w * 32 + lane < p.n && row_there(p, w * 32 + lane));
+    if constexpr (MARK) bits = wide ? s_mask[w] : __ballot_sync(kFull, w * 32 + lane < p.n && row_there(p, w * 32 + lane));
     else bits = p.mask[w];
     const int own = __popc(bits);
     if (share == 0 && threadIdx.x < 32 && w * 32 + lane < p.n)
