@@ -3,9 +3,14 @@
 ``CrossEntropy`` (softmax cross entropy) and ``Distillation`` (the divergence
 from a teacher that is known by its top logits) marshal their arguments to
 ``mt_vocab_loss_*`` of ``include/mt.h``.  The vocabulary is any row tensor: the
-items' weights, or the table's rows of some keys, whose gradient then goes to
-``Table.backward_adam``; targets index its rows, and a row whose target is
-negative (what a lookup's ``inverse`` has for an invalid ID) takes no part.
+items' weights, or the table's rows of distinct IDs, whose gradient then goes to
+``Table.backward_adam`` with that lookup; targets index its rows, and a row whose
+target is negative (what a lookup's ``inverse`` has for an invalid ID) takes no
+part.  IDs that come several times, such as a batch's items, are looked up without
+their rows first: that lookup's ``unique_keys[:U]`` (their low 56 bits) are the IDs
+of a second one whose ``rows`` are the vocabulary, and its ``inverse`` the targets.
+(``rows`` of the first would have one row a position, which ``inverse`` does not
+index.)
 
 The losses come per row, and so do their weights in the backward: ``dloss`` of
 1 / n makes a mean.  Between forward and backward nothing is kept but each row's
