@@ -1,4 +1,6 @@
 """The losses over a vocabulary where a call's shape or values leave the common path; tolerances as in test_gpu_loss."""
+import math
+
 import pytest
 import torch
 
@@ -79,3 +81,25 @@ def test_rows_marked_by_their_pairs(n, top):
 @pytest.mark.parametrize("n", [2047, 2048, 2049])
 def test_rows_marked_by_their_targets(n):
     check_all(make(46, n, 300, 24, "bf16", masked=0.5), "bf16")
+
+
+@pytest.mark.parametrize("n,v,d", [(152 * 128, 1 << 21, 16), (1 << 21, 152 * 128 + 5, 16), (152 * 128, 1 << 20, 128), (2176, 900_000, 2056),
+                                   (640, 2_700_000, 8192), (900_000, 2304, 2056), (1_500_000, 1024, 4096)])
+def test_sums_of_many_equal_terms(n, v, d):
+    """Over a million terms of one sign and size, whose every addition the tensor core cuts off: at most 2^-23 of the sum for 16
+    of them, so at most 2^-9 in the 2^18 after which a sum starts anew at the latest; then the gradient's own rounding."""
+    t, w0 = v // 3, 2.0 ** -math.ceil(math.log2(d))
+    x, w = torch.ones(n, d, device=DEV, dtype=torch.bfloat16), torch.full((v, d), w0, device=DEV, dtype=torch.bfloat16)
+    w[t] = 0.0
+    targets = torch.full((n,), t, device=DEV, dtype=torch.int32)
+    z = d * w0
+    lse = math.log((v - 1) * math.exp(z) + 1.0)
+    dz = 255.0 * 2.0 ** -30  # as bf16 has it
+    handle = mt.CrossEntropy(v, d)
+    dx, dw = handle.backward(torch.full((n,), dz / math.exp(z - lse), device=DEV), x, w, targets, torch.full((n,), lse, device=DEV))
+    tol = 2.0 ** -8 + 2.0 ** -9 + 1e-5
+    keep = torch.arange(v, device=DEV) != t
+    for got, want in ((dx, (v - 1) * dz * w0), (dw[keep], n * dz)):
+        least, most = float(got.min()) / want, float(got.max()) / want
+        assert 1.0 - tol <= least <= most <= 1.0 + tol
+    assert handle.error() == 0

@@ -22,7 +22,8 @@
 // is the value (24 bits in three times 8); a tile then sums the six products of
 // parts that reach 2^-24 of the whole, the small ones first, since the tensor
 // core cuts its accumulator off towards zero at every step and the error goes by
-// the accumulator's size (1.1e-9 of it per 16 products).
+// the accumulator's size (per 16 products 1.1e-9 of it on average over values of
+// either sign; up to 2^-23 where all have one sign and size).
 #pragma once
 
 #include "mt_block.cuh"

@@ -505,6 +505,7 @@ Layout layout_of(const mt_vocab_loss& c, bool backward) {
   l.entropy = take(c.top > 0 ? (size_t)c.n * 4 : 0);
   if (l.copy_w) l.w = take((size_t)c.vocab * l.parts * l.wp * 2);
   const int sms = std::max(1, sm_count());
+  const int64_t runs_v = tiles_of(c.vocab, kLongest), runs_n = tiles_of(c.n, kLongest);  // what the sums over them are cut into at least
   if (!backward) {
     l.max_chunks = (int)(16 * sms / (l.rows / 128) + 1);
     l.picked = take((size_t)c.n * l.top * 4);
@@ -515,10 +516,14 @@ Layout layout_of(const mt_vocab_loss& c, bool backward) {
     l.fused = true;
     const int64_t rt = tiles_of(c.n, kFusedTile), vt = tiles_of(c.vocab, kFusedTile);
     l.coef = take((size_t)c.n * 16);
-    l.runs_dx = (int)std::min<int64_t>(vt, rt < sms ? 8 * sms / rt + 1 : 4);
+    // (cut for kLongest: up to 32 runs within 256 MiB, so that their last round is a full one)
+    const auto cuts = [&](int64_t least, int64_t rows) {
+      return least > 1 ? std::max(least, std::min<int64_t>(32, (int64_t)((256 << 20) / ((size_t)rows * c.dim * 4)))) : 1;
+    };
+    l.runs_dx = (int)std::max(std::min<int64_t>(vt, rt < sms ? 8 * sms / rt + 1 : 4), cuts(runs_v, l.rows));
     l.dx = take((size_t)l.runs_dx * l.rows * c.dim * 4);
-    l.whole = (int)(vt / sms * sms);
-    l.runs_dw = vt > l.whole ? (int)std::min<int64_t>(rt, 8 * sms / (vt - l.whole) + 1) : 0;
+    l.whole = runs_n > 1 ? 0 : (int)(vt / sms * sms);
+    l.runs_dw = vt > l.whole ? (int)std::max(std::min<int64_t>(rt, 8 * sms / (vt - l.whole) + 1), cuts(runs_n, vt * kFusedTile)) : 0;
     l.dw = take((size_t)l.runs_dw * (vt - l.whole) * kFusedTile * c.dim * 4);
   } else {
     l.dz_parts = c.dtype == MT_F32 ? 3 : c.n <= kFewRowsTwice ? 2 : 1;
@@ -530,14 +535,20 @@ Layout layout_of(const mt_vocab_loss& c, bool backward) {
     l.dz = take((size_t)l.rows * l.dz_parts * l.piece * 2);
     const int bn = sum_width(c.dim, c.dtype == MT_F32);
     const int64_t ct = tiles_of(c.dim, bn);
-    // room for runs of the contraction: eight units a block, no run shorter than 8 steps, 256 MiB of dx
+    // room for runs of the contraction: eight units a block, no run shorter than 8 steps, 256 MiB of dx; and as many as kLongest
+    // asks for (a piece's rows times its entries are bounded, so these take 256 MiB for 8192 columns too)
     const int64_t rt = l.rows / 128;
     l.runs_dx = (int)std::max<int64_t>(1, std::min({8 * sms / (rt * ct) + 1, l.piece / 512, (int64_t)((256 << 20) / ((size_t)l.rows * c.dim * 4))}));
+    l.runs_dx = (int)std::max<int64_t>(l.runs_dx, tiles_of(l.piece, kLongest));
     l.dx = take((size_t)l.runs_dx * l.rows * c.dim * 4);
     // dW: only of the tiles behind the whole rounds, fewer than there are blocks
     const int64_t tail = std::min<int64_t>(l.piece / 128 * ct, sms + ct);
     l.runs_dw = (int)std::max<int64_t>(1, std::min<int64_t>(8 * sms / tail + 1, tiles_of(c.n, 512)));
     l.dw_rows = std::min<int64_t>(l.piece, tiles_of(tail, ct) * 256);
+    if (runs_n > 1) {  // all of the piece comes in runs
+      l.dw_rows = l.piece;
+      l.runs_dw = (int)std::max(runs_n, std::min<int64_t>(l.runs_dw, (int64_t)((256 << 20) / ((size_t)l.piece * c.dim * 4))));
+    }
     l.dw = take((size_t)l.runs_dw * l.dw_rows * c.dim * 4);
   }
   l.total = at;

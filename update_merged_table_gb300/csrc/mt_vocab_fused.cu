@@ -65,8 +65,9 @@ struct FusedRing {
 struct FusedUnit {
   int kept, t0, t1, slot;
 };
-// The kept tiles that make whole rounds of the blocks go over all streamed tiles; the rest are cut into `chunks` runs, so
-// that the last round is a full one too (766 kept tiles on 152 blocks: five rounds and a 25th, not six).
+// The kept tiles that make whole rounds of the blocks go over all streamed tiles (if they are no more than kLongest terms); the
+// rest are cut into `chunks` runs, so that the last round is a full one too (766 kept tiles on 152 blocks: five rounds and a
+// 25th, not six).
 struct FusedWork {
   int live, kept_tiles, streamed, whole, chunks;
   __device__ __forceinline__ int units() const { return whole + (kept_tiles - whole) * chunks; }
@@ -128,8 +129,9 @@ k_vocab_fused(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     const int rt = (work.live + kT - 1) / kT, vt = (p.vocab + kT - 1) / kT;
     work.kept_tiles = VOCAB ? vt : rt;
     work.streamed = VOCAB ? rt : vt;
-    work.whole = VOCAB ? p.whole : STATS ? 0 : work.kept_tiles / (int)gridDim.x * (int)gridDim.x;
-    work.chunks = choose_chunks(work.kept_tiles - work.whole, work.streamed, p.max_chunks, gridDim.x, 4);
+    const int least = STATS ? 1 : max(1, (work.streamed + kLongest / kT - 1) / (kLongest / kT));
+    work.whole = VOCAB ? p.whole : STATS || least > 1 ? 0 : work.kept_tiles / (int)gridDim.x * (int)gridDim.x;
+    work.chunks = choose_chunks(work.kept_tiles - work.whole, work.streamed, p.max_chunks, gridDim.x, 4, least);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
       p.cut[0] = STATS ? work.chunks : work.whole * kT;
       p.cut[1] = work.chunks;

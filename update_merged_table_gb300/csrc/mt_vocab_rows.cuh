@@ -16,13 +16,13 @@ __device__ __forceinline__ float exp2_of(float x) {
 __device__ __forceinline__ uint32_t below(int left) { return left >= 32 ? kFull : left <= 0 ? 0u : (1u << left) - 1u; }
 
 // Runs of column tiles for `rt` row tiles on `blocks` blocks (pairs): as many as end the last block soonest, a run's start
-// and end counted as `extra` half tiles.  Every thread calls it.
-__device__ __forceinline__ int choose_chunks(int rt, int tiles, int most, int blocks, int extra) {
+// and end counted as `extra` half tiles, and `least` at least.  Every thread calls it.
+__device__ __forceinline__ int choose_chunks(int rt, int tiles, int most, int blocks, int extra, int least = 1) {
   __shared__ unsigned long long s_best;
   if (threadIdx.x == 0) s_best = ~0ull;
   __syncthreads();
   unsigned long long best = ~0ull;
-  for (int c = threadIdx.x + 1; c <= max(1, min(most, tiles)); c += blockDim.x) {
+  for (int c = threadIdx.x + least; c <= max(least, min(most, tiles)); c += blockDim.x) {
     const long long rounds = ((long long)rt * c + blocks - 1) / blocks;
     const unsigned long long cost = (unsigned long long)rounds * (2 * ((tiles + c - 1) / c) + extra);
     best = min(best, cost << 32 | (unsigned)c);

@@ -40,9 +40,10 @@ struct Sum {
     steps = VOCAB ? (live + tiles::kBK - 1) / tiles::kBK : p.steps;
     rt = (rows + tiles::kBM * CG - 1) / (tiles::kBM * CG);
     const int blocks = gridDim.x / CG;
-    whole = rt * p.ctiles / blocks * blocks / p.ctiles;
+    const int least = max(1, ((VOCAB ? steps : p.usual) + kLongest / tiles::kBK - 1) / (kLongest / tiles::kBK));
+    whole = least > 1 ? 0 : rt * p.ctiles / blocks * blocks / p.ctiles;
     // (a partial product is written and read again, which takes about as long as 24 steps, or 4 of six products each)
-    runs = choose_chunks((rt - whole) * p.ctiles, VOCAB ? steps : p.usual, p.max_runs, blocks, FP32 ? 8 : 48);
+    runs = choose_chunks((rt - whole) * p.ctiles, VOCAB ? steps : p.usual, p.max_runs, blocks, FP32 ? 8 : 48, least);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
       p.cut[0] = whole * (tiles::kBM * CG);
       p.cut[1] = runs;
