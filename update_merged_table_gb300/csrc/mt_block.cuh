@@ -406,18 +406,25 @@ inline bool is_aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0
 
 // Lets a kernel have `most` bytes of dynamic shared memory, what its largest launch needs.  The limit belongs to the kernel
 // and the device, not to a launch: it is set once, to a constant, so that calls from several threads do not lower it for
-// one another.
+// one another.  registers: a kernel that the compiler gave fewer is refused (asked for once, too).
 class SmemLimit {
  public:
   template <typename Kernel>
-  cudaError_t allow(Kernel kernel, size_t most) {
+  cudaError_t allow(Kernel kernel, size_t most, int registers = 0) {
     const int dev = current_device();
     if (dev < 0) return cudaErrorInvalidDevice;
     if (set_[dev].load(std::memory_order_relaxed)) return cudaSuccess;
     const cudaError_t e =
         cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
-    if (e == cudaSuccess) set_[dev].store(true, std::memory_order_relaxed);
-    return e;
+    if (e != cudaSuccess) return e;
+    if (registers > 0) {
+      cudaFuncAttributes f;
+      const cudaError_t fe = cudaFuncGetAttributes(&f, reinterpret_cast<const void*>(kernel));
+      if (fe != cudaSuccess) return fe;
+      if (f.numRegs < registers) return cudaErrorInvalidValue;
+    }
+    set_[dev].store(true, std::memory_order_relaxed);
+    return cudaSuccess;
   }
 
  private:

@@ -536,14 +536,10 @@ cudaError_t launch(const char* name, const CUtensorMap& a, const CUtensorMap& b,
                    size_t extra, size_t most, cudaStream_t s) {
   constexpr size_t ring = 1024 + Ring<Op::kBN, CG, Op::kKeep, Op::kTri>::kTotal + kEpiWarps * Op::kStageOut;  // the stages start on 1024 bytes
   static SmemLimit limit;
-  const cudaError_t e = limit.allow(k_tiles<Op, CG>, ring + most);
+  // (a split of the registers needs the launch to bring them: a kernel that has one is compiled to the most that its launch
+  // bounds leave a thread)
+  const cudaError_t e = limit.allow(k_tiles<Op, CG>, ring + most, Op::kSplit ? kRegsLaunch : 0);
   if (e != cudaSuccess) return e;
-  if constexpr (Op::kSplit) {  // the split of the registers needs the launch to bring them
-    cudaFuncAttributes f;
-    const cudaError_t fe = cudaFuncGetAttributes(&f, reinterpret_cast<const void*>(k_tiles<Op, CG>));
-    if (fe != cudaSuccess) return fe;
-    if (f.numRegs < kRegsLaunch) return cudaErrorInvalidValue;
-  }
   const int blocks = sm_count() / CG;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((units < blocks ? (units > 0 ? units : 1) : blocks) * CG));
