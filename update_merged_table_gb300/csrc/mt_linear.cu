@@ -485,7 +485,7 @@ cudaError_t launch_linear_weights(LinearWeights& p, int dtype, cudaStream_t s) {
   p.tiles = tc ? cut.tiles : ((p.M + kTM - 1) / kTM) * ((p.K + kTN - 1) / kTN);
   p.units = tc ? cut.units : sm_count() * 4;
   if (p.n > 0 && tc) return launch_linear_weights_tc(p, cut, s);
-  if (p.dw16 != nullptr) return p.n > 0 ? cudaErrorInvalidValue : cudaSuccess;
+  if (p.dw16 != nullptr) return cudaErrorInvalidValue;  // (the gated part brings rows that fit, and at least one)
   if (p.n > 0) {
     const int grid = weights_blocks(p);
     MT_LAUNCH("k_linear_weights", s);
@@ -504,8 +504,7 @@ cudaError_t launch_linear_weights(LinearWeights& p, int dtype, cudaStream_t s) {
 }
 
 cudaError_t launch_linear_sums(const LinearWeights& p, cudaStream_t s) {
-  const size_t values = (size_t)p.groups * p.M * p.K;
-  if (p.n == 0) return p.dw16 != nullptr ? cudaMemsetAsync(p.dw16, 0, values * 2, s) : cudaMemsetAsync(p.dw, 0, values * 4, s);
+  if (p.n == 0) return cudaMemsetAsync(p.dw, 0, (size_t)p.groups * p.M * p.K * 4, s);
   MT_LAUNCH("k_linear_sums", s);
   const long long tasks = (long long)p.groups * sum_tasks((size_t)p.M * p.K);
   k_linear_sums<<<grid_for(tasks * 256, 256, 8), 256, weights_smem(p.groups) + (size_t)p.groups * 4, s>>>(p);

@@ -42,7 +42,7 @@ struct LinearWeights {
   int* chosen;      // [1] workspace: the rows of a chunk, as the products chose them, for their sums
   float* part;    // [slots][M][K]: partial products of the groups that have several chunks
   float* dw;      // [groups][M][K]
-  __nv_bfloat16* dw16;  // the same rounded to bf16 in its place (NULL: dw); tensor-core form only
+  __nv_bfloat16* dw16;  // the same rounded to bf16 in its place (NULL: dw); tensor-core form only, n > 0
 };
 
 // Dynamic shared memory for the offsets and what is derived from them.
