@@ -456,14 +456,18 @@ int mt_gated_linear_forward(const mt_gated_linear* cfg, void* h, int64_t ldh, vo
  *  dx  row tensor [n, in_dim], written, or NULL.
  *  dw  device [groups, 2 * out_dim, in_dim] of dtype, written (zeros for an
  *      empty group), or NULL.
- * With bf16 rows the gradients of y and u are rounded to bf16 on the way. */
+ * With bf16 rows the gradients of y and u are rounded to bf16 on the way, so a
+ * gradient's error is about 1.4 times that of its own rounding.  A bf16 dx of
+ * in_dim and out_dim that are multiples of 8 is made by the tensor cores where its
+ * rows all start on 16 bytes, like the other operands'; else by the fp32 pipes, at
+ * a fraction of the rate (as in mt_group_linear_backward). */
 int mt_gated_linear_backward(const mt_gated_linear* cfg, const void* dh, int64_t lddh, void* dx, int64_t lddx, void* dw,
                              void* ws, size_t ws_bytes, mt_stream stream);
 
 /* ---- losses over a vocabulary ------------------------------------------------- */
 
 /* Rows x_i [dim] against a vocabulary of rows w_v (items, or a table's rows of
- * some keys): logits z_iv = scale * (x_i . w_v), never kept in memory as a
+ * distinct keys): logits z_iv = scale * (x_i . w_v), never kept in memory as a
  * whole, and
  *   lse_i = log sum over v of exp z_iv.
  * Cross entropy (top = 0) with target t_i:
@@ -502,8 +506,9 @@ typedef struct {
 } mt_vocab_loss;
 
 /* Workspace bytes of a call on these arguments on the current device (256-byte
- * aligned; 0: refused).  A backward of rows of more than 128 columns, or of
- * fp32, holds up to 4 GiB of the logits' gradient at a time. */
+ * aligned; 0: refused).  A backward of rows of more than 128 columns, of fp32 or
+ * of at most 64 rows holds up to 4 GiB of the logits' gradient at a time, or what
+ * 256 entries of the vocabulary take: 512 bytes a row (fp32: 1536). */
 size_t mt_vocab_loss_workspace_bytes(const mt_vocab_loss* cfg, int backward);
 /* loss, lse: device fp32 [n], written. */
 int mt_vocab_loss_forward(const mt_vocab_loss* cfg, float* loss, float* lse, void* ws, size_t ws_bytes, mt_stream stream);
@@ -513,7 +518,11 @@ int mt_vocab_loss_forward(const mt_vocab_loss* cfg, float* loss, float* lse, voi
  *  dx     row tensor [n, dim], written, or NULL.
  *  dw     device [vocab, dim] of dtype, contiguous, written, or NULL.
  * The logits are computed again, a piece of the vocabulary at a time; with bf16
- * rows a piece's gradient is rounded to bf16 before it is multiplied. */
+ * rows a piece's gradient is rounded to bf16 before it is multiplied (n, rows that
+ * take no part included, of at most 64: to two bf16 parts, so that single terms
+ * keep about 16 bits).  A gradient of bf16 rows is then off by its own rounding and
+ * one like it, and by up to 2^-9 where hundreds of thousands of terms of one sign
+ * and size are added up. */
 int mt_vocab_loss_backward(const mt_vocab_loss* cfg, const float* dloss, const float* lse, void* dx, int64_t lddx, void* dw,
                            void* ws, size_t ws_bytes, mt_stream stream);
 

@@ -103,3 +103,20 @@ def test_sums_of_many_equal_terms(n, v, d):
         least, most = float(got.min()) / want, float(got.max()) / want
         assert 1.0 - tol <= least <= most <= 1.0 + tol
     assert handle.error() == 0
+
+
+@pytest.mark.parametrize("n,v,d", [(64, 5000, 40), (65, 5000, 40), (65, 5000, 256), (2000, 3000, 64), (2000, 3000, 256)])
+def test_padded_batches(n, v, d):
+    """Two rows that take part among many that do not: the gradient of their logits is rounded by what all rows are, and the
+    results stay within what that rounding allows."""
+    s = make(48, n, v, d, "bf16", masked=0.0)
+    keep = torch.zeros(n, dtype=torch.bool, device=DEV)
+    keep[[n // 3, n - 1]] = True
+    s["targets"][~keep] = -1
+    s["dloss"] = torch.full((n,), 0.5, device=DEV)
+    _, _, (dx, dw) = check_all(s, "bf16")
+    # without the padding: the same within both sides' rounding of the logits' gradient and of the result, 2^-8 each
+    few = {k: (t if k == "w" else t[keep]).contiguous() for k, t in s.items()}
+    _, _, (dx2, dw2) = check_all(few, "bf16")
+    for a, b in ((dx[keep], dx2), (dw, dw2)):
+        assert float((a.double() - b.double()).norm()) <= 4 * 2.0 ** -8 * float(b.double().norm())

@@ -6,10 +6,10 @@
 
 namespace mt {
 
-// x as three bf16 numbers whose sum is x: each takes the next eight bits, rounded to nearest, so the parts after it are at
-// most 2^-9 of it.  What three parts leave out is below 2^-26 of x (or below the least subnormal of bf16).  A value that
-// rounds to an infinity is cut off instead; an infinity or NaN is the first part alone, and becomes NaN in a product with
-// parts that are zero.
+// x as three bf16 numbers whose sum is x: each takes the next eight bits, rounded to nearest, so what it leaves is at most 2^-8
+// of it, and three times eight bits are all that x has (what is below the least subnormal of bf16 is lost).  The products of
+// parts that the six leave out are then at most 2 x 2^-25 + 2^-34 of the whole.  A value that rounds to an infinity is cut off
+// instead; an infinity or NaN is the first part alone, and becomes NaN in a product with parts that are zero.
 __device__ __forceinline__ void split3(float x, __nv_bfloat16& a, __nv_bfloat16& b, __nv_bfloat16& c) {
   a = __float2bfloat16_rn(x);
   if (__hisinf(a) && !isinf(x)) a = __float2bfloat16_rz(x);

@@ -25,7 +25,7 @@ struct LogitParams {
   LiveRows rows;
   int v0, columns;      // the piece: its first entry of the vocabulary, how many it has
   int kept;             // steps of x (of all parts) that a block keeps, 0: none
-  int tiles;            // of 128 columns (kept) or 256
+  int tiles;            // of 256 columns
   int max_chunks;       // runs of tiles that the statistics have room for
   float scale2;         // scale * log2(e)
   // statistics

@@ -15,7 +15,7 @@ index.)
 The losses come per row, and so do their weights in the backward: ``dloss`` of
 1 / n makes a mean.  Between forward and backward nothing is kept but each row's
 log sum (``lse``); a backward holds up to 4 GiB of the logits' gradient at a
-time.  Streams, graphs and errors as in ``block``: calls run on the current stream
+time (or 512 bytes a row, fp32 1536, where that is more).  Streams, graphs and errors as in ``block``: calls run on the current stream
 or on ``stream``, a captured call's workspace belongs to its graph, and targets
 outside the vocabulary are latched in the handle's status word (``error()``).
 """
