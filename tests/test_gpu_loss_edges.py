@@ -120,3 +120,61 @@ def test_padded_batches(n, v, d):
     _, _, (dx2, dw2) = check_all(few, "bf16")
     for a, b in ((dx[keep], dx2), (dw, dw2)):
         assert float((a.double() - b.double()).norm()) <= 4 * 2.0 ** -8 * float(b.double().norm())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,v,d,top", [(130, 600, 8192, 0), (300, 520, 8191, 3), (3, 1, 8192, 0), (5000, 1, 64, 0), (5000, 2, 1, 2), (40, 1, 24, 1024),
+                                       (1, 2, 8192, 1024), (1, 70001, 1, 0), (700_001, 3, 8, 0), (300_001, 50, 136, 0)])
+def test_smallest_and_largest_sizes(n, v, d, top, dtype):
+    check_all(make(49, n, v, d, dtype, top=top), dtype, scale=0.5 if top else 1.0)
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-6, 50.0])
+def test_small_and_large_scales(scale):
+    for dtype in ("bf16", "f32"):
+        check_all(make(50, 200, 300, 72, dtype), dtype, scale=scale, smoothing=0.1)
+        check_all(make(51, 200, 300, 72, dtype, top=5), dtype, scale=scale)
+
+
+def test_captured_calls_behind_a_join():
+    """Kernels that follow others by programmatic launches, captured right behind events of other streams, copies and fills."""
+    s = make(52, 600, 4000, 200, "bf16")
+    t = make(53, 300, 2000, 64, "bf16", top=7)
+    ce, kd = mt.CrossEntropy(4000, 200), mt.Distillation(2000, 64, 7)
+    ffn = mt.GatedLinear(2, 200, 64)
+    gen = torch.Generator(device=DEV).manual_seed(54)
+    w1 = (torch.randn(2, 128, 200, generator=gen, device=DEV) * 0.1).bfloat16()
+    off = torch.tensor([0, 100, 600], device=DEV)
+    x, x2 = s["x"].clone(), t["x"].clone()
+
+    def step(side):
+        main = torch.cuda.current_stream()
+        x.copy_(s["x"])
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            x2.copy_(t["x"])
+            k = kd.forward(x2, t["w"], t["ids"], t["logits"])
+            gk = kd.backward(t["dloss"], x2, t["w"], t["ids"], t["logits"], k.lse)
+        r = ce.forward(x, s["w"], s["targets"])
+        gr = ce.backward(s["dloss"], x, s["w"], s["targets"], r.lse)
+        main.wait_stream(side)
+        h = ffn.forward(gr[0], w1, off)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            back = ffn.backward(h, gr[0], w1, off)
+        main.wait_stream(side)
+        return (r.loss, *gr, k.loss, *gk, h, *back)
+
+    side = torch.cuda.Stream()
+    want = [a.clone() for a in step(side)]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step(torch.cuda.Stream())
+    for _ in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        for a in got:
+            a.zero_()
+    assert not ce.error() and not kd.error() and not ffn.error()
