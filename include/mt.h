@@ -457,10 +457,7 @@ int mt_gated_linear_forward(const mt_gated_linear* cfg, void* h, int64_t ldh, vo
  *  dw  device [groups, 2 * out_dim, in_dim] of dtype, written (zeros for an
  *      empty group), or NULL.
  * With bf16 rows the gradients of y and u are rounded to bf16 on the way, so a
- * gradient's error is about 1.4 times that of its own rounding.  A bf16 dx of
- * in_dim and out_dim that are multiples of 8 is made by the tensor cores where its
- * rows all start on 16 bytes, like the other operands'; else by the fp32 pipes, at
- * a fraction of the rate (as in mt_group_linear_backward). */
+ * gradient's error is about 1.4 times that of its own rounding. */
 int mt_gated_linear_backward(const mt_gated_linear* cfg, const void* dh, int64_t lddh, void* dx, int64_t lddx, void* dw,
                              void* ws, size_t ws_bytes, mt_stream stream);
 

@@ -294,7 +294,7 @@ class GatedLinear(_Handle):
     def backward(self, dh, x, weight, offsets, want_dx: bool = True, want_dw: bool = True, out_dx=None, out_dw=None,
                  stream=None):
         """(dx [n, in_dim], dw [num_groups, 2 * out_dim, in_dim]), both in the handle's dtype, of dh [n, out_dim] and the
-        forward's input x.  An out_dx whose bf16 rows do not all start on 16 bytes takes the fp32 pipes: slow."""
+        forward's input x."""
         if not want_dx and not want_dw:
             raise ValueError("nothing to compute")
         args = (*self._cfg, dh, x, weight, offsets, out_dx, out_dw, int(want_dx), int(want_dw))

@@ -22,6 +22,7 @@ struct LinearRows {
   void* c;
   long long ldc;
   int I, J, jtiles;
+  bool any_c;  // the tensor cores also where rows of c do not start on 16 bytes (the gated part's dx)
 };
 
 // dW[g][m][k] = sum over the rows r of group g of dy[r][m] * x[r][k].

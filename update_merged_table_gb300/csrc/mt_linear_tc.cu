@@ -166,7 +166,8 @@ __device__ __forceinline__ void tc_end(uint32_t tmem) {
 // CG = 2: a pair of blocks takes 256 rows, each its 128 and half of the tile's columns of W: a block then writes and
 // reads 64 KB of shared memory per stage instead of 96, which at 128 bytes a clock is what the tensor core's 512 clocks
 // allow (one block alone is bound by its shared memory: 768 clocks).
-template <int BN, bool B_MN, int CG>
+// ANY_C: rows of C on any element, stored by elements.
+template <int BN, bool B_MN, int CG, bool ANY_C>
 __global__ void __launch_bounds__(kWarpsTC * 32, 1)
 k_linear_rows_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w, const LinearRows p) {
   using R = Ring<BN, CG>;
@@ -313,13 +314,24 @@ k_linear_rows_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constan
           *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = o;
         }
         __syncwarp();
-        const int col = j0 + c0 + (lane & 7) * 8;
+        if constexpr (ANY_C) {
+#pragma unroll 4
+          for (int r = 0; r < rows && r < 32; ++r) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const int r = q * 4 + (lane >> 3);
-          if (r < rows && col < p.J)
-            *reinterpret_cast<uint4*>(C + (r0 + r) * p.ldc + col) =
-                *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+            for (int j = lane; j < 64; j += 32)
+              if (j0 + c0 + j < p.J)
+                C[(r0 + r) * p.ldc + j0 + c0 + j] =
+                    *reinterpret_cast<const __nv_bfloat16*>(stage + r * 128 + (((j >> 3) ^ (r & 7)) << 4) + (j & 7) * 2);
+          }
+        } else {
+          const int col = j0 + c0 + (lane & 7) * 8;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const int r = q * 4 + (lane >> 3);
+            if (r < rows && col < p.J)
+              *reinterpret_cast<uint4*>(C + (r0 + r) * p.ldc + col) =
+                  *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+          }
         }
         __syncwarp();
       }
@@ -705,16 +717,16 @@ cudaError_t launch_tc(Kernel kernel, int grid, int threads, size_t smem, int pai
 
 int tc_grid(long long tiles, int pair) { return (int)std::min<long long>(tiles, sm_count() / pair) * pair; }
 
-template <int BN, bool B_MN, int CG>
+template <int BN, bool B_MN, int CG, bool ANY_C = false>
 cudaError_t rows_tc(const CUtensorMap& a, const CUtensorMap& w, LinearRows p, cudaStream_t s) {
   p.jtiles = (p.J + BN - 1) / BN;
   const long long tiles = (p.n / (kBM * CG) + p.groups) * p.jtiles;
   constexpr size_t ring = 1024 + Ring<BN, CG>::kBytes;  // the stages start on 1024 bytes
   static SmemLimit limit;
-  const cudaError_t e = limit.allow(k_linear_rows_tc<BN, B_MN, CG>, ring + rows_smem(MT_MAX_GROUPS));
+  const cudaError_t e = limit.allow(k_linear_rows_tc<BN, B_MN, CG, ANY_C>, ring + rows_smem(MT_MAX_GROUPS));
   if (e != cudaSuccess) return e;
   MT_LAUNCH("k_linear_rows_tc", s);
-  return launch_tc(k_linear_rows_tc<BN, B_MN, CG>, tc_grid(tiles, CG), kWarpsTC * 32, ring + rows_smem(p.groups), CG, s, a, w, p);
+  return launch_tc(k_linear_rows_tc<BN, B_MN, CG, ANY_C>, tc_grid(tiles, CG), kWarpsTC * 32, ring + rows_smem(p.groups), CG, s, a, w, p);
 }
 
 template <int BN, bool X8, int CG>
@@ -744,9 +756,12 @@ cudaError_t weights_tc(const CUtensorMap& x, const CUtensorMap& dy, const Linear
 
 }  // namespace
 
+namespace {
+bool wide_c(const LinearRows& p) { return p.ldc % 8 == 0 && is_aligned(p.c, 16); }
+}  // namespace
+
 bool linear_rows_fits_tc(const LinearRows& p) {
-  return p.I % 8 == 0 && p.J % 8 == 0 && p.lda % 8 == 0 && p.ldc % 8 == 0 && is_aligned(p.a, 16) && is_aligned(p.c, 16) &&
-         is_aligned(p.w, 16);
+  return p.I % 8 == 0 && p.J % 8 == 0 && p.lda % 8 == 0 && (p.any_c || wide_c(p)) && is_aligned(p.a, 16) && is_aligned(p.w, 16);
 }
 
 // Pairs where the product is bound by its arithmetic, and tiles of 256 rows neither waste rows nor leave SMs without work.
@@ -763,6 +778,10 @@ cudaError_t launch_linear_rows_tc(const LinearRows& p, cudaStream_t s) {
   if (b_mn ? !tc::encode_bf16(&w, 3, p.w, p.J, p.I, p.J, p.groups, (uint64_t)p.I * p.J, 64, kBK)
            : !tc::encode_bf16(&w, 3, p.w, p.I, p.J, p.I, p.groups, (uint64_t)p.I * p.J, kBK, pair ? 128 : bn))
     return cudaErrorInvalidValue;
+  if (!wide_c(p)) {  // (dx)
+    if (!b_mn) return cudaErrorInvalidValue;
+    return pair ? rows_tc<256, true, 2, true>(a, w, p, s) : rows_tc<256, true, 1, true>(a, w, p, s);
+  }
   if (pair) return b_mn ? rows_tc<256, true, 2>(a, w, p, s) : rows_tc<256, false, 2>(a, w, p, s);
   if (b_mn)
     return bn == 256 ? rows_tc<256, true, 1>(a, w, p, s) : bn == 128 ? rows_tc<128, true, 1>(a, w, p, s) : rows_tc<64, true, 1>(a, w, p, s);
