@@ -78,7 +78,7 @@ def test_rows_marked_by_their_pairs(n, top):
     assert torch.equal(r.loss, want.loss) and torch.equal(r.lse, want.lse) and float(r.loss[0]) == 0 and handle.error() == 0
 
 
-@pytest.mark.parametrize("n", [2047, 2048, 2049])
+@pytest.mark.parametrize("n", [1023, 1024, 1025, 2047, 2048, 2049])
 def test_rows_marked_by_their_targets(n):
     check_all(make(46, n, 300, 24, "bf16", masked=0.5), "bf16")
 

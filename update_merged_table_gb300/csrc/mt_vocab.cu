@@ -160,12 +160,12 @@ __device__ __forceinline__ void warp_sort(unsigned long long* s, int size, int l
   __syncwarp();
 }
 
-// MARK: few rows, of up to kMarkPairs targets or pairs, which every block looks through itself (no k_vocab_mark before it): a
+// MARK: few rows, up to kMarkRows of up to kMarkPairs targets or pairs in all, which every block looks through itself (no k_vocab_mark before it): a
 // thread to a row of up to kLanePairs, else eight lanes, or 32 from 65 on.  Forward in us, so, with k_vocab_mark, and by a
 // thread to any row: against 32,771 x 320, 37 rows of 8 pairs 16.9, 19.0 and 16.9, 200 of 9 24 (thread) or 27 (lanes) and 26,
-// 64 of 32 18.8, 20.4 and 28.3, 16 of 128 23.8, 25.0 and 38, 2 of 1024 56, 63 and 111; targets against 8192 x 64, 2048 17.6
-// and 16.2, 8192 46 and 31.
-constexpr int kMarkPairs = 2048, kLanePairs = 16;
+// 64 of 32 18.8, 20.4 and 28.3, 16 of 128 23.8, 25.0 and 38, 2 of 1024 56, 63 and 111; against 8192 x 64, 256 targets 13.1 and
+// 13.7, 1024 15.4 and 15.2, 2048 17.6 and 16.2, 1024 rows of 2 pairs 18.3 and 19.2.
+constexpr int kMarkRows = 1024, kMarkPairs = 2048, kLanePairs = 16;
 
 constexpr int kRowBlocks = 4;  // blocks to 32 rows: a warp has one row at most
 
@@ -610,7 +610,7 @@ cudaError_t launch_rows(const mt_vocab_loss& c, const Layout& l, char* ws, const
   r.dloss = dloss;
   r.lse = lse;
   r.coef = dloss != nullptr ? reinterpret_cast<float4*>(ws + l.coef) : nullptr;
-  const bool mark = c.n * l.top <= kMarkPairs;
+  const bool mark = c.n <= kMarkRows && c.n * l.top <= kMarkPairs;
   cudaError_t e = cudaSuccess;
   if (!mark) {
     MT_LAUNCH("k_vocab_mark", s);
