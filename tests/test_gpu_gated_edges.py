@@ -23,3 +23,28 @@ def test_dx_on_any_element(sizes, k, m):
         assert torch.equal(got, dx) and (big[:, :lo] == 7).all() and (big[:, lo + k:] == 7).all()
         big.fill_(7.0)
     assert lin.error() == 0
+
+
+@pytest.mark.parametrize("dtype,k,m", [("bf16", 72, 136), ("f32", 40, 48)])
+def test_as_many_groups_as_there_may_be(dtype, k, m):
+    """1024 groups, most of them of a few rows or of none, one long."""
+    sizes = [(i * 7919) % 5 for i in range(1024)]
+    sizes[77] = 700
+    x, w, dh, off = make(22, sizes, 1, 2, dtype, k, m)
+    check_all(x, w, dh, off, dtype, "gelu")
+
+
+@pytest.mark.slow
+def test_offsets_past_32_bits():
+    """Rows of every operand more than 2^31 elements apart from their first."""
+    n, k, m, ld = 70000, 64, 96, 40000
+    x, w, dh, off = make(23, [1000, n - 1003], 1, 2, "bf16", k, m)
+    lin, h, (dx, dw) = check_all(x, w, dh, off, "bf16", "silu")
+    big = torch.empty(n, ld, device=DEV, dtype=torch.bfloat16)
+    part = [big[:, 1024 * i:1024 * i + c] for i, c in enumerate((k, m, m, k))]
+    part[0].copy_(x), part[1].copy_(dh)
+    assert torch.equal(lin.forward(part[0], w, off, out=part[2]), h)
+    got = lin.backward(part[1], part[0], w, off, out_dx=part[3])
+    assert torch.equal(got[0], dx) and torch.equal(got[1], dw)
+    odd = big[:, 20001:20001 + k]  # rows on one element
+    assert torch.equal(lin.backward(part[1], part[0], w, off, want_dw=False, out_dx=odd)[0], dx)

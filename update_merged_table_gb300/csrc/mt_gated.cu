@@ -384,7 +384,8 @@ __global__ void __launch_bounds__(256, kFewBlocks) k_gated_few(const FewParams p
 // would be copied first), as long as each warp that the SMs hold has no more than kFewTasks tasks.  Measured
 // against the tiles: bf16, 512 -> 1024, 8 tokens on 8 experts 6.4 and 8.6 us, 16 on 8 7.6 and 8.5, 24 on 8 10.7 and 8.5, 64 on 32
 // (more tasks) 19.8 and 16.6; 1 token, 1024 -> 4096, 5.8 and 9.8; 16 on 8, 2048 -> 2048, 31.8 and 30.3.  fp32: 64 on 8, 512 ->
-// 1024, 25.3 and 39.0, 128 on 8 46.3 and 39.1.
+// 1024, 25.3 and 39.0, 128 on 8 46.3 and 39.1 (each further pair of a group's rows reads its weights again: 64 rows on 8 experts
+// 134 MB, from L2 at 5 TB/s, where the weights once are 5 us of HBM).
 constexpr int kFewTc = 2, kFewParts = 8, kFewTasks = 6;
 bool few(const mt_gated_linear& c) {
   const long long tiles = (c.n + std::min<long long>(c.n, c.groups) * (kFewRows - 1)) / kFewRows;  // at most
