@@ -27,7 +27,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct VocabRows {
   long long n;
   int vocab, dim, top;  // top: entries of a row's list (1: cross entropy)
-  bool distill, wide_ids, teacher16;
+  bool wide_ids, teacher16;
   const void* targets;
   const void* teacher;
   int32_t* status;
@@ -55,54 +55,58 @@ __device__ __forceinline__ long long id_at(const VocabRows& p, long long i) {
 __device__ __forceinline__ float teacher_at(const VocabRows& p, long long i) {
   return p.teacher16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.teacher)[i]) : static_cast<const float*>(p.teacher)[i];
 }
+template <bool DISTILL>
 __device__ __forceinline__ bool pair_there(const VocabRows& p, long long i, long long id) {
-  return id >= 0 && id < p.vocab && (!p.distill || !(teacher_at(p, i) == -INFINITY));
+  return id >= 0 && id < p.vocab && (!DISTILL || !(teacher_at(p, i) == -INFINITY));
 }
 
 // Whether a row has a pair that is there among every step-th from `first` on; what is outside the vocabulary is latched.
+template <bool DISTILL>
 __device__ __forceinline__ bool row_there(const VocabRows& p, long long row, int first = 0, int step = 1) {
+  const int top = DISTILL ? p.top : 1;
   bool there = false, bad = false;
-  for (int k = first; k < p.top; k += step) {
-    const long long id = id_at(p, row * p.top + k);
+  for (int k = first; k < top; k += step) {
+    const long long id = id_at(p, row * top + k);
     bad |= id >= p.vocab;
-    there |= pair_there(p, row * p.top + k, id);
+    there |= pair_there<DISTILL>(p, row * top + k, id);
   }
   if (bad && p.status != nullptr) atomicCAS(p.status, 0, MT_EINVAL);
   return there;
 }
 
 // A block per 32 rows: a thread per row where it has one target, else a warp.
+template <bool DISTILL>
 __global__ void __launch_bounds__(256) k_vocab_mark(const VocabRows p) {
   lead();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long words = (p.n + 31) / 32;
-  if (!p.distill) {
+  if constexpr (!DISTILL) {
     for (long long w = (long long)blockIdx.x * 8 + warp; w < words; w += (long long)gridDim.x * 8) {
-      const unsigned bits = __ballot_sync(kFull, w * 32 + lane < p.n && row_there(p, w * 32 + lane));
+      const unsigned bits = __ballot_sync(kFull, w * 32 + lane < p.n && row_there<false>(p, w * 32 + lane));
       if (lane == 0) p.mask[w] = bits;
     }
-    return;
-  }
-  __shared__ uint32_t s_bits;
-  for (long long w = blockIdx.x; w < words; w += gridDim.x) {
-    if (threadIdx.x == 0) s_bits = 0u;
-    __syncthreads();
-    for (int r = warp; r < 32; r += 8) {
-      const long long row = w * 32 + r;
-      bool there = false, bad = false;
-      if (row < p.n) {
-        for (int k = lane; k < p.top; k += 32) {
-          const long long id = id_at(p, row * p.top + k);
-          bad |= id >= p.vocab;
-          there |= pair_there(p, row * p.top + k, id);
+  } else {
+    __shared__ uint32_t s_bits;
+    for (long long w = blockIdx.x; w < words; w += gridDim.x) {
+      if (threadIdx.x == 0) s_bits = 0u;
+      __syncthreads();
+      for (int r = warp; r < 32; r += 8) {
+        const long long row = w * 32 + r;
+        bool there = false, bad = false;
+        if (row < p.n) {
+          for (int k = lane; k < p.top; k += 32) {
+            const long long id = id_at(p, row * p.top + k);
+            bad |= id >= p.vocab;
+            there |= pair_there<true>(p, row * p.top + k, id);
+          }
         }
+        if (bad && p.status != nullptr) atomicCAS(p.status, 0, MT_EINVAL);
+        if (__any_sync(kFull, there) && lane == 0) atomicOr(&s_bits, 1u << r);
       }
-      if (bad && p.status != nullptr) atomicCAS(p.status, 0, MT_EINVAL);
-      if (__any_sync(kFull, there) && lane == 0) atomicOr(&s_bits, 1u << r);
+      __syncthreads();
+      if (threadIdx.x == 0) p.mask[w] = s_bits;
+      __syncthreads();
     }
-    __syncthreads();
-    if (threadIdx.x == 0) p.mask[w] = s_bits;
-    __syncthreads();
   }
 }
 
@@ -171,21 +175,21 @@ constexpr int kRowBlocks = 4;  // blocks to 32 rows: a warp has one row at most
 
 // A quarter of 32 rows' live ones per block, a warp each; the last block writes how many there are and puts zeros behind them up to the
 // next 128 rows (steps of dW's contraction).  T: the rows' type; AL: they can be read in 16-byte vectors.
-template <typename T, bool AL, bool MARK>
+template <typename T, bool AL, bool MARK, bool DISTILL>
 __global__ void __launch_bounds__(256) k_vocab_rows(const VocabRows p) {
   lead();
   if (!MARK) follow();
   constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
   extern __shared__ uint8_t s_mem[];
   __shared__ int s_base;
-  __shared__ uint32_t s_mask[MARK ? kMarkPairs / (kLanePairs + 1) / 32 + 1 : 1];
+  __shared__ uint32_t s_mask[MARK && DISTILL ? kMarkPairs / (kLanePairs + 1) / 32 + 1 : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long words = (p.n + 31) / 32, all = words * kRowBlocks, per = (all + gridDim.x - 1) / gridDim.x;
   const long long q0 = blockIdx.x * per, q1 = min(q0 + per, all);  // a block's quarters lie one after the other
   if (q0 >= q1) return;
   // the live rows before the block's first word
   int before = 0;
-  const bool wide = MARK && p.top > kLanePairs;
+  const bool wide = MARK && DISTILL && p.top > kLanePairs;
   if (threadIdx.x == 0) s_base = 0;
   if (wide) {
     if (threadIdx.x < words) s_mask[threadIdx.x] = 0u;
@@ -194,7 +198,7 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const VocabRows p) {
     const int shift = p.top > 64 ? 5 : 3;
     for (int r0 = 0; r0 < rows; r0 += 256 >> shift) {
       const int row = r0 + ((int)threadIdx.x >> shift);
-      const bool there = row < rows && row_there(p, row, threadIdx.x & ((1 << shift) - 1), 1 << shift);
+      const bool there = row < rows && row_there<DISTILL>(p, row, threadIdx.x & ((1 << shift) - 1), 1 << shift);
       const unsigned bits = __reduce_or_sync(kFull, there ? 1u << (row & 31) : 0u);  // a warp's rows are of one word
       if (lane == 0 && bits != 0u) atomicOr(&s_mask[row >> 5], bits);
     }
@@ -204,7 +208,7 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const VocabRows p) {
     for (long long i = threadIdx.x; i < q0 / kRowBlocks; i += blockDim.x) before += __popc(s_mask[i]);
     __syncwarp();
   } else if constexpr (MARK) {
-    for (long long i = threadIdx.x; i < q0 / kRowBlocks * 32; i += blockDim.x) before += row_there(p, i);
+    for (long long i = threadIdx.x; i < q0 / kRowBlocks * 32; i += blockDim.x) before += row_there<DISTILL>(p, i);
     __syncwarp();
   } else {
     for (long long i = threadIdx.x; i < q0 / kRowBlocks; i += blockDim.x) before += __popc(p.mask[i]);
@@ -217,7 +221,7 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const VocabRows p) {
     const long long w = q / kRowBlocks;
     const int share = (int)(q % kRowBlocks);
     uint32_t bits;
-    if constexpr (MARK) bits = wide ? s_mask[w] : __ballot_sync(kFull, w * 32 + lane < p.n && row_there(p, w * 32 + lane));
+    if constexpr (MARK) bits = wide ? s_mask[w] : __ballot_sync(kFull, w * 32 + lane < p.n && row_there<DISTILL>(p, w * 32 + lane));
     else bits = p.mask[w];
     const int own = __popc(bits);
     if (share == 0 && threadIdx.x < 32 && w * 32 + lane < p.n)
@@ -249,7 +253,7 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const VocabRows p) {
         }
       }
       // its targets and their shares
-      if (!p.distill) {
+      if constexpr (!DISTILL) {
         if (lane == 0) {
           p.ids[at] = (int)id_at(p, row);
           p.share[at] = 1.0f - p.smoothing;
@@ -262,7 +266,7 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const VocabRows p) {
         float top = -INFINITY;
         for (int j = lane; j < p.top; j += 32) {
           const long long id = id_at(p, row * p.top + j);
-          const bool there = pair_there(p, row * p.top + j, id);
+          const bool there = pair_there<true>(p, row * p.top + j, id);
           s_key[j] = (unsigned long long)(there ? (unsigned)id : 0x7FFFFFFFu) << 32 | (unsigned)j;
           s_t[j] = there ? teacher_at(p, row * p.top + j) : -INFINITY;
           top = fmaxf(top, s_t[j]);
@@ -376,6 +380,25 @@ __global__ void __launch_bounds__(256) k_vocab_loss(const VocabLoss p) {
   }
 }
 
+// The sum of `runs` values `step` apart, in their order, four loads under way.  The kernel before wrote them, so they come from
+// L2 (ordinary loads, whichever way they were grouped: backward of 64 rows x 100,003 x 256, dx alone, 94 to 102 us, so 87).
+__device__ __forceinline__ float4 sum_runs(const float4* from, size_t step, int runs) {
+  constexpr int kOnce = 4;
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  auto add = [&](const float4& v) { s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w); };
+  int k = 0;
+  for (; k + kOnce <= runs; k += kOnce, from += kOnce * step) {
+    float4 v[kOnce];
+#pragma unroll
+    for (int q = 0; q < kOnce; ++q) v[q] = __ldcg(from + q * step);
+#pragma unroll
+    for (int q = 0; q < kOnce; ++q) add(v[q]);
+  }
+#pragma unroll 1
+  for (; k < runs; ++k, from += step) add(__ldcg(from));
+  return s;
+}
+
 // dx in its rows' places; zeros for rows that take no part.  The live rows from cut[0] on come in cut[1] runs.  FOUR: four
 // columns a thread.
 template <typename T, bool FOUR>
@@ -393,14 +416,7 @@ __global__ void __launch_bounds__(256) k_vocab_dx_sum(const float* part, size_t 
     const int runs = at >= cut[0] ? cut[1] : 1;
     T* to = dx + row * lddx + j;
     if constexpr (FOUR) {
-      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (at >= 0) {
-#pragma unroll 4
-        for (int k = 0; k < runs; ++k) {
-          const float4 v = *reinterpret_cast<const float4*>(from + (size_t)k * stride * d);
-          s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
-        }
-      }
+      const float4 s = sum_runs(reinterpret_cast<const float4*>(from), stride * d / 4, at >= 0 ? runs : 0);
       if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(to) = s;
       else *reinterpret_cast<uint2*>(to) = make_uint2(bf16x2_of(s.x, s.y), bf16x2_of(s.z, s.w));
     } else {
@@ -422,12 +438,7 @@ __global__ void __launch_bounds__(256) k_vocab_dw_sum(const float* part, size_t 
   const long long values = (rows * d - (long long)first) / kPer;
   for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < values; i += (long long)gridDim.x * blockDim.x) {
     if constexpr (FOUR) {
-      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-      for (int k = 0; k < runs; ++k) {
-        const float4 v = reinterpret_cast<const float4*>(part + (size_t)k * stride * d)[i];
-        s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
-      }
+      const float4 s = sum_runs(reinterpret_cast<const float4*>(part) + i, stride * d / 4, runs);
       if constexpr (sizeof(T) == 4) reinterpret_cast<float4*>(dw + first)[i] = s;
       else reinterpret_cast<uint2*>(dw + first)[i] = make_uint2(bf16x2_of(s.x, s.y), bf16x2_of(s.z, s.w));
     } else {
@@ -588,7 +599,6 @@ cudaError_t launch_rows(const mt_vocab_loss& c, const Layout& l, char* ws, const
   r.vocab = c.vocab;
   r.dim = c.dim;
   r.top = l.top;
-  r.distill = c.top > 0;
   r.wide_ids = c.id_bytes == 8;
   r.teacher16 = c.teacher_dtype == MT_BF16;
   r.targets = c.targets;
@@ -614,7 +624,8 @@ cudaError_t launch_rows(const mt_vocab_loss& c, const Layout& l, char* ws, const
   cudaError_t e = cudaSuccess;
   if (!mark) {
     MT_LAUNCH("k_vocab_mark", s);
-    k_vocab_mark<<<grid_for(c.top > 0 ? tiles_of(c.n, 32) * 256 : c.n, 256, 8), 256, 0, s>>>(r);
+    if (c.top > 0) k_vocab_mark<true><<<grid_for(tiles_of(c.n, 32) * 256, 256, 8), 256, 0, s>>>(r);
+    else k_vocab_mark<false><<<grid_for(c.n, 256, 8), 256, 0, s>>>(r);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
@@ -622,7 +633,7 @@ cudaError_t launch_rows(const mt_vocab_loss& c, const Layout& l, char* ws, const
     const bool al = rows_wide(Rows{const_cast<void*>(c.x), c.n <= 1 ? c.dim : c.ldx, nullptr, nullptr}, c.dim, c.dtype);
     const size_t smem = c.top > 0 ? 8 * list_bytes(c.top) : 0;
     const int grid = grid_for(tiles_of(c.n, 32) * kRowBlocks * 256, 256, 8);
-    static SmemLimit limit[8];
+    static SmemLimit limit[16];
     auto go = [&](auto kernel, int i) {
       const cudaError_t le = limit[i].allow(kernel, 8 * list_bytes(MT_MAX_TOP));
       if (le != cudaSuccess) return le;
@@ -631,12 +642,16 @@ cudaError_t launch_rows(const mt_vocab_loss& c, const Layout& l, char* ws, const
       kernel<<<grid, 256, smem, s>>>(r);
       return cudaGetLastError();
     };
-    auto of = [&](auto few) {
-      constexpr bool M = decltype(few)::value;
-      if (c.dtype == MT_F32) return al ? go(k_vocab_rows<float, true, M>, M) : go(k_vocab_rows<float, false, M>, 2 + M);
-      return al ? go(k_vocab_rows<__nv_bfloat16, true, M>, 4 + M) : go(k_vocab_rows<__nv_bfloat16, false, M>, 6 + M);
+    auto of = [&](auto few, auto distill) {
+      constexpr bool M = decltype(few)::value, D = decltype(distill)::value;
+      constexpr int at = M + 2 * D;
+      if (c.dtype == MT_F32) return al ? go(k_vocab_rows<float, true, M, D>, at) : go(k_vocab_rows<float, false, M, D>, 4 + at);
+      return al ? go(k_vocab_rows<__nv_bfloat16, true, M, D>, 8 + at) : go(k_vocab_rows<__nv_bfloat16, false, M, D>, 12 + at);
     };
-    e = mark ? of(std::true_type{}) : of(std::false_type{});
+    using std::false_type;
+    using std::true_type;
+    if (c.top > 0) e = mark ? of(true_type{}, true_type{}) : of(false_type{}, true_type{});
+    else e = mark ? of(true_type{}, false_type{}) : of(false_type{}, false_type{});
   }
   if (e == cudaSuccess && l.copy_w)
     e = launch_parts(c.w, c.vocab <= 1 ? c.dim : c.ldw, 1, c.vocab, c.vocab, c.dim, c.dtype, reinterpret_cast<__nv_bfloat16*>(ws + l.w), s);
