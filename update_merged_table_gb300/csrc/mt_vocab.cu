@@ -122,20 +122,20 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 
 // A row's targets are put in order by a warp: up to kRankPairs of them each by how many others come before it (a step for each
-// pair of targets), more by a bitonic sort in shared memory.  Forward against 8192 x 64, each way for both: 2 rows of 128 pairs
-// 26 us (counted) and 25 (sorted), of 256 49 and 37, of 1024 353 and 111; 4096 rows of 8 28 and 36, of 64 43 and 49, of 128 62
-// and 65, of 256 118 and 97, of 1024 1048 and 384.
-constexpr int kRankPairs = 128;
+// pair of targets), more by a bitonic sort in shared memory.  Forward against 8192 x 64, each way for both: 2 rows of 8 pairs
+// 12.3 us (counted) and 14.4 (sorted), of 64 16.4 and 16.0, of 128 25 and 17.7, of 1024 606 and 60; 4096 rows of 8 27 and 34,
+// of 64 44.7 and 47.2, of 128 82 and 67, of 1024 1862 and 451.
+constexpr int kRankPairs = 64;
 __host__ __device__ inline int sorted_pairs(int top) {  // places that the sort needs: a power of two
-  int size = 64;
+  int size = kRankPairs;
   while (size < top) size *= 2;
   return size;
 }
-// Shared memory of a warp: the targets to be sorted, and their shares.
-inline size_t list_bytes(int top) { return (size_t)sorted_pairs(top) * 12; }
+// Shared memory of a warp: the targets to be put in order, and their shares.
+inline size_t list_bytes(int top) { return top > kRankPairs ? (size_t)sorted_pairs(top) * 12 : (size_t)top * 8; }
 
 __device__ __forceinline__ void warp_sort(unsigned long long* s, int size, int lane) {
-  constexpr int kOnce = 4;  // pairs a lane has loaded before it stores any
+  constexpr int kOnce = 2;  // pairs a lane has loaded before it stores any (4: 64 registers, 5224 rows of 2 pairs 23.9 to 25.8 us)
   for (int k = 2; k <= size; k *= 2) {
     for (int j = k / 2; j > 0; j /= 2) {
       __syncwarp();
@@ -164,7 +164,7 @@ __device__ __forceinline__ void warp_sort(unsigned long long* s, int size, int l
   __syncwarp();
 }
 
-// MARK: few rows, up to kMarkRows of up to kMarkPairs targets or pairs in all, which every block looks through itself (no k_vocab_mark before it): a
+// MARK: few rows, of up to kMarkRows targets or kMarkPairs pairs, which every block looks through itself (no k_vocab_mark before it): a
 // thread to a row of up to kLanePairs, else eight lanes, or 32 from 65 on.  Forward in us, so, with k_vocab_mark, and by a
 // thread to any row: against 32,771 x 320, 37 rows of 8 pairs 16.9, 19.0 and 16.9, 200 of 9 24 (thread) or 27 (lanes) and 26,
 // 64 of 32 18.8, 20.4 and 28.3, 16 of 128 23.8, 25.0 and 38, 2 of 1024 56, 63 and 111; against 8192 x 64, 256 targets 13.1 and
@@ -175,11 +175,15 @@ constexpr int kRowBlocks = 4;  // blocks to 32 rows: a warp has one row at most
 
 // A quarter of 32 rows' live ones per block, a warp each; the last block writes how many there are and puts zeros behind them up to the
 // next 128 rows (steps of dW's contraction).  T: the rows' type; AL: they can be read in 16-byte vectors.
-template <typename T, bool AL, bool MARK, bool DISTILL>
+// LIST: what a row has, kTarget one target, kCounted and kSorted a teacher's pairs (each form by itself: all in one took a few
+// rows' call a microsecond or two longer).
+enum List { kTarget, kCounted, kSorted };
+template <typename T, bool AL, bool MARK, int LIST>
 __global__ void __launch_bounds__(256) k_vocab_rows(const VocabRows p) {
   lead();
   if (!MARK) follow();
   constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
+  constexpr bool DISTILL = LIST != kTarget;
   extern __shared__ uint8_t s_mem[];
   __shared__ int s_base;
   __shared__ uint32_t s_mask[MARK && DISTILL ? kMarkPairs / (kLanePairs + 1) / 32 + 1 : 1];
@@ -259,40 +263,42 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const VocabRows p) {
           p.share[at] = 1.0f - p.smoothing;
         }
       } else {
-        // a target's key: its id, then its place among the pairs; ids that are not there come last, with a share of zero
-        const int size = sorted_pairs(p.top);
-        unsigned long long* s_key = reinterpret_cast<unsigned long long*>(s_mem) + warp * size;
-        float* s_t = reinterpret_cast<float*>(s_mem + (size_t)8 * size * 8) + warp * size;
+        // (the differences are scaled, not the logits: a type's lowest or largest value times the scale may be no number)
+        const int size = LIST == kSorted ? sorted_pairs(p.top) : p.top;
+        unsigned long long* s_key = reinterpret_cast<unsigned long long*>(s_mem) + warp * size;  // kSorted: the id, then its place among the pairs
+        int* s_id = reinterpret_cast<int*>(s_mem) + warp * size;                                 // kCounted
+        float* s_t = reinterpret_cast<float*>(s_mem + (size_t)8 * size * (LIST == kSorted ? 8 : 4)) + warp * size;
         float top = -INFINITY;
         for (int j = lane; j < p.top; j += 32) {
           const long long id = id_at(p, row * p.top + j);
           const bool there = pair_there<true>(p, row * p.top + j, id);
-          s_key[j] = (unsigned long long)(there ? (unsigned)id : 0x7FFFFFFFu) << 32 | (unsigned)j;
+          const int key = there ? (int)id : 0x7FFFFFFF;  // ids that are not there come last, with a share of zero
+          if constexpr (LIST == kSorted) s_key[j] = (unsigned long long)(unsigned)key << 32 | (unsigned)j;
+          else s_id[j] = key;
           s_t[j] = there ? teacher_at(p, row * p.top + j) : -INFINITY;
           top = fmaxf(top, s_t[j]);
         }
         top = warp_max(top);
-        // (the differences are scaled, not the logits: a type's lowest or largest value times the scale may be no number)
         float sum = 0.0f;
         for (int j = lane; j < p.top; j += 32) sum += expf(p.scale * (s_t[j] - top));
         sum = warp_sum(sum);
         const float inv = 1.0f / sum, log_sum = logf(sum);
         float entropy = 0.0f;
+        __syncwarp();
         for (int j = lane; j < p.top; j += 32) {
           const float d = p.scale * (s_t[j] - top), t = expf(d) * inv;
-          s_t[j] = t;
           if (t != 0.0f) entropy += t * (d - log_sum);
-        }
-        if (p.top <= kRankPairs) {
-          __syncwarp();
-          for (int j = lane; j < p.top; j += 32) {
-            const unsigned long long key = s_key[j];
+          if constexpr (LIST == kSorted) {
+            s_t[j] = t;
+          } else {
+            const int id = s_id[j];
             int rank = 0;
-            for (int i = 0; i < p.top; ++i) rank += s_key[i] < key;
-            p.ids[at * p.top + rank] = (int)(key >> 32);
-            p.share[at * p.top + rank] = s_t[j];
+            for (int i = 0; i < p.top; ++i) rank += s_id[i] < id || (s_id[i] == id && i < j);
+            p.ids[at * p.top + rank] = id;
+            p.share[at * p.top + rank] = t;
           }
-        } else {
+        }
+        if constexpr (LIST == kSorted) {
           for (int j = p.top + lane; j < size; j += 32) s_key[j] = ~0ull;
           warp_sort(s_key, size, lane);
           for (int j = lane; j < p.top; j += 32) {
@@ -394,8 +400,13 @@ __device__ __forceinline__ float4 sum_runs(const float4* from, size_t step, int 
 #pragma unroll
     for (int q = 0; q < kOnce; ++q) add(v[q]);
   }
-#pragma unroll 1
-  for (; k < runs; ++k, from += step) add(__ldcg(from));
+  float4 v[kOnce - 1];
+#pragma unroll
+  for (int q = 0; q < kOnce - 1; ++q)
+    if (k + q < runs) v[q] = __ldcg(from + q * step);
+#pragma unroll
+  for (int q = 0; q < kOnce - 1; ++q)
+    if (k + q < runs) add(v[q]);
   return s;
 }
 
@@ -620,7 +631,7 @@ cudaError_t launch_rows(const mt_vocab_loss& c, const Layout& l, char* ws, const
   r.dloss = dloss;
   r.lse = lse;
   r.coef = dloss != nullptr ? reinterpret_cast<float4*>(ws + l.coef) : nullptr;
-  const bool mark = c.n <= kMarkRows && c.n * l.top <= kMarkPairs;
+  const bool mark = c.top > 0 ? c.n * l.top <= kMarkPairs : c.n <= kMarkRows;
   cudaError_t e = cudaSuccess;
   if (!mark) {
     MT_LAUNCH("k_vocab_mark", s);
@@ -633,7 +644,7 @@ cudaError_t launch_rows(const mt_vocab_loss& c, const Layout& l, char* ws, const
     const bool al = rows_wide(Rows{const_cast<void*>(c.x), c.n <= 1 ? c.dim : c.ldx, nullptr, nullptr}, c.dim, c.dtype);
     const size_t smem = c.top > 0 ? 8 * list_bytes(c.top) : 0;
     const int grid = grid_for(tiles_of(c.n, 32) * kRowBlocks * 256, 256, 8);
-    static SmemLimit limit[16];
+    static SmemLimit limit[24];
     auto go = [&](auto kernel, int i) {
       const cudaError_t le = limit[i].allow(kernel, 8 * list_bytes(MT_MAX_TOP));
       if (le != cudaSuccess) return le;
@@ -642,16 +653,17 @@ cudaError_t launch_rows(const mt_vocab_loss& c, const Layout& l, char* ws, const
       kernel<<<grid, 256, smem, s>>>(r);
       return cudaGetLastError();
     };
-    auto of = [&](auto few, auto distill) {
-      constexpr bool M = decltype(few)::value, D = decltype(distill)::value;
-      constexpr int at = M + 2 * D;
-      if (c.dtype == MT_F32) return al ? go(k_vocab_rows<float, true, M, D>, at) : go(k_vocab_rows<float, false, M, D>, 4 + at);
-      return al ? go(k_vocab_rows<__nv_bfloat16, true, M, D>, 8 + at) : go(k_vocab_rows<__nv_bfloat16, false, M, D>, 12 + at);
+    auto of = [&](auto few, auto list) {
+      constexpr bool M = decltype(few)::value;
+      constexpr int L = decltype(list)::value, at = M + 2 * L;
+      if (c.dtype == MT_F32) return al ? go(k_vocab_rows<float, true, M, L>, at) : go(k_vocab_rows<float, false, M, L>, 6 + at);
+      return al ? go(k_vocab_rows<__nv_bfloat16, true, M, L>, 12 + at) : go(k_vocab_rows<__nv_bfloat16, false, M, L>, 18 + at);
     };
-    using std::false_type;
-    using std::true_type;
-    if (c.top > 0) e = mark ? of(true_type{}, true_type{}) : of(false_type{}, true_type{});
-    else e = mark ? of(true_type{}, false_type{}) : of(false_type{}, false_type{});
+    auto by_list = [&](auto few) {
+      if (c.top == 0) return of(few, std::integral_constant<int, kTarget>{});
+      return c.top <= kRankPairs ? of(few, std::integral_constant<int, kCounted>{}) : of(few, std::integral_constant<int, kSorted>{});
+    };
+    e = mark ? by_list(std::true_type{}) : by_list(std::false_type{});
   }
   if (e == cudaSuccess && l.copy_w)
     e = launch_parts(c.w, c.vocab <= 1 ? c.dim : c.ldw, 1, c.vocab, c.vocab, c.dim, c.dtype, reinterpret_cast<__nv_bfloat16*>(ws + l.w), s);
