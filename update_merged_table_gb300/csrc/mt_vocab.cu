@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(256) k_vocab_rows(const VocabRows p) {
   if (!MARK) follow();
   constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
   constexpr bool DISTILL = LIST != kTarget;
-  extern __shared__ uint8_t s_mem[];
+  extern __shared__ __align__(16) uint8_t s_mem[];
   __shared__ int s_base;
   __shared__ uint32_t s_mask[MARK && DISTILL ? kMarkPairs / (kLanePairs + 1) / 32 + 1 : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
