@@ -495,7 +495,7 @@ struct Layout {
 // dz of up to this many bf16 rows comes in two bf16 parts.  Its rounding (up to 2^-8 of a value) is one of many terms of dx and dw and
 // adds about what their own rounding does; with few rows single terms show (one row: dw's row of the target is one product).
 // Measured, relative error of dw with one part and with two: 2 rows 0.0029 and 0.0014 (its rounding alone 0.0014), 200 rows
-// 0.0022 and 0.0016; backward of 16 x 100,003 x 256 102 and 119 us, of 200 x 100,003 x 64 57 and 105.  The rule goes by all rows,
+// 0.0022 and 0.0016; backward of 16 x 100,003 x 256 91 and 112 us, of 200 x 100,003 x 64 54 and 95.  The rule goes by all rows,
 // those that take no part among them: how many do is known on the device only, and what is laid out and launched is not.
 constexpr int64_t kFewRowsTwice = 64;
 
